@@ -408,6 +408,118 @@ bitnet_status ttq_bwd(const uint16_t* dY, const uint16_t* x, const uint16_t* wt,
                       void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Layer norm over rows of K values (the norm that stands before a BitLinear),
+ * forward and backward:
+ *
+ *   mu[m]   = sum_k x[m,k] / K
+ *   r[m]    = (sum_k (x[m,k] - mu[m])^2 / K + eps)^(-1/2)
+ *   xh[m,k] = (x[m,k] - mu[m]) * r[m]
+ *   y[m,k]  = xh[m,k] * w[k] + b[k]
+ *
+ *   g[m,k]  = dY[m,k] * w[k]
+ *   dX[m,k] = r[m] * (g[m,k] - sum_j g[m,j] / K - xh[m,k] * sum_j g[m,j] xh[m,j] / K)
+ *   dw[k]   = sum_m dY[m,k] * xh[m,k],   db[k] = sum_m dY[m,k]
+ *
+ * Statistics and sums are fp32, each output is rounded once. Sums run in a
+ * fixed order (bitwise deterministic across calls). NaN and infinities
+ * propagate within their row (and into dw, db). K <= 32768.
+ *
+ * x, dX     [M][K] in x_dtype (BITNET_BF16 bits or BITNET_F32).
+ * w, b      [K] in p_dtype (BITNET_BF16 or BITNET_F32), or NULL (1 and 0).
+ * y, dY     [M][K] in y_dtype (BITNET_BF16 or BITNET_F32).
+ * mean, rstd [M] float: mu and r, written by the forward (NULL: not
+ *           written) and read by the backward.
+ * codes, scales  the 8-bit checkpoint of x (bitnet_ckpt_pack's layout; x is
+ *           the input, not xh). The forward writes both if codes is not NULL;
+ *           the backward given codes reads them instead of x (x may then be
+ *           NULL; x_dtype still names dX's type), with mu and r of the
+ *           uncoded row.
+ * dX, dw, db  each NULL if not wanted, at least one not (dw, db in p_dtype).
+ * Data pointers need only their element's alignment; codes and the workspace
+ * 16 bytes.
+ * workspace of the backward: bitnet_layernorm_workspace_bytes(M, K) bytes
+ * (0 for sizes it rejects; NULL allowed when neither dw nor db is wanted);
+ * no initialization, not shared by calls that may run at the same time.
+ */
+size_t bitnet_layernorm_workspace_bytes(int64_t M, int64_t K);
+bitnet_status bitnet_layernorm_fwd(const void* x, bitnet_dtype x_dtype, const void* w, const void* b,
+                                   bitnet_dtype p_dtype, int64_t M, int64_t K, float eps, void* y,
+                                   bitnet_dtype y_dtype, float* mean, float* rstd, int8_t* codes, float* scales,
+                                   void* stream);
+bitnet_status bitnet_layernorm_bwd(const void* dY, bitnet_dtype y_dtype, const void* x, bitnet_dtype x_dtype,
+                                   const int8_t* codes, const float* scales, const void* w, bitnet_dtype p_dtype,
+                                   const float* mean, const float* rstd, int64_t M, int64_t K, void* dX, void* dw,
+                                   void* db, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Activations kept in 8 bits between the forward and the backward pass
+ * (1.03 bytes a value instead of 2 or 4). Each 128 consecutive values of a
+ * row share a scale:
+ *
+ *   s[m,j] = max |x[m,k]| over k = 128j .. 128j + 127 (k < K)
+ *   q[m,k] = clip(round_half_even(127 * x[m,k] / s[m,j]), -127, 127),
+ *            evaluated exactly (0 where s = 0)
+ *
+ * and q stands for fp32(q * fp32(s / 127)). A block that holds an infinity or
+ * a NaN stands for NaN throughout.
+ *
+ * x       [M][K] in x_dtype (BITNET_BF16 bits or BITNET_F32), element
+ *         aligned; unpack rounds once to x_dtype.
+ * codes   [M][Kc] int8, Kc = bitnet_ckpt_pad(K) (K rounded up to 128), 16-byte
+ *         aligned; columns K..Kc-1 are written as 0 and not read back.
+ * scales  [M][Kc/128] float, 4-byte aligned.
+ * M * Kc <= 2^40, K <= 2^24. No workspace.
+ */
+int64_t bitnet_ckpt_pad(int64_t K);
+bitnet_status bitnet_ckpt_pack(const void* x, bitnet_dtype x_dtype, int64_t M, int64_t K, int8_t* codes,
+                               float* scales, void* stream);
+bitnet_status bitnet_ckpt_unpack(const int8_t* codes, const float* scales, int64_t M, int64_t K, void* x,
+                                 bitnet_dtype x_dtype, void* stream);
+
+/*
+ * The gated activation of a feed-forward block, y = act(gate) * up, or
+ * y = act(gate) without up, and its gradients
+ *
+ *   dgate = dY * up * act'(gate),   dup = dY * act(gate)
+ *
+ * BITNET_ACT_SILU: act(g) = g / (1 + e^-g).
+ * BITNET_ACT_RELU2: act(g) = max(g, 0)^2.
+ * fp32 arithmetic, each output rounded once to bf16.
+ *
+ * gate, up    [M] rows of K bf16, ldg and ldu elements apart (>= K), 2-byte
+ *             aligned: they may be the halves of one [M][2K] tensor. up NULL:
+ *             no gate (then dup, up_codes, up_scales are NULL too).
+ * y, dY       [M][K] bf16.
+ * gate_codes, gate_scales, up_codes, up_scales  8-bit checkpoints
+ *             (bitnet_ckpt_pack's layout). The forward writes them if
+ *             gate_codes is not NULL; the backward given gate_codes reads
+ *             them instead of gate and up.
+ * dgate, dup  [M] rows of K bf16, lddg and lddu elements apart (>= K).
+ * Sizes as for bitnet_ckpt_pack. No workspace.
+ */
+typedef enum { BITNET_ACT_SILU = 0, BITNET_ACT_RELU2 = 1 } bitnet_act;
+bitnet_status bitnet_gate_fwd(bitnet_act act, const uint16_t* gate, int64_t ldg, const uint16_t* up, int64_t ldu,
+                              int64_t M, int64_t K, uint16_t* y, int8_t* gate_codes, float* gate_scales,
+                              int8_t* up_codes, float* up_scales, void* stream);
+bitnet_status bitnet_gate_bwd(bitnet_act act, const uint16_t* dY, const uint16_t* gate, int64_t ldg,
+                              const uint16_t* up, int64_t ldu, const int8_t* gate_codes, const float* gate_scales,
+                              const int8_t* up_codes, const float* up_scales, int64_t M, int64_t K,
+                              uint16_t* dgate, int64_t lddg, uint16_t* dup, int64_t lddu, void* stream);
+
+/*
+ * ttq_bwd with x kept as its 8-bit checkpoint (codes and scales of
+ * bitnet_ckpt_pack on x [M][K]): the values, rounded to bf16, are unpacked
+ * into the workspace and take x's place in dW = dY^T x. With dW NULL, codes
+ * and scales may be NULL. workspace: ttq_bwd_ckpt_workspace_bytes(M, N, K)
+ * bytes; the other arguments, the limits and the errors are ttq_bwd's.
+ */
+size_t ttq_bwd_ckpt_workspace_bytes(int64_t M, int64_t N, int64_t K);
+bitnet_status ttq_bwd_ckpt(const uint16_t* dY, const int8_t* codes, const float* scales, const uint16_t* wt,
+                           const uint8_t* w_packed, int64_t M, int64_t N, int64_t K, uint16_t* dX, void* dW,
+                           bitnet_dtype dW_dtype, float* grads, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
  * Test hooks (for the library's own tests and tuning; not needed to use it).
  *
  * bitnet_set_test_knobs - process-wide knobs read by every later launch:

@@ -4,20 +4,28 @@ The compute path is the HIP library ``libbitnet.so`` built from ``csrc/``
 (C ABI declared in ``include/bitnet.h``). ``binding`` wraps its entry points
 with the same names; ``layer`` adds the autograd function and the
 ``QATBitLinear`` module, ``ttq_layer`` the same for the TTQ variant
-(``TTQLinear``). Submodules load lazily so that importing the package (e.g.
+(``TTQLinear``), ``norm`` the layer norm that stands before them
+(``QATLayerNorm``) and ``checkpoint`` activations kept in 8 bits with the
+gated activation between them. Submodules load lazily so that importing the package (e.g.
 for ``workloads``) neither imports torch nor loads the library.
 """
 
 import importlib
 
-__all__ = ["binding", "layer", "ttq_layer", "workloads", "build"]
+_SUBMODULES = ("binding", "layer", "ttq_layer", "norm", "checkpoint", "workloads", "build")
+
+__all__ = list(_SUBMODULES)
 
 
 def __getattr__(name):
-    if name in ("binding", "layer", "ttq_layer", "workloads", "build"):
+    if name in _SUBMODULES:
         return importlib.import_module(f"{__name__}.{name}")
     if name in ("QATBitLinear", "BitLinearFunction"):
         return getattr(importlib.import_module(f"{__name__}.layer"), name)
     if name in ("TTQLinear", "TTQFunction"):
         return getattr(importlib.import_module(f"{__name__}.ttq_layer"), name)
+    if name in ("QATLayerNorm", "layer_norm"):
+        return getattr(importlib.import_module(f"{__name__}.norm"), name)
+    if name in ("compress", "decompress", "gated_activation"):
+        return getattr(importlib.import_module(f"{__name__}.checkpoint"), name)
     raise AttributeError(name)

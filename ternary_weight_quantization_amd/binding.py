@@ -90,6 +90,27 @@ def lib():
     L.ttq_fwd_codes_workspace_bytes.restype = sz
     L.ttq_fwd_codes.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, sz, vp]
     L.ttq_fwd_codes.restype = st
+    f32 = ctypes.c_float
+    L.bitnet_layernorm_workspace_bytes.argtypes = [i64, i64]
+    L.bitnet_layernorm_workspace_bytes.restype = sz
+    L.bitnet_layernorm_fwd.argtypes = [vp, st, vp, vp, st, i64, i64, f32, vp, st, vp, vp, vp, vp, vp]
+    L.bitnet_layernorm_fwd.restype = st
+    L.bitnet_layernorm_bwd.argtypes = [vp, st, vp, st, vp, vp, vp, st, vp, vp, i64, i64, vp, vp, vp, vp, sz, vp]
+    L.bitnet_layernorm_bwd.restype = st
+    L.bitnet_ckpt_pad.argtypes = [i64]
+    L.bitnet_ckpt_pad.restype = i64
+    L.bitnet_ckpt_pack.argtypes = [vp, st, i64, i64, vp, vp, vp]
+    L.bitnet_ckpt_pack.restype = st
+    L.bitnet_ckpt_unpack.argtypes = [vp, vp, i64, i64, vp, st, vp]
+    L.bitnet_ckpt_unpack.restype = st
+    L.bitnet_gate_fwd.argtypes = [st, vp, i64, vp, i64, i64, i64, vp, vp, vp, vp, vp, vp]
+    L.bitnet_gate_fwd.restype = st
+    L.bitnet_gate_bwd.argtypes = [st, vp, vp, i64, vp, i64, vp, vp, vp, vp, i64, i64, vp, i64, vp, i64, vp]
+    L.bitnet_gate_bwd.restype = st
+    L.ttq_bwd_ckpt_workspace_bytes.argtypes = [i64, i64, i64]
+    L.ttq_bwd_ckpt_workspace_bytes.restype = sz
+    L.ttq_bwd_ckpt.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, vp, vp, st, vp, vp, sz, vp]
+    L.ttq_bwd_ckpt.restype = st
     i32, u32 = ctypes.c_int32, ctypes.c_uint32
     L.bitnet_set_test_knobs.argtypes = [st, st, st, u32]
     L.bitnet_set_test_knobs.restype = None
@@ -139,6 +160,46 @@ def _need(t, dtype, shape, name):
         raise ValueError(f"{name}: must be contiguous")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a GPU tensor")
+
+
+def _value_dtype(t, name):
+    if t.dtype == torch.bfloat16:
+        return BITNET_BF16
+    if t.dtype == torch.float32:
+        return BITNET_F32
+    raise TypeError(f"{name}: expected bfloat16 or float32, got {t.dtype}")
+
+
+def _same_device(like, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != like.device:
+            raise ValueError(f"{name}: on {t.device}, expected {like.device}")
+
+
+# the current stream's handle on a device, without building a Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _launch(fn, index, *args):
+    """fn(*args, stream) with device `index` current, on its current stream.
+    No checks but the library's own: for callers that have made theirs."""
+    if index == torch.cuda.current_device():
+        code = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            code = fn(*args, _raw_stream(index))
+    if code:
+        _check(code)
+
+
+def _run(fn, like, stream, *args):
+    """_launch on like's device, on `stream` if one is given."""
+    if stream is None:
+        _launch(fn, like.device.index, *args)
+    else:
+        with torch.cuda.device(like.device):
+            _check(fn(*args, stream.cuda_stream))
 
 
 # --- size queries ----------------------------------------------------------
@@ -432,6 +493,210 @@ def ttq_bwd(dY, x, wt, w_packed, K, dX=None, dW=None, grads=None, workspace=None
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().ttq_bwd(_ptr(dY), _ptr(x), _ptr(wt), _ptr(w_packed), M, N, int(K), _ptr(dX), _ptr(dW),
                          dw_dtype, _ptr(grads), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def ttq_bwd_ckpt_workspace_bytes(M, N, K):
+    return int(lib().ttq_bwd_ckpt_workspace_bytes(int(M), int(N), int(K)))
+
+
+def ttq_bwd_ckpt(dY, codes, scales, wt, w_packed, K, dX=None, dW=None, grads=None, workspace=None, stream=None):
+    """ttq_bwd with x as its 8-bit checkpoint: codes int8 [M, Kc], scales
+    float32 [M, Kc/128] (bitnet_ckpt_pack)."""
+    M, N = dY.shape
+    K = int(K)
+    Kp = bitnet_k_pad(K)
+    _need(dY, torch.bfloat16, (M, N), "dY")
+    _same_device(dY, codes=codes, scales=scales, wt=wt, w_packed=w_packed, dX=dX, dW=dW, grads=grads,
+                 workspace=workspace)
+    if dX is not None:
+        _need(wt, torch.bfloat16, (N, Kp), "wt")
+        _need(dX, torch.bfloat16, (M, K), "dX")
+    dw_dtype = BITNET_BF16
+    if dW is not None:
+        _need_codes(codes, scales, M, K)
+        dw_dtype = _value_dtype(dW, "dW")
+        _need(dW, dW.dtype, (N, K), "dW")
+    if grads is not None:
+        _need(grads, torch.float32, (2,), "grads")
+        _need(w_packed, torch.uint8, (N, Kp // 4), "w_packed")
+    if workspace is None:
+        workspace = _workspace(ttq_bwd_ckpt_workspace_bytes(M, N, K), dY, stream)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _run(lib().ttq_bwd_ckpt, dY, stream, _ptr(dY), _ptr(codes), _ptr(scales), _ptr(wt), _ptr(w_packed), M, N, K,
+         _ptr(dX), _ptr(dW), dw_dtype, _ptr(grads), _ptr(workspace), ws_bytes)
+
+
+# --- layer norm ----------------------------------------------------------------
+
+def bitnet_layernorm_workspace_bytes(M, K):
+    return int(lib().bitnet_layernorm_workspace_bytes(int(M), int(K)))
+
+
+def _norm_params(w, b, K, like):
+    for name, t in (("w", w), ("b", b)):
+        if t is not None:
+            _value_dtype(t, name)
+            _need(t, t.dtype, (K,), name)
+    if w is not None and b is not None and w.dtype != b.dtype:
+        raise TypeError(f"w and b: one dtype expected, got {w.dtype} and {b.dtype}")
+    _same_device(like, w=w, b=b)
+    p = w if w is not None else b
+    return BITNET_F32 if p is None else _value_dtype(p, "w")
+
+
+def bitnet_layernorm_fwd(x, w, b, eps, y, mean=None, rstd=None, codes=None, scales=None, stream=None):
+    """y [M, K] (bf16 or float32) = the layer norm of x [M, K] (bf16 or
+    float32) with w, b [K] or None. Optional outputs: mean, rstd float32 [M];
+    codes int8 [M, Kc] and scales float32 [M, Kc/128], the 8-bit checkpoint
+    of x."""
+    M, K = x.shape
+    xd, yd = _value_dtype(x, "x"), _value_dtype(y, "y")
+    _need(x, x.dtype, (M, K), "x")
+    _need(y, y.dtype, (M, K), "y")
+    pd = _norm_params(w, b, K, x)
+    if mean is not None:
+        _need(mean, torch.float32, (M,), "mean")
+    if rstd is not None:
+        _need(rstd, torch.float32, (M,), "rstd")
+    if codes is not None:
+        _need_codes(codes, scales, M, K)
+    _same_device(x, y=y, mean=mean, rstd=rstd, codes=codes, scales=scales)
+    _run(lib().bitnet_layernorm_fwd, x, stream, _ptr(x), xd, _ptr(w), _ptr(b), pd, M, K, float(eps), _ptr(y), yd,
+         _ptr(mean), _ptr(rstd), _ptr(codes), _ptr(scales))
+
+
+def bitnet_layernorm_bwd(dY, x, w, mean, rstd, dX=None, dw=None, db=None, codes=None, scales=None, x_dtype=None,
+                         workspace=None, stream=None):
+    """dX [M, K], dw and db [K] (each optional) of the layer norm, from dY
+    [M, K], mean and rstd, and x or its 8-bit checkpoint (x None, codes and
+    scales given; x_dtype names dX's dtype when dX is None too)."""
+    M, K = dY.shape
+    yd = _value_dtype(dY, "dY")
+    _need(dY, dY.dtype, (M, K), "dY")
+    if codes is not None:
+        _need_codes(codes, scales, M, K)
+        xt = dX.dtype if dX is not None else (x_dtype or torch.bfloat16)
+    else:
+        if x is None:
+            raise ValueError("x: needed without codes")
+        _value_dtype(x, "x")
+        _need(x, x.dtype, (M, K), "x")
+        xt = x.dtype
+    if dX is not None:
+        _value_dtype(dX, "dX")
+        _need(dX, xt, (M, K), "dX")
+    _need(mean, torch.float32, (M,), "mean")
+    _need(rstd, torch.float32, (M,), "rstd")
+    pd = _norm_params(w, None, K, dY)
+    for name, t in (("dw", dw), ("db", db)):
+        if t is not None:
+            if w is None:
+                pd = _value_dtype(t, name)
+            _need(t, torch.float32 if pd == BITNET_F32 else torch.bfloat16, (K,), name)
+    _same_device(dY, x=x, mean=mean, rstd=rstd, codes=codes, scales=scales, dX=dX, dw=dw, db=db, workspace=workspace)
+    if workspace is None and (dw is not None or db is not None):
+        workspace = _workspace(bitnet_layernorm_workspace_bytes(M, K), dY, stream)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _run(lib().bitnet_layernorm_bwd, dY, stream, _ptr(dY), yd, _ptr(x), BITNET_F32 if xt == torch.float32 else BITNET_BF16,
+         _ptr(codes), _ptr(scales), _ptr(w), pd, _ptr(mean), _ptr(rstd), M, K, _ptr(dX), _ptr(dw), _ptr(db),
+         _ptr(workspace), ws_bytes)
+
+
+# --- 8-bit checkpoints, the gated activation ------------------------------------
+
+BITNET_ACT_SILU = 0
+BITNET_ACT_RELU2 = 1
+
+
+def bitnet_ckpt_pad(K):
+    return int(lib().bitnet_ckpt_pad(int(K)))
+
+
+def _need_codes(codes, scales, M, K, name=""):
+    Kc = (int(K) + 127) // 128 * 128
+    if codes is None or scales is None:
+        raise ValueError(f"{name}codes and scales: both needed")
+    _need(codes, torch.int8, (M, Kc), name + "codes")
+    _need(scales, torch.float32, (M, Kc // 128), name + "scales")
+
+
+def bitnet_ckpt_pack(x, codes, scales, stream=None):
+    """x [M, K] (bf16 or float32) -> codes int8 [M, Kc], scales float32
+    [M, Kc/128], Kc = bitnet_ckpt_pad(K)."""
+    M, K = x.shape
+    xd = _value_dtype(x, "x")
+    _need(x, x.dtype, (M, K), "x")
+    _need_codes(codes, scales, M, K)
+    _same_device(x, codes=codes, scales=scales)
+    _run(lib().bitnet_ckpt_pack, x, stream, _ptr(x), xd, M, K, _ptr(codes), _ptr(scales))
+
+
+def bitnet_ckpt_unpack(codes, scales, x, stream=None):
+    """x [M, K] (bf16 or float32) = the values of codes and scales."""
+    M, K = x.shape
+    xd = _value_dtype(x, "x")
+    _need(x, x.dtype, (M, K), "x")
+    _need_codes(codes, scales, M, K)
+    _same_device(x, codes=codes, scales=scales)
+    _run(lib().bitnet_ckpt_unpack, x, stream, _ptr(codes), _ptr(scales), M, K, _ptr(x), xd)
+
+
+def _need_rows(t, M, K, name):
+    """bf16 rows [M, K] with unit column stride; returns their stride."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
+    if tuple(t.shape) != (M, K):
+        raise ValueError(f"{name}: expected shape {(M, K)}, got {tuple(t.shape)}")
+    if K > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: columns must be contiguous")
+    if M > 1 and t.stride(0) < K:
+        raise ValueError(f"{name}: rows must not overlap")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a GPU tensor")
+    return t.stride(0) if M > 1 else K
+
+
+def bitnet_gate_fwd(act, gate, up, y, gate_codes=None, gate_scales=None, up_codes=None, up_scales=None, stream=None):
+    """y [M, K] = act(gate) * up (up None: act(gate)); gate and up are bf16
+    rows of any stride. With gate_codes the 8-bit checkpoints of both are
+    written too."""
+    M, K = gate.shape
+    ldg = _need_rows(gate, M, K, "gate")
+    ldu = K if up is None else _need_rows(up, M, K, "up")
+    _need(y, torch.bfloat16, (M, K), "y")
+    if gate_codes is not None:
+        _need_codes(gate_codes, gate_scales, M, K, "gate_")
+        if up is not None:
+            _need_codes(up_codes, up_scales, M, K, "up_")
+    _same_device(gate, up=up, y=y, gate_codes=gate_codes, gate_scales=gate_scales, up_codes=up_codes,
+                 up_scales=up_scales)
+    _run(lib().bitnet_gate_fwd, gate, stream, int(act), _ptr(gate), ldg, _ptr(up), ldu, M, K, _ptr(y),
+         _ptr(gate_codes), _ptr(gate_scales), _ptr(up_codes), _ptr(up_scales))
+
+
+def bitnet_gate_bwd(act, dY, dgate, dup=None, gate=None, up=None, gate_codes=None, gate_scales=None, up_codes=None,
+                    up_scales=None, stream=None):
+    """dgate and (with up) dup, bf16 rows of any stride, from dY [M, K] and
+    gate, up or their 8-bit checkpoints."""
+    M, K = dY.shape
+    _need(dY, torch.bfloat16, (M, K), "dY")
+    lddg = _need_rows(dgate, M, K, "dgate")
+    lddu = K if dup is None else _need_rows(dup, M, K, "dup")
+    ldg = ldu = K
+    if gate_codes is not None:
+        _need_codes(gate_codes, gate_scales, M, K, "gate_")
+        if dup is not None:
+            _need_codes(up_codes, up_scales, M, K, "up_")
+    else:
+        if gate is None:
+            raise ValueError("gate: needed without codes")
+        ldg = _need_rows(gate, M, K, "gate")
+        if up is not None:
+            ldu = _need_rows(up, M, K, "up")
+    _same_device(dY, dgate=dgate, dup=dup, gate=gate, up=up, gate_codes=gate_codes, gate_scales=gate_scales,
+                 up_codes=up_codes, up_scales=up_scales)
+    _run(lib().bitnet_gate_bwd, dY, stream, int(act), _ptr(dY), _ptr(gate), ldg, _ptr(up), ldu, _ptr(gate_codes),
+         _ptr(gate_scales), _ptr(up_codes), _ptr(up_scales), M, K, _ptr(dgate), lddg, _ptr(dup), lddu)
 
 
 # --- test hooks --------------------------------------------------------------

@@ -54,6 +54,47 @@ bitnet_status check_gemm_ranges(int64_t M, int64_t N, int64_t K, bool need_xq, b
   return BITNET_OK;
 }
 
+// The arguments of ttq_bwd but its workspace.
+bitnet_status check_ttq_bwd(const uint16_t* dY, const uint16_t* x, const uint16_t* wt, const uint8_t* w_packed,
+                            int64_t M, int64_t N, int64_t K, const uint16_t* dX, const void* dW, bitnet_dtype dW_dtype,
+                            const float* grads) {
+  if (!dY) return BITNET_ERR_NULL;
+  if (!dX && !dW) return BITNET_ERR_NULL;
+  if (dX && !wt) return BITNET_ERR_NULL;
+  if (dW && !x) return BITNET_ERR_NULL;
+  if (grads && (!dW || !w_packed)) return BITNET_ERR_NULL;
+  if (dW && dW_dtype != BITNET_BF16 && dW_dtype != BITNET_F32) return BITNET_ERR_DTYPE;
+  if (bitnet_status st = check_gemm_sizes(M, N, K)) return st;
+  const int64_t Kp = bitnet::k_pad(K);
+  if (32 * 4 * K > (int64_t(1) << 31) || !buffer_range_ok(M, 2 * N)) return BITNET_ERR_SHAPE;
+  if (dX && !buffer_range_ok(N, 2 * Kp)) return BITNET_ERR_SHAPE;
+  if (dW && !buffer_range_ok(M, 2 * K)) return BITNET_ERR_SHAPE;
+  if (grads && !buffer_range_ok(N, Kp / 4)) return BITNET_ERR_SHAPE;
+  if (!aligned(dY, 16)) return BITNET_ERR_ALIGN;
+  if (dX && (!aligned(wt, 16) || !aligned(dX, 16))) return BITNET_ERR_ALIGN;
+  if (dW && (!aligned(x, 16) || !aligned(dW, 16))) return BITNET_ERR_ALIGN;
+  if (grads && (!aligned(grads, 4) || !aligned(w_packed, 16))) return BITNET_ERR_ALIGN;
+  return BITNET_OK;
+}
+
+bool is_value(bitnet_dtype d) { return d == BITNET_BF16 || d == BITNET_F32; }
+uintptr_t elem(bitnet_dtype d) { return d == BITNET_F32 ? 4 : 2; }
+
+bitnet_status check_norm_sizes(int64_t M, int64_t K) {
+  if (bitnet_status st = check_sizes(M, K)) return st;
+  return K > bitnet::kNormMaxK ? BITNET_ERR_SHAPE : BITNET_OK;
+}
+
+// One thread per 8 values, 256 threads a workgroup: at most 2^29 workgroups.
+bitnet_status check_ckpt_sizes(int64_t M, int64_t K) {
+  if (bitnet_status st = check_sizes(M, K)) return st;
+  return K > (int64_t(1) << 24) || M * bitnet::ckpt_pad(K) > (int64_t(1) << 40) ? BITNET_ERR_SHAPE : BITNET_OK;
+}
+bool row_stride_ok(int64_t ld, int64_t K) { return ld >= K && ld <= bitnet::k_pad(int64_t(1) << 30); }
+
+// The bf16 x that ttq_bwd_ckpt unpacks at the start of its workspace.
+size_t ckpt_x_bytes(int64_t M, int64_t K) { return ((size_t)M * K * 2 + 255) / 256 * 256; }
+
 }  // namespace
 
 extern "C" {
@@ -278,26 +319,138 @@ bitnet_status ttq_fwd_codes(const uint16_t* x, const uint8_t* w_packed, const fl
 bitnet_status ttq_bwd(const uint16_t* dY, const uint16_t* x, const uint16_t* wt, const uint8_t* w_packed, int64_t M,
                       int64_t N, int64_t K, uint16_t* dX, void* dW, bitnet_dtype dW_dtype, float* grads,
                       void* workspace, size_t workspace_bytes, void* stream) {
-  if (!dY) return BITNET_ERR_NULL;
-  if (!dX && !dW) return BITNET_ERR_NULL;
-  if (dX && !wt) return BITNET_ERR_NULL;
-  if (dW && !x) return BITNET_ERR_NULL;
-  if (grads && (!dW || !w_packed)) return BITNET_ERR_NULL;
-  if (dW && dW_dtype != BITNET_BF16 && dW_dtype != BITNET_F32) return BITNET_ERR_DTYPE;
-  if (bitnet_status st = check_gemm_sizes(M, N, K)) return st;
-  const int64_t Kp = bitnet::k_pad(K);
-  if (32 * 4 * K > (int64_t(1) << 31) || !buffer_range_ok(M, 2 * N)) return BITNET_ERR_SHAPE;
-  if (dX && !buffer_range_ok(N, 2 * Kp)) return BITNET_ERR_SHAPE;
-  if (dW && !buffer_range_ok(M, 2 * K)) return BITNET_ERR_SHAPE;
-  if (grads && !buffer_range_ok(N, Kp / 4)) return BITNET_ERR_SHAPE;
+  if (bitnet_status st = check_ttq_bwd(dY, x, wt, w_packed, M, N, K, dX, dW, dW_dtype, grads)) return st;
   if (workspace_bytes < ttq_workspace_bytes(M, N, K)) return BITNET_ERR_WORKSPACE;
   if (workspace_bytes > 0 && !workspace) return BITNET_ERR_WORKSPACE;
-  if (!aligned(workspace, 16) || !aligned(dY, 16)) return BITNET_ERR_ALIGN;
-  if (dX && (!aligned(wt, 16) || !aligned(dX, 16))) return BITNET_ERR_ALIGN;
-  if (dW && (!aligned(x, 16) || !aligned(dW, 16))) return BITNET_ERR_ALIGN;
-  if (grads && (!aligned(grads, 4) || !aligned(w_packed, 16))) return BITNET_ERR_ALIGN;
+  if (!aligned(workspace, 16)) return BITNET_ERR_ALIGN;
   return from_hip(bitnet::launch_ttq_bwd(dY, x, wt, w_packed, M, N, K, dX, dW, dW_dtype == BITNET_F32, grads,
                                          workspace, workspace_bytes, static_cast<hipStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// Layer norm, 8-bit checkpoints, the gated activation
+// ---------------------------------------------------------------------------
+
+size_t bitnet_layernorm_workspace_bytes(int64_t M, int64_t K) {
+  if (check_norm_sizes(M, K) != BITNET_OK) return 0;
+  return bitnet::layernorm_bwd_workspace(M, K);
+}
+
+bitnet_status bitnet_layernorm_fwd(const void* x, bitnet_dtype x_dtype, const void* w, const void* b,
+                                   bitnet_dtype p_dtype, int64_t M, int64_t K, float eps, void* y,
+                                   bitnet_dtype y_dtype, float* mean, float* rstd, int8_t* codes, float* scales,
+                                   void* stream) {
+  if (!x || !y || (codes && !scales)) return BITNET_ERR_NULL;
+  if (!is_value(x_dtype) || !is_value(y_dtype) || !is_value(p_dtype)) return BITNET_ERR_DTYPE;
+  if (bitnet_status st = check_norm_sizes(M, K)) return st;
+  if (!aligned(x, elem(x_dtype)) || !aligned(y, elem(y_dtype)) || !aligned(w, elem(p_dtype)) ||
+      !aligned(b, elem(p_dtype)) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(codes, 16) || !aligned(scales, 4))
+    return BITNET_ERR_ALIGN;
+  return from_hip(bitnet::launch_layernorm_fwd(x, x_dtype == BITNET_F32, w, b, p_dtype == BITNET_F32, M, K, eps, y,
+                                               y_dtype == BITNET_F32, mean, rstd, codes, scales,
+                                               static_cast<hipStream_t>(stream)));
+}
+
+bitnet_status bitnet_layernorm_bwd(const void* dY, bitnet_dtype y_dtype, const void* x, bitnet_dtype x_dtype,
+                                   const int8_t* codes, const float* scales, const void* w, bitnet_dtype p_dtype,
+                                   const float* mean, const float* rstd, int64_t M, int64_t K, void* dX, void* dw,
+                                   void* db, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!dY || !mean || !rstd || (!x && !codes) || (codes && !scales)) return BITNET_ERR_NULL;
+  if (!dX && !dw && !db) return BITNET_ERR_NULL;
+  if (!is_value(x_dtype) || !is_value(y_dtype) || !is_value(p_dtype)) return BITNET_ERR_DTYPE;
+  if (bitnet_status st = check_norm_sizes(M, K)) return st;
+  if (dw || db) {
+    if (!workspace || workspace_bytes < bitnet_layernorm_workspace_bytes(M, K)) return BITNET_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return BITNET_ERR_ALIGN;
+  }
+  if (!aligned(dY, elem(y_dtype)) || (!codes && !aligned(x, elem(x_dtype))) || !aligned(w, elem(p_dtype)) ||
+      !aligned(dX, elem(x_dtype)) || !aligned(dw, elem(p_dtype)) || !aligned(db, elem(p_dtype)) || !aligned(mean, 4) ||
+      !aligned(rstd, 4) || !aligned(codes, 16) || !aligned(scales, 4))
+    return BITNET_ERR_ALIGN;
+  return from_hip(bitnet::launch_layernorm_bwd(dY, y_dtype == BITNET_F32, x, x_dtype == BITNET_F32, codes, scales, w,
+                                               p_dtype == BITNET_F32, mean, rstd, M, K, dX, dw, db, workspace,
+                                               static_cast<hipStream_t>(stream)));
+}
+
+int64_t bitnet_ckpt_pad(int64_t K) { return K < 1 ? 0 : bitnet::ckpt_pad(K); }
+
+bitnet_status bitnet_ckpt_pack(const void* x, bitnet_dtype x_dtype, int64_t M, int64_t K, int8_t* codes,
+                               float* scales, void* stream) {
+  if (!x || !codes || !scales) return BITNET_ERR_NULL;
+  if (!is_value(x_dtype)) return BITNET_ERR_DTYPE;
+  if (bitnet_status st = check_ckpt_sizes(M, K)) return st;
+  if (!aligned(x, elem(x_dtype)) || !aligned(codes, 16) || !aligned(scales, 4)) return BITNET_ERR_ALIGN;
+  return from_hip(bitnet::launch_ckpt_pack(x, x_dtype == BITNET_F32, M, K, codes, scales,
+                                           static_cast<hipStream_t>(stream)));
+}
+
+bitnet_status bitnet_ckpt_unpack(const int8_t* codes, const float* scales, int64_t M, int64_t K, void* x,
+                                 bitnet_dtype x_dtype, void* stream) {
+  if (!x || !codes || !scales) return BITNET_ERR_NULL;
+  if (!is_value(x_dtype)) return BITNET_ERR_DTYPE;
+  if (bitnet_status st = check_ckpt_sizes(M, K)) return st;
+  if (!aligned(x, elem(x_dtype)) || !aligned(codes, 16) || !aligned(scales, 4)) return BITNET_ERR_ALIGN;
+  return from_hip(bitnet::launch_ckpt_unpack(codes, scales, M, K, x, x_dtype == BITNET_F32,
+                                             static_cast<hipStream_t>(stream)));
+}
+
+bitnet_status bitnet_gate_fwd(bitnet_act act, const uint16_t* gate, int64_t ldg, const uint16_t* up, int64_t ldu,
+                              int64_t M, int64_t K, uint16_t* y, int8_t* gate_codes, float* gate_scales,
+                              int8_t* up_codes, float* up_scales, void* stream) {
+  if (!gate || !y || (gate_codes && !gate_scales)) return BITNET_ERR_NULL;
+  if (gate_codes && up && (!up_codes || !up_scales)) return BITNET_ERR_NULL;
+  if (act != BITNET_ACT_SILU && act != BITNET_ACT_RELU2) return BITNET_ERR_DTYPE;
+  if (bitnet_status st = check_ckpt_sizes(M, K)) return st;
+  if (!row_stride_ok(ldg, K) || (up && !row_stride_ok(ldu, K))) return BITNET_ERR_SHAPE;
+  if (!aligned(gate, 2) || !aligned(up, 2) || !aligned(y, 2) || !aligned(gate_codes, 16) || !aligned(gate_scales, 4) ||
+      !aligned(up_codes, 16) || !aligned(up_scales, 4))
+    return BITNET_ERR_ALIGN;
+  return from_hip(bitnet::launch_gate_fwd(act == BITNET_ACT_RELU2, gate, ldg, up, ldu, M, K, y, gate_codes,
+                                          gate_scales, up_codes, up_scales, static_cast<hipStream_t>(stream)));
+}
+
+bitnet_status bitnet_gate_bwd(bitnet_act act, const uint16_t* dY, const uint16_t* gate, int64_t ldg,
+                              const uint16_t* up, int64_t ldu, const int8_t* gate_codes, const float* gate_scales,
+                              const int8_t* up_codes, const float* up_scales, int64_t M, int64_t K,
+                              uint16_t* dgate, int64_t lddg, uint16_t* dup, int64_t lddu, void* stream) {
+  if (!dY || !dgate) return BITNET_ERR_NULL;
+  if (gate_codes ? !gate_scales || (dup && (!up_codes || !up_scales)) : !gate || (dup && !up)) return BITNET_ERR_NULL;
+  if (!dup && (gate_codes ? up_codes != nullptr : up != nullptr)) return BITNET_ERR_NULL;
+  if (act != BITNET_ACT_SILU && act != BITNET_ACT_RELU2) return BITNET_ERR_DTYPE;
+  if (bitnet_status st = check_ckpt_sizes(M, K)) return st;
+  if (!row_stride_ok(lddg, K) || (dup && !row_stride_ok(lddu, K))) return BITNET_ERR_SHAPE;
+  if (!gate_codes && (!row_stride_ok(ldg, K) || (up && !row_stride_ok(ldu, K)))) return BITNET_ERR_SHAPE;
+  if (!aligned(dY, 2) || !aligned(gate, 2) || !aligned(up, 2) || !aligned(gate_codes, 16) || !aligned(gate_scales, 4) ||
+      !aligned(up_codes, 16) || !aligned(up_scales, 4) || !aligned(dgate, 2) || !aligned(dup, 2))
+    return BITNET_ERR_ALIGN;
+  return from_hip(bitnet::launch_gate_bwd(act == BITNET_ACT_RELU2, dY, gate, ldg, up, ldu, gate_codes, gate_scales,
+                                          up_codes, up_scales, M, K, dgate, lddg, dup, lddu,
+                                          static_cast<hipStream_t>(stream)));
+}
+
+size_t ttq_bwd_ckpt_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (check_gemm_sizes(M, N, K) != BITNET_OK) return 0;
+  return ckpt_x_bytes(M, K) + ttq_workspace_bytes(M, N, K);
+}
+
+bitnet_status ttq_bwd_ckpt(const uint16_t* dY, const int8_t* codes, const float* scales, const uint16_t* wt,
+                           const uint8_t* w_packed, int64_t M, int64_t N, int64_t K, uint16_t* dX, void* dW,
+                           bitnet_dtype dW_dtype, float* grads, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  if (dW && (!codes || !scales)) return BITNET_ERR_NULL;
+  if (bitnet_status st = check_gemm_sizes(M, N, K)) return st;
+  if (!workspace || workspace_bytes < ttq_bwd_ckpt_workspace_bytes(M, N, K)) return BITNET_ERR_WORKSPACE;
+  if (!aligned(workspace, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return BITNET_ERR_ALIGN;
+  if (dW && M * bitnet::ckpt_pad(K) > (int64_t(1) << 40)) return BITNET_ERR_SHAPE;
+  uint16_t* x = static_cast<uint16_t*>(workspace);
+  const size_t xb = ckpt_x_bytes(M, K);
+  // every argument is checked before the unpacking is enqueued
+  if (bitnet_status st = check_ttq_bwd(dY, x, wt, w_packed, M, N, K, dX, dW, dW_dtype, grads)) return st;
+  if (dW)
+    if (hipError_t e = bitnet::launch_ckpt_unpack(codes, scales, M, K, x, false, static_cast<hipStream_t>(stream)))
+      return from_hip(e);
+  return ttq_bwd(dY, x, wt, w_packed, M, N, K, dX, dW, dW_dtype, grads, static_cast<char*>(workspace) + xb,
+                 workspace_bytes - xb, stream);
 }
 
 // ---------------------------------------------------------------------------

@@ -1,0 +1,251 @@
+// Activations kept in 8 bits between the forward and the backward pass:
+// codes and block scales (row_io.h), packed from bf16 or f32 rows and
+// unpacked again, and the gated activation of a feed-forward block, whose
+// backward reads the codes of its two inputs.
+//
+// Everything here is one pass over HBM: a block of 128 values is 16 lanes of
+// 8, its scale is a rotation maximum within a DPP row, and a lane's 8 codes
+// are one 8-byte store.
+
+#include "internal.h"
+#include "row_io.h"
+
+namespace bitnet {
+
+constexpr int kRowThreads = 256;
+
+// Lane groups of a launch over M rows of nch chunks each: chunk index -> row
+// and chunk within the row. nch is a multiple of 16, so the 16 lanes of a
+// block share a row.
+struct ChunkAt {
+  int64_t row;
+  int ch;
+};
+__device__ __forceinline__ ChunkAt chunk_at(int64_t i, int nch) {
+  ChunkAt c;
+  if (i <= 0xFFFFFFFFll) {
+    const uint32_t r = (uint32_t)i / (uint32_t)nch;
+    c.row = r;
+    c.ch = (int)((uint32_t)i - r * (uint32_t)nch);
+  } else {
+    c.row = i / nch;
+    c.ch = (int)(i - c.row * nch);
+  }
+  return c;
+}
+
+template <class T>
+__global__ __launch_bounds__(kRowThreads) void ckpt_pack_kernel(const T* __restrict__ x, int64_t total, int K, int nch,
+                                                                int8_t* __restrict__ codes,
+                                                                float* __restrict__ scales) {
+  const int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
+  if (i >= total) return;  // total is a multiple of 16: whole blocks leave
+  const ChunkAt at = chunk_at(i, nch);
+  typename ChunkOf<T>::type c = load8(x + at.row * K, 8 * at.ch, K);
+  settle8(c, 8 * at.ch, K);
+  float f[8];
+  c.get(f);
+  const float s = block_scale(f);
+  reinterpret_cast<uint2*>(codes)[i] = codes8(f, s);
+  if ((threadIdx.x & 15) == 0) scales[i >> 4] = s;
+}
+
+template <class T>
+__global__ __launch_bounds__(kRowThreads) void ckpt_unpack_kernel(const int8_t* __restrict__ codes,
+                                                                  const float* __restrict__ scales, int64_t total,
+                                                                  int K, int nch, T* __restrict__ x) {
+  const int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
+  if (i >= total) return;
+  const ChunkAt at = chunk_at(i, nch);
+  float f[8];
+  values8(reinterpret_cast<const uint2*>(codes)[i], scales[i >> 4] / 127.0f, f);
+  store8(x + at.row * K, 8 * at.ch, K, f);
+}
+
+static unsigned row_grid(int64_t total) { return (unsigned)((total + kRowThreads - 1) / kRowThreads); }
+
+hipError_t launch_ckpt_pack(const void* x, bool x_f32, int64_t M, int64_t K, int8_t* codes, float* scales,
+                            hipStream_t stream) {
+  const int nch = (int)(ckpt_pad(K) / 8);
+  const int64_t total = M * nch;
+  if (x_f32)
+    ckpt_pack_kernel<<<row_grid(total), kRowThreads, 0, stream>>>(static_cast<const float*>(x), total, (int)K, nch,
+                                                                  codes, scales);
+  else
+    ckpt_pack_kernel<<<row_grid(total), kRowThreads, 0, stream>>>(static_cast<const uint16_t*>(x), total, (int)K, nch,
+                                                                  codes, scales);
+  return hipGetLastError();
+}
+
+hipError_t launch_ckpt_unpack(const int8_t* codes, const float* scales, int64_t M, int64_t K, void* x, bool x_f32,
+                              hipStream_t stream) {
+  const int nch = (int)(ckpt_pad(K) / 8);
+  const int64_t total = M * nch;
+  if (x_f32)
+    ckpt_unpack_kernel<<<row_grid(total), kRowThreads, 0, stream>>>(codes, scales, total, (int)K, nch,
+                                                                    static_cast<float*>(x));
+  else
+    ckpt_unpack_kernel<<<row_grid(total), kRowThreads, 0, stream>>>(codes, scales, total, (int)K, nch,
+                                                                    static_cast<uint16_t*>(x));
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Gated activation y = act(gate) * up (up absent: y = act(gate)).
+//   silu:  act(g) = g / (1 + e^-g),  act'(g) = t (1 + g (1 - t)), t = 1 / (1 + e^-g)
+//   relu2: act(g) = max(g, 0)^2,     act'(g) = 2 max(g, 0)
+// The quotient is a reciprocal refined by nothing: v_rcp_f32 is within 1 ulp,
+// far below the bf16 rounding of the outputs.
+// ---------------------------------------------------------------------------
+
+struct ActSilu {
+  static __device__ __forceinline__ float sigmoid(float g) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f));
+  }
+  static __device__ __forceinline__ float f(float g) { return g * sigmoid(g); }
+  static __device__ __forceinline__ void fd(float g, float& a, float& da) {
+    const float t = sigmoid(g);
+    a = g * t;
+    da = t + a * (1.0f - t);
+  }
+};
+struct ActRelu2 {
+  static __device__ __forceinline__ float f(float g) {
+    const float r = g > 0.0f ? g : (g == g ? 0.0f : g);  // a NaN stays one
+    return r * r;
+  }
+  static __device__ __forceinline__ void fd(float g, float& a, float& da) {
+    const float r = g > 0.0f ? g : (g == g ? 0.0f : g);
+    a = r * r;
+    da = 2.0f * r;
+  }
+};
+
+// CK: the codes of gate and up are written too.
+template <class A, bool CK, bool UP>
+__global__ __launch_bounds__(kRowThreads) void gate_fwd_kernel(const uint16_t* __restrict__ gate, int64_t ldg,
+                                                               const uint16_t* __restrict__ up, int64_t ldu,
+                                                               int64_t total, int K, int nch, uint16_t* __restrict__ y,
+                                                               int8_t* __restrict__ gq, float* __restrict__ gs,
+                                                               int8_t* __restrict__ uq, float* __restrict__ us) {
+  const int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
+  if (i >= total) return;
+  const ChunkAt at = chunk_at(i, nch);
+  const int k0 = 8 * at.ch;
+  ChunkBf16 cg = load8(gate + at.row * ldg, k0, K), cu;
+  if constexpr (UP) cu = load8(up + at.row * ldu, k0, K);
+  settle8(cg, k0, K);
+  float g[8], u[8], o[8];
+  cg.get(g);
+  if constexpr (UP) {
+    settle8(cu, k0, K);
+    cu.get(u);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) o[e] = UP ? A::f(g[e]) * u[e] : A::f(g[e]);
+  store8(y + at.row * K, k0, K, o);
+  if constexpr (CK) {
+    const float s = block_scale(g);
+    reinterpret_cast<uint2*>(gq)[i] = codes8(g, s);
+    if ((threadIdx.x & 15) == 0) gs[i >> 4] = s;
+    if constexpr (UP) {
+      const float t = block_scale(u);
+      reinterpret_cast<uint2*>(uq)[i] = codes8(u, t);
+      if ((threadIdx.x & 15) == 0) us[i >> 4] = t;
+    }
+  }
+}
+
+// CK: gate and up come from their codes, else from the bf16 rows.
+template <class A, bool CK, bool UP>
+__global__ __launch_bounds__(kRowThreads) void gate_bwd_kernel(const uint16_t* __restrict__ dY,
+                                                               const uint16_t* __restrict__ gate, int64_t ldg,
+                                                               const uint16_t* __restrict__ up, int64_t ldu,
+                                                               const int8_t* __restrict__ gq,
+                                                               const float* __restrict__ gs,
+                                                               const int8_t* __restrict__ uq,
+                                                               const float* __restrict__ us, int64_t total, int K,
+                                                               int nch, uint16_t* __restrict__ dgate, int64_t lddg,
+                                                               uint16_t* __restrict__ dup, int64_t lddu) {
+  const int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
+  if (i >= total) return;
+  const ChunkAt at = chunk_at(i, nch);
+  const int k0 = 8 * at.ch;
+  ChunkBf16 cd = load8(dY + at.row * K, k0, K);
+  float g[8], u[8], d[8];
+  if constexpr (CK) {
+    const uint2 qg = reinterpret_cast<const uint2*>(gq)[i];
+    const float sg = gs[i >> 4];
+    if constexpr (UP) {
+      const uint2 qu = reinterpret_cast<const uint2*>(uq)[i];
+      values8(qu, us[i >> 4] / 127.0f, u);
+    }
+    values8(qg, sg / 127.0f, g);
+  } else {
+    ChunkBf16 cg = load8(gate + at.row * ldg, k0, K), cu;
+    if constexpr (UP) {
+      cu = load8(up + at.row * ldu, k0, K);
+      settle8(cu, k0, K);
+      cu.get(u);
+    }
+    settle8(cg, k0, K);
+    cg.get(g);
+  }
+  settle8(cd, k0, K);
+  cd.get(d);
+  float dg[8], du[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    float a, da;
+    A::fd(g[e], a, da);
+    dg[e] = UP ? d[e] * u[e] * da : d[e] * da;
+    du[e] = d[e] * a;
+  }
+  store8(dgate + at.row * lddg, k0, K, dg);
+  if constexpr (UP) store8(dup + at.row * lddu, k0, K, du);
+}
+
+template <class A>
+static void gate_fwd(const uint16_t* gate, int64_t ldg, const uint16_t* up, int64_t ldu, int64_t M, int64_t K,
+                     uint16_t* y, int8_t* gq, float* gs, int8_t* uq, float* us, hipStream_t st) {
+  const int nch = (int)(ckpt_pad(K) / 8);
+  const int64_t total = M * nch;
+  const unsigned grid = row_grid(total);
+  const int k = (int)K;
+  if (up && gq) gate_fwd_kernel<A, true, true><<<grid, kRowThreads, 0, st>>>(gate, ldg, up, ldu, total, k, nch, y, gq, gs, uq, us);
+  else if (up) gate_fwd_kernel<A, false, true><<<grid, kRowThreads, 0, st>>>(gate, ldg, up, ldu, total, k, nch, y, gq, gs, uq, us);
+  else if (gq) gate_fwd_kernel<A, true, false><<<grid, kRowThreads, 0, st>>>(gate, ldg, up, ldu, total, k, nch, y, gq, gs, uq, us);
+  else gate_fwd_kernel<A, false, false><<<grid, kRowThreads, 0, st>>>(gate, ldg, up, ldu, total, k, nch, y, gq, gs, uq, us);
+}
+
+hipError_t launch_gate_fwd(bool relu2, const uint16_t* gate, int64_t ldg, const uint16_t* up, int64_t ldu, int64_t M,
+                           int64_t K, uint16_t* y, int8_t* gq, float* gs, int8_t* uq, float* us, hipStream_t stream) {
+  if (relu2) gate_fwd<ActRelu2>(gate, ldg, up, ldu, M, K, y, gq, gs, uq, us, stream);
+  else gate_fwd<ActSilu>(gate, ldg, up, ldu, M, K, y, gq, gs, uq, us, stream);
+  return hipGetLastError();
+}
+
+template <class A>
+static void gate_bwd(const uint16_t* dY, const uint16_t* gate, int64_t ldg, const uint16_t* up, int64_t ldu,
+                     const int8_t* gq, const float* gs, const int8_t* uq, const float* us, int64_t M, int64_t K,
+                     uint16_t* dgate, int64_t lddg, uint16_t* dup, int64_t lddu, hipStream_t st) {
+  const int nch = (int)(ckpt_pad(K) / 8);
+  const int64_t total = M * nch;
+  const unsigned grid = row_grid(total);
+  const int k = (int)K;
+  if (dup && gq) gate_bwd_kernel<A, true, true><<<grid, kRowThreads, 0, st>>>(dY, gate, ldg, up, ldu, gq, gs, uq, us, total, k, nch, dgate, lddg, dup, lddu);
+  else if (dup) gate_bwd_kernel<A, false, true><<<grid, kRowThreads, 0, st>>>(dY, gate, ldg, up, ldu, gq, gs, uq, us, total, k, nch, dgate, lddg, dup, lddu);
+  else if (gq) gate_bwd_kernel<A, true, false><<<grid, kRowThreads, 0, st>>>(dY, gate, ldg, up, ldu, gq, gs, uq, us, total, k, nch, dgate, lddg, dup, lddu);
+  else gate_bwd_kernel<A, false, false><<<grid, kRowThreads, 0, st>>>(dY, gate, ldg, up, ldu, gq, gs, uq, us, total, k, nch, dgate, lddg, dup, lddu);
+}
+
+hipError_t launch_gate_bwd(bool relu2, const uint16_t* dY, const uint16_t* gate, int64_t ldg, const uint16_t* up,
+                           int64_t ldu, const int8_t* gq, const float* gs, const int8_t* uq, const float* us,
+                           int64_t M, int64_t K, uint16_t* dgate, int64_t lddg, uint16_t* dup, int64_t lddu,
+                           hipStream_t stream) {
+  if (relu2) gate_bwd<ActRelu2>(dY, gate, ldg, up, ldu, gq, gs, uq, us, M, K, dgate, lddg, dup, lddu, stream);
+  else gate_bwd<ActSilu>(dY, gate, ldg, up, ldu, gq, gs, uq, us, M, K, dgate, lddg, dup, lddu, stream);
+  return hipGetLastError();
+}
+
+}  // namespace bitnet

@@ -181,4 +181,29 @@ hipError_t launch_ttq_bwd(const uint16_t* dY, const uint16_t* x, const uint16_t*
                           int64_t M, int64_t N, int64_t K, uint16_t* dX, void* dW, bool dw_f32, float* grads,
                           void* ws, size_t ws_bytes, hipStream_t stream);
 
+// 8-bit activation checkpoints: columns of the codes, pack, unpack.
+inline int64_t ckpt_pad(int64_t K) { return (K + 127) / 128 * 128; }
+hipError_t launch_ckpt_pack(const void* x, bool x_f32, int64_t M, int64_t K, int8_t* codes, float* scales,
+                            hipStream_t stream);
+hipError_t launch_ckpt_unpack(const int8_t* codes, const float* scales, int64_t M, int64_t K, void* x, bool x_f32,
+                              hipStream_t stream);
+
+// The gated activation (up NULL: none; gq NULL: no codes).
+hipError_t launch_gate_fwd(bool relu2, const uint16_t* gate, int64_t ldg, const uint16_t* up, int64_t ldu, int64_t M,
+                           int64_t K, uint16_t* y, int8_t* gq, float* gs, int8_t* uq, float* us, hipStream_t stream);
+hipError_t launch_gate_bwd(bool relu2, const uint16_t* dY, const uint16_t* gate, int64_t ldg, const uint16_t* up,
+                           int64_t ldu, const int8_t* gq, const float* gs, const int8_t* uq, const float* us,
+                           int64_t M, int64_t K, uint16_t* dgate, int64_t lddg, uint16_t* dup, int64_t lddu,
+                           hipStream_t stream);
+
+// Layer norm, K <= kNormMaxK (a row fits the registers of one workgroup).
+constexpr int64_t kNormMaxK = 32768;
+hipError_t launch_layernorm_fwd(const void* x, bool x_f32, const void* w, const void* b, bool p_f32, int64_t M,
+                                int64_t K, float eps, void* y, bool y_f32, float* mean, float* rstd, int8_t* codes,
+                                float* scales, hipStream_t stream);
+size_t layernorm_bwd_workspace(int64_t M, int64_t K);
+hipError_t launch_layernorm_bwd(const void* dY, bool dy_f32, const void* x, bool x_f32, const int8_t* codes,
+                                const float* scales, const void* w, bool p_f32, const float* mean, const float* rstd,
+                                int64_t M, int64_t K, void* dX, void* dw, void* db, void* ws, hipStream_t stream);
+
 }  // namespace bitnet

@@ -1,0 +1,445 @@
+// Layer norm over rows of K values, forward and backward.
+//
+//   mu = sum x / K,  r = (sum (x - mu)^2 / K + eps)^(-1/2),  xh = (x - mu) r
+//   y  = xh w + b
+//   g  = dY w,  c1 = sum g / K,  c2 = sum g xh / K
+//   dX = r (g - c1 - xh c2),  dw = sum over rows dY xh,  db = sum over rows dY
+//
+// A row lives in the registers of TPR threads (CPT chunks of 8 values each),
+// so x is read once forward and once backward and the variance is the sum of
+// centered squares. Statistics and sums are fp32. With 8-bit codes the
+// forward also writes the row's codes and block scales (row_io.h), and the
+// backward takes x from them; mu and r are those of the uncoded row.
+//
+// The weight's and bias' gradients are column sums over all rows. Each
+// thread of the backward keeps its columns' sums in registers over the rows
+// its block takes, the block adds its rows' sums through LDS and writes one
+// partial row [2][K]; a second launch adds the partial rows in block order.
+// No atomics: the same inputs give the same bits.
+
+#include <type_traits>
+
+#include "internal.h"
+#include "row_io.h"
+
+namespace bitnet {
+
+__device__ __forceinline__ float wave_sum_f32(float v) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, kWave);
+  return v;
+}
+
+// Sum over the TPR threads of a row (whole waves), in every one of them.
+// `slot`: an LDS array of one float per wave of the block, free on entry.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* slot) {
+  v = wave_sum_f32(v);
+  if constexpr (TPR > kWave) {
+    constexpr int W = TPR / kWave;
+    const int w0 = threadIdx.x / TPR * W;
+    if (threadIdx.x % kWave == 0) slot[threadIdx.x / kWave] = v;
+    __syncthreads();
+    v = slot[w0];
+#pragma unroll
+    for (int j = 1; j < W; ++j) v += slot[w0 + j];
+  }
+  return v;
+}
+
+struct NormParams {
+  const void* w;  // [K] or NULL
+  const void* b;
+  bool f32;       // their type
+};
+
+template <class T, int BLOCK, int TPR, int CPT>
+__global__ __launch_bounds__(BLOCK) void layernorm_fwd_kernel(const T* __restrict__ x, NormParams p, int64_t M, int K,
+                                                              float eps, void* __restrict__ y, bool y_f32,
+                                                              float* __restrict__ mean, float* __restrict__ rstd,
+                                                              int8_t* __restrict__ codes, float* __restrict__ scales,
+                                                              int nch) {
+  constexpr int RPB = BLOCK / TPR;
+  __shared__ float s0[BLOCK / kWave], s1[BLOCK / kWave];
+  const int t = threadIdx.x % TPR;
+  // uniform in the wave: whole waves share a row
+  const int64_t row = (int64_t)blockIdx.x * RPB + __builtin_amdgcn_readfirstlane((int)threadIdx.x / TPR);
+  const bool ok = row < M;
+  const T* xr = x + (ok ? row : 0) * K;
+  typename ChunkOf<T>::type c[CPT];
+#pragma unroll
+  for (int i = 0; i < CPT - 1; ++i) c[i] = load8_in(xr + 8 * (t + i * TPR));
+  c[CPT - 1] = load8(xr, 8 * (t + (CPT - 1) * TPR), K);
+  // only a thread's last chunk can reach past K (row_split)
+  settle8(c[CPT - 1], 8 * (t + (CPT - 1) * TPR), K);
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) {
+    float f[8];
+    c[i].get(f);
+    sum += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+  }
+  const float mu = row_sum<TPR>(sum, s0) / (float)K;
+  float sq = 0.0f;
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) {
+    const int left = K - 8 * (t + i * TPR);
+    float f[8];
+    c[i].get(f);
+    if (i < CPT - 1 || left >= 8) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sq = fmaf(f[e] - mu, f[e] - mu, sq);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sq += e < left ? (f[e] - mu) * (f[e] - mu) : 0.0f;
+    }
+  }
+  const float r = 1.0f / sqrtf(row_sum<TPR>(sq, s1) / (float)K + eps);
+  if (!ok) return;
+  if (t == 0) {
+    if (mean) mean[row] = mu;
+    if (rstd) rstd[row] = r;
+  }
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) {
+    const int ch = t + i * TPR, k0 = 8 * ch;
+    if (i == CPT - 1 && ch >= nch) continue;
+    float f[8], o[8];
+    c[i].get(f);
+    if (codes) {  // uniform; the 16 lanes of a block are all here
+      const float s = block_scale(f);
+      reinterpret_cast<uint2*>(codes)[row * nch + ch] = codes8(f, s);
+      if ((t & 15) == 0) scales[(row * nch + ch) >> 4] = s;
+    }
+    if (i == CPT - 1 && k0 >= K) continue;
+    if (p.w) {
+      float w[8];
+      param8(p.w, p.f32, k0, K, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = (f[e] - mu) * r * w[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = (f[e] - mu) * r;
+    }
+    if (p.b) {
+      float b[8];
+      param8(p.b, p.f32, k0, K, b);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] += b[e];
+    }
+    if (y_f32) store8(static_cast<float*>(y) + row * K, k0, K, o);
+    else store8(static_cast<uint16_t*>(y) + row * K, k0, K, o);
+  }
+}
+
+// Where the backward's x comes from: bf16 or f32 rows, or codes.
+struct FromBf16 { typedef ChunkBf16 Chunk; };
+struct FromF32 { typedef ChunkF32 Chunk; };
+struct ChunkCodes {
+  uint2 q;
+  float s;
+  __device__ __forceinline__ void get(float (&f)[8]) const { values8(q, s / 127.0f, f); }
+};
+struct FromCodes { typedef ChunkCodes Chunk; };
+
+struct NormBwd {
+  const void* dY;
+  const void* x;        // rows (FromBf16, FromF32)
+  const int8_t* codes;  // FromCodes
+  const float* scales;
+  NormParams p;
+  const float* mean;
+  const float* rstd;
+  int64_t M;
+  int K, nch;
+  void* dX;
+  float* partials;  // [blocks][2][K], NULL: no column sums
+};
+
+// Chunk ch of a row; IN: it lies inside the row.
+template <class X, bool IN>
+__device__ __forceinline__ typename X::Chunk norm_x(const NormBwd& a, int64_t row, int ch) {
+  if constexpr (std::is_same<X, FromCodes>::value) {
+    ChunkCodes c;
+    const int at = IN || ch < a.nch ? ch : 0;
+    c.q = reinterpret_cast<const uint2*>(a.codes)[row * a.nch + at];
+    c.s = a.scales[(row * a.nch + at) >> 4];
+    return c;
+  } else if constexpr (std::is_same<X, FromF32>::value) {
+    const float* p = static_cast<const float*>(a.x) + row * a.K;
+    if constexpr (IN) return load8_in(p + 8 * ch);
+    else return load8(p, 8 * ch, a.K);
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(a.x) + row * a.K;
+    if constexpr (IN) return load8_in(p + 8 * ch);
+    else return load8(p, 8 * ch, a.K);
+  }
+}
+
+// The weight as fp32 in LDS: every row of the block reads it twice.
+extern __shared__ __attribute__((aligned(16))) float norm_lds[];
+
+// Keeps a loaded chunk as it is across the row's reduction: the values
+// derived from it are computed again after it instead of being held in
+// registers next to the column sums.
+__device__ __forceinline__ void hold(ChunkBf16& c) { asm volatile("" : "+v"(c.v.x), "+v"(c.v.y), "+v"(c.v.z), "+v"(c.v.w)); }
+__device__ __forceinline__ void hold(ChunkF32& c) {
+  asm volatile("" : "+v"(c.a.x), "+v"(c.a.y), "+v"(c.a.z), "+v"(c.a.w), "+v"(c.b.x), "+v"(c.b.y), "+v"(c.b.z), "+v"(c.b.w));
+}
+__device__ __forceinline__ void hold(ChunkCodes& c) { asm volatile("" : "+v"(c.q.x), "+v"(c.q.y), "+v"(c.s)); }
+
+template <class X, class DX, class DY, int BLOCK, int TPR, int CPT>
+__global__ __launch_bounds__(BLOCK, BLOCK == 512 ? 1 : 2) void layernorm_bwd_kernel(NormBwd a) {
+  constexpr int RPB = BLOCK / TPR;
+  __shared__ float slot[4][BLOCK / kWave];
+  const int t = threadIdx.x % TPR;
+  const int rl = __builtin_amdgcn_readfirstlane((int)threadIdx.x / TPR);  // whole waves share a row
+  const int K = a.K;
+  for (int k = threadIdx.x; k < a.nch; k += BLOCK) {
+    float w[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
+    if (a.p.w) param8(a.p.w, a.p.f32, 8 * k, K, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) norm_lds[8 * k + e] = w[e];
+  }
+  __syncthreads();
+  float dw[CPT][8], db[CPT][8];
+#pragma unroll
+  for (int i = 0; i < CPT; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[i][e] = db[i][e] = 0.0f;
+
+  int flip = 0;
+  for (int64_t base = (int64_t)blockIdx.x * RPB; base < a.M; base += (int64_t)gridDim.x * RPB, flip ^= 2) {
+    const int64_t row = base + rl;  // uniform in the wave
+    if (RPB > 1 && row >= a.M) break;  // rows of one wave: no barrier ahead
+    typename ChunkOf<DY>::type cd[CPT];
+    typename X::Chunk cx[CPT];
+    const DY* dr = static_cast<const DY*>(a.dY) + row * K;
+#pragma unroll
+    for (int i = 0; i < CPT - 1; ++i) {
+      cd[i] = load8_in(dr + 8 * (t + i * TPR));
+      cx[i] = norm_x<X, true>(a, row, t + i * TPR);
+    }
+    cd[CPT - 1] = load8(dr, 8 * (t + (CPT - 1) * TPR), K);
+    cx[CPT - 1] = norm_x<X, false>(a, row, t + (CPT - 1) * TPR);
+    const float mu = a.mean[row], r = a.rstd[row];
+    // only a thread's last chunk can reach past K (row_split); dY is zero
+    // there, so nothing is added, and what a chunk past the row's end reads
+    // of the weight (chunk 0) does not matter
+    settle8(cd[CPT - 1], 8 * (t + (CPT - 1) * TPR), K);
+    if constexpr (!std::is_same<X, FromCodes>::value) settle8(cx[CPT - 1], 8 * (t + (CPT - 1) * TPR), K);
+    const bool last = t + (CPT - 1) * TPR < a.nch;
+    float sg = 0.0f, sgx = 0.0f;
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+      const float* w = norm_lds + 8 * (i < CPT - 1 || last ? t + i * TPR : 0);
+      float d[8], x[8];
+      cd[i].get(d);
+      cx[i].get(x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float xh = (x[e] - mu) * r, g = d[e] * w[e];
+        sg += g;
+        sgx = fmaf(g, xh, sgx);
+        dw[i][e] = fmaf(d[e], xh, dw[i][e]);
+        db[i][e] += d[e];
+      }
+      hold(cd[i]);
+      hold(cx[i]);
+      __builtin_amdgcn_sched_barrier(0);  // one chunk's values at a time
+    }
+    // two slot pairs in turn: a row's readers are done with one pair before
+    // the barrier of the next row, after which it may be written again
+    const float c1 = row_sum<TPR>(sg, slot[flip]) / (float)K;
+    const float c2 = row_sum<TPR>(sgx, slot[flip + 1]) / (float)K;
+    if (a.dX == nullptr) continue;
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+      const int k0 = 8 * (t + i * TPR);
+      const float* w = norm_lds + (i < CPT - 1 || last ? k0 : 0);
+      float d[8], x[8], o[8];
+      cd[i].get(d);
+      cx[i].get(x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float xh = (x[e] - mu) * r;
+        o[e] = r * (d[e] * w[e] - c1 - xh * c2);
+      }
+      DX* xr = static_cast<DX*>(a.dX) + row * K;
+      if (i < CPT - 1) store8_in(xr + k0, o);
+      else store8(xr, k0, K, o);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+
+  if (a.partials == nullptr) return;
+  float* out = a.partials + (int64_t)blockIdx.x * 2 * K;
+  if constexpr (RPB > 1) {
+    // the block's rows in turn, one chunk column at a time
+    __shared__ float acc[RPB][TPR][9];
+#pragma unroll
+    for (int q = 0; q < 2 * CPT; ++q) {
+      const int i = q >> 1;
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[rl][t][e] = (q & 1) ? db[i][e] : dw[i][e];
+      __syncthreads();
+      // 8 * TPR sums over RPB rows by the block
+      for (int j = threadIdx.x; j < 8 * TPR; j += BLOCK) {
+        float v = acc[0][j >> 3][j & 7];
+#pragma unroll
+        for (int w = 1; w < RPB; ++w) v += acc[w][j >> 3][j & 7];
+        const int k = 8 * TPR * i + j;
+        if (k < K) out[(q & 1) * (int64_t)K + k] = v;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+      const int k0 = 8 * (t + i * TPR);
+      if (k0 >= K) continue;
+      store8(out, k0, K, dw[i]);
+      store8(out + K, k0, K, db[i]);
+    }
+  }
+}
+
+// The column sums of the partial rows [blocks][cols], columns [0, K) to dw
+// and [K, 2K) to db: a block takes 64 columns, its 16 waves every 16th
+// partial row each, then the wave sums are added in order.
+__global__ __launch_bounds__(1024) void layernorm_cols_kernel(const float* __restrict__ partials, int blocks, int K,
+                                                              void* __restrict__ dw, void* __restrict__ db,
+                                                              bool p_f32) {
+  __shared__ float part[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t col = (int64_t)blockIdx.x * 64 + lane, cols = 2 * (int64_t)K;
+  float v = 0.0f;
+  if (col < cols) {
+    const float* src = partials + col;
+    int r = wave;
+    for (; r + 48 < blocks; r += 64) {  // four loads in flight
+      const float a = src[(int64_t)r * cols], b = src[(int64_t)(r + 16) * cols], c = src[(int64_t)(r + 32) * cols],
+                  d = src[(int64_t)(r + 48) * cols];
+      v += (a + b) + (c + d);
+    }
+    for (; r < blocks; r += 16) v += src[(int64_t)r * cols];
+  }
+  part[wave][lane] = v;
+  __syncthreads();
+  if (wave != 0 || col >= cols) return;
+#pragma unroll
+  for (int w = 1; w < 16; ++w) v += part[w][lane];
+  void* out = col < K ? dw : db;
+  const int64_t k = col < K ? col : col - K;
+  if (out == nullptr) return;
+  if (p_f32) static_cast<float*>(out)[k] = v;
+  else static_cast<uint16_t*>(out)[k] = f32_to_bf16_bits(v);
+}
+
+// ---------------------------------------------------------------------------
+// Launches. Threads per row and chunks per thread from the row length alone:
+// one wave a row up to 2560 (no barriers), 256 threads up to 10240, 512
+// above (kNormMaxK).
+// ---------------------------------------------------------------------------
+
+struct RowSplit {
+  int tpr, cpt;
+};
+// nch and tpr are multiples of 16, so every chunk before a thread's last is a
+// whole chunk of the row (it lies before the row's last block of 128).
+static RowSplit row_split(int64_t K) {
+  const int nch = (int)(ckpt_pad(K) / 8);
+  const int tpr = nch <= 320 ? 64 : nch <= 1280 ? 256 : 512;
+  return {tpr, (nch + tpr - 1) / tpr};
+}
+
+template <class T, int BLOCK, int TPR, int CPT>
+static void norm_fwd_at(const void* x, const NormParams& p, int64_t M, int64_t K, float eps, void* y, bool y_f32,
+                        float* mean, float* rstd, int8_t* codes, float* scales, hipStream_t st) {
+  constexpr int RPB = BLOCK / TPR;
+  layernorm_fwd_kernel<T, BLOCK, TPR, CPT><<<(unsigned)((M + RPB - 1) / RPB), BLOCK, 0, st>>>(
+      static_cast<const T*>(x), p, M, (int)K, eps, y, y_f32, mean, rstd, codes, scales, (int)(ckpt_pad(K) / 8));
+}
+
+#define BITNET_NORM_SHAPES(F)                                                                       \
+  F(64, 1) F(64, 2) F(64, 3) F(64, 4) F(64, 5) F(256, 2) F(256, 3) F(256, 4) F(256, 5) F(512, 3) \
+  F(512, 4) F(512, 5) F(512, 6) F(512, 7) F(512, 8)
+
+template <class T>
+static hipError_t norm_fwd(const void* x, const NormParams& p, int64_t M, int64_t K, float eps, void* y, bool y_f32,
+                           float* mean, float* rstd, int8_t* codes, float* scales, hipStream_t st) {
+  const RowSplit s = row_split(K);
+#define BITNET_CASE(TPR, CPT)                                                                                   \
+  if (s.tpr == TPR && s.cpt == CPT) {                                                                           \
+    norm_fwd_at<T, (TPR < 256 ? 256 : TPR), TPR, CPT>(x, p, M, K, eps, y, y_f32, mean, rstd, codes, scales, st); \
+    return hipGetLastError();                                                                                   \
+  }
+  BITNET_NORM_SHAPES(BITNET_CASE)
+#undef BITNET_CASE
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_layernorm_fwd(const void* x, bool x_f32, const void* w, const void* b, bool p_f32, int64_t M,
+                                int64_t K, float eps, void* y, bool y_f32, float* mean, float* rstd, int8_t* codes,
+                                float* scales, hipStream_t stream) {
+  const NormParams p{w, b, p_f32};
+  return x_f32 ? norm_fwd<float>(x, p, M, K, eps, y, y_f32, mean, rstd, codes, scales, stream)
+               : norm_fwd<uint16_t>(x, p, M, K, eps, y, y_f32, mean, rstd, codes, scales, stream);
+}
+
+// Blocks of the backward: enough for two of 256 threads on each of 256 CUs,
+// no more than there are row groups.
+constexpr int kNormBwdBlocks = 512;
+static int norm_bwd_blocks(int64_t M, int64_t K) {
+  const RowSplit s = row_split(K);
+  const int64_t rpb = s.tpr < 256 ? 256 / s.tpr : 1;
+  const int64_t groups = (M + rpb - 1) / rpb;
+  const int64_t most = s.tpr == 512 ? kNormBwdBlocks / 2 : kNormBwdBlocks;
+  return (int)(groups < most ? groups : most);
+}
+
+size_t layernorm_bwd_workspace(int64_t M, int64_t K) { return (size_t)norm_bwd_blocks(M, K) * 2 * (size_t)K * 4; }
+
+template <class X, class DX, class DY>
+static hipError_t norm_bwd(const NormBwd& a, hipStream_t st) {
+  const RowSplit s = row_split(a.K);
+  const int blocks = norm_bwd_blocks(a.M, a.K);
+#define BITNET_CASE(TPR, CPT)                                                                      \
+  if (s.tpr == TPR && s.cpt == CPT) {                                                              \
+    constexpr int BLOCK = TPR < 256 ? 256 : TPR;                                                   \
+    layernorm_bwd_kernel<X, DX, DY, BLOCK, TPR, CPT><<<blocks, BLOCK, (size_t)a.nch * 32, st>>>(a);    \
+    return hipGetLastError();                                                                      \
+  }
+  BITNET_NORM_SHAPES(BITNET_CASE)
+#undef BITNET_CASE
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_layernorm_bwd(const void* dY, bool dy_f32, const void* x, bool x_f32, const int8_t* codes,
+                                const float* scales, const void* w, bool p_f32, const float* mean, const float* rstd,
+                                int64_t M, int64_t K, void* dX, void* dw, void* db, void* ws, hipStream_t stream) {
+  NormBwd a{};
+  a.dY = dY;
+  a.x = x;
+  a.codes = codes;
+  a.scales = scales;
+  a.p = NormParams{w, nullptr, p_f32};
+  a.mean = mean;
+  a.rstd = rstd;
+  a.M = M;
+  a.K = (int)K;
+  a.nch = (int)(ckpt_pad(K) / 8);
+  a.dX = dX;
+  a.partials = dw || db ? static_cast<float*>(ws) : nullptr;
+  hipError_t e;
+  if (codes && x_f32) e = dy_f32 ? norm_bwd<FromCodes, float, float>(a, stream) : norm_bwd<FromCodes, float, uint16_t>(a, stream);
+  else if (codes) e = dy_f32 ? norm_bwd<FromCodes, uint16_t, float>(a, stream) : norm_bwd<FromCodes, uint16_t, uint16_t>(a, stream);
+  else if (x_f32) e = dy_f32 ? norm_bwd<FromF32, float, float>(a, stream) : norm_bwd<FromF32, float, uint16_t>(a, stream);
+  else e = dy_f32 ? norm_bwd<FromBf16, uint16_t, float>(a, stream) : norm_bwd<FromBf16, uint16_t, uint16_t>(a, stream);
+  if (e != hipSuccess || a.partials == nullptr) return e;
+  layernorm_cols_kernel<<<(unsigned)((2 * K + 63) / 64), 1024, 0, stream>>>(a.partials, norm_bwd_blocks(M, K), (int)K,
+                                                                            dw, db, p_f32);
+  return hipGetLastError();
+}
+
+}  // namespace bitnet

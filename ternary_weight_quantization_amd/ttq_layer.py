@@ -19,6 +19,7 @@ import math
 import torch
 
 from . import binding as B
+from .checkpoint import compress
 
 
 def _inverse_softplus(v):
@@ -67,10 +68,11 @@ class TTQFunction(torch.autograd.Function):
     """y = x @ W_t^T with W_t from Eq. 1. x [..., K] bf16, weight [N, K] bf16
     or float32, params float32 [3] = (delta, Wp, Wn), already positive.
     Gradients: dX bf16, dW in the weight's dtype, d params =
-    (0, dL/dWp, dL/dWn) (the threshold gets none)."""
+    (0, dL/dWp, dL/dWn) (the threshold gets none). checkpoint: x is kept for
+    the backward as 8-bit codes (``checkpoint.compress``)."""
 
     @staticmethod
-    def forward(ctx, x, weight, params):
+    def forward(ctx, x, weight, params, checkpoint=False):
         if x.dtype != torch.bfloat16:
             raise TypeError("TTQ expects bf16 activations")
         N, K = weight.shape
@@ -82,13 +84,23 @@ class TTQFunction(torch.autograd.Function):
         y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
         ws = _workspace(B.ttq_workspace_bytes(M, N, K), x.device)
         B.ttq_fwd(x2, wt, y, workspace=ws)
-        ctx.save_for_backward(x2, wt, w_packed)
+        ctx.checkpoint = checkpoint
+        if checkpoint:
+            # dW alone reads x
+            needs_x = ctx.needs_input_grad[1] or ctx.needs_input_grad[2]
+            codes, scales = compress(x2) if needs_x else (None, None)
+            ctx.save_for_backward(codes, scales, wt, w_packed)
+        else:
+            ctx.save_for_backward(x2, wt, w_packed)
         ctx.shape = (M, N, K, lead, weight.dtype)
         return y.reshape(*lead, N)
 
     @staticmethod
     def backward(ctx, dy):
-        x2, wt, w_packed = ctx.saved_tensors
+        if ctx.checkpoint:
+            codes, scales, wt, w_packed = ctx.saved_tensors
+        else:
+            x2, wt, w_packed = ctx.saved_tensors
         M, N, K, lead, wdtype = ctx.shape
         dY = dy.reshape(M, N).to(torch.bfloat16).contiguous()
         need_x, need_w, need_p = ctx.needs_input_grad[:3]
@@ -98,19 +110,33 @@ class TTQFunction(torch.autograd.Function):
         dW = torch.empty((N, K), dtype=wdtype, device=dy.device) if (need_w or need_p) else None
         dparams = torch.zeros((3,), dtype=torch.float32, device=dy.device) if need_p else None
         if dX is not None or dW is not None:
-            B.ttq_bwd(dY, x2, wt, w_packed, K, dX=dX, dW=dW, grads=None if dparams is None else dparams[1:],
-                      workspace=_workspace(B.ttq_workspace_bytes(M, N, K), dy.device))
-        return (None if dX is None else dX.reshape(*lead, K)), (dW if need_w else None), dparams
+            grads = None if dparams is None else dparams[1:]
+            if ctx.checkpoint:
+                B.ttq_bwd_ckpt(dY, codes, scales, wt, w_packed, K, dX=dX, dW=dW, grads=grads,
+                               workspace=_workspace(B.ttq_bwd_ckpt_workspace_bytes(M, N, K), dy.device))
+            else:
+                B.ttq_bwd(dY, x2, wt, w_packed, K, dX=dX, dW=dW, grads=grads,
+                          workspace=_workspace(B.ttq_workspace_bytes(M, N, K), dy.device))
+        return (None if dX is None else dX.reshape(*lead, K)), (dW if need_w else None), dparams, None
+
+
+def ttq_linear(x, weight, params, checkpoint=False):
+    """x [..., K] bf16 times the TTQ weight of (weight [N, K], params float32
+    [3] = (delta, Wp, Wn), positive): ``TTQFunction`` as a function.
+    ``checkpoint=True`` keeps x in 8 bits for dW."""
+    return TTQFunction.apply(x, weight, params, checkpoint)
 
 
 class TTQLinear(torch.nn.Module):
     """Linear layer with TTQ weights: latent weights [out, in] (bf16 or f32,
     kaiming-uniform(a=sqrt(5)) init like QATBitLinear) and three raw scalars
     whose softplus gives delta, Wp and Wn, initialized from the weights by
-    the library (Eq. 2)."""
+    the library (Eq. 2). checkpoint=True: the input is kept in 8 bits for the
+    backward (``checkpoint.compress``) instead of in bf16."""
 
-    def __init__(self, in_features, out_features, device="cuda", dtype=torch.bfloat16):
+    def __init__(self, in_features, out_features, device="cuda", dtype=torch.bfloat16, checkpoint=False):
         super().__init__()
+        self.checkpoint = checkpoint
         self.in_features = in_features
         self.out_features = out_features
         w = torch.empty((out_features, in_features), dtype=torch.float32)
@@ -137,7 +163,7 @@ class TTQLinear(torch.nn.Module):
         return torch.nn.functional.softplus(self.raw)
 
     def forward(self, x):
-        return TTQFunction.apply(x, self.weight, self.params())
+        return TTQFunction.apply(x, self.weight, self.params(), self.checkpoint)
 
     @torch.no_grad()
     def export_inference(self):
@@ -147,4 +173,5 @@ class TTQLinear(torch.nn.Module):
         return ttq_quantize(self.weight.detach(), p)[0], p
 
     def extra_repr(self):
-        return f"{self.in_features}, {self.out_features}, dtype={self.weight.dtype}"
+        return (f"{self.in_features}, {self.out_features}, dtype={self.weight.dtype}"
+                + (", checkpoint=True" if self.checkpoint else ""))
