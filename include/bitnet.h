@@ -520,6 +520,53 @@ bitnet_status ttq_bwd_ckpt(const uint16_t* dY, const int8_t* codes, const float*
                            void* stream);
 
 /*
+ * A linear layer with softmax cross entropy over a large vocabulary (the head
+ * and the loss of a language model), in pieces of the vocabulary, without
+ * keeping the logits:
+ *
+ *   z[t,v]  = sum_d h[t,d] * w[v,d]
+ *   lse[t]  = log sum_v exp z[t,v]
+ *   loss[t] = lse[t] - z[t,target[t]]    (0 where target[t] == ignore_index)
+ *   total   = sum_t loss[t], or the mean over the rows that count (0 if none)
+ *
+ *   G[t,v]  = c[t] * (exp(z[t,v] - lse[t]) - [v == target[t]])
+ *   dh[t,d] = sum_v G[t,v] * w[v,d],     dw[v,d] = sum_t G[t,v] * h[t,d]
+ *
+ * with c[t] the gradient of whatever is minimised with respect to loss[t]:
+ * dloss[t] (BITNET_REDUCE_NONE), *dloss (SUM), or *dloss divided by the
+ * number of rows that count (MEAN); 0 for ignored rows. Products are exact in
+ * fp32 and sums are fp32; G is rounded to bf16 between the products (a
+ * rounding of 2^-9 of each value, as the outputs'); the logits are never
+ * written. All sums run in a fixed order (bitwise deterministic). What an
+ * ignored row of h holds reaches nothing. A target outside 0..V-1 that is not
+ * ignore_index makes its row's loss, and gradients that it takes part in, NaN.
+ *
+ * h, dh    [T][D] bf16 bits.   w [V][D] bf16 bits.   targets [T] int64.
+ * loss, lse [T] float, written by the forward; lse is read by the backward.
+ * total    [1] float, or NULL.
+ * dw       [V][D] in dw_dtype (BITNET_BF16 or BITNET_F32). dh or dw may be
+ *          NULL (not computed), not both.
+ * Alignment: h, w, dh, dw and the workspace 16 bytes, targets 8, the rest 4.
+ * workspace: bitnet_xent_fwd_workspace_bytes / bitnet_xent_bwd_workspace_bytes
+ * (0 for sizes the call rejects); no initialization, not shared by calls that
+ * may run at the same time. The backward's holds G for one piece of the
+ * vocabulary (128 MiB at most, or 256 columns) and fp32 sums of dh.
+ * Limits: T <= 2^21, V <= 2^28, D <= 65536, (T + 256) * 2 * (D rounded up to
+ * 8) <= 2^31. Widths D that are multiples of 8 are fastest (others copy h,
+ * and w a piece at a time, to padded rows first).
+ */
+typedef enum { BITNET_REDUCE_NONE = 0, BITNET_REDUCE_SUM = 1, BITNET_REDUCE_MEAN = 2 } bitnet_reduce;
+size_t bitnet_xent_fwd_workspace_bytes(int64_t T, int64_t V, int64_t D);
+size_t bitnet_xent_bwd_workspace_bytes(int64_t T, int64_t V, int64_t D);
+bitnet_status bitnet_xent_fwd(const uint16_t* h, const uint16_t* w, const int64_t* targets, int64_t ignore_index,
+                              int64_t T, int64_t V, int64_t D, float* loss, float* lse, float* total,
+                              bitnet_reduce reduce, void* workspace, size_t workspace_bytes, void* stream);
+bitnet_status bitnet_xent_bwd(const uint16_t* h, const uint16_t* w, const int64_t* targets, int64_t ignore_index,
+                              const float* lse, const float* dloss, bitnet_reduce reduce, int64_t T, int64_t V,
+                              int64_t D, uint16_t* dh, void* dw, bitnet_dtype dw_dtype, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
  * Test hooks (for the library's own tests and tuning; not needed to use it).
  *
  * bitnet_set_test_knobs - process-wide knobs read by every later launch:

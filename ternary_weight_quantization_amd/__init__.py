@@ -5,14 +5,15 @@ The compute path is the HIP library ``libbitnet.so`` built from ``csrc/``
 with the same names; ``layer`` adds the autograd function and the
 ``QATBitLinear`` module, ``ttq_layer`` the same for the TTQ variant
 (``TTQLinear``), ``norm`` the layer norm that stands before them
-(``QATLayerNorm``) and ``checkpoint`` activations kept in 8 bits with the
-gated activation between them. Submodules load lazily so that importing the package (e.g.
+(``QATLayerNorm``), ``checkpoint`` activations kept in 8 bits with the
+gated activation between them, and ``loss`` the head of a language model with
+its cross entropy (``LinearCrossEntropy``). Submodules load lazily so that importing the package (e.g.
 for ``workloads``) neither imports torch nor loads the library.
 """
 
 import importlib
 
-_SUBMODULES = ("binding", "layer", "ttq_layer", "norm", "checkpoint", "workloads", "build")
+_SUBMODULES = ("binding", "layer", "ttq_layer", "norm", "checkpoint", "loss", "workloads", "build")
 
 __all__ = list(_SUBMODULES)
 
@@ -28,4 +29,6 @@ def __getattr__(name):
         return getattr(importlib.import_module(f"{__name__}.norm"), name)
     if name in ("compress", "decompress", "gated_activation"):
         return getattr(importlib.import_module(f"{__name__}.checkpoint"), name)
+    if name in ("LinearCrossEntropy", "linear_cross_entropy"):
+        return getattr(importlib.import_module(f"{__name__}.loss"), name)
     raise AttributeError(name)

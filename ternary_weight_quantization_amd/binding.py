@@ -111,6 +111,14 @@ def lib():
     L.ttq_bwd_ckpt_workspace_bytes.restype = sz
     L.ttq_bwd_ckpt.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, vp, vp, st, vp, vp, sz, vp]
     L.ttq_bwd_ckpt.restype = st
+    L.bitnet_xent_fwd_workspace_bytes.argtypes = [i64, i64, i64]
+    L.bitnet_xent_fwd_workspace_bytes.restype = sz
+    L.bitnet_xent_bwd_workspace_bytes.argtypes = [i64, i64, i64]
+    L.bitnet_xent_bwd_workspace_bytes.restype = sz
+    L.bitnet_xent_fwd.argtypes = [vp, vp, vp, i64, i64, i64, i64, vp, vp, vp, st, vp, sz, vp]
+    L.bitnet_xent_fwd.restype = st
+    L.bitnet_xent_bwd.argtypes = [vp, vp, vp, i64, vp, vp, st, i64, i64, i64, vp, vp, st, vp, sz, vp]
+    L.bitnet_xent_bwd.restype = st
     i32, u32 = ctypes.c_int32, ctypes.c_uint32
     L.bitnet_set_test_knobs.argtypes = [st, st, st, u32]
     L.bitnet_set_test_knobs.restype = None
@@ -697,6 +705,68 @@ def bitnet_gate_bwd(act, dY, dgate, dup=None, gate=None, up=None, gate_codes=Non
                  up_codes=up_codes, up_scales=up_scales)
     _run(lib().bitnet_gate_bwd, dY, stream, int(act), _ptr(dY), _ptr(gate), ldg, _ptr(up), ldu, _ptr(gate_codes),
          _ptr(gate_scales), _ptr(up_codes), _ptr(up_scales), M, K, _ptr(dgate), lddg, _ptr(dup), lddu)
+
+
+# --- linear layer with softmax cross entropy -------------------------------------
+
+BITNET_REDUCE_NONE = 0
+BITNET_REDUCE_SUM = 1
+BITNET_REDUCE_MEAN = 2
+
+
+def bitnet_xent_fwd_workspace_bytes(T, V, D):
+    return int(lib().bitnet_xent_fwd_workspace_bytes(int(T), int(V), int(D)))
+
+
+def bitnet_xent_bwd_workspace_bytes(T, V, D):
+    return int(lib().bitnet_xent_bwd_workspace_bytes(int(T), int(V), int(D)))
+
+
+def _need_xent(h, w, targets):
+    T, D = h.shape
+    V = w.shape[0]
+    _need(h, torch.bfloat16, (T, D), "h")
+    _need(w, torch.bfloat16, (V, D), "w")
+    _need(targets, torch.int64, (T,), "targets")
+    return T, V, D
+
+
+def bitnet_xent_fwd(h, w, targets, ignore_index, loss, lse, total=None, reduce=BITNET_REDUCE_NONE, workspace=None,
+                    stream=None):
+    """loss, lse float32 [T] of the logits h [T, D] bf16 @ w [V, D]^T bf16
+    with int64 targets [T], and total float32 [1], their sum or mean."""
+    T, V, D = _need_xent(h, w, targets)
+    _need(loss, torch.float32, (T,), "loss")
+    _need(lse, torch.float32, (T,), "lse")
+    if total is not None:
+        _need(total, torch.float32, (1,), "total")
+    _same_device(h, w=w, targets=targets, loss=loss, lse=lse, total=total, workspace=workspace)
+    if workspace is None:
+        workspace = _workspace(bitnet_xent_fwd_workspace_bytes(T, V, D), h, stream)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _run(lib().bitnet_xent_fwd, h, stream, _ptr(h), _ptr(w), _ptr(targets), int(ignore_index), T, V, D, _ptr(loss),
+         _ptr(lse), _ptr(total), int(reduce), _ptr(workspace), ws_bytes)
+
+
+def bitnet_xent_bwd(h, w, targets, ignore_index, lse, dloss, dh=None, dw=None, reduce=BITNET_REDUCE_NONE,
+                    workspace=None, stream=None):
+    """dh [T, D] bf16 and/or dw [V, D] (bf16 or float32) from lse and dloss
+    (float32 [T], or [1] with a sum or mean)."""
+    T, V, D = _need_xent(h, w, targets)
+    _need(lse, torch.float32, (T,), "lse")
+    _need(dloss, torch.float32, (T,) if int(reduce) == BITNET_REDUCE_NONE else (1,), "dloss")
+    if dh is not None:
+        _need(dh, torch.bfloat16, (T, D), "dh")
+    dd = BITNET_BF16
+    if dw is not None:
+        dd = _value_dtype(dw, "dw")
+        _need(dw, dw.dtype, (V, D), "dw")
+    _same_device(h, w=w, targets=targets, lse=lse, dloss=dloss, dh=dh, dw=dw, workspace=workspace)
+    if workspace is None:
+        workspace = _workspace(bitnet_xent_bwd_workspace_bytes(T, V, D), h, stream)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _run(lib().bitnet_xent_bwd, h, stream, _ptr(h), _ptr(w), _ptr(targets), int(ignore_index), _ptr(lse), _ptr(dloss),
+         int(reduce), T, V, D, _ptr(dh), _ptr(dw), dd, _ptr(workspace), ws_bytes)
 
 
 # --- test hooks --------------------------------------------------------------

@@ -92,6 +92,12 @@ bitnet_status check_ckpt_sizes(int64_t M, int64_t K) {
 }
 bool row_stride_ok(int64_t ld, int64_t K) { return ld >= K && ld <= bitnet::k_pad(int64_t(1) << 30); }
 
+bitnet_status check_xent_sizes(int64_t T, int64_t V, int64_t D) {
+  if (T < 1 || V < 1 || D < 1 || T > (int64_t(1) << 21) || V > (int64_t(1) << 28) || D > 65536) return BITNET_ERR_SHAPE;
+  return buffer_range_ok(T, 2 * ((D + 7) / 8 * 8)) ? BITNET_OK : BITNET_ERR_SHAPE;
+}
+bool is_reduce(bitnet_reduce r) { return r == BITNET_REDUCE_NONE || r == BITNET_REDUCE_SUM || r == BITNET_REDUCE_MEAN; }
+
 // The bf16 x that ttq_bwd_ckpt unpacks at the start of its workspace.
 size_t ckpt_x_bytes(int64_t M, int64_t K) { return ((size_t)M * K * 2 + 255) / 256 * 256; }
 
@@ -451,6 +457,48 @@ bitnet_status ttq_bwd_ckpt(const uint16_t* dY, const int8_t* codes, const float*
       return from_hip(e);
   return ttq_bwd(dY, x, wt, w_packed, M, N, K, dX, dW, dW_dtype, grads, static_cast<char*>(workspace) + xb,
                  workspace_bytes - xb, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Linear layer with softmax cross entropy
+// ---------------------------------------------------------------------------
+
+size_t bitnet_xent_fwd_workspace_bytes(int64_t T, int64_t V, int64_t D) {
+  return check_xent_sizes(T, V, D) != BITNET_OK ? 0 : bitnet::xent_workspace(T, V, D, false);
+}
+size_t bitnet_xent_bwd_workspace_bytes(int64_t T, int64_t V, int64_t D) {
+  return check_xent_sizes(T, V, D) != BITNET_OK ? 0 : bitnet::xent_workspace(T, V, D, true);
+}
+
+bitnet_status bitnet_xent_fwd(const uint16_t* h, const uint16_t* w, const int64_t* targets, int64_t ignore_index,
+                              int64_t T, int64_t V, int64_t D, float* loss, float* lse, float* total,
+                              bitnet_reduce reduce, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!h || !w || !targets || !loss || !lse) return BITNET_ERR_NULL;
+  if (!is_reduce(reduce)) return BITNET_ERR_DTYPE;
+  if (total ? reduce == BITNET_REDUCE_NONE : reduce != BITNET_REDUCE_NONE) return BITNET_ERR_NULL;
+  if (bitnet_status st = check_xent_sizes(T, V, D)) return st;
+  if (!workspace || workspace_bytes < bitnet_xent_fwd_workspace_bytes(T, V, D)) return BITNET_ERR_WORKSPACE;
+  if (!aligned(workspace, 16) || !aligned(h, 16) || !aligned(w, 16) || !aligned(targets, 8) || !aligned(loss, 4) ||
+      !aligned(lse, 4) || !aligned(total, 4))
+    return BITNET_ERR_ALIGN;
+  return from_hip(bitnet::launch_xent_fwd(h, w, targets, ignore_index, T, V, D, loss, lse, total,
+                                          reduce == BITNET_REDUCE_MEAN, workspace, static_cast<hipStream_t>(stream)));
+}
+
+bitnet_status bitnet_xent_bwd(const uint16_t* h, const uint16_t* w, const int64_t* targets, int64_t ignore_index,
+                              const float* lse, const float* dloss, bitnet_reduce reduce, int64_t T, int64_t V,
+                              int64_t D, uint16_t* dh, void* dw, bitnet_dtype dw_dtype, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  if (!h || !w || !targets || !lse || !dloss || (!dh && !dw)) return BITNET_ERR_NULL;
+  if (!is_reduce(reduce) || (dw && !is_value(dw_dtype))) return BITNET_ERR_DTYPE;
+  if (bitnet_status st = check_xent_sizes(T, V, D)) return st;
+  if (!workspace || workspace_bytes < bitnet_xent_bwd_workspace_bytes(T, V, D)) return BITNET_ERR_WORKSPACE;
+  if (!aligned(workspace, 16) || !aligned(h, 16) || !aligned(w, 16) || !aligned(targets, 8) || !aligned(lse, 4) ||
+      !aligned(dloss, 4) || !aligned(dh, 16) || !aligned(dw, 16))
+    return BITNET_ERR_ALIGN;
+  return from_hip(bitnet::launch_xent_bwd(h, w, targets, ignore_index, lse, dloss, reduce == BITNET_REDUCE_NONE,
+                                          reduce == BITNET_REDUCE_MEAN, T, V, D, dh, dw, dw_dtype == BITNET_F32,
+                                          workspace, static_cast<hipStream_t>(stream)));
 }
 
 // ---------------------------------------------------------------------------

@@ -206,4 +206,13 @@ hipError_t launch_layernorm_bwd(const void* dY, bool dy_f32, const void* x, bool
                                 const float* scales, const void* w, bool p_f32, const float* mean, const float* rstd,
                                 int64_t M, int64_t K, void* dX, void* dw, void* db, void* ws, hipStream_t stream);
 
+// Linear layer with softmax cross entropy (h [T][D], w [V][D] bf16).
+size_t xent_workspace(int64_t T, int64_t V, int64_t D, bool bwd);
+hipError_t launch_xent_fwd(const uint16_t* h, const uint16_t* w, const int64_t* targets, int64_t ignore, int64_t T,
+                           int64_t V, int64_t D, float* loss, float* lse, float* total, bool mean, void* ws,
+                           hipStream_t stream);
+hipError_t launch_xent_bwd(const uint16_t* h, const uint16_t* w, const int64_t* targets, int64_t ignore,
+                           const float* lse, const float* dloss, bool per_row, bool mean, int64_t T, int64_t V,
+                           int64_t D, uint16_t* dh, void* dw, bool dw_f32, void* ws, hipStream_t stream);
+
 }  // namespace bitnet

@@ -1,0 +1,898 @@
+// A linear layer with softmax cross entropy at the end of a language model,
+// in pieces of the vocabulary, without keeping the logits.
+//
+//   z[t][v]  = sum_d h[t][d] W[v][d]
+//   lse[t]   = log sum_v exp z[t][v],   loss[t] = lse[t] - z[t][target[t]]
+//   G[t][v]  = c[t] (exp(z[t][v] - lse[t]) - [v == target[t]])
+//   dh       = G W,   dW = G^T h
+//
+// (c[t]: the loss' gradient with respect to loss[t].) The three products are
+// bf16 MFMA GEMMs with fp32 sums, so the whole is MFMA bound for many tokens:
+// 2TVD operations for the loss, 4TVD for the gradients and 2TVD for the
+// logits computed again, because keeping them would take 4TV bytes (2 GB at
+// 4096 x 128256). For few tokens the loss is bound by reading W once.
+//
+// Rows whose target is ignore_index are taken out first: the rows that count
+// are gathered to the front (hc), so that an ignored row costs nothing and
+// nothing it holds, NaN included, reaches a sum. The number n of rows that
+// count stays on the device; tiles past it leave at once.
+//
+// Many tokens:
+//   gather   rows, targets, (backward) lse and c of the rows that count
+//   logits   forward: one 256 x 256 tile of z per workgroup, reduced in the
+//            epilogue to a maximum and a sum of exponentials per token and
+//            128 columns, and the target's logit; nothing else is written
+//   combine  lse and the loss per row from those pairs; then their sum
+//   logits   backward: the same tiles again, G rounded to bf16 for one piece
+//            of the vocabulary at a time (small enough to stay in the last
+//            level cache until it is read)
+//   grads    both products of a piece in one launch: dh's tiles, split over
+//            the piece's columns where they are few, accumulate in fp32
+//            slabs; dW's tiles are final
+//   dh       the slabs summed in a fixed order, rounded once, scattered back
+//            to the rows; ignored rows get zeros
+// No atomics: the same inputs give the same bits.
+
+#include <algorithm>
+
+#include "gemm_core.h"
+#include "internal.h"
+#include "row_io.h"
+
+namespace bitnet {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// Control block at the start of the workspace: n.
+struct XentCtl {
+  int n;
+};
+
+// ---------------------------------------------------------------------------
+// Rows that count
+// ---------------------------------------------------------------------------
+
+struct XentRows {
+  const uint16_t* h;       // [T][D]
+  const int64_t* targets;  // [T]
+  int64_t ignore;
+  int T, D, Dp;            // Dp: D rounded up to 8
+  int64_t V;
+  XentCtl* ctl;
+  uint16_t* hc;            // [T][Dp] rows that count, in order
+  int* pos;                // [T] row -> index among them, -1: ignored
+  int* ct;                 // [T] their targets, -1: out of range
+  // backward only
+  const float* lse;        // [T]
+  const float* dloss;      // [1], or [T] with per_row
+  int per_row, mean;
+  float* lse2;             // [T] lse log2(e) of the rows that count
+  float* c;                // [T] their c
+};
+
+constexpr int kGatherRows = 16;
+
+// Each block finds how many rows that count precede its own and how many
+// there are by reading all targets (a few KB out of L2), so that no launch
+// or wait between blocks is needed.
+template <bool BWD>
+__global__ __launch_bounds__(256) void xent_gather_kernel(XentRows a) {
+  __shared__ int before[4], all[4];
+  const int t0 = blockIdx.x * kGatherRows, tid = threadIdx.x;
+  int b = 0, n = 0;
+  for (int t = tid; t < a.T; t += 256) {
+    const int v = a.targets[t] != a.ignore;
+    n += v;
+    b += v & (t < t0);
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) {
+    b += __shfl_xor(b, off, kWave);
+    n += __shfl_xor(n, off, kWave);
+  }
+  if ((tid & 63) == 0) {
+    before[tid >> 6] = b;
+    all[tid >> 6] = n;
+  }
+  __syncthreads();
+  b = (before[0] + before[1]) + (before[2] + before[3]);
+  n = (all[0] + all[1]) + (all[2] + all[3]);
+  if (blockIdx.x == 0 && tid == 0) a.ctl->n = n;
+  const int nch = a.Dp / 8;
+  for (int r = 0; r < kGatherRows; ++r) {
+    const int t = t0 + r;
+    if (t >= a.T) break;
+    const int64_t target = a.targets[t];
+    if (target == a.ignore) {
+      if (tid == 0) a.pos[t] = -1;
+      continue;
+    }
+    const int at = b++;
+    const bool in = target >= 0 && target < a.V;
+    if (tid == 0) {
+      a.pos[t] = at;
+      a.ct[at] = in ? (int)target : -1;
+      if constexpr (BWD) {
+        float c = a.per_row ? a.dloss[t] : *a.dloss;
+        if (a.mean) c /= (float)n;
+        a.lse2[at] = a.lse[t] * kLog2e;
+        a.c[at] = in ? c : __uint_as_float(0x7FC00000u);  // a target out of range: NaN gradients
+      }
+    }
+    const uint16_t* src = a.h + (int64_t)t * a.D;
+    for (int ch = tid; ch < nch; ch += 256) {
+      ChunkBf16 v = load8(src, 8 * ch, a.D);
+      settle8(v, 8 * ch, a.D);
+      reinterpret_cast<uint4*>(a.hc + (int64_t)at * a.Dp)[ch] = v.v;
+    }
+  }
+}
+
+// Rows of W padded to a whole number of 16-byte chunks (a width that is not a
+// multiple of 8).
+__global__ __launch_bounds__(256) void xent_pad_kernel(const uint16_t* __restrict__ w, int64_t rows, int D, int nch,
+                                                       uint16_t* __restrict__ out) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= rows * nch) return;
+  const int64_t r = i / nch;
+  const int k0 = 8 * (int)(i - r * nch);
+  ChunkBf16 v = load8(w + r * D, k0, D);
+  settle8(v, k0, D);
+  reinterpret_cast<uint4*>(out)[i] = v.v;
+}
+
+// ---------------------------------------------------------------------------
+// Logit tiles
+// ---------------------------------------------------------------------------
+
+struct XentTiles {
+  const uint16_t* w;  // [vc][ldw] rows of the piece
+  int64_t ldw;
+  int vc;             // valid rows
+  int v0;             // the piece's first row
+  int tiles_v, tiles_t, nstages;
+  const uint16_t* hc;  // [n][Dp]
+  int Dp;
+  const XentCtl* ctl;
+  const int* ct;
+  // forward
+  float2* part;  // [2 tiles of 128 columns][T]: reference in base 2, sum
+  int T;
+  float* zt;     // [n] the target's logit
+  // backward
+  const float* lse2;
+  const float* c;
+  uint16_t* G;   // [n][ldg]
+  int ldg;
+};
+
+// Tile p of tiles_v x tiles_t: groups of kGroupV rows of tiles, within a
+// group v fastest, so that the workgroups that run together on an XCD share
+// both their W and their h panels in its L2.
+constexpr int kGroupV = 4;
+__device__ __forceinline__ void xent_tile(int p, int tiles_v, int tiles_t, int& tv, int& tt) {
+  const int g = p / (kGroupV * tiles_t), r = p - g * kGroupV * tiles_t;
+  const int width = min(kGroupV, tiles_v - g * kGroupV);
+  tt = r / width;
+  tv = g * kGroupV + r - tt * width;
+}
+
+// Value e of a lane's 16 of fragment fi: row 32 fi + row_of(e, lane).
+__device__ __forceinline__ int row_of(int e, int lane) { return 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3); }
+
+typedef MfmaBf16::Acc AccTile[kFI][kFJ];
+
+// Forward epilogue of a wave's 128 columns x 128 tokens: the maximum M of
+// z log2(e) and the sum of 2^(z log2(e) - M) per token, over both lanes that
+// hold a token. M is the rounded product, the same in every term, so the
+// pair means sum 2^M exactly.
+__device__ __forceinline__ void xent_stats(const XentTiles& a, const AccTile& acc, int i0, int j0, int n, int lane) {
+  const bool whole = i0 + kWTI <= a.vc;  // uniform
+#pragma unroll
+  for (int fj = 0; fj < kFJ; ++fj) {
+    const int j = j0 + 32 * fj + (lane & 31);
+    float m = -INFINITY;
+#pragma unroll
+    for (int fi = 0; fi < kFI; ++fi)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float z = acc[fi][fj][e];
+        if (whole || i0 + 32 * fi + row_of(e, lane) < a.vc) m = fmaxf(m, z);
+      }
+    m = fmaxf(m, __shfl_xor(m, 32, kWave));
+    const float ref = m == -INFINITY ? 0.0f : m * kLog2e;
+    float s = 0.0f;
+#pragma unroll
+    for (int fi = 0; fi < kFI; ++fi)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float p = __builtin_amdgcn_exp2f(fmaf(acc[fi][fj][e], kLog2e, -ref));
+        if (whole || i0 + 32 * fi + row_of(e, lane) < a.vc) s += p;
+      }
+    s += __shfl_xor(s, 32, kWave);
+    if (j < n) {
+      if (lane < 32) a.part[(int64_t)((a.v0 + i0) / kWTI) * a.T + j] = make_float2(ref, s);
+      const int t = a.ct[j] - a.v0 - i0;  // the target's row in this tile?
+      if (t >= 0 && t < kWTI && t < a.vc - i0 && ((t >> 2) & 1) == (lane >> 5)) {
+#pragma unroll
+        for (int fi = 0; fi < kFI; ++fi)
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (t == 32 * fi + row_of(e, lane)) a.zt[j] = acc[fi][fj][e];
+      }
+    }
+  }
+}
+
+// Backward epilogue: G of the tile, rounded to bf16 (the operand of both
+// products; the rounding, 2^-9 of each value, is the size of the outputs'
+// own), zeros in the columns past the piece.
+__device__ __forceinline__ void xent_g(const XentTiles& a, AccTile& acc, int i0, int j0, int n, int lane, char* wlds) {
+  const bool whole = i0 + kWTI <= a.vc;
+  float c[kFJ], l[kFJ];
+  int t[kFJ];
+#pragma unroll
+  for (int fj = 0; fj < kFJ; ++fj) {
+    const int j = j0 + 32 * fj + (lane & 31);
+    c[fj] = j < n ? a.c[j] : 0.0f;
+    l[fj] = j < n ? a.lse2[j] : 0.0f;
+    t[fj] = j < n ? a.ct[j] - a.v0 - i0 : -1;
+  }
+#pragma unroll
+  for (int fj = 0; fj < kFJ; ++fj) {
+    const bool here = t[fj] >= 0 && t[fj] < kWTI;
+#pragma unroll
+    for (int fi = 0; fi < kFI; ++fi)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        float p = __builtin_amdgcn_exp2f(fmaf(acc[fi][fj][e], kLog2e, -l[fj]));
+        acc[fi][fj][e] = p;
+      }
+    if (here) {  // rare: a target among these 128 columns
+#pragma unroll
+      for (int fi = 0; fi < kFI; ++fi)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (t[fj] == 32 * fi + row_of(e, lane)) acc[fi][fj][e] -= 1.0f;
+    }
+#pragma unroll
+    for (int fi = 0; fi < kFI; ++fi)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = acc[fi][fj][4 * g + e] * c[fj];
+          if (!whole && i0 + 32 * fi + row_of(4 * g + e, lane) >= a.vc) v[e] = 0.0f;
+        }
+        EpStage<2>::put(wlds, lane, fi, g, make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])));
+      }
+    EpStage<2>::drain(wlds, reinterpret_cast<char*>(a.G), a.ldg, n, i0, j0 + 32 * fj, lane);
+  }
+}
+
+typedef CopyLoader<2, true, 1> XentW;
+typedef CopyLoader<2, true, 5> XentH;
+
+template <bool BWD>
+__global__ __launch_bounds__(kThreads, 1) void xent_logits_kernel(XentTiles a) {
+  typedef SmemLayout<XentW, XentH> L;
+  __shared__ __attribute__((aligned(16))) char smem[L::kBytes];
+  static_assert(4 * EpStage<2>::kWaveBytes <= L::kBytes, "the epilogue's staging fits the stage buffers");
+  const int n = a.ctl->n;
+  int tv, tt;
+  xent_tile(cta_order(blockIdx.x, gridDim.x), a.tiles_v, a.tiles_t, tv, tt);
+  const int i0 = tv * kBI, j0 = tt * kBJ;
+  if (j0 >= n) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int pi = (wave % kWavesI) * kWTI, qj = (wave / kWavesI) * kWTJ;
+  const XentW pl{reinterpret_cast<const char*>(a.w), 2 * a.ldw, a.vc, 2 * (int64_t)a.Dp};
+  const XentH ql{reinterpret_cast<const char*>(a.hc), 2 * (int64_t)a.Dp, n, 2 * (int64_t)a.Dp};
+  AccTile acc;
+#pragma unroll
+  for (int fi = 0; fi < kFI; ++fi)
+#pragma unroll
+    for (int fj = 0; fj < kFJ; ++fj) zero_acc(acc[fi][fj]);
+  run_stages<MfmaBf16, 1>(pl, ql, smem, acc, i0, j0, 0, a.nstages, pi, qj, lane, nullptr, 0);
+  if constexpr (BWD) xent_g(a, acc, i0 + pi, j0 + qj, n, lane, smem + wave * EpStage<2>::kWaveBytes);
+  else xent_stats(a, acc, i0 + pi, j0 + qj, n, lane);
+}
+
+// ---------------------------------------------------------------------------
+// Loss from the partial statistics
+// ---------------------------------------------------------------------------
+
+// pos == NULL: the rows are the tokens themselves (none gathered).
+struct XentLoss {
+  const float2* part;  // [parts][T]
+  int parts, T;
+  const float* zt;
+  const int* pos;
+  const int64_t* targets;
+  int64_t ignore, V;
+  float* lse;
+  float* loss;
+};
+
+// (m, s) += (m1, s1): sums of 2^ references; an empty one has m = -inf.
+__device__ __forceinline__ void xent_join(float& m, float& s, float m1, float s1) {
+  const float top = fmaxf(m, m1);
+  if (top == -INFINITY) return;
+  s = s * __builtin_amdgcn_exp2f(m - top) + s1 * __builtin_amdgcn_exp2f(m1 - top);
+  m = top;
+}
+
+// A block takes 16 tokens (a part's 16 pairs are one 128-byte line) and 64
+// groups of parts: 4 groups in a wave, joined by shuffles, then 16 waves.
+constexpr int kLossTokens = 16;
+__global__ __launch_bounds__(1024) void xent_combine_kernel(XentLoss a) {
+  __shared__ float sm[16][kLossTokens], ss[16][kLossTokens];
+  const int l = threadIdx.x % kLossTokens, g = threadIdx.x / kLossTokens;
+  const int t = blockIdx.x * kLossTokens + l;
+  const int64_t target = t < a.T ? a.targets[t] : a.ignore;
+  const bool counts = target != a.ignore;
+  const int at = !counts ? -1 : a.pos ? a.pos[t] : t;
+  float m = -INFINITY, s = 0.0f;
+  if (at >= 0) {
+    const float2* src = a.part + at;
+    int p = g;
+    for (; p + 192 < a.parts; p += 256) {  // four loads in flight
+      const float2 v0 = src[(int64_t)p * a.T], v1 = src[(int64_t)(p + 64) * a.T], v2 = src[(int64_t)(p + 128) * a.T],
+                   v3 = src[(int64_t)(p + 192) * a.T];
+      xent_join(m, s, v0.x, v0.y);
+      xent_join(m, s, v1.x, v1.y);
+      xent_join(m, s, v2.x, v2.y);
+      xent_join(m, s, v3.x, v3.y);
+    }
+    for (; p < a.parts; p += 64) {
+      const float2 v = src[(int64_t)p * a.T];
+      xent_join(m, s, v.x, v.y);
+    }
+  }
+#pragma unroll
+  for (int off = 16; off <= 32; off <<= 1) {
+    const float m1 = __shfl_xor(m, off, kWave), s1 = __shfl_xor(s, off, kWave);
+    xent_join(m, s, m1, s1);
+  }
+  if ((threadIdx.x & 63) < kLossTokens) {
+    sm[threadIdx.x >> 6][l] = m;
+    ss[threadIdx.x >> 6][l] = s;
+  }
+  __syncthreads();
+  if (threadIdx.x >= kLossTokens || t >= a.T) return;
+  if (!counts) {
+    a.lse[t] = 0.0f;
+    a.loss[t] = 0.0f;
+    return;
+  }
+#pragma unroll
+  for (int w = 1; w < 16; ++w) xent_join(m, s, sm[w][l], ss[w][l]);
+  const float lse = (m + __builtin_amdgcn_logf(s)) * kLn2;  // v_log_f32: base 2
+  a.lse[t] = lse;
+  a.loss[t] = target < 0 || target >= a.V ? __uint_as_float(0x7FC00000u) : lse - a.zt[at];
+}
+
+// The rows' sum or mean over the rows that count (0 where none does), in fp64
+// in a fixed order.
+__global__ __launch_bounds__(1024) void xent_reduce_kernel(const float* __restrict__ loss,
+                                                           const int64_t* __restrict__ targets, int64_t ignore, int T,
+                                                           int mean, float* __restrict__ out) {
+  __shared__ double part[16];
+  __shared__ int cnt[16];
+  double v = 0.0;
+  int n = 0;
+  for (int t = threadIdx.x; t < T; t += 1024) {
+    v += (double)loss[t];
+    n += targets[t] != ignore;
+  }
+  v = wave_sum_f64(v);
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) n += __shfl_xor(n, off, kWave);
+  if ((threadIdx.x & 63) == 0) {
+    part[threadIdx.x >> 6] = v;
+    cnt[threadIdx.x >> 6] = n;
+  }
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  v = 0.0;
+  n = 0;
+  for (int w = 0; w < 16; ++w) {
+    v += part[w];
+    n += cnt[w];
+  }
+  *out = (float)(mean && n > 0 ? v / (double)n : v);
+}
+
+// ---------------------------------------------------------------------------
+// Few tokens: one pass over W. A workgroup takes 32 rows of W, its 4 waves
+// every 4th stage of 64 columns; both operands go from memory straight to
+// the fragments (each lane reads 64 contiguous bytes of a row per stage), the
+// waves' sums meet in LDS, and the first wave reduces the tile to one pair
+// per token and 32 rows.
+// ---------------------------------------------------------------------------
+
+constexpr int kFewTokens = 64;
+constexpr int kFewWaves = 4;
+
+struct XentFew {
+  const uint16_t* w;  // [V][D], D a multiple of 8
+  int64_t V;
+  int D;
+  const uint16_t* h;  // [T][D]
+  int T;
+  const int64_t* targets;
+  float2* part;  // [ceil(V / 32)][T]
+  float* zt;     // [T]
+};
+
+template <int MT>
+__global__ __launch_bounds__(kWave * kFewWaves) void xent_few_kernel(XentFew a) {
+  __shared__ float red[kFewWaves][MT][16][kWave];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int64_t v0 = (int64_t)blockIdx.x * 32;
+  const int D = a.D, half = lane >> 5;
+  const int rows = (int)(a.V - v0 < 32 ? a.V - v0 : 32);
+  const rsrc_t rw = make_rsrc(a.w + v0 * D, (uint32_t)(rows * D * 2));
+  const rsrc_t rh = make_rsrc(a.h, (uint32_t)(a.T * D * 2));
+  const uint32_t wo = (uint32_t)((lane & 31) * D * 2);
+  uint32_t ho[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) ho[m] = (uint32_t)((32 * m + (lane & 31)) * D * 2);
+  MfmaBf16::Acc acc[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) zero_acc(acc[m]);
+  const int stages = (D + 63) / 64;
+  uint4 pw[4], ph[MT][4];
+  const auto load = [&](int s) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int k = 64 * s + 32 * half + 8 * c;  // columns past D: an out-of-range offset
+      pw[c] = buf_load16(rw, k < D ? wo + 2 * k : kOob);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) ph[m][c] = buf_load16(rh, k < D ? ho[m] + 2 * k : kOob);
+    }
+  };
+  load(wave);
+  for (int s = wave; s < stages; s += kFewWaves) {
+    uint4 cw[4], ch[MT][4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      cw[c] = pw[c];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) ch[m][c] = ph[m][c];
+    }
+    load(s + kFewWaves);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+        acc[m] = MfmaBf16::mma(__builtin_bit_cast(MfmaBf16::Frag, cw[c]), __builtin_bit_cast(MfmaBf16::Frag, ch[m][c]),
+                               acc[m]);
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) red[wave][m][e][lane] = acc[m][e];
+  __syncthreads();
+  if (wave >= MT) return;
+  const int m = wave, t = 32 * m + (lane & 31);
+  float z[16], top = -INFINITY;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    z[e] = (red[0][m][e][lane] + red[1][m][e][lane]) + (red[2][m][e][lane] + red[3][m][e][lane]);
+    if (row_of(e, lane) < rows) top = fmaxf(top, z[e]);
+  }
+  top = fmaxf(top, __shfl_xor(top, 32, kWave));
+  const float ref = top == -INFINITY ? 0.0f : top * kLog2e;
+  float s = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const float p = __builtin_amdgcn_exp2f(fmaf(z[e], kLog2e, -ref));
+    if (row_of(e, lane) < rows) s += p;
+  }
+  s += __shfl_xor(s, 32, kWave);
+  if (t >= a.T) return;
+  if (half == 0) a.part[(int64_t)blockIdx.x * a.T + t] = make_float2(ref, s);
+  const int64_t r = a.targets[t] - v0;
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    if (r == row_of(e, lane) && r < rows) a.zt[t] = z[e];
+}
+
+// ---------------------------------------------------------------------------
+// Gradients of one piece
+// ---------------------------------------------------------------------------
+
+struct XentGrads {
+  const uint16_t* G;  // [n][ldg]
+  int ldg;
+  const uint16_t* w;  // [vc][ldw]
+  int64_t ldw;
+  int vc;
+  const uint16_t* hc;  // [n][Dp]
+  int Dp, D, T;
+  const XentCtl* ctl;
+  // dh: tiles_d x tiles_t tiles, each split over `split` ranges of the
+  // piece's stages, into slab[split][T][D]
+  int tiles_d, tiles_t, split, stages_v;
+  int first;  // the first piece: the slabs are written, else added to
+  float* slab;
+  int dh_units;
+  // dW: tiles_d x tiles_v tiles
+  void* dw;  // the piece's rows [vc][D]
+};
+
+// fp32 sums into out[j][i] (rows of I), added to what is there unless
+// `first`.
+struct AccumEpilogue {
+  float* out;
+  int64_t I, J;
+  bool first;
+  __device__ __forceinline__ void store(AccTile& acc, int i0, int j0, int lane, char* wlds) const {
+    typedef EpStage<4> E;
+    i0 = __builtin_amdgcn_readfirstlane(i0);
+    j0 = __builtin_amdgcn_readfirstlane(j0);
+#pragma unroll
+    for (int fj = 0; fj < kFJ; ++fj) {
+#pragma unroll
+      for (int fi = 0; fi < kFI; ++fi)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          E::put(wlds, lane, fi, g,
+                 make_uint4(__float_as_uint(acc[fi][fj][4 * g]), __float_as_uint(acc[fi][fj][4 * g + 1]),
+                            __float_as_uint(acc[fi][fj][4 * g + 2]), __float_as_uint(acc[fi][fj][4 * g + 3])));
+      const int c = lane % E::kChunks, rl = lane / E::kChunks;
+      const int64_t i = i0 + 4 * c;
+#pragma unroll
+      for (int k = 0; k < E::kGets; ++k) {
+        const uint4 v = *reinterpret_cast<const uint4*>(wlds + (rl + k * E::kRowsPerGet) * E::kPitch + 16 * c);
+        const int64_t j = j0 + 32 * fj + k * E::kRowsPerGet + rl;
+        if (j >= J || i >= I) continue;
+        float* o = out + j * I + i;
+        if (i + 4 <= I) {
+          float4 f = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+          if (!first) {
+            float4 p;
+            memcpy(&p, o, 16);
+            f.x += p.x; f.y += p.y; f.z += p.z; f.w += p.w;
+          }
+          memcpy(o, &f, 16);
+        } else {
+          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (i + e < I) o[e] = (first ? 0.0f : o[e]) + __uint_as_float(u[e]);
+        }
+      }
+    }
+  }
+};
+
+// dW's tile: rounded once to its type.
+template <bool F32>
+struct DwEpilogue {
+  void* out;
+  int64_t I, J;
+  __device__ __forceinline__ void store(AccTile& acc, int i0, int j0, int lane, char* wlds) const {
+    constexpr int EB = F32 ? 4 : 2;
+#pragma unroll
+    for (int fj = 0; fj < kFJ; ++fj) {
+#pragma unroll
+      for (int fi = 0; fi < kFI; ++fi)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const float v0 = acc[fi][fj][4 * g], v1 = acc[fi][fj][4 * g + 1], v2 = acc[fi][fj][4 * g + 2],
+                      v3 = acc[fi][fj][4 * g + 3];
+          if constexpr (F32)
+            EpStage<4>::put(wlds, lane, fi, g, make_uint4(__float_as_uint(v0), __float_as_uint(v1),
+                                                          __float_as_uint(v2), __float_as_uint(v3)));
+          else
+            EpStage<2>::put(wlds, lane, fi, g, make_uint2(pack_bf16x2(v0, v1), pack_bf16x2(v2, v3)));
+        }
+      EpStage<EB>::drain(wlds, static_cast<char*>(out), I, J, i0, j0 + 32 * fj, lane);
+    }
+  }
+};
+
+typedef RowCopyBf16Loader<5> XentWt;      // dh's P: W as stored, read transposed
+typedef CopyLoader<2, true, 1> XentG;     // dh's Q: G rows
+typedef RowCopyBf16Loader<1> XentHt;      // dW's P: hc as stored
+typedef RowCopyBf16Loader<5> XentGt;      // dW's Q: G as stored
+
+template <bool F32>
+__global__ __launch_bounds__(kThreads, 1) void xent_grads_kernel(XentGrads a) {
+  typedef SmemLayout<XentWt, XentG> L1;
+  typedef SmemLayout<XentHt, XentGt> L2;
+  __shared__ __attribute__((aligned(16))) char smem[L1::kBytes > L2::kBytes ? L1::kBytes : L2::kBytes];
+  static_assert(4 * EpStage<4>::kWaveBytes <= L1::kBytes, "the epilogue's staging fits the stage buffers");
+  const int n = a.ctl->n;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int pi = (wave % kWavesI) * kWTI, qj = (wave / kWavesI) * kWTJ;
+  char* wlds = smem + wave * EpStage<4>::kWaveBytes;
+  AccTile acc;
+#pragma unroll
+  for (int fi = 0; fi < kFI; ++fi)
+#pragma unroll
+    for (int fj = 0; fj < kFJ; ++fj) zero_acc(acc[fi][fj]);
+  int b = blockIdx.x;
+  if (b < a.dh_units) {
+    const int u = cta_order(b, a.dh_units);
+    const int td = u % a.tiles_d, r = u / a.tiles_d, tt = r % a.tiles_t, sp = r / a.tiles_t;
+    const int i0 = td * kBI, j0 = tt * kBJ;
+    if (j0 >= n) return;
+    const int s0 = (int)((int64_t)a.stages_v * sp / a.split), s1 = (int)((int64_t)a.stages_v * (sp + 1) / a.split);
+    const XentWt pl{a.w, a.ldw, a.vc, a.Dp};
+    const XentG ql{reinterpret_cast<const char*>(a.G), 2 * (int64_t)a.ldg, n, 2 * (int64_t)a.ldg};
+    run_stages<MfmaBf16, 0>(pl, ql, smem, acc, i0, j0, s0, s1, pi, qj, lane, nullptr, 0);
+    const AccumEpilogue ep{a.slab + (int64_t)sp * a.T * a.D, a.D, n, a.first != 0};
+    ep.store(acc, i0 + pi, j0 + qj, lane, wlds);
+    return;
+  }
+  b = cta_order(b - a.dh_units, gridDim.x - a.dh_units);
+  const int i0 = (b % a.tiles_d) * kBI, j0 = (b / a.tiles_d) * kBJ;
+  const XentHt pl{a.hc, a.Dp, n, a.Dp};
+  const XentGt ql{a.G, a.ldg, n, a.ldg};
+  run_stages<MfmaBf16, 0>(pl, ql, smem, acc, i0, j0, 0, (n + kRed16 - 1) / kRed16, pi, qj, lane, nullptr, 0);
+  const DwEpilogue<F32> ep{a.dw, a.D, a.vc};
+  ep.store(acc, i0 + pi, j0 + qj, lane, wlds);
+}
+
+// dh [T][D] from the slabs: their sum in order, rounded once, at the rows
+// that count; zeros elsewhere.
+__global__ __launch_bounds__(256) void xent_dh_kernel(const float* __restrict__ slab, int split,
+                                                      const int* __restrict__ pos, int T, int D, int nch,
+                                                      uint16_t* __restrict__ dh) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= (int64_t)T * nch) return;
+  const int t = (int)(i / nch), k0 = 8 * (int)(i - (int64_t)t * nch);
+  const int at = pos[t];
+  float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  if (at >= 0) {
+    for (int s = 0; s < split; ++s) {
+      ChunkF32 c = load8(slab + ((int64_t)s * T + at) * D, k0, D);
+      settle8(c, k0, D);
+      float f[8];
+      c.get(f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += f[e];
+    }
+  }
+  store8(dh + (int64_t)t * D, k0, D, v);
+}
+
+// ---------------------------------------------------------------------------
+// Plans, workspaces, launches
+// ---------------------------------------------------------------------------
+
+static int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+
+// G's piece: at most this many bytes, so that the products that read it after
+// it is written find it in the 256 MB last level cache.
+constexpr int64_t kXentGBytes = int64_t(1) << 27;
+// Rows of W copied with padding at a time.
+constexpr int64_t kXentPadBytes = int64_t(1) << 28;
+
+// Tiles of 256 columns per piece. Pieces are equal, so that each fills the
+// CUs about as well as the others.
+static int64_t piece_tiles(int64_t V, int64_t most_rows) {
+  const int64_t tiles = (V + kBI - 1) / kBI, most = std::max<int64_t>(1, most_rows / kBI);
+  const int64_t pieces = (tiles + most - 1) / most;
+  return (tiles + pieces - 1) / pieces;
+}
+// The loaders' 32-bit offsets: (rows + 256) * pitch bytes <= 2^31.
+constexpr int64_t kReach = int64_t(1) << 31;
+
+struct XentPlan {
+  int64_t Dp, tiles;    // tiles of columns per piece
+  int64_t pos, ct, hc, part, zt, lse2, c, G, slab, pad, total;  // byte offsets
+  int64_t ldg, split;
+  bool padded;          // W's pieces are copied first
+};
+
+static XentPlan xent_plan(int64_t T, int64_t V, int64_t D, bool bwd) {
+  XentPlan p{};
+  p.Dp = up(D, 8);
+  p.padded = p.Dp != D;
+  int64_t rows = kReach / (2 * p.Dp) - 256;
+  if (p.padded) rows = std::min(rows, kXentPadBytes / (2 * p.Dp));
+  if (bwd) rows = std::min(rows, std::min(kXentGBytes / (2 * T), kReach / (2 * (T + 256))));
+  p.tiles = piece_tiles(V, rows);
+  int64_t at = 256;
+  const auto take = [&](int64_t bytes) {
+    const int64_t o = at;
+    at += up(bytes, 256);
+    return o;
+  };
+  p.pos = take(4 * T);
+  p.ct = take(4 * T);
+  p.hc = take(2 * T * p.Dp);
+  if (!bwd) {
+    p.part = take((V + 127) / 128 * 8 * T + 8 * T);
+    p.zt = take(4 * T);
+  } else {
+    p.lse2 = take(4 * T);
+    p.c = take(4 * T);
+    p.ldg = std::min(p.tiles * kBI, up(V, 64));
+    p.G = take(2 * T * p.ldg);
+    // dh's tiles split over the piece's columns until a unit is at most
+    // about 0.85 of a CU's share of the piece's work, so that units and dW's
+    // tiles pack the CUs evenly
+    const int64_t td = (D + kBI - 1) / kBI, tt = (T + kBJ - 1) / kBJ;
+    const int64_t sv = p.tiles * kBI / kRed16, st = (T + kRed16 - 1) / kRed16;
+    const double share = (double)(td * tt * sv + td * p.tiles * st) / 256.0;
+    int64_t split = (int64_t)((double)sv / (0.85 * share) + 0.999);
+    split = std::min<int64_t>(split, std::max<int64_t>(1, sv / 16));
+    p.split = std::max<int64_t>(1, split);
+    p.slab = take(4 * p.split * T * D);
+  }
+  if (p.padded) p.pad = take(2 * p.tiles * kBI * p.Dp);
+  p.total = at;
+  return p;
+}
+
+static bool xent_few(int64_t T, int64_t D) { return T <= kFewTokens && D % 8 == 0; }
+
+size_t xent_workspace(int64_t T, int64_t V, int64_t D, bool bwd) {
+  if (!bwd && xent_few(T, D)) return (size_t)(up((V + 31) / 32 * 8 * T, 256) + up(4 * T, 256));
+  return (size_t)xent_plan(T, V, D, bwd).total;
+}
+
+static hipError_t launch_pad(const uint16_t* w, int64_t rows, int64_t D, int64_t Dp, uint16_t* out, hipStream_t st) {
+  const int64_t chunks = rows * (Dp / 8);
+  xent_pad_kernel<<<(unsigned)((chunks + 255) / 256), 256, 0, st>>>(w, rows, (int)D, (int)(Dp / 8), out);
+  return hipGetLastError();
+}
+
+static hipError_t launch_loss(const XentLoss& l, const int64_t* targets, int64_t ignore, float* total, bool mean,
+                              hipStream_t st) {
+  xent_combine_kernel<<<(l.T + kLossTokens - 1) / kLossTokens, 1024, 0, st>>>(l);
+  if (hipError_t e = hipGetLastError()) return e;
+  if (total == nullptr) return hipSuccess;
+  xent_reduce_kernel<<<1, 1024, 0, st>>>(l.loss, targets, ignore, l.T, mean ? 1 : 0, total);
+  return hipGetLastError();
+}
+
+hipError_t launch_xent_fwd(const uint16_t* h, const uint16_t* w, const int64_t* targets, int64_t ignore, int64_t T,
+                           int64_t V, int64_t D, float* loss, float* lse, float* total, bool mean, void* ws,
+                           hipStream_t stream) {
+  char* base = static_cast<char*>(ws);
+  if (xent_few(T, D)) {
+    XentFew f{w, V, (int)D, h, (int)T, targets, reinterpret_cast<float2*>(base),
+              reinterpret_cast<float*>(base + up((V + 31) / 32 * 8 * T, 256))};
+    const unsigned grid = (unsigned)((V + 31) / 32);
+    if (T <= 32) xent_few_kernel<1><<<grid, kWave * kFewWaves, 0, stream>>>(f);
+    else xent_few_kernel<2><<<grid, kWave * kFewWaves, 0, stream>>>(f);
+    if (hipError_t e = hipGetLastError()) return e;
+    const XentLoss l{f.part, (int)grid, (int)T, f.zt, nullptr, targets, ignore, V, lse, loss};
+    return launch_loss(l, targets, ignore, total, mean, stream);
+  }
+  const XentPlan p = xent_plan(T, V, D, false);
+  XentRows r{};
+  r.h = h;
+  r.targets = targets;
+  r.ignore = ignore;
+  r.T = (int)T;
+  r.D = (int)D;
+  r.Dp = (int)p.Dp;
+  r.V = V;
+  r.ctl = reinterpret_cast<XentCtl*>(base);
+  r.hc = reinterpret_cast<uint16_t*>(base + p.hc);
+  r.pos = reinterpret_cast<int*>(base + p.pos);
+  r.ct = reinterpret_cast<int*>(base + p.ct);
+  xent_gather_kernel<false><<<(unsigned)((T + kGatherRows - 1) / kGatherRows), 256, 0, stream>>>(r);
+  if (hipError_t e = hipGetLastError()) return e;
+  XentTiles a{};
+  a.hc = r.hc;
+  a.Dp = r.Dp;
+  a.ctl = r.ctl;
+  a.ct = r.ct;
+  a.part = reinterpret_cast<float2*>(base + p.part);
+  a.T = r.T;
+  a.zt = reinterpret_cast<float*>(base + p.zt);
+  a.tiles_t = (int)((T + kBJ - 1) / kBJ);
+  a.nstages = (int)((p.Dp + kRed16 - 1) / kRed16);
+  for (int64_t v0 = 0; v0 < V; v0 += p.tiles * kBI) {
+    const int64_t vc = std::min(V - v0, p.tiles * kBI);
+    a.w = w + v0 * D;
+    a.ldw = D;
+    if (p.padded) {
+      uint16_t* pad = reinterpret_cast<uint16_t*>(base + p.pad);
+      if (hipError_t e = launch_pad(a.w, vc, D, p.Dp, pad, stream)) return e;
+      a.w = pad;
+      a.ldw = p.Dp;
+    }
+    a.vc = (int)vc;
+    a.v0 = (int)v0;
+    a.tiles_v = (int)((vc + kBI - 1) / kBI);
+    xent_logits_kernel<false><<<(unsigned)(a.tiles_v * a.tiles_t), kThreads, 0, stream>>>(a);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  const XentLoss l{a.part, (int)((V + 127) / 128), (int)T, a.zt, r.pos, targets, ignore, V, lse, loss};
+  return launch_loss(l, targets, ignore, total, mean, stream);
+}
+
+hipError_t launch_xent_bwd(const uint16_t* h, const uint16_t* w, const int64_t* targets, int64_t ignore,
+                           const float* lse, const float* dloss, bool per_row, bool mean, int64_t T, int64_t V,
+                           int64_t D, uint16_t* dh, void* dw, bool dw_f32, void* ws, hipStream_t stream) {
+  char* base = static_cast<char*>(ws);
+  const XentPlan p = xent_plan(T, V, D, true);
+  XentRows r{};
+  r.h = h;
+  r.targets = targets;
+  r.ignore = ignore;
+  r.T = (int)T;
+  r.D = (int)D;
+  r.Dp = (int)p.Dp;
+  r.V = V;
+  r.ctl = reinterpret_cast<XentCtl*>(base);
+  r.hc = reinterpret_cast<uint16_t*>(base + p.hc);
+  r.pos = reinterpret_cast<int*>(base + p.pos);
+  r.ct = reinterpret_cast<int*>(base + p.ct);
+  r.lse = lse;
+  r.dloss = dloss;
+  r.per_row = per_row ? 1 : 0;
+  r.mean = mean ? 1 : 0;
+  r.lse2 = reinterpret_cast<float*>(base + p.lse2);
+  r.c = reinterpret_cast<float*>(base + p.c);
+  xent_gather_kernel<true><<<(unsigned)((T + kGatherRows - 1) / kGatherRows), 256, 0, stream>>>(r);
+  if (hipError_t e = hipGetLastError()) return e;
+  XentTiles a{};
+  a.hc = r.hc;
+  a.Dp = r.Dp;
+  a.ctl = r.ctl;
+  a.ct = r.ct;
+  a.T = r.T;
+  a.lse2 = r.lse2;
+  a.c = r.c;
+  a.G = reinterpret_cast<uint16_t*>(base + p.G);
+  a.ldg = (int)p.ldg;
+  a.tiles_t = (int)((T + kBJ - 1) / kBJ);
+  a.nstages = (int)((p.Dp + kRed16 - 1) / kRed16);
+  XentGrads g{};
+  g.G = a.G;
+  g.ldg = a.ldg;
+  g.hc = a.hc;
+  g.Dp = a.Dp;
+  g.D = (int)D;
+  g.T = r.T;
+  g.ctl = r.ctl;
+  g.tiles_d = (int)((D + kBI - 1) / kBI);
+  g.tiles_t = a.tiles_t;
+  g.slab = reinterpret_cast<float*>(base + p.slab);
+  g.split = (int)p.split;
+  g.dh_units = dh ? g.tiles_d * g.tiles_t * g.split : 0;
+  for (int64_t v0 = 0; v0 < V; v0 += p.tiles * kBI) {
+    const int64_t vc = std::min(V - v0, p.tiles * kBI);
+    a.w = w + v0 * D;
+    a.ldw = D;
+    if (p.padded) {
+      uint16_t* pad = reinterpret_cast<uint16_t*>(base + p.pad);
+      if (hipError_t e = launch_pad(a.w, vc, D, p.Dp, pad, stream)) return e;
+      a.w = pad;
+      a.ldw = p.Dp;
+    }
+    a.vc = (int)vc;
+    a.v0 = (int)v0;
+    a.tiles_v = (int)((vc + kBI - 1) / kBI);
+    xent_logits_kernel<true><<<(unsigned)(a.tiles_v * a.tiles_t), kThreads, 0, stream>>>(a);
+    if (hipError_t e = hipGetLastError()) return e;
+    g.w = a.w;
+    g.ldw = a.ldw;
+    g.vc = a.vc;
+    // columns [vc, up(vc, 64)) of G hold zeros
+    g.stages_v = (int)((vc + kRed16 - 1) / kRed16);
+    g.first = v0 == 0 ? 1 : 0;
+    g.dw = dw ? static_cast<char*>(dw) + v0 * D * (dw_f32 ? 4 : 2) : nullptr;
+    const unsigned grid = (unsigned)(g.dh_units + (dw ? g.tiles_d * a.tiles_v : 0));
+    if (dw_f32) xent_grads_kernel<true><<<grid, kThreads, 0, stream>>>(g);
+    else xent_grads_kernel<false><<<grid, kThreads, 0, stream>>>(g);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  if (dh == nullptr) return hipSuccess;
+  const int nch = (int)(p.Dp / 8);
+  xent_dh_kernel<<<(unsigned)((T * nch + 255) / 256), 256, 0, stream>>>(g.slab, g.split, r.pos, r.T, r.D, nch, dh);
+  return hipGetLastError();
+}
+
+}  // namespace bitnet

@@ -1,5 +1,5 @@
-"""Refusals of the layer norm, 8-bit checkpoint and gated activation entry
-points without a GPU: the C ABI rejects bad arguments with the documented
+"""Refusals of the layer norm, 8-bit checkpoint, gated activation and cross
+entropy entry points without a GPU: the C ABI rejects bad arguments with the documented
 codes before touching the device, and the Python entry points raise before
 they call it."""
 
@@ -139,3 +139,54 @@ def test_python_refusals():
         B._need_rows(x.t().contiguous().t(), 4, 64, "gate")
     with pytest.raises(ValueError):
         B._need_rows(x[:1].expand(4, 64), 4, 64, "gate")
+
+
+def test_xent_refusals(L):
+    T, V, D = 100, 1000, 64
+    nf, nb = L.bitnet_xent_fwd_workspace_bytes(T, V, D), L.bitnet_xent_bwd_workspace_bytes(T, V, D)
+    assert nf > 0 and nb > 2 * T * V  # G for the one piece
+    for f in (L.bitnet_xent_fwd_workspace_bytes, L.bitnet_xent_bwd_workspace_bytes):
+        assert f(0, V, D) == 0 and f(T, 0, D) == 0 and f(T, V, 0) == 0 and f(T, V, 65537) == 0
+        assert f((1 << 21) + 1, V, 8) == 0 and f(T, (1 << 28) + 1, D) == 0 and f(1 << 20, V, 2048) == 0
+    # G never holds the whole vocabulary of a large problem
+    assert L.bitnet_xent_bwd_workspace_bytes(4096, 128256, 2560) < 2 * 4096 * 128256 // 4
+    assert L.bitnet_xent_fwd_workspace_bytes(16, 32000, 2560) < 1 << 20
+
+    def fwd(h=P, w=P, t=P, T=T, V=V, D=D, loss=P, lse=P, total=P, red=2, ws=P, n=nf):
+        return L.bitnet_xent_fwd(h, w, t, -100, T, V, D, loss, lse, total, red, ws, n, None)
+
+    assert fwd(h=None) == ENULL and fwd(w=None) == ENULL and fwd(t=None) == ENULL and fwd(loss=None) == ENULL
+    assert fwd(lse=None) == ENULL and fwd(total=None) == ENULL and fwd(red=0) == ENULL
+    assert fwd(red=3) == EDTYPE and fwd(T=0) == ESHAPE and fwd(D=70000) == ESHAPE
+    assert fwd(ws=None) == EWS and fwd(n=nf - 1) == EWS
+    assert fwd(h=P + 8) == EALIGN and fwd(w=P + 2) == EALIGN and fwd(t=P + 4) == EALIGN and fwd(ws=P + 8) == EALIGN
+
+    def bwd(h=P, w=P, t=P, lse=P, dl=P, red=2, T=T, V=V, D=D, dh=P, dw=P, d=BF, ws=P, n=nb):
+        return L.bitnet_xent_bwd(h, w, t, -100, lse, dl, red, T, V, D, dh, dw, d, ws, n, None)
+
+    assert bwd(h=None) == ENULL and bwd(lse=None) == ENULL and bwd(dl=None) == ENULL and bwd(dh=None, dw=None) == ENULL
+    assert bwd(red=-1) == EDTYPE and bwd(d=SIGN1) == EDTYPE and bwd(V=0) == ESHAPE
+    assert bwd(ws=None) == EWS and bwd(n=nb - 1) == EWS
+    assert bwd(dh=P + 8) == EALIGN and bwd(dw=P + 4) == EALIGN and bwd(lse=P + 2) == EALIGN
+
+
+def test_xent_python_refusals():
+    from ternary_weight_quantization_amd.loss import linear_cross_entropy
+
+    h, w, t = torch.zeros(4, 8, dtype=torch.bfloat16), torch.zeros(9, 8, dtype=torch.bfloat16), torch.zeros(4).long()
+    with pytest.raises(TypeError):
+        linear_cross_entropy(h.float(), w, t)
+    with pytest.raises(TypeError):
+        linear_cross_entropy(h, w.half(), t)
+    with pytest.raises(TypeError):
+        linear_cross_entropy(h, w, t.int())
+    with pytest.raises(ValueError):
+        linear_cross_entropy(h, w[:, :4], t)
+    with pytest.raises(ValueError):
+        linear_cross_entropy(h, w[:0], t)
+    with pytest.raises(ValueError):
+        linear_cross_entropy(h, w, t[:3])
+    with pytest.raises(ValueError):
+        linear_cross_entropy(h, w, t, reduction="max")
+    with pytest.raises(ValueError):
+        linear_cross_entropy(h, w, t)  # not on a GPU
