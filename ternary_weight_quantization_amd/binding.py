@@ -143,6 +143,22 @@ def lib():
     return _lib
 
 
+_ops = None
+
+
+def ops():
+    """The torch autograd functions over the library (csrc/host/torch_ops.cpp)."""
+    global _ops
+    if _ops is None:
+        lib()
+        if not os.path.exists(os.path.join(HERE, "_bitnet_ops.so")):
+            raise RuntimeError("_bitnet_ops.so is not built; run `python -m ternary_weight_quantization_amd.build`")
+        from . import _bitnet_ops
+
+        _ops = _bitnet_ops
+    return _ops
+
+
 def _check(code):
     if code != BITNET_OK:
         msg = lib().bitnet_status_string(code).decode()

@@ -71,7 +71,7 @@ struct XentRows {
   float* c;                // [T] their c
 };
 
-constexpr int kGatherRows = 16;
+constexpr int kGatherRows = 8;  // two for each of the block's waves
 
 // Each block finds how many rows that count precede its own and how many
 // there are by reading all targets (a few KB out of L2), so that no launch
@@ -81,6 +81,7 @@ __global__ __launch_bounds__(256) void xent_gather_kernel(XentRows a) {
   __shared__ int before[4], all[4];
   const int t0 = blockIdx.x * kGatherRows, tid = threadIdx.x;
   int b = 0, n = 0;
+#pragma unroll 8
   for (int t = tid; t < a.T; t += 256) {
     const int v = a.targets[t] != a.ignore;
     n += v;
@@ -99,18 +100,20 @@ __global__ __launch_bounds__(256) void xent_gather_kernel(XentRows a) {
   b = (before[0] + before[1]) + (before[2] + before[3]);
   n = (all[0] + all[1]) + (all[2] + all[3]);
   if (blockIdx.x == 0 && tid == 0) a.ctl->n = n;
-  const int nch = a.Dp / 8;
-  for (int r = 0; r < kGatherRows; ++r) {
+  const int lane = tid & 63, wave = tid >> 6, nch = a.Dp / 8;
+  // which of the block's rows count, in every lane of every wave
+  const int tl = t0 + (lane & (kGatherRows - 1));
+  const unsigned long long mask = __ballot(lane < kGatherRows && tl < a.T && a.targets[tl < a.T ? tl : 0] != a.ignore);
+  for (int r = wave; r < kGatherRows && t0 + r < a.T; r += 4) {
     const int t = t0 + r;
-    if (t >= a.T) break;
-    const int64_t target = a.targets[t];
-    if (target == a.ignore) {
-      if (tid == 0) a.pos[t] = -1;
+    if (!((mask >> r) & 1)) {
+      if (lane == 0) a.pos[t] = -1;
       continue;
     }
-    const int at = b++;
+    const int at = b + __popcll(mask & ((1ull << r) - 1));
+    const int64_t target = a.targets[t];
     const bool in = target >= 0 && target < a.V;
-    if (tid == 0) {
+    if (lane == 0) {
       a.pos[t] = at;
       a.ct[at] = in ? (int)target : -1;
       if constexpr (BWD) {
@@ -121,10 +124,17 @@ __global__ __launch_bounds__(256) void xent_gather_kernel(XentRows a) {
       }
     }
     const uint16_t* src = a.h + (int64_t)t * a.D;
-    for (int ch = tid; ch < nch; ch += 256) {
-      ChunkBf16 v = load8(src, 8 * ch, a.D);
-      settle8(v, 8 * ch, a.D);
-      reinterpret_cast<uint4*>(a.hc + (int64_t)at * a.Dp)[ch] = v.v;
+    uint4* dst = reinterpret_cast<uint4*>(a.hc + (int64_t)at * a.Dp);
+    for (int c0 = 0; c0 < nch; c0 += 256) {
+      ChunkBf16 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = load8(src, 8 * (c0 + lane + 64 * i), a.D);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int ch = c0 + lane + 64 * i;
+        settle8(v[i], 8 * ch, a.D);
+        if (ch < nch) dst[ch] = v[i].v;
+      }
     }
   }
 }

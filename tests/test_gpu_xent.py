@@ -399,3 +399,15 @@ def test_a_model_with_every_operator():
     for g, k in zip(first, second):
         assert torch.isfinite(g).all() and torch.equal(g, k)
     assert all(g.any() for g in first)
+
+
+def test_not_differentiable_twice():
+    from ternary_weight_quantization_amd.checkpoint import gated_activation
+    from ternary_weight_quantization_amd.loss import linear_cross_entropy
+    from ternary_weight_quantization_amd.norm import layer_norm
+
+    h, w, t = make(12, 40, 64, seed=20)
+    h.requires_grad_(True)
+    for out in (linear_cross_entropy(h, w, t), layer_norm(h).float().sum(), gated_activation(h).float().sum()):
+        with pytest.raises(RuntimeError):
+            torch.autograd.grad(out, h, create_graph=True)
