@@ -41,11 +41,10 @@ __global__ __launch_bounds__(kRowThreads) void ckpt_pack_kernel(const T* __restr
   const int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
   if (i >= total) return;  // total is a multiple of 16: whole blocks leave
   const ChunkAt at = chunk_at(i, nch);
-  typename ChunkOf<T>::type c = load8(x + at.row * K, 8 * at.ch, K);
-  settle8(c, 8 * at.ch, K);
+  const typename ChunkOf<T>::type c = chunk8(x + at.row * K, 8 * at.ch, K);
   float f[8];
   c.get(f);
-  const float s = block_scale(f);
+  const float s = block_scale(c);
   reinterpret_cast<uint2*>(codes)[i] = codes8(f, s);
   if ((threadIdx.x & 15) == 0) scales[i >> 4] = s;
 }
@@ -132,24 +131,29 @@ __global__ __launch_bounds__(kRowThreads) void gate_fwd_kernel(const uint16_t* _
   if (i >= total) return;
   const ChunkAt at = chunk_at(i, nch);
   const int k0 = 8 * at.ch;
-  ChunkBf16 cg = load8(gate + at.row * ldg, k0, K), cu;
-  if constexpr (UP) cu = load8(up + at.row * ldu, k0, K);
-  settle8(cg, k0, K);
+  // every load before the first use
+  ChunkBf16 cg, cu;
+  if (K < 8) {
+    cg = load8<true>(gate + at.row * ldg, k0, K);
+    if constexpr (UP) cu = load8<true>(up + at.row * ldu, k0, K);
+  } else {
+    cg = load8<false>(gate + at.row * ldg, k0, K);
+    if constexpr (UP) cu = load8<false>(up + at.row * ldu, k0, K);
+    settle8<false>(cg, k0, K);
+    if constexpr (UP) settle8<false>(cu, k0, K);
+  }
   float g[8], u[8], o[8];
   cg.get(g);
-  if constexpr (UP) {
-    settle8(cu, k0, K);
-    cu.get(u);
-  }
+  if constexpr (UP) cu.get(u);
 #pragma unroll
   for (int e = 0; e < 8; ++e) o[e] = UP ? A::f(g[e]) * u[e] : A::f(g[e]);
   store8(y + at.row * K, k0, K, o);
   if constexpr (CK) {
-    const float s = block_scale(g);
+    const float s = block_scale(cg);
     reinterpret_cast<uint2*>(gq)[i] = codes8(g, s);
     if ((threadIdx.x & 15) == 0) gs[i >> 4] = s;
     if constexpr (UP) {
-      const float t = block_scale(u);
+      const float t = block_scale(cu);
       reinterpret_cast<uint2*>(uq)[i] = codes8(u, t);
       if ((threadIdx.x & 15) == 0) us[i >> 4] = t;
     }
@@ -171,28 +175,24 @@ __global__ __launch_bounds__(kRowThreads) void gate_bwd_kernel(const uint16_t* _
   if (i >= total) return;
   const ChunkAt at = chunk_at(i, nch);
   const int k0 = 8 * at.ch;
-  ChunkBf16 cd = load8(dY + at.row * K, k0, K);
   float g[8], u[8], d[8];
   if constexpr (CK) {
     const uint2 qg = reinterpret_cast<const uint2*>(gq)[i];
     const float sg = gs[i >> 4];
+    uint2 qu = make_uint2(0u, 0u);
+    float su = 0.0f;
     if constexpr (UP) {
-      const uint2 qu = reinterpret_cast<const uint2*>(uq)[i];
-      values8(qu, us[i >> 4] / 127.0f, u);
+      qu = reinterpret_cast<const uint2*>(uq)[i];
+      su = us[i >> 4];
     }
+    chunk8(dY + at.row * K, k0, K).get(d);
     values8(qg, sg / 127.0f, g);
+    if constexpr (UP) values8(qu, su / 127.0f, u);
   } else {
-    ChunkBf16 cg = load8(gate + at.row * ldg, k0, K), cu;
-    if constexpr (UP) {
-      cu = load8(up + at.row * ldu, k0, K);
-      settle8(cu, k0, K);
-      cu.get(u);
-    }
-    settle8(cg, k0, K);
-    cg.get(g);
+    chunk8(gate + at.row * ldg, k0, K).get(g);
+    if constexpr (UP) chunk8(up + at.row * ldu, k0, K).get(u);
+    chunk8(dY + at.row * K, k0, K).get(d);
   }
-  settle8(cd, k0, K);
-  cd.get(d);
   float dg[8], du[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {

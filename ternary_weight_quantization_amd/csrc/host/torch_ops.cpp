@@ -1,6 +1,7 @@
 // The operators around the ternary linear layers as torch autograd functions
 // over the C ABI (include/bitnet.h): layer norm, 8-bit activation checkpoints,
-// the gated activation and the linear layer with cross entropy.
+// the gated activation, the TTQ layer with its input kept in 8 bits, and the
+// linear layer with cross entropy.
 //
 // Only checks of arguments, allocation of outputs and workspaces, and calls of
 // libbitnet.so on the tensors' device and its current stream. They are C++
@@ -46,6 +47,12 @@ Tensor scratch(size_t bytes, const Tensor& like) {
 // t [..., K] as contiguous rows [M][K].
 Tensor rows(const Tensor& t) {
   return (t.dim() == 2 ? t : t.reshape({-1, t.size(-1)})).contiguous();
+}
+
+// t contiguous, starting at a multiple of 16 bytes.
+Tensor aligned(const Tensor& t) {
+  Tensor c = t.contiguous();
+  return reinterpret_cast<uintptr_t>(c.data_ptr()) % 16 == 0 ? c : c.clone();
 }
 
 void no_second_derivative() {
@@ -301,13 +308,68 @@ Tensor gated_activation(const Tensor& gate, const optional<Tensor>& up, int64_t 
   return gate_forward(gate, u, act, Tensor());
 }
 
-// --- linear layer with cross entropy -------------------------------------------------
+// --- the TTQ layer with an 8-bit checkpoint of its input --------------------------------
 
-// t contiguous, starting at a multiple of 16 bytes.
-Tensor aligned(const Tensor& t) {
-  Tensor c = t.contiguous();
-  return reinterpret_cast<uintptr_t>(c.data_ptr()) % 16 == 0 ? c : c.clone();
+struct TtqFn : torch::autograd::Function<TtqFn> {
+  static Tensor forward(AutogradContext* ctx, const Tensor& x, const Tensor& weight, const Tensor& params) {
+    const Tensor x2 = aligned(rows(x)), w = aligned(weight), p = params.to(at::kFloat).contiguous();
+    const int64_t M = x2.size(0), K = x2.size(1), N = w.size(0), Kp = bitnet_k_pad(K);
+    std::vector<int64_t> shape = x.sizes().vec();
+    shape.back() = N;
+    Tensor y = at::empty(shape, x.options());
+    const Tensor codes_w = at::empty({N, Kp / 4}, x.options().dtype(at::kByte)), wt = at::empty({N, Kp}, x.options());
+    const size_t bytes = ttq_workspace_bytes(M, N, K);
+    const Tensor ws = scratch(bytes, x);
+    {
+      On on(x2);
+      check(ttq_quantize(ptr(w), code(w.scalar_type()), N, K, f32(p), static_cast<uint8_t*>(ptr(codes_w)), bf16(wt),
+                         on.stream));
+      check(ttq_fwd(bf16(x2), bf16(wt), M, N, K, bf16(y), ptr(ws), bytes, on.stream));
+    }
+    Tensor codes, scales;
+    if (weight.requires_grad() || params.requires_grad()) std::tie(codes, scales) = compress(x2);  // dW alone reads x
+    ctx->save_for_backward({codes, scales, wt, codes_w});
+    ctx->saved_data["x"] = x.sizes();
+    ctx->saved_data["wt"] = static_cast<int64_t>(weight.scalar_type());
+    return y;
+  }
+
+  static variable_list backward(AutogradContext* ctx, const variable_list& grads) {
+    no_second_derivative();
+    const variable_list saved = ctx->get_saved_variables();
+    const Tensor &codes = saved[0], &scales = saved[1], &wt = saved[2], &codes_w = saved[3];
+    const std::vector<int64_t> shape = ctx->saved_data["x"].toIntVector();
+    const auto wdt = static_cast<at::ScalarType>(ctx->saved_data["wt"].toInt());
+    const Tensor dY = aligned(rows(grads[0].to(at::kBFloat16)));
+    const int64_t M = dY.size(0), N = dY.size(1), K = shape.back();
+    const bool need_x = ctx->needs_input_grad(0), need_w = ctx->needs_input_grad(1), need_p = ctx->needs_input_grad(2);
+    Tensor dX, dW, dp;
+    if (need_x) dX = at::empty(shape, dY.options());
+    // the scales' gradients come from dW's epilogue; the threshold has none
+    if (need_w || need_p) dW = at::empty({N, K}, dY.options().dtype(wdt));
+    if (need_p) dp = at::zeros({3}, dY.options().dtype(at::kFloat));
+    const size_t bytes = ttq_bwd_ckpt_workspace_bytes(M, N, K);
+    const Tensor ws = scratch(bytes, dY);
+    On on(dY);
+    check(ttq_bwd_ckpt(bf16(dY), i8(codes), f32(scales), bf16(wt), static_cast<uint8_t*>(ptr(codes_w)), M, N, K, bf16(dX),
+                       ptr(dW), code(wdt), dp.defined() ? f32(dp) + 1 : nullptr, ptr(ws), bytes, on.stream));
+    return {dX, need_w ? dW : Tensor(), dp};
+  }
+};
+
+Tensor ttq_linear_checkpoint(const Tensor& x, const Tensor& weight, const Tensor& params) {
+  TORCH_CHECK_TYPE(x.scalar_type() == at::kBFloat16, "TTQ expects bf16 activations");
+  TORCH_CHECK_TYPE(is_value(weight.scalar_type()), "weight: expected bf16 or float32, got ", weight.scalar_type());
+  check_activation("ttq_linear", x);
+  TORCH_CHECK_VALUE(weight.dim() == 2 && weight.size(1) == x.size(-1) && weight.size(0) >= 1,
+                    "weight: expected [out_features, ", x.size(-1), "], got ", weight.sizes());
+  TORCH_CHECK_VALUE(params.numel() == 3 && params.dim() == 1, "params: expected shape [3], got ", params.sizes());
+  TORCH_CHECK_VALUE(weight.device() == x.device() && params.device() == x.device(),
+                    "x, weight and params: must be GPU tensors of one device");
+  return TtqFn::apply(x, weight, params);
 }
+
+// --- linear layer with cross entropy -------------------------------------------------
 
 struct Xent {
   Tensor h, w, t, loss, lse, total;
@@ -391,5 +453,6 @@ PYBIND11_MODULE(_bitnet_ops, m) {
   m.def("compress", &compress, free_gil);
   m.def("decompress", &decompress, free_gil);
   m.def("gated_activation", &gated_activation, free_gil);
+  m.def("ttq_linear_checkpoint", &ttq_linear_checkpoint, free_gil);
   m.def("linear_cross_entropy", &linear_cross_entropy, free_gil);
 }

@@ -17,6 +17,7 @@
 // partial row [2][K]; a second launch adds the partial rows in block order.
 // No atomics: the same inputs give the same bits.
 
+#include <algorithm>
 #include <type_traits>
 
 #include "internal.h"
@@ -53,82 +54,134 @@ struct NormParams {
   bool f32;       // their type
 };
 
-template <class T, int BLOCK, int TPR, int CPT>
-__global__ __launch_bounds__(BLOCK) void layernorm_fwd_kernel(const T* __restrict__ x, NormParams p, int64_t M, int K,
-                                                              float eps, void* __restrict__ y, bool y_f32,
-                                                              float* __restrict__ mean, float* __restrict__ rstd,
-                                                              int8_t* __restrict__ codes, float* __restrict__ scales,
-                                                              int nch) {
+// Keeps a loaded chunk as it is across a row's reduction: the values derived
+// from it are computed again after it instead of being held in registers.
+__device__ __forceinline__ void hold(ChunkBf16& c) { asm volatile("" : "+v"(c.v.x), "+v"(c.v.y), "+v"(c.v.z), "+v"(c.v.w)); }
+__device__ __forceinline__ void hold(ChunkF32& c) {
+  asm volatile("" : "+v"(c.a.x), "+v"(c.a.y), "+v"(c.a.z), "+v"(c.a.w), "+v"(c.b.x), "+v"(c.b.y), "+v"(c.b.z), "+v"(c.b.w));
+}
+
+struct NormFwd {
+  const void* x;
+  NormParams p;
+  int64_t M;
+  int K, nch;
+  float eps;
+  void* y;
+  bool y_f32;
+  float* mean;    // each NULL if not wanted
+  float* rstd;
+  int8_t* codes;
+  float* scales;
+};
+
+// A block takes rows (TPR threads each) in turn; the weight and bias stay in
+// its registers as loaded, and the next row is requested before the current
+// one is reduced. P: the parameters' type. SHORT: K < 8 (one chunk a row).
+template <class T, class P, int BLOCK, int TPR, int CPT, bool SHORT>
+__global__ __launch_bounds__(BLOCK) void layernorm_fwd_kernel(NormFwd a) {
   constexpr int RPB = BLOCK / TPR;
-  __shared__ float s0[BLOCK / kWave], s1[BLOCK / kWave];
+  __shared__ float slot[4][BLOCK / kWave];
   const int t = threadIdx.x % TPR;
-  // uniform in the wave: whole waves share a row
-  const int64_t row = (int64_t)blockIdx.x * RPB + __builtin_amdgcn_readfirstlane((int)threadIdx.x / TPR);
-  const bool ok = row < M;
-  const T* xr = x + (ok ? row : 0) * K;
-  typename ChunkOf<T>::type c[CPT];
-#pragma unroll
-  for (int i = 0; i < CPT - 1; ++i) c[i] = load8_in(xr + 8 * (t + i * TPR));
-  c[CPT - 1] = load8(xr, 8 * (t + (CPT - 1) * TPR), K);
+  const int rl = __builtin_amdgcn_readfirstlane((int)threadIdx.x / TPR);  // whole waves share a row
+  const int K = a.K;
+  const int ch_last = t + (CPT - 1) * TPR, k_last = 8 * ch_last;
+  typename ChunkOf<P>::type cw[CPT] = {}, cb[CPT] = {};
+  typename ChunkOf<T>::type c[CPT], nx[CPT];
   // only a thread's last chunk can reach past K (row_split)
-  settle8(c[CPT - 1], 8 * (t + (CPT - 1) * TPR), K);
-  float sum = 0.0f;
+  const auto load = [&](auto* row, auto (&v)[CPT]) {
 #pragma unroll
-  for (int i = 0; i < CPT; ++i) {
-    float f[8];
-    c[i].get(f);
-    sum += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
-  }
-  const float mu = row_sum<TPR>(sum, s0) / (float)K;
-  float sq = 0.0f;
+    for (int i = 0; i < CPT - 1; ++i) v[i] = load8_in(row + 8 * (t + i * TPR));
+    v[CPT - 1] = load8<SHORT>(row, k_last, K);
+  };
+  const T* x = static_cast<const T*>(a.x);
+  // Every thread passes every barrier: past the last row a wave (rows are
+  // uniform in a wave) repeats it and writes nothing.
+  const int64_t stride = (int64_t)gridDim.x * RPB, last = a.M - 1;
+  int64_t base = (int64_t)blockIdx.x * RPB, row = base + rl < last ? base + rl : last;
+  load(x + row * K, c);
+  if (a.p.w) load(static_cast<const P*>(a.p.w), cw);
+  if (a.p.b) load(static_cast<const P*>(a.p.b), cb);
+  settle8<SHORT>(cw[CPT - 1], k_last, K);
+  settle8<SHORT>(cb[CPT - 1], k_last, K);
+  int flip = 0;
+  for (; base < a.M; base += stride, flip ^= 2) {
+    const bool ok = base + rl < a.M;
+    const int64_t want = base + stride + rl, next = want < last ? want : last;
+    const bool more = base + stride < a.M;  // uniform
+    if (more) load(x + next * K, nx);
+    settle8<SHORT>(c[CPT - 1], k_last, K);
+    float sum = 0.0f;
 #pragma unroll
-  for (int i = 0; i < CPT; ++i) {
-    const int left = K - 8 * (t + i * TPR);
-    float f[8];
-    c[i].get(f);
-    if (i < CPT - 1 || left >= 8) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sq = fmaf(f[e] - mu, f[e] - mu, sq);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sq += e < left ? (f[e] - mu) * (f[e] - mu) : 0.0f;
+    for (int i = 0; i < CPT; ++i) {
+      float f[8];
+      c[i].get(f);
+      sum += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+      hold(c[i]);
     }
-  }
-  const float r = 1.0f / sqrtf(row_sum<TPR>(sq, s1) / (float)K + eps);
-  if (!ok) return;
-  if (t == 0) {
-    if (mean) mean[row] = mu;
-    if (rstd) rstd[row] = r;
-  }
+    // two slot pairs in turn: a row's readers are done with one pair before
+    // the barrier of the next row, after which it may be written again
+    const float mu = row_sum<TPR>(sum, slot[flip]) / (float)K;
+    float sq = 0.0f;
 #pragma unroll
-  for (int i = 0; i < CPT; ++i) {
-    const int ch = t + i * TPR, k0 = 8 * ch;
-    if (i == CPT - 1 && ch >= nch) continue;
-    float f[8], o[8];
-    c[i].get(f);
-    if (codes) {  // uniform; the 16 lanes of a block are all here
-      const float s = block_scale(f);
-      reinterpret_cast<uint2*>(codes)[row * nch + ch] = codes8(f, s);
-      if ((t & 15) == 0) scales[(row * nch + ch) >> 4] = s;
+    for (int i = 0; i < CPT; ++i) {
+      const int left = K - 8 * (t + i * TPR);
+      float f[8];
+      c[i].get(f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] -= mu;
+      if (i == CPT - 1 && left < 8) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = e < left ? f[e] : 0.0f;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sq = fmaf(f[e], f[e], sq);
+      hold(c[i]);
     }
-    if (i == CPT - 1 && k0 >= K) continue;
-    if (p.w) {
-      float w[8];
-      param8(p.w, p.f32, k0, K, w);
+    const float r = 1.0f / sqrtf(row_sum<TPR>(sq, slot[flip + 1]) / (float)K + a.eps);
+    if (ok) {
+      if (t == 0) {
+        if (a.mean) a.mean[row] = mu;
+        if (a.rstd) a.rstd[row] = r;
+      }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = (f[e] - mu) * r * w[e];
-    } else {
+      for (int i = 0; i < CPT; ++i) {
+        const int ch = t + i * TPR, k0 = 8 * ch;
+        if (i == CPT - 1 && ch >= a.nch) continue;
+        float f[8], w[8], b[8];
+        c[i].get(f);
+        if (a.codes) {  // uniform; the 16 lanes of a block are all here
+          const float s = block_scale(c[i]);
+          reinterpret_cast<uint2*>(a.codes)[row * a.nch + ch] = codes8(f, s);
+          if ((t & 15) == 0) a.scales[(row * a.nch + ch) >> 4] = s;
+        }
+        cw[i].get(w);
+        cb[i].get(b);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = (f[e] - mu) * r;
+        for (int e = 0; e < 8; ++e) f[e] = (f[e] - mu) * r;
+        if (a.p.w) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = fmaf(f[e], w[e], b[e]);  // b: zeros where there is none
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] += b[e];
+        }
+        if (a.y_f32) {
+          float* yr = static_cast<float*>(a.y) + row * K;
+          if (i < CPT - 1) store8_in(yr + k0, f);
+          else store8(yr, k0, K, f);
+        } else {
+          uint16_t* yr = static_cast<uint16_t*>(a.y) + row * K;
+          if (i < CPT - 1) store8_in(yr + k0, f);
+          else store8(yr, k0, K, f);
+        }
+      }
     }
-    if (p.b) {
-      float b[8];
-      param8(p.b, p.f32, k0, K, b);
+    if (more) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] += b[e];
+      for (int i = 0; i < CPT; ++i) c[i] = nx[i];
     }
-    if (y_f32) store8(static_cast<float*>(y) + row * K, k0, K, o);
-    else store8(static_cast<uint16_t*>(y) + row * K, k0, K, o);
+    row = next;
   }
 }
 
@@ -138,9 +191,23 @@ struct FromF32 { typedef ChunkF32 Chunk; };
 struct ChunkCodes {
   uint2 q;
   float s;
-  __device__ __forceinline__ void get(float (&f)[8]) const { values8(q, s / 127.0f, f); }
 };
 struct FromCodes { typedef ChunkCodes Chunk; };
+
+// xh = x r + (-mu r), one operation a value; of a code, (q s / 127) r with
+// the scale's factors taken together.
+template <class C>
+__device__ __forceinline__ void normalized8(const C& c, float r, float nmr, float (&xh)[8]) {
+  float k = r;
+  if constexpr (std::is_same<C, ChunkCodes>::value) {
+    k = c.s / 127.0f * r;
+    values8(c.q, 1.0f, xh);
+  } else {
+    c.get(xh);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) xh[e] = fmaf(xh[e], k, nmr);
+}
 
 struct NormBwd {
   const void* dY;
@@ -157,7 +224,7 @@ struct NormBwd {
 };
 
 // Chunk ch of a row; IN: it lies inside the row.
-template <class X, bool IN>
+template <class X, bool IN, bool SHORT>
 __device__ __forceinline__ typename X::Chunk norm_x(const NormBwd& a, int64_t row, int ch) {
   if constexpr (std::is_same<X, FromCodes>::value) {
     ChunkCodes c;
@@ -168,27 +235,20 @@ __device__ __forceinline__ typename X::Chunk norm_x(const NormBwd& a, int64_t ro
   } else if constexpr (std::is_same<X, FromF32>::value) {
     const float* p = static_cast<const float*>(a.x) + row * a.K;
     if constexpr (IN) return load8_in(p + 8 * ch);
-    else return load8(p, 8 * ch, a.K);
+    else return load8<SHORT>(p, 8 * ch, a.K);
   } else {
     const uint16_t* p = static_cast<const uint16_t*>(a.x) + row * a.K;
     if constexpr (IN) return load8_in(p + 8 * ch);
-    else return load8(p, 8 * ch, a.K);
+    else return load8<SHORT>(p, 8 * ch, a.K);
   }
 }
 
 // The weight as fp32 in LDS: every row of the block reads it twice.
 extern __shared__ __attribute__((aligned(16))) float norm_lds[];
 
-// Keeps a loaded chunk as it is across the row's reduction: the values
-// derived from it are computed again after it instead of being held in
-// registers next to the column sums.
-__device__ __forceinline__ void hold(ChunkBf16& c) { asm volatile("" : "+v"(c.v.x), "+v"(c.v.y), "+v"(c.v.z), "+v"(c.v.w)); }
-__device__ __forceinline__ void hold(ChunkF32& c) {
-  asm volatile("" : "+v"(c.a.x), "+v"(c.a.y), "+v"(c.a.z), "+v"(c.a.w), "+v"(c.b.x), "+v"(c.b.y), "+v"(c.b.z), "+v"(c.b.w));
-}
 __device__ __forceinline__ void hold(ChunkCodes& c) { asm volatile("" : "+v"(c.q.x), "+v"(c.q.y), "+v"(c.s)); }
 
-template <class X, class DX, class DY, int BLOCK, int TPR, int CPT>
+template <class X, class DX, class DY, int BLOCK, int TPR, int CPT, bool SHORT>
 __global__ __launch_bounds__(BLOCK, BLOCK == 512 ? 1 : 2) void layernorm_bwd_kernel(NormBwd a) {
   constexpr int RPB = BLOCK / TPR;
   __shared__ float slot[4][BLOCK / kWave];
@@ -208,40 +268,59 @@ __global__ __launch_bounds__(BLOCK, BLOCK == 512 ? 1 : 2) void layernorm_bwd_ker
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[i][e] = db[i][e] = 0.0f;
 
-  int flip = 0;
-  for (int64_t base = (int64_t)blockIdx.x * RPB; base < a.M; base += (int64_t)gridDim.x * RPB, flip ^= 2) {
-    const int64_t row = base + rl;  // uniform in the wave
-    if (RPB > 1 && row >= a.M) break;  // rows of one wave: no barrier ahead
-    typename ChunkOf<DY>::type cd[CPT];
-    typename X::Chunk cx[CPT];
+  // the chunks of a row; only a thread's last can reach past K (row_split):
+  // dY is zero there, so nothing is added
+  const auto load = [&](int64_t row, typename ChunkOf<DY>::type (&cd)[CPT], typename X::Chunk (&cx)[CPT]) {
     const DY* dr = static_cast<const DY*>(a.dY) + row * K;
 #pragma unroll
     for (int i = 0; i < CPT - 1; ++i) {
       cd[i] = load8_in(dr + 8 * (t + i * TPR));
-      cx[i] = norm_x<X, true>(a, row, t + i * TPR);
+      cx[i] = norm_x<X, true, SHORT>(a, row, t + i * TPR);
     }
-    cd[CPT - 1] = load8(dr, 8 * (t + (CPT - 1) * TPR), K);
-    cx[CPT - 1] = norm_x<X, false>(a, row, t + (CPT - 1) * TPR);
-    const float mu = a.mean[row], r = a.rstd[row];
-    // only a thread's last chunk can reach past K (row_split); dY is zero
-    // there, so nothing is added, and what a chunk past the row's end reads
-    // of the weight (chunk 0) does not matter
-    settle8(cd[CPT - 1], 8 * (t + (CPT - 1) * TPR), K);
-    if constexpr (!std::is_same<X, FromCodes>::value) settle8(cx[CPT - 1], 8 * (t + (CPT - 1) * TPR), K);
-    const bool last = t + (CPT - 1) * TPR < a.nch;
+    cd[CPT - 1] = load8<SHORT>(dr, 8 * (t + (CPT - 1) * TPR), K);
+    cx[CPT - 1] = norm_x<X, false, SHORT>(a, row, t + (CPT - 1) * TPR);
+  };
+  // what a chunk past the row's end reads of the weight (chunk 0) does not matter
+  const int k_last = t + (CPT - 1) * TPR < a.nch ? 8 * (t + (CPT - 1) * TPR) : 0;
+  // The next row is loaded while this one is reduced where both fit the
+  // registers next to the column sums (measured at 2048 x 6912, f32 x: 55 us
+  // with it and spilled, 33 us without; at 16384 x 6912 from codes 118 us with
+  // it, 147 us without).
+  constexpr bool AHEAD = (sizeof(typename ChunkOf<DY>::type) + sizeof(typename X::Chunk)) / 4 * CPT <= 36;
+  typename ChunkOf<DY>::type cd[CPT], nd[CPT];
+  typename X::Chunk cx[CPT], nx[CPT];
+  // The block's row groups; every thread passes every barrier. Past the last
+  // row a wave (rows are uniform in a wave) repeats it with dY = 0.
+  const int64_t stride = (int64_t)gridDim.x * RPB, last = a.M - 1;
+  int64_t base = (int64_t)blockIdx.x * RPB, row = base + rl < last ? base + rl : last;
+  if constexpr (AHEAD) load(row, cd, cx);
+  float mu = a.mean[row], r = a.rstd[row];
+  int flip = 0;
+  for (; base < a.M; base += stride, flip ^= 2) {
+    const bool ok = base + rl < a.M;
+    const int64_t want = base + stride + rl, next = want < last ? want : last;
+    if constexpr (AHEAD) load(next, nd, nx);
+    else load(row, cd, cx);
+    const float nmu = a.mean[next], nr = a.rstd[next], nmr = -mu * r;
+    if (!ok) {
+#pragma unroll
+      for (int i = 0; i < CPT; ++i) cd[i] = typename ChunkOf<DY>::type{};
+    }
+    settle8<SHORT>(cd[CPT - 1], 8 * (t + (CPT - 1) * TPR), K);
+    if constexpr (!std::is_same<X, FromCodes>::value) settle8<SHORT>(cx[CPT - 1], 8 * (t + (CPT - 1) * TPR), K);
     float sg = 0.0f, sgx = 0.0f;
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
-      const float* w = norm_lds + 8 * (i < CPT - 1 || last ? t + i * TPR : 0);
-      float d[8], x[8];
+      const float* w = norm_lds + (i < CPT - 1 ? 8 * (t + i * TPR) : k_last);
+      float d[8], xh[8];
       cd[i].get(d);
-      cx[i].get(x);
+      normalized8(cx[i], r, nmr, xh);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float xh = (x[e] - mu) * r, g = d[e] * w[e];
+        const float g = d[e] * w[e];
         sg += g;
-        sgx = fmaf(g, xh, sgx);
-        dw[i][e] = fmaf(d[e], xh, dw[i][e]);
+        sgx = fmaf(g, xh[e], sgx);
+        dw[i][e] = fmaf(d[e], xh[e], dw[i][e]);
         db[i][e] += d[e];
       }
       hold(cd[i]);
@@ -250,26 +329,33 @@ __global__ __launch_bounds__(BLOCK, BLOCK == 512 ? 1 : 2) void layernorm_bwd_ker
     }
     // two slot pairs in turn: a row's readers are done with one pair before
     // the barrier of the next row, after which it may be written again
-    const float c1 = row_sum<TPR>(sg, slot[flip]) / (float)K;
-    const float c2 = row_sum<TPR>(sgx, slot[flip + 1]) / (float)K;
-    if (a.dX == nullptr) continue;
-#pragma unroll
-    for (int i = 0; i < CPT; ++i) {
-      const int k0 = 8 * (t + i * TPR);
-      const float* w = norm_lds + (i < CPT - 1 || last ? k0 : 0);
-      float d[8], x[8], o[8];
-      cd[i].get(d);
-      cx[i].get(x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float xh = (x[e] - mu) * r;
-        o[e] = r * (d[e] * w[e] - c1 - xh * c2);
-      }
+    const float c1 = row_sum<TPR>(sg, slot[flip]) / (float)K * r;
+    const float c2 = row_sum<TPR>(sgx, slot[flip + 1]) / (float)K * r;
+    if (a.dX != nullptr && ok) {
       DX* xr = static_cast<DX*>(a.dX) + row * K;
-      if (i < CPT - 1) store8_in(xr + k0, o);
-      else store8(xr, k0, K, o);
-      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < CPT; ++i) {
+        const float* w = norm_lds + (i < CPT - 1 ? 8 * (t + i * TPR) : k_last);
+        float d[8], xh[8], o[8];
+        cd[i].get(d);
+        normalized8(cx[i], r, nmr, xh);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = fmaf(-c2, xh[e], fmaf(d[e] * w[e], r, -c1));
+        if (i < CPT - 1) store8_in(xr + 8 * (t + i * TPR), o);
+        else store8(xr, 8 * (t + i * TPR), K, o);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int i = 0; i < CPT; ++i) {
+        cd[i] = nd[i];
+        cx[i] = nx[i];
+      }
+    }
+    mu = nmu;
+    r = nr;
+    row = next;
   }
 
   if (a.partials == nullptr) return;
@@ -338,8 +424,8 @@ __global__ __launch_bounds__(1024) void layernorm_cols_kernel(const float* __res
 
 // ---------------------------------------------------------------------------
 // Launches. Threads per row and chunks per thread from the row length alone:
-// one wave a row up to 2560 (no barriers), 256 threads up to 10240, 512
-// above (kNormMaxK).
+// one wave up to two chunks a thread (no barriers), two waves up to three, 4
+// waves up to four, 8 above (kNormMaxK).
 // ---------------------------------------------------------------------------
 
 struct RowSplit {
@@ -349,31 +435,44 @@ struct RowSplit {
 // whole chunk of the row (it lies before the row's last block of 128).
 static RowSplit row_split(int64_t K) {
   const int nch = (int)(ckpt_pad(K) / 8);
-  const int tpr = nch <= 320 ? 64 : nch <= 1280 ? 256 : 512;
+  const int tpr = nch <= 128 ? 64 : nch <= 384 ? 128 : nch <= 1024 ? 256 : 512;
   return {tpr, (nch + tpr - 1) / tpr};
 }
 
-template <class T, int BLOCK, int TPR, int CPT>
-static void norm_fwd_at(const void* x, const NormParams& p, int64_t M, int64_t K, float eps, void* y, bool y_f32,
-                        float* mean, float* rstd, int8_t* codes, float* scales, hipStream_t st) {
-  constexpr int RPB = BLOCK / TPR;
-  layernorm_fwd_kernel<T, BLOCK, TPR, CPT><<<(unsigned)((M + RPB - 1) / RPB), BLOCK, 0, st>>>(
-      static_cast<const T*>(x), p, M, (int)K, eps, y, y_f32, mean, rstd, codes, scales, (int)(ckpt_pad(K) / 8));
+// Every pair that row_split gives, and rows of fewer than 8 values.
+#define BITNET_NORM_SHAPES(F)                                                                                  \
+  F(64, 1, true) F(64, 1, false) F(64, 2, false) F(128, 2, false) F(128, 3, false) F(256, 2, false)            \
+  F(256, 3, false) F(256, 4, false) F(512, 3, false) F(512, 4, false) F(512, 5, false) F(512, 6, false)        \
+  F(512, 7, false) F(512, 8, false)
+
+// Row groups of a launch.
+static int64_t row_groups(int64_t M, const RowSplit& s) {
+  const int64_t rpb = s.tpr < 256 ? 256 / s.tpr : 1;
+  return (M + rpb - 1) / rpb;
 }
 
-#define BITNET_NORM_SHAPES(F)                                                                       \
-  F(64, 1) F(64, 2) F(64, 3) F(64, 4) F(64, 5) F(256, 2) F(256, 3) F(256, 4) F(256, 5) F(512, 3) \
-  F(512, 4) F(512, 5) F(512, 6) F(512, 7) F(512, 8)
+// Blocks of the forward: as many as run together on 256 CUs, so that each
+// block's weight and bias are read once and no block starts late.
+template <class T, class P, int TPR, int CPT, bool SHORT>
+static hipError_t norm_fwd_at(const NormFwd& a, int64_t groups, hipStream_t st) {
+  constexpr int BLOCK = TPR < 256 ? 256 : TPR;
+  static const int per_cu = [] {
+    int n = 0;
+    const hipError_t e = hipOccupancyMaxActiveBlocksPerMultiprocessor(
+        &n, layernorm_fwd_kernel<T, P, BLOCK, TPR, CPT, SHORT>, BLOCK, 0);
+    return e == hipSuccess && n > 0 ? n : 1;
+  }();
+  const int64_t most = 256 * (int64_t)per_cu;
+  layernorm_fwd_kernel<T, P, BLOCK, TPR, CPT, SHORT><<<(unsigned)std::min(groups, most), BLOCK, 0, st>>>(a);
+  return hipGetLastError();
+}
 
-template <class T>
-static hipError_t norm_fwd(const void* x, const NormParams& p, int64_t M, int64_t K, float eps, void* y, bool y_f32,
-                           float* mean, float* rstd, int8_t* codes, float* scales, hipStream_t st) {
-  const RowSplit s = row_split(K);
-#define BITNET_CASE(TPR, CPT)                                                                                   \
-  if (s.tpr == TPR && s.cpt == CPT) {                                                                           \
-    norm_fwd_at<T, (TPR < 256 ? 256 : TPR), TPR, CPT>(x, p, M, K, eps, y, y_f32, mean, rstd, codes, scales, st); \
-    return hipGetLastError();                                                                                   \
-  }
+template <class T, class P>
+static hipError_t norm_fwd(const NormFwd& a, hipStream_t st) {
+  const RowSplit s = row_split(a.K);
+#define BITNET_CASE(TPR, CPT, SHORT)                        \
+  if (s.tpr == TPR && s.cpt == CPT && SHORT == (a.K < 8))   \
+    return norm_fwd_at<T, P, TPR, CPT, SHORT>(a, row_groups(a.M, s), st);
   BITNET_NORM_SHAPES(BITNET_CASE)
 #undef BITNET_CASE
   return hipErrorInvalidValue;
@@ -382,9 +481,9 @@ static hipError_t norm_fwd(const void* x, const NormParams& p, int64_t M, int64_
 hipError_t launch_layernorm_fwd(const void* x, bool x_f32, const void* w, const void* b, bool p_f32, int64_t M,
                                 int64_t K, float eps, void* y, bool y_f32, float* mean, float* rstd, int8_t* codes,
                                 float* scales, hipStream_t stream) {
-  const NormParams p{w, b, p_f32};
-  return x_f32 ? norm_fwd<float>(x, p, M, K, eps, y, y_f32, mean, rstd, codes, scales, stream)
-               : norm_fwd<uint16_t>(x, p, M, K, eps, y, y_f32, mean, rstd, codes, scales, stream);
+  const NormFwd a{x, NormParams{w, b, p_f32}, M, (int)K, (int)(ckpt_pad(K) / 8), eps, y, y_f32, mean, rstd, codes, scales};
+  if (x_f32) return p_f32 ? norm_fwd<float, float>(a, stream) : norm_fwd<float, uint16_t>(a, stream);
+  return p_f32 ? norm_fwd<uint16_t, float>(a, stream) : norm_fwd<uint16_t, uint16_t>(a, stream);
 }
 
 // Blocks of the backward: enough for two of 256 threads on each of 256 CUs,
@@ -392,10 +491,7 @@ hipError_t launch_layernorm_fwd(const void* x, bool x_f32, const void* w, const 
 constexpr int kNormBwdBlocks = 512;
 static int norm_bwd_blocks(int64_t M, int64_t K) {
   const RowSplit s = row_split(K);
-  const int64_t rpb = s.tpr < 256 ? 256 / s.tpr : 1;
-  const int64_t groups = (M + rpb - 1) / rpb;
-  const int64_t most = s.tpr == 512 ? kNormBwdBlocks / 2 : kNormBwdBlocks;
-  return (int)(groups < most ? groups : most);
+  return (int)std::min<int64_t>(row_groups(M, s), s.tpr == 512 ? kNormBwdBlocks / 2 : kNormBwdBlocks);
 }
 
 size_t layernorm_bwd_workspace(int64_t M, int64_t K) { return (size_t)norm_bwd_blocks(M, K) * 2 * (size_t)K * 4; }
@@ -404,10 +500,10 @@ template <class X, class DX, class DY>
 static hipError_t norm_bwd(const NormBwd& a, hipStream_t st) {
   const RowSplit s = row_split(a.K);
   const int blocks = norm_bwd_blocks(a.M, a.K);
-#define BITNET_CASE(TPR, CPT)                                                                      \
-  if (s.tpr == TPR && s.cpt == CPT) {                                                              \
+#define BITNET_CASE(TPR, CPT, SHORT)                                                               \
+  if (s.tpr == TPR && s.cpt == CPT && SHORT == (a.K < 8)) {                                        \
     constexpr int BLOCK = TPR < 256 ? 256 : TPR;                                                   \
-    layernorm_bwd_kernel<X, DX, DY, BLOCK, TPR, CPT><<<blocks, BLOCK, (size_t)a.nch * 32, st>>>(a);    \
+    layernorm_bwd_kernel<X, DX, DY, BLOCK, TPR, CPT, SHORT><<<blocks, BLOCK, (size_t)a.nch * 32, st>>>(a); \
     return hipGetLastError();                                                                      \
   }
   BITNET_NORM_SHAPES(BITNET_CASE)

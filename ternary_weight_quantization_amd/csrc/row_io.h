@@ -28,15 +28,17 @@ template <class T> struct ChunkOf;
 template <> struct ChunkOf<uint16_t> { typedef ChunkBf16 type; };
 template <> struct ChunkOf<float> { typedef ChunkF32 type; };
 
-// The 8 values k0 .. k0 + 7 of a row of K, zeros at or past K. The loads are
-// unconditional, so that all chunks of a row are in flight together (a load
-// under a condition is waited for where the branches join): a chunk that
-// crosses or lies past the row's end loads the row's last 8 values and moves
-// them down. Rows may start at any element (unaligned 16-byte loads). Rows of
-// fewer than 8 values are read one by one.
+// The 8 values k0 .. k0 + 7 of a row of K, zeros at or past K, in two steps:
+// load8 and, once it is needed, settle8. The load is unconditional, so that
+// all chunks of a row are in flight together (a load under a condition is
+// waited for where the branches join): a chunk that crosses or lies past the
+// row's end loads the row's last 8 values, which settle8 moves down. Rows may
+// start at any element (unaligned 16-byte loads). SHORT: rows of fewer than 8
+// values, read one by one.
+template <bool SHORT>
 __device__ __forceinline__ ChunkBf16 load8(const uint16_t* row, int k0, int K) {
   ChunkBf16 c;
-  if (K < 8) {
+  if constexpr (SHORT) {
     uint32_t d[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -50,9 +52,10 @@ __device__ __forceinline__ ChunkBf16 load8(const uint16_t* row, int k0, int K) {
   memcpy(&c.v, row + (k0 + 8 <= K ? k0 : K - 8), 16);
   return c;
 }
+template <bool SHORT>
 __device__ __forceinline__ void settle8(ChunkBf16& c, int k0, int K) {
   const int d = k0 + 8 - K;  // values to drop
-  if (K < 8 || d <= 0) return;
+  if (SHORT || d <= 0) return;
   if (d >= 8) {
     c.v = make_uint4(0u, 0u, 0u, 0u);
     return;
@@ -66,9 +69,10 @@ __device__ __forceinline__ void settle8(ChunkBf16& c, int k0, int K) {
   }
   c.v = make_uint4(w[0], w[1], w[2], w[3]);
 }
+template <bool SHORT>
 __device__ __forceinline__ ChunkF32 load8(const float* row, int k0, int K) {
   ChunkF32 c;
-  if (K < 8) {
+  if constexpr (SHORT) {
     uint32_t d[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) d[j] = k0 + j < K ? __float_as_uint(row[k0 + j]) : 0u;
@@ -81,9 +85,10 @@ __device__ __forceinline__ ChunkF32 load8(const float* row, int k0, int K) {
   memcpy(&c.b, p + 4, 16);
   return c;
 }
+template <bool SHORT>
 __device__ __forceinline__ void settle8(ChunkF32& c, int k0, int K) {
   const int d = k0 + 8 - K;
-  if (K < 8 || d <= 0) return;
+  if (SHORT || d <= 0) return;
   uint32_t w[8] = {c.a.x, c.a.y, c.a.z, c.a.w, c.b.x, c.b.y, c.b.z, c.b.w};
 #pragma unroll
   for (int s = 4; s >= 1; s >>= 1)
@@ -112,18 +117,20 @@ __device__ __forceinline__ ChunkF32 load8_in(const float* p) {
   return c;
 }
 
+// Both steps, rows of any length.
+template <class T>
+__device__ __forceinline__ typename ChunkOf<T>::type chunk8(const T* row, int k0, int K) {
+  if (K < 8) return load8<true>(row, k0, K);
+  typename ChunkOf<T>::type c = load8<false>(row, k0, K);
+  settle8<false>(c, k0, K);
+  return c;
+}
+
 // 8 values of a parameter vector [K] of either type (f32: is_f32), zeros at
 // or past K.
 __device__ __forceinline__ void param8(const void* p, bool is_f32, int k0, int K, float (&f)[8]) {
-  if (is_f32) {
-    ChunkF32 c = load8(static_cast<const float*>(p), k0, K);
-    settle8(c, k0, K);
-    c.get(f);
-  } else {
-    ChunkBf16 c = load8(static_cast<const uint16_t*>(p), k0, K);
-    settle8(c, k0, K);
-    c.get(f);
-  }
+  if (is_f32) chunk8(static_cast<const float*>(p), k0, K).get(f);
+  else chunk8(static_cast<const uint16_t*>(p), k0, K).get(f);
 }
 
 // 8 values, all inside the row.
@@ -134,23 +141,48 @@ __device__ __forceinline__ void store8_in(uint16_t* p, const float (&f)[8]) {
 }
 __device__ __forceinline__ void store8_in(float* p, const float (&f)[8]) { memcpy(p, f, 32); }
 
-// Values k0 .. k0 + 7 of a row, those below K.
+// Values k0 .. k0 + 7 of a row, those below K: a broken chunk in pieces of 4,
+// 2 and 1.
 __device__ __forceinline__ void store8(uint16_t* row, int k0, int K, const float (&f)[8]) {
-  if (k0 + 8 <= K) {
-    store8_in(row + k0, f);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (k0 + e < K) row[k0 + e] = f32_to_bf16_bits(f[e]);
+  const int n = K - k0;
+  uint16_t* p = row + k0;
+  if (n >= 8) {
+    store8_in(p, f);
+  } else if (n > 0) {
+    uint2 a = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+    const uint2 b = make_uint2(pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+    if (n & 4) {
+      memcpy(p, &a, 8);
+      p += 4;
+      a = b;
+    }
+    if (n & 2) {
+      memcpy(p, &a.x, 4);
+      p += 2;
+      a.x = a.y;
+    }
+    if (n & 1) *p = (uint16_t)a.x;
   }
 }
 __device__ __forceinline__ void store8(float* row, int k0, int K, const float (&f)[8]) {
-  if (k0 + 8 <= K) {
-    store8_in(row + k0, f);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (k0 + e < K) row[k0 + e] = f[e];
+  const int n = K - k0;
+  float* p = row + k0;
+  if (n >= 8) {
+    store8_in(p, f);
+  } else if (n > 0) {
+    float4 a = make_float4(f[0], f[1], f[2], f[3]);
+    if (n & 4) {
+      memcpy(p, &a, 16);
+      p += 4;
+      a = make_float4(f[4], f[5], f[6], f[7]);
+    }
+    if (n & 2) {
+      const float2 v = make_float2(a.x, a.y);
+      memcpy(p, &v, 8);
+      p += 2;
+      a.x = a.z;
+    }
+    if (n & 1) *p = a.x;
   }
 }
 
@@ -169,14 +201,30 @@ __device__ __forceinline__ uint32_t row_ror(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + N, 0xF, 0xF, true);
 }
 
-// The scale of a block, in each of its 16 lanes.
-__device__ __forceinline__ float block_scale(const float (&f)[8]) {
+// The largest magnitude of a lane's 8 values as a bit pattern.
+__device__ __forceinline__ uint32_t magnitude8(const ChunkF32& c) {
+  const uint32_t w[8] = {c.a.x, c.a.y, c.a.z, c.a.w, c.b.x, c.b.y, c.b.z, c.b.w};
   uint32_t m = 0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const uint32_t a = __float_as_uint(f[e]) & 0x7FFFFFFFu;
+    const uint32_t a = w[e] & 0x7FFFFFFFu;
     m = a > m ? a : m;
   }
+  return m;
+}
+__device__ __forceinline__ uint32_t magnitude8(const ChunkBf16& c) {  // two values an instruction
+  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+  const auto mag = [](uint32_t w) { return __builtin_bit_cast(u16x2, w & 0x7FFF7FFFu); };
+  const u16x2 m = __builtin_elementwise_max(__builtin_elementwise_max(mag(c.v.x), mag(c.v.y)),
+                                            __builtin_elementwise_max(mag(c.v.z), mag(c.v.w)));
+  const uint32_t lo = m.x, hi = m.y;
+  return (lo > hi ? lo : hi) << 16;
+}
+
+// The scale of a block, in each of its 16 lanes.
+template <class C>
+__device__ __forceinline__ float block_scale(const C& c) {
+  uint32_t m = magnitude8(c);
   uint32_t o;
   o = row_ror<8>(m); m = o > m ? o : m;
   o = row_ror<4>(m); m = o > m ? o : m;
@@ -186,35 +234,35 @@ __device__ __forceinline__ float block_scale(const float (&f)[8]) {
 }
 
 // round_half_even(127 x / s) for |x| <= s as the fp32 value 1.5 * 2^23 + q,
-// whose low byte is q. p = x * fl(127/s) is within 1.6e-5 of the quotient, so
-// more than 2^-15 away from a half integer its nearest integer is the
-// quotient's; otherwise the quotient is taken in fp64, whose rounding error
-// (below 2^-46) is far below the least distance (2^-33) of a quotient of fp32
-// values from a half integer that it is not.
+// whose low byte is q. t = fl(x fl(127/s) + 1.5 * 2^23) holds the integer
+// nearest to x fl(127/s), which is within 1.6e-5 of the quotient; where their
+// distance is less than 1/2 - 2^-15 that integer is the quotient's too.
+// Otherwise the quotient is taken in fp64, whose rounding error (below 2^-46)
+// is far below the least distance (2^-33) of a quotient of fp32 values from a
+// half integer that it is not.
 constexpr float kCodeMagic = 12582912.0f;  // 1.5 * 2^23
+constexpr float kCodeSure = 0.49996948f;   // 1/2 - 2^-15
 __device__ __forceinline__ float code_exact(float x, float s) {
   return (float)__builtin_rint(127.0 * (double)x / (double)s) + kCodeMagic;
 }
 
 // The codes of 8 values of a block with scale s. Scales so small that 127 / s
-// would not be a finite fp32 number, and zero, take the exact route.
+// would not be a finite fp32 number, and zero, take the exact route. The
+// largest of the 8 distances decides once for all (four operations a value:
+// the code, its integer, the distance, its maximum).
 __device__ __forceinline__ uint2 codes8(const float (&f)[8], float s) {
   const bool tiny = s < 1e-30f;
   const float r127 = tiny ? 0.0f : 127.0f / s;
-  float t[8];
-  bool slow = tiny && s > 0.0f;
+  float t[8], far = 0.0f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float p = f[e] * r127;
-    t[e] = p + kCodeMagic;
-    slow |= fabsf(p - (t[e] - kCodeMagic)) > 0.49996948f;  // 0.5 - 2^-15
+    t[e] = fmaf(f[e], r127, kCodeMagic);
+    far = fmaxf(far, fabsf(fmaf(f[e], r127, -(t[e] - kCodeMagic))));
   }
-  if (slow) {
+  if (far > kCodeSure || (tiny && s > 0.0f)) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float p = f[e] * r127, u = p + kCodeMagic;
-      t[e] = tiny || fabsf(p - (u - kCodeMagic)) > 0.49996948f ? code_exact(f[e], s) : u;
-    }
+    for (int e = 0; e < 8; ++e)
+      if (tiny || fabsf(fmaf(f[e], r127, -(t[e] - kCodeMagic))) > kCodeSure) t[e] = code_exact(f[e], s);
   }
   const auto pack = [](float a, float b, float c, float d) {
     const uint32_t lo = perm(__float_as_uint(b), __float_as_uint(a), 0x0C0C0400u);

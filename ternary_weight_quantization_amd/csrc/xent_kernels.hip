@@ -6,7 +6,11 @@
 //   G[t][v]  = c[t] (exp(z[t][v] - lse[t]) - [v == target[t]])
 //   dh       = G W,   dW = G^T h
 //
-// (c[t]: the loss' gradient with respect to loss[t].) The three products are
+// (c[t]: the loss' gradient with respect to loss[t]. Under a sum or a mean it
+// is one number c for all rows, and G is computed without it and the products
+// are multiplied by it in fp32: the target's element is then p - 1, which
+// bf16 holds to within p, where c (p - 1) would be rounded by the same 2^-9
+// in every row.) The three products are
 // bf16 MFMA GEMMs with fp32 sums, so the whole is MFMA bound for many tokens:
 // 2TVD operations for the loss, 4TVD for the gradients and 2TVD for the
 // logits computed again, because keeping them would take 4TV bytes (2 GB at
@@ -44,9 +48,11 @@ namespace bitnet {
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
-// Control block at the start of the workspace: n.
+// Control block at the start of the workspace: n, and c where it is one for
+// all rows (1 otherwise).
 struct XentCtl {
   int n;
+  float c;
 };
 
 // ---------------------------------------------------------------------------
@@ -68,7 +74,7 @@ struct XentRows {
   const float* dloss;      // [1], or [T] with per_row
   int per_row, mean;
   float* lse2;             // [T] lse log2(e) of the rows that count
-  float* c;                // [T] their c
+  float* c;                // [T] what G's rows are multiplied by
 };
 
 constexpr int kGatherRows = 8;  // two for each of the block's waves
@@ -99,7 +105,10 @@ __global__ __launch_bounds__(256) void xent_gather_kernel(XentRows a) {
   __syncthreads();
   b = (before[0] + before[1]) + (before[2] + before[3]);
   n = (all[0] + all[1]) + (all[2] + all[3]);
-  if (blockIdx.x == 0 && tid == 0) a.ctl->n = n;
+  if (blockIdx.x == 0 && tid == 0) {
+    a.ctl->n = n;
+    if constexpr (BWD) a.ctl->c = a.per_row ? 1.0f : a.mean ? *a.dloss / (float)n : *a.dloss;
+  }
   const int lane = tid & 63, wave = tid >> 6, nch = a.Dp / 8;
   // which of the block's rows count, in every lane of every wave
   const int tl = t0 + (lane & (kGatherRows - 1));
@@ -117,8 +126,7 @@ __global__ __launch_bounds__(256) void xent_gather_kernel(XentRows a) {
       a.pos[t] = at;
       a.ct[at] = in ? (int)target : -1;
       if constexpr (BWD) {
-        float c = a.per_row ? a.dloss[t] : *a.dloss;
-        if (a.mean) c /= (float)n;
+        const float c = a.per_row ? a.dloss[t] : 1.0f;
         a.lse2[at] = a.lse[t] * kLog2e;
         a.c[at] = in ? c : __uint_as_float(0x7FC00000u);  // a target out of range: NaN gradients
       }
@@ -128,11 +136,12 @@ __global__ __launch_bounds__(256) void xent_gather_kernel(XentRows a) {
     for (int c0 = 0; c0 < nch; c0 += 256) {
       ChunkBf16 v[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = load8(src, 8 * (c0 + lane + 64 * i), a.D);
+      for (int i = 0; i < 4; ++i)
+        v[i] = a.D < 8 ? load8<true>(src, 8 * (c0 + lane + 64 * i), a.D) : load8<false>(src, 8 * (c0 + lane + 64 * i), a.D);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int ch = c0 + lane + 64 * i;
-        settle8(v[i], 8 * ch, a.D);
+        if (a.D >= 8) settle8<false>(v[i], 8 * ch, a.D);
         if (ch < nch) dst[ch] = v[i].v;
       }
     }
@@ -147,9 +156,7 @@ __global__ __launch_bounds__(256) void xent_pad_kernel(const uint16_t* __restric
   if (i >= rows * nch) return;
   const int64_t r = i / nch;
   const int k0 = 8 * (int)(i - r * nch);
-  ChunkBf16 v = load8(w + r * D, k0, D);
-  settle8(v, k0, D);
-  reinterpret_cast<uint4*>(out)[i] = v.v;
+  reinterpret_cast<uint4*>(out)[i] = chunk8(w + r * D, k0, D).v;
 }
 
 // ---------------------------------------------------------------------------
@@ -579,11 +586,12 @@ struct AccumEpilogue {
   }
 };
 
-// dW's tile: rounded once to its type.
+// dW's tile times c, rounded once to its type.
 template <bool F32>
 struct DwEpilogue {
   void* out;
   int64_t I, J;
+  float c;
   __device__ __forceinline__ void store(AccTile& acc, int i0, int j0, int lane, char* wlds) const {
     constexpr int EB = F32 ? 4 : 2;
 #pragma unroll
@@ -592,8 +600,8 @@ struct DwEpilogue {
       for (int fi = 0; fi < kFI; ++fi)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const float v0 = acc[fi][fj][4 * g], v1 = acc[fi][fj][4 * g + 1], v2 = acc[fi][fj][4 * g + 2],
-                      v3 = acc[fi][fj][4 * g + 3];
+          const float v0 = acc[fi][fj][4 * g] * c, v1 = acc[fi][fj][4 * g + 1] * c, v2 = acc[fi][fj][4 * g + 2] * c,
+                      v3 = acc[fi][fj][4 * g + 3] * c;
           if constexpr (F32)
             EpStage<4>::put(wlds, lane, fi, g, make_uint4(__float_as_uint(v0), __float_as_uint(v1),
                                                           __float_as_uint(v2), __float_as_uint(v3)));
@@ -644,14 +652,16 @@ __global__ __launch_bounds__(kThreads, 1) void xent_grads_kernel(XentGrads a) {
   const XentHt pl{a.hc, a.Dp, n, a.Dp};
   const XentGt ql{a.G, a.ldg, n, a.ldg};
   run_stages<MfmaBf16, 0>(pl, ql, smem, acc, i0, j0, 0, (n + kRed16 - 1) / kRed16, pi, qj, lane, nullptr, 0);
-  const DwEpilogue<F32> ep{a.dw, a.D, a.vc};
+  // no row counts: G and hc are empty and c may be anything
+  const DwEpilogue<F32> ep{a.dw, a.D, a.vc, n > 0 ? a.ctl->c : 0.0f};
   ep.store(acc, i0 + pi, j0 + qj, lane, wlds);
 }
 
-// dh [T][D] from the slabs: their sum in order, rounded once, at the rows
-// that count; zeros elsewhere.
+// dh [T][D] from the slabs: their sum in order times c, rounded once, at the
+// rows that count; zeros elsewhere.
 __global__ __launch_bounds__(256) void xent_dh_kernel(const float* __restrict__ slab, int split,
-                                                      const int* __restrict__ pos, int T, int D, int nch,
+                                                      const int* __restrict__ pos,
+                                                      const XentCtl* __restrict__ ctl, int T, int D, int nch,
                                                       uint16_t* __restrict__ dh) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= (int64_t)T * nch) return;
@@ -660,13 +670,14 @@ __global__ __launch_bounds__(256) void xent_dh_kernel(const float* __restrict__ 
   float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
   if (at >= 0) {
     for (int s = 0; s < split; ++s) {
-      ChunkF32 c = load8(slab + ((int64_t)s * T + at) * D, k0, D);
-      settle8(c, k0, D);
       float f[8];
-      c.get(f);
+      chunk8(slab + ((int64_t)s * T + at) * D, k0, D).get(f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] += f[e];
     }
+    const float c = ctl->c;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= c;
   }
   store8(dh + (int64_t)t * D, k0, D, v);
 }
@@ -901,7 +912,7 @@ hipError_t launch_xent_bwd(const uint16_t* h, const uint16_t* w, const int64_t* 
   }
   if (dh == nullptr) return hipSuccess;
   const int nch = (int)(p.Dp / 8);
-  xent_dh_kernel<<<(unsigned)((T * nch + 255) / 256), 256, 0, stream>>>(g.slab, g.split, r.pos, r.T, r.D, nch, dh);
+  xent_dh_kernel<<<(unsigned)((T * nch + 255) / 256), 256, 0, stream>>>(g.slab, g.split, r.pos, r.ctl, r.T, r.D, nch, dh);
   return hipGetLastError();
 }
 

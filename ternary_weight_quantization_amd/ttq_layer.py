@@ -19,7 +19,6 @@ import math
 import torch
 
 from . import binding as B
-from .checkpoint import compress
 
 
 def _inverse_softplus(v):
@@ -68,11 +67,10 @@ class TTQFunction(torch.autograd.Function):
     """y = x @ W_t^T with W_t from Eq. 1. x [..., K] bf16, weight [N, K] bf16
     or float32, params float32 [3] = (delta, Wp, Wn), already positive.
     Gradients: dX bf16, dW in the weight's dtype, d params =
-    (0, dL/dWp, dL/dWn) (the threshold gets none). checkpoint: x is kept for
-    the backward as 8-bit codes (``checkpoint.compress``)."""
+    (0, dL/dWp, dL/dWn) (the threshold gets none)."""
 
     @staticmethod
-    def forward(ctx, x, weight, params, checkpoint=False):
+    def forward(ctx, x, weight, params):
         if x.dtype != torch.bfloat16:
             raise TypeError("TTQ expects bf16 activations")
         N, K = weight.shape
@@ -84,23 +82,13 @@ class TTQFunction(torch.autograd.Function):
         y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
         ws = _workspace(B.ttq_workspace_bytes(M, N, K), x.device)
         B.ttq_fwd(x2, wt, y, workspace=ws)
-        ctx.checkpoint = checkpoint
-        if checkpoint:
-            # dW alone reads x
-            needs_x = ctx.needs_input_grad[1] or ctx.needs_input_grad[2]
-            codes, scales = compress(x2) if needs_x else (None, None)
-            ctx.save_for_backward(codes, scales, wt, w_packed)
-        else:
-            ctx.save_for_backward(x2, wt, w_packed)
+        ctx.save_for_backward(x2, wt, w_packed)
         ctx.shape = (M, N, K, lead, weight.dtype)
         return y.reshape(*lead, N)
 
     @staticmethod
     def backward(ctx, dy):
-        if ctx.checkpoint:
-            codes, scales, wt, w_packed = ctx.saved_tensors
-        else:
-            x2, wt, w_packed = ctx.saved_tensors
+        x2, wt, w_packed = ctx.saved_tensors
         M, N, K, lead, wdtype = ctx.shape
         dY = dy.reshape(M, N).to(torch.bfloat16).contiguous()
         need_x, need_w, need_p = ctx.needs_input_grad[:3]
@@ -110,21 +98,19 @@ class TTQFunction(torch.autograd.Function):
         dW = torch.empty((N, K), dtype=wdtype, device=dy.device) if (need_w or need_p) else None
         dparams = torch.zeros((3,), dtype=torch.float32, device=dy.device) if need_p else None
         if dX is not None or dW is not None:
-            grads = None if dparams is None else dparams[1:]
-            if ctx.checkpoint:
-                B.ttq_bwd_ckpt(dY, codes, scales, wt, w_packed, K, dX=dX, dW=dW, grads=grads,
-                               workspace=_workspace(B.ttq_bwd_ckpt_workspace_bytes(M, N, K), dy.device))
-            else:
-                B.ttq_bwd(dY, x2, wt, w_packed, K, dX=dX, dW=dW, grads=grads,
-                          workspace=_workspace(B.ttq_workspace_bytes(M, N, K), dy.device))
-        return (None if dX is None else dX.reshape(*lead, K)), (dW if need_w else None), dparams, None
+            B.ttq_bwd(dY, x2, wt, w_packed, K, dX=dX, dW=dW, grads=None if dparams is None else dparams[1:],
+                      workspace=_workspace(B.ttq_workspace_bytes(M, N, K), dy.device))
+        return (None if dX is None else dX.reshape(*lead, K)), (dW if need_w else None), dparams
 
 
 def ttq_linear(x, weight, params, checkpoint=False):
     """x [..., K] bf16 times the TTQ weight of (weight [N, K], params float32
     [3] = (delta, Wp, Wn), positive): ``TTQFunction`` as a function.
-    ``checkpoint=True`` keeps x in 8 bits for dW."""
-    return TTQFunction.apply(x, weight, params, checkpoint)
+    ``checkpoint=True`` keeps x for dW as 8-bit codes (``checkpoint.compress``)
+    instead of in bf16; dW then is that of the codes' values."""
+    if checkpoint:
+        return B.ops().ttq_linear_checkpoint(x, weight, params)
+    return TTQFunction.apply(x, weight, params)
 
 
 class TTQLinear(torch.nn.Module):
@@ -132,7 +118,7 @@ class TTQLinear(torch.nn.Module):
     kaiming-uniform(a=sqrt(5)) init like QATBitLinear) and three raw scalars
     whose softplus gives delta, Wp and Wn, initialized from the weights by
     the library (Eq. 2). checkpoint=True: the input is kept in 8 bits for the
-    backward (``checkpoint.compress``) instead of in bf16."""
+    backward instead of in bf16."""
 
     def __init__(self, in_features, out_features, device="cuda", dtype=torch.bfloat16, checkpoint=False):
         super().__init__()
@@ -163,7 +149,7 @@ class TTQLinear(torch.nn.Module):
         return torch.nn.functional.softplus(self.raw)
 
     def forward(self, x):
-        return TTQFunction.apply(x, self.weight, self.params(), self.checkpoint)
+        return ttq_linear(x, self.weight, self.params(), self.checkpoint)
 
     @torch.no_grad()
     def export_inference(self):
