@@ -422,15 +422,27 @@ __global__ __launch_bounds__(1024) void xent_reduce_kernel(const float* __restri
 }
 
 // ---------------------------------------------------------------------------
-// Few tokens: one pass over W. A workgroup takes 32 rows of W, its 4 waves
+// Few tokens: one pass over W. A workgroup takes kFewRows rows of W, its waves
 // every 4th stage of 64 columns; both operands go from memory straight to
-// the fragments (each lane reads 64 contiguous bytes of a row per stage), the
-// waves' sums meet in LDS, and the first wave reduces the tile to one pair
-// per token and 32 rows.
+// the fragments of v_mfma_f32_16x16x32_bf16, the waves' sums meet in LDS, and
+// each group of 16 tokens reduces its column of the tile to one pair per
+// token and kFewRows rows.
+//
+// A fragment's lane l holds 8 values of row l % 16 at reduction chunk l / 16,
+// so a load covers 64 contiguous bytes of 16 rows and the stage's second load
+// the rest of those 128-byte lines. (With 32 x 32 fragments a load takes 32
+// bytes of 32 rows; the other three loads of a line then often found it gone
+// from L1: 36 us at 16 x 2560 against 32000 columns, where this takes 29 us,
+// 5.6 TB/s of W, and slower the more loads were in flight.) Measured there for
+// the whole loss: 64 rows and 4 waves a workgroup 39.0 us, 8 waves 40.1 us, 16
+// waves 44.4 us, 32 rows 43.3 us; one launch in which the last workgroup joins
+// the pairs 58-78 us (arrivals at one address run 25 ns apart).
 // ---------------------------------------------------------------------------
 
 constexpr int kFewTokens = 64;
+constexpr int kFewRows = 64;
 constexpr int kFewWaves = 4;
+constexpr int kFewFrags = kFewRows / 16;
 
 struct XentFew {
   const uint16_t* w;  // [V][D], D a multiple of 8
@@ -439,82 +451,103 @@ struct XentFew {
   const uint16_t* h;  // [T][D]
   int T;
   const int64_t* targets;
-  float2* part;  // [ceil(V / 32)][T]
+  float2* part;  // [ceil(V / kFewRows)][T]
   float* zt;     // [T]
 };
 
-template <int MT>
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+// TT groups of 16 tokens.
+template <int TT>
 __global__ __launch_bounds__(kWave * kFewWaves) void xent_few_kernel(XentFew a) {
-  __shared__ float red[kFewWaves][MT][16][kWave];
+  constexpr int W = kFewWaves;
+  __shared__ f32x4_t red[W][TT][kFewFrags][kWave];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int64_t v0 = (int64_t)blockIdx.x * 32;
-  const int D = a.D, half = lane >> 5;
-  const int rows = (int)(a.V - v0 < 32 ? a.V - v0 : 32);
+  const int64_t v0 = (int64_t)blockIdx.x * kFewRows;
+  const int D = a.D, q = lane >> 4;
+  const int rows = (int)(a.V - v0 < kFewRows ? a.V - v0 : kFewRows);
   const rsrc_t rw = make_rsrc(a.w + v0 * D, (uint32_t)(rows * D * 2));
   const rsrc_t rh = make_rsrc(a.h, (uint32_t)(a.T * D * 2));
-  const uint32_t wo = (uint32_t)((lane & 31) * D * 2);
-  uint32_t ho[MT];
+  const uint32_t row = (uint32_t)((lane & 15) * D * 2);  // rows past the end read as zeros
+  f32x4_t acc[TT][kFewFrags];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) ho[m] = (uint32_t)((32 * m + (lane & 31)) * D * 2);
-  MfmaBf16::Acc acc[MT];
+  for (int t = 0; t < TT; ++t)
 #pragma unroll
-  for (int m = 0; m < MT; ++m) zero_acc(acc[m]);
+    for (int f = 0; f < kFewFrags; ++f) acc[t][f] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   const int stages = (D + 63) / 64;
-  uint4 pw[4], ph[MT][4];
+  uint4 pw[kFewFrags][2], ph[TT][2];
   const auto load = [&](int s) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int k = 64 * s + 32 * half + 8 * c;  // columns past D: an out-of-range offset
-      pw[c] = buf_load16(rw, k < D ? wo + 2 * k : kOob);
+    for (int c = 0; c < 2; ++c) {
+      const int k = 64 * s + 32 * c + 8 * q;
+      const uint32_t off = k < D ? row + 2 * k : kOob;  // columns past D: an out-of-range offset
 #pragma unroll
-      for (int m = 0; m < MT; ++m) ph[m][c] = buf_load16(rh, k < D ? ho[m] + 2 * k : kOob);
+      for (int f = 0; f < kFewFrags; ++f) pw[f][c] = buf_load16(rw, off + (uint32_t)(32 * f * D));
+#pragma unroll
+      for (int t = 0; t < TT; ++t) ph[t][c] = buf_load16(rh, off + (uint32_t)(32 * t * D));
     }
   };
   load(wave);
-  for (int s = wave; s < stages; s += kFewWaves) {
-    uint4 cw[4], ch[MT][4];
+  for (int s = wave; s < stages; s += W) {
+    uint4 cw[kFewFrags][2], ch[TT][2];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      cw[c] = pw[c];
+    for (int c = 0; c < 2; ++c) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m) ch[m][c] = ph[m][c];
+      for (int f = 0; f < kFewFrags; ++f) cw[f][c] = pw[f][c];
+#pragma unroll
+      for (int t = 0; t < TT; ++t) ch[t][c] = ph[t][c];
     }
-    load(s + kFewWaves);
+    load(s + W);
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+    for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-        acc[m] = MfmaBf16::mma(__builtin_bit_cast(MfmaBf16::Frag, cw[c]), __builtin_bit_cast(MfmaBf16::Frag, ch[m][c]),
-                               acc[m]);
+      for (int f = 0; f < kFewFrags; ++f)
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+          acc[t][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(MfmaBf16::Frag, cw[f][c]),
+                                                              __builtin_bit_cast(MfmaBf16::Frag, ch[t][c]), acc[t][f], 0,
+                                                              0, 0);
   }
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int t = 0; t < TT; ++t)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) red[wave][m][e][lane] = acc[m][e];
+    for (int f = 0; f < kFewFrags; ++f) red[wave][t][f][lane] = acc[t][f];
   __syncthreads();
-  if (wave >= MT) return;
-  const int m = wave, t = 32 * m + (lane & 31);
-  float z[16], top = -INFINITY;
+  if (wave >= TT) return;
+  // lane l: token l % 16 of the wave's group, rows 16 f + 4 (l / 16) + e
+  const int t = 16 * wave + (lane & 15);
+  float top = -INFINITY;
+  f32x4_t z[kFewFrags];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    z[e] = (red[0][m][e][lane] + red[1][m][e][lane]) + (red[2][m][e][lane] + red[3][m][e][lane]);
-    if (row_of(e, lane) < rows) top = fmaxf(top, z[e]);
+  for (int f = 0; f < kFewFrags; ++f) {
+    z[f] = red[0][wave][f][lane];
+#pragma unroll
+    for (int w = 1; w < W; ++w) z[f] += red[w][wave][f][lane];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (16 * f + 4 * q + e < rows) top = fmaxf(top, z[f][e]);
   }
+  top = fmaxf(top, __shfl_xor(top, 16, kWave));
   top = fmaxf(top, __shfl_xor(top, 32, kWave));
   const float ref = top == -INFINITY ? 0.0f : top * kLog2e;
   float s = 0.0f;
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    const float p = __builtin_amdgcn_exp2f(fmaf(z[e], kLog2e, -ref));
-    if (row_of(e, lane) < rows) s += p;
-  }
+  for (int f = 0; f < kFewFrags; ++f)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float p = __builtin_amdgcn_exp2f(fmaf(z[f][e], kLog2e, -ref));
+      if (16 * f + 4 * q + e < rows) s += p;
+    }
+  s += __shfl_xor(s, 16, kWave);
   s += __shfl_xor(s, 32, kWave);
   if (t >= a.T) return;
-  if (half == 0) a.part[(int64_t)blockIdx.x * a.T + t] = make_float2(ref, s);
+  if (q == 0) a.part[(int64_t)blockIdx.x * a.T + t] = make_float2(ref, s);
   const int64_t r = a.targets[t] - v0;
 #pragma unroll
-  for (int e = 0; e < 16; ++e)
-    if (r == row_of(e, lane) && r < rows) a.zt[t] = z[e];
+  for (int f = 0; f < kFewFrags; ++f)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (r == 16 * f + 4 * q + e && r < rows) a.zt[t] = z[f][e];
 }
 
 // ---------------------------------------------------------------------------
@@ -755,7 +788,7 @@ static XentPlan xent_plan(int64_t T, int64_t V, int64_t D, bool bwd) {
 static bool xent_few(int64_t T, int64_t D) { return T <= kFewTokens && D % 8 == 0; }
 
 size_t xent_workspace(int64_t T, int64_t V, int64_t D, bool bwd) {
-  if (!bwd && xent_few(T, D)) return (size_t)(up((V + 31) / 32 * 8 * T, 256) + up(4 * T, 256));
+  if (!bwd && xent_few(T, D)) return (size_t)(up((V + kFewRows - 1) / kFewRows * 8 * T, 256) + up(4 * T, 256));
   return (size_t)xent_plan(T, V, D, bwd).total;
 }
 
@@ -780,10 +813,11 @@ hipError_t launch_xent_fwd(const uint16_t* h, const uint16_t* w, const int64_t* 
   char* base = static_cast<char*>(ws);
   if (xent_few(T, D)) {
     XentFew f{w, V, (int)D, h, (int)T, targets, reinterpret_cast<float2*>(base),
-              reinterpret_cast<float*>(base + up((V + 31) / 32 * 8 * T, 256))};
-    const unsigned grid = (unsigned)((V + 31) / 32);
-    if (T <= 32) xent_few_kernel<1><<<grid, kWave * kFewWaves, 0, stream>>>(f);
-    else xent_few_kernel<2><<<grid, kWave * kFewWaves, 0, stream>>>(f);
+              reinterpret_cast<float*>(base + up((V + kFewRows - 1) / kFewRows * 8 * T, 256))};
+    const unsigned grid = (unsigned)((V + kFewRows - 1) / kFewRows);
+    if (T <= 16) xent_few_kernel<1><<<grid, kWave * kFewWaves, 0, stream>>>(f);
+    else if (T <= 32) xent_few_kernel<2><<<grid, kWave * kFewWaves, 0, stream>>>(f);
+    else xent_few_kernel<4><<<grid, kWave * kFewWaves, 0, stream>>>(f);
     if (hipError_t e = hipGetLastError()) return e;
     const XentLoss l{f.part, (int)grid, (int)T, f.zt, nullptr, targets, ignore, V, lse, loss};
     return launch_loss(l, targets, ignore, total, mean, stream);
