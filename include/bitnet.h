@@ -507,12 +507,19 @@ bitnet_status bitnet_gate_bwd(bitnet_act act, const uint16_t* dY, const uint16_t
                               uint16_t* dgate, int64_t lddg, uint16_t* dup, int64_t lddu, void* stream);
 
 /*
- * ttq_bwd with x kept as its 8-bit checkpoint (codes and scales of
- * bitnet_ckpt_pack on x [M][K]): the values, rounded to bf16, are unpacked
- * into the workspace and take x's place in dW = dY^T x. With dW NULL, codes
- * and scales may be NULL. workspace: ttq_bwd_ckpt_workspace_bytes(M, N, K)
- * bytes; the other arguments, the limits and the errors are ttq_bwd's.
+ * TTQ with x kept as its 8-bit checkpoint: ttq_fwd that also writes the codes
+ * and scales of x [M][K] (bitnet_ckpt_pack's; codes NULL: not written), and
+ * ttq_bwd that reads them: the values, rounded to bf16, take x's place in
+ * dW = dY^T x. With dW NULL, codes and scales may be NULL. Widths that are not
+ * multiples of 8 are copied to padded rows in the workspace (x forward, dY
+ * backward), with the same results. workspace:
+ * ttq_fwd_ckpt_workspace_bytes / ttq_bwd_ckpt_workspace_bytes; the other
+ * arguments and the errors are ttq_fwd's and ttq_bwd's, the limits too, with K
+ * and N rounded up to 64.
  */
+size_t ttq_fwd_ckpt_workspace_bytes(int64_t M, int64_t N, int64_t K);
+bitnet_status ttq_fwd_ckpt(const uint16_t* x, const uint16_t* wt, int64_t M, int64_t N, int64_t K, uint16_t* y,
+                           int8_t* codes, float* scales, void* workspace, size_t workspace_bytes, void* stream);
 size_t ttq_bwd_ckpt_workspace_bytes(int64_t M, int64_t N, int64_t K);
 bitnet_status ttq_bwd_ckpt(const uint16_t* dY, const int8_t* codes, const float* scales, const uint16_t* wt,
                            const uint8_t* w_packed, int64_t M, int64_t N, int64_t K, uint16_t* dX, void* dW,

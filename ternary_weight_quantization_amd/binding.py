@@ -107,6 +107,10 @@ def lib():
     L.bitnet_gate_fwd.restype = st
     L.bitnet_gate_bwd.argtypes = [st, vp, vp, i64, vp, i64, vp, vp, vp, vp, i64, i64, vp, i64, vp, i64, vp]
     L.bitnet_gate_bwd.restype = st
+    L.ttq_fwd_ckpt_workspace_bytes.argtypes = [i64, i64, i64]
+    L.ttq_fwd_ckpt_workspace_bytes.restype = sz
+    L.ttq_fwd_ckpt.argtypes = [vp, vp, i64, i64, i64, vp, vp, vp, vp, sz, vp]
+    L.ttq_fwd_ckpt.restype = st
     L.ttq_bwd_ckpt_workspace_bytes.argtypes = [i64, i64, i64]
     L.ttq_bwd_ckpt_workspace_bytes.restype = sz
     L.ttq_bwd_ckpt.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, vp, vp, st, vp, vp, sz, vp]
@@ -517,6 +521,30 @@ def ttq_bwd(dY, x, wt, w_packed, K, dX=None, dW=None, grads=None, workspace=None
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().ttq_bwd(_ptr(dY), _ptr(x), _ptr(wt), _ptr(w_packed), M, N, int(K), _ptr(dX), _ptr(dW),
                          dw_dtype, _ptr(grads), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def ttq_fwd_ckpt_workspace_bytes(M, N, K):
+    return int(lib().ttq_fwd_ckpt_workspace_bytes(int(M), int(N), int(K)))
+
+
+def ttq_fwd_ckpt(x, wt, y, codes=None, scales=None, workspace=None, stream=None):
+    """ttq_fwd that also writes the 8-bit checkpoint of x: codes int8
+    [M, Kc], scales float32 [M, Kc/128]."""
+    M, K = x.shape
+    N, Kp = wt.shape
+    if Kp != bitnet_k_pad(K):
+        raise ValueError("wt: second dimension must be bitnet_k_pad(K)")
+    _need(x, torch.bfloat16, (M, K), "x")
+    _need(wt, torch.bfloat16, (N, Kp), "wt")
+    _need(y, torch.bfloat16, (M, N), "y")
+    if codes is not None:
+        _need_codes(codes, scales, M, K)
+    _same_device(x, wt=wt, y=y, codes=codes, scales=scales, workspace=workspace)
+    if workspace is None:
+        workspace = _workspace(ttq_fwd_ckpt_workspace_bytes(M, N, K), x, stream)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _run(lib().ttq_fwd_ckpt, x, stream, _ptr(x), _ptr(wt), M, N, K, _ptr(y), _ptr(codes), _ptr(scales),
+         _ptr(workspace), ws_bytes)
 
 
 def ttq_bwd_ckpt_workspace_bytes(M, N, K):

@@ -98,8 +98,8 @@ bitnet_status check_xent_sizes(int64_t T, int64_t V, int64_t D) {
 }
 bool is_reduce(bitnet_reduce r) { return r == BITNET_REDUCE_NONE || r == BITNET_REDUCE_SUM || r == BITNET_REDUCE_MEAN; }
 
-// The bf16 x that ttq_bwd_ckpt unpacks at the start of its workspace.
-size_t ckpt_x_bytes(int64_t M, int64_t K) { return ((size_t)M * K * 2 + 255) / 256 * 256; }
+// bf16 rows [M][ld] in a workspace.
+size_t rows_bytes(int64_t M, int64_t ld) { return ((size_t)M * ld * 2 + 255) / 256 * 256; }
 
 }  // namespace
 
@@ -329,7 +329,7 @@ bitnet_status ttq_bwd(const uint16_t* dY, const uint16_t* x, const uint16_t* wt,
   if (workspace_bytes < ttq_workspace_bytes(M, N, K)) return BITNET_ERR_WORKSPACE;
   if (workspace_bytes > 0 && !workspace) return BITNET_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return BITNET_ERR_ALIGN;
-  return from_hip(bitnet::launch_ttq_bwd(dY, x, wt, w_packed, M, N, K, dX, dW, dW_dtype == BITNET_F32, grads,
+  return from_hip(bitnet::launch_ttq_bwd(dY, N, x, K, wt, w_packed, M, N, K, dX, dW, dW_dtype == BITNET_F32, grads,
                                          workspace, workspace_bytes, static_cast<hipStream_t>(stream)));
 }
 
@@ -396,7 +396,7 @@ bitnet_status bitnet_ckpt_unpack(const int8_t* codes, const float* scales, int64
   if (!is_value(x_dtype)) return BITNET_ERR_DTYPE;
   if (bitnet_status st = check_ckpt_sizes(M, K)) return st;
   if (!aligned(x, elem(x_dtype)) || !aligned(codes, 16) || !aligned(scales, 4)) return BITNET_ERR_ALIGN;
-  return from_hip(bitnet::launch_ckpt_unpack(codes, scales, M, K, x, x_dtype == BITNET_F32,
+  return from_hip(bitnet::launch_ckpt_unpack(codes, scales, M, K, x, K, x_dtype == BITNET_F32,
                                              static_cast<hipStream_t>(stream)));
 }
 
@@ -434,9 +434,40 @@ bitnet_status bitnet_gate_bwd(bitnet_act act, const uint16_t* dY, const uint16_t
                                           static_cast<hipStream_t>(stream)));
 }
 
+size_t ttq_fwd_ckpt_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (check_gemm_sizes(M, N, K) != BITNET_OK) return 0;
+  return (K % 8 == 0 ? 0 : rows_bytes(M, bitnet::k_pad(K))) + ttq_workspace_bytes(M, N, K);
+}
+
+bitnet_status ttq_fwd_ckpt(const uint16_t* x, const uint16_t* wt, int64_t M, int64_t N, int64_t K, uint16_t* y,
+                           int8_t* codes, float* scales, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!x || !wt || !y || (codes && !scales)) return BITNET_ERR_NULL;
+  if (bitnet_status st = check_gemm_sizes(M, N, K)) return st;
+  const int64_t Kp = bitnet::k_pad(K);
+  if (32 * 4 * N > (int64_t(1) << 31) || !buffer_range_ok(M, 2 * Kp) || !buffer_range_ok(N, 2 * Kp))
+    return BITNET_ERR_SHAPE;
+  if (workspace_bytes < ttq_fwd_ckpt_workspace_bytes(M, N, K)) return BITNET_ERR_WORKSPACE;
+  if (workspace_bytes > 0 && !workspace) return BITNET_ERR_WORKSPACE;
+  if (!aligned(workspace, 16) || !aligned(x, 16) || !aligned(wt, 16) || !aligned(y, 16) || !aligned(codes, 16) ||
+      !aligned(scales, 4))
+    return BITNET_ERR_ALIGN;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  if (K % 8 == 0) {
+    if (codes)
+      if (hipError_t e = bitnet::launch_ckpt_pack(x, false, M, K, codes, scales, st)) return from_hip(e);
+    return from_hip(bitnet::launch_ttq_fwd(x, wt, M, N, K, y, ws, workspace_bytes, st));
+  }
+  uint16_t* xp = reinterpret_cast<uint16_t*>(ws);
+  const size_t xb = rows_bytes(M, Kp);
+  if (hipError_t e = bitnet::launch_pad_rows(x, M, K, xp, Kp, codes, scales, st)) return from_hip(e);
+  return from_hip(bitnet::launch_ttq_fwd(xp, wt, M, N, Kp, y, ws + xb, workspace_bytes - xb, st));
+}
+
 size_t ttq_bwd_ckpt_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (check_gemm_sizes(M, N, K) != BITNET_OK) return 0;
-  return ckpt_x_bytes(M, K) + ttq_workspace_bytes(M, N, K);
+  return rows_bytes(M, bitnet::k_pad(K)) + (N % 8 == 0 ? 0 : rows_bytes(M, bitnet::k_pad(N))) +
+         bitnet::gemm_workspace_bytes(bitnet::GemmKind::kTtqBwdPadded, M, N, K);
 }
 
 bitnet_status ttq_bwd_ckpt(const uint16_t* dY, const int8_t* codes, const float* scales, const uint16_t* wt,
@@ -447,16 +478,26 @@ bitnet_status ttq_bwd_ckpt(const uint16_t* dY, const int8_t* codes, const float*
   if (bitnet_status st = check_gemm_sizes(M, N, K)) return st;
   if (!workspace || workspace_bytes < ttq_bwd_ckpt_workspace_bytes(M, N, K)) return BITNET_ERR_WORKSPACE;
   if (!aligned(workspace, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return BITNET_ERR_ALIGN;
-  if (dW && M * bitnet::ckpt_pad(K) > (int64_t(1) << 40)) return BITNET_ERR_SHAPE;
-  uint16_t* x = static_cast<uint16_t*>(workspace);
-  const size_t xb = ckpt_x_bytes(M, K);
-  // every argument is checked before the unpacking is enqueued
+  const int64_t Kp = bitnet::k_pad(K), Np = bitnet::k_pad(N);
+  if (!buffer_range_ok(M, 2 * Kp) || !buffer_range_ok(M, 2 * Np)) return BITNET_ERR_SHAPE;
+  char* ws = static_cast<char*>(workspace);
+  uint16_t* x = reinterpret_cast<uint16_t*>(ws);
+  // every argument is checked before anything is enqueued
   if (bitnet_status st = check_ttq_bwd(dY, x, wt, w_packed, M, N, K, dX, dW, dW_dtype, grads)) return st;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  size_t used = rows_bytes(M, Kp);
   if (dW)
-    if (hipError_t e = bitnet::launch_ckpt_unpack(codes, scales, M, K, x, false, static_cast<hipStream_t>(stream)))
-      return from_hip(e);
-  return ttq_bwd(dY, x, wt, w_packed, M, N, K, dX, dW, dW_dtype, grads, static_cast<char*>(workspace) + xb,
-                 workspace_bytes - xb, stream);
+    if (hipError_t e = bitnet::launch_ckpt_unpack(codes, scales, M, K, x, Kp, false, st)) return from_hip(e);
+  int64_t ldy = N;
+  if (N % 8 != 0) {
+    uint16_t* yp = reinterpret_cast<uint16_t*>(ws + used);
+    used += rows_bytes(M, Np);
+    if (hipError_t e = bitnet::launch_pad_rows(dY, M, N, yp, Np, nullptr, nullptr, st)) return from_hip(e);
+    dY = yp;
+    ldy = Np;
+  }
+  return from_hip(bitnet::launch_ttq_bwd(dY, ldy, x, Kp, wt, w_packed, M, N, K, dX, dW, dW_dtype == BITNET_F32, grads,
+                                         ws + used, workspace_bytes - used, st));
 }
 
 // ---------------------------------------------------------------------------

@@ -49,16 +49,35 @@ __global__ __launch_bounds__(kRowThreads) void ckpt_pack_kernel(const T* __restr
   if ((threadIdx.x & 15) == 0) scales[i >> 4] = s;
 }
 
+// Rows of ld values: the codes past K stand for zeros.
 template <class T>
 __global__ __launch_bounds__(kRowThreads) void ckpt_unpack_kernel(const int8_t* __restrict__ codes,
                                                                   const float* __restrict__ scales, int64_t total,
-                                                                  int K, int nch, T* __restrict__ x) {
+                                                                  int ld, int nch, T* __restrict__ x) {
   const int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
   if (i >= total) return;
   const ChunkAt at = chunk_at(i, nch);
   float f[8];
   values8(reinterpret_cast<const uint2*>(codes)[i], scales[i >> 4] / 127.0f, f);
-  store8(x + at.row * K, 8 * at.ch, K, f);
+  store8(x + at.row * ld, 8 * at.ch, ld, f);
+}
+
+// Rows of K bf16 values copied to rows of ld (zeros past K), and with codes
+// their checkpoint from the same registers.
+__global__ __launch_bounds__(kRowThreads) void pad_rows_kernel(const uint16_t* __restrict__ x, int64_t total, int K,
+                                                               int nch, uint16_t* __restrict__ padded, int ld,
+                                                               int8_t* __restrict__ codes, float* __restrict__ scales) {
+  const int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
+  if (i >= total) return;
+  const ChunkAt at = chunk_at(i, nch);
+  const ChunkBf16 c = chunk8(x + at.row * K, 8 * at.ch, K);
+  if (8 * at.ch < ld) *reinterpret_cast<uint4*>(padded + at.row * ld + 8 * at.ch) = c.v;
+  if (codes == nullptr) return;
+  float f[8];
+  c.get(f);
+  const float s = block_scale(c);
+  reinterpret_cast<uint2*>(codes)[i] = codes8(f, s);
+  if ((threadIdx.x & 15) == 0) scales[i >> 4] = s;
 }
 
 static unsigned row_grid(int64_t total) { return (unsigned)((total + kRowThreads - 1) / kRowThreads); }
@@ -76,15 +95,23 @@ hipError_t launch_ckpt_pack(const void* x, bool x_f32, int64_t M, int64_t K, int
   return hipGetLastError();
 }
 
-hipError_t launch_ckpt_unpack(const int8_t* codes, const float* scales, int64_t M, int64_t K, void* x, bool x_f32,
-                              hipStream_t stream) {
+hipError_t launch_pad_rows(const uint16_t* x, int64_t M, int64_t K, uint16_t* padded, int64_t ld, int8_t* codes,
+                           float* scales, hipStream_t stream) {
+  const int nch = (int)(ckpt_pad(K) / 8);
+  const int64_t total = M * nch;
+  pad_rows_kernel<<<row_grid(total), kRowThreads, 0, stream>>>(x, total, (int)K, nch, padded, (int)ld, codes, scales);
+  return hipGetLastError();
+}
+
+hipError_t launch_ckpt_unpack(const int8_t* codes, const float* scales, int64_t M, int64_t K, void* x, int64_t ld,
+                              bool x_f32, hipStream_t stream) {
   const int nch = (int)(ckpt_pad(K) / 8);
   const int64_t total = M * nch;
   if (x_f32)
-    ckpt_unpack_kernel<<<row_grid(total), kRowThreads, 0, stream>>>(codes, scales, total, (int)K, nch,
+    ckpt_unpack_kernel<<<row_grid(total), kRowThreads, 0, stream>>>(codes, scales, total, (int)ld, nch,
                                                                     static_cast<float*>(x));
   else
-    ckpt_unpack_kernel<<<row_grid(total), kRowThreads, 0, stream>>>(codes, scales, total, (int)K, nch,
+    ckpt_unpack_kernel<<<row_grid(total), kRowThreads, 0, stream>>>(codes, scales, total, (int)ld, nch,
                                                                     static_cast<uint16_t*>(x));
   return hipGetLastError();
 }

@@ -1003,7 +1003,7 @@ static GemmShape shape_of(GemmKind kind, int64_t M, int64_t N, int64_t K) {
     case GemmKind::kTtqFwd: return {(N + kBI - 1) / kBI, (M + kBJ - 1) / kBJ, (Kp + kRed16 - 1) / kRed16, 20};
     case GemmKind::kBwdDx:
       return {(K + kBI - 1) / kBI, (M + kBJ - 1) / kBJ, (N + kRed16 - 1) / kRed16, kBwdPieceCost};
-    case GemmKind::kBwdDw: case GemmKind::kBwdPair: case GemmKind::kTtqBwd: break;
+    case GemmKind::kBwdDw: case GemmKind::kBwdPair: case GemmKind::kTtqBwd: case GemmKind::kTtqBwdPadded: break;
   }
   return {(K + kBI - 1) / kBI, (N + kBJ - 1) / kBJ, (M + kRed16 - 1) / kRed16, kBwdPieceCost};
 }
@@ -1399,9 +1399,9 @@ static bool pair_gate(int64_t M, int64_t N, int64_t K) {
 static bool pair_eligible(int64_t M, int64_t N, int64_t K) {
   return N % 8 == 0 && !skinny(M) && pair_gate(M, N, K);
 }
-// TTQ's pair: both operands copied as stored (N, K multiples of 8).
-static bool ttq_pair_eligible(int64_t M, int64_t N, int64_t K) {
-  return N % 8 == 0 && K % 8 == 0 && pair_gate(M, N, K);
+// TTQ's pair: both operands copied as stored (row pitches multiples of 8).
+static bool ttq_pair_eligible(int64_t M, int64_t N, int64_t K, int64_t ldy, int64_t ldx) {
+  return ldy % 8 == 0 && ldx % 8 == 0 && pair_gate(M, N, K);
 }
 static size_t pair_split_bytes(int64_t M, int64_t N, int64_t K) {
   const PairPlan pp = plan_pair(shape_of(GemmKind::kBwdDx, M, N, K), shape_of(GemmKind::kBwdDw, M, N, K),
@@ -1437,10 +1437,13 @@ size_t gemm_workspace_bytes(GemmKind kind, int64_t M, int64_t N, int64_t K) {
                       gemm_workspace_bytes(GemmKind::kBwdDw, M, N, K));
     }
     case GemmKind::kTtqBwd: {
-      if (ttq_pair_eligible(M, N, K) && pair_split_bytes(M, N, K) > 0)
+      if (ttq_pair_eligible(M, N, K, N, K) && pair_split_bytes(M, N, K) > 0)
         return ttq_partials_bytes(N, K) + pair_split_bytes(M, N, K);
       return ttq_partials_bytes(N, K) + std::max(alone(GemmKind::kBwdDx), alone(GemmKind::kBwdDw));
     }
+    case GemmKind::kTtqBwdPadded:
+      return ttq_partials_bytes(N, K) + std::max(pair_gate(M, N, K) ? pair_split_bytes(M, N, K) : 0,
+                                                 std::max(alone(GemmKind::kBwdDx), alone(GemmKind::kBwdDw)));
   }
   return 0;
 }
@@ -1537,49 +1540,53 @@ hipError_t launch_ttq_fwd_codes(const uint16_t* x, const uint8_t* w_packed, cons
 }
 
 // dX [M][K] = dY [M][N] . wt: wt staged as stored (rows n) and read
-// transposed (TrFrags), dY copied as stored.
-static hipError_t launch_ttq_dx(const uint16_t* dY, const uint16_t* wt, int64_t M, int64_t N, int64_t K,
+// transposed (TrFrags), dY copied as stored. dY's rows are ldy apart; where
+// ldy > N the columns past N hold zeros.
+static hipError_t launch_ttq_dx(const uint16_t* dY, int64_t ldy, const uint16_t* wt, int64_t M, int64_t N, int64_t K,
                                 uint16_t* dX, void* ws, size_t ws_bytes, hipStream_t stream) {
   const int64_t Kp = k_pad(K);
   const RowCopyBf16Loader<5> pl{wt, Kp, N, K};
   const Bf16Epilogue<false> ep{dX, nullptr, K, M};
   const GemmShape g = shape_of(GemmKind::kBwdDx, M, N, K);
   const char* db = reinterpret_cast<const char*>(dY);
-  if (N % 8 == 0) return run_gemm<MfmaBf16, 0>(pl, CopyLoader<2, true, 1>{db, 2 * N, M, 2 * N}, ep, g, ws, ws_bytes, stream);
+  if (ldy % 8 == 0)
+    return run_gemm<MfmaBf16, 0>(pl, CopyLoader<2, true, 1>{db, 2 * ldy, M, 2 * ldy}, ep, g, ws, ws_bytes, stream);
   return run_gemm<MfmaBf16, 0>(pl, CopyLoader<2, false, 1>{db, 2 * N, M, 2 * N}, ep, g, ws, ws_bytes, stream);
 }
 
-// dW [N][K] = dY^T x with the masked sums (TtqDwEpilogue).
+// dW [N][K] = dY^T x with the masked sums (TtqDwEpilogue); rows of dY and x
+// ldy and ldx apart (zeros past N and K).
 template <bool OUT_F32>
-static hipError_t launch_ttq_dw(const uint16_t* dY, const uint16_t* x, const uint8_t* w_packed, int64_t M, int64_t N,
-                                int64_t K, void* dW, float2* partials, void* ws, size_t ws_bytes, hipStream_t stream) {
+static hipError_t launch_ttq_dw(const uint16_t* dY, int64_t ldy, const uint16_t* x, int64_t ldx,
+                                const uint8_t* w_packed, int64_t M, int64_t N, int64_t K, void* dW, float2* partials,
+                                void* ws, size_t ws_bytes, hipStream_t stream) {
   const GemmShape g = shape_of(GemmKind::kBwdDw, M, N, K);
   const TtqDwEpilogue<OUT_F32> ep{Bf16Epilogue<OUT_F32>{dW, nullptr, K, N}, w_packed, (uint32_t)(k_pad(K) / 4),
                                   partials, (int)(2 * g.tiles_i)};
-  if (K % 8 == 0 && N % 8 == 0)
-    return run_gemm<MfmaBf16, 0>(RowCopyBf16Loader<1>{x, K, M, K}, RowCopyBf16Loader<5>{dY, N, M, N}, ep, g, ws,
+  if (ldx % 8 == 0 && ldy % 8 == 0)
+    return run_gemm<MfmaBf16, 0>(RowCopyBf16Loader<1>{x, ldx, M, K}, RowCopyBf16Loader<5>{dY, ldy, M, N}, ep, g, ws,
                                  ws_bytes, stream);
-  if (K % 4 == 0 && N % 4 == 0)
+  if (ldx == K && ldy == N && K % 4 == 0 && N % 4 == 0)
     return run_gemm<MfmaBf16, 0>(RowTransposeBf16Loader<true, 3>{x, K, M, K},
                                  RowTransposeBf16Loader<true, 5>{dY, N, M, N}, ep, g, ws, ws_bytes, stream);
-  return run_gemm<MfmaBf16, 0>(RowTransposeBf16Loader<false, 3>{x, K, M, K},
-                               RowTransposeBf16Loader<false, 5>{dY, N, M, N}, ep, g, ws, ws_bytes, stream);
+  return run_gemm<MfmaBf16, 0>(RowTransposeBf16Loader<false, 3>{x, ldx, M, K},
+                               RowTransposeBf16Loader<false, 5>{dY, ldy, M, N}, ep, g, ws, ws_bytes, stream);
 }
 
 // dX and dW in one gemm_pair_kernel launch (as the BitNet backward):
 // hipErrorNotSupported when the shape or the device does not allow it.
 template <bool OUT_F32>
-static hipError_t launch_ttq_pair(const uint16_t* dY, const uint16_t* x, const uint16_t* wt, const uint8_t* w_packed,
-                                  int64_t M, int64_t N, int64_t K, uint16_t* dX, void* dW, float2* partials,
-                                  char* ws, size_t ws_bytes, hipStream_t stream) {
-  if (!ttq_pair_eligible(M, N, K)) return hipErrorNotSupported;
+static hipError_t launch_ttq_pair(const uint16_t* dY, int64_t ldy, const uint16_t* x, int64_t ldx, const uint16_t* wt,
+                                  const uint8_t* w_packed, int64_t M, int64_t N, int64_t K, uint16_t* dX, void* dW,
+                                  float2* partials, char* ws, size_t ws_bytes, hipStream_t stream) {
+  if (!ttq_pair_eligible(M, N, K, ldy, ldx)) return hipErrorNotSupported;
   const int64_t Kp = k_pad(K);
   const GemmShape g1 = shape_of(GemmKind::kBwdDx, M, N, K), g2 = shape_of(GemmKind::kBwdDw, M, N, K);
   const RowCopyBf16Loader<5> p1{wt, Kp, N, K};
-  const CopyLoader<2, true, 1> q1{reinterpret_cast<const char*>(dY), 2 * N, M, 2 * N};
+  const CopyLoader<2, true, 1> q1{reinterpret_cast<const char*>(dY), 2 * ldy, M, 2 * ldy};
   const Bf16Epilogue<false> e1{dX, nullptr, K, M};
-  const RowCopyBf16Loader<1> p2{x, K, M, K};
-  const RowCopyBf16Loader<5> q2{dY, N, M, N};
+  const RowCopyBf16Loader<1> p2{x, ldx, M, K};
+  const RowCopyBf16Loader<5> q2{dY, ldy, M, N};
   const TtqDwEpilogue<OUT_F32> e2{Bf16Epilogue<OUT_F32>{dW, nullptr, K, N}, w_packed, (uint32_t)(Kp / 4), partials,
                                   (int)(2 * g2.tiles_i)};
   // stage costs as for the BitNet pair: measured alone at 4096x2560->6912,
@@ -1589,9 +1596,9 @@ static hipError_t launch_ttq_pair(const uint16_t* dY, const uint16_t* x, const u
   return run_pair<0, 0>(p1, q1, e1, g1, kDxCosts, p2, q2, e2, g2, kDwCosts, ws, ws_bytes, stream);
 }
 
-hipError_t launch_ttq_bwd(const uint16_t* dY, const uint16_t* x, const uint16_t* wt, const uint8_t* w_packed,
-                          int64_t M, int64_t N, int64_t K, uint16_t* dX, void* dW, bool dw_f32, float* grads,
-                          void* ws, size_t ws_bytes, hipStream_t stream) {
+hipError_t launch_ttq_bwd(const uint16_t* dY, int64_t ldy, const uint16_t* x, int64_t ldx, const uint16_t* wt,
+                          const uint8_t* w_packed, int64_t M, int64_t N, int64_t K, uint16_t* dX, void* dW, bool dw_f32,
+                          float* grads, void* ws, size_t ws_bytes, hipStream_t stream) {
   const size_t pb = ttq_partials_bytes(N, K);
   if (ws == nullptr || ws_bytes < pb) return hipErrorInvalidValue;  // the C ABI sized it
   float2* partials = static_cast<float2*>(ws);
@@ -1600,8 +1607,8 @@ hipError_t launch_ttq_bwd(const uint16_t* dY, const uint16_t* x, const uint16_t*
   float2* p = grads != nullptr ? partials : nullptr;
   if (dX != nullptr && dW != nullptr) {
     const hipError_t e =
-        dw_f32 ? launch_ttq_pair<true>(dY, x, wt, w_packed, M, N, K, dX, dW, p, split_ws, split_bytes, stream)
-               : launch_ttq_pair<false>(dY, x, wt, w_packed, M, N, K, dX, dW, p, split_ws, split_bytes, stream);
+        dw_f32 ? launch_ttq_pair<true>(dY, ldy, x, ldx, wt, w_packed, M, N, K, dX, dW, p, split_ws, split_bytes, stream)
+               : launch_ttq_pair<false>(dY, ldy, x, ldx, wt, w_packed, M, N, K, dX, dW, p, split_ws, split_bytes, stream);
     if (e != hipErrorNotSupported) {
       if (e != hipSuccess || grads == nullptr) return e;
       ttq_grads_kernel<<<1, 256, 0, stream>>>(partials, (int)ttq_wave_tiles(N, K), grads);
@@ -1609,10 +1616,11 @@ hipError_t launch_ttq_bwd(const uint16_t* dY, const uint16_t* x, const uint16_t*
     }
   }
   if (dX != nullptr)
-    if (hipError_t e = launch_ttq_dx(dY, wt, M, N, K, dX, split_ws, split_bytes, stream)) return e;
+    if (hipError_t e = launch_ttq_dx(dY, ldy, wt, M, N, K, dX, split_ws, split_bytes, stream)) return e;
   if (dW != nullptr) {
-    const hipError_t e = dw_f32 ? launch_ttq_dw<true>(dY, x, w_packed, M, N, K, dW, p, split_ws, split_bytes, stream)
-                                : launch_ttq_dw<false>(dY, x, w_packed, M, N, K, dW, p, split_ws, split_bytes, stream);
+    const hipError_t e =
+        dw_f32 ? launch_ttq_dw<true>(dY, ldy, x, ldx, w_packed, M, N, K, dW, p, split_ws, split_bytes, stream)
+               : launch_ttq_dw<false>(dY, ldy, x, ldx, w_packed, M, N, K, dW, p, split_ws, split_bytes, stream);
     if (e != hipSuccess) return e;
     if (grads != nullptr) {
       ttq_grads_kernel<<<1, 256, 0, stream>>>(partials, (int)ttq_wave_tiles(N, K), grads);

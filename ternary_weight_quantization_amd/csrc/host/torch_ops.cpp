@@ -318,16 +318,14 @@ struct TtqFn : torch::autograd::Function<TtqFn> {
     shape.back() = N;
     Tensor y = at::empty(shape, x.options());
     const Tensor codes_w = at::empty({N, Kp / 4}, x.options().dtype(at::kByte)), wt = at::empty({N, Kp}, x.options());
-    const size_t bytes = ttq_workspace_bytes(M, N, K);
+    const size_t bytes = ttq_fwd_ckpt_workspace_bytes(M, N, K);
     const Tensor ws = scratch(bytes, x);
-    {
-      On on(x2);
-      check(ttq_quantize(ptr(w), code(w.scalar_type()), N, K, f32(p), static_cast<uint8_t*>(ptr(codes_w)), bf16(wt),
-                         on.stream));
-      check(ttq_fwd(bf16(x2), bf16(wt), M, N, K, bf16(y), ptr(ws), bytes, on.stream));
-    }
     Tensor codes, scales;
-    if (weight.requires_grad() || params.requires_grad()) std::tie(codes, scales) = compress(x2);  // dW alone reads x
+    if (weight.requires_grad() || params.requires_grad()) std::tie(codes, scales) = empty_codes(M, K, x2);  // dW alone reads x
+    On on(x2);
+    check(ttq_quantize(ptr(w), code(w.scalar_type()), N, K, f32(p), static_cast<uint8_t*>(ptr(codes_w)), bf16(wt),
+                       on.stream));
+    check(ttq_fwd_ckpt(bf16(x2), bf16(wt), M, N, K, bf16(y), i8(codes), f32(scales), ptr(ws), bytes, on.stream));
     ctx->save_for_backward({codes, scales, wt, codes_w});
     ctx->saved_data["x"] = x.sizes();
     ctx->saved_data["wt"] = static_cast<int64_t>(weight.scalar_type());

@@ -109,7 +109,7 @@ hipError_t launch_act_quant(const uint16_t* x, int64_t M, int64_t K,
 // backward). Each may split output tiles over workgroups (stream-K)
 // when its tile count leaves the CUs partly idle; that needs the workspace
 // gemm_workspace_bytes() gives (fewer bytes: whole tiles, no split).
-enum class GemmKind { kFwd, kBwdDx, kBwdDw, kBwdPair, kTtqFwd, kTtqBwd };
+enum class GemmKind { kFwd, kBwdDx, kBwdDw, kBwdPair, kTtqFwd, kTtqBwd, kTtqBwdPadded };
 size_t gemm_workspace_bytes(GemmKind kind, int64_t M, int64_t N, int64_t K);
 
 // INT8 forward GEMM with fused rescale, an optional bf16 bias [N] (NULL:
@@ -176,17 +176,24 @@ hipError_t launch_ttq_fwd_codes(const uint16_t* x, const uint8_t* w_packed, cons
 hipError_t launch_ttq_fwd(const uint16_t* x, const uint16_t* wt, int64_t M, int64_t N, int64_t K, uint16_t* y,
                           void* ws, size_t ws_bytes, hipStream_t stream);
 // dX = dY wt, dW = dY^T x (bf16 or f32), grads = {dL/dWp, dL/dWn} (NULL: not
-// computed; needs dW). Workspace: gemm_workspace_bytes(kTtqBwd).
-hipError_t launch_ttq_bwd(const uint16_t* dY, const uint16_t* x, const uint16_t* wt, const uint8_t* w_packed,
-                          int64_t M, int64_t N, int64_t K, uint16_t* dX, void* dW, bool dw_f32, float* grads,
-                          void* ws, size_t ws_bytes, hipStream_t stream);
+// computed; needs dW). Rows of dY and x are ldy and ldx values apart, zeros
+// past N and K. Workspace: gemm_workspace_bytes(kTtqBwd) for dense rows
+// (ldy = N, ldx = K), kTtqBwdPadded for padded ones.
+hipError_t launch_ttq_bwd(const uint16_t* dY, int64_t ldy, const uint16_t* x, int64_t ldx, const uint16_t* wt,
+                          const uint8_t* w_packed, int64_t M, int64_t N, int64_t K, uint16_t* dX, void* dW, bool dw_f32,
+                          float* grads, void* ws, size_t ws_bytes, hipStream_t stream);
 
 // 8-bit activation checkpoints: columns of the codes, pack, unpack.
 inline int64_t ckpt_pad(int64_t K) { return (K + 127) / 128 * 128; }
 hipError_t launch_ckpt_pack(const void* x, bool x_f32, int64_t M, int64_t K, int8_t* codes, float* scales,
                             hipStream_t stream);
-hipError_t launch_ckpt_unpack(const int8_t* codes, const float* scales, int64_t M, int64_t K, void* x, bool x_f32,
-                              hipStream_t stream);
+// bf16 rows also (codes not NULL) or only copied to rows of `ld` values (at
+// least K, at most ckpt_pad(K), a multiple of 8) with zeros past K.
+hipError_t launch_pad_rows(const uint16_t* x, int64_t M, int64_t K, uint16_t* padded, int64_t ld, int8_t* codes,
+                           float* scales, hipStream_t stream);
+// x rows of `ld` values (ld >= K; zeros past K).
+hipError_t launch_ckpt_unpack(const int8_t* codes, const float* scales, int64_t M, int64_t K, void* x, int64_t ld,
+                              bool x_f32, hipStream_t stream);
 
 // The gated activation (up NULL: none; gq NULL: no codes).
 hipError_t launch_gate_fwd(bool relu2, const uint16_t* gate, int64_t ldg, const uint16_t* up, int64_t ldu, int64_t M,

@@ -97,6 +97,16 @@ def test_ttq_ckpt_refusals(L):
     M, N, K = 128, 256, 320
     need = L.ttq_bwd_ckpt_workspace_bytes(M, N, K)
     assert need >= L.ttq_workspace_bytes(M, N, K) + 2 * M * K
+    assert L.ttq_fwd_ckpt_workspace_bytes(M, N, K) == L.ttq_workspace_bytes(M, N, K)
+    odd = L.ttq_fwd_ckpt_workspace_bytes(M, N, K + 1)
+    assert odd >= 2 * M * (K + 64) and L.ttq_fwd_ckpt_workspace_bytes(M, 0, K) == 0
+
+    def fwd(x=P, wt=P, M=M, N=N, K=K + 1, y=P, c=P, s=P, ws=P, n=odd):
+        return L.ttq_fwd_ckpt(x, wt, M, N, K, y, c, s, ws, n, None)
+
+    assert fwd(x=None) == ENULL and fwd(wt=None) == ENULL and fwd(y=None) == ENULL and fwd(s=None) == ENULL
+    assert fwd(M=0) == ESHAPE and fwd(ws=None) == EWS and fwd(n=odd - 1) == EWS
+    assert fwd(x=P + 8) == EALIGN and fwd(c=P + 8) == EALIGN and fwd(s=P + 2) == EALIGN
 
     def f(dY=P, c=P, s=P, wt=P, wp=P, M=M, N=N, K=K, dX=P, dW=P, d=BF, g=P, ws=P, n=need):
         return L.ttq_bwd_ckpt(dY, c, s, wt, wp, M, N, K, dX, dW, d, g, ws, n, None)
