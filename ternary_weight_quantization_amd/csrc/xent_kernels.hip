@@ -422,11 +422,11 @@ __global__ __launch_bounds__(1024) void xent_reduce_kernel(const float* __restri
 }
 
 // ---------------------------------------------------------------------------
-// Few tokens: one pass over W. A workgroup takes kFewRows rows of W, its waves
+// Few tokens: one pass over W. A workgroup takes 64 or 128 rows of W, its waves
 // every 4th stage of 64 columns; both operands go from memory straight to
 // the fragments of v_mfma_f32_16x16x32_bf16, the waves' sums meet in LDS, and
 // each group of 16 tokens reduces its column of the tile to one pair per
-// token and kFewRows rows.
+// token (forward) or writes its columns of G (backward).
 //
 // A fragment's lane l holds 8 values of row l % 16 at reduction chunk l / 16,
 // so a load covers 64 contiguous bytes of 16 rows and the stage's second load
@@ -440,60 +440,68 @@ __global__ __launch_bounds__(1024) void xent_reduce_kernel(const float* __restri
 // ---------------------------------------------------------------------------
 
 constexpr int kFewTokens = 64;
-constexpr int kFewRows = 64;
 constexpr int kFewWaves = 4;
-constexpr int kFewFrags = kFewRows / 16;
 
 struct XentFew {
-  const uint16_t* w;  // [V][D], D a multiple of 8
+  const uint16_t* w;  // [V][D] (backward: a piece's rows), D a multiple of 8
   int64_t V;
   int D;
-  const uint16_t* h;  // [T][D]
+  const uint16_t* h;  // [T][D] (backward: the rows that count)
   int T;
+  // forward
   const int64_t* targets;
-  float2* part;  // [ceil(V / kFewRows)][T]
+  float2* part;  // [tiles][T]
   float* zt;     // [T]
+  // backward: G for the piece that starts at column v0
+  const XentCtl* ctl;
+  const int* ct;
+  const float* lse2;
+  const float* c;
+  int v0;
+  uint16_t* G;
+  int ldg;
 };
 
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
-// TT groups of 16 tokens.
-template <int TT>
+// TT groups of 16 tokens, FR fragments of 16 rows a tile.
+template <bool BWD, int TT, int FR>
 __global__ __launch_bounds__(kWave * kFewWaves) void xent_few_kernel(XentFew a) {
-  constexpr int W = kFewWaves;
-  __shared__ f32x4_t red[W][TT][kFewFrags][kWave];
+  constexpr int W = kFewWaves, ROWS = 16 * FR;
+  __shared__ f32x4_t red[W][TT][FR][kWave];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int64_t v0 = (int64_t)blockIdx.x * kFewRows;
+  const int64_t v0 = (int64_t)blockIdx.x * ROWS;
   const int D = a.D, q = lane >> 4;
-  const int rows = (int)(a.V - v0 < kFewRows ? a.V - v0 : kFewRows);
+  const int rows = (int)(a.V - v0 < ROWS ? a.V - v0 : ROWS);
   const rsrc_t rw = make_rsrc(a.w + v0 * D, (uint32_t)(rows * D * 2));
-  const rsrc_t rh = make_rsrc(a.h, (uint32_t)(a.T * D * 2));
+  const int n = BWD ? a.ctl->n : a.T;
+  const rsrc_t rh = make_rsrc(a.h, (uint32_t)(n * D * 2));
   const uint32_t row = (uint32_t)((lane & 15) * D * 2);  // rows past the end read as zeros
-  f32x4_t acc[TT][kFewFrags];
+  f32x4_t acc[TT][FR];
 #pragma unroll
   for (int t = 0; t < TT; ++t)
 #pragma unroll
-    for (int f = 0; f < kFewFrags; ++f) acc[t][f] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int f = 0; f < FR; ++f) acc[t][f] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   const int stages = (D + 63) / 64;
-  uint4 pw[kFewFrags][2], ph[TT][2];
+  uint4 pw[FR][2], ph[TT][2];
   const auto load = [&](int s) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int k = 64 * s + 32 * c + 8 * q;
       const uint32_t off = k < D ? row + 2 * k : kOob;  // columns past D: an out-of-range offset
 #pragma unroll
-      for (int f = 0; f < kFewFrags; ++f) pw[f][c] = buf_load16(rw, off + (uint32_t)(32 * f * D));
+      for (int f = 0; f < FR; ++f) pw[f][c] = buf_load16(rw, off + (uint32_t)(32 * f * D));
 #pragma unroll
       for (int t = 0; t < TT; ++t) ph[t][c] = buf_load16(rh, off + (uint32_t)(32 * t * D));
     }
   };
   load(wave);
   for (int s = wave; s < stages; s += W) {
-    uint4 cw[kFewFrags][2], ch[TT][2];
+    uint4 cw[FR][2], ch[TT][2];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
 #pragma unroll
-      for (int f = 0; f < kFewFrags; ++f) cw[f][c] = pw[f][c];
+      for (int f = 0; f < FR; ++f) cw[f][c] = pw[f][c];
 #pragma unroll
       for (int t = 0; t < TT; ++t) ch[t][c] = ph[t][c];
     }
@@ -501,7 +509,7 @@ __global__ __launch_bounds__(kWave * kFewWaves) void xent_few_kernel(XentFew a) 
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int f = 0; f < kFewFrags; ++f)
+      for (int f = 0; f < FR; ++f)
 #pragma unroll
         for (int t = 0; t < TT; ++t)
           acc[t][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(MfmaBf16::Frag, cw[f][c]),
@@ -511,28 +519,49 @@ __global__ __launch_bounds__(kWave * kFewWaves) void xent_few_kernel(XentFew a) 
 #pragma unroll
   for (int t = 0; t < TT; ++t)
 #pragma unroll
-    for (int f = 0; f < kFewFrags; ++f) red[wave][t][f][lane] = acc[t][f];
+    for (int f = 0; f < FR; ++f) red[wave][t][f][lane] = acc[t][f];
   __syncthreads();
   if (wave >= TT) return;
   // lane l: token l % 16 of the wave's group, rows 16 f + 4 (l / 16) + e
   const int t = 16 * wave + (lane & 15);
-  float top = -INFINITY;
-  f32x4_t z[kFewFrags];
+  f32x4_t z[FR];
 #pragma unroll
-  for (int f = 0; f < kFewFrags; ++f) {
+  for (int f = 0; f < FR; ++f) {
     z[f] = red[0][wave][f][lane];
 #pragma unroll
     for (int w = 1; w < W; ++w) z[f] += red[w][wave][f][lane];
+  }
+  if constexpr (BWD) {  // G, zeros in the rows past the piece that G's pitch holds
+    if (t >= n) return;
+    const float c = a.c[t], l = a.lse2[t];
+    const int r = a.ct[t] - a.v0 - (int)v0;
+#pragma unroll
+    for (int f = 0; f < FR; ++f) {
+      float g[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = 16 * f + 4 * q + e;
+        const float p = __builtin_amdgcn_exp2f(fmaf(z[f][e], kLog2e, -l));
+        g[e] = i < rows ? (i == r ? p - 1.0f : p) * c : 0.0f;
+      }
+      if (v0 + 16 * f + 4 * q < a.ldg)
+        *reinterpret_cast<uint2*>(a.G + (int64_t)t * a.ldg + v0 + 16 * f + 4 * q) =
+            make_uint2(pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]));
+    }
+    return;
+  }
+  float top = -INFINITY;
+#pragma unroll
+  for (int f = 0; f < FR; ++f)
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       if (16 * f + 4 * q + e < rows) top = fmaxf(top, z[f][e]);
-  }
   top = fmaxf(top, __shfl_xor(top, 16, kWave));
   top = fmaxf(top, __shfl_xor(top, 32, kWave));
   const float ref = top == -INFINITY ? 0.0f : top * kLog2e;
   float s = 0.0f;
 #pragma unroll
-  for (int f = 0; f < kFewFrags; ++f)
+  for (int f = 0; f < FR; ++f)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float p = __builtin_amdgcn_exp2f(fmaf(z[f][e], kLog2e, -ref));
@@ -544,10 +573,33 @@ __global__ __launch_bounds__(kWave * kFewWaves) void xent_few_kernel(XentFew a) 
   if (q == 0) a.part[(int64_t)blockIdx.x * a.T + t] = make_float2(ref, s);
   const int64_t r = a.targets[t] - v0;
 #pragma unroll
-  for (int f = 0; f < kFewFrags; ++f)
+  for (int f = 0; f < FR; ++f)
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       if (r == 16 * f + 4 * q + e && r < rows) a.zt[t] = z[f][e];
+}
+
+// Rows of W a workgroup takes: with more than 16 tokens h's fragments are as
+// many bytes as W's, and 128 rows share them where that leaves enough
+// workgroups. Measured at D = 2560, 128 against 64 rows: 32 tokens 41.5 / 46.0
+// us against 32000 columns and 147 / 168 against 128256, but 29.7 / 20.5
+// against 8000; 64 tokens 52.9 / 59.8, 188 / 218 and 35.4 / 25.6.
+static int few_rows(int64_t T, int64_t V) { return T > 16 && V >= 192 * 128 ? 128 : 64; }
+static int64_t few_tiles(int64_t T, int64_t V) { return (V + few_rows(T, V) - 1) / few_rows(T, V); }
+
+template <bool BWD, int TT>
+static void few_at(const XentFew& f, hipStream_t st) {
+  const unsigned grid = (unsigned)few_tiles(f.T, f.V);
+  if (few_rows(f.T, f.V) == 128) xent_few_kernel<BWD, TT, TT == 1 ? 4 : 8><<<grid, kWave * kFewWaves, 0, st>>>(f);
+  else xent_few_kernel<BWD, TT, 4><<<grid, kWave * kFewWaves, 0, st>>>(f);
+}
+template <bool BWD>
+static hipError_t launch_few(const XentFew& f, hipStream_t st) {
+  if (f.T <= 16) few_at<BWD, 1>(f, st);
+  else if (f.T <= 32) few_at<BWD, 2>(f, st);
+  else if (f.T <= 48) few_at<BWD, 3>(f, st);
+  else few_at<BWD, 4>(f, st);
+  return hipGetLastError();
 }
 
 // ---------------------------------------------------------------------------
@@ -788,7 +840,7 @@ static XentPlan xent_plan(int64_t T, int64_t V, int64_t D, bool bwd) {
 static bool xent_few(int64_t T, int64_t D) { return T <= kFewTokens && D % 8 == 0; }
 
 size_t xent_workspace(int64_t T, int64_t V, int64_t D, bool bwd) {
-  if (!bwd && xent_few(T, D)) return (size_t)(up((V + kFewRows - 1) / kFewRows * 8 * T, 256) + up(4 * T, 256));
+  if (!bwd && xent_few(T, D)) return (size_t)(up(few_tiles(T, V) * 8 * T, 256) + up(4 * T, 256));
   return (size_t)xent_plan(T, V, D, bwd).total;
 }
 
@@ -812,14 +864,17 @@ hipError_t launch_xent_fwd(const uint16_t* h, const uint16_t* w, const int64_t* 
                            hipStream_t stream) {
   char* base = static_cast<char*>(ws);
   if (xent_few(T, D)) {
-    XentFew f{w, V, (int)D, h, (int)T, targets, reinterpret_cast<float2*>(base),
-              reinterpret_cast<float*>(base + up((V + kFewRows - 1) / kFewRows * 8 * T, 256))};
-    const unsigned grid = (unsigned)((V + kFewRows - 1) / kFewRows);
-    if (T <= 16) xent_few_kernel<1><<<grid, kWave * kFewWaves, 0, stream>>>(f);
-    else if (T <= 32) xent_few_kernel<2><<<grid, kWave * kFewWaves, 0, stream>>>(f);
-    else xent_few_kernel<4><<<grid, kWave * kFewWaves, 0, stream>>>(f);
-    if (hipError_t e = hipGetLastError()) return e;
-    const XentLoss l{f.part, (int)grid, (int)T, f.zt, nullptr, targets, ignore, V, lse, loss};
+    XentFew f{};
+    f.w = w;
+    f.V = V;
+    f.D = (int)D;
+    f.h = h;
+    f.T = (int)T;
+    f.targets = targets;
+    f.part = reinterpret_cast<float2*>(base);
+    f.zt = reinterpret_cast<float*>(base + up(few_tiles(T, V) * 8 * T, 256));
+    if (hipError_t e = launch_few<false>(f, stream)) return e;
+    const XentLoss l{f.part, (int)few_tiles(T, V), (int)T, f.zt, nullptr, targets, ignore, V, lse, loss};
     return launch_loss(l, targets, ignore, total, mean, stream);
   }
   const XentPlan p = xent_plan(T, V, D, false);
@@ -930,8 +985,25 @@ hipError_t launch_xent_bwd(const uint16_t* h, const uint16_t* w, const int64_t* 
     a.vc = (int)vc;
     a.v0 = (int)v0;
     a.tiles_v = (int)((vc + kBI - 1) / kBI);
-    xent_logits_kernel<true><<<(unsigned)(a.tiles_v * a.tiles_t), kThreads, 0, stream>>>(a);
-    if (hipError_t e = hipGetLastError()) return e;
+    if (T <= kFewTokens) {
+      XentFew f{};
+      f.w = a.w;
+      f.V = vc;
+      f.D = a.Dp;
+      f.h = a.hc;
+      f.T = r.T;
+      f.ctl = a.ctl;
+      f.ct = a.ct;
+      f.lse2 = a.lse2;
+      f.c = a.c;
+      f.v0 = a.v0;
+      f.G = a.G;
+      f.ldg = a.ldg;
+      if (hipError_t e = launch_few<true>(f, stream)) return e;
+    } else {
+      xent_logits_kernel<true><<<(unsigned)(a.tiles_v * a.tiles_t), kThreads, 0, stream>>>(a);
+      if (hipError_t e = hipGetLastError()) return e;
+    }
     g.w = a.w;
     g.ldw = a.ldw;
     g.vc = a.vc;

@@ -411,3 +411,11 @@ def test_not_differentiable_twice():
     for out in (linear_cross_entropy(h, w, t), layer_norm(h).float().sum(), gated_activation(h).float().sum()):
         with pytest.raises(RuntimeError):
             torch.autograd.grad(out, h, create_graph=True)
+
+
+@pytest.mark.parametrize("T", [16, 17, 32, 33, 48, 49, 64])
+@pytest.mark.parametrize("V", [24575, 24576, 24700])
+def test_few_tokens_many_columns(T, V):
+    """Around the change of the rows a workgroup takes, each group of 16
+    tokens, rows that do not count among them."""
+    check(*make(T, V, 72, seed=T + V, ignored=T // 5))
