@@ -75,11 +75,19 @@ struct NormFwd {
   float* scales;
 };
 
+// Waves a SIMD holds: what the chunks held per thread leave registers for. The
+// launch takes as many blocks as run together, so that each block's weight and
+// bias are read once and no block starts late.
+template <class T, int CPT>
+constexpr int norm_fwd_waves() {
+  return CPT <= 2 ? 4 : CPT == 3 ? (sizeof(T) == 2 ? 4 : 3) : CPT == 4 && sizeof(T) == 2 ? 3 : 2;
+}
+
 // A block takes rows (TPR threads each) in turn; the weight and bias stay in
 // its registers as loaded, and the next row is requested before the current
 // one is reduced. P: the parameters' type. SHORT: K < 8 (one chunk a row).
 template <class T, class P, int BLOCK, int TPR, int CPT, bool SHORT>
-__global__ __launch_bounds__(BLOCK) void layernorm_fwd_kernel(NormFwd a) {
+__global__ __launch_bounds__(BLOCK, (norm_fwd_waves<T, CPT>())) void layernorm_fwd_kernel(NormFwd a) {
   constexpr int RPB = BLOCK / TPR;
   __shared__ float slot[4][BLOCK / kWave];
   const int t = threadIdx.x % TPR;
@@ -451,19 +459,11 @@ static int64_t row_groups(int64_t M, const RowSplit& s) {
   return (M + rpb - 1) / rpb;
 }
 
-// Blocks of the forward: as many as run together on 256 CUs, so that each
-// block's weight and bias are read once and no block starts late.
 template <class T, class P, int TPR, int CPT, bool SHORT>
 static hipError_t norm_fwd_at(const NormFwd& a, int64_t groups, hipStream_t st) {
   constexpr int BLOCK = TPR < 256 ? 256 : TPR;
-  static const int per_cu = [] {
-    int n = 0;
-    const hipError_t e = hipOccupancyMaxActiveBlocksPerMultiprocessor(
-        &n, layernorm_fwd_kernel<T, P, BLOCK, TPR, CPT, SHORT>, BLOCK, 0);
-    return e == hipSuccess && n > 0 ? n : 1;
-  }();
-  const int64_t most = 256 * (int64_t)per_cu;
-  layernorm_fwd_kernel<T, P, BLOCK, TPR, CPT, SHORT><<<(unsigned)std::min(groups, most), BLOCK, 0, st>>>(a);
+  constexpr int64_t kMost = 256 * (norm_fwd_waves<T, CPT>() * 256 / BLOCK);  // on 256 CUs
+  layernorm_fwd_kernel<T, P, BLOCK, TPR, CPT, SHORT><<<(unsigned)std::min(groups, kMost), BLOCK, 0, st>>>(a);
   return hipGetLastError();
 }
 

@@ -77,15 +77,17 @@ struct XentRows {
   float* c;                // [T] what G's rows are multiplied by
 };
 
-constexpr int kGatherRows = 8;  // two for each of the block's waves
+constexpr int kGatherRows = 8;  // at a time: two for each of the block's waves
 
 // Each block finds how many rows that count precede its own and how many
 // there are by reading all targets (a few KB out of L2), so that no launch
-// or wait between blocks is needed.
+// or wait between blocks is needed. `groups` of kGatherRows rows a block: more
+// with many rows, which keeps the reading linear.
 template <bool BWD>
-__global__ __launch_bounds__(256) void xent_gather_kernel(XentRows a) {
+__global__ __launch_bounds__(256) void xent_gather_kernel(XentRows a, int groups) {
   __shared__ int before[4], all[4];
-  const int t0 = blockIdx.x * kGatherRows, tid = threadIdx.x;
+  const int tid = threadIdx.x;
+  int t0 = blockIdx.x * groups * kGatherRows;
   int b = 0, n = 0;
 #pragma unroll 8
   for (int t = tid; t < a.T; t += 256) {
@@ -110,41 +112,44 @@ __global__ __launch_bounds__(256) void xent_gather_kernel(XentRows a) {
     if constexpr (BWD) a.ctl->c = a.per_row ? 1.0f : a.mean ? *a.dloss / (float)n : *a.dloss;
   }
   const int lane = tid & 63, wave = tid >> 6, nch = a.Dp / 8;
-  // which of the block's rows count, in every lane of every wave
-  const int tl = t0 + (lane & (kGatherRows - 1));
-  const unsigned long long mask = __ballot(lane < kGatherRows && tl < a.T && a.targets[tl < a.T ? tl : 0] != a.ignore);
-  for (int r = wave; r < kGatherRows && t0 + r < a.T; r += 4) {
-    const int t = t0 + r;
-    if (!((mask >> r) & 1)) {
-      if (lane == 0) a.pos[t] = -1;
-      continue;
-    }
-    const int at = b + __popcll(mask & ((1ull << r) - 1));
-    const int64_t target = a.targets[t];
-    const bool in = target >= 0 && target < a.V;
-    if (lane == 0) {
-      a.pos[t] = at;
-      a.ct[at] = in ? (int)target : -1;
-      if constexpr (BWD) {
-        const float c = a.per_row ? a.dloss[t] : 1.0f;
-        a.lse2[at] = a.lse[t] * kLog2e;
-        a.c[at] = in ? c : __uint_as_float(0x7FC00000u);  // a target out of range: NaN gradients
+  for (int end = min(a.T, t0 + groups * kGatherRows); t0 < end; t0 += kGatherRows) {
+    // which of the block's rows count, in every lane of every wave
+    const int tl = t0 + (lane & (kGatherRows - 1));
+    const unsigned long long mask = __ballot(lane < kGatherRows && tl < a.T && a.targets[tl < a.T ? tl : 0] != a.ignore);
+    for (int r = wave; r < kGatherRows && t0 + r < a.T; r += 4) {
+      const int t = t0 + r;
+      if (!((mask >> r) & 1)) {
+        if (lane == 0) a.pos[t] = -1;
+        continue;
+      }
+      const int at = b + __popcll(mask & ((1ull << r) - 1));
+      const int64_t target = a.targets[t];
+      const bool in = target >= 0 && target < a.V;
+      if (lane == 0) {
+        a.pos[t] = at;
+        a.ct[at] = in ? (int)target : -1;
+        if constexpr (BWD) {
+          const float c = a.per_row ? a.dloss[t] : 1.0f;
+          a.lse2[at] = a.lse[t] * kLog2e;
+          a.c[at] = in ? c : __uint_as_float(0x7FC00000u);  // a target out of range: NaN gradients
+        }
+      }
+      const uint16_t* src = a.h + (int64_t)t * a.D;
+      uint4* dst = reinterpret_cast<uint4*>(a.hc + (int64_t)at * a.Dp);
+      for (int c0 = 0; c0 < nch; c0 += 256) {
+        ChunkBf16 v[4];
+  #pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[i] = a.D < 8 ? load8<true>(src, 8 * (c0 + lane + 64 * i), a.D) : load8<false>(src, 8 * (c0 + lane + 64 * i), a.D);
+  #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int ch = c0 + lane + 64 * i;
+          if (a.D >= 8) settle8<false>(v[i], 8 * ch, a.D);
+          if (ch < nch) dst[ch] = v[i].v;
+        }
       }
     }
-    const uint16_t* src = a.h + (int64_t)t * a.D;
-    uint4* dst = reinterpret_cast<uint4*>(a.hc + (int64_t)at * a.Dp);
-    for (int c0 = 0; c0 < nch; c0 += 256) {
-      ChunkBf16 v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        v[i] = a.D < 8 ? load8<true>(src, 8 * (c0 + lane + 64 * i), a.D) : load8<false>(src, 8 * (c0 + lane + 64 * i), a.D);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int ch = c0 + lane + 64 * i;
-        if (a.D >= 8) settle8<false>(v[i], 8 * ch, a.D);
-        if (ch < nch) dst[ch] = v[i].v;
-      }
-    }
+    b += __popcll(mask);
   }
 }
 
@@ -803,6 +808,8 @@ static XentPlan xent_plan(int64_t T, int64_t V, int64_t D, bool bwd) {
   int64_t rows = kReach / (2 * p.Dp) - 256;
   if (p.padded) rows = std::min(rows, kXentPadBytes / (2 * p.Dp));
   if (bwd) rows = std::min(rows, std::min(kXentGBytes / (2 * T), kReach / (2 * (T + 256))));
+  const int64_t tt = (T + kBJ - 1) / kBJ;
+  rows = std::min(rows, std::max<int64_t>(1, (int64_t(1) << 22) / tt) * kBI);  // a launch's tiles fit an int
   p.tiles = piece_tiles(V, rows);
   int64_t at = 256;
   const auto take = [&](int64_t bytes) {
@@ -824,7 +831,7 @@ static XentPlan xent_plan(int64_t T, int64_t V, int64_t D, bool bwd) {
     // dh's tiles split over the piece's columns until a unit is at most
     // about 0.85 of a CU's share of the piece's work, so that units and dW's
     // tiles pack the CUs evenly
-    const int64_t td = (D + kBI - 1) / kBI, tt = (T + kBJ - 1) / kBJ;
+    const int64_t td = (D + kBI - 1) / kBI;
     const int64_t sv = p.tiles * kBI / kRed16, st = (T + kRed16 - 1) / kRed16;
     const double share = (double)(td * tt * sv + td * p.tiles * st) / 256.0;
     int64_t split = (int64_t)((double)sv / (0.85 * share) + 0.999);
@@ -842,6 +849,12 @@ static bool xent_few(int64_t T, int64_t D) { return T <= kFewTokens && D % 8 == 
 size_t xent_workspace(int64_t T, int64_t V, int64_t D, bool bwd) {
   if (!bwd && xent_few(T, D)) return (size_t)(up(few_tiles(T, V) * 8 * T, 256) + up(4 * T, 256));
   return (size_t)xent_plan(T, V, D, bwd).total;
+}
+
+template <bool BWD>
+static void launch_gather(const XentRows& r, hipStream_t st) {
+  const int groups = 1 + r.T / (1 << 14), rows = groups * kGatherRows;
+  xent_gather_kernel<BWD><<<(unsigned)((r.T + rows - 1) / rows), 256, 0, st>>>(r, groups);
 }
 
 static hipError_t launch_pad(const uint16_t* w, int64_t rows, int64_t D, int64_t Dp, uint16_t* out, hipStream_t st) {
@@ -890,7 +903,7 @@ hipError_t launch_xent_fwd(const uint16_t* h, const uint16_t* w, const int64_t* 
   r.hc = reinterpret_cast<uint16_t*>(base + p.hc);
   r.pos = reinterpret_cast<int*>(base + p.pos);
   r.ct = reinterpret_cast<int*>(base + p.ct);
-  xent_gather_kernel<false><<<(unsigned)((T + kGatherRows - 1) / kGatherRows), 256, 0, stream>>>(r);
+  launch_gather<false>(r, stream);
   if (hipError_t e = hipGetLastError()) return e;
   XentTiles a{};
   a.hc = r.hc;
@@ -945,7 +958,7 @@ hipError_t launch_xent_bwd(const uint16_t* h, const uint16_t* w, const int64_t* 
   r.mean = mean ? 1 : 0;
   r.lse2 = reinterpret_cast<float*>(base + p.lse2);
   r.c = reinterpret_cast<float*>(base + p.c);
-  xent_gather_kernel<true><<<(unsigned)((T + kGatherRows - 1) / kGatherRows), 256, 0, stream>>>(r);
+  launch_gather<true>(r, stream);
   if (hipError_t e = hipGetLastError()) return e;
   XentTiles a{};
   a.hc = r.hc;

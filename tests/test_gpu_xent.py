@@ -419,3 +419,11 @@ def test_few_tokens_many_columns(T, V):
     """Around the change of the rows a workgroup takes, each group of 16
     tokens, rows that do not count among them."""
     check(*make(T, V, 72, seed=T + V, ignored=T // 5))
+
+
+@pytest.mark.parametrize("T", [16383, 16384, 40001])
+def test_many_rows(T):
+    """Several groups of rows per gathering block, runs of ignored rows."""
+    h, w, t = make(T, 70, 24, seed=T, ignored=T // 3)
+    t[1000:1900] = -100
+    check(h, w, t, reduction="mean")
