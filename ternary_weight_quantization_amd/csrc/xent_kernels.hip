@@ -205,44 +205,58 @@ __device__ __forceinline__ int row_of(int e, int lane) { return 8 * (e >> 2) + 4
 
 typedef MfmaBf16::Acc AccTile[kFI][kFJ];
 
-// Forward epilogue of a wave's 128 columns x 128 tokens: the maximum M of
-// z log2(e) and the sum of 2^(z log2(e) - M) per token, over both lanes that
-// hold a token. M is the rounded product, the same in every term, so the
-// pair means sum 2^M exactly.
-__device__ __forceinline__ void xent_stats(const XentTiles& a, const AccTile& acc, int i0, int j0, int n, int lane) {
-  const bool whole = i0 + kWTI <= a.vc;  // uniform
+// What the epilogues need of a tile's 256 tokens, staged in LDS before the main
+// loop: the target's row within the tile (out of 0..255 where it is elsewhere)
+// and, backward, lse log2(e) and c.
+struct XentTokens {
+  int target[kBJ];
+  float lse2[kBJ], c[kBJ];
+};
+
+// Rows past the piece count as logits of -inf: 2^-inf is 0.
+__device__ __forceinline__ void xent_mask(AccTile& acc, int rows, int lane) {
+  if (rows >= kWTI) return;  // uniform
+#pragma unroll
+  for (int fi = 0; fi < kFI; ++fi)
+#pragma unroll
+    for (int fj = 0; fj < kFJ; ++fj)
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (32 * fi + row_of(e, lane) >= rows) acc[fi][fj][e] = -INFINITY;
+}
+
+// Forward epilogue of a wave's 128 columns (from i0 of the piece) x 128 tokens
+// (from j0; the tile's token qj): the maximum M of z log2(e) and the sum of
+// 2^(z log2(e) - M) per token, over both lanes that hold a token. M is the
+// rounded product, the same in every term, so the pair means sum 2^M exactly.
+__device__ __forceinline__ void xent_stats(const XentTiles& a, const XentTokens& tok, AccTile& acc, int i0, int j0,
+                                           int qj, int n, int lane) {
+  xent_mask(acc, a.vc - i0, lane);
 #pragma unroll
   for (int fj = 0; fj < kFJ; ++fj) {
     const int j = j0 + 32 * fj + (lane & 31);
+    const int t = tok.target[qj + 32 * fj + (lane & 31)] - i0 % kBI;  // the target's row among these 128?
     float m = -INFINITY;
 #pragma unroll
     for (int fi = 0; fi < kFI; ++fi)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float z = acc[fi][fj][e];
-        if (whole || i0 + 32 * fi + row_of(e, lane) < a.vc) m = fmaxf(m, z);
-      }
+      for (int e = 0; e < 16; ++e) m = fmaxf(m, acc[fi][fj][e]);
     m = fmaxf(m, __shfl_xor(m, 32, kWave));
     const float ref = m == -INFINITY ? 0.0f : m * kLog2e;
-    float s = 0.0f;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // four chains
 #pragma unroll
     for (int fi = 0; fi < kFI; ++fi)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float p = __builtin_amdgcn_exp2f(fmaf(acc[fi][fj][e], kLog2e, -ref));
-        if (whole || i0 + 32 * fi + row_of(e, lane) < a.vc) s += p;
-      }
-    s += __shfl_xor(s, 32, kWave);
-    if (j < n) {
-      if (lane < 32) a.part[(int64_t)((a.v0 + i0) / kWTI) * a.T + j] = make_float2(ref, s);
-      const int t = a.ct[j] - a.v0 - i0;  // the target's row in this tile?
-      if (t >= 0 && t < kWTI && t < a.vc - i0 && ((t >> 2) & 1) == (lane >> 5)) {
+      for (int e = 0; e < 16; ++e) s[e & 3] += __builtin_amdgcn_exp2f(fmaf(acc[fi][fj][e], kLog2e, -ref));
+    float sum = (s[0] + s[1]) + (s[2] + s[3]);
+    sum += __shfl_xor(sum, 32, kWave);
+    if (j < n && lane < 32) a.part[(int64_t)((a.v0 + i0) / kWTI) * a.T + j] = make_float2(ref, sum);
+    if (t >= 0 && t < kWTI && j < n && ((t >> 2) & 1) == (lane >> 5)) {  // rare
 #pragma unroll
-        for (int fi = 0; fi < kFI; ++fi)
+      for (int fi = 0; fi < kFI; ++fi)
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (t == 32 * fi + row_of(e, lane)) a.zt[j] = acc[fi][fj][e];
-      }
+        for (int e = 0; e < 16; ++e)
+          if (t == 32 * fi + row_of(e, lane)) a.zt[j] = acc[fi][fj][e];
     }
   }
 }
@@ -250,46 +264,33 @@ __device__ __forceinline__ void xent_stats(const XentTiles& a, const AccTile& ac
 // Backward epilogue: G of the tile, rounded to bf16 (the operand of both
 // products; the rounding, 2^-9 of each value, is the size of the outputs'
 // own), zeros in the columns past the piece.
-__device__ __forceinline__ void xent_g(const XentTiles& a, AccTile& acc, int i0, int j0, int n, int lane, char* wlds) {
-  const bool whole = i0 + kWTI <= a.vc;
-  float c[kFJ], l[kFJ];
-  int t[kFJ];
+__device__ __forceinline__ void xent_g(const XentTiles& a, const XentTokens& tok, AccTile& acc, int i0, int j0, int qj,
+                                       int n, int lane, char* wlds) {
+  xent_mask(acc, a.vc - i0, lane);
 #pragma unroll
   for (int fj = 0; fj < kFJ; ++fj) {
-    const int j = j0 + 32 * fj + (lane & 31);
-    c[fj] = j < n ? a.c[j] : 0.0f;
-    l[fj] = j < n ? a.lse2[j] : 0.0f;
-    t[fj] = j < n ? a.ct[j] - a.v0 - i0 : -1;
-  }
-#pragma unroll
-  for (int fj = 0; fj < kFJ; ++fj) {
-    const bool here = t[fj] >= 0 && t[fj] < kWTI;
-#pragma unroll
-    for (int fi = 0; fi < kFI; ++fi)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        float p = __builtin_amdgcn_exp2f(fmaf(acc[fi][fj][e], kLog2e, -l[fj]));
-        acc[fi][fj][e] = p;
-      }
-    if (here) {  // rare: a target among these 128 columns
-#pragma unroll
-      for (int fi = 0; fi < kFI; ++fi)
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (t[fj] == 32 * fi + row_of(e, lane)) acc[fi][fj][e] -= 1.0f;
-    }
+    const int at = qj + 32 * fj + (lane & 31);
+    const int t = tok.target[at] - i0 % kBI;
+    const float c = tok.c[at], l = tok.lse2[at];
 #pragma unroll
     for (int fi = 0; fi < kFI; ++fi)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         float v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[e] = acc[fi][fj][4 * g + e] * c[fj];
-          if (!whole && i0 + 32 * fi + row_of(4 * g + e, lane) >= a.vc) v[e] = 0.0f;
-        }
+        for (int e = 0; e < 4; ++e) v[e] = __builtin_amdgcn_exp2f(fmaf(acc[fi][fj][4 * g + e], kLog2e, -l)) * c;
         EpStage<2>::put(wlds, lane, fi, g, make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])));
       }
+    if (t >= 0 && t < kWTI && ((t >> 2) & 1) == (lane >> 5)) {  // rare: the target is one of this lane's rows
+      float z = 0.0f;
+#pragma unroll
+      for (int fi = 0; fi < kFI; ++fi)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (t == 32 * fi + row_of(e, lane)) z = acc[fi][fj][e];
+      const float v = (__builtin_amdgcn_exp2f(fmaf(z, kLog2e, -l)) - 1.0f) * c;
+      *reinterpret_cast<uint16_t*>(wlds + (lane & 31) * EpStage<2>::kPitch + 2 * t) = f32_to_bf16_bits(v);
+    }
     EpStage<2>::drain(wlds, reinterpret_cast<char*>(a.G), a.ldg, n, i0, j0 + 32 * fj, lane);
   }
 }
@@ -302,11 +303,23 @@ __global__ __launch_bounds__(kThreads, 1) void xent_logits_kernel(XentTiles a) {
   typedef SmemLayout<XentW, XentH> L;
   __shared__ __attribute__((aligned(16))) char smem[L::kBytes];
   static_assert(4 * EpStage<2>::kWaveBytes <= L::kBytes, "the epilogue's staging fits the stage buffers");
+  __shared__ XentTokens tok;
   const int n = a.ctl->n;
   int tv, tt;
   xent_tile(cta_order(blockIdx.x, gridDim.x), a.tiles_v, a.tiles_t, tv, tt);
   const int i0 = tv * kBI, j0 = tt * kBJ;
   if (j0 >= n) return;
+  {  // read after the main loop's barriers
+    const int t = threadIdx.x, j = j0 + t;
+    static_assert(kThreads == kBJ, "a thread a token");
+    // a target out of range (-1) or in another piece is in no tile
+    const int r = j < n ? a.ct[j] : -1;
+    tok.target[t] = r >= a.v0 + i0 && r < a.v0 + min(a.vc, i0 + kBI) ? r - a.v0 - i0 : -kBI;
+    if constexpr (BWD) {
+      tok.lse2[t] = j < n ? a.lse2[j] : 0.0f;
+      tok.c[t] = j < n ? a.c[j] : 0.0f;
+    }
+  }
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int pi = (wave % kWavesI) * kWTI, qj = (wave / kWavesI) * kWTJ;
   const XentW pl{reinterpret_cast<const char*>(a.w), 2 * a.ldw, a.vc, 2 * (int64_t)a.Dp};
@@ -317,8 +330,8 @@ __global__ __launch_bounds__(kThreads, 1) void xent_logits_kernel(XentTiles a) {
 #pragma unroll
     for (int fj = 0; fj < kFJ; ++fj) zero_acc(acc[fi][fj]);
   run_stages<MfmaBf16, 1>(pl, ql, smem, acc, i0, j0, 0, a.nstages, pi, qj, lane, nullptr, 0);
-  if constexpr (BWD) xent_g(a, acc, i0 + pi, j0 + qj, n, lane, smem + wave * EpStage<2>::kWaveBytes);
-  else xent_stats(a, acc, i0 + pi, j0 + qj, n, lane);
+  if constexpr (BWD) xent_g(a, tok, acc, i0 + pi, j0 + qj, qj, n, lane, smem + wave * EpStage<2>::kWaveBytes);
+  else xent_stats(a, tok, acc, i0 + pi, j0 + qj, qj, n, lane);
 }
 
 // ---------------------------------------------------------------------------
