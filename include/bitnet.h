@@ -468,7 +468,7 @@ bitnet_status bitnet_layernorm_bwd(const void* dY, bitnet_dtype y_dtype, const v
  * codes   [M][Kc] int8, Kc = bitnet_ckpt_pad(K) (K rounded up to 128), 16-byte
  *         aligned; columns K..Kc-1 are written as 0 and not read back.
  * scales  [M][Kc/128] float, 4-byte aligned.
- * M * Kc <= 2^40, K <= 2^24. No workspace.
+ * M * Kc <= 2^34, K <= 2^24. No workspace.
  */
 int64_t bitnet_ckpt_pad(int64_t K);
 bitnet_status bitnet_ckpt_pack(const void* x, bitnet_dtype x_dtype, int64_t M, int64_t K, int8_t* codes,

@@ -85,10 +85,11 @@ bitnet_status check_norm_sizes(int64_t M, int64_t K) {
   return K > bitnet::kNormMaxK ? BITNET_ERR_SHAPE : BITNET_OK;
 }
 
-// One thread per 8 values, 256 threads a workgroup: at most 2^29 workgroups.
+// One thread per 8 values, 256 threads a workgroup: a launch holds fewer than
+// 2^32 threads.
 bitnet_status check_ckpt_sizes(int64_t M, int64_t K) {
   if (bitnet_status st = check_sizes(M, K)) return st;
-  return K > (int64_t(1) << 24) || M * bitnet::ckpt_pad(K) > (int64_t(1) << 40) ? BITNET_ERR_SHAPE : BITNET_OK;
+  return K > (int64_t(1) << 24) || M * bitnet::ckpt_pad(K) > (int64_t(1) << 34) ? BITNET_ERR_SHAPE : BITNET_OK;
 }
 bool row_stride_ok(int64_t ld, int64_t K) { return ld >= K && ld <= bitnet::k_pad(int64_t(1) << 30); }
 

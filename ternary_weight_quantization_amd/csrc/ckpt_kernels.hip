@@ -14,31 +14,24 @@ namespace bitnet {
 
 constexpr int kRowThreads = 256;
 
-// Lane groups of a launch over M rows of nch chunks each: chunk index -> row
-// and chunk within the row. nch is a multiple of 16, so the 16 lanes of a
-// block share a row.
+// A thread per chunk, `total` of them (below 2^32: the most threads a launch
+// may have): chunk index -> row and chunk within the row. nch is a multiple of
+// 16, so the 16 lanes of a block share a row.
 struct ChunkAt {
   int64_t row;
   int ch;
 };
-__device__ __forceinline__ ChunkAt chunk_at(int64_t i, int nch) {
-  ChunkAt c;
-  if (i <= 0xFFFFFFFFll) {
-    const uint32_t r = (uint32_t)i / (uint32_t)nch;
-    c.row = r;
-    c.ch = (int)((uint32_t)i - r * (uint32_t)nch);
-  } else {
-    c.row = i / nch;
-    c.ch = (int)(i - c.row * nch);
-  }
-  return c;
+__device__ __forceinline__ uint32_t chunk_index() { return blockIdx.x * (uint32_t)kRowThreads + threadIdx.x; }
+__device__ __forceinline__ ChunkAt chunk_at(uint32_t i, int nch) {
+  const uint32_t r = i / (uint32_t)nch;
+  return {(int64_t)r, (int)(i - r * (uint32_t)nch)};
 }
 
 template <class T>
-__global__ __launch_bounds__(kRowThreads) void ckpt_pack_kernel(const T* __restrict__ x, int64_t total, int K, int nch,
+__global__ __launch_bounds__(kRowThreads) void ckpt_pack_kernel(const T* __restrict__ x, uint32_t total, int K, int nch,
                                                                 int8_t* __restrict__ codes,
                                                                 float* __restrict__ scales) {
-  const int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
+  const uint32_t i = chunk_index();
   if (i >= total) return;  // total is a multiple of 16: whole blocks leave
   const ChunkAt at = chunk_at(i, nch);
   const typename ChunkOf<T>::type c = chunk8(x + at.row * K, 8 * at.ch, K);
@@ -52,9 +45,9 @@ __global__ __launch_bounds__(kRowThreads) void ckpt_pack_kernel(const T* __restr
 // Rows of ld values: the codes past K stand for zeros.
 template <class T>
 __global__ __launch_bounds__(kRowThreads) void ckpt_unpack_kernel(const int8_t* __restrict__ codes,
-                                                                  const float* __restrict__ scales, int64_t total,
+                                                                  const float* __restrict__ scales, uint32_t total,
                                                                   int ld, int nch, T* __restrict__ x) {
-  const int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
+  const uint32_t i = chunk_index();
   if (i >= total) return;
   const ChunkAt at = chunk_at(i, nch);
   float f[8];
@@ -64,10 +57,10 @@ __global__ __launch_bounds__(kRowThreads) void ckpt_unpack_kernel(const int8_t* 
 
 // Rows of K bf16 values copied to rows of ld (zeros past K), and with codes
 // their checkpoint from the same registers.
-__global__ __launch_bounds__(kRowThreads) void pad_rows_kernel(const uint16_t* __restrict__ x, int64_t total, int K,
+__global__ __launch_bounds__(kRowThreads) void pad_rows_kernel(const uint16_t* __restrict__ x, uint32_t total, int K,
                                                                int nch, uint16_t* __restrict__ padded, int ld,
                                                                int8_t* __restrict__ codes, float* __restrict__ scales) {
-  const int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
+  const uint32_t i = chunk_index();
   if (i >= total) return;
   const ChunkAt at = chunk_at(i, nch);
   const ChunkBf16 c = chunk8(x + at.row * K, 8 * at.ch, K);
@@ -80,12 +73,12 @@ __global__ __launch_bounds__(kRowThreads) void pad_rows_kernel(const uint16_t* _
   if ((threadIdx.x & 15) == 0) scales[i >> 4] = s;
 }
 
-static unsigned row_grid(int64_t total) { return (unsigned)((total + kRowThreads - 1) / kRowThreads); }
+static unsigned row_grid(uint32_t total) { return (total + kRowThreads - 1) / kRowThreads; }
 
 hipError_t launch_ckpt_pack(const void* x, bool x_f32, int64_t M, int64_t K, int8_t* codes, float* scales,
                             hipStream_t stream) {
   const int nch = (int)(ckpt_pad(K) / 8);
-  const int64_t total = M * nch;
+  const uint32_t total = (uint32_t)(M * nch);
   if (x_f32)
     ckpt_pack_kernel<<<row_grid(total), kRowThreads, 0, stream>>>(static_cast<const float*>(x), total, (int)K, nch,
                                                                   codes, scales);
@@ -98,7 +91,7 @@ hipError_t launch_ckpt_pack(const void* x, bool x_f32, int64_t M, int64_t K, int
 hipError_t launch_pad_rows(const uint16_t* x, int64_t M, int64_t K, uint16_t* padded, int64_t ld, int8_t* codes,
                            float* scales, hipStream_t stream) {
   const int nch = (int)(ckpt_pad(K) / 8);
-  const int64_t total = M * nch;
+  const uint32_t total = (uint32_t)(M * nch);
   pad_rows_kernel<<<row_grid(total), kRowThreads, 0, stream>>>(x, total, (int)K, nch, padded, (int)ld, codes, scales);
   return hipGetLastError();
 }
@@ -106,7 +99,7 @@ hipError_t launch_pad_rows(const uint16_t* x, int64_t M, int64_t K, uint16_t* pa
 hipError_t launch_ckpt_unpack(const int8_t* codes, const float* scales, int64_t M, int64_t K, void* x, int64_t ld,
                               bool x_f32, hipStream_t stream) {
   const int nch = (int)(ckpt_pad(K) / 8);
-  const int64_t total = M * nch;
+  const uint32_t total = (uint32_t)(M * nch);
   if (x_f32)
     ckpt_unpack_kernel<<<row_grid(total), kRowThreads, 0, stream>>>(codes, scales, total, (int)ld, nch,
                                                                     static_cast<float*>(x));
@@ -151,10 +144,10 @@ struct ActRelu2 {
 template <class A, bool CK, bool UP>
 __global__ __launch_bounds__(kRowThreads) void gate_fwd_kernel(const uint16_t* __restrict__ gate, int64_t ldg,
                                                                const uint16_t* __restrict__ up, int64_t ldu,
-                                                               int64_t total, int K, int nch, uint16_t* __restrict__ y,
+                                                               uint32_t total, int K, int nch, uint16_t* __restrict__ y,
                                                                int8_t* __restrict__ gq, float* __restrict__ gs,
                                                                int8_t* __restrict__ uq, float* __restrict__ us) {
-  const int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
+  const uint32_t i = chunk_index();
   if (i >= total) return;
   const ChunkAt at = chunk_at(i, nch);
   const int k0 = 8 * at.ch;
@@ -195,10 +188,10 @@ __global__ __launch_bounds__(kRowThreads) void gate_bwd_kernel(const uint16_t* _
                                                                const int8_t* __restrict__ gq,
                                                                const float* __restrict__ gs,
                                                                const int8_t* __restrict__ uq,
-                                                               const float* __restrict__ us, int64_t total, int K,
+                                                               const float* __restrict__ us, uint32_t total, int K,
                                                                int nch, uint16_t* __restrict__ dgate, int64_t lddg,
                                                                uint16_t* __restrict__ dup, int64_t lddu) {
-  const int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
+  const uint32_t i = chunk_index();
   if (i >= total) return;
   const ChunkAt at = chunk_at(i, nch);
   const int k0 = 8 * at.ch;
@@ -236,7 +229,7 @@ template <class A>
 static void gate_fwd(const uint16_t* gate, int64_t ldg, const uint16_t* up, int64_t ldu, int64_t M, int64_t K,
                      uint16_t* y, int8_t* gq, float* gs, int8_t* uq, float* us, hipStream_t st) {
   const int nch = (int)(ckpt_pad(K) / 8);
-  const int64_t total = M * nch;
+  const uint32_t total = (uint32_t)(M * nch);
   const unsigned grid = row_grid(total);
   const int k = (int)K;
   if (up && gq) gate_fwd_kernel<A, true, true><<<grid, kRowThreads, 0, st>>>(gate, ldg, up, ldu, total, k, nch, y, gq, gs, uq, us);
@@ -257,7 +250,7 @@ static void gate_bwd(const uint16_t* dY, const uint16_t* gate, int64_t ldg, cons
                      const int8_t* gq, const float* gs, const int8_t* uq, const float* us, int64_t M, int64_t K,
                      uint16_t* dgate, int64_t lddg, uint16_t* dup, int64_t lddu, hipStream_t st) {
   const int nch = (int)(ckpt_pad(K) / 8);
-  const int64_t total = M * nch;
+  const uint32_t total = (uint32_t)(M * nch);
   const unsigned grid = row_grid(total);
   const int k = (int)K;
   if (dup && gq) gate_bwd_kernel<A, true, true><<<grid, kRowThreads, 0, st>>>(dY, gate, ldg, up, ldu, gq, gs, uq, us, total, k, nch, dgate, lddg, dup, lddu);

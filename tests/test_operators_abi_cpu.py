@@ -200,3 +200,12 @@ def test_xent_python_refusals():
         linear_cross_entropy(h, w, t, reduction="max")
     with pytest.raises(ValueError):
         linear_cross_entropy(h, w, t)  # not on a GPU
+
+
+def test_checkpoint_size_limit(L):
+    """More values than a launch holds threads for."""
+    for M, K in ((1 << 27, 129), ((1 << 27) + 1, 128), (1 << 30, 17)):
+        assert L.bitnet_ckpt_pack(P, BF, M, K, P, P, None) == ESHAPE
+        assert L.bitnet_ckpt_unpack(P, P, M, K, P, F32, None) == ESHAPE
+        assert L.bitnet_gate_fwd(0, P, K, P, K, M, K, P, None, None, None, None, None) == ESHAPE
+        assert L.bitnet_gate_bwd(0, P, P, K, P, K, None, None, None, None, M, K, P, K, P, K, None) == ESHAPE
