@@ -138,10 +138,10 @@ __global__ __launch_bounds__(256) void xent_gather_kernel(XentRows a, int groups
       uint4* dst = reinterpret_cast<uint4*>(a.hc + (int64_t)at * a.Dp);
       for (int c0 = 0; c0 < nch; c0 += 256) {
         ChunkBf16 v[4];
-  #pragma unroll
+#pragma unroll
         for (int i = 0; i < 4; ++i)
           v[i] = a.D < 8 ? load8<true>(src, 8 * (c0 + lane + 64 * i), a.D) : load8<false>(src, 8 * (c0 + lane + 64 * i), a.D);
-  #pragma unroll
+#pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int ch = c0 + lane + 64 * i;
           if (a.D >= 8) settle8<false>(v[i], 8 * ch, a.D);
@@ -289,7 +289,8 @@ __device__ __forceinline__ void xent_g(const XentTiles& a, const XentTokens& tok
         for (int e = 0; e < 16; ++e)
           if (t == 32 * fi + row_of(e, lane)) z = acc[fi][fj][e];
       const float v = (__builtin_amdgcn_exp2f(fmaf(z, kLog2e, -l)) - 1.0f) * c;
-      *reinterpret_cast<uint16_t*>(wlds + (lane & 31) * EpStage<2>::kPitch + 2 * t) = f32_to_bf16_bits(v);
+      const uint16_t bits = f32_to_bf16_bits(v);
+      memcpy(wlds + (lane & 31) * EpStage<2>::kPitch + 2 * t, &bits, 2);
     }
     EpStage<2>::drain(wlds, reinterpret_cast<char*>(a.G), a.ldg, n, i0, j0 + 32 * fj, lane);
   }
