@@ -10,6 +10,7 @@
 // Python took 130 us of host time a step (the autograd engine runs a GPU
 // node's backward on its own thread, where Python code runs cold).
 
+#include <c10/hip/HIPGraphsC10Utils.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/extension.h>
 
@@ -55,8 +56,20 @@ Tensor aligned(const Tensor& t) {
   return reinterpret_cast<uintptr_t>(c.data_ptr()) % 16 == 0 ? c : c.clone();
 }
 
-void no_second_derivative() {
+// What every backward refuses: a second derivative, and being captured into a
+// graph while a gradient goes on to a node of the default stream, which no
+// capture can take in. Such a node is the accumulator of a leaf of which a
+// graph made on the default stream is still alive.
+void check_backward() {
   TORCH_CHECK(!at::GradMode::is_enabled(), "this operator's gradients cannot be differentiated again");
+  if (c10::hip::currentStreamCaptureStatusMayInitCtx() == c10::hip::CaptureStatus::None) return;
+  for (const torch::autograd::Edge& e : torch::autograd::get_current_node()->next_edges()) {
+    if (!e.is_valid()) continue;
+    const optional<c10::Stream> s = e.function->stream();
+    TORCH_CHECK(!s.has_value() || s->id() != c10::hip::getDefaultHIPStream(s->device_index()).id(),
+                "a backward pass is being captured whose gradient goes to a node of the default stream: free the "
+                "results of earlier calls that use the same leaves (or make them on another stream) first");
+  }
 }
 
 bool wants_grad(std::initializer_list<const Tensor*> ts) {
@@ -150,7 +163,7 @@ struct LayerNormFn : torch::autograd::Function<LayerNormFn> {
   }
 
   static variable_list backward(AutogradContext* ctx, const variable_list& grads) {
-    no_second_derivative();
+    check_backward();
     const variable_list saved = ctx->get_saved_variables();
     const Tensor &x2 = saved[0], &codes = saved[1], &scales = saved[2], &w = saved[3], &stats = saved[4];
     const std::vector<int64_t> shape = ctx->saved_data["shape"].toIntVector();
@@ -271,7 +284,7 @@ struct GateFn : torch::autograd::Function<GateFn> {
   }
 
   static variable_list backward(AutogradContext* ctx, const variable_list& grads) {
-    no_second_derivative();
+    check_backward();
     const variable_list saved = ctx->get_saved_variables();
     const bool checkpoint = ctx->saved_data["checkpoint"].toBool(), gated = ctx->saved_data["up"].toBool();
     const auto act = static_cast<bitnet_act>(ctx->saved_data["act"].toInt());
@@ -311,7 +324,8 @@ Tensor gated_activation(const Tensor& gate, const optional<Tensor>& up, int64_t 
 // --- the TTQ layer with an 8-bit checkpoint of its input --------------------------------
 
 struct TtqFn : torch::autograd::Function<TtqFn> {
-  static Tensor forward(AutogradContext* ctx, const Tensor& x, const Tensor& weight, const Tensor& params) {
+  // keep: dW or the scales' gradients are wanted, which alone read x
+  static Tensor forward(AutogradContext* ctx, const Tensor& x, const Tensor& weight, const Tensor& params, bool keep) {
     const Tensor x2 = aligned(rows(x)), w = aligned(weight), p = params.to(at::kFloat).contiguous();
     const int64_t M = x2.size(0), K = x2.size(1), N = w.size(0), Kp = bitnet_k_pad(K);
     std::vector<int64_t> shape = x.sizes().vec();
@@ -321,7 +335,7 @@ struct TtqFn : torch::autograd::Function<TtqFn> {
     const size_t bytes = ttq_fwd_ckpt_workspace_bytes(M, N, K);
     const Tensor ws = scratch(bytes, x);
     Tensor codes, scales;
-    if (weight.requires_grad() || params.requires_grad()) std::tie(codes, scales) = empty_codes(M, K, x2);  // dW alone reads x
+    if (keep) std::tie(codes, scales) = empty_codes(M, K, x2);
     On on(x2);
     check(ttq_quantize(ptr(w), code(w.scalar_type()), N, K, f32(p), static_cast<uint8_t*>(ptr(codes_w)), bf16(wt),
                        on.stream));
@@ -333,7 +347,7 @@ struct TtqFn : torch::autograd::Function<TtqFn> {
   }
 
   static variable_list backward(AutogradContext* ctx, const variable_list& grads) {
-    no_second_derivative();
+    check_backward();
     const variable_list saved = ctx->get_saved_variables();
     const Tensor &codes = saved[0], &scales = saved[1], &wt = saved[2], &codes_w = saved[3];
     const std::vector<int64_t> shape = ctx->saved_data["x"].toIntVector();
@@ -351,7 +365,7 @@ struct TtqFn : torch::autograd::Function<TtqFn> {
     On on(dY);
     check(ttq_bwd_ckpt(bf16(dY), i8(codes), f32(scales), bf16(wt), static_cast<uint8_t*>(ptr(codes_w)), M, N, K, bf16(dX),
                        ptr(dW), code(wdt), dp.defined() ? f32(dp) + 1 : nullptr, ptr(ws), bytes, on.stream));
-    return {dX, need_w ? dW : Tensor(), dp};
+    return {dX, need_w ? dW : Tensor(), dp, Tensor()};
   }
 };
 
@@ -364,7 +378,7 @@ Tensor ttq_linear_checkpoint(const Tensor& x, const Tensor& weight, const Tensor
   TORCH_CHECK_VALUE(params.numel() == 3 && params.dim() == 1, "params: expected shape [3], got ", params.sizes());
   TORCH_CHECK_VALUE(weight.device() == x.device() && params.device() == x.device(),
                     "x, weight and params: must be GPU tensors of one device");
-  return TtqFn::apply(x, weight, params);
+  return TtqFn::apply(x, weight, params, wants_grad({&weight, &params}));
 }
 
 // --- linear layer with cross entropy -------------------------------------------------
@@ -399,7 +413,7 @@ struct XentFn : torch::autograd::Function<XentFn> {
   }
 
   static variable_list backward(AutogradContext* ctx, const variable_list& grads) {
-    no_second_derivative();
+    check_backward();
     const variable_list saved = ctx->get_saved_variables();
     const Tensor &h = saved[0], &w = saved[1], &t = saved[2], &lse = saved[3];
     const auto reduce = static_cast<bitnet_reduce>(ctx->saved_data["reduce"].toInt());
