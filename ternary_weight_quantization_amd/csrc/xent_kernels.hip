@@ -458,8 +458,14 @@ __global__ __launch_bounds__(1024) void xent_reduce_kernel(const float* __restri
 // the pairs 58-78 us (arrivals at one address run 25 ns apart).
 // ---------------------------------------------------------------------------
 
-constexpr int kFewTokens = 64;
 constexpr int kFewWaves = 4;
+
+// Few tokens: up to 64, and up to 48 where the 256 x 256 tiles of W's rows
+// fill most of the CUs, which then take W no slower. The loss in us, this way
+// / by tiles, at D = 2560: 48 tokens 44 / 67 against 32000 columns, 155 / 152
+// against 128256; 64 tokens 52 / 67 against 32000, 97 / 84 against 64000, 187 /
+// 152 against 128256.
+static bool few_tokens(int64_t T, int64_t V) { return T <= (V < 224 * kBI ? 64 : 48); }
 
 struct XentFew {
   const uint16_t* w;  // [V][D] (backward: a piece's rows), D a multiple of 8
@@ -602,7 +608,7 @@ __global__ __launch_bounds__(kWave * kFewWaves) void xent_few_kernel(XentFew a) 
 // many bytes as W's, and 128 rows share them where that leaves enough
 // workgroups. Measured at D = 2560, 128 against 64 rows: 32 tokens 41.5 / 46.0
 // us against 32000 columns and 147 / 168 against 128256, but 29.7 / 20.5
-// against 8000; 64 tokens 52.9 / 59.8, 188 / 218 and 35.4 / 25.6.
+// against 8000; 64 tokens 52.9 / 59.8 against 32000 and 35.4 / 25.6 against 8000.
 static int few_rows(int64_t T, int64_t V) { return T > 16 && V >= 192 * 128 ? 128 : 64; }
 static int64_t few_tiles(int64_t T, int64_t V) { return (V + few_rows(T, V) - 1) / few_rows(T, V); }
 
@@ -858,10 +864,10 @@ static XentPlan xent_plan(int64_t T, int64_t V, int64_t D, bool bwd) {
   return p;
 }
 
-static bool xent_few(int64_t T, int64_t D) { return T <= kFewTokens && D % 8 == 0; }
+static bool xent_few(int64_t T, int64_t V, int64_t D) { return few_tokens(T, V) && D % 8 == 0; }
 
 size_t xent_workspace(int64_t T, int64_t V, int64_t D, bool bwd) {
-  if (!bwd && xent_few(T, D)) return (size_t)(up(few_tiles(T, V) * 8 * T, 256) + up(4 * T, 256));
+  if (!bwd && xent_few(T, V, D)) return (size_t)(up(few_tiles(T, V) * 8 * T, 256) + up(4 * T, 256));
   return (size_t)xent_plan(T, V, D, bwd).total;
 }
 
@@ -890,7 +896,7 @@ hipError_t launch_xent_fwd(const uint16_t* h, const uint16_t* w, const int64_t* 
                            int64_t V, int64_t D, float* loss, float* lse, float* total, bool mean, void* ws,
                            hipStream_t stream) {
   char* base = static_cast<char*>(ws);
-  if (xent_few(T, D)) {
+  if (xent_few(T, V, D)) {
     XentFew f{};
     f.w = w;
     f.V = V;
@@ -1012,7 +1018,7 @@ hipError_t launch_xent_bwd(const uint16_t* h, const uint16_t* w, const int64_t* 
     a.vc = (int)vc;
     a.v0 = (int)v0;
     a.tiles_v = (int)((vc + kBI - 1) / kBI);
-    if (T <= kFewTokens) {
+    if (few_tokens(T, V)) {
       XentFew f{};
       f.w = a.w;
       f.V = vc;

@@ -421,6 +421,13 @@ def test_few_tokens_many_columns(T, V):
     check(*make(T, V, 72, seed=T + V, ignored=T // 5))
 
 
+@pytest.mark.parametrize("T", [48, 49, 64])
+@pytest.mark.parametrize("V", [57343, 57344])
+def test_few_tokens_or_tiles(T, V):
+    """Either side of the choice between the kernels."""
+    check(*make(T, V, 72, seed=T + V, ignored=T // 5))
+
+
 @pytest.mark.parametrize("T", [16383, 16384, 40001])
 def test_many_rows(T):
     """Several groups of rows per gathering block, runs of ignored rows."""
