@@ -432,8 +432,12 @@ __global__ __launch_bounds__(1024) void layernorm_cols_kernel(const float* __res
 
 // ---------------------------------------------------------------------------
 // Launches. Threads per row and chunks per thread from the row length alone:
-// one wave up to two chunks a thread (no barriers), two waves up to three, 4
-// waves up to four, 8 above (kNormMaxK).
+// one wave (no barriers) up to five chunks a thread, two waves for three, four
+// up to four chunks, eight above (kNormMaxK). Measured, forward and backward in
+// us, without / with codes: 32768 x 1536 one wave 102 / 102, two 121 / 136;
+// 16384 x 2560 one wave 84 / 93, two 86 / 96, four 112 / 130; 16384 x 2900 one
+// wave (six chunks) 138 / 155, two 104 / 108; 8192 x 4096 four waves 72 / 81,
+// two 74 / 89; 8192 x 6912 four waves 121 / 125, eight 119 / 158.
 // ---------------------------------------------------------------------------
 
 struct RowSplit {
@@ -443,15 +447,15 @@ struct RowSplit {
 // whole chunk of the row (it lies before the row's last block of 128).
 static RowSplit row_split(int64_t K) {
   const int nch = (int)(ckpt_pad(K) / 8);
-  const int tpr = nch <= 128 ? 64 : nch <= 384 ? 128 : nch <= 1024 ? 256 : 512;
+  const int tpr = nch <= 320 ? 64 : nch <= 384 ? 128 : nch <= 1024 ? 256 : 512;
   return {tpr, (nch + tpr - 1) / tpr};
 }
 
 // Every pair that row_split gives, and rows of fewer than 8 values.
 #define BITNET_NORM_SHAPES(F)                                                                                  \
-  F(64, 1, true) F(64, 1, false) F(64, 2, false) F(128, 2, false) F(128, 3, false) F(256, 2, false)            \
-  F(256, 3, false) F(256, 4, false) F(512, 3, false) F(512, 4, false) F(512, 5, false) F(512, 6, false)        \
-  F(512, 7, false) F(512, 8, false)
+  F(64, 1, true) F(64, 1, false) F(64, 2, false) F(64, 3, false) F(64, 4, false) F(64, 5, false)               \
+  F(128, 3, false) F(256, 2, false) F(256, 3, false) F(256, 4, false) F(512, 3, false) F(512, 4, false)        \
+  F(512, 5, false) F(512, 6, false) F(512, 7, false) F(512, 8, false)
 
 // Row groups of a launch.
 static int64_t row_groups(int64_t M, const RowSplit& s) {
