@@ -19,7 +19,8 @@
 // Rows whose target is ignore_index are taken out first: the rows that count
 // are gathered to the front (hc), so that an ignored row costs nothing and
 // nothing it holds, NaN included, reaches a sum. The number n of rows that
-// count stays on the device; tiles past it leave at once.
+// count stays on the device; tiles past it leave at once. Where all T rows
+// count and need no padding, nothing is copied and h is read in place.
 //
 // Many tokens:
 //   gather   rows, targets, (backward) lse and c of the rows that count
@@ -77,7 +78,7 @@ struct XentRows {
   float* c;                // [T] what G's rows are multiplied by
 };
 
-constexpr int kGatherRows = 8;  // at a time: two for each of the block's waves
+constexpr int kGatherRows = 4;  // at a time: one for each of the block's waves
 
 // Each block finds how many rows that count precede its own and how many
 // there are by reading all targets (a few KB out of L2), so that no launch
@@ -111,17 +112,15 @@ __global__ __launch_bounds__(256) void xent_gather_kernel(XentRows a, int groups
     a.ctl->n = n;
     if constexpr (BWD) a.ctl->c = a.per_row ? 1.0f : a.mean ? *a.dloss / (float)n : *a.dloss;
   }
-  const int lane = tid & 63, wave = tid >> 6, nch = a.Dp / 8;
+  const int lane = tid & 63, wave = tid >> 6, nch = n == a.T && a.Dp == a.D ? 0 : a.Dp / 8;
   for (int end = min(a.T, t0 + groups * kGatherRows); t0 < end; t0 += kGatherRows) {
     // which of the block's rows count, in every lane of every wave
     const int tl = t0 + (lane & (kGatherRows - 1));
     const unsigned long long mask = __ballot(lane < kGatherRows && tl < a.T && a.targets[tl < a.T ? tl : 0] != a.ignore);
-    for (int r = wave; r < kGatherRows && t0 + r < a.T; r += 4) {
-      const int t = t0 + r;
-      if (!((mask >> r) & 1)) {
-        if (lane == 0) a.pos[t] = -1;
-        continue;
-      }
+    const int r = wave, t = t0 + r;
+    if (t < a.T && !((mask >> r) & 1)) {
+      if (lane == 0) a.pos[t] = -1;
+    } else if (t < a.T) {
       const int at = b + __popcll(mask & ((1ull << r) - 1));
       const int64_t target = a.targets[t];
       const bool in = target >= 0 && target < a.V;
@@ -164,6 +163,15 @@ __global__ __launch_bounds__(256) void xent_pad_kernel(const uint16_t* __restric
   reinterpret_cast<uint4*>(out)[i] = chunk8(w + r * D, k0, D).v;
 }
 
+// The rows that count [n][Dp]: the gathered ones, or h itself where all T
+// count (`all` is hc too where h's width is padded).
+struct XentHidden {
+  const uint16_t* hc;
+  const uint16_t* all;
+  int T;
+  __device__ __forceinline__ const uint16_t* rows(int n) const { return n == T ? all : hc; }
+};
+
 // ---------------------------------------------------------------------------
 // Logit tiles
 // ---------------------------------------------------------------------------
@@ -174,7 +182,7 @@ struct XentTiles {
   int vc;             // valid rows
   int v0;             // the piece's first row
   int tiles_v, tiles_t, nstages;
-  const uint16_t* hc;  // [n][Dp]
+  XentHidden h;
   int Dp;
   const XentCtl* ctl;
   const int* ct;
@@ -324,7 +332,7 @@ __global__ __launch_bounds__(kThreads, 1) void xent_logits_kernel(XentTiles a) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int pi = (wave % kWavesI) * kWTI, qj = (wave / kWavesI) * kWTJ;
   const XentW pl{reinterpret_cast<const char*>(a.w), 2 * a.ldw, a.vc, 2 * (int64_t)a.Dp};
-  const XentH ql{reinterpret_cast<const char*>(a.hc), 2 * (int64_t)a.Dp, n, 2 * (int64_t)a.Dp};
+  const XentH ql{reinterpret_cast<const char*>(a.h.rows(n)), 2 * (int64_t)a.Dp, n, 2 * (int64_t)a.Dp};
   AccTile acc;
 #pragma unroll
   for (int fi = 0; fi < kFI; ++fi)
@@ -471,7 +479,7 @@ struct XentFew {
   const uint16_t* w;  // [V][D] (backward: a piece's rows), D a multiple of 8
   int64_t V;
   int D;
-  const uint16_t* h;  // [T][D] (backward: the rows that count)
+  XentHidden h;  // [T][D] (backward: the rows that count)
   int T;
   // forward
   const int64_t* targets;
@@ -500,7 +508,7 @@ __global__ __launch_bounds__(kWave * kFewWaves) void xent_few_kernel(XentFew a) 
   const int rows = (int)(a.V - v0 < ROWS ? a.V - v0 : ROWS);
   const rsrc_t rw = make_rsrc(a.w + v0 * D, (uint32_t)(rows * D * 2));
   const int n = BWD ? a.ctl->n : a.T;
-  const rsrc_t rh = make_rsrc(a.h, (uint32_t)(n * D * 2));
+  const rsrc_t rh = make_rsrc(a.h.rows(n), (uint32_t)(n * D * 2));
   const uint32_t row = (uint32_t)((lane & 15) * D * 2);  // rows past the end read as zeros
   f32x4_t acc[TT][FR];
 #pragma unroll
@@ -637,7 +645,7 @@ struct XentGrads {
   const uint16_t* w;  // [vc][ldw]
   int64_t ldw;
   int vc;
-  const uint16_t* hc;  // [n][Dp]
+  XentHidden h;
   int Dp, D, T;
   const XentCtl* ctl;
   // dh: tiles_d x tiles_t tiles, each split over `split` ranges of the
@@ -759,7 +767,7 @@ __global__ __launch_bounds__(kThreads, 1) void xent_grads_kernel(XentGrads a) {
   }
   b = cta_order(b - a.dh_units, gridDim.x - a.dh_units);
   const int i0 = (b % a.tiles_d) * kBI, j0 = (b / a.tiles_d) * kBJ;
-  const XentHt pl{a.hc, a.Dp, n, a.Dp};
+  const XentHt pl{a.h.rows(n), a.Dp, n, a.Dp};
   const XentGt ql{a.G, a.ldg, n, a.ldg};
   run_stages<MfmaBf16, 0>(pl, ql, smem, acc, i0, j0, 0, (n + kRed16 - 1) / kRed16, pi, qj, lane, nullptr, 0);
   // no row counts: G and hc are empty and c may be anything
@@ -873,7 +881,7 @@ size_t xent_workspace(int64_t T, int64_t V, int64_t D, bool bwd) {
 
 template <bool BWD>
 static void launch_gather(const XentRows& r, hipStream_t st) {
-  const int groups = 1 + r.T / (1 << 14), rows = groups * kGatherRows;
+  const int groups = 1 + r.T / (1 << 13), rows = groups * kGatherRows;
   xent_gather_kernel<BWD><<<(unsigned)((r.T + rows - 1) / rows), 256, 0, st>>>(r, groups);
 }
 
@@ -901,7 +909,7 @@ hipError_t launch_xent_fwd(const uint16_t* h, const uint16_t* w, const int64_t* 
     f.w = w;
     f.V = V;
     f.D = (int)D;
-    f.h = h;
+    f.h = XentHidden{h, h, (int)T};
     f.T = (int)T;
     f.targets = targets;
     f.part = reinterpret_cast<float2*>(base);
@@ -926,7 +934,7 @@ hipError_t launch_xent_fwd(const uint16_t* h, const uint16_t* w, const int64_t* 
   launch_gather<false>(r, stream);
   if (hipError_t e = hipGetLastError()) return e;
   XentTiles a{};
-  a.hc = r.hc;
+  a.h = XentHidden{r.hc, p.padded ? r.hc : h, r.T};
   a.Dp = r.Dp;
   a.ctl = r.ctl;
   a.ct = r.ct;
@@ -981,7 +989,7 @@ hipError_t launch_xent_bwd(const uint16_t* h, const uint16_t* w, const int64_t* 
   launch_gather<true>(r, stream);
   if (hipError_t e = hipGetLastError()) return e;
   XentTiles a{};
-  a.hc = r.hc;
+  a.h = XentHidden{r.hc, p.padded ? r.hc : h, r.T};
   a.Dp = r.Dp;
   a.ctl = r.ctl;
   a.ct = r.ct;
@@ -995,7 +1003,7 @@ hipError_t launch_xent_bwd(const uint16_t* h, const uint16_t* w, const int64_t* 
   XentGrads g{};
   g.G = a.G;
   g.ldg = a.ldg;
-  g.hc = a.hc;
+  g.h = a.h;
   g.Dp = a.Dp;
   g.D = (int)D;
   g.T = r.T;
@@ -1023,7 +1031,7 @@ hipError_t launch_xent_bwd(const uint16_t* h, const uint16_t* w, const int64_t* 
       f.w = a.w;
       f.V = vc;
       f.D = a.Dp;
-      f.h = a.hc;
+      f.h = a.h;
       f.T = r.T;
       f.ctl = a.ctl;
       f.ct = a.ct;
