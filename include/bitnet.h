@@ -583,7 +583,8 @@ bitnet_status bitnet_xent_bwd(const uint16_t* h, const uint16_t* w, const int64_
  *               < 0: whole tiles only.
  *   pair_cols   0: the cost model; k >= 1: a paired backward launch gives
  *               dX k of its 8-workgroup columns.
- *   no_skinny   nonzero: the large-M GEMMs also for M <= 64 (workspace
+ *   no_skinny   nonzero: the cross entropy by tiles for every size, and the
+ *               large-M GEMMs also for M <= 64 (workspace
  *               sizes queried while it is set cover that route).
  *   spin_limit  polls (each a short sleep) before a workgroup waiting for
  *               another's partial tile gives up; the default,

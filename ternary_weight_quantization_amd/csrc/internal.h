@@ -16,7 +16,8 @@ namespace bitnet {
 //              workgroups (and no paired backward launch); < 0: whole tiles
 //  pair_cols   0: cost model; k >= 1: dX gets k of the 8-workgroup columns
 //              of a paired backward launch
-//  no_skinny   nonzero: the large-M GEMMs also for few tokens
+//  no_skinny   nonzero: the large-M GEMMs also for few tokens, and the cross
+//              entropy by tiles for every size
 //  spin_limit  polls before a wait for another workgroup's partial tile
 //              gives up (the tile is then written as a sentinel and counted)
 constexpr uint32_t kDefaultSpinLimit = 1u << 24;

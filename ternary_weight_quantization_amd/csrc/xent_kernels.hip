@@ -37,6 +37,15 @@
 //   dh       the slabs summed in a fixed order, rounded once, scattered back
 //            to the rows; ignored rows get zeros
 // No atomics: the same inputs give the same bits.
+//
+// Measured in us: 4096 tokens, 128256 columns, D = 2560: logits forward 2208
+// (1218 TFLOP/s; this card's best library product alone, which writes the
+// logits, takes 2024), backward logits 8 x 287, grads 8 x 547 (1229 TFLOP/s;
+// the two products as library calls 377 + 393), gather 6, combine 11, dh 13.
+// 1000 tokens of which 750 count, 50257 columns: 230 + 240 + 470 with 591
+// tiles of logits on 256 CUs (three rounds for 2.3 of work) and dW tiles of 12
+// stages. Workgroups that stay for every 256th tile and load the next one
+// during the last stages of the current one were 5 % slower.
 
 #include <algorithm>
 
@@ -449,9 +458,10 @@ __global__ __launch_bounds__(1024) void xent_reduce_kernel(const float* __restri
 }
 
 // ---------------------------------------------------------------------------
-// Few tokens: one pass over W. A workgroup takes 64 or 128 rows of W, its waves
-// every 4th stage of 64 columns; both operands go from memory straight to
-// the fragments of v_mfma_f32_16x16x32_bf16, the waves' sums meet in LDS, and
+// Few tokens, or few tiles: a workgroup takes 64 tokens (or all, in groups of
+// 16) and 64 or 128 rows of W, its waves every 4th stage of 64 columns; with up
+// to 64 tokens that is one pass over W. Both operands go from memory straight
+// to the fragments of v_mfma_f32_16x16x32_bf16, the waves' sums meet in LDS, and
 // each group of 16 tokens reduces its column of the tile to one pair per
 // token (forward) or writes its columns of G (backward).
 //
@@ -467,20 +477,29 @@ __global__ __launch_bounds__(1024) void xent_reduce_kernel(const float* __restri
 // ---------------------------------------------------------------------------
 
 constexpr int kFewWaves = 4;
+constexpr int kFewGroup = 64;  // tokens a workgroup takes at most
 
-// Few tokens: up to 64, and up to 48 where the 256 x 256 tiles of W's rows
-// fill most of the CUs, which then take W no slower. The loss in us, this way
-// / by tiles, at D = 2560: 48 tokens 44 / 67 against 32000 columns, 155 / 152
-// against 128256; 64 tokens 52 / 67 against 32000, 97 / 84 against 64000, 187 /
-// 152 against 128256.
-static bool few_tokens(int64_t T, int64_t V) { return T <= (V < 224 * kBI ? 64 : 48); }
+// The choice between this way and 256 x 256 tiles. At most 512 workgroups of
+// 64 tokens x 64 rows (two a CU): this way, where tiles would leave most CUs
+// idle. More: this way up to 64 tokens, up to 48 where the tiles of W's rows
+// fill most of the CUs. The loss in us, this way / by tiles, at D = 2560: 100
+// tokens 26 / 57 against 8000 columns and 67 / 61 against 20000, 256 tokens 37 /
+// 58 against 8000 and 67 / 59 against 16000, 1000 tokens 26 / 60 against 1000 and
+// 67 / 61 against 4000; 48 tokens 44 / 67 against 32000, 155 / 152 against 128256;
+// 64 tokens 52 / 67 against 32000, 97 / 84 against 64000, 187 / 152 against
+// 128256. The no_skinny test knob keeps to the tiles.
+static int64_t few_groups(int64_t T) { return (T + kFewGroup - 1) / kFewGroup; }
+static bool few_tokens(int64_t T, int64_t V) {
+  if (test_knobs().no_skinny.load(std::memory_order_relaxed) != 0) return false;
+  return T <= (V < 224 * kBI ? 64 : 48) || few_groups(T) * ((V + 63) / 64) <= 512;
+}
 
 struct XentFew {
   const uint16_t* w;  // [V][D] (backward: a piece's rows), D a multiple of 8
   int64_t V;
   int D;
   XentHidden h;  // [T][D] (backward: the rows that count)
-  int T;
+  int T, groups;  // of kFewGroup tokens
   // forward
   const int64_t* targets;
   float2* part;  // [tiles][T]
@@ -503,12 +522,16 @@ __global__ __launch_bounds__(kWave * kFewWaves) void xent_few_kernel(XentFew a) 
   constexpr int W = kFewWaves, ROWS = 16 * FR;
   __shared__ f32x4_t red[W][TT][FR][kWave];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int64_t v0 = (int64_t)blockIdx.x * ROWS;
+  // the token groups of a tile of W run next to each other on an XCD
+  const int b = a.groups == 1 ? blockIdx.x : cta_order(blockIdx.x, gridDim.x);
+  const int tile = b / a.groups, t0 = (b - tile * a.groups) * kFewGroup;
+  const int64_t v0 = (int64_t)tile * ROWS;
   const int D = a.D, q = lane >> 4;
   const int rows = (int)(a.V - v0 < ROWS ? a.V - v0 : ROWS);
   const rsrc_t rw = make_rsrc(a.w + v0 * D, (uint32_t)(rows * D * 2));
   const int n = BWD ? a.ctl->n : a.T;
-  const rsrc_t rh = make_rsrc(a.h.rows(n), (uint32_t)(n * D * 2));
+  if (t0 >= n) return;
+  const rsrc_t rh = make_rsrc(a.h.rows(n) + (int64_t)t0 * D, (uint32_t)(min(n - t0, kFewGroup) * D * 2));
   const uint32_t row = (uint32_t)((lane & 15) * D * 2);  // rows past the end read as zeros
   f32x4_t acc[TT][FR];
 #pragma unroll
@@ -556,7 +579,7 @@ __global__ __launch_bounds__(kWave * kFewWaves) void xent_few_kernel(XentFew a) 
   __syncthreads();
   if (wave >= TT) return;
   // lane l: token l % 16 of the wave's group, rows 16 f + 4 (l / 16) + e
-  const int t = 16 * wave + (lane & 15);
+  const int t = t0 + 16 * wave + (lane & 15);
   f32x4_t z[FR];
 #pragma unroll
   for (int f = 0; f < FR; ++f) {
@@ -603,7 +626,7 @@ __global__ __launch_bounds__(kWave * kFewWaves) void xent_few_kernel(XentFew a) 
   s += __shfl_xor(s, 16, kWave);
   s += __shfl_xor(s, 32, kWave);
   if (t >= a.T) return;
-  if (q == 0) a.part[(int64_t)blockIdx.x * a.T + t] = make_float2(ref, s);
+  if (q == 0) a.part[(int64_t)tile * a.T + t] = make_float2(ref, s);
   const int64_t r = a.targets[t] - v0;
 #pragma unroll
   for (int f = 0; f < FR; ++f)
@@ -614,15 +637,16 @@ __global__ __launch_bounds__(kWave * kFewWaves) void xent_few_kernel(XentFew a) 
 
 // Rows of W a workgroup takes: with more than 16 tokens h's fragments are as
 // many bytes as W's, and 128 rows share them where that leaves enough
-// workgroups. Measured at D = 2560, 128 against 64 rows: 32 tokens 41.5 / 46.0
+// workgroups (all groups of tokens counted). Measured at D = 2560, 128 against 64 rows: 32 tokens 41.5 / 46.0
 // us against 32000 columns and 147 / 168 against 128256, but 29.7 / 20.5
-// against 8000; 64 tokens 52.9 / 59.8 against 32000 and 35.4 / 25.6 against 8000.
-static int few_rows(int64_t T, int64_t V) { return T > 16 && V >= 192 * 128 ? 128 : 64; }
+// against 8000; 64 tokens 52.9 / 59.8 against 32000 and 35.4 / 25.6 against 8000;
+// 256 tokens 37 / 44 against 8000.
+static int few_rows(int64_t T, int64_t V) { return T > 16 && few_groups(T) * V >= 192 * 128 ? 128 : 64; }
 static int64_t few_tiles(int64_t T, int64_t V) { return (V + few_rows(T, V) - 1) / few_rows(T, V); }
 
 template <bool BWD, int TT>
 static void few_at(const XentFew& f, hipStream_t st) {
-  const unsigned grid = (unsigned)few_tiles(f.T, f.V);
+  const unsigned grid = (unsigned)(few_tiles(f.T, f.V) * f.groups);
   if (few_rows(f.T, f.V) == 128) xent_few_kernel<BWD, TT, TT == 1 ? 4 : 8><<<grid, kWave * kFewWaves, 0, st>>>(f);
   else xent_few_kernel<BWD, TT, 4><<<grid, kWave * kFewWaves, 0, st>>>(f);
 }
@@ -911,6 +935,7 @@ hipError_t launch_xent_fwd(const uint16_t* h, const uint16_t* w, const int64_t* 
     f.D = (int)D;
     f.h = XentHidden{h, h, (int)T};
     f.T = (int)T;
+    f.groups = (int)few_groups(T);
     f.targets = targets;
     f.part = reinterpret_cast<float2*>(base);
     f.zt = reinterpret_cast<float*>(base + up(few_tiles(T, V) * 8 * T, 256));
@@ -1033,6 +1058,7 @@ hipError_t launch_xent_bwd(const uint16_t* h, const uint16_t* w, const int64_t* 
       f.D = a.Dp;
       f.h = a.h;
       f.T = r.T;
+      f.groups = (int)few_groups(T);
       f.ctl = a.ctl;
       f.ct = a.ct;
       f.lse2 = a.lse2;
