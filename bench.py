@@ -57,7 +57,7 @@ PEAK_HBM_GBS = 8000.0
 PAGES_L4_TOPS = 49.4
 HEADLINE = "c2_up_4096x2560x6912"
 
-KERNEL_SOURCES = ["gemm_kernels.hip", "skinny_kernels.hip", "quant_kernels.hip", "device_common.h"]
+KERNEL_SOURCES = ["gemm_core.h", "gemm_kernels.hip", "skinny_kernels.hip", "quant_kernels.hip", "device_common.h"]
 # the other layer workloads reported in the same line, and the 8-layer stack
 OTHER_WORKLOADS = ["c1_small", "c3_down_4096x6912x2560", "c5_skinny_32x6912x2560"]
 
