@@ -1,6 +1,7 @@
-"""The operators around the ternary layers in HIP graphs through their autograd
-functions: a training step captured once and replayed on other inputs has the
-bits of the same step run eagerly, and a capture that cannot work is refused."""
+"""The operators around the ternary layers as a program uses them: their autograd
+functions captured into HIP graphs, where a training step replayed on other
+inputs has the bits of the same step run eagerly and a capture that cannot work
+is refused; offsets past 2^31; two threads at once."""
 
 import pytest
 import torch
@@ -193,3 +194,80 @@ def test_a_capture_next_to_a_live_graph_of_the_default_stream_is_refused():
             graph.replay()
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_offsets_past_two_to_the_31():
+    """More than 2^31 values: the last rows have the bits of the same rows on
+    their own, forward and backward, and the columns' gradients those of the
+    rows that are not zero."""
+    from ternary_weight_quantization_amd import compress, decompress, gated_activation, layer_norm
+
+    note("2^31 + 20480 values")
+    M, K, n = (1 << 19) + 5, 4096, 7
+    x = torch.zeros(M, K, device="cuda", dtype=BF)
+    tail, dtail = randn(n, K, seed=40), randn(n, K, seed=41)
+    x[-n:] = tail
+    dy = torch.zeros_like(x)
+    dy[-n:] = dtail
+    x.requires_grad_(True)
+    w = randn(K, seed=42).requires_grad_(True)
+
+    for f in (lambda v: layer_norm(v, w), lambda v: layer_norm(v, w, checkpoint=True),
+              lambda v: gated_activation(v, v, "silu") + 0.0 * w, lambda v: gated_activation(v, None, "relu2", False) + 0.0 * w):
+        small = tail.clone().requires_grad_(True)
+        ys = f(small)
+        ds, dws = torch.autograd.grad(ys, (small, w), dtail)
+        y = f(x)
+        dx, dw = torch.autograd.grad(y, (x, w), dy)
+        assert torch.equal(y[-n:], ys) and torch.equal(dx[-n:], ds)
+        assert not dx[:-n].any()
+        # the sums over 2^19 rows of zeros and n others: the same n terms in fp32, in another order
+        assert (dw.double() - dws.double()).abs().max() <= 2.0 ** -7 * dws.double().abs().max()
+        del y, dx
+    codes, scales = compress(x)
+    cs, ss = compress(tail)
+    assert torch.equal(codes[-n:], cs) and torch.equal(scales[-n:], ss)
+    assert torch.equal(decompress(codes, scales, K)[-n:], decompress(cs, ss, K))
+
+
+def test_two_threads_at_once():
+    """Steps on two streams of two threads, with the bits of the same steps
+    one after the other."""
+    import threading
+
+    from ternary_weight_quantization_amd import gated_activation, layer_norm, linear_cross_entropy
+
+    note("two threads")
+
+    def step(seed):
+        x, w = randn(700, 512, seed=seed).requires_grad_(True), randn(512, seed=seed + 1).requires_grad_(True)
+        head = randn(3000, 256, seed=seed + 2).requires_grad_(True)
+        t = torch.randint(0, 3000, (700,), generator=torch.Generator().manual_seed(seed)).cuda()
+        t[::7] = -100
+        torch.cuda.current_stream().synchronize()
+        out = []
+        for _ in range(10):
+            h = layer_norm(x, w, checkpoint=True)
+            loss = linear_cross_entropy(gated_activation(h[:, :256], h[:, 256:]), head, t)
+            out.append((loss.detach(),) + torch.autograd.grad(loss, (x, w, head)))
+        return out
+
+    got = {}
+
+    def work(seed):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            got[seed] = step(seed)
+            s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(s,)) for s in (50, 60)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for seed in (50, 60):
+        want = step(seed)
+        torch.cuda.synchronize()
+        assert len(got[seed]) == 10
+        for a, b in zip(got[seed], want):
+            assert all(torch.equal(p, q) for p, q in zip(a, b))
