@@ -495,7 +495,7 @@ static bool few_tokens(int64_t T, int64_t V) {
 }
 
 struct XentFew {
-  const uint16_t* w;  // [V][D] (backward: a piece's rows), D a multiple of 8
+  const uint16_t* w;  // [V][D] (backward: a piece's rows, D a multiple of 8)
   int64_t V;
   int D;
   XentHidden h;  // [T][D] (backward: the rows that count)
@@ -516,8 +516,10 @@ struct XentFew {
 
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
-// TT groups of 16 tokens, FR fragments of 16 rows a tile.
-template <bool BWD, int TT, int FR>
+// TT groups of 16 tokens, FR fragments of 16 rows a tile. ODD: rows that are not
+// whole 16-byte chunks (D >= 8), read where they are: rows past the end repeat
+// the last one, whose results are not used.
+template <bool BWD, bool ODD, int TT, int FR>
 __global__ __launch_bounds__(kWave * kFewWaves) void xent_few_kernel(XentFew a) {
   constexpr int W = kFewWaves, ROWS = 16 * FR;
   __shared__ f32x4_t red[W][TT][FR][kWave];
@@ -544,6 +546,15 @@ __global__ __launch_bounds__(kWave * kFewWaves) void xent_few_kernel(XentFew a) 
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int k = 64 * s + 32 * c + 8 * q;
+      if constexpr (ODD) {
+#pragma unroll
+        for (int f = 0; f < FR; ++f)
+          pw[f][c] = load8<false>(a.w + v0 * D + min(16 * f + (lane & 15), rows - 1) * D, k, D).v;
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+          ph[t][c] = load8<false>(a.h.rows(n) + ((int64_t)t0 + min(16 * t + (lane & 15), n - t0 - 1)) * D, k, D).v;
+        continue;
+      }
       const uint32_t off = k < D ? row + 2 * k : kOob;  // columns past D: an out-of-range offset
 #pragma unroll
       for (int f = 0; f < FR; ++f) pw[f][c] = buf_load16(rw, off + (uint32_t)(32 * f * D));
@@ -560,6 +571,18 @@ __global__ __launch_bounds__(kWave * kFewWaves) void xent_few_kernel(XentFew a) 
       for (int f = 0; f < FR; ++f) cw[f][c] = pw[f][c];
 #pragma unroll
       for (int t = 0; t < TT; ++t) ch[t][c] = ph[t][c];
+      if constexpr (ODD) {
+        const int k = 64 * s + 32 * c + 8 * q;
+        const auto settle = [&](uint4& v) {
+          ChunkBf16 x{v};
+          settle8<false>(x, k, D);
+          v = x.v;
+        };
+#pragma unroll
+        for (int f = 0; f < FR; ++f) settle(cw[f][c]);
+#pragma unroll
+        for (int t = 0; t < TT; ++t) settle(ch[t][c]);
+      }
     }
     load(s + W);
 #pragma unroll
@@ -644,11 +667,21 @@ __global__ __launch_bounds__(kWave * kFewWaves) void xent_few_kernel(XentFew a) 
 static int few_rows(int64_t T, int64_t V) { return T > 16 && few_groups(T) * V >= 192 * 128 ? 128 : 64; }
 static int64_t few_tiles(int64_t T, int64_t V) { return (V + few_rows(T, V) - 1) / few_rows(T, V); }
 
-template <bool BWD, int TT>
+template <bool BWD, int TT, int FR>
 static void few_at(const XentFew& f, hipStream_t st) {
   const unsigned grid = (unsigned)(few_tiles(f.T, f.V) * f.groups);
-  if (few_rows(f.T, f.V) == 128) xent_few_kernel<BWD, TT, TT == 1 ? 4 : 8><<<grid, kWave * kFewWaves, 0, st>>>(f);
-  else xent_few_kernel<BWD, TT, 4><<<grid, kWave * kFewWaves, 0, st>>>(f);
+  if constexpr (!BWD) {  // the backward's rows are padded
+    if (f.D % 8 != 0) {
+      xent_few_kernel<false, true, TT, FR><<<grid, kWave * kFewWaves, 0, st>>>(f);
+      return;
+    }
+  }
+  xent_few_kernel<BWD, false, TT, FR><<<grid, kWave * kFewWaves, 0, st>>>(f);
+}
+template <bool BWD, int TT>
+static void few_at(const XentFew& f, hipStream_t st) {
+  if (few_rows(f.T, f.V) == 128) few_at<BWD, TT, TT == 1 ? 4 : 8>(f, st);
+  else few_at<BWD, TT, 4>(f, st);
 }
 template <bool BWD>
 static hipError_t launch_few(const XentFew& f, hipStream_t st) {
@@ -896,7 +929,7 @@ static XentPlan xent_plan(int64_t T, int64_t V, int64_t D, bool bwd) {
   return p;
 }
 
-static bool xent_few(int64_t T, int64_t V, int64_t D) { return few_tokens(T, V) && D % 8 == 0; }
+static bool xent_few(int64_t T, int64_t V, int64_t D) { return few_tokens(T, V) && D >= 8; }
 
 size_t xent_workspace(int64_t T, int64_t V, int64_t D, bool bwd) {
   if (!bwd && xent_few(T, V, D)) return (size_t)(up(few_tiles(T, V) * 8 * T, 256) + up(4 * T, 256));
