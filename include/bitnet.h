@@ -560,7 +560,8 @@ bitnet_status ttq_bwd_ckpt(const uint16_t* dY, const int8_t* codes, const float*
  * vocabulary (128 MiB at most, or 256 columns) and fp32 sums of dh.
  * Limits: T <= 2^21, V <= 2^28, D <= 65536, (T + 256) * 2 * (D rounded up to
  * 8) <= 2^31. Widths D that are multiples of 8 are fastest (others copy h,
- * and w a piece at a time, to padded rows first).
+ * and w a piece at a time, to padded rows first, but for the loss of few
+ * tokens).
  */
 typedef enum { BITNET_REDUCE_NONE = 0, BITNET_REDUCE_SUM = 1, BITNET_REDUCE_MEAN = 2 } bitnet_reduce;
 size_t bitnet_xent_fwd_workspace_bytes(int64_t T, int64_t V, int64_t D);

@@ -34,3 +34,11 @@ def test_either_side_groups_of_tokens(T):
     check(*make(T, 700, 200, seed=T))
     check(*make(T, 6500, 72, seed=T, ignored=T // 2), reduction="mean")
     check(*make(T, 333, 77, seed=T, ignored=3), reduction="sum")
+
+
+@pytest.mark.parametrize("T", [1, 16, 17, 33, 49, 64, 70, 200])
+@pytest.mark.parametrize("V,D", [(1, 9), (63, 203), (130, 2555), (2000, 77), (25000, 75)])
+def test_either_side_odd_widths(T, V, D):
+    """Rows that are not whole chunks, read in place by the loss, each number
+    of groups and both tile heights."""
+    check(*make(T, V, D, seed=T + V, ignored=T // 3), reduction="sum")
