@@ -63,8 +63,10 @@ Tensor aligned(const Tensor& t) {
 void check_backward() {
   TORCH_CHECK(!at::GradMode::is_enabled(), "this operator's gradients cannot be differentiated again");
   if (c10::hip::currentStreamCaptureStatusMayInitCtx() == c10::hip::CaptureStatus::None) return;
-  for (const torch::autograd::Edge& e : torch::autograd::get_current_node()->next_edges()) {
-    if (!e.is_valid()) continue;
+  const auto node = torch::autograd::get_current_node();
+  for (size_t i = 0; i < node->num_outputs(); ++i) {
+    const torch::autograd::Edge& e = node->next_edge(i);
+    if (!e.is_valid() || !node->task_should_compute_output(i)) continue;
     const optional<c10::Stream> s = e.function->stream();
     TORCH_CHECK(!s.has_value() || s->id() != c10::hip::getDefaultHIPStream(s->device_index()).id(),
                 "a backward pass is being captured whose gradient goes to a node of the default stream: free the "

@@ -196,6 +196,27 @@ def test_a_capture_next_to_a_live_graph_of_the_default_stream_is_refused():
             assert all(torch.equal(a, b) for a, b in zip(out, want))
 
 
+def test_a_capture_that_leaves_the_live_leaf_out():
+    """A live eager graph of a leaf whose gradient the captured pass does not
+    compute is no obstacle."""
+    from ternary_weight_quantization_amd import layer_norm
+
+    note("capture of the weight's gradient alone")
+    x, dy = randn(40, 128, seed=33).requires_grad_(True), randn(40, 128, seed=34)
+    w = randn(128, seed=35).requires_grad_(True)
+    eager = layer_norm(x)  # alive, of x alone
+
+    def step():
+        return torch.autograd.grad(layer_norm(x, w), (w,), dy)
+
+    graph, out = captured(step)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], step()[0])
+    assert eager.requires_grad
+
+
 def test_offsets_past_two_to_the_31():
     """More than 2^31 values: the last rows have the bits of the same rows on
     their own, forward and backward, and the columns' gradients those of the
