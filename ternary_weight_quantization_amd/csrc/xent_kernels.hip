@@ -366,6 +366,10 @@ struct XentLoss {
   int64_t ignore, V;
   float* lse;
   float* loss;
+  // one workgroup (up to kLossTokens tokens) also writes their sum or mean;
+  // NULL: not wanted, or xent_reduce_kernel does
+  float* total;
+  int mean;
 };
 
 // (m, s) += (m1, s1): sums of 2^ references; an empty one has m = -inf.
@@ -377,7 +381,8 @@ __device__ __forceinline__ void xent_join(float& m, float& s, float m1, float s1
 }
 
 // A block takes 16 tokens (a part's 16 pairs are one 128-byte line) and 64
-// groups of parts: 4 groups in a wave, joined by shuffles, then 16 waves.
+// groups of parts: 4 groups in a wave, joined by shuffles, then 16 waves. Up to
+// 16 tokens it also reduces their losses, without a launch for that.
 constexpr int kLossTokens = 16;
 __global__ __launch_bounds__(1024) void xent_combine_kernel(XentLoss a) {
   __shared__ float sm[16][kLossTokens], ss[16][kLossTokens];
@@ -413,17 +418,27 @@ __global__ __launch_bounds__(1024) void xent_combine_kernel(XentLoss a) {
     ss[threadIdx.x >> 6][l] = s;
   }
   __syncthreads();
-  if (threadIdx.x >= kLossTokens || t >= a.T) return;
-  if (!counts) {
-    a.lse[t] = 0.0f;
-    a.loss[t] = 0.0f;
-    return;
-  }
+  if (threadIdx.x >= kLossTokens) return;
+  float loss = 0.0f, lse = 0.0f;
+  if (counts) {
 #pragma unroll
-  for (int w = 1; w < 16; ++w) xent_join(m, s, sm[w][l], ss[w][l]);
-  const float lse = (m + __builtin_amdgcn_logf(s)) * kLn2;  // v_log_f32: base 2
-  a.lse[t] = lse;
-  a.loss[t] = target < 0 || target >= a.V ? __uint_as_float(0x7FC00000u) : lse - a.zt[at];
+    for (int w = 1; w < 16; ++w) xent_join(m, s, sm[w][l], ss[w][l]);
+    lse = (m + __builtin_amdgcn_logf(s)) * kLn2;  // v_log_f32: base 2
+    loss = target < 0 || target >= a.V ? __uint_as_float(0x7FC00000u) : lse - a.zt[at];
+  }
+  if (t < a.T) {
+    a.lse[t] = lse;
+    a.loss[t] = loss;
+  }
+  if (a.total == nullptr) return;
+  double v = (double)loss;
+  int n = counts ? 1 : 0;
+#pragma unroll
+  for (int off = 1; off < kLossTokens; off <<= 1) {
+    v += __shfl_xor(v, off, kWave);
+    n += __shfl_xor(n, off, kWave);
+  }
+  if (l == 0) *a.total = (float)(a.mean && n > 0 ? v / (double)n : v);
 }
 
 // The rows' sum or mean over the rows that count (0 where none does), in fp64
@@ -952,9 +967,13 @@ static hipError_t launch_pad(const uint16_t* w, int64_t rows, int64_t D, int64_t
 
 static hipError_t launch_loss(const XentLoss& l, const int64_t* targets, int64_t ignore, float* total, bool mean,
                               hipStream_t st) {
-  xent_combine_kernel<<<(l.T + kLossTokens - 1) / kLossTokens, 1024, 0, st>>>(l);
+  const bool together = l.T <= kLossTokens;
+  XentLoss a = l;
+  a.total = together ? total : nullptr;
+  a.mean = mean ? 1 : 0;
+  xent_combine_kernel<<<(l.T + kLossTokens - 1) / kLossTokens, 1024, 0, st>>>(a);
   if (hipError_t e = hipGetLastError()) return e;
-  if (total == nullptr) return hipSuccess;
+  if (total == nullptr || together) return hipSuccess;
   xent_reduce_kernel<<<1, 1024, 0, st>>>(l.loss, targets, ignore, l.T, mean ? 1 : 0, total);
   return hipGetLastError();
 }
@@ -975,7 +994,7 @@ hipError_t launch_xent_fwd(const uint16_t* h, const uint16_t* w, const int64_t* 
     f.part = reinterpret_cast<float2*>(base);
     f.zt = reinterpret_cast<float*>(base + up(few_tiles(T, V) * 8 * T, 256));
     if (hipError_t e = launch_few<false>(f, stream)) return e;
-    const XentLoss l{f.part, (int)few_tiles(T, V), (int)T, f.zt, nullptr, targets, ignore, V, lse, loss};
+    const XentLoss l{f.part, (int)few_tiles(T, V), (int)T, f.zt, nullptr, targets, ignore, V, lse, loss, nullptr, 0};
     return launch_loss(l, targets, ignore, total, mean, stream);
   }
   const XentPlan p = xent_plan(T, V, D, false);
@@ -1019,7 +1038,7 @@ hipError_t launch_xent_fwd(const uint16_t* h, const uint16_t* w, const int64_t* 
     xent_logits_kernel<false><<<(unsigned)(a.tiles_v * a.tiles_t), kThreads, 0, stream>>>(a);
     if (hipError_t e = hipGetLastError()) return e;
   }
-  const XentLoss l{a.part, (int)((V + 127) / 128), (int)T, a.zt, r.pos, targets, ignore, V, lse, loss};
+  const XentLoss l{a.part, (int)((V + 127) / 128), (int)T, a.zt, r.pos, targets, ignore, V, lse, loss, nullptr, 0};
   return launch_loss(l, targets, ignore, total, mean, stream);
 }
 
