@@ -10,8 +10,10 @@
 // Python took 130 us of host time a step (the autograd engine runs a GPU
 // node's backward on its own thread, where Python code runs cold).
 
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/hip/HIPGraphsC10Utils.h>
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/jit/frontend/tracer.h>
 #include <torch/extension.h>
 
 #include "bitnet.h"
@@ -74,6 +76,26 @@ void check_backward() {
   }
 }
 
+bool is_tracing() {
+  using c10::impl::TorchDispatchModeKey;
+  using c10::impl::TorchDispatchModeTLS;
+  if (torch::jit::tracer::isTracing()) return true;
+  if (!TorchDispatchModeTLS::any_modes_set()) return false;
+  for (const auto k : {TorchDispatchModeKey::FAKE, TorchDispatchModeKey::PROXY, TorchDispatchModeKey::FUNCTIONAL})
+    if (TorchDispatchModeTLS::get_mode(k).has_value()) return true;
+  return false;
+}
+
+// What every function refuses: being traced (the kernels' launches are in no
+// trace, which would hold the allocation of the outputs alone) and a tangent of
+// forward-mode differentiation (which would be dropped).
+void check_eager(const char* what, std::initializer_list<const Tensor*> ts) {
+  TORCH_CHECK_NOT_IMPLEMENTED(!is_tracing(), what, ": cannot be traced");
+  if (!c10::AutogradState::get_tls_state().get_fw_grad_mode()) return;
+  for (const Tensor* t : ts)
+    TORCH_CHECK_NOT_IMPLEMENTED(!t->defined() || !t->_fw_grad(0).defined(), what, ": no forward-mode derivative");
+}
+
 bool wants_grad(std::initializer_list<const Tensor*> ts) {
   if (!at::GradMode::is_enabled()) return false;
   for (const Tensor* t : ts)
@@ -94,6 +116,7 @@ std::pair<Tensor, Tensor> empty_codes(int64_t M, int64_t K, const Tensor& like) 
 }
 
 std::pair<Tensor, Tensor> compress(const Tensor& x) {
+  check_eager("compress", {&x});
   TORCH_CHECK_TYPE(is_value(x.scalar_type()), "compress expects bf16 or float32, got ", x.scalar_type());
   check_activation("compress", x);
   at::NoGradGuard off;
@@ -108,6 +131,7 @@ std::pair<Tensor, Tensor> compress(const Tensor& x) {
 }
 
 Tensor decompress(const Tensor& codes, const Tensor& scales, int64_t K, at::ScalarType dtype) {
+  check_eager("decompress", {&scales});
   TORCH_CHECK_TYPE(is_value(dtype), "decompress gives bf16 or float32, not ", dtype);
   TORCH_CHECK_TYPE(codes.scalar_type() == at::kChar && scales.scalar_type() == at::kFloat,
                    "codes: expected int8 and scales float32, got ", codes.scalar_type(), " and ", scales.scalar_type());
@@ -201,10 +225,11 @@ struct LayerNormFn : torch::autograd::Function<LayerNormFn> {
 
 Tensor layer_norm(const Tensor& x, const optional<Tensor>& weight, const optional<Tensor>& bias, double eps,
                   at::ScalarType out, bool checkpoint) {
+  const Tensor w = weight.value_or(Tensor()), b = bias.value_or(Tensor());
+  check_eager("layer_norm", {&x, &w, &b});
   TORCH_CHECK_TYPE(is_value(x.scalar_type()), "layer_norm expects bf16 or float32 activations, got ", x.scalar_type());
   TORCH_CHECK_TYPE(is_value(out), "out_dtype: expected bfloat16 or float32, got ", out);
   check_activation("layer_norm", x);
-  const Tensor w = weight.value_or(Tensor()), b = bias.value_or(Tensor());
   for (const Tensor* p : {&w, &b}) {
     if (!p->defined()) continue;
     TORCH_CHECK_TYPE(is_value(p->scalar_type()), "weight and bias: expected bf16 or float32, got ", p->scalar_type());
@@ -313,6 +338,7 @@ struct GateFn : torch::autograd::Function<GateFn> {
 
 Tensor gated_activation(const Tensor& gate, const optional<Tensor>& up, int64_t act, bool checkpoint) {
   const Tensor u = up.value_or(Tensor());
+  check_eager("gated_activation", {&gate, &u});
   TORCH_CHECK_TYPE(gate.scalar_type() == at::kBFloat16 && (!u.defined() || u.scalar_type() == at::kBFloat16),
                    "gated_activation expects bf16 activations");
   TORCH_CHECK_VALUE(!u.defined() || u.sizes() == gate.sizes(), "up: expected shape ", gate.sizes(), ", got ",
@@ -372,6 +398,7 @@ struct TtqFn : torch::autograd::Function<TtqFn> {
 };
 
 Tensor ttq_linear_checkpoint(const Tensor& x, const Tensor& weight, const Tensor& params) {
+  check_eager("ttq_linear", {&x, &weight, &params});
   TORCH_CHECK_TYPE(x.scalar_type() == at::kBFloat16, "TTQ expects bf16 activations");
   TORCH_CHECK_TYPE(is_value(weight.scalar_type()), "weight: expected bf16 or float32, got ", weight.scalar_type());
   check_activation("ttq_linear", x);
@@ -436,6 +463,7 @@ struct XentFn : torch::autograd::Function<XentFn> {
 
 Tensor linear_cross_entropy(const Tensor& hidden, const Tensor& weight, const Tensor& targets, int64_t ignore,
                             int64_t reduce) {
+  check_eager("linear_cross_entropy", {&hidden, &weight});
   TORCH_CHECK_TYPE(hidden.scalar_type() == at::kBFloat16, "linear_cross_entropy expects bf16 hidden states, got ",
                    hidden.scalar_type());
   TORCH_CHECK_TYPE(is_value(weight.scalar_type()), "weight: expected bf16 or float32, got ", weight.scalar_type());
