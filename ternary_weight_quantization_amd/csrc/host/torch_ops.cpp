@@ -87,13 +87,19 @@ bool is_tracing() {
 }
 
 // What every function refuses: being traced (the kernels' launches are in no
-// trace, which would hold the allocation of the outputs alone) and a tangent of
-// forward-mode differentiation (which would be dropped).
+// trace, which would hold the allocation of the outputs alone), a tangent of
+// forward-mode differentiation (which would be dropped) and tensors without
+// memory, such as fake, functional and wrapped ones: what data_ptr() gives of
+// a fake one is its offset in bytes, which a kernel would read as an address.
 void check_eager(const char* what, std::initializer_list<const Tensor*> ts) {
   TORCH_CHECK_NOT_IMPLEMENTED(!is_tracing(), what, ": cannot be traced");
-  if (!c10::AutogradState::get_tls_state().get_fw_grad_mode()) return;
-  for (const Tensor* t : ts)
-    TORCH_CHECK_NOT_IMPLEMENTED(!t->defined() || !t->_fw_grad(0).defined(), what, ": no forward-mode derivative");
+  const bool forward = c10::AutogradState::get_tls_state().get_fw_grad_mode();
+  for (const Tensor* t : ts) {
+    if (!t->defined()) continue;
+    TORCH_CHECK_NOT_IMPLEMENTED(!forward || !t->_fw_grad(0).defined(), what, ": no forward-mode derivative");
+    TORCH_CHECK_NOT_IMPLEMENTED(t->has_storage() && (t->numel() == 0 || t->storage().data() != nullptr), what,
+                                ": a tensor without memory");
+  }
 }
 
 bool wants_grad(std::initializer_list<const Tensor*> ts) {
@@ -131,7 +137,7 @@ std::pair<Tensor, Tensor> compress(const Tensor& x) {
 }
 
 Tensor decompress(const Tensor& codes, const Tensor& scales, int64_t K, at::ScalarType dtype) {
-  check_eager("decompress", {&scales});
+  check_eager("decompress", {&codes, &scales});
   TORCH_CHECK_TYPE(is_value(dtype), "decompress gives bf16 or float32, not ", dtype);
   TORCH_CHECK_TYPE(codes.scalar_type() == at::kChar && scales.scalar_type() == at::kFloat,
                    "codes: expected int8 and scales float32, got ", codes.scalar_type(), " and ", scales.scalar_type());
@@ -463,7 +469,7 @@ struct XentFn : torch::autograd::Function<XentFn> {
 
 Tensor linear_cross_entropy(const Tensor& hidden, const Tensor& weight, const Tensor& targets, int64_t ignore,
                             int64_t reduce) {
-  check_eager("linear_cross_entropy", {&hidden, &weight});
+  check_eager("linear_cross_entropy", {&hidden, &weight, &targets});
   TORCH_CHECK_TYPE(hidden.scalar_type() == at::kBFloat16, "linear_cross_entropy expects bf16 hidden states, got ",
                    hidden.scalar_type());
   TORCH_CHECK_TYPE(is_value(weight.scalar_type()), "weight: expected bf16 or float32, got ", weight.scalar_type());

@@ -1,7 +1,8 @@
 """What the operators around the layers refuse of torch's transformations,
 without a GPU: a tangent of forward-mode differentiation (with and without
-requires_grad, under no_grad) and every kind of trace. Each refusal comes before
-the checks of devices."""
+requires_grad, under no_grad), every kind of trace, and tensors that have no
+memory, whose data pointers are no addresses. Each refusal comes before the
+checks of devices."""
 
 import pytest
 import torch
@@ -74,3 +75,30 @@ def test_modes_that_only_look_on():
     for _, f, a in calls():
         with FlopCounterMode(display=False), pytest.raises(ValueError):
             f(a)
+
+
+def without_memory(a):
+    """Tensors like a that have none: fake ones outside their mode, at an
+    offset too, functional ones and those of other devices' metadata."""
+    from torch._subclasses import FakeTensorMode
+
+    with FakeTensorMode():
+        fake = torch.empty((2 * a.shape[0],) + a.shape[1:], dtype=a.dtype)
+        halves = [fake[:a.shape[0]], fake[a.shape[0]:]]
+    return halves + [torch._to_functional_tensor(torch.cat([a, a]))[a.shape[0]:], torch.empty_like(a, device="meta")]
+
+
+def test_tensors_without_memory():
+    for name, f, a in calls():
+        for b in without_memory(a):
+            with pytest.raises(NotImplementedError, match=f"{name}: a tensor without memory"):
+                f(b)
+
+
+@pytest.mark.parametrize("transform", ["grad", "vjp", "vmap", "functionalize"])
+def test_function_transforms(transform):
+    for name, f, a in calls():
+        run = {"grad": lambda: torch.func.grad(lambda b: f(b).float().sum())(a), "vjp": lambda: torch.func.vjp(f, a),
+               "vmap": lambda: torch.vmap(f)(torch.stack([a, a])), "functionalize": lambda: torch.func.functionalize(f)(a)}
+        with pytest.raises(NotImplementedError, match=f"{name}: a tensor without memory"):
+            run[transform]()
