@@ -16,6 +16,9 @@
 #include <torch/csrc/jit/frontend/tracer.h>
 #include <torch/extension.h>
 
+#include <unordered_set>
+#include <vector>
+
 #include "bitnet.h"
 
 namespace {
@@ -59,20 +62,27 @@ Tensor aligned(const Tensor& t) {
 }
 
 // What every backward refuses: a second derivative, and being captured into a
-// graph while a gradient goes on to a node of the default stream, which no
-// capture can take in. Such a node is the accumulator of a leaf of which a
-// graph made on the default stream is still alive.
+// graph while a gradient goes on to a node of the default stream, at once or
+// through other nodes (a view, a module's parametrization), which no capture
+// can take in. Such a node is the accumulator of a leaf of which a graph made
+// on the default stream is still alive, or one made there before the capture.
 void check_backward() {
   TORCH_CHECK(!at::GradMode::is_enabled(), "this operator's gradients cannot be differentiated again");
   if (c10::hip::currentStreamCaptureStatusMayInitCtx() == c10::hip::CaptureStatus::None) return;
-  const auto node = torch::autograd::get_current_node();
-  for (size_t i = 0; i < node->num_outputs(); ++i) {
-    const torch::autograd::Edge& e = node->next_edge(i);
-    if (!e.is_valid() || !node->task_should_compute_output(i)) continue;
-    const optional<c10::Stream> s = e.function->stream();
-    TORCH_CHECK(!s.has_value() || s->id() != c10::hip::getDefaultHIPStream(s->device_index()).id(),
-                "a backward pass is being captured whose gradient goes to a node of the default stream: free the "
-                "results of earlier calls that use the same leaves (or make them on another stream) first");
+  std::vector<const torch::autograd::Node*> todo{torch::autograd::get_current_node().get()};
+  std::unordered_set<const torch::autograd::Node*> seen(todo.begin(), todo.end());
+  while (!todo.empty()) {
+    const torch::autograd::Node* node = todo.back();
+    todo.pop_back();
+    for (size_t i = 0; i < node->num_outputs(); ++i) {
+      const torch::autograd::Edge& e = node->next_edge(i);
+      if (!e.is_valid() || !node->task_should_compute_output(i)) continue;
+      const optional<c10::Stream> s = e.function->stream();
+      TORCH_CHECK(!s.has_value() || s->id() != c10::hip::getDefaultHIPStream(s->device_index()).id(),
+                  "a backward pass is being captured whose gradient goes to a node of the default stream: free the "
+                  "results of earlier calls that use the same leaves (or make them on another stream) first");
+      if (seen.insert(e.function.get()).second) todo.push_back(e.function.get());
+    }
   }
 }
 

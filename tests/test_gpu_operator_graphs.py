@@ -292,3 +292,52 @@ def test_two_threads_at_once():
         assert len(got[seed]) == 10
         for a, b in zip(got[seed], want):
             assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_a_capture_whose_gradient_reaches_the_default_stream_through_other_nodes_is_refused():
+    """Between the operator and the leaf whose eager graph is alive stand a
+    view (states of three dimensions), a module's parametrization (the TTQ
+    layer's softplus), another of the operators, or nodes that were made on the
+    default stream before the capture."""
+    from ternary_weight_quantization_amd import gated_activation, layer_norm, linear_cross_entropy
+    from ternary_weight_quantization_amd.ttq_layer import TTQLinear
+
+    torch.manual_seed(0)
+    h = randn(4, 10, 128, seed=36).requires_grad_(True)
+    head, w = randn(256, 128, seed=37), randn(128, seed=38)
+    t = torch.arange(40, device="cuda").view(4, 10)
+    ttq, x = TTQLinear(128, 256, checkpoint=True), randn(40, 128, seed=39)
+    for name, f, leaves in (("states of three dimensions", lambda: linear_cross_entropy(h, head, t), (h,)),
+                            ("a parametrization", lambda: ttq(x), (ttq.raw,)),
+                            ("a product", lambda: layer_norm(h * 2, w), (h,)),
+                            ("halves", lambda: gated_activation(h[..., :64], h[..., 64:]), (h,)),
+                            ("norm and loss", lambda: linear_cross_entropy(layer_norm(h.view(40, 128), w), head, t.view(40)),
+                             (h,))):
+        note(f"refused capture through {name}")
+
+        def step():
+            y = f()
+            return torch.autograd.grad(y, leaves, torch.ones_like(y))
+
+        eager = f()  # alive, made on the default stream
+        graph = torch.cuda.CUDAGraph()
+        with pytest.raises(RuntimeError, match="default stream"):
+            with torch.cuda.graph(graph):
+                step()
+        torch.cuda.synchronize()
+        want = torch.autograd.grad(eager, leaves, torch.ones_like(eager))
+        del eager, graph
+        graph, out = captured(step)
+        for _ in range(3):
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+    note("refused capture of a node made before it")
+    early = h.view(40, 128)
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(RuntimeError, match="default stream"):
+        with torch.cuda.graph(graph):
+            y = layer_norm(early, w)
+            torch.autograd.grad(y, (h,), torch.ones_like(y))
+    torch.cuda.synchronize()
