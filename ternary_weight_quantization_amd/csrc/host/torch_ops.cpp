@@ -375,6 +375,10 @@ struct TtqFn : torch::autograd::Function<TtqFn> {
     std::vector<int64_t> shape = x.sizes().vec();
     shape.back() = N;
     Tensor y = at::empty(shape, x.options());
+    ctx->saved_data["x"] = x.sizes();
+    ctx->saved_data["wt"] = static_cast<int64_t>(weight.scalar_type());
+    ctx->saved_data["n"] = N;
+    if (M == 0) return y;
     const Tensor codes_w = at::empty({N, Kp / 4}, x.options().dtype(at::kByte)), wt = at::empty({N, Kp}, x.options());
     const size_t bytes = ttq_fwd_ckpt_workspace_bytes(M, N, K);
     const Tensor ws = scratch(bytes, x);
@@ -385,21 +389,27 @@ struct TtqFn : torch::autograd::Function<TtqFn> {
                        on.stream));
     check(ttq_fwd_ckpt(bf16(x2), bf16(wt), M, N, K, bf16(y), i8(codes), f32(scales), ptr(ws), bytes, on.stream));
     ctx->save_for_backward({codes, scales, wt, codes_w});
-    ctx->saved_data["x"] = x.sizes();
-    ctx->saved_data["wt"] = static_cast<int64_t>(weight.scalar_type());
     return y;
   }
 
   static variable_list backward(AutogradContext* ctx, const variable_list& grads) {
     check_backward();
-    const variable_list saved = ctx->get_saved_variables();
-    const Tensor &codes = saved[0], &scales = saved[1], &wt = saved[2], &codes_w = saved[3];
     const std::vector<int64_t> shape = ctx->saved_data["x"].toIntVector();
     const auto wdt = static_cast<at::ScalarType>(ctx->saved_data["wt"].toInt());
-    const Tensor dY = aligned(rows(grads[0].to(at::kBFloat16)));
-    const int64_t M = dY.size(0), N = dY.size(1), K = shape.back();
+    const int64_t K = shape.back(), N = ctx->saved_data["n"].toInt();
     const bool need_x = ctx->needs_input_grad(0), need_w = ctx->needs_input_grad(1), need_p = ctx->needs_input_grad(2);
     Tensor dX, dW, dp;
+    if (grads[0].numel() == 0) {  // no rows
+      const auto o = grads[0].options();
+      if (need_x) dX = at::empty(shape, o.dtype(at::kBFloat16));
+      if (need_w) dW = at::zeros({N, K}, o.dtype(wdt));
+      if (need_p) dp = at::zeros({3}, o.dtype(at::kFloat));
+      return {dX, dW, dp, Tensor()};
+    }
+    const variable_list saved = ctx->get_saved_variables();
+    const Tensor &codes = saved[0], &scales = saved[1], &wt = saved[2], &codes_w = saved[3];
+    const Tensor dY = aligned(rows(grads[0].to(at::kBFloat16)));
+    const int64_t M = dY.size(0);
     if (need_x) dX = at::empty(shape, dY.options());
     // the scales' gradients come from dW's epilogue; the threshold has none
     if (need_w || need_p) dW = at::empty({N, K}, dY.options().dtype(wdt));

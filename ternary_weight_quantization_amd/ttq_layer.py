@@ -67,7 +67,7 @@ class TTQFunction(torch.autograd.Function):
     """y = x @ W_t^T with W_t from Eq. 1. x [..., K] bf16, weight [N, K] bf16
     or float32, params float32 [3] = (delta, Wp, Wn), already positive.
     Gradients: dX bf16, dW in the weight's dtype, d params =
-    (0, dL/dWp, dL/dWn) (the threshold gets none)."""
+    (0, dL/dWp, dL/dWn) (the threshold gets none). x may have no rows."""
 
     @staticmethod
     def forward(ctx, x, weight, params):
@@ -78,20 +78,26 @@ class TTQFunction(torch.autograd.Function):
         x2 = x.reshape(-1, K).contiguous()
         M = x2.shape[0]
         params = params.detach().to(torch.float32).contiguous()
-        w_packed, wt = ttq_quantize(weight.detach(), params)
         y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        ctx.shape = (M, N, K, lead, weight.dtype)
+        if M == 0:
+            return y.reshape(*lead, N)
+        w_packed, wt = ttq_quantize(weight.detach(), params)
         ws = _workspace(B.ttq_workspace_bytes(M, N, K), x.device)
         B.ttq_fwd(x2, wt, y, workspace=ws)
         ctx.save_for_backward(x2, wt, w_packed)
-        ctx.shape = (M, N, K, lead, weight.dtype)
         return y.reshape(*lead, N)
 
     @staticmethod
     def backward(ctx, dy):
-        x2, wt, w_packed = ctx.saved_tensors
         M, N, K, lead, wdtype = ctx.shape
-        dY = dy.reshape(M, N).to(torch.bfloat16).contiguous()
         need_x, need_w, need_p = ctx.needs_input_grad[:3]
+        if M == 0:
+            return (dy.new_empty((*lead, K), dtype=torch.bfloat16) if need_x else None,
+                    dy.new_zeros((N, K), dtype=wdtype) if need_w else None,
+                    dy.new_zeros((3,), dtype=torch.float32) if need_p else None)
+        x2, wt, w_packed = ctx.saved_tensors
+        dY = dy.reshape(M, N).to(torch.bfloat16).contiguous()
         dX = torch.empty((M, K), dtype=torch.bfloat16, device=dy.device) if need_x else None
         # the scale gradients come from dW's epilogue, so dW is computed
         # whenever either is needed

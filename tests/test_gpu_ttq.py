@@ -394,3 +394,25 @@ def test_ttq_export_and_forward_codes():
         C.check(y.float().cpu().numpy(), y_ref.float().cpu().numpy().astype(np.float64), "y_ttq")
         if M == 200:  # the same GEMM on the same values
             assert torch.equal(y.view(torch.int16), y_ref.view(torch.int16))
+
+
+@pytest.mark.parametrize("checkpoint", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("shape", [(0, 96), (3, 0, 96)])
+def test_no_rows(checkpoint, dtype, shape):
+    """An empty batch passes: an empty y and dX, zeros for the rest, and zeros
+    added to gradients that are there."""
+    from ternary_weight_quantization_amd.ttq_layer import TTQLinear
+
+    m = TTQLinear(96, 40, dtype=dtype, checkpoint=checkpoint)
+    x = torch.empty(shape, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    y = m(x)
+    assert y.shape == shape[:-1] + (40,) and y.dtype == torch.bfloat16
+    y.sum().backward()
+    assert x.grad.shape == shape
+    for p in (m.weight, m.raw):
+        assert p.grad.dtype == p.dtype and torch.equal(p.grad, torch.zeros_like(p))
+    with torch.no_grad():
+        assert m(x).shape == y.shape
+    only_x, = torch.autograd.grad(m(x), x, torch.empty_like(y))
+    assert only_x.shape == shape
