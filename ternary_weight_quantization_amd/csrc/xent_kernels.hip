@@ -267,7 +267,8 @@ __device__ __forceinline__ void xent_stats(const XentTiles& a, const XentTokens&
       for (int e = 0; e < 16; ++e) s[e & 3] += __builtin_amdgcn_exp2f(fmaf(acc[fi][fj][e], kLog2e, -ref));
     float sum = (s[0] + s[1]) + (s[2] + s[3]);
     sum += __shfl_xor(sum, 32, kWave);
-    if (j < n && lane < 32) a.part[(int64_t)((a.v0 + i0) / kWTI) * a.T + j] = make_float2(ref, sum);
+    if (j < n && lane < 32)
+      a.part[(int64_t)((a.v0 + i0) / kWTI) * a.T + j] = make_float2(m == -INFINITY ? m : ref, sum);
     if (t >= 0 && t < kWTI && j < n && ((t >> 2) & 1) == (lane >> 5)) {  // rare
 #pragma unroll
       for (int fi = 0; fi < kFI; ++fi)
@@ -372,10 +373,14 @@ struct XentLoss {
   int mean;
 };
 
-// (m, s) += (m1, s1): sums of 2^ references; an empty one has m = -inf.
+// (m, s) += (m1, s1): sums of 2^ references. One that is empty, or of logits
+// that are all -inf, has m = -inf and s = 0, or NaN if a logit is.
 __device__ __forceinline__ void xent_join(float& m, float& s, float m1, float s1) {
   const float top = fmaxf(m, m1);
-  if (top == -INFINITY) return;
+  if (top == -INFINITY) {
+    s += s1;
+    return;
+  }
   s = s * __builtin_amdgcn_exp2f(m - top) + s1 * __builtin_amdgcn_exp2f(m1 - top);
   m = top;
 }
@@ -666,7 +671,7 @@ __global__ __launch_bounds__(kWave * kFewWaves) void xent_few_kernel(XentFew a) 
   s += __shfl_xor(s, 16, kWave);
   s += __shfl_xor(s, 32, kWave);
   if (t >= a.T) return;
-  if (q == 0) a.part[(int64_t)tile * a.T + t] = make_float2(ref, s);
+  if (q == 0) a.part[(int64_t)tile * a.T + t] = make_float2(top == -INFINITY ? top : ref, s);
   const int64_t r = a.targets[t] - v0;
 #pragma unroll
   for (int f = 0; f < FR; ++f)

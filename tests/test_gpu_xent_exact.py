@@ -1,0 +1,95 @@
+"""Linear layer with softmax cross entropy where the logits are exact: small
+integers and powers of two, whose products and sums fp32 holds without a
+rounding, so that what is left are the operator's own steps.
+
+u = 2^-24 (half an fp32 step); a rounding to bf16 is off by at most 2^-8 of the
+value.
+"""
+
+import pytest
+import torch
+
+from tests.gpu_util import note
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+U = 2.0 ** -24
+H = 2.0 ** -8
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.fail("no GPU visible")
+    from ternary_weight_quantization_amd import binding
+    binding.lib()
+
+
+def ints(*shape, low, high, seed):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randint(low, high + 1, shape, generator=g).to(device="cuda", dtype=F32)
+
+
+def softmax64(h, w, t):
+    z = torch.mm(h.double(), w.double().t().contiguous())
+    lse = torch.logsumexp(z, 1)
+    return z, lse, z.gather(1, t[:, None])[:, 0]
+
+
+@pytest.mark.parametrize("tiles", [0, 1])
+@pytest.mark.parametrize("T", [9, 40, 130])
+@pytest.mark.parametrize("level", [-500.0, -80.0, 0.0, 60.0])
+def test_columns_of_minus_infinity(T, level, tiles, set_knobs):
+    """Columns whose logits overflow to -inf, whole statistics blocks of 64 and
+    128 of them, count as nothing, however low the others are. The loss is off
+    by the additions of the sum of 300 exponentials (64 + 25 of them: 89 u), the
+    exponentials (2 u times their arguments' size of up to 10, and 4 u) and the
+    differences of logits around `level` (4 roundings)."""
+    from ternary_weight_quantization_amd.loss import linear_cross_entropy
+
+    note(f"columns of -inf T={T} level={level} tiles={tiles}")
+    set_knobs(no_skinny=tiles)
+    V, D = 700, 16
+    h = torch.ones(T, D, device="cuda", dtype=BF)
+    w = ints(V, D, low=-1, high=1, seed=T) / 4 + level / D
+    off = torch.zeros(V, dtype=torch.bool, device="cuda")
+    off[64:192] = off[256:512] = off[690:] = True
+    w[off] = -3e38
+    w = w.to(BF)
+    keep = (~off).nonzero()[:, 0]
+    t = keep[torch.arange(T, device="cuda") * 7 % len(keep)]
+    z = torch.mm(h.double(), w.double().t().contiguous())
+    lse = torch.logsumexp(z[:, keep], 1)
+    want = lse - z.gather(1, t[:, None])[:, 0]
+    hs, ws = h.clone().requires_grad_(True), w.clone().requires_grad_(True)
+    loss = linear_cross_entropy(hs, ws, t, reduction="none")
+    tol = (89 + 24) * U + 8 * U * (abs(level) + 10)
+    assert ((loss.double() - want).abs() <= tol).all(), (loss.double() - want).abs().max().item()
+    dh, dw = torch.autograd.grad(loss, (hs, ws), torch.ones_like(loss))
+    assert not dw[off].any() and torch.isfinite(dh.float()).all()
+    G = (z - lse[:, None]).exp()
+    G.scatter_add_(1, t[:, None], -torch.ones(T, 1, device="cuda", dtype=torch.float64))
+    G = G[:, keep]
+    rdh, rdw, wd = torch.mm(G, w[keep].double()), torch.mm(G.t().contiguous(), h.double()), w[keep].double().abs()
+    rel = H + 2 * tol + (V + 64) * 2 * U  # of |G| + p, which bounds both parts of the target's element
+    size = G.abs() + 2 * (z[:, keep] - lse[:, None]).exp()
+    assert ((dh.double() - rdh).abs() <= H * rdh.abs() + rel * torch.mm(size, wd)).all()
+    assert ((dw[keep].double() - rdw).abs() <= H * rdw.abs() + rel * torch.mm(size.t().contiguous(), h.double())).all()
+
+
+@pytest.mark.parametrize("tiles", [0, 1])
+def test_nan_among_columns_of_minus_infinity(tiles, set_knobs):
+    from ternary_weight_quantization_amd.loss import linear_cross_entropy
+
+    note(f"NaN among columns of -inf, tiles={tiles}")
+    set_knobs(no_skinny=tiles)
+    h = torch.ones(40, 16, device="cuda", dtype=BF)
+    w = ints(700, 16, low=-1, high=1, seed=3)
+    w[256:512] = -3e38
+    w[300, 2] = float("nan")
+    t = torch.arange(40, device="cuda")
+    assert torch.isnan(linear_cross_entropy(h, w.to(BF), t, reduction="none")).all()
+    # no column left
+    w[:] = -3e38
+    assert torch.isnan(linear_cross_entropy(h, w.to(BF), t, reduction="none")).all()
