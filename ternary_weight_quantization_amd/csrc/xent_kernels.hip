@@ -196,7 +196,7 @@ struct XentTiles {
   const XentCtl* ctl;
   const int* ct;
   // forward
-  float2* part;  // [2 tiles of 128 columns][T]: reference in base 2, sum
+  float2* part;  // [2 tiles of 128 columns][T]: maximum, sum
   int T;
   float* zt;     // [n] the target's logit
   // backward
@@ -243,9 +243,11 @@ __device__ __forceinline__ void xent_mask(AccTile& acc, int rows, int lane) {
 }
 
 // Forward epilogue of a wave's 128 columns (from i0 of the piece) x 128 tokens
-// (from j0; the tile's token qj): the maximum M of z log2(e) and the sum of
-// 2^(z log2(e) - M) per token, over both lanes that hold a token. M is the
-// rounded product, the same in every term, so the pair means sum 2^M exactly.
+// (from j0; the tile's token qj): the maximum m of z and the sum of e^(z - m)
+// per token, over both lanes that hold a token. The difference is taken before
+// it is scaled for the base 2: it is exact near the maximum and 0 there, so
+// that the sum is at least 1 and its logarithm at least 0 (a rounded m log2(e)
+// as the reference left its own rounding in the loss, 1e-4 at logits of 1500).
 __device__ __forceinline__ void xent_stats(const XentTiles& a, const XentTokens& tok, AccTile& acc, int i0, int j0,
                                            int qj, int n, int lane) {
   xent_mask(acc, a.vc - i0, lane);
@@ -259,16 +261,15 @@ __device__ __forceinline__ void xent_stats(const XentTiles& a, const XentTokens&
 #pragma unroll
       for (int e = 0; e < 16; ++e) m = fmaxf(m, acc[fi][fj][e]);
     m = fmaxf(m, __shfl_xor(m, 32, kWave));
-    const float ref = m == -INFINITY ? 0.0f : m * kLog2e;
+    const float ref = m == -INFINITY ? 0.0f : m;
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // four chains
 #pragma unroll
     for (int fi = 0; fi < kFI; ++fi)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) s[e & 3] += __builtin_amdgcn_exp2f(fmaf(acc[fi][fj][e], kLog2e, -ref));
+      for (int e = 0; e < 16; ++e) s[e & 3] += __builtin_amdgcn_exp2f((acc[fi][fj][e] - ref) * kLog2e);
     float sum = (s[0] + s[1]) + (s[2] + s[3]);
     sum += __shfl_xor(sum, 32, kWave);
-    if (j < n && lane < 32)
-      a.part[(int64_t)((a.v0 + i0) / kWTI) * a.T + j] = make_float2(m == -INFINITY ? m : ref, sum);
+    if (j < n && lane < 32) a.part[(int64_t)((a.v0 + i0) / kWTI) * a.T + j] = make_float2(m, sum);
     if (t >= 0 && t < kWTI && j < n && ((t >> 2) & 1) == (lane >> 5)) {  // rare
 #pragma unroll
       for (int fi = 0; fi < kFI; ++fi)
@@ -373,7 +374,7 @@ struct XentLoss {
   int mean;
 };
 
-// (m, s) += (m1, s1): sums of 2^ references. One that is empty, or of logits
+// (m, s) += (m1, s1): sums of exponentials over e^m. One that is empty, or of logits
 // that are all -inf, has m = -inf and s = 0, or NaN if a logit is.
 __device__ __forceinline__ void xent_join(float& m, float& s, float m1, float s1) {
   const float top = fmaxf(m, m1);
@@ -381,7 +382,7 @@ __device__ __forceinline__ void xent_join(float& m, float& s, float m1, float s1
     s += s1;
     return;
   }
-  s = s * __builtin_amdgcn_exp2f(m - top) + s1 * __builtin_amdgcn_exp2f(m1 - top);
+  s = s * __builtin_amdgcn_exp2f((m - top) * kLog2e) + s1 * __builtin_amdgcn_exp2f((m1 - top) * kLog2e);
   m = top;
 }
 
@@ -428,8 +429,11 @@ __global__ __launch_bounds__(1024) void xent_combine_kernel(XentLoss a) {
   if (counts) {
 #pragma unroll
     for (int w = 1; w < 16; ++w) xent_join(m, s, sm[w][l], ss[w][l]);
-    lse = (m + __builtin_amdgcn_logf(s)) * kLn2;  // v_log_f32: base 2
-    loss = target < 0 || target >= a.V ? __uint_as_float(0x7FC00000u) : lse - a.zt[at];
+    // the loss takes the difference of the two logits, not that of the rounded
+    // lse: 0 for a target that is all of the sum
+    const float log_s = __builtin_amdgcn_logf(s);  // v_log_f32: base 2
+    lse = fmaf(log_s, kLn2, m);
+    loss = target < 0 || target >= a.V ? __uint_as_float(0x7FC00000u) : fmaf(log_s, kLn2, m - a.zt[at]);
   }
   if (t < a.T) {
     a.lse[t] = lse;
@@ -659,19 +663,19 @@ __global__ __launch_bounds__(kWave * kFewWaves) void xent_few_kernel(XentFew a) 
       if (16 * f + 4 * q + e < rows) top = fmaxf(top, z[f][e]);
   top = fmaxf(top, __shfl_xor(top, 16, kWave));
   top = fmaxf(top, __shfl_xor(top, 32, kWave));
-  const float ref = top == -INFINITY ? 0.0f : top * kLog2e;
+  const float ref = top == -INFINITY ? 0.0f : top;
   float s = 0.0f;
 #pragma unroll
   for (int f = 0; f < FR; ++f)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float p = __builtin_amdgcn_exp2f(fmaf(z[f][e], kLog2e, -ref));
+      const float p = __builtin_amdgcn_exp2f((z[f][e] - ref) * kLog2e);
       if (16 * f + 4 * q + e < rows) s += p;
     }
   s += __shfl_xor(s, 16, kWave);
   s += __shfl_xor(s, 32, kWave);
   if (t >= a.T) return;
-  if (q == 0) a.part[(int64_t)tile * a.T + t] = make_float2(top == -INFINITY ? top : ref, s);
+  if (q == 0) a.part[(int64_t)tile * a.T + t] = make_float2(top, s);
   const int64_t r = a.targets[t] - v0;
 #pragma unroll
   for (int f = 0; f < FR; ++f)

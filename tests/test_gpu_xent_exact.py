@@ -3,7 +3,13 @@ integers and powers of two, whose products and sums fp32 holds without a
 rounding, so that what is left are the operator's own steps.
 
 u = 2^-24 (half an fp32 step); a rounding to bf16 is off by at most 2^-8 of the
-value.
+value. With m a row's largest logit and s = sum_v exp(z_v - m) >= 1,
+  loss = (m - z_target) + log s
+A difference of such logits is exact. Its exponential is off by the rounding of
+the argument (2 u |z_v - m|) and 4 u. A target that is the largest makes the
+loss log s alone: it is never below 0, and where s is 1 plus one term e, it is
+off by the rounding of s (u), the logarithm (2 u near 1) and e's own error: 8 u
+in all.
 """
 
 import pytest
@@ -29,6 +35,22 @@ def _gpu():
 def ints(*shape, low, high, seed):
     g = torch.Generator().manual_seed(seed)
     return torch.randint(low, high + 1, shape, generator=g).to(device="cuda", dtype=F32)
+
+
+def confident(T, V, scale, gaps, seed):
+    """Rows whose target's logit is about 770 scale, far above every other but,
+    for gaps > 0, one that is gaps[t] below it; D = 64."""
+    D = 64
+    h = ints(T, D, low=1, high=2, seed=seed) * torch.where(ints(T, D, low=0, high=1, seed=seed + 1) > 0, 1.0, -1.0)
+    h[:, 0] = 1.0
+    w = ints(V, D, low=-1, high=1, seed=seed + 2)
+    t = torch.randperm(V // 2, generator=torch.Generator().manual_seed(seed + 3))[:T].cuda()
+    w[t] = torch.where(h > 0, 1.0, -1.0) * 8.0 * scale
+    near = gaps > 0
+    w[V // 2 + t[near]] = w[t[near]]
+    w[V // 2 + t[near], 0] -= gaps[near]
+    assert torch.equal(w.to(BF).float(), w) and torch.equal(h.to(BF).float(), h)
+    return h.to(BF), w.to(BF), t
 
 
 def softmax64(h, w, t):
@@ -93,3 +115,26 @@ def test_nan_among_columns_of_minus_infinity(tiles, set_knobs):
     # no column left
     w[:] = -3e38
     assert torch.isnan(linear_cross_entropy(h, w.to(BF), t, reduction="none")).all()
+
+
+@pytest.mark.parametrize("tiles", [0, 1])
+@pytest.mark.parametrize("T,V", [(12, 500), (40, 500), (300, 3000)])
+@pytest.mark.parametrize("scale", [0.125, 1.0, 2.0])
+def test_confident_rows(T, V, scale, tiles, set_knobs):
+    """Logits of 100, 770 and 1540: the loss of a row whose target takes all
+    is 0, of one with a rival d below it log(1 + e^-d)."""
+    from ternary_weight_quantization_amd.loss import linear_cross_entropy
+
+    note(f"confident rows T={T} V={V} scale={scale} tiles={tiles}")
+    set_knobs(no_skinny=tiles)
+    gaps = (torch.arange(T, device="cuda") % 13).float()  # 0: no rival
+    h, w, t = confident(T, V, scale, gaps, seed=T)
+    z, lse, zt = softmax64(h, w, t)
+    assert (zt == z.amax(1)).all()
+    true = torch.log1p(torch.where(gaps > 0, torch.exp(-gaps.double()), 0.0))
+    assert (lse - zt - true).abs().max() < 1e-9
+    loss = linear_cross_entropy(h, w, t, reduction="none")
+    assert (loss >= 0).all(), loss.min().item()
+    err = (loss.double() - true).abs()
+    assert (err <= 8 * U).all(), (err.max() / U).item()
+    assert not loss[gaps == 0].any()
