@@ -83,7 +83,7 @@ struct XentRows {
   const float* lse;        // [T]
   const float* dloss;      // [1], or [T] with per_row
   int per_row, mean;
-  float* lse2;             // [T] lse log2(e) of the rows that count
+  float* lsec;             // [T] lse of the rows that count
   float* c;                // [T] what G's rows are multiplied by
 };
 
@@ -138,7 +138,7 @@ __global__ __launch_bounds__(256) void xent_gather_kernel(XentRows a, int groups
         a.ct[at] = in ? (int)target : -1;
         if constexpr (BWD) {
           const float c = a.per_row ? a.dloss[t] : 1.0f;
-          a.lse2[at] = a.lse[t] * kLog2e;
+          a.lsec[at] = a.lse[t];
           a.c[at] = in ? c : __uint_as_float(0x7FC00000u);  // a target out of range: NaN gradients
         }
       }
@@ -200,7 +200,7 @@ struct XentTiles {
   int T;
   float* zt;     // [n] the target's logit
   // backward
-  const float* lse2;
+  const float* lsec;
   const float* c;
   uint16_t* G;   // [n][ldg]
   int ldg;
@@ -224,10 +224,10 @@ typedef MfmaBf16::Acc AccTile[kFI][kFJ];
 
 // What the epilogues need of a tile's 256 tokens, staged in LDS before the main
 // loop: the target's row within the tile (out of 0..255 where it is elsewhere)
-// and, backward, lse log2(e) and c.
+// and, backward, lse and c.
 struct XentTokens {
   int target[kBJ];
-  float lse2[kBJ], c[kBJ];
+  float lse[kBJ], c[kBJ];
 };
 
 // Rows past the piece count as logits of -inf: 2^-inf is 0.
@@ -282,7 +282,9 @@ __device__ __forceinline__ void xent_stats(const XentTiles& a, const XentTokens&
 
 // Backward epilogue: G of the tile, rounded to bf16 (the operand of both
 // products; the rounding, 2^-9 of each value, is the size of the outputs'
-// own), zeros in the columns past the piece.
+// own), zeros in the columns past the piece. As in the forward the difference
+// of z and lse is taken before it is scaled, so that p of a target that takes
+// nearly all is off by lse's one rounding.
 __device__ __forceinline__ void xent_g(const XentTiles& a, const XentTokens& tok, AccTile& acc, int i0, int j0, int qj,
                                        int n, int lane, char* wlds) {
   xent_mask(acc, a.vc - i0, lane);
@@ -290,14 +292,14 @@ __device__ __forceinline__ void xent_g(const XentTiles& a, const XentTokens& tok
   for (int fj = 0; fj < kFJ; ++fj) {
     const int at = qj + 32 * fj + (lane & 31);
     const int t = tok.target[at] - i0 % kBI;
-    const float c = tok.c[at], l = tok.lse2[at];
+    const float c = tok.c[at], l = tok.lse[at];
 #pragma unroll
     for (int fi = 0; fi < kFI; ++fi)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         float v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = __builtin_amdgcn_exp2f(fmaf(acc[fi][fj][4 * g + e], kLog2e, -l)) * c;
+        for (int e = 0; e < 4; ++e) v[e] = __builtin_amdgcn_exp2f((acc[fi][fj][4 * g + e] - l) * kLog2e) * c;
         EpStage<2>::put(wlds, lane, fi, g, make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])));
       }
     if (t >= 0 && t < kWTI && ((t >> 2) & 1) == (lane >> 5)) {  // rare: the target is one of this lane's rows
@@ -307,7 +309,7 @@ __device__ __forceinline__ void xent_g(const XentTiles& a, const XentTokens& tok
 #pragma unroll
         for (int e = 0; e < 16; ++e)
           if (t == 32 * fi + row_of(e, lane)) z = acc[fi][fj][e];
-      const float v = (__builtin_amdgcn_exp2f(fmaf(z, kLog2e, -l)) - 1.0f) * c;
+      const float v = (__builtin_amdgcn_exp2f((z - l) * kLog2e) - 1.0f) * c;
       const uint16_t bits = f32_to_bf16_bits(v);
       memcpy(wlds + (lane & 31) * EpStage<2>::kPitch + 2 * t, &bits, 2);
     }
@@ -336,7 +338,7 @@ __global__ __launch_bounds__(kThreads, 1) void xent_logits_kernel(XentTiles a) {
     const int r = j < n ? a.ct[j] : -1;
     tok.target[t] = r >= a.v0 + i0 && r < a.v0 + min(a.vc, i0 + kBI) ? r - a.v0 - i0 : -kBI;
     if constexpr (BWD) {
-      tok.lse2[t] = j < n ? a.lse2[j] : 0.0f;
+      tok.lse[t] = j < n ? a.lsec[j] : 0.0f;
       tok.c[t] = j < n ? a.c[j] : 0.0f;
     }
   }
@@ -531,7 +533,7 @@ struct XentFew {
   // backward: G for the piece that starts at column v0
   const XentCtl* ctl;
   const int* ct;
-  const float* lse2;
+  const float* lsec;
   const float* c;
   int v0;
   uint16_t* G;
@@ -638,7 +640,7 @@ __global__ __launch_bounds__(kWave * kFewWaves) void xent_few_kernel(XentFew a) 
   }
   if constexpr (BWD) {  // G, zeros in the rows past the piece that G's pitch holds
     if (t >= n) return;
-    const float c = a.c[t], l = a.lse2[t];
+    const float c = a.c[t], l = a.lsec[t];
     const int r = a.ct[t] - a.v0 - (int)v0;
 #pragma unroll
     for (int f = 0; f < FR; ++f) {
@@ -646,7 +648,7 @@ __global__ __launch_bounds__(kWave * kFewWaves) void xent_few_kernel(XentFew a) 
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int i = 16 * f + 4 * q + e;
-        const float p = __builtin_amdgcn_exp2f(fmaf(z[f][e], kLog2e, -l));
+        const float p = __builtin_amdgcn_exp2f((z[f][e] - l) * kLog2e);
         g[e] = i < rows ? (i == r ? p - 1.0f : p) * c : 0.0f;
       }
       if (v0 + 16 * f + 4 * q < a.ldg)
@@ -907,7 +909,7 @@ constexpr int64_t kReach = int64_t(1) << 31;
 
 struct XentPlan {
   int64_t Dp, tiles;    // tiles of columns per piece
-  int64_t pos, ct, hc, part, zt, lse2, c, G, slab, pad, total;  // byte offsets
+  int64_t pos, ct, hc, part, zt, lsec, c, G, slab, pad, total;  // byte offsets
   int64_t ldg, split;
   bool padded;          // W's pieces are copied first
 };
@@ -935,7 +937,7 @@ static XentPlan xent_plan(int64_t T, int64_t V, int64_t D, bool bwd) {
     p.part = take((V + 127) / 128 * 8 * T + 8 * T);
     p.zt = take(4 * T);
   } else {
-    p.lse2 = take(4 * T);
+    p.lsec = take(4 * T);
     p.c = take(4 * T);
     p.ldg = std::min(p.tiles * kBI, up(V, 64));
     p.G = take(2 * T * p.ldg);
@@ -1072,7 +1074,7 @@ hipError_t launch_xent_bwd(const uint16_t* h, const uint16_t* w, const int64_t* 
   r.dloss = dloss;
   r.per_row = per_row ? 1 : 0;
   r.mean = mean ? 1 : 0;
-  r.lse2 = reinterpret_cast<float*>(base + p.lse2);
+  r.lsec = reinterpret_cast<float*>(base + p.lsec);
   r.c = reinterpret_cast<float*>(base + p.c);
   launch_gather<true>(r, stream);
   if (hipError_t e = hipGetLastError()) return e;
@@ -1082,7 +1084,7 @@ hipError_t launch_xent_bwd(const uint16_t* h, const uint16_t* w, const int64_t* 
   a.ctl = r.ctl;
   a.ct = r.ct;
   a.T = r.T;
-  a.lse2 = r.lse2;
+  a.lsec = r.lsec;
   a.c = r.c;
   a.G = reinterpret_cast<uint16_t*>(base + p.G);
   a.ldg = (int)p.ldg;
@@ -1124,7 +1126,7 @@ hipError_t launch_xent_bwd(const uint16_t* h, const uint16_t* w, const int64_t* 
       f.groups = (int)few_groups(T);
       f.ctl = a.ctl;
       f.ct = a.ct;
-      f.lse2 = a.lse2;
+      f.lsec = a.lsec;
       f.c = a.c;
       f.v0 = a.v0;
       f.G = a.G;

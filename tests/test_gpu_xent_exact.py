@@ -9,7 +9,8 @@ A difference of such logits is exact. Its exponential is off by the rounding of
 the argument (2 u |z_v - m|) and 4 u. A target that is the largest makes the
 loss log s alone: it is never below 0, and where s is 1 plus one term e, it is
 off by the rounding of s (u), the logarithm (2 u near 1) and e's own error: 8 u
-in all.
+in all. p_v = exp(z_v - lse) of the backward is further off by the rounding of
+lse = m + log s to fp32, u |lse|.
 """
 
 import pytest
@@ -138,3 +139,37 @@ def test_confident_rows(T, V, scale, tiles, set_knobs):
     err = (loss.double() - true).abs()
     assert (err <= 8 * U).all(), (err.max() / U).item()
     assert not loss[gaps == 0].any()
+
+
+@pytest.mark.parametrize("tiles", [0, 1])
+@pytest.mark.parametrize("T,V", [(12, 500), (40, 500), (300, 3000)])
+@pytest.mark.parametrize("scale", [0.125, 1.0, 2.0])
+def test_gradients_of_confident_rows(T, V, scale, tiles, set_knobs):
+    """Logits of 100, 770 and 1540: the gradient of a row whose target takes all
+    is 0, those of rows with a rival are off by p u |lse|, the exponentials'
+    4 u |z - lse| + 8 u and G's rounding. An exponential, its product with c = 1
+    and G's bf16 value below 2^-126, the least normal number, may become 0:
+    each loses at most 2^-126, together less than 2^-124."""
+    from ternary_weight_quantization_amd.loss import linear_cross_entropy
+
+    note(f"gradients of confident rows T={T} V={V} scale={scale} tiles={tiles}")
+    set_knobs(no_skinny=tiles)
+    gaps = (torch.arange(T, device="cuda") % 13).float()  # 0: no rival
+    h, w, t = confident(T, V, scale, gaps, seed=T)
+    z, lse, zt = softmax64(h, w, t)
+    assert (zt == z.amax(1)).all()
+    hs, ws = h.clone().requires_grad_(True), w.clone().requires_grad_(True)
+    loss = linear_cross_entropy(hs, ws, t, reduction="none")
+    dh, dw = torch.autograd.grad(loss, (hs, ws), torch.ones_like(loss))
+    p = (z - lse[:, None]).exp()
+    G = p.clone()
+    G.scatter_add_(1, t[:, None], -torch.ones(T, 1, device="cuda", dtype=torch.float64))
+    eg = H * G.abs() + p * (U * lse.abs()[:, None] + 4 * U * (z - lse[:, None]).abs() + 8 * U) + 2.0 ** -124
+    rdh, rdw = torch.mm(G, w.double()), torch.mm(G.t().contiguous(), h.double())
+    edh = H * rdh.abs() + torch.mm(eg, w.double().abs()) + (V + 64) * 2 * U * torch.mm(G.abs(), w.double().abs())
+    edw = H * rdw.abs() + torch.mm(eg.t().contiguous(), h.double().abs()) + (T + 64) * 2 * U * torch.mm(
+        G.abs().t().contiguous(), h.double().abs())
+    assert ((dh.double() - rdh).abs() <= edh + 2.0 ** -126).all(), ((dh.double() - rdh).abs() / edh).max().item()
+    assert ((dw.double() - rdw).abs() <= edw + 2.0 ** -126).all()
+    # no rival: every other logit is at least 50 below, and V e^-50 times |w| <= 16 is below 1e-15
+    assert dh[gaps == 0].abs().max() <= 1e-15
