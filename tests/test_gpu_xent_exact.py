@@ -173,3 +173,57 @@ def test_gradients_of_confident_rows(T, V, scale, tiles, set_knobs):
     assert ((dw.double() - rdw).abs() <= edw + 2.0 ** -126).all()
     # no rival: every other logit is at least 50 below, and V e^-50 times |w| <= 16 is below 1e-15
     assert dh[gaps == 0].abs().max() <= 1e-15
+
+
+@pytest.mark.parametrize("D", [4096, 4097])
+def test_weight_past_two_gigabytes_every_gradient(D):
+    """A weight and a dW whose bytes pass 32-bit offsets, in a width that is read
+    in place and in one that is padded, every value of dh and dW checked. The
+    logits are exact multiples of 1/8, so that the bounds hold G's and the
+    outputs' roundings, the exponentials and the sums alone: the loss is off by
+    V / 2048 + 120 additions of u and the terms' 2 u |z - m| + 4 u with |z - m| <
+    120, p by what the header says, dh and dW by V + 64 and T + 64 additions of
+    2 u. The bounds are small beside the values: zeros, or another row's, fail."""
+    from ternary_weight_quantization_amd.loss import linear_cross_entropy
+
+    V, T, step = 270001, 70, 30000
+    note(f"xent past 2 GiB T={T} V={V} D={D}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(D)
+    w = torch.empty(V, D, device="cuda", dtype=BF)
+    for v in range(0, V, step):
+        w[v:v + step] = torch.randint(-2, 3, (min(step, V - v), D), generator=g, device="cuda").to(BF) / 8
+    h = torch.randint(-1, 2, (T, D), generator=g, device="cuda").to(BF)
+    t = torch.randint(0, V, (T,), generator=g, device="cuda")
+    t[0], t[1], t[2] = V - 1, 0, 262144
+    hd = h.double()
+    chunks = [(v, min(step, V - v)) for v in range(0, V, step)]
+    z = torch.cat([torch.mm(hd, w[v:v + n].double().t().contiguous()) for v, n in chunks], 1)
+    assert torch.equal(z * 8, (z * 8).round()) and (z.amax(1) - z.amin(1)).max() < 120 and w.numel() * 2 > 2 ** 31
+    lse = torch.logsumexp(z, 1)
+    want = lse - z.gather(1, t[:, None])[:, 0]
+    tol = (V / 2048 + 120 + 2 * 120 + 4) * U + 4 * U * want.abs()
+    hs, ws = h.requires_grad_(True), w.requires_grad_(True)
+    loss = linear_cross_entropy(hs, ws, t, reduction="none")
+    few = linear_cross_entropy(h[:9].detach(), w.detach(), t[:9], reduction="none")
+    assert ((loss.double() - want).abs() <= tol).all() and ((few.double() - want[:9]).abs() <= tol[:9]).all()
+    dh, dw = torch.autograd.grad(loss, (hs, ws), torch.ones_like(loss))
+    with torch.no_grad():
+        G = z.sub_(lse[:, None])
+        eg = 4 * U * G.abs() + (U * lse.abs()[:, None] + 8 * U) + tol[:, None]
+        eg *= G.exp_()
+        G.scatter_add_(1, t[:, None], -torch.ones(T, 1, device="cuda", dtype=torch.float64))
+        eg += H * G.abs() + 2.0 ** -124
+        rdh, edh = torch.zeros(T, D, device="cuda", dtype=torch.float64), torch.zeros(T, D, device="cuda", dtype=torch.float64)
+        for v, n in chunks:
+            wd, Gv, ev = w[v:v + n].double(), G[:, v:v + n].contiguous(), eg[:, v:v + n].contiguous()
+            rdh += torch.mm(Gv, wd)
+            edh += torch.mm(ev + (V + 64) * 2 * U * Gv.abs(), wd.abs())
+            rdw = torch.mm(Gv.t().contiguous(), hd)
+            edw = H * rdw.abs() + torch.mm((ev + (T + 64) * 2 * U * Gv.abs()).t().contiguous(), hd.abs())
+            assert ((dw[v:v + n].double() - rdw).abs() <= edw + 2.0 ** -126).all(), v
+        edh += H * rdh.abs()
+        assert ((dh.double() - rdh).abs() <= edh).all()
+        assert (edh <= 0.1 * rdh.abs()).double().mean() > 0.5  # how sharp the bound is, not the kernel
+        at = G.gather(1, t[:, None]).abs() * hd.abs()  # |dW| at the targets' rows is about this
+        assert (eg.gather(1, t[:, None]) <= 0.01 * at.amax(1, keepdim=True)).all()
