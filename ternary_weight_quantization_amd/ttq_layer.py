@@ -126,6 +126,8 @@ class TTQLinear(torch.nn.Module):
     the library (Eq. 2). checkpoint=True: the input is kept in 8 bits for the
     backward instead of in bf16."""
 
+    checkpoint = False  # of modules pickled before it was an attribute
+
     def __init__(self, in_features, out_features, device="cuda", dtype=torch.bfloat16, checkpoint=False):
         super().__init__()
         self.checkpoint = checkpoint
