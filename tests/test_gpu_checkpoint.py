@@ -352,3 +352,44 @@ def test_checkpointed_block():
     for a, b in zip(*got):
         a, b = a.double(), b.double()
         assert (a - b).norm() <= 0.1 * a.norm()
+
+
+@pytest.mark.parametrize("wt", [BF, F32])
+@pytest.mark.parametrize("M,K,N", [(512, 1001, 2001), (1024, 2555, 1025), (640, 1285, 1283)])
+def test_ttq_checkpoint_odd_widths_in_the_paired_launch(M, K, N, wt):
+    """Widths that are padded, at sizes whose two products run in one launch
+    (stated by the profiler's kernel names), everything exact: integers, with
+    127 in each block so that the codes are the values, scales of 1/2, sums
+    below 2^24. dX and a bf16 dW are rounded once; an fp32 dW is equal."""
+    from torch.profiler import ProfilerActivity, profile
+
+    from ternary_weight_quantization_amd.ttq_layer import ttq_linear
+
+    note(f"ttq checkpoint, padded pair M={M} K={K} N={N} {wt}")
+    g = torch.Generator().manual_seed(M)
+    x = torch.randint(-8, 9, (M, K), generator=g).float()
+    x[:, ::128] = 127.0
+    dy = torch.randint(-2, 3, (M, N), generator=g).float()
+    q = torch.randint(-1, 2, (N, K), generator=g).float()
+    x, dy = (t.to(device="cuda", dtype=BF) for t in (x, dy))
+    q = q.cuda()
+    x.requires_grad_(True)
+    w, p = q.to(wt).requires_grad_(True), torch.tensor([0.25, 0.5, 0.5], device="cuda", requires_grad=True)
+    y = ttq_linear(x, w, p, checkpoint=True)
+    first = torch.autograd.grad(y, (x, w, p), dy, retain_graph=True)
+    torch.cuda.synchronize()
+    with profile(activities=[ProfilerActivity.CPU, ProfilerActivity.CUDA]) as trace:
+        dx, dw, dp = torch.autograd.grad(y, (x, w, p), dy)
+        torch.cuda.synchronize()
+    names = " ".join(e.key for e in trace.key_averages())
+    assert "gemm_pair_kernel" in names and "pad_rows_kernel" in names, names
+    assert all(torch.equal(a, b) for a, b in zip(first, (dx, dw, dp)))
+    xd, dd, qd = x.detach().double(), dy.double(), q.double()
+    rdx, rdw = torch.mm(dd, qd) / 2, torch.mm(dd.t().contiguous(), xd)
+    assert rdw.abs().max() < 2 ** 24 and rdx.abs().max() < 2 ** 24
+    assert torch.equal(y, (torch.mm(xd, qd.t().contiguous()) / 2).to(BF))
+    assert torch.equal(dx, rdx.to(BF)) and torch.equal(dw, rdw.to(wt))
+    for got, mask, sign in ((dp[1], qd == 1, 1.0), (dp[2], qd == -1, -1.0)):
+        ref = sign * rdw[mask].sum()
+        assert abs(got.double() - ref) <= U * abs(ref)
+    assert dp[0] == 0
