@@ -533,7 +533,9 @@ bitnet_status ttq_bwd_ckpt(const uint16_t* dY, const int8_t* codes, const float*
  *
  *   z[t,v]  = sum_d h[t,d] * w[v,d]
  *   lse[t]  = log sum_v exp z[t,v]
- *   loss[t] = lse[t] - z[t,target[t]]    (0 where target[t] == ignore_index)
+ *   loss[t] = lse[t] - z[t,target[t]]    (0 where target[t] == ignore_index),
+ *             taken as (m - z[t,target[t]]) + log sum_v exp(z[t,v] - m) with m the
+ *             largest logit: 0 for a target that is all of the sum
  *   total   = sum_t loss[t], or the mean over the rows that count (0 if none)
  *
  *   G[t,v]  = c[t] * (exp(z[t,v] - lse[t]) - [v == target[t]])

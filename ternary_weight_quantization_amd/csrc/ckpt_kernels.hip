@@ -6,8 +6,8 @@
 // Everything here is one pass over HBM: a block of 128 values is 16 lanes of
 // 8, its scale is a rotation maximum within a DPP row, and a lane's 8 codes
 // are one 8-byte store. Measured at 4096 x 6912 with gate, up and both codes:
-// forward 43.8 us (228 MB, 5.2 TB/s), backward 37.9 us (228 MB, some of it from
-// the last level cache); 2048 x 2560 packed in 5.7 us and unpacked in 6.3.
+// forward 46.5 us (228 MB, 4.9 TB/s), backward 37.8 us (228 MB, some of it from
+// the last level cache); 2048 x 2560 packed in 6.2 us and unpacked in 6.8.
 
 #include "internal.h"
 #include "row_io.h"

@@ -5,9 +5,12 @@
 //   g  = dY w,  c1 = sum g / K,  c2 = sum g xh / K
 //   dX = r (g - c1 - xh c2),  dw = sum over rows dY xh,  db = sum over rows dY
 //
-// A row lives in the registers of TPR threads (CPT chunks of 8 values each),
-// so x is read once forward and once backward and the variance is the sum of
-// centered squares. Statistics and sums are fp32. With 8-bit codes the
+// A row of up to 16384 values lives in the registers of TPR threads (CPT chunks
+// of 8 values each), so x is read once forward and once backward and the
+// variance is the sum of centered squares. Wider rows do too, but with 5 to 8
+// chunks in each of 512 threads the backward no longer fits the registers
+// beside its column sums (6 to 310 spilled, at most 936 bytes of scratch a
+// thread), nor does the forward from 7 chunks on (f32: 6; up to 223 spilled). Statistics and sums are fp32. With 8-bit codes the
 // forward also writes the row's codes and block scales (row_io.h), and the
 // backward takes x from them; mu and r are those of the uncoded row.
 //
@@ -17,11 +20,17 @@
 // partial row [2][K]; a second launch adds the partial rows in block order.
 // No atomics: the same inputs give the same bits.
 //
-// About 10 operations a value, so HBM bounds both directions. Measured,
-// forward / backward / column sums in us: 16384 x 6912 bf16 with codes
-// 117 / 124 / 5.5 (4.9 and 4.6 TB/s, a copy reaches 5.2), 4096 x 2560 bf16
-// 10.9 / 18.1 / 4.4 (operands partly in the last level cache), 2048 x 6912 f32
-// 18.4 / 31.1 / 5.3 (4.6 and 4.5 TB/s), one row of 2560 3.9.
+// About 10 operations a value, so HBM bounds both directions of long
+// problems. Measured, forward / backward / column sums in us, traced back to
+// back: 16384 x 6912 bf16 with codes 130 / 133 / 6.0 (4.4 and 4.3 TB/s, a copy
+// reaches 5.2; 244 for all three among other work), 2048 x 6912 f32 17.9 /
+// 31.2 / 5.3 (4.7 and 4.5 TB/s), 4096 x 16384 bf16 61 / 91 / 6.7, one row of
+// 2560 3.7. Short problems pay for each block's start and end, the weight to
+// LDS, its rows' sums and a partial row, whatever the width: 4096 x 2560 bf16
+// 11.0 / 18.0 / 4.3 (a copy of its bytes: 8 and 12), 1537 x 2560 with codes
+// 10.1 / 13.9 / 3.9 and 1537 x 2555 11.0 / 14.3 / 3.9. Where registers spill
+// the scratch traffic bounds the backward: 4096 x 24576 bf16 67 / 434 / 9.0, f32
+// 144 / 821 / 9.2, 2048 x 32768 bf16 110 / 516 / 11.
 
 #include <algorithm>
 #include <type_traits>
@@ -440,7 +449,8 @@ __global__ __launch_bounds__(1024) void layernorm_cols_kernel(const float* __res
 // ---------------------------------------------------------------------------
 // Launches. Threads per row and chunks per thread from the row length alone:
 // one wave (no barriers) up to five chunks a thread, two waves for three, four
-// up to four chunks, eight above (kNormMaxK). Measured, forward and backward in
+// up to four chunks, eight above, up to the eight chunks of kNormMaxK (no other
+// split was tried above 8192). Measured, forward and backward in
 // us, without / with codes: 32768 x 1536 one wave 102 / 102, two 121 / 136;
 // 16384 x 2560 one wave 84 / 93, two 86 / 96, four 112 / 130; 16384 x 2900 one
 // wave (six chunks) 138 / 155, two 104 / 108; 8192 x 4096 four waves 72 / 81,

@@ -16,11 +16,13 @@
 // logits computed again, because keeping them would take 4TV bytes (2 GB at
 // 4096 x 128256). For few tokens the loss is bound by reading W once.
 //
-// Rows whose target is ignore_index are taken out first: the rows that count
-// are gathered to the front (hc), so that an ignored row costs nothing and
-// nothing it holds, NaN included, reaches a sum. The number n of rows that
-// count stays on the device; tiles past it leave at once. Where all T rows
-// count and need no padding, nothing is copied and h is read in place.
+// With tiles and in the backward rows whose target is ignore_index are taken
+// out first: the rows that count are gathered to the front (hc), so that an
+// ignored row costs nothing there. The number n of rows that count stays on the
+// device; tiles past it leave at once. Where all T rows count and need no
+// padding, nothing is copied and h is read in place. The few-token loss gathers
+// nothing: an ignored row's logits are computed and not used. Either way
+// nothing an ignored row holds, NaN included, reaches a sum.
 //
 // Many tokens:
 //   gather   rows, targets, (backward) lse and c of the rows that count
@@ -38,11 +40,11 @@
 //            to the rows; ignored rows get zeros
 // No atomics: the same inputs give the same bits.
 //
-// Measured in us: 4096 tokens, 128256 columns, D = 2560: logits forward 2208
-// (1218 TFLOP/s; this card's best library product alone, which writes the
-// logits, takes 2024), backward logits 8 x 287, grads 8 x 547 (1229 TFLOP/s;
-// the two products as library calls 377 + 393), gather 6, combine 11, dh 13.
-// 1000 tokens of which 750 count, 50257 columns: 230 + 240 + 470 with 591
+// Measured in us: 4096 tokens, 128256 columns, D = 2560: logits forward 2177
+// (1235 TFLOP/s; this card's best library product alone, which writes the
+// logits, takes 2024), backward logits 8 x 287, grads 8 x 537 (1252 TFLOP/s;
+// the two products as library calls 377 + 393), gather 6, combine 12, dh 12.
+// 1000 tokens of which 750 count, 50257 columns: 201 + 204 + 405 with 591
 // tiles of logits on 256 CUs (three rounds for 2.3 of work) and dW tiles of 12
 // stages. Workgroups that stay for every 256th tile and load the next one
 // during the last stages of the current one were 5 % slower.
@@ -90,9 +92,11 @@ struct XentRows {
 constexpr int kGatherRows = 4;  // at a time: one for each of the block's waves
 
 // Each block finds how many rows that count precede its own and how many
-// there are by reading all targets (a few KB out of L2), so that no launch
-// or wait between blocks is needed. `groups` of kGatherRows rows a block: more
-// with many rows, which keeps the reading linear.
+// there are by reading all targets, so that no launch or wait between blocks is
+// needed: 8 T bytes out of the caches a block, 34 MB in all with 4096 tokens
+// (the launch takes 6 us). `groups` of kGatherRows rows a block keep the
+// blocks below 2048 and the reading linear above 8192 tokens; with the most
+// that are accepted, 2^21, it is still 34 GB a launch.
 template <bool BWD>
 __global__ __launch_bounds__(256) void xent_gather_kernel(XentRows a, int groups) {
   __shared__ int before[4], all[4];
@@ -495,11 +499,13 @@ __global__ __launch_bounds__(1024) void xent_reduce_kernel(const float* __restri
 // so a load covers 64 contiguous bytes of 16 rows and the stage's second load
 // the rest of those 128-byte lines. (With 32 x 32 fragments a load takes 32
 // bytes of 32 rows; the other three loads of a line then often found it gone
-// from L1: 36 us at 16 x 2560 against 32000 columns, where this takes 29 us,
-// 5.6 TB/s of W, and slower the more loads were in flight.) Measured there for
+// from L1: 36 us at 16 x 2560 against 32000 columns, where this takes 28 us,
+// 5.9 TB/s of W, and slower the more loads were in flight.) Measured there for
 // the whole loss: 64 rows and 4 waves a workgroup 39.0 us, 8 waves 40.1 us, 16
 // waves 44.4 us, 32 rows 43.3 us; one launch in which the last workgroup joins
-// the pairs 58-78 us (arrivals at one address run 25 ns apart).
+// the pairs 58-78 us (arrivals at one address run 25 ns apart). (These with
+// rounded references in base 2; the exact differences take 1 us more in the
+// join: 40.0 us.)
 // ---------------------------------------------------------------------------
 
 constexpr int kFewWaves = 4;
@@ -513,7 +519,13 @@ constexpr int kFewGroup = 64;  // tokens a workgroup takes at most
 // 58 against 8000 and 67 / 59 against 16000, 1000 tokens 26 / 60 against 1000 and
 // 67 / 61 against 4000; 48 tokens 44 / 67 against 32000, 155 / 152 against 128256;
 // 64 tokens 52 / 67 against 32000, 97 / 84 against 64000, 187 / 152 against
-// 128256. The no_skinny test knob keeps to the tiles.
+// 128256. The rule does not look at D. Repeated on one W at D = 512, 2560 and
+// 8192, this way / by tiles: 16 tokens against 32000 columns 14 / 26, 33 / 58 and
+// 117 / 168, 256 against 8000 15 / 27, 37 / 59 and 94 / 146, 1000 against 2000
+// 15 / 29, 37 / 61 and 94 / 148; but with 48 tokens against 128256 columns 45 /
+// 49, 157 / 149 and 456 / 402, and with 64 against 57300 26 / 30, 92 / 70 and
+// 247 / 197: there tiles are faster from D = 2560 on and are not taken. The
+// no_skinny test knob keeps to the tiles.
 static int64_t few_groups(int64_t T) { return (T + kFewGroup - 1) / kFewGroup; }
 static bool few_tokens(int64_t T, int64_t V) {
   if (test_knobs().no_skinny.load(std::memory_order_relaxed) != 0) return false;

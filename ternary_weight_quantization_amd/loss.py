@@ -22,7 +22,9 @@ def linear_cross_entropy(hidden, weight, targets, ignore_index=-100, reduction="
     are 0, whatever they hold. reduction: "mean" over the rows that count (0 if
     there are none), "sum", or "none" (float32 losses of targets' shape). A
     target outside 0 .. V-1 that is not ignore_index gives NaN. Gradients: of
-    hidden in bf16, of weight in its dtype (differentiable once)."""
+    hidden in bf16, of weight in its dtype (differentiable once, in reverse
+    mode). Of a float32 weight each call makes a bf16 copy, which is kept until
+    the backward."""
     code = REDUCTIONS.get(reduction)
     if code is None:
         raise ValueError(f"reduction: expected one of {sorted(REDUCTIONS)}, got {reduction!r}")

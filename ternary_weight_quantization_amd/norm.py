@@ -18,7 +18,8 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, out_dtype=torch.bfloat16, ch
     (K <= 32768), times weight [K] plus bias [K] (bf16 or float32, one dtype;
     each may be None), in out_dtype (bf16, what the linear layers take, or
     float32). ``checkpoint=True`` keeps x in 8 bits for the backward. Gradients:
-    dX in x's dtype, those of weight and bias in theirs (differentiable once)."""
+    dX in x's dtype, those of weight and bias in theirs (differentiable once,
+    in reverse mode)."""
     return B.ops().layer_norm(x, weight, bias, eps, out_dtype, checkpoint)
 
 

@@ -113,7 +113,9 @@ def ttq_linear(x, weight, params, checkpoint=False):
     """x [..., K] bf16 times the TTQ weight of (weight [N, K], params float32
     [3] = (delta, Wp, Wn), positive): ``TTQFunction`` as a function.
     ``checkpoint=True`` keeps x for dW as 8-bit codes (``checkpoint.compress``)
-    instead of in bf16; dW then is that of the codes' values."""
+    instead of in bf16; dW then is that of the codes' values, each rounded to
+    bf16 for the product (whose relative error grows from 0.0017 to 0.0023
+    against fp32 values)."""
     if checkpoint:
         return B.ops().ttq_linear_checkpoint(x, weight, params)
     return TTQFunction.apply(x, weight, params)
