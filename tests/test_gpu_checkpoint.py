@@ -393,3 +393,27 @@ def test_ttq_checkpoint_odd_widths_in_the_paired_launch(M, K, N, wt):
         ref = sign * rdw[mask].sum()
         assert abs(got.double() - ref) <= U * abs(ref)
     assert dp[0] == 0
+
+
+@pytest.mark.parametrize("ckpt", [True, False])
+def test_silu_of_every_negative_value(ckpt):
+    """Down to where silu(g) = g e^g leaves the normal numbers (g = -91.7), e^-g
+    passing 2^126 and 2^128 on the way, and 0 or a subnormal below: every
+    negative bf16 value, with an up and a dY of powers of two."""
+    from ternary_weight_quantization_amd.checkpoint import gated_activation
+
+    bits = torch.arange(0x8000, 0xFF80, dtype=torch.int32).to(torch.int16)
+    g = bits.view(BF).cuda()
+    g = g[None, :].expand(2, -1).contiguous() if not ckpt else g[:, None].expand(-1, 2).contiguous()
+    note(f"silu of every negative value, ckpt={ckpt}")
+    up, dy = torch.full_like(g, 4.0), torch.full_like(g, 0.5)
+    gs, us = g.clone().requires_grad_(True), up.requires_grad_(True)
+    y = gated_activation(gs, us, "silu", checkpoint=ckpt)
+    dg, du = torch.autograd.grad(y, (gs, us), dy)
+    d = g.double()
+    a, da = act("silu", d)
+    # the formulas' own rounding in 64 bits is far below; 2^-124: subnormal fp32 terms times 4 may become 0
+    E = (24 + 3 * d.abs()) * U
+    for got, ref, size in ((y, 4 * a, 4 * a.abs()), (dg, 2 * da, 2 / (1 + torch.exp(-d)) * (1 + d.abs())), (du, a / 2, a.abs() / 2)):
+        err = (got.double() - ref).abs()
+        assert (err <= H * ref.abs() + E * size + 2.0 ** -124).all(), d[err > H * ref.abs() + E * size + 2.0 ** -124][:9]
