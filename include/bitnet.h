@@ -577,6 +577,145 @@ bitnet_status bitnet_xent_bwd(const uint16_t* h, const uint16_t* w, const int64_
                               size_t workspace_bytes, void* stream);
 
 /*
+ * Root-mean-square norm over rows of K values, with the residual's addition
+ * before it and an output in 8 bits with a scale a row (what bitnet_act_quant
+ * makes of bf16 rows, here from the norm's fp32 values):
+ *
+ *   h[m,k] = round(res[m,k] + x[m,k]) in the stream's type, or x without res
+ *   r[m]   = (sum_k h[m,k]^2 / K + eps)^(-1/2),  v[m,k] = h[m,k] * r[m] * w[k]
+ *   y[m,k] = round(v[m,k]),  or
+ *   s[m]   = max(max_k |v[m,k]|, 1e-8f),
+ *   x_q[m,k] = clip(round_half_even(127 * v[m,k] / s[m]), -127, 127)
+ *
+ *   g[m,k]  = dY[m,k] * w[k],  hn[m,k] = h[m,k] * r[m]
+ *   dh[m,k] = r[m] * (g[m,k] - hn[m,k] * sum_j g[m,j] hn[m,j] / K) + dH[m,k]
+ *   dw[k]   = sum_m dY[m,k] * hn[m,k]
+ *
+ * dh is the gradient of x and of res alike (straight through the
+ * quantization). Statistics and sums are fp32, in a fixed order; squares are
+ * summed in fp32, so magnitudes have to stay below about 1e19 / sqrt(K). Each
+ * output is rounded once. NaN and infinities propagate within their row (and
+ * into dw): a row of 8-bit codes that holds one has s = NaN. K <= 16384.
+ *
+ * x       [M][K] in x_dtype: with res BITNET_BF16 or the stream's type, without
+ *         res the stream's type h_dtype.
+ * res, h  [M][K] in h_dtype (BITNET_BF16 or BITNET_F32); both or neither.
+ * w       [K] in p_dtype, or NULL (1).
+ * y       [M][K] in y_dtype (BITNET_BF16 or BITNET_F32), or NULL: then
+ * x_q     [M][Kp] int8 (Kp = bitnet_k_pad(K), columns K..Kp-1 are written as 0)
+ * s_x     [M] float.
+ * rstd    [M] float: r, written by the forward (NULL: not written), read by the
+ *         backward.
+ * dY      [M][K] in y_dtype.  dH [M][K] in h_dtype, the gradient of h itself,
+ *         or NULL (0).
+ * dh      [M][K] in h_dtype, or NULL.  dx [M][K] bf16, the same gradient for a
+ *         bf16 x beside a float stream (h_dtype BITNET_F32), or NULL.
+ * dw      [K] in p_dtype, or NULL. At least one of dh, dx, dw.
+ * Data pointers need only their element's alignment; x_q, s_x and the workspace
+ * 16 bytes.
+ * workspace of the backward: bitnet_rmsnorm_workspace_bytes(M, K) bytes (0 for
+ * sizes it rejects; NULL allowed without dw); no initialization, not shared by
+ * calls that may run at the same time.
+ */
+size_t bitnet_rmsnorm_workspace_bytes(int64_t M, int64_t K);
+bitnet_status bitnet_rmsnorm_fwd(const void* x, bitnet_dtype x_dtype, const void* res, bitnet_dtype h_dtype,
+                                 const void* w, bitnet_dtype p_dtype, int64_t M, int64_t K, float eps, void* h,
+                                 void* y, bitnet_dtype y_dtype, int8_t* x_q, float* s_x, float* rstd, void* stream);
+bitnet_status bitnet_rmsnorm_bwd(const void* dY, bitnet_dtype y_dtype, const void* dH, const void* h,
+                                 bitnet_dtype h_dtype, const void* w, bitnet_dtype p_dtype, const float* rstd,
+                                 int64_t M, int64_t K, void* dh, uint16_t* dx, void* dw, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/*
+ * 8-bit rows with a scale a row (bitnet_act_quant's layout): made of bf16 or
+ * float rows by bitnet_act_quant's arithmetic, and the values they stand for,
+ * x[m,k] = bf16_rne(fp32(x_q[m,k] * fp32(s_x[m] / 127))).
+ *
+ * rows_quant: x [M][K] in x_dtype, 16-byte aligned (M <= 2^23 for BITNET_F32);
+ *             x_q [M][Kp], s_x [M], both 16-byte aligned. A float row that holds
+ *             an infinity or a NaN has s_x = NaN.
+ * rows_unpack: x [M][K] bf16 bits, 2-byte aligned. M * Kp <= 2^34.
+ */
+bitnet_status bitnet_rows_quant(const void* x, bitnet_dtype x_dtype, int64_t M, int64_t K, int8_t* x_q, float* s_x,
+                                void* stream);
+bitnet_status bitnet_rows_unpack(const int8_t* x_q, const float* s_x, int64_t M, int64_t K, uint16_t* x, void* stream);
+
+/*
+ * The gated pair of ternary projections of a feed-forward block:
+ *
+ *   g[m,n] = acc_g * (s_x[m]/127) * gamma[0],  u[m,n] = acc_u * (s_x[m]/127) * gamma[1]
+ *   y[m,n] = bf16_rne(act(g[m,n]) * u[m,n])
+ *
+ * with acc_g and acc_u the exact int32 products of x_q with the codes of the
+ * gate (rows 0..N-1 of w_packed) and of the up projection (rows N..2N-1), fp32
+ * after them; and its straight-through backward (gamma treated as constants)
+ *
+ *   Dg = bf16(dY p gamma[0] c),  Du = bf16(dY a gamma[1] c),  c[m] = s_x[m]/127
+ *   dX[m,k] = sum_n (Dg[m,n] q_g[n,k] + Du[m,n] q_u[n,k]) / c[m]
+ *   dW_gate[n,k] = sum_m Dg[m,n] x_q[m,k] / gamma[0],  dW_up likewise with Du, gamma[1]
+ *
+ * (dg = dY u act'(g) and du = dY act(g) with the scales of what they are multiplied
+ * by, rounded once; fp32 sums, divided in fp32.)
+ *
+ * x_q, s_x   8-bit rows (bitnet_act_quant, bitnet_rmsnorm_fwd).
+ * w_packed   [2N][Kp/4] codes and gamma [2] as bitnet_ternarize_pack writes them
+ *            for each weight [N][K].
+ * y, dY      [M][N] bf16 bits.
+ * slopes     bitnet_gated_slopes_bytes(M, N) bytes: y's derivatives p = u act'(g) and
+ *            a = act(g), written by the forward (NULL: not written) and read by the
+ *            backward, the upper 24 bits of their fp32 values.
+ * dX         [M][K] bf16 bits, or NULL.
+ * dW_gate, dW_up [N][K] in dW_dtype (BITNET_BF16 or BITNET_F32), both or neither.
+ * The backward without dW takes x_q NULL, and s_x NULL too (c is then 1); without dX
+ * w_packed NULL.
+ * workspace  bitnet_gated_fwd_workspace_bytes / bitnet_gated_bwd_workspace_bytes
+ *            (0 for sizes the call rejects); as for bitlinear_fwd.
+ * Pointers 16-byte aligned but gamma, the backward's s_x (4) and dY (2). Limits: those
+ * of the GEMM entry points for a weight of 2 Nd rows, (M + 256) * 4 Nd <= 2^31.
+ */
+size_t bitnet_gated_slopes_bytes(int64_t M, int64_t N);
+size_t bitnet_gated_fwd_workspace_bytes(int64_t M, int64_t N, int64_t K);
+bitnet_status bitnet_gated_fwd(bitnet_act act, const int8_t* x_q, const float* s_x, const uint8_t* w_packed,
+                               const float* gamma, int64_t M, int64_t N, int64_t K, uint16_t* y, void* slopes,
+                               void* workspace, size_t workspace_bytes, void* stream);
+size_t bitnet_gated_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K);
+bitnet_status bitnet_gated_bwd(const uint16_t* dY, const void* slopes, const int8_t* x_q,
+                               const float* s_x, const uint8_t* w_packed, const float* gamma, int64_t M, int64_t N,
+                               int64_t K, uint16_t* dX, void* dW_gate, void* dW_up, bitnet_dtype dW_dtype,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * A linear layer in 8-bit integers with a scale per token and per channel (what a
+ * model keeps out of its ternary layers, such as its head):
+ *
+ *   y[m,n]  = bf16_rne(acc[m,n] * (s_x[m]/127) * (s_w[n]/127) + bias[n]), acc exact int32
+ *   dX[m,k] = sum_n dY[m,n] * w_hat[n,k],  w_hat = bf16_rne(w_q * s_w/127)
+ *   dW[n,k] = sum_m dY[m,n] * x_hat[m,k],  x_hat = bf16_rne(x_q * s_x/127)
+ *
+ * (fp32 rescale and sums; the gradients are straight through both quantizations;
+ * the bias' gradient is bitlinear_bias_grad's).
+ *
+ * x_q [M][Kp], s_x [M]; w_q [N][Kp], s_w [N]: 8-bit rows (bitnet_rows_quant), columns
+ *            K..Kp-1 zero.
+ * bias       [N] bf16 bits, or NULL.   y, dY [M][N] bf16 bits.
+ * dX         [M][K] bf16 bits, or NULL.  dW [N][K] in dW_dtype, or NULL; not both NULL.
+ * workspace  bitnet_int8_fwd_workspace_bytes / bitnet_int8_bwd_workspace_bytes (0 for
+ *            sizes the call rejects); as for bitlinear_fwd. The backward's holds both
+ *            bf16 operands.
+ * Pointers 16-byte aligned. K <= 131072 (the int32 sums); (M + 256) * 2 Kp,
+ * (N + 256) * 2 Kp and (M + 256) * 2 Nd bytes <= 2^31 (Nd = bitnet_k_pad(N); the forward
+ * needs (M + 256) * Kp and (N + 256) * Kp only), N <= 2^24.
+ */
+size_t bitnet_int8_fwd_workspace_bytes(int64_t M, int64_t N, int64_t K);
+bitnet_status bitnet_int8_fwd(const int8_t* x_q, const float* s_x, const int8_t* w_q, const float* s_w,
+                              const uint16_t* bias, int64_t M, int64_t N, int64_t K, uint16_t* y, void* workspace,
+                              size_t workspace_bytes, void* stream);
+size_t bitnet_int8_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K);
+bitnet_status bitnet_int8_bwd(const uint16_t* dY, const int8_t* x_q, const float* s_x, const int8_t* w_q,
+                              const float* s_w, int64_t M, int64_t N, int64_t K, uint16_t* dX, void* dW,
+                              bitnet_dtype dW_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Test hooks (for the library's own tests and tuning; not needed to use it).
  *
  * bitnet_set_test_knobs - process-wide knobs read by every later launch:

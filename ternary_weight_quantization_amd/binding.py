@@ -123,6 +123,29 @@ def lib():
     L.bitnet_xent_fwd.restype = st
     L.bitnet_xent_bwd.argtypes = [vp, vp, vp, i64, vp, vp, st, i64, i64, i64, vp, vp, st, vp, sz, vp]
     L.bitnet_xent_bwd.restype = st
+    for name in ("bitnet_gated_fwd", "bitnet_gated_bwd", "bitnet_int8_fwd", "bitnet_int8_bwd"):
+        f = getattr(L, name + "_workspace_bytes")
+        f.argtypes, f.restype = [i64, i64, i64], sz
+    L.bitnet_gated_slopes_bytes.argtypes = [i64, i64]
+    L.bitnet_gated_slopes_bytes.restype = sz
+    L.bitnet_rmsnorm_workspace_bytes.argtypes = [i64, i64]
+    L.bitnet_rmsnorm_workspace_bytes.restype = sz
+    L.bitnet_rmsnorm_fwd.argtypes = [vp, st, vp, st, vp, st, i64, i64, f32, vp, vp, st, vp, vp, vp, vp]
+    L.bitnet_rmsnorm_fwd.restype = st
+    L.bitnet_rmsnorm_bwd.argtypes = [vp, st, vp, vp, st, vp, st, vp, i64, i64, vp, vp, vp, vp, sz, vp]
+    L.bitnet_rmsnorm_bwd.restype = st
+    L.bitnet_rows_quant.argtypes = [vp, st, i64, i64, vp, vp, vp]
+    L.bitnet_rows_quant.restype = st
+    L.bitnet_rows_unpack.argtypes = [vp, vp, i64, i64, vp, vp]
+    L.bitnet_rows_unpack.restype = st
+    L.bitnet_gated_fwd.argtypes = [st, vp, vp, vp, vp, i64, i64, i64, vp, vp, vp, sz, vp]
+    L.bitnet_gated_fwd.restype = st
+    L.bitnet_gated_bwd.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, vp, vp, vp, st, vp, sz, vp]
+    L.bitnet_gated_bwd.restype = st
+    L.bitnet_int8_fwd.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, vp, vp, sz, vp]
+    L.bitnet_int8_fwd.restype = st
+    L.bitnet_int8_bwd.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, vp, vp, st, vp, sz, vp]
+    L.bitnet_int8_bwd.restype = st
     i32, u32 = ctypes.c_int32, ctypes.c_uint32
     L.bitnet_set_test_knobs.argtypes = [st, st, st, u32]
     L.bitnet_set_test_knobs.restype = None
@@ -749,6 +772,200 @@ def bitnet_gate_bwd(act, dY, dgate, dup=None, gate=None, up=None, gate_codes=Non
                  up_codes=up_codes, up_scales=up_scales)
     _run(lib().bitnet_gate_bwd, dY, stream, int(act), _ptr(dY), _ptr(gate), ldg, _ptr(up), ldu, _ptr(gate_codes),
          _ptr(gate_scales), _ptr(up_codes), _ptr(up_scales), M, K, _ptr(dgate), lddg, _ptr(dup), lddu)
+
+
+# --- root-mean-square norm, 8-bit rows -------------------------------------------
+
+def bitnet_rmsnorm_workspace_bytes(M, K):
+    return int(lib().bitnet_rmsnorm_workspace_bytes(int(M), int(K)))
+
+
+def _need_rows8(q, s, M, K, name):
+    _need(q, torch.int8, (M, bitnet_k_pad(K)), name + "_q")
+    _need(s, torch.float32, (M,), "s_" + name)
+
+
+def bitnet_rmsnorm_fwd(x, w, eps, res=None, h=None, y=None, x_q=None, s_x=None, rstd=None, stream=None):
+    """The RMS norm of x [M, K], or of h = res + x (written to h, of res' dtype), with
+    w [K] or None: y [M, K] (bf16 or float32), or 8-bit rows x_q int8 [M, Kp], s_x
+    float32 [M]. Optional: rstd float32 [M]."""
+    M, K = x.shape
+    xd = _value_dtype(x, "x")
+    _need(x, x.dtype, (M, K), "x")
+    hd = xd
+    if res is not None:
+        hd = _value_dtype(res, "res")
+        _need(res, res.dtype, (M, K), "res")
+        if h is None:
+            raise ValueError("h: needed with res")
+        _need(h, res.dtype, (M, K), "h")
+    pd = _norm_params(w, None, K, x)
+    yd = BITNET_BF16
+    if y is not None:
+        yd = _value_dtype(y, "y")
+        _need(y, y.dtype, (M, K), "y")
+    if x_q is not None:
+        if s_x is None:
+            raise ValueError("s_x: needed with x_q")
+        _need_rows8(x_q, s_x, M, K, "x")
+    if rstd is not None:
+        _need(rstd, torch.float32, (M,), "rstd")
+    _same_device(x, res=res, h=h, y=y, x_q=x_q, s_x=s_x, rstd=rstd)
+    _run(lib().bitnet_rmsnorm_fwd, x, stream, _ptr(x), xd, _ptr(res), hd, _ptr(w), pd, M, K, float(eps), _ptr(h), _ptr(y),
+         yd, _ptr(x_q), _ptr(s_x), _ptr(rstd))
+
+
+def bitnet_rmsnorm_bwd(dY, h, w, rstd, dH=None, dh=None, dx=None, dw=None, workspace=None, stream=None):
+    """dh [M, K] in h's dtype, dx its bf16 copy (h float32) and dw [K] (each
+    optional) of the RMS norm, from dY [M, K], the normed rows h, rstd and dH [M, K],
+    the gradient of h itself, or None."""
+    M, K = dY.shape
+    yd, hd = _value_dtype(dY, "dY"), _value_dtype(h, "h")
+    _need(dY, dY.dtype, (M, K), "dY")
+    _need(h, h.dtype, (M, K), "h")
+    _need(rstd, torch.float32, (M,), "rstd")
+    for name, t, dt in (("dH", dH, h.dtype), ("dh", dh, h.dtype), ("dx", dx, torch.bfloat16)):
+        if t is not None:
+            _need(t, dt, (M, K), name)
+    pd = _norm_params(w, None, K, dY)
+    if dw is not None:
+        if w is None:
+            pd = _value_dtype(dw, "dw")
+        _need(dw, torch.float32 if pd == BITNET_F32 else torch.bfloat16, (K,), "dw")
+    _same_device(dY, h=h, rstd=rstd, dH=dH, dh=dh, dx=dx, dw=dw, workspace=workspace)
+    if workspace is None and dw is not None:
+        workspace = _workspace(bitnet_rmsnorm_workspace_bytes(M, K), dY, stream)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _run(lib().bitnet_rmsnorm_bwd, dY, stream, _ptr(dY), yd, _ptr(dH), _ptr(h), hd, _ptr(w), pd, _ptr(rstd), M, K,
+         _ptr(dh), _ptr(dx), _ptr(dw), _ptr(workspace), ws_bytes)
+
+
+def bitnet_rows_quant(x, x_q, s_x, stream=None):
+    """x [M, K] (bf16 or float32) -> x_q int8 [M, Kp], s_x float32 [M]."""
+    M, K = x.shape
+    xd = _value_dtype(x, "x")
+    _need(x, x.dtype, (M, K), "x")
+    _need_rows8(x_q, s_x, M, K, "x")
+    _same_device(x, x_q=x_q, s_x=s_x)
+    _run(lib().bitnet_rows_quant, x, stream, _ptr(x), xd, M, K, _ptr(x_q), _ptr(s_x))
+
+
+def bitnet_rows_unpack(x_q, s_x, x, stream=None):
+    """x [M, K] bf16 = the values of x_q and s_x."""
+    M, K = x.shape
+    _need(x, torch.bfloat16, (M, K), "x")
+    _need_rows8(x_q, s_x, M, K, "x")
+    _same_device(x, x_q=x_q, s_x=s_x)
+    _run(lib().bitnet_rows_unpack, x, stream, _ptr(x_q), _ptr(s_x), M, K, _ptr(x))
+
+
+# --- the gated pair of ternary projections ---------------------------------------
+
+def bitnet_gated_slopes_bytes(M, N):
+    return int(lib().bitnet_gated_slopes_bytes(int(M), int(N)))
+
+
+def bitnet_gated_fwd_workspace_bytes(M, N, K):
+    return int(lib().bitnet_gated_fwd_workspace_bytes(int(M), int(N), int(K)))
+
+
+def bitnet_gated_bwd_workspace_bytes(M, N, K):
+    return int(lib().bitnet_gated_bwd_workspace_bytes(int(M), int(N), int(K)))
+
+
+def _ws_args(workspace, need, like, stream):
+    if workspace is None:
+        workspace = _workspace(need, like, stream)
+    return _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def bitnet_gated_fwd(act, x_q, s_x, w_packed, gamma, K, y, slopes=None, workspace=None, stream=None):
+    """y [M, N] bf16 = act(gate) * up of 8-bit rows x_q, s_x and the codes w_packed
+    uint8 [2N, Kp/4] with gamma float32 [2]; slopes uint8
+    [bitnet_gated_slopes_bytes(M, N)] is written too if given."""
+    M, N = y.shape
+    _need(y, torch.bfloat16, (M, N), "y")
+    _need_rows8(x_q, s_x, M, K, "x")
+    _need(w_packed, torch.uint8, (2 * N, bitnet_k_pad(K) // 4), "w_packed")
+    _need(gamma, torch.float32, (2,), "gamma")
+    if slopes is not None:
+        _need(slopes, torch.uint8, (bitnet_gated_slopes_bytes(M, N),), "slopes")
+    _same_device(y, x_q=x_q, s_x=s_x, w_packed=w_packed, gamma=gamma, slopes=slopes, workspace=workspace)
+    ws, n = _ws_args(workspace, bitnet_gated_fwd_workspace_bytes(M, N, K), y, stream)
+    _run(lib().bitnet_gated_fwd, y, stream, int(act), _ptr(x_q), _ptr(s_x), _ptr(w_packed), _ptr(gamma), M, N, int(K),
+         _ptr(y), _ptr(slopes), ws, n)
+
+
+def bitnet_gated_bwd(dY, slopes, x_q, s_x, w_packed, gamma, K, dX=None, dW_gate=None, dW_up=None, workspace=None,
+                     stream=None):
+    """dX [M, K] bf16 and/or dW_gate and dW_up [N, K] (bf16 or float32) from dY [M, N]
+    and what bitnet_gated_fwd read and wrote (x_q, s_x may be None without the
+    weights' gradients, w_packed without dX)."""
+    M, N = dY.shape
+    Kp = bitnet_k_pad(K)
+    _need(dY, torch.bfloat16, (M, N), "dY")
+    _need(slopes, torch.uint8, (bitnet_gated_slopes_bytes(M, N),), "slopes")
+    _need(gamma, torch.float32, (2,), "gamma")
+    if dX is not None:
+        _need(dX, torch.bfloat16, (M, K), "dX")
+        _need(w_packed, torch.uint8, (2 * N, Kp // 4), "w_packed")
+    dd = BITNET_BF16
+    if dW_gate is not None:
+        dd = _value_dtype(dW_gate, "dW_gate")
+        for name, t in (("dW_gate", dW_gate), ("dW_up", dW_up)):
+            if t is None:
+                raise ValueError("dW_gate and dW_up: both or neither")
+            _need(t, dW_gate.dtype, (N, K), name)
+        _need_rows8(x_q, s_x, M, K, "x")
+    _same_device(dY, slopes=slopes, x_q=x_q, s_x=s_x, w_packed=w_packed, gamma=gamma, dX=dX, dW_gate=dW_gate,
+                 dW_up=dW_up, workspace=workspace)
+    ws, n = _ws_args(workspace, bitnet_gated_bwd_workspace_bytes(M, N, K), dY, stream)
+    _run(lib().bitnet_gated_bwd, dY, stream, _ptr(dY), _ptr(slopes), _ptr(x_q), _ptr(s_x), _ptr(w_packed),
+         _ptr(gamma), M, N, int(K), _ptr(dX), _ptr(dW_gate), _ptr(dW_up), dd, ws, n)
+
+
+# --- linear layer in 8-bit integers -----------------------------------------------
+
+def bitnet_int8_fwd_workspace_bytes(M, N, K):
+    return int(lib().bitnet_int8_fwd_workspace_bytes(int(M), int(N), int(K)))
+
+
+def bitnet_int8_bwd_workspace_bytes(M, N, K):
+    return int(lib().bitnet_int8_bwd_workspace_bytes(int(M), int(N), int(K)))
+
+
+def bitnet_int8_fwd(x_q, s_x, w_q, s_w, K, y, bias=None, workspace=None, stream=None):
+    """y [M, N] bf16 of 8-bit rows x_q, s_x (tokens) and w_q, s_w (channels), with an
+    optional bf16 bias [N]."""
+    M, N = y.shape
+    _need(y, torch.bfloat16, (M, N), "y")
+    _need_rows8(x_q, s_x, M, K, "x")
+    _need_rows8(w_q, s_w, N, K, "w")
+    if bias is not None:
+        _need(bias, torch.bfloat16, (N,), "bias")
+    _same_device(y, x_q=x_q, s_x=s_x, w_q=w_q, s_w=s_w, bias=bias, workspace=workspace)
+    ws, n = _ws_args(workspace, bitnet_int8_fwd_workspace_bytes(M, N, K), y, stream)
+    _run(lib().bitnet_int8_fwd, y, stream, _ptr(x_q), _ptr(s_x), _ptr(w_q), _ptr(s_w), _ptr(bias), M, N, int(K), _ptr(y),
+         ws, n)
+
+
+def bitnet_int8_bwd(dY, x_q, s_x, w_q, s_w, K, dX=None, dW=None, workspace=None, stream=None):
+    """dX [M, K] bf16 and/or dW [N, K] (bf16 or float32) from dY [M, N] (w_q, s_w may be
+    None without dX, x_q, s_x without dW)."""
+    M, N = dY.shape
+    _need(dY, torch.bfloat16, (M, N), "dY")
+    dd = BITNET_BF16
+    if dX is not None:
+        _need(dX, torch.bfloat16, (M, K), "dX")
+        _need_rows8(w_q, s_w, N, K, "w")
+    if dW is not None:
+        dd = _value_dtype(dW, "dW")
+        _need(dW, dW.dtype, (N, K), "dW")
+        _need_rows8(x_q, s_x, M, K, "x")
+    _same_device(dY, x_q=x_q, s_x=s_x, w_q=w_q, s_w=s_w, dX=dX, dW=dW, workspace=workspace)
+    ws, n = _ws_args(workspace, bitnet_int8_bwd_workspace_bytes(M, N, K), dY, stream)
+    _run(lib().bitnet_int8_bwd, dY, stream, _ptr(dY), _ptr(x_q), _ptr(s_x), _ptr(w_q), _ptr(s_w), M, N, int(K), _ptr(dX),
+         _ptr(dW), dd, ws, n)
 
 
 # --- linear layer with softmax cross entropy -------------------------------------

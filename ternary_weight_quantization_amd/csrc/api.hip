@@ -85,6 +85,30 @@ bitnet_status check_norm_sizes(int64_t M, int64_t K) {
   return K > bitnet::kNormMaxK ? BITNET_ERR_SHAPE : BITNET_OK;
 }
 
+bitnet_status check_rms_sizes(int64_t M, int64_t K) {
+  if (bitnet_status st = check_sizes(M, K)) return st;
+  return K > bitnet::kRmsMaxK ? BITNET_ERR_SHAPE : BITNET_OK;
+}
+
+// The products over a weight of 2 Nd rows, in both directions.
+bitnet_status check_gated_sizes(int64_t M, int64_t N, int64_t K) {
+  if (M < 1 || N < 1 || K < 1 || N > kMaxDim / 4) return BITNET_ERR_SHAPE;
+  const int64_t J = 2 * bitnet::k_pad(N);
+  if (bitnet_status st = check_gemm_sizes(M, J, K)) return st;
+  if (bitnet_status st = check_gemm_ranges(M, J, K, true, true, true, J)) return st;
+  return 32 * 4 * K > (int64_t(1) << 31) ? BITNET_ERR_SHAPE : BITNET_OK;  // the epilogues of dX and dW
+}
+
+bitnet_status check_int8_sizes(int64_t M, int64_t N, int64_t K, bool bwd) {
+  if (K > 131072) return BITNET_ERR_SHAPE;  // 127 * 127 * Kp < 2^31
+  if (bitnet_status st = check_gemm_sizes(M, N, K)) return st;
+  const int64_t Kp = bitnet::k_pad(K);
+  if (32 * 4 * N > (int64_t(1) << 31) || !buffer_range_ok(M, Kp) || !buffer_range_ok(N, Kp)) return BITNET_ERR_SHAPE;
+  if (bwd && (!buffer_range_ok(M, 2 * Kp) || !buffer_range_ok(N, 2 * Kp) || !buffer_range_ok(M, 2 * bitnet::k_pad(N))))
+    return BITNET_ERR_SHAPE;
+  return BITNET_OK;
+}
+
 // One thread per 8 values, 256 threads a workgroup: a launch holds fewer than
 // 2^32 threads.
 bitnet_status check_ckpt_sizes(int64_t M, int64_t K) {
@@ -499,6 +523,158 @@ bitnet_status ttq_bwd_ckpt(const uint16_t* dY, const int8_t* codes, const float*
   }
   return from_hip(bitnet::launch_ttq_bwd(dY, ldy, x, Kp, wt, w_packed, M, N, K, dX, dW, dW_dtype == BITNET_F32, grads,
                                          ws + used, workspace_bytes - used, st));
+}
+
+// ---------------------------------------------------------------------------
+// Root-mean-square norm, 8-bit rows
+// ---------------------------------------------------------------------------
+
+size_t bitnet_rmsnorm_workspace_bytes(int64_t M, int64_t K) {
+  if (check_rms_sizes(M, K) != BITNET_OK) return 0;
+  return bitnet::rmsnorm_bwd_workspace(M, K);
+}
+
+bitnet_status bitnet_rmsnorm_fwd(const void* x, bitnet_dtype x_dtype, const void* res, bitnet_dtype h_dtype,
+                                 const void* w, bitnet_dtype p_dtype, int64_t M, int64_t K, float eps, void* h,
+                                 void* y, bitnet_dtype y_dtype, int8_t* x_q, float* s_x, float* rstd, void* stream) {
+  if (!x || (res != nullptr) != (h != nullptr) || (y != nullptr) == (x_q != nullptr) || (x_q && !s_x))
+    return BITNET_ERR_NULL;
+  if (!is_value(x_dtype) || !is_value(h_dtype) || !is_value(p_dtype) || (y && !is_value(y_dtype))) return BITNET_ERR_DTYPE;
+  if (x_dtype != h_dtype && (!res || x_dtype != BITNET_BF16)) return BITNET_ERR_DTYPE;
+  if (bitnet_status st = check_rms_sizes(M, K)) return st;
+  if (!aligned(x, elem(x_dtype)) || !aligned(res, elem(h_dtype)) || !aligned(h, elem(h_dtype)) ||
+      !aligned(w, elem(p_dtype)) || (y && !aligned(y, elem(y_dtype))) || !aligned(x_q, 16) || (x_q && !aligned(s_x, 16)) ||
+      !aligned(rstd, 4))
+    return BITNET_ERR_ALIGN;
+  return from_hip(bitnet::launch_rmsnorm_fwd(x, x_dtype == BITNET_F32, res, h_dtype == BITNET_F32, w,
+                                             p_dtype == BITNET_F32, M, K, eps, h, y, y_dtype == BITNET_F32, x_q, s_x,
+                                             rstd, static_cast<hipStream_t>(stream)));
+}
+
+bitnet_status bitnet_rmsnorm_bwd(const void* dY, bitnet_dtype y_dtype, const void* dH, const void* h,
+                                 bitnet_dtype h_dtype, const void* w, bitnet_dtype p_dtype, const float* rstd,
+                                 int64_t M, int64_t K, void* dh, uint16_t* dx, void* dw, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  if (!dY || !h || !rstd || (!dh && !dx && !dw)) return BITNET_ERR_NULL;
+  if (!is_value(y_dtype) || !is_value(h_dtype) || !is_value(p_dtype)) return BITNET_ERR_DTYPE;
+  if (dx && h_dtype != BITNET_F32) return BITNET_ERR_DTYPE;
+  if (bitnet_status st = check_rms_sizes(M, K)) return st;
+  if (dw) {
+    if (!workspace || workspace_bytes < bitnet_rmsnorm_workspace_bytes(M, K)) return BITNET_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return BITNET_ERR_ALIGN;
+  }
+  if (!aligned(dY, elem(y_dtype)) || !aligned(dH, elem(h_dtype)) || !aligned(h, elem(h_dtype)) ||
+      !aligned(w, elem(p_dtype)) || !aligned(rstd, 4) || !aligned(dh, elem(h_dtype)) || !aligned(dx, 2) ||
+      !aligned(dw, elem(p_dtype)))
+    return BITNET_ERR_ALIGN;
+  return from_hip(bitnet::launch_rmsnorm_bwd(dY, y_dtype == BITNET_F32, dH, h, h_dtype == BITNET_F32, w,
+                                             p_dtype == BITNET_F32, rstd, M, K, dh, dx, dw, workspace,
+                                             static_cast<hipStream_t>(stream)));
+}
+
+bitnet_status bitnet_rows_quant(const void* x, bitnet_dtype x_dtype, int64_t M, int64_t K, int8_t* x_q, float* s_x,
+                                void* stream) {
+  if (!x || !x_q || !s_x) return BITNET_ERR_NULL;
+  if (!is_value(x_dtype)) return BITNET_ERR_DTYPE;
+  if (x_dtype == BITNET_BF16) return bitnet_act_quant(static_cast<const uint16_t*>(x), M, K, x_q, s_x, stream);
+  if (bitnet_status st = check_sizes(M, K)) return st;
+  if (M > (int64_t(1) << 23) || K > (int64_t(1) << 24)) return BITNET_ERR_SHAPE;
+  if (!aligned(x, 16) || !aligned(x_q, 16) || !aligned(s_x, 16)) return BITNET_ERR_ALIGN;
+  return from_hip(bitnet::launch_rows_quant_f32(static_cast<const float*>(x), M, K, x_q, s_x,
+                                                static_cast<hipStream_t>(stream)));
+}
+
+bitnet_status bitnet_rows_unpack(const int8_t* x_q, const float* s_x, int64_t M, int64_t K, uint16_t* x, void* stream) {
+  if (!x_q || !s_x || !x) return BITNET_ERR_NULL;
+  if (bitnet_status st = check_ckpt_sizes(M, K)) return st;
+  if (!aligned(x_q, 16) || !aligned(s_x, 4) || !aligned(x, 2)) return BITNET_ERR_ALIGN;
+  return from_hip(bitnet::launch_rows_unpack(x_q, s_x, M, K, x, static_cast<hipStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// The gated pair of ternary projections
+// ---------------------------------------------------------------------------
+
+size_t bitnet_gated_slopes_bytes(int64_t M, int64_t N) {
+  return M < 1 || N < 1 || M > kMaxDim || N > kMaxDim ? 0 : bitnet::gated_slopes_bytes(M, N);
+}
+size_t bitnet_gated_fwd_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  return check_gated_sizes(M, N, K) != BITNET_OK ? 0 : bitnet::gated_fwd_workspace(M, N, K);
+}
+size_t bitnet_gated_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  return check_gated_sizes(M, N, K) != BITNET_OK ? 0 : bitnet::gated_bwd_workspace(M, N, K);
+}
+
+bitnet_status bitnet_gated_fwd(bitnet_act act, const int8_t* x_q, const float* s_x, const uint8_t* w_packed,
+                               const float* gamma, int64_t M, int64_t N, int64_t K, uint16_t* y, void* slopes,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  if (!x_q || !s_x || !w_packed || !gamma || !y) return BITNET_ERR_NULL;
+  if (act != BITNET_ACT_SILU && act != BITNET_ACT_RELU2) return BITNET_ERR_DTYPE;
+  if (bitnet_status st = check_gated_sizes(M, N, K)) return st;
+  const size_t need = bitnet_gated_fwd_workspace_bytes(M, N, K);
+  if (workspace_bytes < need || (workspace_bytes > 0 && !workspace)) return BITNET_ERR_WORKSPACE;
+  if (!aligned(workspace, 16) || !aligned(x_q, 16) || !aligned(s_x, 16) || !aligned(w_packed, 16) ||
+      !aligned(gamma, 4) || !aligned(y, 16) || !aligned(slopes, 16))
+    return BITNET_ERR_ALIGN;
+  return from_hip(bitnet::launch_gated_fwd(act == BITNET_ACT_RELU2, x_q, s_x, w_packed, gamma, M, N, K, y,
+                                           static_cast<uint16_t*>(slopes), workspace, workspace_bytes, static_cast<hipStream_t>(stream)));
+}
+
+bitnet_status bitnet_gated_bwd(const uint16_t* dY, const void* slopes, const int8_t* x_q,
+                               const float* s_x, const uint8_t* w_packed, const float* gamma, int64_t M, int64_t N,
+                               int64_t K, uint16_t* dX, void* dW_gate, void* dW_up, bitnet_dtype dW_dtype,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  if (!dY || !slopes || !gamma || (!dX && !dW_gate) || (dW_gate != nullptr) != (dW_up != nullptr)) return BITNET_ERR_NULL;
+  if ((dX && !w_packed) || (dW_gate && (!x_q || !s_x))) return BITNET_ERR_NULL;
+  if (dW_gate && !is_value(dW_dtype)) return BITNET_ERR_DTYPE;
+  if (bitnet_status st = check_gated_sizes(M, N, K)) return st;
+  if (!workspace || workspace_bytes < bitnet_gated_bwd_workspace_bytes(M, N, K)) return BITNET_ERR_WORKSPACE;
+  if (!aligned(workspace, 16) || !aligned(dY, 2) || !aligned(slopes, 16) || !aligned(gamma, 4)) return BITNET_ERR_ALIGN;
+  if (!aligned(s_x, 4) || (dX && (!aligned(w_packed, 16) || !aligned(dX, 16)))) return BITNET_ERR_ALIGN;
+  if (dW_gate && (!aligned(x_q, 16) || !aligned(dW_gate, 16) || !aligned(dW_up, 16)))
+    return BITNET_ERR_ALIGN;
+  return from_hip(bitnet::launch_gated_bwd(dY, static_cast<const uint16_t*>(slopes), x_q, s_x, w_packed, gamma, M, N, K, dX,
+                                           dW_gate, dW_up, dW_dtype == BITNET_F32, workspace, workspace_bytes,
+                                           static_cast<hipStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// Linear layer in 8-bit integers
+// ---------------------------------------------------------------------------
+
+size_t bitnet_int8_fwd_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  return check_int8_sizes(M, N, K, false) != BITNET_OK ? 0 : bitnet::int8_fwd_workspace(M, N, K);
+}
+size_t bitnet_int8_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  return check_int8_sizes(M, N, K, true) != BITNET_OK ? 0 : bitnet::int8_bwd_workspace(M, N, K);
+}
+
+bitnet_status bitnet_int8_fwd(const int8_t* x_q, const float* s_x, const int8_t* w_q, const float* s_w,
+                              const uint16_t* bias, int64_t M, int64_t N, int64_t K, uint16_t* y, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  if (!x_q || !s_x || !w_q || !s_w || !y) return BITNET_ERR_NULL;
+  if (bitnet_status st = check_int8_sizes(M, N, K, false)) return st;
+  const size_t need = bitnet_int8_fwd_workspace_bytes(M, N, K);
+  if (workspace_bytes < need || (workspace_bytes > 0 && !workspace)) return BITNET_ERR_WORKSPACE;
+  if (!aligned(workspace, 16) || !aligned(x_q, 16) || !aligned(s_x, 16) || !aligned(w_q, 16) || !aligned(s_w, 16) ||
+      !aligned(bias, 16) || !aligned(y, 16))
+    return BITNET_ERR_ALIGN;
+  return from_hip(bitnet::launch_int8_fwd(x_q, s_x, w_q, s_w, bias, M, N, K, y, workspace, workspace_bytes,
+                                          static_cast<hipStream_t>(stream)));
+}
+
+bitnet_status bitnet_int8_bwd(const uint16_t* dY, const int8_t* x_q, const float* s_x, const int8_t* w_q,
+                              const float* s_w, int64_t M, int64_t N, int64_t K, uint16_t* dX, void* dW,
+                              bitnet_dtype dW_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!dY || (!dX && !dW) || (dX && (!w_q || !s_w)) || (dW && (!x_q || !s_x))) return BITNET_ERR_NULL;
+  if (dW && !is_value(dW_dtype)) return BITNET_ERR_DTYPE;
+  if (bitnet_status st = check_int8_sizes(M, N, K, true)) return st;
+  if (!workspace || workspace_bytes < bitnet_int8_bwd_workspace_bytes(M, N, K)) return BITNET_ERR_WORKSPACE;
+  if (!aligned(workspace, 16) || !aligned(dY, 16)) return BITNET_ERR_ALIGN;
+  if (dX && (!aligned(w_q, 16) || !aligned(s_w, 16) || !aligned(dX, 16))) return BITNET_ERR_ALIGN;
+  if (dW && (!aligned(x_q, 16) || !aligned(s_x, 16) || !aligned(dW, 16))) return BITNET_ERR_ALIGN;
+  return from_hip(bitnet::launch_int8_bwd(dY, x_q, s_x, w_q, s_w, M, N, K, dX, dW, dW_dtype == BITNET_F32, workspace,
+                                          workspace_bytes, static_cast<hipStream_t>(stream)));
 }
 
 // ---------------------------------------------------------------------------

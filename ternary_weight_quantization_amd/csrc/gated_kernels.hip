@@ -1,0 +1,518 @@
+// The gated pair of ternary projections of a feed-forward block in one kernel,
+//
+//   g = (x_q . tg^T) s/127 gamma_g,  u = (x_q . tu^T) s/127 gamma_u,  y = act(g) u
+//
+// and its straight-through backward
+//
+//   dg = dY u act'(g),  du = dY act(g)
+//   dX = gamma_g dg tg + gamma_u du tu,  dWg = dg^T x_hat,  dWu = du^T x_hat
+//
+// Forward: the int8 product of gemm_kernels.hip over the rows of both weights.
+// A wave's 128 code rows are 64 of the gate and the same 64 of the up
+// projection, so that a lane holds g and u of the same outputs in its
+// accumulators and the epilogue applies the activation there: neither
+// projection is written and read again. For the backward it stores y's slopes
+// dy/dg = u act'(g) and dy/du = act(g) next to y, as the upper 24 bits of their
+// fp32 values (cut off: at most 2^-16 of the value).
+//
+// Backward: one pass makes D = [gamma_g dg | gamma_u du] s/127 in bf16, then the
+// two products of gemm_kernels.hip on D, the codes of both weights below each
+// other and the int8 rows as bf16 (exact). The scales are all in D: dX sums over
+// both halves, whose scales differ, and dW over the tokens; dX's epilogue divides
+// a token's row by s/127 and dW's each half by its gamma, in fp32. So every
+// gradient sees two roundings to bf16, D's and its own: 0.0024 of its norm off
+// the exact one (g and u kept in bf16, D without s and x_hat rounded gave
+// 0.0037, and 0.0044 for relu2). Rows of D, of the slopes and of the transposed
+// codes are padded to Nd = N rounded up to 64 in each half, so that every width
+// runs the aligned loaders and no 32 rows of dW belong to both halves.
+
+#include <algorithm>
+
+#include "activation.h"
+#include "bwd_prep.h"
+#include "gemm_split.h"
+#include "row_io.h"
+#include "skinny_core.h"
+
+namespace bitnet {
+
+hipError_t take_gated_split_timeouts(unsigned int* count) { return take_local_split_timeouts(count); }
+
+static int64_t n_half(int64_t N) { return (N + 63) / 64 * 64; }
+size_t gated_slopes_bytes(int64_t M, int64_t N) { return (size_t)M * 2 * n_half(N) * 3; }
+
+// P: the codes [2N][Kp/4], gate rows first. Row r of tile ti (row0 = 256 ti): wave
+// half r / 128, then 64 gate rows and 64 up rows of outputs
+// 128 ti + 64 (r / 128) + r % 64.
+struct GatedCodesLoader : RowCodesLoader<CodesI8Frags> {
+  int64_t N;
+  __device__ __forceinline__ void load(Regs& r, int row0, int s) const {
+    const int t = threadIdx.x;
+    const int64_t n = row0 / 2 + 64 * (t >> 7) + (t & 63);
+    const rsrc_t rs = make_rsrc(packed, (uint32_t)(rows * pitch));
+    r.lane_off = n < N ? (uint32_t)(((t & 64) ? N + n : n) * pitch) : kOob;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) r.v[h] = buf_load16(rs, offset(r, s, h));
+  }
+};
+
+// LDS staging of 32 output rows x 64 columns of bf16 (EpStage's scheme): a lane
+// puts 4 values of row l % 32 at column 32fi + 8g + 4(l / 32), and every wave
+// store is 8 rows of 128 bytes.
+struct HalfStage {
+  static constexpr int kPitch = 128 + 16;
+  static constexpr int kBytes = 32 * kPitch;
+  static __device__ __forceinline__ void put(char* w, int lane, int fi, int g, uint2 v) {
+    *reinterpret_cast<uint2*>(w + (lane & 31) * kPitch + 8 * (lane >> 5) + (32 * fi + 8 * g) * 2) = v;
+  }
+  // Rows j0 .. j0 + 31 (those below J), columns i0 .. i0 + 63 (those below I) of
+  // out [J][ld]. i0, j0 are uniform in the wave; 32 * ld * 2 < 2^31.
+  static __device__ __forceinline__ void drain(const char* w, uint16_t* out, int64_t ld, int64_t I, int64_t J, int i0,
+                                               int j0, int lane) {
+    i0 = __builtin_amdgcn_readfirstlane(i0);
+    j0 = __builtin_amdgcn_readfirstlane(j0);
+    int c = lane & 7, rl = lane >> 3;
+    asm volatile("" : "+v"(c), "+v"(rl));  // as EpStage::drain
+    const char* src = w + rl * kPitch + 16 * c;
+    uint4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const uint4*>(src + 8 * k * kPitch);
+    const int rows_in = J - j0 < 32 ? (int)(J - j0) : 32;
+    if (((ld | I) & 7) == 0) {
+      const uint32_t row_b = (uint32_t)ld * 2;
+      const rsrc_t rs = make_rsrc(out + (int64_t)j0 * ld + i0, 32u * row_b);
+      const uint32_t lane_off = i0 + 8 * c < I ? rl * row_b + 16 * c : kOob;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        buf_store16_stream(rs, rl < rows_in - 8 * k ? lane_off : kOob, (uint32_t)(8 * k) * row_b, v[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (8 * k + rl >= rows_in) continue;
+        uint16_t* row = out + (int64_t)(j0 + 8 * k + rl) * ld + i0 + 8 * c;
+        const int64_t n = I - (i0 + 8 * c);  // values of this chunk inside the row
+        if (n >= 8) {
+          memcpy(row, &v[k], 16);
+        } else {
+          const uint32_t wv[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (e < n) row[e] = (uint16_t)(wv[e >> 1] >> (16 * (e & 1)));
+        }
+      }
+    }
+  }
+};
+
+// The same for the slopes' low bytes: 32 rows x 64 bytes, a lane's 4 values one
+// dword, every wave store 16 rows of 64 bytes (ld, I multiples of 64).
+struct ByteStage {
+  static constexpr int kPitch = 64 + 16;
+  static constexpr int kBytes = 32 * kPitch;
+  static __device__ __forceinline__ void put(char* w, int lane, int fi, int g, uint32_t v) {
+    *reinterpret_cast<uint32_t*>(w + (lane & 31) * kPitch + 4 * (lane >> 5) + 32 * fi + 8 * g) = v;
+  }
+  static __device__ __forceinline__ void drain(const char* w, uint8_t* out, int64_t ld, int64_t I, int64_t J, int i0,
+                                               int j0, int lane) {
+    i0 = __builtin_amdgcn_readfirstlane(i0);
+    j0 = __builtin_amdgcn_readfirstlane(j0);
+    const int c = lane & 3, rl = lane >> 2;
+    const char* src = w + rl * kPitch + 16 * c;
+    const uint4 v[2] = {*reinterpret_cast<const uint4*>(src), *reinterpret_cast<const uint4*>(src + 16 * kPitch)};
+    const int rows_in = J - j0 < 32 ? (int)(J - j0) : 32;
+    const rsrc_t rs = make_rsrc(out + (int64_t)j0 * ld + i0, 32u * (uint32_t)ld);
+    const uint32_t lane_off = i0 + 16 * c < I ? rl * (uint32_t)ld + 16 * c : kOob;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      buf_store16_stream(rs, rl < rows_in - 16 * k ? lane_off : kOob, (uint32_t)(16 * k) * (uint32_t)ld, v[k]);
+  }
+};
+
+// A slope is kept as the upper 16 bits of its fp32 value and the 8 bits below
+// them, in two planes: [M][2 Nd] of 16 bits, then [M][2 Nd] bytes.
+__device__ __forceinline__ uint2 slopes_hi(const float (&v)[4]) {
+  return make_uint2(perm(__float_as_uint(v[1]), __float_as_uint(v[0]), 0x07060302u),
+                    perm(__float_as_uint(v[3]), __float_as_uint(v[2]), 0x07060302u));
+}
+__device__ __forceinline__ uint32_t slopes_lo(const float (&v)[4]) {
+  return perm(perm(__float_as_uint(v[3]), __float_as_uint(v[2]), 0x0C0C0501u),
+              perm(__float_as_uint(v[1]), __float_as_uint(v[0]), 0x0C0C0501u), 0x05040100u);
+}
+__device__ __forceinline__ void slopes8(uint4 hi, uint2 lo, float (&f)[8]) {
+  const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[2] = {lo.x, lo.y};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    f[e] = __uint_as_float(((e & 1) ? h[e >> 1] & 0xFFFF0000u : h[e >> 1] << 16) | ((l[e >> 2] >> (8 * (e & 3))) & 0xFFu) << 8);
+}
+
+// y = act(g) u and, with SLOPES, dy/dg and dy/du.
+template <class ACT, bool SLOPES>
+__device__ __forceinline__ void gated_value(float g, float u, float& y, float& dg, float& du) {
+  if constexpr (SLOPES) {
+    float da;
+    ACT::fd(g, du, da);
+    dg = da * u;
+    y = du * u;
+  } else {
+    y = ACT::f(g) * u;
+  }
+}
+
+// acc: fragments fi 0, 1 hold the gate, 2, 3 the up projection of the same
+// outputs. SAVE: the slopes are stored too, [M][2 Nd].
+template <class ACT, bool SAVE>
+struct GatedEpilogue {
+  uint16_t* y;    // [M][N]
+  uint16_t* slopes;
+  const float* s;
+  const float* gamma;  // [2]
+  int64_t N, Nd, M;
+
+  struct Pre { float gg, gu; float sj[kFJ]; };
+  static constexpr int kDg = HalfStage::kBytes, kDu = 2 * HalfStage::kBytes;  // LDS offsets
+  static constexpr int kDgLo = 3 * HalfStage::kBytes, kDuLo = kDgLo + ByteStage::kBytes;
+  static constexpr int kWaveLds = kDuLo + ByteStage::kBytes;
+  __device__ __forceinline__ Pre prefetch(int j0, int lane) const {
+    Pre pre;
+    pre.gg = gamma[0];
+    pre.gu = gamma[1];
+#pragma unroll
+    for (int fj = 0; fj < kFJ; ++fj) {
+      const int64_t j = j0 + 32 * fj + (lane & 31);
+      pre.sj[fj] = j < M ? s[j] : 0.0f;
+    }
+    return pre;
+  }
+  __device__ __forceinline__ void store(MfmaI8::Acc (&acc)[kFI][kFJ], const Pre& pre, int i0, int j0, int lane,
+                                        char* wlds) const {
+    const int n0 = i0 / 2;
+#pragma unroll
+    for (int fj = 0; fj < kFJ; ++fj) {
+      const float cg = pre.sj[fj] * pre.gg / 127.0f, cu = pre.sj[fj] * pre.gu / 127.0f;
+#pragma unroll
+      for (int fi = 0; fi < 2; ++fi)
+#pragma unroll
+        for (int gi = 0; gi < 4; ++gi) {
+          float dg[4], du[4], y4[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            gated_value<ACT, SAVE>((float)acc[fi][fj][4 * gi + e] * cg, (float)acc[fi + 2][fj][4 * gi + e] * cu, y4[e],
+                                   dg[e], du[e]);
+          HalfStage::put(wlds, lane, fi, gi, make_uint2(pack_bf16x2(y4[0], y4[1]), pack_bf16x2(y4[2], y4[3])));
+          if constexpr (SAVE) {
+            HalfStage::put(wlds + kDg, lane, fi, gi, slopes_hi(dg));
+            HalfStage::put(wlds + kDu, lane, fi, gi, slopes_hi(du));
+            ByteStage::put(wlds + kDgLo, lane, fi, gi, slopes_lo(dg));
+            ByteStage::put(wlds + kDuLo, lane, fi, gi, slopes_lo(du));
+          }
+        }
+      HalfStage::drain(wlds, y, N, N, M, n0, j0 + 32 * fj, lane);
+      if constexpr (SAVE) {
+        uint8_t* lo = reinterpret_cast<uint8_t*>(slopes + M * 2 * Nd);
+        HalfStage::drain(wlds + kDg, slopes, 2 * Nd, Nd, M, n0, j0 + 32 * fj, lane);
+        HalfStage::drain(wlds + kDu, slopes + Nd, 2 * Nd, Nd, M, n0, j0 + 32 * fj, lane);
+        ByteStage::drain(wlds + kDgLo, lo, 2 * Nd, Nd, M, n0, j0 + 32 * fj, lane);
+        ByteStage::drain(wlds + kDuLo, lo + Nd, 2 * Nd, Nd, M, n0, j0 + 32 * fj, lane);
+      }
+    }
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Few tokens (M <= kSkinnyMaxM): skinny_kernels.hip's loop. A workgroup's 32 code
+// rows are 16 of the gate and the same 16 of the up projection.
+// ---------------------------------------------------------------------------
+
+template <class ACT, int MT, int W, int P>
+__global__ __launch_bounds__(kWave * W) void gated_skinny_kernel(SkArgs a, const float* __restrict__ s,
+                                                                 const float* __restrict__ gamma, int64_t N, int64_t Nd,
+                                                                 uint16_t* __restrict__ y, uint16_t* __restrict__ slopes) {
+  __shared__ __attribute__((aligned(16))) char smem[skinny_lds<MT, W>()];
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, h = lane >> 5;
+  const int64_t n0 = (int64_t)blockIdx.x * 16, nr = n0 + (lane & 15);
+  skinny_partials<SkFwd, MT, W, P>(a, nr < N ? ((lane & 16) ? N + nr : nr) : -1, smem);
+  // rows 8q + 4h + 0..3 of the tile: the gate's for q < 2, the up projection's for q + 2
+  const int q = wave % 2, mt = wave / 2;
+  const int64_t m = 32 * mt + (lane & 31);
+  if (mt >= MT || m >= a.M) return;
+  int vg[4], vu[4];
+  skinny_sum<SkFwd, MT, W>(smem, q, mt, vg);
+  skinny_sum<SkFwd, MT, W>(smem, q + 2, mt, vu);
+  const float cg = s[m] * gamma[0] / 127.0f, cu = s[m] * gamma[1] / 127.0f;  // the large-M epilogue's expressions
+  const int64_t nb = n0 + 8 * q + 4 * h;
+  float dg[4], du[4], o[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) gated_value<ACT, true>((float)vg[e] * cg, (float)vu[e] * cu, o[e], dg[e], du[e]);
+  uint16_t* yr = y + m * N;
+  if (N % 4 == 0 && nb + 4 <= N) {
+    *reinterpret_cast<uint2*>(yr + nb) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (nb + e < N) yr[nb + e] = f32_to_bf16_bits(o[e]);
+  }
+  if (slopes != nullptr) {  // the padding's columns up to Nd past the last workgroup's stay unwritten and are not read
+    uint16_t* r = slopes + m * 2 * Nd + nb;
+    uint8_t* lo = reinterpret_cast<uint8_t*>(slopes + a.M * 2 * Nd) + m * 2 * Nd + nb;
+    *reinterpret_cast<uint2*>(r) = slopes_hi(dg);
+    *reinterpret_cast<uint2*>(r + Nd) = slopes_hi(du);
+    *reinterpret_cast<uint32_t*>(lo) = slopes_lo(dg);
+    *reinterpret_cast<uint32_t*>(lo + Nd) = slopes_lo(du);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Backward, elementwise: D [M][2 Nd] from dY [M][N] and the slopes, times the
+// half's gamma and (sx not NULL) the token's sx/127. A thread takes 8 columns of
+// both halves; columns past N are zeros.
+// ---------------------------------------------------------------------------
+
+__global__ __launch_bounds__(256) void gated_dgrad_kernel(const uint16_t* __restrict__ dY,
+                                                          const uint16_t* __restrict__ slopes,
+                                                          const float* __restrict__ gamma, const float* __restrict__ sx,
+                                                          int64_t total, int N, int Nd, uint16_t* __restrict__ D) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= total) return;
+  const int nch = Nd / 8;
+  const int64_t row = i / nch;
+  const int k0 = 8 * (int)(i - row * nch);
+  const int64_t at = row * 2 * Nd + k0;
+  const int64_t src = k0 < N ? at : at - k0;  // past N: any written columns, not used
+  const uint8_t* lo = reinterpret_cast<const uint8_t*>(slopes + total * 16);  // total / nch rows of 2 Nd = 16 nch
+  const uint4 hg = *reinterpret_cast<const uint4*>(slopes + src), hu = *reinterpret_cast<const uint4*>(slopes + src + Nd);
+  const uint2 lg = *reinterpret_cast<const uint2*>(lo + src), lu = *reinterpret_cast<const uint2*>(lo + src + Nd);
+  float d[8], g[8], u[8];
+  chunk8(dY + row * N, k0, N).get(d);
+  slopes8(hg, lg, g);
+  slopes8(hu, lu, u);
+  const float sc = sx != nullptr ? sx[row] / 127.0f : 1.0f, gg = gamma[0] * sc, gu = gamma[1] * sc;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const bool in_row = k0 + e < N;  // a slope of the padding may be anything
+    g[e] = in_row ? d[e] * g[e] * gg : 0.0f;
+    u[e] = in_row ? d[e] * u[e] * gu : 0.0f;
+  }
+  store8_in(D + at, g);
+  store8_in(D + at + Nd, u);
+}
+
+// Both operands that the products rebuild, in one launch: the codes of both
+// weights transposed to fp4 [Kp][2 Nd / 2] (the first wt_bx * wt_by blocks) and
+// the int8 rows as bf16 [M][Kp] (the other xhat_nb).
+__global__ __launch_bounds__(256) void gated_prep_kernel(const uint8_t* __restrict__ packed, int64_t N, int64_t Kp,
+                                                         int64_t Nd, uint8_t* __restrict__ wt, int wt_bx, int wt_by,
+                                                         const int8_t* __restrict__ xq, int64_t M,
+                                                         uint16_t* __restrict__ xhat, int xhat_nb) {
+  const int b = blockIdx.x, nwt = wt_bx * wt_by;
+  if (b < nwt) {
+    const int v = xcd_major(b, nwt);
+    const auto row = [N, Nd](int64_t n) {
+      const int64_t c = n < Nd ? n : n - Nd;
+      return c < N ? (n < Nd ? c : N + c) : int64_t(-1);
+    };
+    wt_fp4_block(packed, row, Kp, 2 * Nd, wt, v % wt_bx, v / wt_bx);
+  } else {
+    xhat_blocks(xq, nullptr, M, Kp, xhat, b - nwt, xhat_nb);
+  }
+}
+
+// dX: a token's row is divided by the s/127 in D (s NULL: none is).
+struct TokenEpilogue {
+  uint16_t* out;  // [J][I]
+  const float* s;
+  int64_t I, J;   // K, M
+
+  struct Pre { float c[kFJ]; };
+  static constexpr int kWaveLds = EpStage<2>::kWaveBytes;
+  __device__ __forceinline__ Pre prefetch(int j0, int lane) const {
+    Pre pre;
+#pragma unroll
+    for (int fj = 0; fj < kFJ; ++fj) {
+      const int64_t j = j0 + 32 * fj + (lane & 31);
+      pre.c[fj] = s != nullptr && j < J ? 127.0f / s[j] : 1.0f;
+    }
+    return pre;
+  }
+  __device__ __forceinline__ void store(MfmaBf16::Acc (&acc)[kFI][kFJ], const Pre& pre, int i0, int j0, int lane,
+                                        char* wlds) const {
+#pragma unroll
+    for (int fj = 0; fj < kFJ; ++fj) {
+      const float c = pre.c[fj];
+#pragma unroll
+      for (int fi = 0; fi < kFI; ++fi)
+#pragma unroll
+        for (int gi = 0; gi < 4; ++gi)
+          EpStage<2>::put(wlds, lane, fi, gi,
+                          make_uint2(pack_bf16x2(acc[fi][fj][4 * gi] * c, acc[fi][fj][4 * gi + 1] * c),
+                                     pack_bf16x2(acc[fi][fj][4 * gi + 2] * c, acc[fi][fj][4 * gi + 3] * c)));
+      EpStage<2>::drain(wlds, reinterpret_cast<char*>(out), I, J, i0, j0 + 32 * fj, lane);
+    }
+  }
+};
+
+// dW of both halves: rows j < Nd go to out[0], the others to out[1], divided by
+// the half's scale (in D).
+template <bool OUT_F32>
+struct HalvesEpilogue {
+  void* out[2];
+  const float* gamma;  // [2]
+  int64_t I, N, Nd;    // outputs [N][I]
+
+  struct Pre { float g[2]; };
+  static constexpr int kEB = OUT_F32 ? 4 : 2;
+  static constexpr int kWaveLds = EpStage<kEB>::kWaveBytes;
+  __device__ __forceinline__ Pre prefetch(int, int) const { return Pre{{gamma[0], gamma[1]}}; }
+  __device__ __forceinline__ void store(MfmaBf16::Acc (&acc)[kFI][kFJ], const Pre& pre, int i0, int j0, int lane,
+                                        char* wlds) const {
+#pragma unroll
+    for (int fj = 0; fj < kFJ; ++fj) {
+      const int j = __builtin_amdgcn_readfirstlane(j0 + 32 * fj);
+      const bool up = j >= Nd;  // of all 32 rows: Nd is a multiple of 64
+      const int jh = up ? (int)(j - Nd) : j;
+      if (jh >= N) continue;
+      const float sc = 1.0f / (up ? pre.g[1] : pre.g[0]);
+#pragma unroll
+      for (int fi = 0; fi < kFI; ++fi)
+#pragma unroll
+        for (int gi = 0; gi < 4; ++gi) {
+          const float v0 = acc[fi][fj][4 * gi] * sc, v1 = acc[fi][fj][4 * gi + 1] * sc;
+          const float v2 = acc[fi][fj][4 * gi + 2] * sc, v3 = acc[fi][fj][4 * gi + 3] * sc;
+          if constexpr (OUT_F32)
+            EpStage<4>::put(wlds, lane, fi, gi, make_uint4(__float_as_uint(v0), __float_as_uint(v1),
+                                                           __float_as_uint(v2), __float_as_uint(v3)));
+          else
+            EpStage<2>::put(wlds, lane, fi, gi, make_uint2(pack_bf16x2(v0, v1), pack_bf16x2(v2, v3)));
+        }
+      EpStage<kEB>::drain(wlds, static_cast<char*>(out[up]), I, N, i0, jh, lane);
+    }
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Launches
+// ---------------------------------------------------------------------------
+
+static bool few(int64_t M) {
+  return M <= kSkinnyMaxM && test_knobs().no_skinny.load(std::memory_order_relaxed) == 0;
+}
+
+static GemmShape fwd_shape(int64_t M, int64_t N, int64_t K) {
+  return {(N + 127) / 128, (M + kBJ - 1) / kBJ, (k_pad(K) + kStageBytes - 1) / kStageBytes, kFwdPieceCost};
+}
+
+size_t gated_fwd_workspace(int64_t M, int64_t N, int64_t K) {
+  if (few(M)) return 0;
+  const GemmShape g = fwd_shape(M, N, K);
+  return split_workspace(g, split_grid(g, device_cus()));
+}
+
+template <class ACT>
+static hipError_t gated_fwd(const int8_t* x_q, const float* s_x, const uint8_t* w_packed, const float* gamma, int64_t M,
+                            int64_t N, int64_t K, uint16_t* y, uint16_t* slopes, void* ws, size_t ws_bytes,
+                            hipStream_t stream) {
+  const int64_t Kp = k_pad(K), Nd = n_half(N);
+  if (few(M)) {
+    const SkArgs a{w_packed, 2 * N, Kp / 4, Kp / 4, x_q, Kp, Kp, (int)M, 0u, 0u};
+    const unsigned grid = (unsigned)((N + 15) / 16);
+    if (M <= 32) gated_skinny_kernel<ACT, 1, 16, 3><<<grid, kWave * 16, 0, stream>>>(a, s_x, gamma, N, Nd, y, slopes);
+    else gated_skinny_kernel<ACT, 2, 8, 3><<<grid, kWave * 8, 0, stream>>>(a, s_x, gamma, N, Nd, y, slopes);
+    return hipGetLastError();
+  }
+  GatedCodesLoader pl;
+  pl.packed = w_packed;
+  pl.pitch = Kp / 4;
+  pl.rows = 2 * N;
+  pl.N = N;
+  const CopyLoader<1, true> ql{reinterpret_cast<const char*>(x_q), Kp, M, Kp};
+  const GemmShape g = fwd_shape(M, N, K);
+  if (slopes != nullptr)
+    return run_gemm<MfmaI8, 1>(pl, ql, GatedEpilogue<ACT, true>{y, slopes, s_x, gamma, N, Nd, M}, g, ws, ws_bytes, stream);
+  return run_gemm<MfmaI8, 1>(pl, ql, GatedEpilogue<ACT, false>{y, nullptr, s_x, gamma, N, Nd, M}, g, ws, ws_bytes, stream);
+}
+
+hipError_t launch_gated_fwd(bool relu2, const int8_t* x_q, const float* s_x, const uint8_t* w_packed, const float* gamma,
+                            int64_t M, int64_t N, int64_t K, uint16_t* y, uint16_t* slopes, void* ws, size_t ws_bytes,
+                            hipStream_t stream) {
+  return relu2 ? gated_fwd<ActRelu2>(x_q, s_x, w_packed, gamma, M, N, K, y, slopes, ws, ws_bytes, stream)
+               : gated_fwd<ActSilu>(x_q, s_x, w_packed, gamma, M, N, K, y, slopes, ws, ws_bytes, stream);
+}
+
+// The backward's workspace: D, the transposed codes, x_hat, then the products'
+// split tiles.
+struct GatedWs {
+  size_t d, wt, xhat, split;
+};
+static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+static GatedWs gated_ws(int64_t M, int64_t N, int64_t K) {
+  const int64_t Kp = k_pad(K), Nd = n_half(N);
+  const GemmShape g1 = shape_of(GemmKind::kBwdDx, M, 2 * Nd, K), g2 = shape_of(GemmKind::kBwdDw, M, 2 * Nd, K);
+  const int cus = device_cus();
+  const PairPlan pp = plan_pair(g1, g2, cus, kDxCosts, kDwCosts);
+  return {up256((size_t)M * 4 * Nd), up256((size_t)Kp * Nd), up256((size_t)M * Kp * 2),
+          std::max(pp.k1 == 0 ? 0 : pp.s1 + pp.s2,
+                   std::max(split_workspace(g1, split_grid(g1, cus)), split_workspace(g2, split_grid(g2, cus))))};
+}
+size_t gated_bwd_workspace(int64_t M, int64_t N, int64_t K) {
+  const GatedWs w = gated_ws(M, N, K);
+  return w.d + w.wt + w.xhat + w.split;
+}
+
+// As gemm_kernels.hip's rule for its own pair: both products split on the whole
+// device under a 3-stage piece cost.
+static bool pair_pays(GemmShape dx, GemmShape dw) {
+  dx.overhead = dw.overhead = 3;
+  return split_pays(dx, device_cus()) > 0 && split_pays(dw, device_cus()) > 0;
+}
+
+template <bool OUT_F32>
+static hipError_t gated_products(const uint16_t* D, const uint8_t* wt, const uint16_t* xhat, const float* gamma,
+                                 const float* s_x, int64_t M, int64_t N, int64_t K, uint16_t* dX, void* dWg, void* dWu, char* ws,
+                                 size_t ws_bytes, hipStream_t stream) {
+  const int64_t Kp = k_pad(K), Nd = n_half(N), J = 2 * Nd;
+  const GemmShape g1 = shape_of(GemmKind::kBwdDx, M, J, K), g2 = shape_of(GemmKind::kBwdDw, M, J, K);
+  const RowCodesLoader<CodesFp4Frags> p1{wt, J / 2, Kp};
+  const CopyLoader<2, true> q1{reinterpret_cast<const char*>(D), 2 * J, M, 2 * J};
+  const TokenEpilogue e1{dX, s_x, K, M};
+  const RowCopyBf16Loader<1> p2{xhat, Kp, M, Kp};
+  const RowCopyBf16Loader<5> q2{D, J, M, J};
+  const HalvesEpilogue<OUT_F32> e2{{dWg, dWu}, gamma, K, N, Nd};
+  if (dX != nullptr && dWg != nullptr && !few(M) && pair_pays(g1, g2)) {
+    const hipError_t e = run_pair<1, 0>(p1, q1, e1, g1, kDxCosts, p2, q2, e2, g2, kDwCosts, ws, ws_bytes, stream);
+    if (e != hipErrorNotSupported) return e;
+  }
+  if (dX != nullptr) {
+    const hipError_t e = few(M) ? launch_dx_skinny(wt, D, nullptr, s_x, M, J, K, dX, stream)
+                                : run_gemm<MfmaBf16, 1>(p1, q1, e1, g1, ws, ws_bytes, stream);
+    if (e != hipSuccess) return e;
+  }
+  return dWg != nullptr ? run_gemm<MfmaBf16, 0>(p2, q2, e2, g2, ws, ws_bytes, stream) : hipSuccess;
+}
+
+hipError_t launch_gated_bwd(const uint16_t* dY, const uint16_t* slopes, const int8_t* x_q, const float* s_x,
+                            const uint8_t* w_packed, const float* gamma, int64_t M, int64_t N, int64_t K, uint16_t* dX,
+                            void* dWg, void* dWu, bool dw_f32, void* ws, size_t ws_bytes, hipStream_t stream) {
+  const int64_t Kp = k_pad(K), Nd = n_half(N);
+  const GatedWs w = gated_ws(M, N, K);
+  char* base = static_cast<char*>(ws);
+  uint16_t* D = reinterpret_cast<uint16_t*>(base);
+  uint8_t* wt = reinterpret_cast<uint8_t*>(base + w.d);
+  uint16_t* xhat = reinterpret_cast<uint16_t*>(base + w.d + w.wt);
+  char* split = base + w.d + w.wt + w.xhat;
+  const size_t split_bytes = ws_bytes - (w.d + w.wt + w.xhat);
+
+  const int64_t total = M * (Nd / 8);
+  const unsigned grid = (unsigned)((total + 255) / 256);
+  gated_dgrad_kernel<<<grid, 256, 0, stream>>>(dY, slopes, gamma, s_x, total, (int)N, (int)Nd, D);
+  if (hipError_t e = hipGetLastError()) return e;
+
+  const int wt_bx = dX != nullptr ? (int)(Kp / 64) : 0, wt_by = (int)((2 * Nd + 255) / 256);
+  const int64_t want = (M * (Kp / 16) + 255) / 256;
+  const int xhat_nb = dWg != nullptr ? (int)std::min<int64_t>(want, 4096) : 0;
+  gated_prep_kernel<<<wt_bx * wt_by + xhat_nb, 256, 0, stream>>>(w_packed, N, Kp, Nd, wt, wt_bx, wt_by, x_q, M, xhat,
+                                                                 xhat_nb);
+  if (hipError_t e = hipGetLastError()) return e;
+  return dw_f32 ? gated_products<true>(D, wt, xhat, gamma, s_x, M, N, K, dX, dWg, dWu, split, split_bytes, stream)
+                : gated_products<false>(D, wt, xhat, gamma, s_x, M, N, K, dX, dWg, dWu, split, split_bytes, stream);
+}
+
+}  // namespace bitnet

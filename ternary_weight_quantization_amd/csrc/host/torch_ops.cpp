@@ -1,7 +1,8 @@
 // The operators around the ternary linear layers as torch autograd functions
 // over the C ABI (include/bitnet.h): layer norm, 8-bit activation checkpoints,
-// the gated activation, the TTQ layer with its input kept in 8 bits, and the
-// linear layer with cross entropy.
+// the gated activation, the TTQ layer with its input kept in 8 bits, the
+// linear layer with cross entropy, the root-mean-square norm with 8-bit rows,
+// the gated pair of ternary projections and the linear layer in 8-bit integers.
 //
 // Only checks of arguments, allocation of outputs and workspaces, and calls of
 // libbitnet.so on the tensors' device and its current stream. They are C++
@@ -513,6 +514,697 @@ Tensor linear_cross_entropy(const Tensor& hidden, const Tensor& weight, const Te
   return reduce == BITNET_REDUCE_NONE && targets.dim() != 1 ? out.reshape(targets.sizes()) : out;
 }
 
+// --- 8-bit rows ----------------------------------------------------------------------
+
+// Rows of 8-bit codes with a scale each, as the functions take them: codes [M, Kp],
+// scales [M], and a carrier, a bf16 tensor of the shape [..., K] that the rows
+// stand for, whose strides are 0 (it holds no values, only the shape and the
+// place in the autograd graph that gradients of the rows' values go to).
+Tensor make_carrier(at::IntArrayRef shape, const Tensor& like) {
+  return at::empty_strided(shape, std::vector<int64_t>(shape.size(), 0), like.options().dtype(at::kBFloat16));
+}
+
+void check_rows(const char* what, const Tensor& carrier, const Tensor& codes, const Tensor& scales) {
+  TORCH_CHECK_TYPE(codes.scalar_type() == at::kChar && scales.scalar_type() == at::kFloat &&
+                       carrier.scalar_type() == at::kBFloat16,
+                   what, ": 8-bit rows have int8 codes and float32 scales, got ", codes.scalar_type(), " and ",
+                   scales.scalar_type());
+  check_activation(what, carrier);
+  const int64_t K = carrier.size(-1), M = carrier.numel() / K;
+  TORCH_CHECK_VALUE(codes.dim() == 2 && codes.size(0) == M && codes.size(1) == bitnet_k_pad(K) && scales.dim() == 1 &&
+                        scales.size(0) == M,
+                    what, ": not the 8-bit rows of ", carrier.sizes(), ": codes ", codes.sizes(), " and scales ",
+                    scales.sizes());
+  TORCH_CHECK_VALUE(codes.device() == carrier.device() && scales.device() == carrier.device(), what,
+                    ": codes and scales must be on ", carrier.device());
+}
+
+Tensor unpack_rows(const Tensor& carrier, const Tensor& codes, const Tensor& scales) {
+  const Tensor q = aligned(codes), s = scales.contiguous();
+  Tensor x = at::empty(carrier.sizes(), carrier.options());
+  if (x.numel() > 0) {
+    On on(q);
+    check(bitnet_rows_unpack(i8(q), f32(s), q.size(0), carrier.size(-1), bf16(x), on.stream));
+  }
+  return x;
+}
+
+struct UnpackRowsFn : torch::autograd::Function<UnpackRowsFn> {
+  static Tensor forward(AutogradContext*, const Tensor& carrier, const Tensor& codes, const Tensor& scales) {
+    return unpack_rows(carrier, codes, scales);
+  }
+  static variable_list backward(AutogradContext*, const variable_list& grads) {
+    check_backward();
+    return {grads[0], Tensor(), Tensor()};
+  }
+};
+
+Tensor rows_values(const Tensor& carrier, const Tensor& codes, const Tensor& scales) {
+  check_eager("dequantize", {&carrier, &codes, &scales});
+  check_rows("dequantize", carrier, codes, scales);
+  return wants_grad({&carrier}) ? UnpackRowsFn::apply(carrier, codes, scales) : unpack_rows(carrier, codes, scales);
+}
+
+// x of a layer as 8-bit rows: those given, or made of bf16 activations.
+struct Rows {
+  Tensor q, s, x2;  // x2: activations that are still to be quantized into q and s
+  int64_t M, K;
+  Rows(const Tensor& x, const Tensor& codes, const Tensor& scales) : K(x.size(-1)) {
+    M = x.numel() / K;
+    if (codes.defined()) {
+      q = aligned(codes);
+      s = aligned(scales);
+      return;
+    }
+    x2 = aligned(rows(x));
+    q = at::empty({M, bitnet_k_pad(K)}, x.options().dtype(at::kChar));
+    s = at::empty({M}, x.options().dtype(at::kFloat));
+  }
+  void quantize(void* stream) const {
+    if (x2.defined()) check(bitnet_act_quant(bf16(x2), M, K, i8(q), f32(s), stream));
+  }
+};
+
+void check_layer_input(const char* what, const Tensor& x, const Tensor& codes, const Tensor& scales) {
+  if (codes.defined() || scales.defined()) {
+    TORCH_CHECK_VALUE(codes.defined() && scales.defined(), what, ": codes and scales: both needed");
+    check_rows(what, x, codes, scales);
+  } else {
+    TORCH_CHECK_TYPE(x.scalar_type() == at::kBFloat16, what, " expects bf16 activations, got ", x.scalar_type());
+    check_activation(what, x);
+  }
+}
+
+std::vector<int64_t> with_last(at::IntArrayRef shape, int64_t n) {
+  std::vector<int64_t> s = shape.vec();
+  s.back() = n;
+  return s;
+}
+
+// --- root-mean-square norm -------------------------------------------------------------
+
+struct Rms {
+  Tensor x2, r2, w, h, y, q, s, rstd;
+  int64_t M, K;
+  // out undefined: 8-bit rows (y is their carrier)
+  Rms(const Tensor& x, const Tensor& weight, const Tensor& residual, double eps, optional<at::ScalarType> out, bool keep)
+      : x2(rows(x)), M(x2.size(0)), K(x2.size(1)) {
+    if (weight.defined()) w = weight.contiguous();
+    if (residual.defined()) {
+      r2 = rows(residual);
+      h = at::empty(x.sizes(), residual.options());
+    }
+    const auto o = x.options();
+    if (out.has_value()) {
+      y = at::empty(x.sizes(), o.dtype(*out));
+    } else {
+      y = make_carrier(x.sizes(), x);
+      q = at::empty({M, bitnet_k_pad(K)}, o.dtype(at::kChar));
+      s = at::empty({M}, o.dtype(at::kFloat));
+    }
+    if (keep) rstd = at::empty({M}, o.dtype(at::kFloat));
+    if (M == 0) return;
+    const bitnet_dtype xd = code(x2.scalar_type()), hd = r2.defined() ? code(r2.scalar_type()) : xd;
+    On on(x2);
+    check(bitnet_rmsnorm_fwd(ptr(x2), xd, ptr(r2), hd, ptr(w), w.defined() ? code(w.scalar_type()) : BITNET_F32, M, K,
+                             static_cast<float>(eps), ptr(h), out.has_value() ? ptr(y) : nullptr, code(y.scalar_type()),
+                             i8(q), f32(s), f32(rstd), on.stream));
+  }
+};
+
+// Outputs: y (or the rows' carrier), codes and scales (undefined without), h
+// (undefined without a residual).
+struct RmsNormFn : torch::autograd::Function<RmsNormFn> {
+  static variable_list forward(AutogradContext* ctx, const Tensor& x, const optional<Tensor>& weight,
+                               const optional<Tensor>& residual, double eps, bool quantize, at::ScalarType out) {
+    const Tensor r = residual.value_or(Tensor());
+    const Rms n(x, weight.value_or(Tensor()), r, eps, quantize ? optional<at::ScalarType>() : out, true);
+    ctx->save_for_backward({r.defined() ? n.h : n.x2, n.w, n.rstd});
+    ctx->set_materialize_grads(false);
+    ctx->saved_data["shape"] = x.sizes();
+    ctx->saved_data["x"] = static_cast<int64_t>(x.scalar_type());
+    ctx->saved_data["y"] = static_cast<int64_t>(n.y.scalar_type());
+    ctx->saved_data["quantize"] = quantize;
+    ctx->saved_data["w"] = weight.has_value();
+    ctx->saved_data["r"] = residual.has_value();
+    variable_list res{n.y};
+    if (quantize) {
+      ctx->mark_non_differentiable({n.q, n.s});
+      res.push_back(n.q);
+      res.push_back(n.s);
+    }
+    if (r.defined()) res.push_back(n.h);
+    return res;
+  }
+
+  static variable_list backward(AutogradContext* ctx, const variable_list& grads) {
+    check_backward();
+    const variable_list saved = ctx->get_saved_variables();
+    const Tensor &h = saved[0], &w = saved[1], &rstd = saved[2];
+    const std::vector<int64_t> shape = ctx->saved_data["shape"].toIntVector();
+    const auto xt = static_cast<at::ScalarType>(ctx->saved_data["x"].toInt());
+    const auto yt = static_cast<at::ScalarType>(ctx->saved_data["y"].toInt());
+    const bool quantize = ctx->saved_data["quantize"].toBool();
+    const bool has_w = ctx->saved_data["w"].toBool(), has_r = ctx->saved_data["r"].toBool();
+    const bool need_x = ctx->needs_input_grad(0), need_w = has_w && ctx->needs_input_grad(1);
+    const bool need_r = has_r && ctx->needs_input_grad(1 + has_w);
+    const auto ht = h.scalar_type();
+    const int64_t K = shape.back(), M = rstd.size(0);
+    Tensor dH = has_r ? grads[quantize ? 3 : 1] : Tensor();
+    Tensor dx, dr, dw;
+    const auto ho = h.options();
+    if (!grads[0].defined() || M == 0) {  // the norm's output was not used, or has no rows
+      if (need_w) dw = at::zeros({K}, w.options());
+      if (!dH.defined() && M == 0) dH = at::zeros(shape, ho);
+      if (dH.defined()) {
+        if (need_x) dx = dH.to(xt);
+        if (need_r) dr = dH.to(ht);
+      }
+      return {dx, dw, dr, Tensor(), Tensor(), Tensor()};
+    }
+    const Tensor dY = rows(grads[0].to(yt));
+    if (dH.defined()) dH = rows(dH.to(ht));
+    // one gradient for both where they are of one type
+    const bool split = xt != ht;
+    if ((need_x && !split) || need_r) dr = at::empty(shape, ho);
+    if (need_x) dx = split ? at::empty(shape, ho.dtype(xt)) : dr;
+    Tensor ws;
+    size_t bytes = 0;
+    if (need_w) {
+      dw = at::empty({K}, w.options());
+      bytes = bitnet_rmsnorm_workspace_bytes(M, K);
+      ws = scratch(bytes, dY);
+    }
+    On on(dY);
+    check(bitnet_rmsnorm_bwd(ptr(dY), code(yt), ptr(dH), ptr(h), code(ht), ptr(w),
+                             w.defined() ? code(w.scalar_type()) : BITNET_F32, f32(rstd), M, K, ptr(dr),
+                             split && need_x ? bf16(dx) : nullptr, ptr(dw), ptr(ws), bytes, on.stream));
+    return {dx, dw, need_r ? dr : Tensor(), Tensor(), Tensor(), Tensor()};
+  }
+};
+
+// (y or the rows' carrier, codes, scales, h), those that there are.
+std::tuple<Tensor, Tensor, Tensor, Tensor> rms_norm(const Tensor& x, const optional<Tensor>& weight,
+                                                    const optional<Tensor>& residual, double eps, bool quantize,
+                                                    at::ScalarType out) {
+  const Tensor w = weight.value_or(Tensor()), r = residual.value_or(Tensor());
+  check_eager("rms_norm", {&x, &w, &r});
+  TORCH_CHECK_TYPE(is_value(x.scalar_type()), "rms_norm expects bf16 or float32 activations, got ", x.scalar_type());
+  TORCH_CHECK_TYPE(is_value(out), "out_dtype: expected bfloat16 or float32, got ", out);
+  check_activation("rms_norm", x);
+  if (w.defined()) {
+    TORCH_CHECK_TYPE(is_value(w.scalar_type()), "weight: expected bf16 or float32, got ", w.scalar_type());
+    TORCH_CHECK_VALUE(w.dim() == 1 && w.size(0) == x.size(-1), "weight: expected shape [", x.size(-1), "], got ",
+                      w.sizes());
+    TORCH_CHECK_VALUE(w.device() == x.device(), "weight: on ", w.device(), ", expected ", x.device());
+  }
+  if (r.defined()) {
+    TORCH_CHECK_TYPE(is_value(r.scalar_type()), "residual: expected bf16 or float32, got ", r.scalar_type());
+    TORCH_CHECK_TYPE(x.scalar_type() == at::kBFloat16 || x.scalar_type() == r.scalar_type(),
+                     "x: expected bf16 or the residual's dtype, got ", x.scalar_type());
+    TORCH_CHECK_VALUE(r.sizes() == x.sizes(), "residual: expected shape ", x.sizes(), ", got ", r.sizes());
+    TORCH_CHECK_VALUE(r.device() == x.device(), "residual: on ", r.device(), ", expected ", x.device());
+  }
+  if (wants_grad({&x, &w, &r})) {
+    const variable_list o = RmsNormFn::apply(x, weight, residual, eps, quantize, out);
+    if (quantize) return {o[0], o[1], o[2], r.defined() ? o[3] : Tensor()};
+    return {o[0], Tensor(), Tensor(), r.defined() ? o[1] : Tensor()};
+  }
+  const Rms n(x, w, r, eps, quantize ? optional<at::ScalarType>() : out, false);
+  return {n.y, n.q, n.s, n.h};
+}
+
+// --- the gated pair of ternary projections ------------------------------------------------
+
+// Both weights' codes below each other and both scales; x is quantized in the
+// gate weight's launch where it still is to be.
+struct GatedState {
+  Tensor packed, gamma;
+  GatedState(const Rows& x, const Tensor& w_gate, const Tensor& w_up) {
+    const Tensor wg = aligned(w_gate), wu = aligned(w_up);
+    const int64_t N = wg.size(0), K = x.K, row = bitnet_k_pad(K) / 4;
+    packed = at::empty({2 * N, row}, wg.options().dtype(at::kByte));
+    gamma = at::empty({2}, wg.options().dtype(at::kFloat));
+    const size_t bytes = bitnet_ternarize_workspace_bytes(N, K);
+    const Tensor ws = scratch(bytes, wg);
+    uint8_t* p = static_cast<uint8_t*>(ptr(packed));
+    const bitnet_dtype gd = code(wg.scalar_type()), ud = code(wu.scalar_type());
+    On on(wg);
+    if (x.x2.defined() && x.M > 0)
+      check(bitnet_quantize(ptr(wg), gd, N, K, bf16(x.x2), x.M, p, f32(gamma), i8(x.q), f32(x.s), ptr(ws), bytes,
+                            on.stream));
+    else
+      check(bitnet_ternarize_pack(ptr(wg), gd, N, K, p, f32(gamma), ptr(ws), bytes, on.stream));
+    check(bitnet_ternarize_pack(ptr(wu), ud, N, K, p + N * row, f32(gamma) + 1, ptr(ws), bytes, on.stream));
+  }
+};
+
+Tensor gated_forward(const Rows& x, at::IntArrayRef shape, const Tensor& packed, const Tensor& gamma, int64_t act,
+                     const Tensor& slopes) {
+  const int64_t N = packed.size(0) / 2;
+  Tensor y = at::empty(with_last(shape, N), packed.options().dtype(at::kBFloat16));
+  if (x.M == 0) return y;
+  const size_t bytes = bitnet_gated_fwd_workspace_bytes(x.M, N, x.K);
+  const Tensor ws = scratch(bytes, packed);
+  On on(packed);
+  check(bitnet_gated_fwd(static_cast<bitnet_act>(act), i8(x.q), f32(x.s), static_cast<uint8_t*>(ptr(packed)), f32(gamma),
+                         x.M, N, x.K, bf16(y), ptr(slopes), bytes ? ptr(ws) : nullptr, bytes, on.stream));
+  return y;
+}
+
+Tensor empty_slopes(int64_t M, int64_t N, const Tensor& like) {
+  return scratch(bitnet_gated_slopes_bytes(M, N), like);
+}
+
+struct GatedGrads {
+  Tensor dx, dwg, dwu;
+};
+GatedGrads gated_backward(const Tensor& grad, const Tensor& slopes, const Tensor& q, const Tensor& s,
+                          const Tensor& packed, const Tensor& gamma, at::IntArrayRef shape, bool need_x,
+                          bool need_w, at::ScalarType wt) {
+  GatedGrads r;
+  const int64_t N = packed.size(0) / 2, K = shape.back(), M = q.size(0);
+  const Tensor dY = rows(grad.to(at::kBFloat16));
+  if (need_x) r.dx = at::empty(shape, dY.options());
+  if (need_w) {
+    const auto o = dY.options().dtype(wt);
+    r.dwg = M > 0 ? at::empty({N, K}, o) : at::zeros({N, K}, o);
+    r.dwu = M > 0 ? at::empty({N, K}, o) : at::zeros({N, K}, o);
+  }
+  if (M == 0 || (!need_x && !need_w)) return r;
+  const size_t bytes = bitnet_gated_bwd_workspace_bytes(M, N, K);
+  const Tensor ws = scratch(bytes, dY);
+  On on(dY);
+  check(bitnet_gated_bwd(bf16(dY), ptr(slopes), i8(q), f32(s),
+                         static_cast<uint8_t*>(ptr(packed)), f32(gamma), M, N, K, bf16(r.dx), ptr(r.dwg), ptr(r.dwu),
+                         code(wt), ptr(ws), bytes, on.stream));
+  return r;
+}
+
+struct GatedFn : torch::autograd::Function<GatedFn> {
+  static Tensor forward(AutogradContext* ctx, const Tensor& x, const optional<Tensor>& codes,
+                        const optional<Tensor>& scales, const Tensor& w_gate, const Tensor& w_up, int64_t act) {
+    const Rows r(x, codes.value_or(Tensor()), scales.value_or(Tensor()));
+    const GatedState st(r, w_gate, w_up);
+    const Tensor slopes = empty_slopes(r.M, w_gate.size(0), r.q);
+    Tensor y = gated_forward(r, x.sizes(), st.packed, st.gamma, act, slopes);
+    ctx->save_for_backward({slopes, r.q, r.s, st.packed, st.gamma});
+    ctx->saved_data["shape"] = x.sizes();
+    ctx->saved_data["wt"] = static_cast<int64_t>(w_gate.scalar_type());
+    ctx->saved_data["at"] = static_cast<int64_t>(codes.has_value() ? 3 : 1);  // the gate weight's place among the tensors
+    return y;
+  }
+  static variable_list backward(AutogradContext* ctx, const variable_list& grads) {
+    check_backward();
+    const variable_list v = ctx->get_saved_variables();
+    const int64_t at = ctx->saved_data["at"].toInt();
+    const bool need_g = ctx->needs_input_grad(at), need_u = ctx->needs_input_grad(at + 1);
+    const GatedGrads r = gated_backward(grads[0], v[0], v[1], v[2], v[3], v[4], ctx->saved_data["shape"].toIntVector(),
+                                        ctx->needs_input_grad(0), need_g || need_u,
+                                        static_cast<at::ScalarType>(ctx->saved_data["wt"].toInt()));
+    return {r.dx, Tensor(), Tensor(), need_g ? r.dwg : Tensor(), need_u ? r.dwu : Tensor(), Tensor()};
+  }
+};
+
+Tensor gated_bitlinear(const Tensor& x, const optional<Tensor>& codes, const optional<Tensor>& scales,
+                       const Tensor& w_gate, const Tensor& w_up, int64_t act) {
+  const Tensor q = codes.value_or(Tensor()), s = scales.value_or(Tensor());
+  check_eager("gated_bitlinear", {&x, &q, &s, &w_gate, &w_up});
+  check_layer_input("gated_bitlinear", x, q, s);
+  TORCH_CHECK_TYPE(is_value(w_gate.scalar_type()) && w_up.scalar_type() == w_gate.scalar_type(),
+                   "w_gate and w_up: expected bf16 or float32 and one dtype, got ", w_gate.scalar_type(), " and ",
+                   w_up.scalar_type());
+  TORCH_CHECK_VALUE(w_gate.dim() == 2 && w_gate.size(1) == x.size(-1) && w_gate.size(0) >= 1 &&
+                        w_up.sizes() == w_gate.sizes(),
+                    "w_gate and w_up: expected [out_features, ", x.size(-1), "] both, got ", w_gate.sizes(), " and ",
+                    w_up.sizes());
+  TORCH_CHECK_VALUE(w_gate.device() == x.device() && w_up.device() == x.device(),
+                    "x, w_gate and w_up: must be GPU tensors of one device");
+  if (wants_grad({&x, &w_gate, &w_up})) return GatedFn::apply(x, codes, scales, w_gate, w_up, act);
+  const Rows r(x, q, s);
+  const GatedState st(r, w_gate, w_up);
+  return gated_forward(r, x.sizes(), st.packed, st.gamma, act, Tensor());
+}
+
+// The same from the stored state; gradients of x alone.
+struct GatedFrozenFn : torch::autograd::Function<GatedFrozenFn> {
+  static Tensor forward(AutogradContext* ctx, const Tensor& x, const optional<Tensor>& codes,
+                        const optional<Tensor>& scales, const Tensor& packed, const Tensor& gamma, int64_t act) {
+    const Rows r(x, codes.value_or(Tensor()), scales.value_or(Tensor()));
+    const Tensor slopes = empty_slopes(r.M, packed.size(0) / 2, r.q);
+    if (r.M > 0) {
+      On on(r.q);
+      r.quantize(on.stream);
+    }
+    Tensor y = gated_forward(r, x.sizes(), packed, gamma, act, slopes);
+    ctx->save_for_backward({slopes, packed, gamma});
+    ctx->saved_data["m"] = r.M;
+    ctx->saved_data["shape"] = x.sizes();
+    return y;
+  }
+  static variable_list backward(AutogradContext* ctx, const variable_list& grads) {
+    check_backward();
+    const variable_list v = ctx->get_saved_variables();
+    const std::vector<int64_t> shape = ctx->saved_data["shape"].toIntVector();
+    const Tensor &slopes = v[0], &packed = v[1], &gamma = v[2];
+    const Tensor dY = rows(grads[0].to(at::kBFloat16));
+    const int64_t N = packed.size(0) / 2, K = shape.back(), M = ctx->saved_data["m"].toInt();
+    const Tensor dx = at::empty(shape, dY.options());
+    if (M > 0) {
+      const size_t bytes = bitnet_gated_bwd_workspace_bytes(M, N, K);
+      const Tensor ws = scratch(bytes, dY);
+      On on(dY);
+      check(bitnet_gated_bwd(bf16(dY), ptr(slopes), nullptr, nullptr,
+                             static_cast<uint8_t*>(ptr(packed)), f32(gamma), M, N, K, bf16(dx), nullptr, nullptr,
+                             BITNET_BF16, ptr(ws), bytes, on.stream));
+    }
+    return {dx, Tensor(), Tensor(), Tensor(), Tensor(), Tensor()};
+  }
+};
+
+Tensor gated_bitlinear_inference(const Tensor& x, const optional<Tensor>& codes, const optional<Tensor>& scales,
+                                 const Tensor& w_packed, const Tensor& gamma_, int64_t in_features, int64_t act) {
+  const Tensor q = codes.value_or(Tensor()), s = scales.value_or(Tensor());
+  check_eager("gated_bitlinear", {&x, &q, &s, &w_packed, &gamma_});
+  check_layer_input("gated_bitlinear", x, q, s);
+  TORCH_CHECK_VALUE(x.size(-1) == in_features, "x: expected a last dimension of ", in_features, ", got ", x.sizes());
+  TORCH_CHECK_TYPE(w_packed.scalar_type() == at::kByte && gamma_.scalar_type() == at::kFloat,
+                   "w_packed: expected uint8 and gamma float32, got ", w_packed.scalar_type(), " and ",
+                   gamma_.scalar_type());
+  TORCH_CHECK_VALUE(w_packed.dim() == 2 && w_packed.size(0) >= 2 && w_packed.size(0) % 2 == 0 &&
+                        w_packed.size(1) == bitnet_k_pad(in_features) / 4 && gamma_.dim() == 1 && gamma_.size(0) == 2,
+                    "w_packed: expected [2 out_features, ", bitnet_k_pad(in_features) / 4, "] and gamma [2], got ",
+                    w_packed.sizes(), " and ", gamma_.sizes());
+  TORCH_CHECK_VALUE(w_packed.device() == x.device() && gamma_.device() == x.device(),
+                    "x, w_packed and gamma: must be GPU tensors of one device");
+  const Tensor packed = aligned(w_packed), gamma = gamma_.contiguous();
+  if (wants_grad({&x})) return GatedFrozenFn::apply(x, codes, scales, packed, gamma, act);
+  const Rows r(x, q, s);
+  if (r.M > 0) {
+    On on(r.q);
+    r.quantize(on.stream);
+  }
+  return gated_forward(r, x.sizes(), packed, gamma, act, Tensor());
+}
+
+// --- linear layer in 8-bit integers -----------------------------------------------------------
+
+// The weight's rows as int8 with a scale each.
+std::pair<Tensor, Tensor> int8_weight(const Tensor& weight) {
+  const Tensor w = aligned(weight);
+  const int64_t N = w.size(0), K = w.size(1);
+  std::pair<Tensor, Tensor> r{at::empty({N, bitnet_k_pad(K)}, w.options().dtype(at::kChar)),
+                              at::empty({N}, w.options().dtype(at::kFloat))};
+  On on(w);
+  check(bitnet_rows_quant(ptr(w), code(w.scalar_type()), N, K, i8(r.first), f32(r.second), on.stream));
+  return r;
+}
+
+Tensor int8_forward(const Rows& x, at::IntArrayRef shape, const Tensor& wq, const Tensor& sw, const Tensor& bias) {
+  const int64_t N = wq.size(0);
+  Tensor y = at::empty(with_last(shape, N), wq.options().dtype(at::kBFloat16));
+  if (x.M == 0) return y;
+  const Tensor b = bias.defined() ? aligned(bias.to(at::kBFloat16)) : Tensor();
+  const size_t bytes = bitnet_int8_fwd_workspace_bytes(x.M, N, x.K);
+  const Tensor ws = scratch(bytes, wq);
+  On on(wq);
+  x.quantize(on.stream);
+  check(bitnet_int8_fwd(i8(x.q), f32(x.s), i8(wq), f32(sw), bf16(b), x.M, N, x.K, bf16(y), bytes ? ptr(ws) : nullptr,
+                        bytes, on.stream));
+  return y;
+}
+
+// dx, dw (undefined unless wanted) and the bias' gradient.
+void int8_backward(const Tensor& grad, const Tensor& q, const Tensor& s, const Tensor& wq, const Tensor& sw,
+                   at::IntArrayRef shape, Tensor* dx, Tensor* dw, at::ScalarType wt, Tensor* db, at::ScalarType bt) {
+  const int64_t N = wq.size(0), K = shape.back();
+  const Tensor dY = aligned(rows(grad.to(at::kBFloat16)));
+  const int64_t M = dY.size(0);
+  const auto o = dY.options();
+  if (dx) *dx = at::empty(shape, o);
+  if (M == 0) {
+    if (dw) *dw = at::zeros({N, K}, o.dtype(wt));
+    if (db) *db = at::zeros({N}, o.dtype(bt));
+    return;
+  }
+  if (dw) *dw = at::empty({N, K}, o.dtype(wt));
+  if (db) *db = at::empty({N}, o.dtype(bt));
+  On on(dY);
+  if (dx || dw) {
+    const size_t bytes = bitnet_int8_bwd_workspace_bytes(M, N, K);
+    const Tensor ws = scratch(bytes, dY);
+    check(bitnet_int8_bwd(bf16(dY), dw ? i8(q) : nullptr, dw ? f32(s) : nullptr, dx ? i8(wq) : nullptr,
+                          dx ? f32(sw) : nullptr, M, N, K, dx ? bf16(*dx) : nullptr, dw ? ptr(*dw) : nullptr, code(wt),
+                          ptr(ws), bytes, on.stream));
+  }
+  if (db) check(bitlinear_bias_grad(bf16(dY), M, N, ptr(*db), code(bt), on.stream));
+}
+
+struct Int8Fn : torch::autograd::Function<Int8Fn> {
+  static Tensor forward(AutogradContext* ctx, const Tensor& x, const optional<Tensor>& codes,
+                        const optional<Tensor>& scales, const Tensor& weight, const optional<Tensor>& bias) {
+    const Rows r(x, codes.value_or(Tensor()), scales.value_or(Tensor()));
+    const auto w = int8_weight(weight);
+    Tensor y = int8_forward(r, x.sizes(), w.first, w.second, bias.value_or(Tensor()));
+    ctx->save_for_backward({r.q, r.s, w.first, w.second});
+    ctx->saved_data["shape"] = x.sizes();
+    ctx->saved_data["wt"] = static_cast<int64_t>(weight.scalar_type());
+    ctx->saved_data["bt"] = static_cast<int64_t>(bias.has_value() ? bias->scalar_type() : at::kBFloat16);
+    ctx->saved_data["b"] = bias.has_value();
+    ctx->saved_data["at"] = static_cast<int64_t>(codes.has_value() ? 3 : 1);  // the weight's place among the tensors
+    return y;
+  }
+  static variable_list backward(AutogradContext* ctx, const variable_list& grads) {
+    check_backward();
+    const variable_list v = ctx->get_saved_variables();
+    const int64_t at = ctx->saved_data["at"].toInt();
+    const bool need_x = ctx->needs_input_grad(0), need_w = ctx->needs_input_grad(at);
+    const bool need_b = ctx->saved_data["b"].toBool() && ctx->needs_input_grad(at + 1);
+    Tensor dx, dw, db;
+    int8_backward(grads[0], v[0], v[1], v[2], v[3], ctx->saved_data["shape"].toIntVector(), need_x ? &dx : nullptr,
+                  need_w ? &dw : nullptr, static_cast<at::ScalarType>(ctx->saved_data["wt"].toInt()),
+                  need_b ? &db : nullptr, static_cast<at::ScalarType>(ctx->saved_data["bt"].toInt()));
+    return {dx, Tensor(), Tensor(), dw, db};
+  }
+};
+
+// The same from the stored state; gradients of x and the bias.
+struct Int8FrozenFn : torch::autograd::Function<Int8FrozenFn> {
+  static Tensor forward(AutogradContext* ctx, const Tensor& x, const optional<Tensor>& codes,
+                        const optional<Tensor>& scales, const Tensor& wq, const Tensor& sw, const optional<Tensor>& bias) {
+    const Rows r(x, codes.value_or(Tensor()), scales.value_or(Tensor()));
+    Tensor y = int8_forward(r, x.sizes(), wq, sw, bias.value_or(Tensor()));
+    ctx->save_for_backward({wq, sw});
+    ctx->saved_data["shape"] = x.sizes();
+    ctx->saved_data["bt"] = static_cast<int64_t>(bias.has_value() ? bias->scalar_type() : at::kBFloat16);
+    ctx->saved_data["b"] = static_cast<int64_t>(bias.has_value() ? (codes.has_value() ? 5 : 3) : 0);
+    return y;
+  }
+  static variable_list backward(AutogradContext* ctx, const variable_list& grads) {
+    check_backward();
+    const variable_list v = ctx->get_saved_variables();
+    const int64_t b = ctx->saved_data["b"].toInt();
+    const bool need_x = ctx->needs_input_grad(0), need_b = b > 0 && ctx->needs_input_grad(b);
+    Tensor dx, db;
+    int8_backward(grads[0], Tensor(), Tensor(), v[0], v[1], ctx->saved_data["shape"].toIntVector(),
+                  need_x ? &dx : nullptr, nullptr, at::kBFloat16, need_b ? &db : nullptr,
+                  static_cast<at::ScalarType>(ctx->saved_data["bt"].toInt()));
+    return {dx, Tensor(), Tensor(), Tensor(), Tensor(), db};
+  }
+};
+
+void check_bias(const Tensor& b, int64_t N, const Tensor& x) {
+  if (!b.defined()) return;
+  TORCH_CHECK_TYPE(is_value(b.scalar_type()), "bias: expected bf16 or float32, got ", b.scalar_type());
+  TORCH_CHECK_VALUE(b.dim() == 1 && b.size(0) == N, "bias: expected shape [", N, "], got ", b.sizes());
+  TORCH_CHECK_VALUE(b.device() == x.device(), "bias: on ", b.device(), ", expected ", x.device());
+}
+
+Tensor int8_linear(const Tensor& x, const optional<Tensor>& codes, const optional<Tensor>& scales, const Tensor& weight,
+                   const optional<Tensor>& bias) {
+  const Tensor q = codes.value_or(Tensor()), s = scales.value_or(Tensor()), b = bias.value_or(Tensor());
+  check_eager("int8_linear", {&x, &q, &s, &weight, &b});
+  check_layer_input("int8_linear", x, q, s);
+  TORCH_CHECK_TYPE(is_value(weight.scalar_type()), "weight: expected bf16 or float32, got ", weight.scalar_type());
+  TORCH_CHECK_VALUE(weight.dim() == 2 && weight.size(1) == x.size(-1) && weight.size(0) >= 1,
+                    "weight: expected [out_features, ", x.size(-1), "], got ", weight.sizes());
+  TORCH_CHECK_VALUE(weight.device() == x.device(), "x and weight: must be GPU tensors of one device");
+  check_bias(b, weight.size(0), x);
+  if (wants_grad({&x, &weight, &b})) return Int8Fn::apply(x, codes, scales, weight, bias);
+  const auto w = int8_weight(weight);
+  return int8_forward(Rows(x, q, s), x.sizes(), w.first, w.second, b);
+}
+
+Tensor int8_linear_inference(const Tensor& x, const optional<Tensor>& codes, const optional<Tensor>& scales,
+                             const Tensor& w_q, const Tensor& s_w, int64_t in_features, const optional<Tensor>& bias) {
+  const Tensor q = codes.value_or(Tensor()), s = scales.value_or(Tensor()), b = bias.value_or(Tensor());
+  check_eager("int8_linear", {&x, &q, &s, &w_q, &s_w, &b});
+  check_layer_input("int8_linear", x, q, s);
+  TORCH_CHECK_VALUE(x.size(-1) == in_features, "x: expected a last dimension of ", in_features, ", got ", x.sizes());
+  TORCH_CHECK_TYPE(w_q.scalar_type() == at::kChar && s_w.scalar_type() == at::kFloat,
+                   "w_q: expected int8 and s_w float32, got ", w_q.scalar_type(), " and ", s_w.scalar_type());
+  TORCH_CHECK_VALUE(w_q.dim() == 2 && w_q.size(0) >= 1 && w_q.size(1) == bitnet_k_pad(in_features) && s_w.dim() == 1 &&
+                        s_w.size(0) == w_q.size(0),
+                    "w_q: expected [out_features, ", bitnet_k_pad(in_features), "] and s_w [out_features], got ",
+                    w_q.sizes(), " and ", s_w.sizes());
+  TORCH_CHECK_VALUE(w_q.device() == x.device() && s_w.device() == x.device(),
+                    "x, w_q and s_w: must be GPU tensors of one device");
+  check_bias(b, w_q.size(0), x);
+  const Tensor wq = aligned(w_q), sw = aligned(s_w);
+  if (wants_grad({&x, &b})) return Int8FrozenFn::apply(x, codes, scales, wq, sw, bias);
+  return int8_forward(Rows(x, q, s), x.sizes(), wq, sw, b);
+}
+
+// The stored state of a weight, for the inference form.
+std::pair<Tensor, Tensor> int8_quantize_weight(const Tensor& weight) {
+  check_eager("int8_linear", {&weight});
+  TORCH_CHECK_TYPE(is_value(weight.scalar_type()), "weight: expected bf16 or float32, got ", weight.scalar_type());
+  TORCH_CHECK_VALUE(weight.dim() == 2 && weight.numel() > 0 && weight.is_cuda(),
+                    "weight: expected a GPU tensor [out_features, in_features], got ", weight.sizes());
+  at::NoGradGuard off;
+  return int8_weight(weight);
+}
+
+// --- the ternary layer of 8-bit rows ---------------------------------------------------------
+
+struct Ternary {
+  Tensor packed, gamma;
+  explicit Ternary(const Tensor& weight) {
+    const Tensor w = aligned(weight);
+    const int64_t N = w.size(0), K = w.size(1);
+    packed = at::empty({N, bitnet_k_pad(K) / 4}, w.options().dtype(at::kByte));
+    gamma = at::empty({1}, w.options().dtype(at::kFloat));
+    const size_t bytes = bitnet_ternarize_workspace_bytes(N, K);
+    const Tensor ws = scratch(bytes, w);
+    On on(w);
+    check(bitnet_ternarize_pack(ptr(w), code(w.scalar_type()), N, K, static_cast<uint8_t*>(ptr(packed)), f32(gamma),
+                                ptr(ws), bytes, on.stream));
+  }
+};
+
+Tensor bitlinear_forward(const Rows& x, at::IntArrayRef shape, const Tensor& packed, const Tensor& gamma,
+                         const Tensor& bias) {
+  const int64_t N = packed.size(0);
+  Tensor y = at::empty(with_last(shape, N), packed.options().dtype(at::kBFloat16));
+  if (x.M == 0) return y;
+  const Tensor b = bias.defined() ? aligned(bias.to(at::kBFloat16)) : Tensor();
+  const size_t bytes = bitlinear_fwd_workspace_bytes(x.M, N, x.K);
+  const Tensor ws = scratch(bytes, packed);
+  On on(packed);
+  check(bitlinear_fwd_bias(i8(x.q), f32(x.s), static_cast<uint8_t*>(ptr(packed)), f32(gamma), bf16(b), x.M, N, x.K,
+                           bf16(y), nullptr, bytes ? ptr(ws) : nullptr, bytes, on.stream));
+  return y;
+}
+
+void bitlinear_backward(const Tensor& grad, const Tensor& q, const Tensor& s, const Tensor& packed, const Tensor& gamma,
+                        at::IntArrayRef shape, Tensor* dx, Tensor* dw, at::ScalarType wt, Tensor* db, at::ScalarType bt) {
+  const int64_t N = packed.size(0), K = shape.back();
+  const Tensor dY = aligned(rows(grad.to(at::kBFloat16)));
+  const int64_t M = dY.size(0);
+  const auto o = dY.options();
+  if (dx) *dx = at::empty(shape, o);
+  if (M == 0) {
+    if (dw) *dw = at::zeros({N, K}, o.dtype(wt));
+    if (db) *db = at::zeros({N}, o.dtype(bt));
+    return;
+  }
+  if (dw) *dw = at::empty({N, K}, o.dtype(wt));
+  if (db) *db = at::empty({N}, o.dtype(bt));
+  On on(dY);
+  if (dx || dw) {
+    const size_t bytes = bitlinear_bwd_workspace_bytes(M, N, K);
+    const Tensor ws = scratch(bytes, dY);
+    check(bitlinear_bwd(bf16(dY), dw ? i8(q) : nullptr, dw ? f32(s) : nullptr, static_cast<uint8_t*>(ptr(packed)),
+                        f32(gamma), M, N, K, dx ? bf16(*dx) : nullptr, dw ? ptr(*dw) : nullptr, code(wt),
+                        bytes ? ptr(ws) : nullptr, bytes, on.stream));
+  }
+  if (db) check(bitlinear_bias_grad(bf16(dY), M, N, ptr(*db), code(bt), on.stream));
+}
+
+struct RowsBitLinearFn : torch::autograd::Function<RowsBitLinearFn> {
+  static Tensor forward(AutogradContext* ctx, const Tensor& x, const Tensor& codes, const Tensor& scales,
+                        const Tensor& weight, const optional<Tensor>& bias) {
+    const Rows r(x, codes, scales);
+    const Ternary w(weight);
+    Tensor y = bitlinear_forward(r, x.sizes(), w.packed, w.gamma, bias.value_or(Tensor()));
+    ctx->save_for_backward({r.q, r.s, w.packed, w.gamma});
+    ctx->saved_data["shape"] = x.sizes();
+    ctx->saved_data["wt"] = static_cast<int64_t>(weight.scalar_type());
+    ctx->saved_data["bt"] = static_cast<int64_t>(bias.has_value() ? bias->scalar_type() : at::kBFloat16);
+    ctx->saved_data["b"] = bias.has_value();
+    return y;
+  }
+  static variable_list backward(AutogradContext* ctx, const variable_list& grads) {
+    check_backward();
+    const variable_list v = ctx->get_saved_variables();
+    const bool need_x = ctx->needs_input_grad(0), need_w = ctx->needs_input_grad(3);
+    const bool need_b = ctx->saved_data["b"].toBool() && ctx->needs_input_grad(4);
+    Tensor dx, dw, db;
+    bitlinear_backward(grads[0], v[0], v[1], v[2], v[3], ctx->saved_data["shape"].toIntVector(), need_x ? &dx : nullptr,
+                       need_w ? &dw : nullptr, static_cast<at::ScalarType>(ctx->saved_data["wt"].toInt()),
+                       need_b ? &db : nullptr, static_cast<at::ScalarType>(ctx->saved_data["bt"].toInt()));
+    return {dx, Tensor(), Tensor(), dw, db};
+  }
+};
+
+struct RowsFrozenBitLinearFn : torch::autograd::Function<RowsFrozenBitLinearFn> {
+  static Tensor forward(AutogradContext* ctx, const Tensor& x, const Tensor& codes, const Tensor& scales,
+                        const Tensor& packed, const Tensor& gamma, const optional<Tensor>& bias) {
+    Tensor y = bitlinear_forward(Rows(x, codes, scales), x.sizes(), packed, gamma, bias.value_or(Tensor()));
+    ctx->save_for_backward({packed, gamma});
+    ctx->saved_data["shape"] = x.sizes();
+    ctx->saved_data["bt"] = static_cast<int64_t>(bias.has_value() ? bias->scalar_type() : at::kBFloat16);
+    ctx->saved_data["b"] = bias.has_value();
+    return y;
+  }
+  static variable_list backward(AutogradContext* ctx, const variable_list& grads) {
+    check_backward();
+    const variable_list v = ctx->get_saved_variables();
+    const bool need_b = ctx->saved_data["b"].toBool() && ctx->needs_input_grad(5);
+    Tensor dx, db;
+    bitlinear_backward(grads[0], Tensor(), Tensor(), v[0], v[1], ctx->saved_data["shape"].toIntVector(),
+                       ctx->needs_input_grad(0) ? &dx : nullptr, nullptr, at::kBFloat16, need_b ? &db : nullptr,
+                       static_cast<at::ScalarType>(ctx->saved_data["bt"].toInt()));
+    return {dx, Tensor(), Tensor(), Tensor(), Tensor(), db};
+  }
+};
+
+Tensor rows_bitlinear(const Tensor& x, const Tensor& codes, const Tensor& scales, const Tensor& weight,
+                      const optional<Tensor>& bias) {
+  const Tensor b = bias.value_or(Tensor());
+  check_eager("BitLinear", {&x, &codes, &scales, &weight, &b});
+  check_rows("BitLinear", x, codes, scales);
+  TORCH_CHECK_TYPE(is_value(weight.scalar_type()), "weight: expected bf16 or float32, got ", weight.scalar_type());
+  TORCH_CHECK_VALUE(weight.dim() == 2 && weight.size(1) == x.size(-1) && weight.size(0) >= 1,
+                    "weight: expected [out_features, ", x.size(-1), "], got ", weight.sizes());
+  TORCH_CHECK_VALUE(weight.device() == x.device(), "x and weight: must be GPU tensors of one device");
+  check_bias(b, weight.size(0), x);
+  if (wants_grad({&x, &weight, &b})) return RowsBitLinearFn::apply(x, codes, scales, weight, bias);
+  const Ternary w(weight);
+  return bitlinear_forward(Rows(x, codes, scales), x.sizes(), w.packed, w.gamma, b);
+}
+
+Tensor rows_bitlinear_inference(const Tensor& x, const Tensor& codes, const Tensor& scales, const Tensor& w_packed,
+                                const Tensor& gamma_, int64_t in_features, const optional<Tensor>& bias) {
+  const Tensor b = bias.value_or(Tensor());
+  check_eager("BitLinear", {&x, &codes, &scales, &w_packed, &gamma_, &b});
+  check_rows("BitLinear", x, codes, scales);
+  TORCH_CHECK_VALUE(x.size(-1) == in_features, "x: expected a last dimension of ", in_features, ", got ", x.sizes());
+  TORCH_CHECK_TYPE(w_packed.scalar_type() == at::kByte && gamma_.scalar_type() == at::kFloat,
+                   "w_packed: expected uint8 and gamma float32, got ", w_packed.scalar_type(), " and ",
+                   gamma_.scalar_type());
+  TORCH_CHECK_VALUE(w_packed.dim() == 2 && w_packed.size(0) >= 1 &&
+                        w_packed.size(1) == bitnet_k_pad(in_features) / 4 && gamma_.numel() == 1,
+                    "w_packed: expected [out_features, ", bitnet_k_pad(in_features) / 4, "] and gamma [1], got ",
+                    w_packed.sizes(), " and ", gamma_.sizes());
+  TORCH_CHECK_VALUE(w_packed.device() == x.device() && gamma_.device() == x.device(),
+                    "x, w_packed and gamma: must be GPU tensors of one device");
+  check_bias(b, w_packed.size(0), x);
+  const Tensor packed = aligned(w_packed), gamma = gamma_.contiguous();
+  if (wants_grad({&x, &b})) return RowsFrozenBitLinearFn::apply(x, codes, scales, packed, gamma, bias);
+  return bitlinear_forward(Rows(x, codes, scales), x.sizes(), packed, gamma, b);
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_bitnet_ops, m) {
@@ -523,4 +1215,13 @@ PYBIND11_MODULE(_bitnet_ops, m) {
   m.def("gated_activation", &gated_activation, free_gil);
   m.def("ttq_linear_checkpoint", &ttq_linear_checkpoint, free_gil);
   m.def("linear_cross_entropy", &linear_cross_entropy, free_gil);
+  m.def("rows_values", &rows_values, free_gil);
+  m.def("rms_norm", &rms_norm, free_gil);
+  m.def("gated_bitlinear", &gated_bitlinear, free_gil);
+  m.def("gated_bitlinear_inference", &gated_bitlinear_inference, free_gil);
+  m.def("int8_linear", &int8_linear, free_gil);
+  m.def("int8_linear_inference", &int8_linear_inference, free_gil);
+  m.def("int8_quantize_weight", &int8_quantize_weight, free_gil);
+  m.def("rows_bitlinear", &rows_bitlinear, free_gil);
+  m.def("rows_bitlinear_inference", &rows_bitlinear_inference, free_gil);
 }

@@ -1,0 +1,297 @@
+// Linear layer in 8-bit integers with a scale per token and per channel:
+//
+//   y  = (x_q . w_q^T) sx/127 sw/127 (+ bias)        int32 sums, exact
+//   dX = dY w_hat,  dW = dY^T x_hat                  (straight through both quantizations)
+//
+// with x_hat = bf16(x_q sx/127), w_hat = bf16(w_q sw/127). The forward is the
+// scheme of gemm_kernels.hip with both operands int8 copied as stored; the
+// backward rebuilds both bf16 operands in one launch and runs the bf16
+// products of the TTQ layer on them (launch_ttq_bwd), which take any widths once
+// dY's rows are a multiple of 8.
+
+#include <algorithm>
+
+#include "bwd_prep.h"
+#include "gemm_split.h"
+#include "row_norm.h"
+#include "skinny_core.h"
+
+namespace bitnet {
+
+hipError_t take_int8_split_timeouts(unsigned int* count) { return take_local_split_timeouts(count); }
+
+// ---------------------------------------------------------------------------
+// f32 rows to int8 with a scale a row (bf16 rows: launch_act_quant), the same
+// arithmetic: s = max(max |x|, 1e-8), q = round_half_even(127 x / s), exactly.
+// One block a row, which is read twice (the second time from L2).
+// ---------------------------------------------------------------------------
+
+__global__ __launch_bounds__(256) void rows_quant_f32_kernel(const float* __restrict__ x, int K, int nq,
+                                                             int8_t* __restrict__ xq, float* __restrict__ sx) {
+  __shared__ float slot[4];
+  const int64_t row = blockIdx.x;
+  const float* xr = x + row * K;
+  uint32_t m = 0;
+  for (int k = threadIdx.x; k < K; k += 256) {
+    const uint32_t b = __float_as_uint(xr[k]) & 0x7FFFFFFFu;
+    m = b > m ? b : m;
+  }
+  m = row_max_bits<256>(m, slot);
+  // a row that holds an infinity or a NaN stands for NaN throughout
+  const float s = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : fmaxf(__uint_as_float(m), 1e-8f);
+  if (threadIdx.x == 0) sx[row] = s;
+  for (int ch = threadIdx.x; ch < nq; ch += 256) {
+    float f[8];
+    chunk8(xr, 8 * ch, K).get(f);
+    reinterpret_cast<uint2*>(xq)[row * nq + ch] = codes8(f, s);
+  }
+}
+
+hipError_t launch_rows_quant_f32(const float* x, int64_t M, int64_t K, int8_t* x_q, float* s_x, hipStream_t stream) {
+  rows_quant_f32_kernel<<<(unsigned)M, 256, 0, stream>>>(x, (int)K, (int)(k_pad(K) / 8), x_q, s_x);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Forward
+// ---------------------------------------------------------------------------
+
+// The tile's channel scales (over 127) and biases, staged before its main loop.
+__shared__ __attribute__((aligned(16))) float s_tile_sw[kBI];
+__shared__ __attribute__((aligned(16))) float s_tile_b[kBI];
+
+struct Int8Epilogue {
+  uint16_t* y;  // [J][I]
+  const float* s;
+  const float* sw;
+  const uint16_t* bias;  // [I] or NULL
+  int64_t I, J;          // N, M
+
+  struct Pre { float sj[kFJ]; };
+  __device__ __forceinline__ Pre prefetch(int j0, int lane) const {
+    Pre pre;
+#pragma unroll
+    for (int fj = 0; fj < kFJ; ++fj) {
+      const int64_t j = j0 + 32 * fj + (lane & 31);
+      pre.sj[fj] = j < J ? s[j] : 0.0f;
+    }
+    return pre;
+  }
+  static constexpr int kWaveLds = EpStage<2>::kWaveBytes;
+  static constexpr bool kStagesBias = true;
+  __device__ __forceinline__ void stage_bias(int ti0) const {
+    const int64_t n = (int64_t)ti0 + threadIdx.x;  // kThreads = kBI
+    s_tile_sw[threadIdx.x] = n < I ? sw[n] / 127.0f : 0.0f;
+    s_tile_b[threadIdx.x] = bias != nullptr && n < I ? bf16_to_f32(bias[n]) : 0.0f;
+  }
+  __device__ __forceinline__ void store(MfmaI8::Acc (&acc)[kFI][kFJ], const Pre& pre, int i0, int j0, int lane,
+                                        char* wlds) const {
+#pragma unroll
+    for (int fj = 0; fj < kFJ; ++fj) {
+      const float c = pre.sj[fj] / 127.0f;
+#pragma unroll
+      for (int fi = 0; fi < kFI; ++fi)
+#pragma unroll
+        for (int gi = 0; gi < 4; ++gi) {
+          const int at = (i0 % kBI) + 32 * fi + 8 * gi + 4 * (lane >> 5);
+          const float4 w = *reinterpret_cast<const float4*>(s_tile_sw + at);
+          const float4 b = *reinterpret_cast<const float4*>(s_tile_b + at);
+          const float v0 = fmaf((float)acc[fi][fj][4 * gi] * c, w.x, b.x);
+          const float v1 = fmaf((float)acc[fi][fj][4 * gi + 1] * c, w.y, b.y);
+          const float v2 = fmaf((float)acc[fi][fj][4 * gi + 2] * c, w.z, b.z);
+          const float v3 = fmaf((float)acc[fi][fj][4 * gi + 3] * c, w.w, b.w);
+          EpStage<2>::put(wlds, lane, fi, gi, make_uint2(pack_bf16x2(v0, v1), pack_bf16x2(v2, v3)));
+        }
+      EpStage<2>::drain(wlds, reinterpret_cast<char*>(y), I, J, i0, j0 + 32 * fj, lane);
+    }
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Few tokens: the scheme of skinny_kernels.hip with 128 weight bytes a row and
+// super-step instead of 32 code bytes, read straight from memory by the lanes
+// that multiply them (each weight byte is used by one wave, once).
+// ---------------------------------------------------------------------------
+
+struct Int8Few {
+  const int8_t* wq;
+  const int8_t* xq;
+  int64_t N, Kp;
+  int M;
+};
+
+template <int MT, int W, int P>
+__global__ __launch_bounds__(kWave * W) void int8_skinny_kernel(Int8Few a, const float* __restrict__ s,
+                                                                const float* __restrict__ sw,
+                                                                const uint16_t* __restrict__ bias,
+                                                                uint16_t* __restrict__ y) {
+  constexpr int kThr = kWave * W;
+  constexpr int kChunkB = 128 * W;
+  constexpr int kPitchB = kChunkB + 16;
+  constexpr int kPieces = kChunkB / 16;
+  __shared__ __attribute__((aligned(16))) char smem[skinny_lds<MT, W>()];
+  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+  const int h = lane >> 5, r32 = lane & 31;
+  const int64_t i0 = (int64_t)blockIdx.x * 32;
+  const int nchunks = (int)((a.Kp + kChunkB - 1) / kChunkB);
+  const rsrc_t rw = make_rsrc(a.wq, (uint32_t)(a.N * a.Kp));
+  const uint32_t woff = i0 + r32 < a.N ? (uint32_t)((i0 + r32) * a.Kp) : kOob;
+  const rsrc_t rx = make_rsrc(a.xq, (uint32_t)(a.M * a.Kp));
+  struct Chunk {
+    uint4 x[4 * MT], w[4];
+  };
+  const auto load = [&](Chunk& b, int c) {
+#pragma unroll
+    for (int p = 0; p < 4 * MT; ++p) {
+      const int e = p * kThr + tid, row = e / kPieces, col = 16 * (e % kPieces);
+      const int64_t k = (int64_t)c * kChunkB + col;
+      b.x[p] = buf_load16(rx, row < a.M && k < a.Kp ? (uint32_t)(row * a.Kp + k) : kOob);
+    }
+    const int64_t k = (int64_t)c * kChunkB + 128 * wave + 64 * h;  // Kp is a multiple of 64
+#pragma unroll
+    for (int j = 0; j < 4; ++j) b.w[j] = buf_load16(rw, k < a.Kp ? woff + (uint32_t)(k + 16 * j) : kOob);
+  };
+  i32x16_t acc[MT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[mt][e] = 0;
+  Chunk buf[P];
+#pragma unroll
+  for (int d = 0; d < P; ++d) load(buf[d], d);
+  for (int i = 0; i < nchunks; i += P) {
+#pragma unroll
+    for (int d = 0; d < P; ++d) {
+      if (i + d < nchunks) {
+        __syncthreads();  // the previous chunk's fragment reads are done
+#pragma unroll
+        for (int p = 0; p < 4 * MT; ++p) {
+          const int e = p * kThr + tid;
+          *reinterpret_cast<uint4*>(smem + (e / kPieces) * kPitchB + 16 * (e % kPieces)) = buf[d].x[p];
+        }
+        __syncthreads();
+        const char* xr = smem + r32 * kPitchB + 128 * wave + 64 * h;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+            acc[mt] = MfmaI8::mma(__builtin_bit_cast(i32x4_t, buf[d].w[j]),
+                                  *reinterpret_cast<const i32x4_t*>(xr + 32 * mt * kPitchB + 16 * j), acc[mt]);
+        load(buf[d], i + d + P);  // past the last chunk: zeros, never staged
+      }
+    }
+  }
+  __syncthreads();
+  int* red = reinterpret_cast<int*>(smem);  // [wave][mt][16][lane]
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) red[((wave * MT + mt) * 16 + e) * kWave + lane] = acc[mt][e];
+  __syncthreads();
+  const int g = wave % 4, mt = wave / 4;
+  const int64_t m = 32 * mt + r32;
+  if (mt >= MT || m >= a.M) return;
+  int v[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[e] = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) v[e] += red[((w * MT + mt) * 16 + 4 * g + e) * kWave + lane];
+  }
+  const float c = s[m] / 127.0f;  // the large-M epilogue's expressions
+  const int64_t nb = i0 + 8 * g + 4 * h;
+  float f[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    f[e] = nb + e < a.N
+               ? fmaf((float)v[e] * c, sw[nb + e] / 127.0f, bias != nullptr ? bf16_to_f32(bias[nb + e]) : 0.0f)
+               : 0.0f;
+  uint16_t* yr = y + m * a.N;
+  if (a.N % 4 == 0 && nb + 4 <= a.N) {
+    *reinterpret_cast<uint2*>(yr + nb) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (nb + e < a.N) yr[nb + e] = f32_to_bf16_bits(f[e]);
+  }
+}
+
+static bool few(int64_t M) {
+  return M <= kSkinnyMaxM && test_knobs().no_skinny.load(std::memory_order_relaxed) == 0;
+}
+
+size_t int8_fwd_workspace(int64_t M, int64_t N, int64_t K) {
+  if (few(M)) return 0;
+  const GemmShape g = shape_of(GemmKind::kFwd, M, N, K);
+  return split_workspace(g, split_grid(g, device_cus()));
+}
+
+hipError_t launch_int8_fwd(const int8_t* x_q, const float* s_x, const int8_t* w_q, const float* s_w,
+                           const uint16_t* bias, int64_t M, int64_t N, int64_t K, uint16_t* y, void* ws,
+                           size_t ws_bytes, hipStream_t stream) {
+  const int64_t Kp = k_pad(K);
+  if (few(M)) {
+    const Int8Few a{w_q, x_q, N, Kp, (int)M};
+    const unsigned grid = (unsigned)((N + 31) / 32);
+    if (M <= 32) int8_skinny_kernel<1, 16, 2><<<grid, kWave * 16, 0, stream>>>(a, s_x, s_w, bias, y);
+    else int8_skinny_kernel<2, 8, 3><<<grid, kWave * 8, 0, stream>>>(a, s_x, s_w, bias, y);
+    return hipGetLastError();
+  }
+  const CopyLoader<1, true, 1> pl{reinterpret_cast<const char*>(w_q), Kp, N, Kp};
+  const CopyLoader<1, true, 5> ql{reinterpret_cast<const char*>(x_q), Kp, M, Kp};
+  return run_gemm<MfmaI8, 1>(pl, ql, Int8Epilogue{y, s_x, s_w, bias, N, M}, shape_of(GemmKind::kFwd, M, N, K), ws,
+                             ws_bytes, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Backward
+// ---------------------------------------------------------------------------
+
+// x_hat [M][Kp] (the first xb blocks) and w_hat [N][Kp] in one launch.
+__global__ __launch_bounds__(256) void int8_prep_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
+                                                        int64_t M, uint16_t* __restrict__ xhat, int xb,
+                                                        const int8_t* __restrict__ wq, const float* __restrict__ sw,
+                                                        int64_t N, uint16_t* __restrict__ what, int wb, int64_t Kp) {
+  const int b = blockIdx.x;
+  if (b < xb) xhat_blocks(xq, sx, M, Kp, xhat, b, xb);
+  else xhat_blocks(wq, sw, N, Kp, what, b - xb, wb);
+}
+
+static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+struct Int8Ws {
+  size_t xhat, what, dy;
+};
+static Int8Ws int8_ws(int64_t M, int64_t N, int64_t K) {
+  const int64_t Kp = k_pad(K);
+  return {up256((size_t)M * Kp * 2), up256((size_t)N * Kp * 2), N % 8 == 0 ? 0 : up256((size_t)M * k_pad(N) * 2)};
+}
+size_t int8_bwd_workspace(int64_t M, int64_t N, int64_t K) {
+  const Int8Ws w = int8_ws(M, N, K);
+  return w.xhat + w.what + w.dy + gemm_workspace_bytes(GemmKind::kTtqBwdPadded, M, N, K);
+}
+
+hipError_t launch_int8_bwd(const uint16_t* dY, const int8_t* x_q, const float* s_x, const int8_t* w_q,
+                           const float* s_w, int64_t M, int64_t N, int64_t K, uint16_t* dX, void* dW, bool dw_f32,
+                           void* ws, size_t ws_bytes, hipStream_t stream) {
+  const int64_t Kp = k_pad(K);
+  const Int8Ws w = int8_ws(M, N, K);
+  char* base = static_cast<char*>(ws);
+  uint16_t* xhat = reinterpret_cast<uint16_t*>(base);
+  uint16_t* what = reinterpret_cast<uint16_t*>(base + w.xhat);
+  char* rest = base + w.xhat + w.what + w.dy;
+  const auto blocks = [&](int64_t rows) { return (int)std::min<int64_t>((rows * (Kp / 16) + 255) / 256, 4096); };
+  const int xb = dW != nullptr ? blocks(M) : 0, wb = dX != nullptr ? blocks(N) : 0;
+  int8_prep_kernel<<<xb + wb, 256, 0, stream>>>(x_q, s_x, M, xhat, xb, w_q, s_w, N, what, wb, Kp);
+  if (hipError_t e = hipGetLastError()) return e;
+  int64_t ldy = N;
+  if (N % 8 != 0) {
+    uint16_t* dyp = reinterpret_cast<uint16_t*>(base + w.xhat + w.what);
+    ldy = k_pad(N);
+    if (hipError_t e = launch_pad_rows(dY, M, N, dyp, ldy, nullptr, nullptr, stream)) return e;
+    dY = dyp;
+  }
+  return launch_ttq_bwd(dY, ldy, xhat, Kp, what, nullptr, M, N, K, dX, dW, dw_f32, nullptr, rest,
+                        ws_bytes - (w.xhat + w.what + w.dy), stream);
+}
+
+}  // namespace bitnet

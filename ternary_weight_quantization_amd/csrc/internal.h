@@ -32,6 +32,8 @@ TestKnobs& test_knobs();
 // Waits for published partial tiles that gave up since the last call (read
 // and cleared on the current device; synchronizes the device).
 hipError_t take_split_timeouts(unsigned int* count);
+hipError_t take_gated_split_timeouts(unsigned int* count);  // of the products of gated_kernels.hip
+hipError_t take_int8_split_timeouts(unsigned int* count);   // and of int8_kernels.hip
 
 // MFMA rate probe: one launch of register-only MFMA chains on every SIMD
 // (bf16 32x32x16 or int8 32x32x32), `iters` rounds; mfma_probe_ops() is the
@@ -129,8 +131,9 @@ hipError_t launch_fwd_skinny(const int8_t* x_q, const float* s_x, const uint8_t*
                              uint16_t* y, int32_t* acc_out, hipStream_t stream);
 
 // STE dX for few tokens (M <= kSkinnyMaxM, N % 8 == 0) from the fp4
-// transposed codes wt [Kp][Np/2] (Np = N rounded up to 64).
-hipError_t launch_dx_skinny(const uint8_t* wt, const uint16_t* dY, const float* gamma, int64_t M,
+// transposed codes wt [Kp][Np/2] (Np = N rounded up to 64). gamma NULL:
+// 1, or 127 / s[m] where s is not NULL.
+hipError_t launch_dx_skinny(const uint8_t* wt, const uint16_t* dY, const float* gamma, const float* s, int64_t M,
                             int64_t N, int64_t K, uint16_t* dX, hipStream_t stream);
 
 // STE backward GEMMs.
@@ -213,6 +216,50 @@ size_t layernorm_bwd_workspace(int64_t M, int64_t K);
 hipError_t launch_layernorm_bwd(const void* dY, bool dy_f32, const void* x, bool x_f32, const int8_t* codes,
                                 const float* scales, const void* w, bool p_f32, const float* mean, const float* rstd,
                                 int64_t M, int64_t K, void* dX, void* dw, void* db, void* ws, hipStream_t stream);
+
+// Column sums of partial rows [blocks][sets * K]: the first K to dw, the next to
+// db (either may be NULL).
+hipError_t launch_norm_cols(const float* partials, int blocks, int sets, int64_t K, void* dw, void* db, bool p_f32,
+                            hipStream_t stream);
+
+// Root-mean-square norm, K <= kRmsMaxK (a row fits the registers of one
+// workgroup beside its column sums). res NULL: none (h NULL, x in the stream's
+// type); y NULL: 8-bit rows x_q [M][k_pad(K)], s_x [M].
+constexpr int64_t kRmsMaxK = 16384;
+hipError_t launch_rmsnorm_fwd(const void* x, bool x_f32, const void* res, bool h_f32, const void* w, bool p_f32,
+                              int64_t M, int64_t K, float eps, void* h, void* y, bool y_f32, int8_t* x_q, float* s_x,
+                              float* rstd, hipStream_t stream);
+size_t rmsnorm_bwd_workspace(int64_t M, int64_t K);
+hipError_t launch_rmsnorm_bwd(const void* dY, bool y_f32, const void* dH, const void* h, bool h_f32, const void* w,
+                              bool p_f32, const float* rstd, int64_t M, int64_t K, void* dh, uint16_t* dx, void* dw,
+                              void* ws, hipStream_t stream);
+// bf16 values [M][K] of 8-bit rows x_q [M][k_pad(K)], s_x [M].
+hipError_t launch_rows_unpack(const int8_t* x_q, const float* s_x, int64_t M, int64_t K, uint16_t* x,
+                              hipStream_t stream);
+
+// The gated pair of ternary projections: codes [2N][Kp/4] and scales gamma [2],
+// gate first. slopes: dy/dg and dy/du in 24 bits (NULL: not kept). dWg and dWu
+// both or neither; s_x NULL only without them.
+size_t gated_slopes_bytes(int64_t M, int64_t N);
+size_t gated_fwd_workspace(int64_t M, int64_t N, int64_t K);
+hipError_t launch_gated_fwd(bool relu2, const int8_t* x_q, const float* s_x, const uint8_t* w_packed, const float* gamma,
+                            int64_t M, int64_t N, int64_t K, uint16_t* y, uint16_t* slopes, void* ws, size_t ws_bytes,
+                            hipStream_t stream);
+size_t gated_bwd_workspace(int64_t M, int64_t N, int64_t K);
+hipError_t launch_gated_bwd(const uint16_t* dY, const uint16_t* slopes, const int8_t* x_q, const float* s_x,
+                            const uint8_t* w_packed, const float* gamma, int64_t M, int64_t N, int64_t K, uint16_t* dX,
+                            void* dWg, void* dWu, bool dw_f32, void* ws, size_t ws_bytes, hipStream_t stream);
+
+// Linear layer in 8-bit integers: x_q [M][Kp], w_q [N][Kp], a scale a row each.
+hipError_t launch_rows_quant_f32(const float* x, int64_t M, int64_t K, int8_t* x_q, float* s_x, hipStream_t stream);
+size_t int8_fwd_workspace(int64_t M, int64_t N, int64_t K);
+hipError_t launch_int8_fwd(const int8_t* x_q, const float* s_x, const int8_t* w_q, const float* s_w,
+                           const uint16_t* bias, int64_t M, int64_t N, int64_t K, uint16_t* y, void* ws,
+                           size_t ws_bytes, hipStream_t stream);
+size_t int8_bwd_workspace(int64_t M, int64_t N, int64_t K);
+hipError_t launch_int8_bwd(const uint16_t* dY, const int8_t* x_q, const float* s_x, const int8_t* w_q,
+                           const float* s_w, int64_t M, int64_t N, int64_t K, uint16_t* dX, void* dW, bool dw_f32,
+                           void* ws, size_t ws_bytes, hipStream_t stream);
 
 // Linear layer with softmax cross entropy (h [T][D], w [V][D] bf16).
 size_t xent_workspace(int64_t T, int64_t V, int64_t D, bool bwd);

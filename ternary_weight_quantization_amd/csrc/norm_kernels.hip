@@ -36,45 +36,15 @@
 #include <type_traits>
 
 #include "internal.h"
-#include "row_io.h"
+#include "row_norm.h"
 
 namespace bitnet {
-
-__device__ __forceinline__ float wave_sum_f32(float v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, kWave);
-  return v;
-}
-
-// Sum over the TPR threads of a row (whole waves), in every one of them.
-// `slot`: an LDS array of one float per wave of the block, free on entry.
-template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float* slot) {
-  v = wave_sum_f32(v);
-  if constexpr (TPR > kWave) {
-    constexpr int W = TPR / kWave;
-    const int w0 = threadIdx.x / TPR * W;
-    if (threadIdx.x % kWave == 0) slot[threadIdx.x / kWave] = v;
-    __syncthreads();
-    v = slot[w0];
-#pragma unroll
-    for (int j = 1; j < W; ++j) v += slot[w0 + j];
-  }
-  return v;
-}
 
 struct NormParams {
   const void* w;  // [K] or NULL
   const void* b;
   bool f32;       // their type
 };
-
-// Keeps a loaded chunk as it is across a row's reduction: the values derived
-// from it are computed again after it instead of being held in registers.
-__device__ __forceinline__ void hold(ChunkBf16& c) { asm volatile("" : "+v"(c.v.x), "+v"(c.v.y), "+v"(c.v.z), "+v"(c.v.w)); }
-__device__ __forceinline__ void hold(ChunkF32& c) {
-  asm volatile("" : "+v"(c.a.x), "+v"(c.a.y), "+v"(c.a.z), "+v"(c.a.w), "+v"(c.b.x), "+v"(c.b.y), "+v"(c.b.z), "+v"(c.b.w));
-}
 
 struct NormFwd {
   const void* x;
@@ -414,15 +384,15 @@ __global__ __launch_bounds__(BLOCK, BLOCK == 512 ? 1 : 2) void layernorm_bwd_ker
   }
 }
 
-// The column sums of the partial rows [blocks][cols], columns [0, K) to dw
-// and [K, 2K) to db: a block takes 64 columns, its 16 waves every 16th
-// partial row each, then the wave sums are added in order.
-__global__ __launch_bounds__(1024) void layernorm_cols_kernel(const float* __restrict__ partials, int blocks, int K,
-                                                              void* __restrict__ dw, void* __restrict__ db,
-                                                              bool p_f32) {
+// The column sums of the partial rows [blocks][cols] (cols K or 2K), columns
+// [0, K) to dw and [K, 2K) to db: a block takes 64 columns, its 16 waves every
+// 16th partial row each, then the wave sums are added in order.
+__global__ __launch_bounds__(1024) void norm_cols_kernel(const float* __restrict__ partials, int blocks, int64_t cols,
+                                                         int K, void* __restrict__ dw, void* __restrict__ db,
+                                                         bool p_f32) {
   __shared__ float part[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t col = (int64_t)blockIdx.x * 64 + lane, cols = 2 * (int64_t)K;
+  const int64_t col = (int64_t)blockIdx.x * 64 + lane;
   float v = 0.0f;
   if (col < cols) {
     const float* src = partials + col;
@@ -444,6 +414,13 @@ __global__ __launch_bounds__(1024) void layernorm_cols_kernel(const float* __res
   if (out == nullptr) return;
   if (p_f32) static_cast<float*>(out)[k] = v;
   else static_cast<uint16_t*>(out)[k] = f32_to_bf16_bits(v);
+}
+
+hipError_t launch_norm_cols(const float* partials, int blocks, int sets, int64_t K, void* dw, void* db, bool p_f32,
+                            hipStream_t stream) {
+  const int64_t cols = sets * K;
+  norm_cols_kernel<<<(unsigned)((cols + 63) / 64), 1024, 0, stream>>>(partials, blocks, cols, (int)K, dw, db, p_f32);
+  return hipGetLastError();
 }
 
 // ---------------------------------------------------------------------------
@@ -554,9 +531,7 @@ hipError_t launch_layernorm_bwd(const void* dY, bool dy_f32, const void* x, bool
   else if (x_f32) e = dy_f32 ? norm_bwd<FromF32, float, float>(a, stream) : norm_bwd<FromF32, float, uint16_t>(a, stream);
   else e = dy_f32 ? norm_bwd<FromBf16, uint16_t, float>(a, stream) : norm_bwd<FromBf16, uint16_t, uint16_t>(a, stream);
   if (e != hipSuccess || a.partials == nullptr) return e;
-  layernorm_cols_kernel<<<(unsigned)((2 * K + 63) / 64), 1024, 0, stream>>>(a.partials, norm_bwd_blocks(M, K), (int)K,
-                                                                            dw, db, p_f32);
-  return hipGetLastError();
+  return launch_norm_cols(a.partials, norm_bwd_blocks(M, K), 2, K, dw, db, p_f32, stream);
 }
 
 }  // namespace bitnet

@@ -17,6 +17,7 @@ import math
 import torch
 
 from . import binding as B
+from .rows import QuantizedRows, layer_input
 
 
 def ternarize(weight):
@@ -106,8 +107,11 @@ def bitlinear_inference(x, w_packed, gamma, in_features, bias=None):
     """The forward from a stored ternary state, e.g. the pair
     ``export_inference`` returns: y = BitLinear(x) with w_packed uint8
     [N, Kp/4] and gamma float32 [1] as bitnet_ternarize_pack writes them, x
-    [..., in_features] bf16, optional bf16 bias [N]. Differentiable in x
-    (the STE dX from the same state); the weights get no gradient."""
+    [..., in_features] bf16 (or ``QuantizedRows``, which are not quantized
+    again), optional bf16 bias [N]. Differentiable in x (the STE dX from the
+    same state); the weights get no gradient."""
+    if isinstance(x, QuantizedRows):
+        return B.ops().rows_bitlinear_inference(*layer_input(x), w_packed, gamma, int(in_features), bias)
     return FrozenBitLinearFunction.apply(x, w_packed, gamma, in_features, bias)
 
 
@@ -185,9 +189,12 @@ class QATBitLinear(torch.nn.Module):
         return m
 
     def forward(self, x):
+        """x [..., in_features]: bf16 activations, or the ``QuantizedRows`` of a
+        norm, which are not quantized again."""
         if self.frozen:
-            return FrozenBitLinearFunction.apply(x, self._frozen_packed, self._frozen_gamma, self.in_features,
-                                                 self.bias)
+            return bitlinear_inference(x, self._frozen_packed, self._frozen_gamma, self.in_features, self.bias)
+        if isinstance(x, QuantizedRows):
+            return B.ops().rows_bitlinear(*layer_input(x), self.weight, self.bias)
         return BitLinearFunction.apply(x, self.weight, self.bias)
 
     @torch.no_grad()
