@@ -30,9 +30,9 @@
 
 #include "activation.h"
 #include "bwd_prep.h"
+#include "few8.h"
 #include "gemm_split.h"
 #include "row_io.h"
-#include "skinny_core.h"
 
 namespace bitnet {
 
@@ -219,45 +219,47 @@ struct GatedEpilogue {
 };
 
 // ---------------------------------------------------------------------------
-// Few tokens (M <= kSkinnyMaxM): skinny_kernels.hip's loop. A workgroup's 32 code
-// rows are 16 of the gate and the same 16 of the up projection.
+// Few tokens (M <= kSkinnyMaxM, few8.h): a workgroup's two tiles are 16 rows of the
+// gate and the same 16 of the up projection.
 // ---------------------------------------------------------------------------
 
-template <class ACT, int MT, int W, int P>
-__global__ __launch_bounds__(kWave * W) void gated_skinny_kernel(SkArgs a, const float* __restrict__ s,
-                                                                 const float* __restrict__ gamma, int64_t N, int64_t Nd,
-                                                                 uint16_t* __restrict__ y, uint16_t* __restrict__ slopes) {
-  __shared__ __attribute__((aligned(16))) char smem[skinny_lds<MT, W>()];
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, h = lane >> 5;
-  const int64_t n0 = (int64_t)blockIdx.x * 16, nr = n0 + (lane & 15);
-  skinny_partials<SkFwd, MT, W, P>(a, nr < N ? ((lane & 16) ? N + nr : nr) : -1, smem);
-  // rows 8q + 4h + 0..3 of the tile: the gate's for q < 2, the up projection's for q + 2
-  const int q = wave % 2, mt = wave / 2;
-  const int64_t m = 32 * mt + (lane & 31);
-  if (mt >= MT || m >= a.M) return;
-  int vg[4], vu[4];
-  skinny_sum<SkFwd, MT, W>(smem, q, mt, vg);
-  skinny_sum<SkFwd, MT, W>(smem, q + 2, mt, vu);
-  const float cg = s[m] * gamma[0] / 127.0f, cu = s[m] * gamma[1] / 127.0f;  // the large-M epilogue's expressions
-  const int64_t nb = n0 + 8 * q + 4 * h;
-  float dg[4], du[4], o[4];
+// RP: pairs of tiles.
+template <class ACT, int RP, int MT, int W, int P, bool TX>
+__global__ __launch_bounds__(kWave * W) void gated_few_kernel(FewArgs a, const float* __restrict__ s,
+                                                              const float* __restrict__ gamma, int64_t N, int64_t Nd,
+                                                              uint16_t* __restrict__ y, uint16_t* __restrict__ slopes) {
+  __shared__ __attribute__((aligned(16))) char smem[few_lds<true, 2 * RP, MT, W, TX, false>()];
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * RP);
+  int64_t row[2 * RP];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) gated_value<ACT, true>((float)vg[e] * cg, (float)vu[e] * cu, o[e], dg[e], du[e]);
-  uint16_t* yr = y + m * N;
-  if (N % 4 == 0 && nb + 4 <= N) {
-    *reinterpret_cast<uint2*>(yr + nb) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (nb + e < N) yr[nb + e] = f32_to_bf16_bits(o[e]);
+  for (int p = 0; p < RP; ++p) {
+    const int64_t n = n0 + 16 * p + (lane & 15);
+    row[2 * p] = n < N ? n : -1;
+    row[2 * p + 1] = n < N ? N + n : -1;
   }
-  if (slopes != nullptr) {  // the padding's columns up to Nd past the last workgroup's stay unwritten and are not read
-    uint16_t* r = slopes + m * 2 * Nd + nb;
-    uint8_t* lo = reinterpret_cast<uint8_t*>(slopes + a.M * 2 * Nd) + m * 2 * Nd + nb;
-    *reinterpret_cast<uint2*>(r) = slopes_hi(dg);
-    *reinterpret_cast<uint2*>(r + Nd) = slopes_hi(du);
-    *reinterpret_cast<uint32_t*>(lo) = slopes_lo(dg);
-    *reinterpret_cast<uint32_t*>(lo + Nd) = slopes_lo(du);
+  few_tokens_product<true, 2 * RP, MT, W, P, TX, false>(a, row, smem);
+  for (int i = wave; i < RP * MT; i += W) {
+    const int p = i % RP, mt = i / RP;
+    const int64_t m = 16 * mt + (lane & 15);
+    if (m >= a.M) continue;
+    int vg[4], vu[4];
+    few_tokens_sum<2 * RP, MT, W>(smem, 2 * p, mt, vg);
+    few_tokens_sum<2 * RP, MT, W>(smem, 2 * p + 1, mt, vu);
+    const float cg = s[m] * gamma[0] / 127.0f, cu = s[m] * gamma[1] / 127.0f;  // the large-M epilogue's expressions
+    const int64_t nb = n0 + 16 * p + 4 * (lane >> 4);
+    float dg[4], du[4], o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) gated_value<ACT, true>((float)vg[e] * cg, (float)vu[e] * cu, o[e], dg[e], du[e]);
+    store4(y + m * N, nb, N, o);
+    if (slopes != nullptr && nb < Nd) {  // the padding's columns past the last workgroup's stay unwritten and are not read
+      uint16_t* r = slopes + m * 2 * Nd + nb;
+      uint8_t* lo = reinterpret_cast<uint8_t*>(slopes + a.M * 2 * Nd) + m * 2 * Nd + nb;
+      *reinterpret_cast<uint2*>(r) = slopes_hi(dg);
+      *reinterpret_cast<uint2*>(r + Nd) = slopes_hi(du);
+      *reinterpret_cast<uint32_t*>(lo) = slopes_lo(dg);
+      *reinterpret_cast<uint32_t*>(lo + Nd) = slopes_lo(du);
+    }
   }
 }
 
@@ -406,16 +408,32 @@ size_t gated_fwd_workspace(int64_t M, int64_t N, int64_t K) {
   return split_workspace(g, split_grid(g, device_cus()));
 }
 
+template <class ACT, int RP, int MT, int W, int P, bool TX>
+static void gated_few(const FewArgs& a, const float* s, const float* gamma, int64_t N, int64_t Nd, uint16_t* y,
+                      uint16_t* slopes, hipStream_t st) {
+  gated_few_kernel<ACT, RP, MT, W, P, TX>
+      <<<(unsigned)((N + 16 * RP - 1) / (16 * RP)), kWave * W, 0, st>>>(a, s, gamma, N, Nd, y, slopes);
+}
+
 template <class ACT>
 static hipError_t gated_fwd(const int8_t* x_q, const float* s_x, const uint8_t* w_packed, const float* gamma, int64_t M,
                             int64_t N, int64_t K, uint16_t* y, uint16_t* slopes, void* ws, size_t ws_bytes,
                             hipStream_t stream) {
   const int64_t Kp = k_pad(K), Nd = n_half(N);
   if (few(M)) {
-    const SkArgs a{w_packed, 2 * N, Kp / 4, Kp / 4, x_q, Kp, Kp, (int)M, 0u, 0u};
-    const unsigned grid = (unsigned)((N + 15) / 16);
-    if (M <= 32) gated_skinny_kernel<ACT, 1, 16, 3><<<grid, kWave * 16, 0, stream>>>(a, s_x, gamma, N, Nd, y, slopes);
-    else gated_skinny_kernel<ACT, 2, 8, 3><<<grid, kWave * 8, 0, stream>>>(a, s_x, gamma, N, Nd, y, slopes);
+    const FewArgs a{w_packed, 2 * N, Kp / 4, x_q, Kp, (int)M};
+    // Up to 32 tokens 16 outputs a workgroup of 4 waves, or 8 where each would have more
+    // than 3 steps (1 token, 6912 -> 2 x 2560: 6.0 us with 8, 7.1 with 4; 2560 -> 2 x 6912
+    // 8.1 and 5.7). Above, x_q's traffic counts: 32 outputs share it (64 tokens, 2560 -> 2 x
+    // 6912: 8.7 us against 15.3 with 16, 6912 -> 2 x 2560 12.4 against 13.5).
+    const bool deep = Kp > 12 * FewStep<true>::kK;
+    if (M > 32) gated_few<ACT, 2, 4, 8, 1, true>(a, s_x, gamma, N, Nd, y, slopes, stream);
+    else if (M > 16 && deep) gated_few<ACT, 1, 2, 8, 2, true>(a, s_x, gamma, N, Nd, y, slopes, stream);
+    else if (M > 16) gated_few<ACT, 1, 2, 4, 2, true>(a, s_x, gamma, N, Nd, y, slopes, stream);
+    else if (M > 2 && deep) gated_few<ACT, 1, 1, 8, 3, true>(a, s_x, gamma, N, Nd, y, slopes, stream);
+    else if (M > 2) gated_few<ACT, 1, 1, 4, 3, true>(a, s_x, gamma, N, Nd, y, slopes, stream);
+    else if (deep) gated_few<ACT, 1, 1, 8, 3, false>(a, s_x, gamma, N, Nd, y, slopes, stream);
+    else gated_few<ACT, 1, 1, 4, 3, false>(a, s_x, gamma, N, Nd, y, slopes, stream);
     return hipGetLastError();
   }
   GatedCodesLoader pl;

@@ -12,9 +12,9 @@
 #include <algorithm>
 
 #include "bwd_prep.h"
+#include "few8.h"
 #include "gemm_split.h"
 #include "row_norm.h"
-#include "skinny_core.h"
 
 namespace bitnet {
 
@@ -107,113 +107,58 @@ struct Int8Epilogue {
   }
 };
 
-// ---------------------------------------------------------------------------
-// Few tokens: the scheme of skinny_kernels.hip with 128 weight bytes a row and
-// super-step instead of 32 code bytes, read straight from memory by the lanes
-// that multiply them (each weight byte is used by one wave, once).
-// ---------------------------------------------------------------------------
-
-struct Int8Few {
-  const int8_t* wq;
-  const int8_t* xq;
-  int64_t N, Kp;
-  int M;
-};
-
-template <int MT, int W, int P>
-__global__ __launch_bounds__(kWave * W) void int8_skinny_kernel(Int8Few a, const float* __restrict__ s,
-                                                                const float* __restrict__ sw,
-                                                                const uint16_t* __restrict__ bias,
-                                                                uint16_t* __restrict__ y) {
-  constexpr int kThr = kWave * W;
-  constexpr int kChunkB = 128 * W;
-  constexpr int kPitchB = kChunkB + 16;
-  constexpr int kPieces = kChunkB / 16;
-  __shared__ __attribute__((aligned(16))) char smem[skinny_lds<MT, W>()];
-  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-  const int h = lane >> 5, r32 = lane & 31;
-  const int64_t i0 = (int64_t)blockIdx.x * 32;
-  const int nchunks = (int)((a.Kp + kChunkB - 1) / kChunkB);
-  const rsrc_t rw = make_rsrc(a.wq, (uint32_t)(a.N * a.Kp));
-  const uint32_t woff = i0 + r32 < a.N ? (uint32_t)((i0 + r32) * a.Kp) : kOob;
-  const rsrc_t rx = make_rsrc(a.xq, (uint32_t)(a.M * a.Kp));
-  struct Chunk {
-    uint4 x[4 * MT], w[4];
-  };
-  const auto load = [&](Chunk& b, int c) {
+// Few tokens (few8.h).
+template <int RT, int MT, int W, int P, bool TX>
+__global__ __launch_bounds__(kWave * W) void int8_few_kernel(FewArgs a, const float* __restrict__ s,
+                                                             const float* __restrict__ sw,
+                                                             const uint16_t* __restrict__ bias,
+                                                             uint16_t* __restrict__ y) {
+  __shared__ __attribute__((aligned(16))) char smem[few_lds<false, RT, MT, W, TX, true>()];
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * RT), N = a.rows;
+  int64_t row[RT];
 #pragma unroll
-    for (int p = 0; p < 4 * MT; ++p) {
-      const int e = p * kThr + tid, row = e / kPieces, col = 16 * (e % kPieces);
-      const int64_t k = (int64_t)c * kChunkB + col;
-      b.x[p] = buf_load16(rx, row < a.M && k < a.Kp ? (uint32_t)(row * a.Kp + k) : kOob);
-    }
-    const int64_t k = (int64_t)c * kChunkB + 128 * wave + 64 * h;  // Kp is a multiple of 64
-#pragma unroll
-    for (int j = 0; j < 4; ++j) b.w[j] = buf_load16(rw, k < a.Kp ? woff + (uint32_t)(k + 16 * j) : kOob);
-  };
-  i32x16_t acc[MT];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) acc[mt][e] = 0;
-  Chunk buf[P];
-#pragma unroll
-  for (int d = 0; d < P; ++d) load(buf[d], d);
-  for (int i = 0; i < nchunks; i += P) {
-#pragma unroll
-    for (int d = 0; d < P; ++d) {
-      if (i + d < nchunks) {
-        __syncthreads();  // the previous chunk's fragment reads are done
-#pragma unroll
-        for (int p = 0; p < 4 * MT; ++p) {
-          const int e = p * kThr + tid;
-          *reinterpret_cast<uint4*>(smem + (e / kPieces) * kPitchB + 16 * (e % kPieces)) = buf[d].x[p];
-        }
-        __syncthreads();
-        const char* xr = smem + r32 * kPitchB + 128 * wave + 64 * h;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-            acc[mt] = MfmaI8::mma(__builtin_bit_cast(i32x4_t, buf[d].w[j]),
-                                  *reinterpret_cast<const i32x4_t*>(xr + 32 * mt * kPitchB + 16 * j), acc[mt]);
-        load(buf[d], i + d + P);  // past the last chunk: zeros, never staged
-      }
-    }
-  }
-  __syncthreads();
-  int* red = reinterpret_cast<int*>(smem);  // [wave][mt][16][lane]
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) red[((wave * MT + mt) * 16 + e) * kWave + lane] = acc[mt][e];
-  __syncthreads();
-  const int g = wave % 4, mt = wave / 4;
-  const int64_t m = 32 * mt + r32;
-  if (mt >= MT || m >= a.M) return;
-  int v[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    v[e] = 0;
-#pragma unroll
-    for (int w = 0; w < W; ++w) v[e] += red[((w * MT + mt) * 16 + 4 * g + e) * kWave + lane];
-  }
-  const float c = s[m] / 127.0f;  // the large-M epilogue's expressions
-  const int64_t nb = i0 + 8 * g + 4 * h;
-  float f[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    f[e] = nb + e < a.N
-               ? fmaf((float)v[e] * c, sw[nb + e] / 127.0f, bias != nullptr ? bf16_to_f32(bias[nb + e]) : 0.0f)
-               : 0.0f;
-  uint16_t* yr = y + m * a.N;
-  if (a.N % 4 == 0 && nb + 4 <= a.N) {
-    *reinterpret_cast<uint2*>(yr + nb) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
-  } else {
+  for (int t = 0; t < RT; ++t) row[t] = n0;
+  few_tokens_product<false, RT, MT, W, P, TX, true>(a, row, smem);
+  for (int i = wave; i < RT * MT; i += W) {
+    const int t = i % RT, mt = i / RT;
+    const int64_t m = 16 * mt + (lane & 15);
+    if (m >= a.M) continue;
+    int v[4];
+    few_tokens_sum<RT, MT, W>(smem, t, mt, v);
+    const float c = s[m] / 127.0f;  // the large-M epilogue's expressions
+    const int64_t nb = n0 + 16 * t + 4 * (lane >> 4);
+    float f[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (nb + e < a.N) yr[nb + e] = f32_to_bf16_bits(f[e]);
+      f[e] = nb + e < N ? fmaf((float)v[e] * c, sw[nb + e] / 127.0f, bias != nullptr ? bf16_to_f32(bias[nb + e]) : 0.0f)
+                        : 0.0f;
+    store4(y + m * N, nb, N, f);
   }
+}
+
+template <int RT, int MT, int W, int P, bool TX>
+static void int8_few_at(const FewArgs& a, const float* s, const float* sw, const uint16_t* bias, uint16_t* y,
+                        hipStream_t st) {
+  int8_few_kernel<RT, MT, W, P, TX><<<(unsigned)((a.rows + 16 * RT - 1) / (16 * RT)), kWave * W, 0, st>>>(a, s, sw, bias, y);
+}
+
+// Up to 16 tokens 16 rows a workgroup of 4 waves, at every N (16 tokens 2560 -> 32000: 15.5
+// us, with 32 rows 16.5). Above, x_q's traffic counts and more rows share it as long as
+// the workgroups fill the CUs: 32 tokens 2560 -> 32000 18.7 us with 64 rows, 24.6 with 16;
+// 6912 -> 2560 8.7 with 16, 11.0 with 32; 64 tokens 2560 -> 6912 8.9 with 32 rows and 8
+// waves, 10.4 with 16, 9.7 with 64.
+static void int8_few(const FewArgs& a, const float* s, const float* sw, const uint16_t* bias, uint16_t* y,
+                     hipStream_t st) {
+  const int64_t tiles = (a.rows + 15) / 16;
+  if (a.M <= 2) int8_few_at<1, 1, 4, 5, false>(a, s, sw, bias, y, st);
+  else if (a.M <= 16) int8_few_at<1, 1, 4, 5, true>(a, s, sw, bias, y, st);
+  else if (a.M <= 32 && tiles <= 256) int8_few_at<1, 2, 4, 5, true>(a, s, sw, bias, y, st);
+  else if (a.M <= 32 && tiles <= 512) int8_few_at<2, 2, 4, 4, true>(a, s, sw, bias, y, st);
+  else if (a.M <= 32) int8_few_at<4, 2, 4, 2, true>(a, s, sw, bias, y, st);
+  else if (tiles <= 256) int8_few_at<1, 4, 8, 3, true>(a, s, sw, bias, y, st);
+  else if (tiles <= 512) int8_few_at<2, 4, 8, 2, true>(a, s, sw, bias, y, st);
+  else int8_few_at<4, 4, 8, 1, true>(a, s, sw, bias, y, st);
 }
 
 static bool few(int64_t M) {
@@ -231,10 +176,8 @@ hipError_t launch_int8_fwd(const int8_t* x_q, const float* s_x, const int8_t* w_
                            size_t ws_bytes, hipStream_t stream) {
   const int64_t Kp = k_pad(K);
   if (few(M)) {
-    const Int8Few a{w_q, x_q, N, Kp, (int)M};
-    const unsigned grid = (unsigned)((N + 31) / 32);
-    if (M <= 32) int8_skinny_kernel<1, 16, 2><<<grid, kWave * 16, 0, stream>>>(a, s_x, s_w, bias, y);
-    else int8_skinny_kernel<2, 8, 3><<<grid, kWave * 8, 0, stream>>>(a, s_x, s_w, bias, y);
+    const FewArgs a{reinterpret_cast<const uint8_t*>(w_q), N, Kp, x_q, Kp, (int)M};
+    int8_few(a, s_x, s_w, bias, y, stream);
     return hipGetLastError();
   }
   const CopyLoader<1, true, 1> pl{reinterpret_cast<const char*>(w_q), Kp, N, Kp};
