@@ -585,7 +585,8 @@ bitnet_status bitnet_xent_bwd(const uint16_t* h, const uint16_t* w, const int64_
  *   r[m]   = (sum_k h[m,k]^2 / K + eps)^(-1/2),  v[m,k] = h[m,k] * r[m] * w[k]
  *   y[m,k] = round(v[m,k]),  or
  *   s[m]   = max(max_k |v[m,k]|, 1e-8f),
- *   x_q[m,k] = clip(round_half_even(127 * v[m,k] / s[m]), -127, 127)
+ *   x_q[m,k] = round_half_even(127 * v[m,k] / s[m]), the quotient in fp32 (off by a
+ *              few 2^-24 of its value)
  *
  *   g[m,k]  = dY[m,k] * w[k],  hn[m,k] = h[m,k] * r[m]
  *   dh[m,k] = r[m] * (g[m,k] - hn[m,k] * sum_j g[m,j] hn[m,j] / K) + dH[m,k]

@@ -6,10 +6,11 @@
 //
 // Backward: rms_bwd_kernels.hip. A row lives in the registers of TPR threads
 // in chunks of 8 values, as in the layer norm (norm_kernels.hip): every input
-// is read once, the stream and the rows are written once. Two row reductions,
-// the sum of squares and, for 8-bit rows, the largest magnitude; v is computed
-// again after each rather than held. Statistics are fp32, v is quantized from
-// fp32 without a rounding to bf16 between.
+// is read once, the stream and the rows are written once. For 8-bit rows the
+// largest |h w| is taken along with the sum of squares, before r is known: then
+// s = r max |h w|, q = round(h w (127 r / s)), one reduction and one pass over the
+// row's registers. Statistics are fp32, and no rounding to bf16 comes between h
+// and q.
 
 #include <algorithm>
 
@@ -27,7 +28,7 @@ struct RmsFwd {
   int K, nch, nq;  // chunks of a row, of its 8-bit codes
   float eps;
   void* h;
-  void* y;  // NULL: 8-bit rows
+  void* y;  // (not QUANT)
   bool y_f32;
   int8_t* xq;
   float* sx;
@@ -43,17 +44,57 @@ __device__ __forceinline__ void from8(ChunkF32& c, const float (&f)[8]) {
 }
 
 // Waves a SIMD holds: what a thread's chunks (this row's, the next row's, the
-// weight in fp32) leave registers for.
-template <class T, int CPT>
+// weight and h w in fp32) leave registers for. The launch takes as many blocks as
+// run together. B: bytes read a value.
+template <int B, int CPT>
 constexpr int rms_fwd_waves() {
+  if (B == 2) return CPT <= 4 ? 4 : 3;
+  if (B == 8) return CPT <= 2 ? 3 : CPT <= 4 ? 2 : 1;
   return CPT <= 2 ? 4 : CPT == 3 ? 3 : 2;
 }
+template <class T, class X, bool ADD>
+constexpr int rms_fwd_bytes() { return (int)(sizeof(T) + (ADD ? sizeof(X) : 0)); }
 
-// T: the stream's type. X: the branch's type where ADD (else T). SHORT: K < 8.
+// round_half_even(f k) of 8 values as int8, |f k| <= 127.
+__device__ __forceinline__ uint2 codes8_scaled(const float (&f)[8], float k) {
+  uint32_t t[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) t[e] = __float_as_uint(fmaf(f[e], k, kCodeMagic));  // the low byte
+  const auto pack = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return perm(perm(d, c, 0x0C0C0400u), perm(b, a, 0x0C0C0400u), 0x05040100u);
+  };
+  return make_uint2(pack(t[0], t[1], t[2], t[3]), pack(t[4], t[5], t[6], t[7]));
+}
+
+// Sum of v and maximum of m over the TPR threads of a row, in every one of them.
+template <int TPR>
+__device__ __forceinline__ void row_sum_max(float& v, float& m, float* vs, float* ms) {
+  v = wave_sum_f32(v);
+  m = wave_max_f32(m);
+  if constexpr (TPR > kWave) {
+    constexpr int W = TPR / kWave;
+    const int w0 = threadIdx.x / TPR * W;
+    if (threadIdx.x % kWave == 0) {
+      vs[threadIdx.x / kWave] = v;
+      ms[threadIdx.x / kWave] = m;
+    }
+    __syncthreads();
+    v = vs[w0];
+    m = ms[w0];
+#pragma unroll
+    for (int j = 1; j < W; ++j) {
+      v += vs[w0 + j];
+      m = fmaxf(m, ms[w0 + j]);
+    }
+  }
+}
+
+// T: the stream's type. X: the branch's type where ADD (else T). QUANT: 8-bit rows.
+// SHORT: K < 8.
 // A block takes rows (TPR threads each) in turn; the weight stays in its
 // registers and the next row is requested before the current one is reduced.
-template <class T, class X, bool ADD, int BLOCK, int TPR, int CPT, bool SHORT>
-__global__ __launch_bounds__(BLOCK, (rms_fwd_waves<T, CPT>())) void rmsnorm_fwd_kernel(RmsFwd a) {
+template <class T, class X, bool ADD, bool QUANT, int BLOCK, int TPR, int CPT, bool SHORT>
+__global__ __launch_bounds__(BLOCK, (rms_fwd_waves<rms_fwd_bytes<T, X, ADD>(), CPT>())) void rmsnorm_fwd_kernel(RmsFwd a) {
   constexpr int RPB = BLOCK / TPR;
   __shared__ float slot[4][BLOCK / kWave];
   const int t = threadIdx.x % TPR;
@@ -86,6 +127,15 @@ __global__ __launch_bounds__(BLOCK, (rms_fwd_waves<T, CPT>())) void rmsnorm_fwd_
       for (int e = 0; e < 8; ++e) w[i][e] = 1.0f;
     }
   }
+  bool w_bad = false;  // a weight that is not finite: every row stands for NaN
+  if constexpr (QUANT) {
+    int bad = 0;
+#pragma unroll
+    for (int i = 0; i < CPT; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) bad |= (__float_as_uint(w[i][e]) & 0x7F800000u) == 0x7F800000u;
+    w_bad = __syncthreads_or(bad) != 0;
+  }
   const float inv_k = 1.0f / (float)K;
   int flip = 0;
   for (; base < a.M; base += stride, flip ^= 2) {
@@ -98,7 +148,7 @@ __global__ __launch_bounds__(BLOCK, (rms_fwd_waves<T, CPT>())) void rmsnorm_fwd_
     }
     settle8<SHORT>(c[CPT - 1], k_last, K);
     if constexpr (ADD) settle8<SHORT>(cx[CPT - 1], k_last, K);
-    float sq = 0.0f;
+    float sq = 0.0f, mx = 0.0f, hw[CPT][8];  // hw, mx: QUANT
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
       float f[8];
@@ -118,49 +168,42 @@ __global__ __launch_bounds__(BLOCK, (rms_fwd_waves<T, CPT>())) void rmsnorm_fwd_
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) sq = fmaf(f[e], f[e], sq);
-      hold(c[i]);
+      if constexpr (QUANT) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          hw[i][e] = f[e] * w[i][e];
+          mx = fmaxf(mx, fabsf(hw[i][e]));
+        }
+      } else {
+        hold(c[i]);
+      }
     }
     // two slot pairs in turn: a row's readers are done with one pair before
     // the barrier of the next row, after which it may be written again
-    const float r = 1.0f / sqrtf(row_sum<TPR>(sq, slot[flip]) * inv_k + a.eps);
+    if constexpr (QUANT) row_sum_max<TPR>(sq, mx, slot[flip], slot[flip + 1]);
+    else sq = row_sum<TPR>(sq, slot[flip]);
+    const float r = 1.0f / sqrtf(sq * inv_k + a.eps);
     if (ok && t == 0 && a.rstd) a.rstd[row] = r;
-    const auto value8 = [&](int i, float (&f)[8]) {
-      c[i].get(f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = f[e] * r * w[i][e];
-      if (i == CPT - 1) {  // a row with a NaN has NaNs past its end too
-        const int left = K - k_last;
-        if (left < 8) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = e < left ? f[e] : 0.0f;
-        }
-      }
-    };
-    if (a.y == nullptr) {  // uniform: 8-bit rows
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < CPT; ++i) {
-        float f[8];
-        value8(i, f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t b = __float_as_uint(f[e]) & 0x7FFFFFFFu;
-          m = b > m ? b : m;
-        }
-        hold(c[i]);
-      }
-      m = row_max_bits<TPR>(m, slot[flip + 1]);
+    if constexpr (QUANT) {
       // a row that holds an infinity or a NaN stands for NaN throughout
-      const float s = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : fmaxf(__uint_as_float(m), 1e-8f);
+      const bool fine = sq < __uint_as_float(0x7F800000u) && mx < __uint_as_float(0x7F800000u) && !w_bad;
+      const float s = fine ? fmaxf(r * mx, 1e-8f) : __uint_as_float(0x7FC00000u);
+      const float k = 127.0f * r / s;
       if (ok) {
         if (t == 0) a.sx[row] = s;
 #pragma unroll
         for (int i = 0; i < CPT; ++i) {
           const int ch = t + i * TPR;
-          if (i == CPT - 1 && ch >= a.nq) continue;
-          float f[8];
-          value8(i, f);
-          reinterpret_cast<uint2*>(a.xq)[row * a.nq + ch] = codes8(f, s);
+          if (i == CPT - 1) {
+            if (ch >= a.nq) continue;
+            const int left = K - k_last;
+            if (left < 8) {  // in a row with a NaN the padding would be NaN too
+#pragma unroll
+              for (int e = 0; e < 8; ++e) hw[i][e] = e < left ? hw[i][e] : 0.0f;
+            }
+          }
+          const uint2 q = codes8_scaled(hw[i], fine ? k : 0.0f);
+          reinterpret_cast<uint2*>(a.xq)[row * a.nq + ch] = q;
         }
       }
     } else if (ok) {
@@ -168,7 +211,9 @@ __global__ __launch_bounds__(BLOCK, (rms_fwd_waves<T, CPT>())) void rmsnorm_fwd_
       for (int i = 0; i < CPT; ++i) {
         const int k0 = 8 * (t + i * TPR);
         float f[8];
-        value8(i, f);
+        c[i].get(f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = f[e] * r * w[i][e];
         if (a.y_f32) {
           float* yr = static_cast<float*>(a.y) + row * K;
           if (i < CPT - 1) store8_in(yr + k0, f);
@@ -191,23 +236,28 @@ __global__ __launch_bounds__(BLOCK, (rms_fwd_waves<T, CPT>())) void rmsnorm_fwd_
   }
 }
 
-template <class T, class X, bool ADD, int TPR, int CPT, bool SHORT>
+template <class T, class X, bool ADD, bool QUANT, int TPR, int CPT, bool SHORT>
 static hipError_t rms_fwd_at(const RmsFwd& a, int64_t groups, hipStream_t st) {
   constexpr int BLOCK = TPR < 256 ? 256 : TPR;
-  constexpr int64_t kMost = 256 * (rms_fwd_waves<T, CPT>() * 256 / BLOCK);  // on 256 CUs
-  rmsnorm_fwd_kernel<T, X, ADD, BLOCK, TPR, CPT, SHORT><<<(unsigned)std::min(groups, kMost), BLOCK, 0, st>>>(a);
+  constexpr int64_t kMost = 256 * (rms_fwd_waves<rms_fwd_bytes<T, X, ADD>(), CPT>() * 256 / BLOCK);  // on 256 CUs
+  rmsnorm_fwd_kernel<T, X, ADD, QUANT, BLOCK, TPR, CPT, SHORT><<<(unsigned)std::min(groups, kMost), BLOCK, 0, st>>>(a);
   return hipGetLastError();
 }
 
-template <class T, class X, bool ADD>
+template <class T, class X, bool ADD, bool QUANT>
 static hipError_t rms_fwd(const RmsFwd& a, hipStream_t st) {
   const RmsSplit s = rms_split(a.K);
 #define BITNET_CASE(TPR, CPT, SHORT)                      \
   if (s.tpr == TPR && s.cpt == CPT && SHORT == (a.K < 8)) \
-    return rms_fwd_at<T, X, ADD, TPR, CPT, SHORT>(a, rms_groups(a.M, s), st);
+    return rms_fwd_at<T, X, ADD, QUANT, TPR, CPT, SHORT>(a, rms_groups(a.M, s), st);
   BITNET_RMS_SHAPES(BITNET_CASE)
 #undef BITNET_CASE
   return hipErrorInvalidValue;
+}
+
+template <class T, class X, bool ADD>
+static hipError_t rms_fwd(const RmsFwd& a, hipStream_t st) {
+  return a.y == nullptr ? rms_fwd<T, X, ADD, true>(a, st) : rms_fwd<T, X, ADD, false>(a, st);
 }
 
 hipError_t launch_rmsnorm_fwd(const void* x, bool x_f32, const void* res, bool h_f32, const void* w, bool p_f32,
