@@ -632,13 +632,17 @@ bitnet_status bitnet_rmsnorm_bwd(const void* dY, bitnet_dtype y_dtype, const voi
  * float rows by bitnet_act_quant's arithmetic, and the values they stand for,
  * x[m,k] = bf16_rne(fp32(x_q[m,k] * fp32(s_x[m] / 127))).
  *
- * rows_quant: x [M][K] in x_dtype, 16-byte aligned (M <= 2^23 for BITNET_F32);
- *             x_q [M][Kp], s_x [M], both 16-byte aligned. A float row that holds
- *             an infinity or a NaN has s_x = NaN.
+ * rows_quant: x [M][K] in x_dtype, element aligned (M <= 2^23, K <= 2^24); x_q [M][Kp],
+ *             s_x [M], both 16-byte aligned. A row that holds an infinity or a NaN has
+ *             s_x = NaN.
+ * rows_quant2: the rows of bf16 x [M][K] and of w [N][K] in w_dtype (a layer's activations
+ *             and channels) in one launch; M or N may be 0.
  * rows_unpack: x [M][K] bf16 bits, 2-byte aligned. M * Kp <= 2^34.
  */
 bitnet_status bitnet_rows_quant(const void* x, bitnet_dtype x_dtype, int64_t M, int64_t K, int8_t* x_q, float* s_x,
                                 void* stream);
+bitnet_status bitnet_rows_quant2(const uint16_t* x, int64_t M, int8_t* x_q, float* s_x, const void* w,
+                                 bitnet_dtype w_dtype, int64_t N, int8_t* w_q, float* s_w, int64_t K, void* stream);
 bitnet_status bitnet_rows_unpack(const int8_t* x_q, const float* s_x, int64_t M, int64_t K, uint16_t* x, void* stream);
 
 /*
@@ -692,18 +696,20 @@ bitnet_status bitnet_gated_bwd(const uint16_t* dY, const void* slopes, const int
  *   y[m,n]  = bf16_rne(acc[m,n] * (s_x[m]/127) * (s_w[n]/127) + bias[n]), acc exact int32
  *   dX[m,k] = sum_n dY[m,n] * w_hat[n,k],  w_hat = bf16_rne(w_q * s_w/127)
  *   dW[n,k] = sum_m dY[m,n] * x_hat[m,k],  x_hat = bf16_rne(x_q * s_x/127)
+ *   db[n]   = sum_m dY[m,n]
  *
- * (fp32 rescale and sums; the gradients are straight through both quantizations;
- * the bias' gradient is bitlinear_bias_grad's).
+ * (fp32 rescale and sums, in a fixed order; the gradients are straight through both
+ * quantizations).
  *
  * x_q [M][Kp], s_x [M]; w_q [N][Kp], s_w [N]: 8-bit rows (bitnet_rows_quant), columns
  *            K..Kp-1 zero.
  * bias       [N] bf16 bits, or NULL.   y, dY [M][N] bf16 bits.
- * dX         [M][K] bf16 bits, or NULL.  dW [N][K] in dW_dtype, or NULL; not both NULL.
+ * dX         [M][K] bf16 bits, or NULL.  dW [N][K] in dW_dtype, or NULL.  db [N] in
+ *            db_dtype, or NULL; not all NULL.
  * workspace  bitnet_int8_fwd_workspace_bytes / bitnet_int8_bwd_workspace_bytes (0 for
  *            sizes the call rejects); as for bitlinear_fwd. The backward's holds both
  *            bf16 operands.
- * Pointers 16-byte aligned. K <= 131072 (the int32 sums); (M + 256) * 2 Kp,
+ * Pointers 16-byte aligned but db (its element). K <= 131072 (the int32 sums); (M + 256) * 2 Kp,
  * (N + 256) * 2 Kp and (M + 256) * 2 Nd bytes <= 2^31 (Nd = bitnet_k_pad(N); the forward
  * needs (M + 256) * Kp and (N + 256) * Kp only), N <= 2^24.
  */
@@ -714,7 +720,8 @@ bitnet_status bitnet_int8_fwd(const int8_t* x_q, const float* s_x, const int8_t*
 size_t bitnet_int8_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K);
 bitnet_status bitnet_int8_bwd(const uint16_t* dY, const int8_t* x_q, const float* s_x, const int8_t* w_q,
                               const float* s_w, int64_t M, int64_t N, int64_t K, uint16_t* dX, void* dW,
-                              bitnet_dtype dW_dtype, void* workspace, size_t workspace_bytes, void* stream);
+                              bitnet_dtype dW_dtype, void* db, bitnet_dtype db_dtype, void* workspace,
+                              size_t workspace_bytes, void* stream);
 
 /*
  * Test hooks (for the library's own tests and tuning; not needed to use it).

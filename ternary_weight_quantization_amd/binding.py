@@ -136,6 +136,8 @@ def lib():
     L.bitnet_rmsnorm_bwd.restype = st
     L.bitnet_rows_quant.argtypes = [vp, st, i64, i64, vp, vp, vp]
     L.bitnet_rows_quant.restype = st
+    L.bitnet_rows_quant2.argtypes = [vp, i64, vp, vp, vp, st, i64, vp, vp, i64, vp]
+    L.bitnet_rows_quant2.restype = st
     L.bitnet_rows_unpack.argtypes = [vp, vp, i64, i64, vp, vp]
     L.bitnet_rows_unpack.restype = st
     L.bitnet_gated_fwd.argtypes = [st, vp, vp, vp, vp, i64, i64, i64, vp, vp, vp, sz, vp]
@@ -144,7 +146,7 @@ def lib():
     L.bitnet_gated_bwd.restype = st
     L.bitnet_int8_fwd.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, vp, vp, sz, vp]
     L.bitnet_int8_fwd.restype = st
-    L.bitnet_int8_bwd.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, vp, vp, st, vp, sz, vp]
+    L.bitnet_int8_bwd.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, vp, vp, st, vp, st, vp, sz, vp]
     L.bitnet_int8_bwd.restype = st
     i32, u32 = ctypes.c_int32, ctypes.c_uint32
     L.bitnet_set_test_knobs.argtypes = [st, st, st, u32]
@@ -850,6 +852,19 @@ def bitnet_rows_quant(x, x_q, s_x, stream=None):
     _run(lib().bitnet_rows_quant, x, stream, _ptr(x), xd, M, K, _ptr(x_q), _ptr(s_x))
 
 
+def bitnet_rows_quant2(x, x_q, s_x, w, w_q, s_w, stream=None):
+    """bitnet_rows_quant of x [M, K] bf16 and of w [N, K] (bf16 or float32) in one
+    launch."""
+    (M, K), N = x.shape, w.shape[0]
+    wd = _value_dtype(w, "w")
+    _need(x, torch.bfloat16, (M, K), "x")
+    _need(w, w.dtype, (N, K), "w")
+    _need_rows8(x_q, s_x, M, K, "x")
+    _need_rows8(w_q, s_w, N, K, "w")
+    _same_device(x, x_q=x_q, s_x=s_x, w=w, w_q=w_q, s_w=s_w)
+    _run(lib().bitnet_rows_quant2, x, stream, _ptr(x), M, _ptr(x_q), _ptr(s_x), _ptr(w), wd, N, _ptr(w_q), _ptr(s_w), K)
+
+
 def bitnet_rows_unpack(x_q, s_x, x, stream=None):
     """x [M, K] bf16 = the values of x_q and s_x."""
     M, K = x.shape
@@ -949,12 +964,12 @@ def bitnet_int8_fwd(x_q, s_x, w_q, s_w, K, y, bias=None, workspace=None, stream=
          ws, n)
 
 
-def bitnet_int8_bwd(dY, x_q, s_x, w_q, s_w, K, dX=None, dW=None, workspace=None, stream=None):
-    """dX [M, K] bf16 and/or dW [N, K] (bf16 or float32) from dY [M, N] (w_q, s_w may be
-    None without dX, x_q, s_x without dW)."""
+def bitnet_int8_bwd(dY, x_q, s_x, w_q, s_w, K, dX=None, dW=None, db=None, workspace=None, stream=None):
+    """dX [M, K] bf16, dW [N, K] and db [N] (bf16 or float32), each optional, from dY [M, N]
+    (w_q, s_w may be None without dX, x_q, s_x without dW)."""
     M, N = dY.shape
     _need(dY, torch.bfloat16, (M, N), "dY")
-    dd = BITNET_BF16
+    dd = bd = BITNET_BF16
     if dX is not None:
         _need(dX, torch.bfloat16, (M, K), "dX")
         _need_rows8(w_q, s_w, N, K, "w")
@@ -962,10 +977,13 @@ def bitnet_int8_bwd(dY, x_q, s_x, w_q, s_w, K, dX=None, dW=None, workspace=None,
         dd = _value_dtype(dW, "dW")
         _need(dW, dW.dtype, (N, K), "dW")
         _need_rows8(x_q, s_x, M, K, "x")
-    _same_device(dY, x_q=x_q, s_x=s_x, w_q=w_q, s_w=s_w, dX=dX, dW=dW, workspace=workspace)
+    if db is not None:
+        bd = _value_dtype(db, "db")
+        _need(db, db.dtype, (N,), "db")
+    _same_device(dY, x_q=x_q, s_x=s_x, w_q=w_q, s_w=s_w, dX=dX, dW=dW, db=db, workspace=workspace)
     ws, n = _ws_args(workspace, bitnet_int8_bwd_workspace_bytes(M, N, K), dY, stream)
     _run(lib().bitnet_int8_bwd, dY, stream, _ptr(dY), _ptr(x_q), _ptr(s_x), _ptr(w_q), _ptr(s_w), M, N, int(K), _ptr(dX),
-         _ptr(dW), dd, ws, n)
+         _ptr(dW), dd, _ptr(db), bd, ws, n)
 
 
 # --- linear layer with softmax cross entropy -------------------------------------

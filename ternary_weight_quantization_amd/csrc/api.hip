@@ -574,14 +574,20 @@ bitnet_status bitnet_rmsnorm_bwd(const void* dY, bitnet_dtype y_dtype, const voi
 
 bitnet_status bitnet_rows_quant(const void* x, bitnet_dtype x_dtype, int64_t M, int64_t K, int8_t* x_q, float* s_x,
                                 void* stream) {
-  if (!x || !x_q || !s_x) return BITNET_ERR_NULL;
-  if (!is_value(x_dtype)) return BITNET_ERR_DTYPE;
-  if (x_dtype == BITNET_BF16) return bitnet_act_quant(static_cast<const uint16_t*>(x), M, K, x_q, s_x, stream);
-  if (bitnet_status st = check_sizes(M, K)) return st;
-  if (M > (int64_t(1) << 23) || K > (int64_t(1) << 24)) return BITNET_ERR_SHAPE;
-  if (!aligned(x, 16) || !aligned(x_q, 16) || !aligned(s_x, 16)) return BITNET_ERR_ALIGN;
-  return from_hip(bitnet::launch_rows_quant_f32(static_cast<const float*>(x), M, K, x_q, s_x,
-                                                static_cast<hipStream_t>(stream)));
+  if (M < 1) return BITNET_ERR_SHAPE;
+  return bitnet_rows_quant2(nullptr, 0, nullptr, nullptr, x, x_dtype, M, x_q, s_x, K, stream);
+}
+
+bitnet_status bitnet_rows_quant2(const uint16_t* x, int64_t M, int8_t* x_q, float* s_x, const void* w,
+                                 bitnet_dtype w_dtype, int64_t N, int8_t* w_q, float* s_w, int64_t K, void* stream) {
+  if (M < 0 || N < 0 || M + N < 1 || M > (int64_t(1) << 23) || N > (int64_t(1) << 23) || K < 1 || K > (int64_t(1) << 24))
+    return BITNET_ERR_SHAPE;
+  if ((M > 0 && (!x || !x_q || !s_x)) || (N > 0 && (!w || !w_q || !s_w))) return BITNET_ERR_NULL;
+  if (N > 0 && !is_value(w_dtype)) return BITNET_ERR_DTYPE;
+  if (M > 0 && (!aligned(x, 2) || !aligned(x_q, 16) || !aligned(s_x, 16))) return BITNET_ERR_ALIGN;
+  if (N > 0 && (!aligned(w, elem(w_dtype)) || !aligned(w_q, 16) || !aligned(s_w, 16))) return BITNET_ERR_ALIGN;
+  return from_hip(bitnet::launch_rows_quant(x, M, x_q, s_x, w, w_dtype == BITNET_F32, N, w_q, s_w, K,
+                                            static_cast<hipStream_t>(stream)));
 }
 
 bitnet_status bitnet_rows_unpack(const int8_t* x_q, const float* s_x, int64_t M, int64_t K, uint16_t* x, void* stream) {
@@ -665,16 +671,18 @@ bitnet_status bitnet_int8_fwd(const int8_t* x_q, const float* s_x, const int8_t*
 
 bitnet_status bitnet_int8_bwd(const uint16_t* dY, const int8_t* x_q, const float* s_x, const int8_t* w_q,
                               const float* s_w, int64_t M, int64_t N, int64_t K, uint16_t* dX, void* dW,
-                              bitnet_dtype dW_dtype, void* workspace, size_t workspace_bytes, void* stream) {
-  if (!dY || (!dX && !dW) || (dX && (!w_q || !s_w)) || (dW && (!x_q || !s_x))) return BITNET_ERR_NULL;
-  if (dW && !is_value(dW_dtype)) return BITNET_ERR_DTYPE;
+                              bitnet_dtype dW_dtype, void* db, bitnet_dtype db_dtype, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  if (!dY || (!dX && !dW && !db) || (dX && (!w_q || !s_w)) || (dW && (!x_q || !s_x))) return BITNET_ERR_NULL;
+  if ((dW && !is_value(dW_dtype)) || (db && !is_value(db_dtype))) return BITNET_ERR_DTYPE;
   if (bitnet_status st = check_int8_sizes(M, N, K, true)) return st;
   if (!workspace || workspace_bytes < bitnet_int8_bwd_workspace_bytes(M, N, K)) return BITNET_ERR_WORKSPACE;
-  if (!aligned(workspace, 16) || !aligned(dY, 16)) return BITNET_ERR_ALIGN;
+  if (!aligned(workspace, 16) || !aligned(dY, 16) || (db && !aligned(db, elem(db_dtype)))) return BITNET_ERR_ALIGN;
   if (dX && (!aligned(w_q, 16) || !aligned(s_w, 16) || !aligned(dX, 16))) return BITNET_ERR_ALIGN;
   if (dW && (!aligned(x_q, 16) || !aligned(s_x, 16) || !aligned(dW, 16))) return BITNET_ERR_ALIGN;
-  return from_hip(bitnet::launch_int8_bwd(dY, x_q, s_x, w_q, s_w, M, N, K, dX, dW, dW_dtype == BITNET_F32, workspace,
-                                          workspace_bytes, static_cast<hipStream_t>(stream)));
+  return from_hip(bitnet::launch_int8_bwd(dY, x_q, s_x, w_q, s_w, M, N, K, dX, dW, dW_dtype == BITNET_F32, db,
+                                          db_dtype == BITNET_F32, workspace, workspace_bytes,
+                                          static_cast<hipStream_t>(stream)));
 }
 
 // ---------------------------------------------------------------------------

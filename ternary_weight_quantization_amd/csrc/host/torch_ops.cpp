@@ -581,7 +581,7 @@ struct Rows {
     s = at::empty({M}, x.options().dtype(at::kFloat));
   }
   void quantize(void* stream) const {
-    if (x2.defined()) check(bitnet_act_quant(bf16(x2), M, K, i8(q), f32(s), stream));
+    if (x2.defined()) check(bitnet_rows_quant(bf16(x2), BITNET_BF16, M, K, i8(q), f32(s), stream));
   }
 };
 
@@ -909,14 +909,15 @@ Tensor gated_bitlinear_inference(const Tensor& x, const optional<Tensor>& codes,
 
 // --- linear layer in 8-bit integers -----------------------------------------------------------
 
-// The weight's rows as int8 with a scale each.
-std::pair<Tensor, Tensor> int8_weight(const Tensor& weight) {
-  const Tensor w = aligned(weight);
-  const int64_t N = w.size(0), K = w.size(1);
+// The weight's rows as int8 with a scale each, and those of x that are still to be made.
+std::pair<Tensor, Tensor> int8_weight(const Tensor& weight, const Rows* x) {
+  const Tensor w = weight.contiguous();
+  const int64_t N = w.size(0), K = w.size(1), M = x && x->x2.defined() ? x->M : 0;
   std::pair<Tensor, Tensor> r{at::empty({N, bitnet_k_pad(K)}, w.options().dtype(at::kChar)),
                               at::empty({N}, w.options().dtype(at::kFloat))};
   On on(w);
-  check(bitnet_rows_quant(ptr(w), code(w.scalar_type()), N, K, i8(r.first), f32(r.second), on.stream));
+  check(bitnet_rows_quant2(M ? bf16(x->x2) : nullptr, M, M ? i8(x->q) : nullptr, M ? f32(x->s) : nullptr, ptr(w),
+                           code(w.scalar_type()), N, i8(r.first), f32(r.second), K, on.stream));
   return r;
 }
 
@@ -928,13 +929,12 @@ Tensor int8_forward(const Rows& x, at::IntArrayRef shape, const Tensor& wq, cons
   const size_t bytes = bitnet_int8_fwd_workspace_bytes(x.M, N, x.K);
   const Tensor ws = scratch(bytes, wq);
   On on(wq);
-  x.quantize(on.stream);
   check(bitnet_int8_fwd(i8(x.q), f32(x.s), i8(wq), f32(sw), bf16(b), x.M, N, x.K, bf16(y), bytes ? ptr(ws) : nullptr,
                         bytes, on.stream));
   return y;
 }
 
-// dx, dw (undefined unless wanted) and the bias' gradient.
+// Those that are wanted.
 void int8_backward(const Tensor& grad, const Tensor& q, const Tensor& s, const Tensor& wq, const Tensor& sw,
                    at::IntArrayRef shape, Tensor* dx, Tensor* dw, at::ScalarType wt, Tensor* db, at::ScalarType bt) {
   const int64_t N = wq.size(0), K = shape.back();
@@ -949,22 +949,20 @@ void int8_backward(const Tensor& grad, const Tensor& q, const Tensor& s, const T
   }
   if (dw) *dw = at::empty({N, K}, o.dtype(wt));
   if (db) *db = at::empty({N}, o.dtype(bt));
+  if (!dx && !dw && !db) return;
+  const size_t bytes = bitnet_int8_bwd_workspace_bytes(M, N, K);
+  const Tensor ws = scratch(bytes, dY);
   On on(dY);
-  if (dx || dw) {
-    const size_t bytes = bitnet_int8_bwd_workspace_bytes(M, N, K);
-    const Tensor ws = scratch(bytes, dY);
-    check(bitnet_int8_bwd(bf16(dY), dw ? i8(q) : nullptr, dw ? f32(s) : nullptr, dx ? i8(wq) : nullptr,
-                          dx ? f32(sw) : nullptr, M, N, K, dx ? bf16(*dx) : nullptr, dw ? ptr(*dw) : nullptr, code(wt),
-                          ptr(ws), bytes, on.stream));
-  }
-  if (db) check(bitlinear_bias_grad(bf16(dY), M, N, ptr(*db), code(bt), on.stream));
+  check(bitnet_int8_bwd(bf16(dY), dw ? i8(q) : nullptr, dw ? f32(s) : nullptr, dx ? i8(wq) : nullptr,
+                        dx ? f32(sw) : nullptr, M, N, K, dx ? bf16(*dx) : nullptr, dw ? ptr(*dw) : nullptr, code(wt),
+                        db ? ptr(*db) : nullptr, code(bt), ptr(ws), bytes, on.stream));
 }
 
 struct Int8Fn : torch::autograd::Function<Int8Fn> {
   static Tensor forward(AutogradContext* ctx, const Tensor& x, const optional<Tensor>& codes,
                         const optional<Tensor>& scales, const Tensor& weight, const optional<Tensor>& bias) {
     const Rows r(x, codes.value_or(Tensor()), scales.value_or(Tensor()));
-    const auto w = int8_weight(weight);
+    const auto w = int8_weight(weight, &r);
     Tensor y = int8_forward(r, x.sizes(), w.first, w.second, bias.value_or(Tensor()));
     ctx->save_for_backward({r.q, r.s, w.first, w.second});
     ctx->saved_data["shape"] = x.sizes();
@@ -993,6 +991,10 @@ struct Int8FrozenFn : torch::autograd::Function<Int8FrozenFn> {
   static Tensor forward(AutogradContext* ctx, const Tensor& x, const optional<Tensor>& codes,
                         const optional<Tensor>& scales, const Tensor& wq, const Tensor& sw, const optional<Tensor>& bias) {
     const Rows r(x, codes.value_or(Tensor()), scales.value_or(Tensor()));
+    if (r.M > 0) {
+      On on(r.q);
+      r.quantize(on.stream);
+    }
     Tensor y = int8_forward(r, x.sizes(), wq, sw, bias.value_or(Tensor()));
     ctx->save_for_backward({wq, sw});
     ctx->saved_data["shape"] = x.sizes();
@@ -1031,8 +1033,9 @@ Tensor int8_linear(const Tensor& x, const optional<Tensor>& codes, const optiona
   TORCH_CHECK_VALUE(weight.device() == x.device(), "x and weight: must be GPU tensors of one device");
   check_bias(b, weight.size(0), x);
   if (wants_grad({&x, &weight, &b})) return Int8Fn::apply(x, codes, scales, weight, bias);
-  const auto w = int8_weight(weight);
-  return int8_forward(Rows(x, q, s), x.sizes(), w.first, w.second, b);
+  const Rows r(x, q, s);
+  const auto w = int8_weight(weight, &r);
+  return int8_forward(r, x.sizes(), w.first, w.second, b);
 }
 
 Tensor int8_linear_inference(const Tensor& x, const optional<Tensor>& codes, const optional<Tensor>& scales,
@@ -1052,7 +1055,12 @@ Tensor int8_linear_inference(const Tensor& x, const optional<Tensor>& codes, con
   check_bias(b, w_q.size(0), x);
   const Tensor wq = aligned(w_q), sw = aligned(s_w);
   if (wants_grad({&x, &b})) return Int8FrozenFn::apply(x, codes, scales, wq, sw, bias);
-  return int8_forward(Rows(x, q, s), x.sizes(), wq, sw, b);
+  const Rows r(x, q, s);
+  if (r.M > 0) {
+    On on(r.q);
+    r.quantize(on.stream);
+  }
+  return int8_forward(r, x.sizes(), wq, sw, b);
 }
 
 // The stored state of a weight, for the inference form.
@@ -1062,7 +1070,7 @@ std::pair<Tensor, Tensor> int8_quantize_weight(const Tensor& weight) {
   TORCH_CHECK_VALUE(weight.dim() == 2 && weight.numel() > 0 && weight.is_cuda(),
                     "weight: expected a GPU tensor [out_features, in_features], got ", weight.sizes());
   at::NoGradGuard off;
-  return int8_weight(weight);
+  return int8_weight(weight, nullptr);
 }
 
 // --- the ternary layer of 8-bit rows ---------------------------------------------------------

@@ -5,52 +5,20 @@
 //
 // with x_hat = bf16(x_q sx/127), w_hat = bf16(w_q sw/127). The forward is the
 // scheme of gemm_kernels.hip with both operands int8 copied as stored; the
-// backward rebuilds both bf16 operands in one launch and runs the bf16
-// products of the TTQ layer on them (launch_ttq_bwd), which take any widths once
-// dY's rows are a multiple of 8.
+// backward rebuilds both bf16 operands in one launch, which also takes dY's column
+// sums for the bias, and runs the bf16 products of the TTQ layer on them
+// (launch_ttq_bwd), which take any widths once dY's rows are a multiple of 8.
 
 #include <algorithm>
 
 #include "bwd_prep.h"
 #include "few8.h"
 #include "gemm_split.h"
-#include "row_norm.h"
+#include "row_io.h"
 
 namespace bitnet {
 
 hipError_t take_int8_split_timeouts(unsigned int* count) { return take_local_split_timeouts(count); }
-
-// ---------------------------------------------------------------------------
-// f32 rows to int8 with a scale a row (bf16 rows: launch_act_quant), the same
-// arithmetic: s = max(max |x|, 1e-8), q = round_half_even(127 x / s), exactly.
-// One block a row, which is read twice (the second time from L2).
-// ---------------------------------------------------------------------------
-
-__global__ __launch_bounds__(256) void rows_quant_f32_kernel(const float* __restrict__ x, int K, int nq,
-                                                             int8_t* __restrict__ xq, float* __restrict__ sx) {
-  __shared__ float slot[4];
-  const int64_t row = blockIdx.x;
-  const float* xr = x + row * K;
-  uint32_t m = 0;
-  for (int k = threadIdx.x; k < K; k += 256) {
-    const uint32_t b = __float_as_uint(xr[k]) & 0x7FFFFFFFu;
-    m = b > m ? b : m;
-  }
-  m = row_max_bits<256>(m, slot);
-  // a row that holds an infinity or a NaN stands for NaN throughout
-  const float s = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : fmaxf(__uint_as_float(m), 1e-8f);
-  if (threadIdx.x == 0) sx[row] = s;
-  for (int ch = threadIdx.x; ch < nq; ch += 256) {
-    float f[8];
-    chunk8(xr, 8 * ch, K).get(f);
-    reinterpret_cast<uint2*>(xq)[row * nq + ch] = codes8(f, s);
-  }
-}
-
-hipError_t launch_rows_quant_f32(const float* x, int64_t M, int64_t K, int8_t* x_q, float* s_x, hipStream_t stream) {
-  rows_quant_f32_kernel<<<(unsigned)M, 256, 0, stream>>>(x, (int)K, (int)(k_pad(K) / 8), x_q, s_x);
-  return hipGetLastError();
-}
 
 // ---------------------------------------------------------------------------
 // Forward
@@ -190,51 +158,91 @@ hipError_t launch_int8_fwd(const int8_t* x_q, const float* s_x, const int8_t* w_
 // Backward
 // ---------------------------------------------------------------------------
 
-// x_hat [M][Kp] (the first xb blocks) and w_hat [N][Kp] in one launch.
+// What the products read, in one launch: x_hat [M][Kp] (xb blocks), w_hat [N][Kp] (wb
+// blocks) and, where dY's rows are not a multiple of 8 or their sum is wanted, one pass
+// over dY (the first yb blocks, which take longest): rows copied to `padded` [M][ld] (zeros past N), and
+// partial column sums, a row [N] for each of the `groups` groups of rows. A block takes
+// 2048 columns of a group's rows in turn, a thread 8 of them.
+struct Int8Dy {
+  const uint16_t* dY;
+  int64_t M;
+  int N;
+  uint16_t* padded;  // NULL: not wanted
+  int ld;
+  float* sums;       // NULL: not wanted
+  int groups, cols;  // blocks: groups * cols
+};
+constexpr int kDyCols = 2048;
+
+__device__ __forceinline__ void dy_block(const Int8Dy& a, int b) {
+  const int g = b / a.cols, k0 = (b % a.cols) * kDyCols + 8 * threadIdx.x;
+  const int64_t lo = a.M * g / a.groups, hi = a.M * (g + 1) / a.groups;
+  const int end = a.padded ? a.ld : a.N;
+  if (k0 >= end) return;
+  float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int64_t m = lo; m < hi; ++m) {
+    const ChunkBf16 c = chunk8(a.dY + m * a.N, k0, a.N);
+    if (a.padded) *reinterpret_cast<uint4*>(a.padded + m * a.ld + k0) = c.v;
+    float f[8];
+    c.get(f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] += f[e];
+  }
+  if (a.sums) store8(a.sums + (int64_t)g * a.N, k0, a.N, sum);
+}
+
 __global__ __launch_bounds__(256) void int8_prep_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
                                                         int64_t M, uint16_t* __restrict__ xhat, int xb,
                                                         const int8_t* __restrict__ wq, const float* __restrict__ sw,
-                                                        int64_t N, uint16_t* __restrict__ what, int wb, int64_t Kp) {
-  const int b = blockIdx.x;
-  if (b < xb) xhat_blocks(xq, sx, M, Kp, xhat, b, xb);
+                                                        int64_t N, uint16_t* __restrict__ what, int wb, int64_t Kp,
+                                                        Int8Dy dy, int yb) {
+  const int b = (int)blockIdx.x - yb;
+  if (b < 0) dy_block(dy, b + yb);
+  else if (b < xb) xhat_blocks(xq, sx, M, Kp, xhat, b, xb);
   else xhat_blocks(wq, sw, N, Kp, what, b - xb, wb);
 }
 
 static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+// Groups of rows of the pass over dY: 16 rows or more each, at most 256 groups (4096 x
+// 6912: the launch takes 25 us with the sums and 18 without; with 64 groups 42).
+static int dy_groups(int64_t M) { return (int)std::max<int64_t>(1, std::min<int64_t>(256, M / 16)); }
 struct Int8Ws {
-  size_t xhat, what, dy;
+  size_t xhat, what, dy, sums;
+  size_t before() const { return xhat + what + dy + sums; }
 };
 static Int8Ws int8_ws(int64_t M, int64_t N, int64_t K) {
   const int64_t Kp = k_pad(K);
-  return {up256((size_t)M * Kp * 2), up256((size_t)N * Kp * 2), N % 8 == 0 ? 0 : up256((size_t)M * k_pad(N) * 2)};
+  return {up256((size_t)M * Kp * 2), up256((size_t)N * Kp * 2), N % 8 == 0 ? 0 : up256((size_t)M * k_pad(N) * 2),
+          up256((size_t)dy_groups(M) * N * 4)};
 }
 size_t int8_bwd_workspace(int64_t M, int64_t N, int64_t K) {
-  const Int8Ws w = int8_ws(M, N, K);
-  return w.xhat + w.what + w.dy + gemm_workspace_bytes(GemmKind::kTtqBwdPadded, M, N, K);
+  return int8_ws(M, N, K).before() + gemm_workspace_bytes(GemmKind::kTtqBwdPadded, M, N, K);
 }
 
 hipError_t launch_int8_bwd(const uint16_t* dY, const int8_t* x_q, const float* s_x, const int8_t* w_q,
                            const float* s_w, int64_t M, int64_t N, int64_t K, uint16_t* dX, void* dW, bool dw_f32,
-                           void* ws, size_t ws_bytes, hipStream_t stream) {
+                           void* db, bool db_f32, void* ws, size_t ws_bytes, hipStream_t stream) {
   const int64_t Kp = k_pad(K);
   const Int8Ws w = int8_ws(M, N, K);
   char* base = static_cast<char*>(ws);
   uint16_t* xhat = reinterpret_cast<uint16_t*>(base);
   uint16_t* what = reinterpret_cast<uint16_t*>(base + w.xhat);
-  char* rest = base + w.xhat + w.what + w.dy;
+  const bool products = dX != nullptr || dW != nullptr, pad = products && N % 8 != 0;
+  const int64_t ldy = pad ? k_pad(N) : N;
+  Int8Dy dy{dY, M, (int)N, pad ? reinterpret_cast<uint16_t*>(base + w.xhat + w.what) : nullptr, (int)ldy,
+            db != nullptr ? reinterpret_cast<float*>(base + w.xhat + w.what + w.dy) : nullptr, dy_groups(M),
+            (int)((ldy + kDyCols - 1) / kDyCols)};
   const auto blocks = [&](int64_t rows) { return (int)std::min<int64_t>((rows * (Kp / 16) + 255) / 256, 4096); };
   const int xb = dW != nullptr ? blocks(M) : 0, wb = dX != nullptr ? blocks(N) : 0;
-  int8_prep_kernel<<<xb + wb, 256, 0, stream>>>(x_q, s_x, M, xhat, xb, w_q, s_w, N, what, wb, Kp);
+  const int yb = pad || db != nullptr ? dy.groups * dy.cols : 0;
+  int8_prep_kernel<<<xb + wb + yb, 256, 0, stream>>>(x_q, s_x, M, xhat, xb, w_q, s_w, N, what, wb, Kp, dy, yb);
   if (hipError_t e = hipGetLastError()) return e;
-  int64_t ldy = N;
-  if (N % 8 != 0) {
-    uint16_t* dyp = reinterpret_cast<uint16_t*>(base + w.xhat + w.what);
-    ldy = k_pad(N);
-    if (hipError_t e = launch_pad_rows(dY, M, N, dyp, ldy, nullptr, nullptr, stream)) return e;
-    dY = dyp;
-  }
-  return launch_ttq_bwd(dY, ldy, xhat, Kp, what, nullptr, M, N, K, dX, dW, dw_f32, nullptr, rest,
-                        ws_bytes - (w.xhat + w.what + w.dy), stream);
+  if (db != nullptr)
+    if (hipError_t e = launch_norm_cols(dy.sums, dy.groups, 1, N, db, nullptr, db_f32, stream)) return e;
+  if (!products) return hipSuccess;
+  return launch_ttq_bwd(pad ? dy.padded : dY, ldy, xhat, Kp, what, nullptr, M, N, K, dX, dW, dw_f32, nullptr,
+                        base + w.before(), ws_bytes - w.before(), stream);
 }
 
 }  // namespace bitnet

@@ -233,6 +233,9 @@ size_t rmsnorm_bwd_workspace(int64_t M, int64_t K);
 hipError_t launch_rmsnorm_bwd(const void* dY, bool y_f32, const void* dH, const void* h, bool h_f32, const void* w,
                               bool p_f32, const float* rstd, int64_t M, int64_t K, void* dh, uint16_t* dx, void* dw,
                               void* ws, hipStream_t stream);
+// 8-bit rows of x [M][K] (bf16) and of w [N][K] in one launch (M or N may be 0).
+hipError_t launch_rows_quant(const uint16_t* x, int64_t M, int8_t* x_q, float* s_x, const void* w, bool w_f32, int64_t N,
+                             int8_t* w_q, float* s_w, int64_t K, hipStream_t stream);
 // bf16 values [M][K] of 8-bit rows x_q [M][k_pad(K)], s_x [M].
 hipError_t launch_rows_unpack(const int8_t* x_q, const float* s_x, int64_t M, int64_t K, uint16_t* x,
                               hipStream_t stream);
@@ -251,7 +254,6 @@ hipError_t launch_gated_bwd(const uint16_t* dY, const uint16_t* slopes, const in
                             void* dWg, void* dWu, bool dw_f32, void* ws, size_t ws_bytes, hipStream_t stream);
 
 // Linear layer in 8-bit integers: x_q [M][Kp], w_q [N][Kp], a scale a row each.
-hipError_t launch_rows_quant_f32(const float* x, int64_t M, int64_t K, int8_t* x_q, float* s_x, hipStream_t stream);
 size_t int8_fwd_workspace(int64_t M, int64_t N, int64_t K);
 hipError_t launch_int8_fwd(const int8_t* x_q, const float* s_x, const int8_t* w_q, const float* s_w,
                            const uint16_t* bias, int64_t M, int64_t N, int64_t K, uint16_t* y, void* ws,
@@ -259,7 +261,7 @@ hipError_t launch_int8_fwd(const int8_t* x_q, const float* s_x, const int8_t* w_
 size_t int8_bwd_workspace(int64_t M, int64_t N, int64_t K);
 hipError_t launch_int8_bwd(const uint16_t* dY, const int8_t* x_q, const float* s_x, const int8_t* w_q,
                            const float* s_w, int64_t M, int64_t N, int64_t K, uint16_t* dX, void* dW, bool dw_f32,
-                           void* ws, size_t ws_bytes, hipStream_t stream);
+                           void* db, bool db_f32, void* ws, size_t ws_bytes, hipStream_t stream);
 
 // Linear layer with softmax cross entropy (h [T][D], w [V][D] bf16).
 size_t xent_workspace(int64_t T, int64_t V, int64_t D, bool bwd);

@@ -72,7 +72,8 @@ __global__ __launch_bounds__(BLOCK, BLOCK == 512 ? 1 : 2) void rmsnorm_bwd_kerne
   // what a chunk past the row's end reads of the weight (chunk 0) does not matter
   const int k_last = t + (CPT - 1) * TPR < a.nch ? k_end : 0;
   // The next row is loaded while this one is reduced where both fit the
-  // registers next to the column sums.
+  // registers next to the column sums (4096 x 2560 bf16 with dH, 60 dwords a row and
+  // thread: 18.9 us without it, 23.8 with it and 18 registers spilled).
   constexpr bool AHEAD = (sizeof(CD) + sizeof(CT) * (DH ? 2 : 1)) / 4 * CPT <= 40;
   CD cd[CPT], nd[CPT];
   CT ch[CPT], nh[CPT], cg[CPT], ng[CPT];

@@ -270,28 +270,4 @@ hipError_t launch_rmsnorm_fwd(const void* x, bool x_f32, const void* res, bool h
   return x_f32 ? rms_fwd<float, float, true>(a, stream) : rms_fwd<float, uint16_t, true>(a, stream);
 }
 
-// ---------------------------------------------------------------------------
-// What 8-bit rows stand for: x[m,k] = fp32(q * fp32(s / 127)), rounded to bf16.
-// A thread takes 8 codes.
-// ---------------------------------------------------------------------------
-
-__global__ __launch_bounds__(256) void rows_unpack_kernel(const int8_t* __restrict__ xq, const float* __restrict__ s,
-                                                          int64_t total, int K, int nq, uint16_t* __restrict__ x) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t row = i / nq;
-    const int ch = (int)(i - row * nq);
-    float f[8];
-    values8(reinterpret_cast<const uint2*>(xq)[i], s[row] / 127.0f, f);
-    store8(x + row * K, 8 * ch, K, f);
-  }
-}
-
-hipError_t launch_rows_unpack(const int8_t* x_q, const float* s_x, int64_t M, int64_t K, uint16_t* x,
-                              hipStream_t stream) {
-  const int nq = (int)(k_pad(K) / 8);
-  const int64_t total = M * nq, blocks = (total + 255) / 256;
-  rows_unpack_kernel<<<(unsigned)std::min<int64_t>(blocks, 1 << 20), 256, 0, stream>>>(x_q, s_x, total, (int)K, nq, x);
-  return hipGetLastError();
-}
-
 }  // namespace bitnet

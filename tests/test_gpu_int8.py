@@ -144,6 +144,42 @@ def test_the_largest_sums():
         assert (y[:, ::2] == K).all() and (y[:, 1::2] == -K).all()
 
 
+@pytest.mark.parametrize("M,N", [(1, 1), (15, 8), (16, 2047), (33, 2048), (70, 2049), (1500, 5000), (40000, 9)])
+def test_bias_gradient(M, N):
+    """Column sums of dY, odd and even widths, more and fewer rows than groups: at
+    most M / 256 + 32 additions in a group, then 16 and 16 of the groups."""
+    from ternary_weight_quantization_amd import binding as B
+
+    note(f"int8 bias gradient M={M} N={N}")
+    dY, K = randn(M, N, seed=M), 8
+    for dt in (BF, F32):
+        db = torch.empty(N, dtype=dt, device="cuda")
+        B.bitnet_int8_bwd(dY, None, None, None, None, K, db=db)
+        want = dY.double().sum(0)
+        tol = torch.finfo(dt).eps / 2 * want.abs() + (M / 64 + 96) * U * dY.double().abs().sum(0)
+        assert ((db.double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("K", [5, 64, 130, 1000, 1030, 2555, 4104, 16384, 16390])
+def test_weight_and_activations_quantized_together(dtype, K):
+    """One launch for both, each exactly what the rows alone give."""
+    from ternary_weight_quantization_amd import binding as B
+
+    note(f"rows_quant2 {dtype} K={K}")
+    Kp = -(-K // 64) * 64
+    x, w = randn(7, K, seed=K), randn(9, K, seed=K + 1, dtype=dtype)
+    new = lambda n: (torch.full((n, Kp), 7, dtype=torch.int8, device="cuda"), torch.zeros(n, device="cuda"))  # noqa: E731
+    (xq, sx), (wq, sw) = new(7), new(9)
+    B.bitnet_rows_quant2(x, xq, sx, w, wq, sw)
+    for t, q, s in ((x, xq, sx), (w, wq, sw)):
+        ref, rs = rows64(t)
+        assert torch.equal(q[:, :K].double(), ref) and torch.equal(s.double()[:, None], rs) and not q[:, K:].any()
+        q1, s1 = new(len(t))
+        B.bitnet_rows_quant(t, q1, s1)
+        assert torch.equal(q1, q) and torch.equal(s1, s)
+
+
 def test_gradients_one_at_a_time():
     from ternary_weight_quantization_amd.int8_layer import int8_linear
 
@@ -256,7 +292,10 @@ def test_a_workspace_of_garbage():
         y = torch.empty(M, N, dtype=BF, device="cuda")
         B.bitnet_int8_fwd(xq, sx, wq, sw, K, y)
         ws = torch.full((B.bitnet_int8_bwd_workspace_bytes(M, N, K),), fill, dtype=torch.uint8, device="cuda")
-        dX, dW = torch.empty(M, K, dtype=BF, device="cuda"), torch.empty(N, K, device="cuda")
-        B.bitnet_int8_bwd(dY, xq, sx, wq, sw, K, dX=dX, dW=dW, workspace=ws)
-        outs.append((y, dX, dW))
+        dX, dW, db = torch.empty(M, K, dtype=BF, device="cuda"), torch.empty(N, K, device="cuda"), torch.empty(N, device="cuda")
+        B.bitnet_int8_bwd(dY, xq, sx, wq, sw, K, dX=dX, dW=dW, db=db, workspace=ws)
+        only = torch.empty(N, device="cuda")
+        B.bitnet_int8_bwd(dY, None, None, None, None, K, db=only, workspace=ws)
+        assert torch.equal(only, db)
+        outs.append((y, dX, dW, db))
     assert all(torch.equal(a, b) for a, b in zip(*outs))

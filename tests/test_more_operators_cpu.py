@@ -62,8 +62,18 @@ def test_rows_refusals(L):
     for d in (BF, F32):
         assert f(x=None, d=d) == ENULL and f(q=None, d=d) == ENULL and f(s=None, d=d) == ENULL
         assert f(M=0, d=d) == ESHAPE and f(K=0, d=d) == ESHAPE
-        assert f(x=P + 8, d=d) == EALIGN and f(q=P + 8, d=d) == EALIGN and f(s=P + 8, d=d) == EALIGN
-    assert f(d=SIGN1) == EDTYPE and f(d=F32, M=(1 << 23) + 1) == ESHAPE
+        assert f(x=P + 1, d=d) == EALIGN and f(q=P + 8, d=d) == EALIGN and f(s=P + 8, d=d) == EALIGN
+        assert f(d=d, M=(1 << 23) + 1) == ESHAPE and f(d=d, K=(1 << 24) + 1) == ESHAPE
+    assert f(d=SIGN1) == EDTYPE and f(x=P + 2, d=F32) == EALIGN
+
+    def two(x=P, M=4, q=P, s=P, w=P, d=BF, N=3, wq=P, sw=P, K=64):
+        return L.bitnet_rows_quant2(x, M, q, s, w, d, N, wq, sw, K, None)
+
+    assert two(x=None) == ENULL and two(q=None) == ENULL and two(s=None) == ENULL
+    assert two(w=None) == ENULL and two(wq=None) == ENULL and two(sw=None) == ENULL
+    assert two(M=0, N=0) == ESHAPE and two(M=-1) == ESHAPE and two(N=-1) == ESHAPE and two(K=0) == ESHAPE
+    assert two(d=SIGN1) == EDTYPE and two(x=P + 1) == EALIGN and two(w=P + 2, d=F32) == EALIGN
+    assert two(q=P + 8) == EALIGN and two(sw=P + 8) == EALIGN
 
     def u(q=P, s=P, M=4, K=64, x=P):
         return L.bitnet_rows_unpack(q, s, M, K, x, None)
@@ -117,10 +127,11 @@ def test_int8_refusals(L):
     assert fwd(q=P + 8) == EALIGN and fwd(sw=P + 4) == EALIGN and fwd(b=P + 2) == EALIGN and fwd(y=P + 2) == EALIGN
     assert fwd(ws=None, n=nf + 1) == EWS
 
-    def bwd(dY=P, q=P, s=P, w=P, sw=P, M=M, N=N, K=K, dX=P, dW=P, d=BF, ws=P, n=nb):
-        return L.bitnet_int8_bwd(dY, q, s, w, sw, M, N, K, dX, dW, d, ws, n, None)
+    def bwd(dY=P, q=P, s=P, w=P, sw=P, M=M, N=N, K=K, dX=P, dW=P, d=BF, db=P, bd=BF, ws=P, n=nb):
+        return L.bitnet_int8_bwd(dY, q, s, w, sw, M, N, K, dX, dW, d, db, bd, ws, n, None)
 
-    assert bwd(dY=None) == ENULL and bwd(dX=None, dW=None) == ENULL and bwd(w=None) == ENULL and bwd(sw=None) == ENULL
+    assert bwd(dY=None) == ENULL and bwd(dX=None, dW=None, db=None) == ENULL and bwd(w=None) == ENULL
+    assert bwd(sw=None) == ENULL and bwd(bd=SIGN1) == EDTYPE and bwd(db=P + 1) == EALIGN and bwd(db=P + 2, bd=F32) == EALIGN
     assert bwd(q=None) == ENULL and bwd(s=None) == ENULL and bwd(d=SIGN1) == EDTYPE and bwd(K=131073) == ESHAPE
     assert bwd(ws=None) == EWS and bwd(n=nb - 1) == EWS and bwd(dY=P + 8) == EALIGN and bwd(dW=P + 8) == EALIGN
     assert bwd(s=P + 4) == EALIGN and bwd(ws=P + 8) == EALIGN
