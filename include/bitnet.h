@@ -174,6 +174,19 @@ bitnet_status bitnet_quantize_static(const void* W, bitnet_dtype w_dtype, int64_
                                      void* stream);
 
 /*
+ * bitnet_quantize2 - bitnet_ternarize_pack of two weights of one size and
+ * type, for a layer that puts both to one input: the codes [2 N][Kp/4] of W0
+ * and below them those of W1, gamma[0] and gamma[1], each bit for bit what
+ * that call alone gives. x may be NULL (M, x_q and s_x are not used then);
+ * otherwise its M rows become x_q and s_x as bitnet_rows_quant makes them, in
+ * the weights' launch. Errors as those calls'; workspace as
+ * bitnet_ternarize_pack's.
+ */
+bitnet_status bitnet_quantize2(const void* W0, const void* W1, bitnet_dtype w_dtype, int64_t N, int64_t K,
+                               const uint16_t* x, int64_t M, uint8_t* w_packed, float* gamma,
+                               int8_t* x_q, float* s_x, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * bitnet_code_counts - how many weights each ternary value takes, for the
  * share of -1, 0 and +1 ("bitlinear.py", BitLinear.ternary_stats):
  *

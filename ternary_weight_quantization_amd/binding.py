@@ -62,6 +62,8 @@ def lib():
     L.bitnet_ternarize_pack.restype = st
     L.bitnet_quantize.argtypes = [vp, st, i64, i64, vp, i64, vp, vp, vp, vp, vp, sz, vp]
     L.bitnet_quantize.restype = st
+    L.bitnet_quantize2.argtypes = [vp, vp, st, i64, i64, vp, i64, vp, vp, vp, vp, vp, sz, vp]
+    L.bitnet_quantize2.restype = st
     L.bitnet_quantize_static.argtypes = [vp, st, i64, i64, vp, i64, vp, vp, vp, vp, vp]
     L.bitnet_quantize_static.restype = st
     L.bitnet_code_counts.argtypes = [vp, i64, i64, vp, vp]
@@ -335,6 +337,33 @@ def bitnet_quantize(W, x, w_packed, gamma, x_q, s_x, workspace, stream=None):
     ws_bytes = workspace.numel() * workspace.element_size()
     _check(lib().bitnet_quantize(_ptr(W), wd, N, K, _ptr(x), M, _ptr(w_packed), _ptr(gamma), _ptr(x_q), _ptr(s_x),
                                  _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def bitnet_quantize2(W0, W1, x, w_packed, gamma, x_q, s_x, workspace, stream=None):
+    """bitnet_ternarize_pack of W0 and W1 [N, K] (one dtype) -> w_packed uint8
+    [2 N, Kp/4], gamma float32 [2]; x bf16 [M, K] or None -> x_q, s_x as
+    bitnet_rows_quant makes them."""
+    N, K = W0.shape
+    Kp = bitnet_k_pad(K)
+    if W0.dtype == torch.bfloat16:
+        wd = BITNET_BF16
+    elif W0.dtype == torch.float32:
+        wd = BITNET_F32
+    else:
+        raise TypeError(f"W0: expected bfloat16 or float32, got {W0.dtype}")
+    _need(W0, W0.dtype, (N, K), "W0")
+    _need(W1, W0.dtype, (N, K), "W1")
+    _need(w_packed, torch.uint8, (2 * N, Kp // 4), "w_packed")
+    _need(gamma, torch.float32, (2,), "gamma")
+    M = 0
+    if x is not None:
+        M = x.shape[0]
+        _need(x, torch.bfloat16, (M, K), "x")
+        _need(x_q, torch.int8, (M, Kp), "x_q")
+        _need(s_x, torch.float32, (M,), "s_x")
+    ws_bytes = workspace.numel() * workspace.element_size()
+    _check(lib().bitnet_quantize2(_ptr(W0), _ptr(W1), wd, N, K, _ptr(x), M, _ptr(w_packed), _ptr(gamma), _ptr(x_q),
+                                  _ptr(s_x), _ptr(workspace), ws_bytes, _stream(stream)))
 
 
 def bitnet_quantize_static(W, x, w_packed, gamma, x_q, s_x, stream=None):

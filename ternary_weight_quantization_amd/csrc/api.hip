@@ -191,6 +191,24 @@ bitnet_status bitnet_quantize(const void* W, bitnet_dtype w_dtype, int64_t N, in
                                           static_cast<double*>(workspace), static_cast<hipStream_t>(stream)));
 }
 
+bitnet_status bitnet_quantize2(const void* W0, const void* W1, bitnet_dtype w_dtype, int64_t N, int64_t K,
+                               const uint16_t* x, int64_t M, uint8_t* w_packed, float* gamma, int8_t* x_q, float* s_x,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  if (!W0 || !W1 || !w_packed || !gamma) return BITNET_ERR_NULL;
+  if (x && (!x_q || !s_x)) return BITNET_ERR_NULL;
+  if (w_dtype != BITNET_BF16 && w_dtype != BITNET_F32) return BITNET_ERR_DTYPE;
+  if (bitnet_status st = check_sizes(N, K)) return st;
+  if (x)
+    if (bitnet_status st = check_sizes(M, K)) return st;
+  if (N * K > (int64_t(1) << 53)) return BITNET_ERR_SHAPE;
+  if (!aligned(W0, 16) || !aligned(W1, 16) || !aligned(w_packed, 16) || !aligned(gamma, 4)) return BITNET_ERR_ALIGN;
+  if (x && (!aligned(x, 16) || !aligned(x_q, 16) || !aligned(s_x, 16))) return BITNET_ERR_ALIGN;
+  if (!workspace || workspace_bytes < bitnet_ternarize_workspace_bytes(N, K)) return BITNET_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return BITNET_ERR_ALIGN;
+  return from_hip(bitnet::launch_quantize2(W0, W1, w_dtype == BITNET_F32, N, K, x, M, w_packed, gamma, x_q, s_x,
+                                           static_cast<double*>(workspace), static_cast<hipStream_t>(stream)));
+}
+
 bitnet_status bitnet_code_counts(const uint8_t* w_packed, int64_t N, int64_t K, uint64_t* counts, void* stream) {
   if (!w_packed || !counts) return BITNET_ERR_NULL;
   if (bitnet_status st = check_sizes(N, K)) return st;

@@ -736,8 +736,8 @@ std::tuple<Tensor, Tensor, Tensor, Tensor> rms_norm(const Tensor& x, const optio
 
 // --- the gated pair of ternary projections ------------------------------------------------
 
-// Both weights' codes below each other and both scales; x is quantized in the
-// gate weight's launch where it still is to be.
+// Both weights' codes below each other and both scales; x is quantized with
+// them where it still is to be.
 struct GatedState {
   Tensor packed, gamma;
   GatedState(const Rows& x, const Tensor& w_gate, const Tensor& w_up) {
@@ -747,15 +747,11 @@ struct GatedState {
     gamma = at::empty({2}, wg.options().dtype(at::kFloat));
     const size_t bytes = bitnet_ternarize_workspace_bytes(N, K);
     const Tensor ws = scratch(bytes, wg);
-    uint8_t* p = static_cast<uint8_t*>(ptr(packed));
-    const bitnet_dtype gd = code(wg.scalar_type()), ud = code(wu.scalar_type());
+    const bool rows = x.x2.defined() && x.M > 0;
     On on(wg);
-    if (x.x2.defined() && x.M > 0)
-      check(bitnet_quantize(ptr(wg), gd, N, K, bf16(x.x2), x.M, p, f32(gamma), i8(x.q), f32(x.s), ptr(ws), bytes,
-                            on.stream));
-    else
-      check(bitnet_ternarize_pack(ptr(wg), gd, N, K, p, f32(gamma), ptr(ws), bytes, on.stream));
-    check(bitnet_ternarize_pack(ptr(wu), ud, N, K, p + N * row, f32(gamma) + 1, ptr(ws), bytes, on.stream));
+    check(bitnet_quantize2(ptr(wg), ptr(wu), code(wg.scalar_type()), N, K, rows ? bf16(x.x2) : nullptr, x.M,
+                           static_cast<uint8_t*>(ptr(packed)), f32(gamma), i8(x.q), f32(x.s), ptr(ws), bytes,
+                           on.stream));
   }
 };
 

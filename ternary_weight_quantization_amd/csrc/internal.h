@@ -94,6 +94,12 @@ hipError_t launch_quantize(const void* W, bool w_is_f32, int64_t N, int64_t K, c
                            uint8_t* w_packed, float* gamma, int8_t* x_q, float* s_x, double* partials,
                            hipStream_t stream);
 
+// Two weights of one size, their codes [2 N][k_pad / 4] below each other and
+// their scales gamma[2], and (x not NULL) the activation rows.
+hipError_t launch_quantize2(const void* W0, const void* W1, bool w_is_f32, int64_t N, int64_t K, const uint16_t* x,
+                            int64_t M, uint8_t* w_packed, float* gamma, int8_t* x_q, float* s_x, double* partials,
+                            hipStream_t stream);
+
 // Bias gradient db[n] = sum_m dY[m][n] (fp32, fixed order), db as f32 or
 // bf16 bits.
 hipError_t launch_bias_grad(const uint16_t* dY, int64_t M, int64_t N, void* db, bool db_is_f32,

@@ -18,6 +18,7 @@
 
 #include "device_common.h"
 #include "internal.h"
+#include "rows_quant.h"
 
 namespace bitnet {
 
@@ -174,10 +175,9 @@ __device__ __forceinline__ double partials_total(const double* __restrict__ part
 }
 
 template <bool F32, bool VEC>
-__global__ __launch_bounds__(kPackThreads) void ternarize_pack_kernel(
-    const void* __restrict__ w, int64_t N, int64_t K, int64_t words_per_row,
-    const double* __restrict__ partials, uint32_t* __restrict__ packed,
-    float* __restrict__ gamma_out) {
+__device__ __forceinline__ void ternarize_pack(const void* __restrict__ w, int64_t N, int64_t K, int64_t words_per_row,
+                                               const double* __restrict__ partials, uint32_t* __restrict__ packed,
+                                               float* __restrict__ gamma_out) {
   __shared__ double sred[kPackThreads / kWave];
   __shared__ float s_half;
   const int64_t total = N * words_per_row;
@@ -216,6 +216,14 @@ __global__ __launch_bounds__(kPackThreads) void ternarize_pack_kernel(
     }
     packed[wi] = word;
   }
+}
+
+template <bool F32, bool VEC>
+__global__ __launch_bounds__(kPackThreads) void ternarize_pack_kernel(
+    const void* __restrict__ w, int64_t N, int64_t K, int64_t words_per_row,
+    const double* __restrict__ partials, uint32_t* __restrict__ packed,
+    float* __restrict__ gamma_out) {
+  ternarize_pack<F32, VEC>(w, N, K, words_per_row, partials, packed, gamma_out);
 }
 
 // The pack pass (gamma from the partials, codes, packing).
@@ -862,6 +870,7 @@ void launch_onepass(const uint16_t* W, int64_t N, int64_t K, void* ws, uint32_t*
     launch_onepass_v<kOnePassVecsLarge>(W, N, K, sync, tag, spin, packed, gamma, x, M, xq, s, st);
 }
 
+static_assert(sizeof(QuantSync) >= 2 * kAbsmeanBlocks * sizeof(double), "the partials of two weights");
 size_t quant_workspace_bytes() { return sizeof(QuantSync); }
 
 hipError_t take_onepass_recomputes(unsigned int* count) {
@@ -943,6 +952,93 @@ hipError_t launch_quantize(const void* W, bool w_is_f32, int64_t N, int64_t K, c
   else launch_front<false>(W, N * K, partials, x, M, K, Kp, x_q, s_x, stream);
   if (hipError_t e = hipGetLastError()) return e;
   return launch_pack(W, w_is_f32, N, K, w_packed, gamma, partials, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Two weights of one size, with the activation rows they share where x is
+// given: the partials of both and the rows in one launch, the codes of both
+// in the next. Each gamma has the bits that its weight alone gives. The weights are
+// read twice: two of 6912 x 2560 do not fit the registers of the one-pass kernel
+// together. Bound by these reads: with 4096 rows of 2560 22.4 + 15.8 us (173 MB, 4.5
+// TB/s; a one-pass launch for each weight 23.1 + 17.4), with 1021 rows 15.7 + 15.5
+// (18.7 + 16.8). Four words a thread requested ahead of gamma's reduction made the
+// second launch no faster (16.3).
+// ---------------------------------------------------------------------------
+
+// The rows, kAbsmeanThreads / TPR a block, then the partials of w0 and of w1.
+template <bool F32, int TPR, int CPT, bool SHORT>
+__global__ __launch_bounds__(kAbsmeanThreads) void quant_front2_kernel(
+    const void* __restrict__ w0, const void* __restrict__ w1, int64_t n, double* __restrict__ partials,
+    QuantRows<uint16_t> x, int K, int nq) {
+  __shared__ float slot[kAbsmeanThreads / kWave];
+  const int rows = (int)gridDim.x - 2 * kAbsmeanBlocks, b = (int)blockIdx.x - rows;
+  if (b < 0) {
+    const int rl = __builtin_amdgcn_readfirstlane((int)threadIdx.x / TPR);
+    quant_row<uint16_t, TPR, CPT, SHORT>(x, (int64_t)blockIdx.x * (kAbsmeanThreads / TPR) + rl, K, nq, slot);
+  } else if (b < kAbsmeanBlocks) {
+    absmean_block<F32>(w0, n, partials, b);
+  } else {
+    absmean_block<F32>(w1, n, partials + kAbsmeanBlocks, b - kAbsmeanBlocks);
+  }
+}
+
+// The codes of both, blockIdx.y's each: partials, codes and gamma lie behind the
+// first's.
+template <bool F32, bool VEC>
+__global__ __launch_bounds__(kPackThreads) void ternarize_pack2_kernel(
+    const void* __restrict__ w0, const void* __restrict__ w1, int64_t N, int64_t K, int64_t words_per_row,
+    const double* __restrict__ partials, uint32_t* __restrict__ packed, float* __restrict__ gamma_out) {
+  const int y = blockIdx.y;
+  ternarize_pack<F32, VEC>(y ? w1 : w0, N, K, words_per_row, partials + y * kAbsmeanBlocks,
+                           packed + y * N * words_per_row, gamma_out + y);
+}
+
+// Rows take 64 threads up to 512 chunks and 128 up to 1024 for the reason above;
+// the longest are quantized by a launch of their own.
+template <bool F32>
+static hipError_t launch_front2(const void* W0, const void* W1, int64_t n, double* partials,
+                                const QuantRows<uint16_t>& x, int64_t K, hipStream_t st) {
+  const int nq = (int)(k_pad(K) / 8);
+  const int tpr = nq > 128 * 8 ? 256 : nq > 64 * 8 ? 128 : 64, cpt = (nq + tpr - 1) / tpr;
+  const int64_t rpb = kAbsmeanThreads / tpr;
+  const unsigned grid = (unsigned)((x.rows + rpb - 1) / rpb + 2 * kAbsmeanBlocks);
+#define BITNET_CASE(TPR, CPT, SHORT)                                                                             \
+  if (tpr == TPR && cpt == CPT && SHORT == (K < 8)) {                                                            \
+    quant_front2_kernel<F32, TPR, CPT, SHORT><<<grid, kAbsmeanThreads, 0, st>>>(W0, W1, n, partials, x, (int)K, nq); \
+    return hipGetLastError();                                                                                    \
+  }
+  BITNET_CASE(64, 1, true) BITNET_CASE(64, 1, false) BITNET_CASE(64, 2, false) BITNET_CASE(64, 3, false)
+  BITNET_CASE(64, 4, false) BITNET_CASE(64, 5, false) BITNET_CASE(64, 6, false) BITNET_CASE(64, 7, false)
+  BITNET_CASE(64, 8, false) BITNET_CASE(128, 5, false) BITNET_CASE(128, 6, false) BITNET_CASE(128, 7, false)
+  BITNET_CASE(128, 8, false) BITNET_CASE(256, 5, false) BITNET_CASE(256, 6, false) BITNET_CASE(256, 7, false)
+  BITNET_CASE(256, 8, false)
+#undef BITNET_CASE
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_quantize2(const void* W0, const void* W1, bool w_is_f32, int64_t N, int64_t K, const uint16_t* x,
+                            int64_t M, uint8_t* w_packed, float* gamma, int8_t* x_q, float* s_x, double* partials,
+                            hipStream_t stream) {
+  QuantRows<uint16_t> rows{x, x != nullptr ? M : 0, x_q, s_x};
+  int64_t Kr = K;  // the rows' width; 1 where no rows share the launch
+  if (k_pad(K) > 256 * 8 * 8) {
+    if (rows.rows > 0)
+      if (hipError_t e = launch_rows_quant(x, M, x_q, s_x, nullptr, false, 0, nullptr, nullptr, K, stream)) return e;
+    rows.rows = 0;
+  }
+  if (rows.rows == 0) Kr = 1;
+  if (hipError_t e = w_is_f32 ? launch_front2<true>(W0, W1, N * K, partials, rows, Kr, stream)
+                              : launch_front2<false>(W0, W1, N * K, partials, rows, Kr, stream))
+    return e;
+  const int64_t wpr = k_pad(K) / 16, want = (N * wpr + kPackThreads - 1) / kPackThreads;
+  const dim3 grid((unsigned)(want < 2048 ? want : 2048), 2);
+  uint32_t* pw = reinterpret_cast<uint32_t*>(w_packed);
+#define BITNET_CASE(F32, VEC)                                                                                     \
+  if (w_is_f32 == F32 && (K % (F32 ? 4 : 8) == 0) == VEC)                                                         \
+    ternarize_pack2_kernel<F32, VEC><<<grid, kPackThreads, 0, stream>>>(W0, W1, N, K, wpr, partials, pw, gamma);
+  BITNET_CASE(true, true) BITNET_CASE(true, false) BITNET_CASE(false, true) BITNET_CASE(false, false)
+#undef BITNET_CASE
+  return hipGetLastError();
 }
 
 // ---------------------------------------------------------------------------

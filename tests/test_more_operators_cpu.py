@@ -112,6 +112,21 @@ def test_gated_refusals(L):
     assert bwd(dY=P + 1) == EALIGN and bwd(dX=P + 8) == EALIGN and bwd(b=P + 8) == EALIGN and bwd(s=P + 2) == EALIGN
 
 
+def test_quantize2_refusals(L):
+    n = L.bitnet_ternarize_workspace_bytes(200, 130)
+
+    def f(a=P, b=P, d=BF, N=200, K=130, x=P, M=4, p=P, g=P, q=P, s=P, ws=P, n=n):
+        return L.bitnet_quantize2(a, b, d, N, K, x, M, p, g, q, s, ws, n, None)
+
+    assert f(a=None) == ENULL and f(b=None) == ENULL and f(p=None) == ENULL and f(g=None) == ENULL
+    assert f(q=None) == ENULL and f(s=None) == ENULL and f(d=SIGN1) == EDTYPE
+    assert f(N=0) == ESHAPE and f(K=0) == ESHAPE and f(M=0) == ESHAPE and f(N=1 << 31) == ESHAPE
+    assert f(a=P + 8) == EALIGN and f(b=P + 8) == EALIGN and f(x=P + 8) == EALIGN and f(p=P + 8) == EALIGN
+    assert f(g=P + 2) == EALIGN and f(q=P + 8) == EALIGN and f(s=P + 8) == EALIGN and f(ws=P + 8) == EALIGN
+    assert f(ws=None) == EWS and f(n=n - 1) == EWS
+    assert f(x=None, M=0, q=None, s=None, ws=None) == EWS  # no rows: M, q and s are not looked at
+
+
 def test_int8_refusals(L):
     M, N, K = 300, 201, 130
     nf, nb = L.bitnet_int8_fwd_workspace_bytes(M, N, K), L.bitnet_int8_bwd_workspace_bytes(M, N, K)
