@@ -264,57 +264,68 @@ __global__ __launch_bounds__(kWave * W) void gated_few_kernel(FewArgs a, const f
 }
 
 // ---------------------------------------------------------------------------
-// Backward, elementwise: D [M][2 Nd] from dY [M][N] and the slopes, times the
-// half's gamma and (sx not NULL) the token's sx/127. A thread takes 8 columns of
-// both halves; columns past N are zeros.
+// Backward, what the products read, in one launch: D, the codes of both weights
+// transposed to fp4 [Kp][2 Nd / 2] and the int8 rows as bf16 [M][Kp].
 // ---------------------------------------------------------------------------
 
-__global__ __launch_bounds__(256) void gated_dgrad_kernel(const uint16_t* __restrict__ dY,
-                                                          const uint16_t* __restrict__ slopes,
-                                                          const float* __restrict__ gamma, const float* __restrict__ sx,
-                                                          int64_t total, int N, int Nd, uint16_t* __restrict__ D) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= total) return;
-  const int nch = Nd / 8;
+// D [M][2 Nd] from dY [M][N] and the slopes, times the half's gamma and (sx not
+// NULL) the token's sx/127. A thread takes 8 columns of both halves; columns past N
+// are zeros.
+struct GatedD {
+  const uint16_t* dY;
+  const uint16_t* slopes;
+  const float* gamma;
+  const float* sx;
+  int64_t total;  // M Nd / 8
+  int N, Nd;
+  uint16_t* D;
+};
+
+__device__ __forceinline__ void gated_d_block(const GatedD& a, int64_t b) {
+  const int64_t i = b * 256 + threadIdx.x;
+  if (i >= a.total) return;
+  const int nch = a.Nd / 8, N = a.N, Nd = a.Nd;
   const int64_t row = i / nch;
   const int k0 = 8 * (int)(i - row * nch);
   const int64_t at = row * 2 * Nd + k0;
   const int64_t src = k0 < N ? at : at - k0;  // past N: any written columns, not used
-  const uint8_t* lo = reinterpret_cast<const uint8_t*>(slopes + total * 16);  // total / nch rows of 2 Nd = 16 nch
-  const uint4 hg = *reinterpret_cast<const uint4*>(slopes + src), hu = *reinterpret_cast<const uint4*>(slopes + src + Nd);
+  const uint8_t* lo = reinterpret_cast<const uint8_t*>(a.slopes + a.total * 16);  // total / nch rows of 2 Nd = 16 nch
+  const uint4 hg = *reinterpret_cast<const uint4*>(a.slopes + src);
+  const uint4 hu = *reinterpret_cast<const uint4*>(a.slopes + src + Nd);
   const uint2 lg = *reinterpret_cast<const uint2*>(lo + src), lu = *reinterpret_cast<const uint2*>(lo + src + Nd);
   float d[8], g[8], u[8];
-  chunk8(dY + row * N, k0, N).get(d);
+  chunk8(a.dY + row * N, k0, N).get(d);
   slopes8(hg, lg, g);
   slopes8(hu, lu, u);
-  const float sc = sx != nullptr ? sx[row] / 127.0f : 1.0f, gg = gamma[0] * sc, gu = gamma[1] * sc;
+  const float sc = a.sx != nullptr ? a.sx[row] / 127.0f : 1.0f, gg = a.gamma[0] * sc, gu = a.gamma[1] * sc;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const bool in_row = k0 + e < N;  // a slope of the padding may be anything
     g[e] = in_row ? d[e] * g[e] * gg : 0.0f;
     u[e] = in_row ? d[e] * u[e] * gu : 0.0f;
   }
-  store8_in(D + at, g);
-  store8_in(D + at + Nd, u);
+  store8_in(a.D + at, g);
+  store8_in(a.D + at + Nd, u);
 }
 
-// Both operands that the products rebuild, in one launch: the codes of both
-// weights transposed to fp4 [Kp][2 Nd / 2] (the first wt_bx * wt_by blocks) and
-// the int8 rows as bf16 [M][Kp] (the other xhat_nb).
+// Blocks: wt_bx * wt_by of the transposed codes, xhat_nb of the rows, then D's.
 __global__ __launch_bounds__(256) void gated_prep_kernel(const uint8_t* __restrict__ packed, int64_t N, int64_t Kp,
                                                          int64_t Nd, uint8_t* __restrict__ wt, int wt_bx, int wt_by,
                                                          const int8_t* __restrict__ xq, int64_t M,
-                                                         uint16_t* __restrict__ xhat, int xhat_nb) {
-  const int b = blockIdx.x, nwt = wt_bx * wt_by;
-  if (b < nwt) {
-    const int v = xcd_major(b, nwt);
+                                                         uint16_t* __restrict__ xhat, int xhat_nb, GatedD d) {
+  const int64_t b = blockIdx.x;
+  const int nwt = wt_bx * wt_by;
+  if (b >= nwt + xhat_nb) {
+    gated_d_block(d, b - (nwt + xhat_nb));
+  } else if (b < nwt) {
+    const int v = xcd_major((int)b, nwt);
     const auto row = [N, Nd](int64_t n) {
       const int64_t c = n < Nd ? n : n - Nd;
       return c < N ? (n < Nd ? c : N + c) : int64_t(-1);
     };
     wt_fp4_block(packed, row, Kp, 2 * Nd, wt, v % wt_bx, v / wt_bx);
   } else {
-    xhat_blocks(xq, nullptr, M, Kp, xhat, b - nwt, xhat_nb);
+    xhat_blocks(xq, nullptr, M, Kp, xhat, (int)b - nwt, xhat_nb);
   }
 }
 
@@ -518,16 +529,12 @@ hipError_t launch_gated_bwd(const uint16_t* dY, const uint16_t* slopes, const in
   char* split = base + w.d + w.wt + w.xhat;
   const size_t split_bytes = ws_bytes - (w.d + w.wt + w.xhat);
 
-  const int64_t total = M * (Nd / 8);
-  const unsigned grid = (unsigned)((total + 255) / 256);
-  gated_dgrad_kernel<<<grid, 256, 0, stream>>>(dY, slopes, gamma, s_x, total, (int)N, (int)Nd, D);
-  if (hipError_t e = hipGetLastError()) return e;
-
+  const GatedD d{dY, slopes, gamma, s_x, M * (Nd / 8), (int)N, (int)Nd, D};
   const int wt_bx = dX != nullptr ? (int)(Kp / 64) : 0, wt_by = (int)((2 * Nd + 255) / 256);
   const int64_t want = (M * (Kp / 16) + 255) / 256;
   const int xhat_nb = dWg != nullptr ? (int)std::min<int64_t>(want, 4096) : 0;
-  gated_prep_kernel<<<wt_bx * wt_by + xhat_nb, 256, 0, stream>>>(w_packed, N, Kp, Nd, wt, wt_bx, wt_by, x_q, M, xhat,
-                                                                 xhat_nb);
+  const int64_t grid = wt_bx * wt_by + xhat_nb + (d.total + 255) / 256;
+  gated_prep_kernel<<<(unsigned)grid, 256, 0, stream>>>(w_packed, N, Kp, Nd, wt, wt_bx, wt_by, x_q, M, xhat, xhat_nb, d);
   if (hipError_t e = hipGetLastError()) return e;
   return dw_f32 ? gated_products<true>(D, wt, xhat, gamma, s_x, M, N, K, dX, dWg, dWu, split, split_bytes, stream)
                 : gated_products<false>(D, wt, xhat, gamma, s_x, M, N, K, dX, dWg, dWu, split, split_bytes, stream);
