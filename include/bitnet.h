@@ -651,7 +651,10 @@ bitnet_status bitnet_rmsnorm_bwd(const void* dY, bitnet_dtype y_dtype, const voi
  * rows_quant2: the rows of bf16 x [M][K] and of w [N][K] in w_dtype (a layer's activations
  *             and channels) in one launch; M or N may be 0.
  * rows_unpack: x [M][K] bf16 bits, 2-byte aligned. M * Kp <= 2^34.
+ * rows_direct: how many tokens of K values the forwards of the layers below take as
+ *             they are, each workgroup making the codes for itself (0: none).
  */
+int bitnet_rows_direct(int64_t K);
 bitnet_status bitnet_rows_quant(const void* x, bitnet_dtype x_dtype, int64_t M, int64_t K, int8_t* x_q, float* s_x,
                                 void* stream);
 bitnet_status bitnet_rows_quant2(const uint16_t* x, int64_t M, int8_t* x_q, float* s_x, const void* w,
@@ -675,7 +678,10 @@ bitnet_status bitnet_rows_unpack(const int8_t* x_q, const float* s_x, int64_t M,
  * (dg = dY u act'(g) and du = dY act(g) with the scales of what they are multiplied
  * by, rounded once; fp32 sums, divided in fp32.)
  *
- * x_q, s_x   8-bit rows (bitnet_act_quant, bitnet_rmsnorm_fwd).
+ * x          NULL, or the rows [M][K] as bf16 bits (2-byte aligned, M <=
+ *            bitnet_rows_direct(K)): they are quantized on the way as
+ *            bitnet_rows_quant does, and x_q and s_x are not used.
+ * x_q, s_x   8-bit rows (bitnet_rows_quant, bitnet_rmsnorm_fwd).
  * w_packed   [2N][Kp/4] codes and gamma [2] as bitnet_ternarize_pack writes them
  *            for each weight [N][K].
  * y, dY      [M][N] bf16 bits.
@@ -693,7 +699,7 @@ bitnet_status bitnet_rows_unpack(const int8_t* x_q, const float* s_x, int64_t M,
  */
 size_t bitnet_gated_slopes_bytes(int64_t M, int64_t N);
 size_t bitnet_gated_fwd_workspace_bytes(int64_t M, int64_t N, int64_t K);
-bitnet_status bitnet_gated_fwd(bitnet_act act, const int8_t* x_q, const float* s_x, const uint8_t* w_packed,
+bitnet_status bitnet_gated_fwd(bitnet_act act, const uint16_t* x, const int8_t* x_q, const float* s_x, const uint8_t* w_packed,
                                const float* gamma, int64_t M, int64_t N, int64_t K, uint16_t* y, void* slopes,
                                void* workspace, size_t workspace_bytes, void* stream);
 size_t bitnet_gated_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K);
@@ -715,7 +721,7 @@ bitnet_status bitnet_gated_bwd(const uint16_t* dY, const void* slopes, const int
  * quantizations).
  *
  * x_q [M][Kp], s_x [M]; w_q [N][Kp], s_w [N]: 8-bit rows (bitnet_rows_quant), columns
- *            K..Kp-1 zero.
+ *            K..Kp-1 zero.  x: as for bitnet_gated_fwd.
  * bias       [N] bf16 bits, or NULL.   y, dY [M][N] bf16 bits.
  * dX         [M][K] bf16 bits, or NULL.  dW [N][K] in dW_dtype, or NULL.  db [N] in
  *            db_dtype, or NULL; not all NULL.
@@ -727,7 +733,7 @@ bitnet_status bitnet_gated_bwd(const uint16_t* dY, const void* slopes, const int
  * needs (M + 256) * Kp and (N + 256) * Kp only), N <= 2^24.
  */
 size_t bitnet_int8_fwd_workspace_bytes(int64_t M, int64_t N, int64_t K);
-bitnet_status bitnet_int8_fwd(const int8_t* x_q, const float* s_x, const int8_t* w_q, const float* s_w,
+bitnet_status bitnet_int8_fwd(const uint16_t* x, const int8_t* x_q, const float* s_x, const int8_t* w_q, const float* s_w,
                               const uint16_t* bias, int64_t M, int64_t N, int64_t K, uint16_t* y, void* workspace,
                               size_t workspace_bytes, void* stream);
 size_t bitnet_int8_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K);

@@ -142,11 +142,13 @@ def lib():
     L.bitnet_rows_quant2.restype = st
     L.bitnet_rows_unpack.argtypes = [vp, vp, i64, i64, vp, vp]
     L.bitnet_rows_unpack.restype = st
-    L.bitnet_gated_fwd.argtypes = [st, vp, vp, vp, vp, i64, i64, i64, vp, vp, vp, sz, vp]
+    L.bitnet_gated_fwd.argtypes = [st, vp, vp, vp, vp, vp, i64, i64, i64, vp, vp, vp, sz, vp]
+    L.bitnet_rows_direct.argtypes = [i64]
+    L.bitnet_rows_direct.restype = ctypes.c_int
     L.bitnet_gated_fwd.restype = st
     L.bitnet_gated_bwd.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, vp, vp, vp, st, vp, sz, vp]
     L.bitnet_gated_bwd.restype = st
-    L.bitnet_int8_fwd.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, vp, vp, sz, vp]
+    L.bitnet_int8_fwd.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, vp, vp, sz, vp]
     L.bitnet_int8_fwd.restype = st
     L.bitnet_int8_bwd.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, vp, vp, st, vp, st, vp, sz, vp]
     L.bitnet_int8_bwd.restype = st
@@ -923,21 +925,28 @@ def _ws_args(workspace, need, like, stream):
     return _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 
-def bitnet_gated_fwd(act, x_q, s_x, w_packed, gamma, K, y, slopes=None, workspace=None, stream=None):
-    """y [M, N] bf16 = act(gate) * up of 8-bit rows x_q, s_x and the codes w_packed
-    uint8 [2N, Kp/4] with gamma float32 [2]; slopes uint8
-    [bitnet_gated_slopes_bytes(M, N)] is written too if given."""
+def bitnet_rows_direct(K):
+    return int(lib().bitnet_rows_direct(int(K)))
+
+
+def bitnet_gated_fwd(act, x_q, s_x, w_packed, gamma, K, y, slopes=None, workspace=None, stream=None, x=None):
+    """y [M, N] bf16 = act(gate) * up of 8-bit rows x_q, s_x (or of x bf16 [M, K], M <=
+    bitnet_rows_direct(K)) and the codes w_packed uint8 [2N, Kp/4] with gamma float32 [2];
+    slopes uint8 [bitnet_gated_slopes_bytes(M, N)] is written too if given."""
     M, N = y.shape
     _need(y, torch.bfloat16, (M, N), "y")
-    _need_rows8(x_q, s_x, M, K, "x")
+    if x is None:
+        _need_rows8(x_q, s_x, M, K, "x")
+    else:
+        _need(x, torch.bfloat16, (M, K), "x")
     _need(w_packed, torch.uint8, (2 * N, bitnet_k_pad(K) // 4), "w_packed")
     _need(gamma, torch.float32, (2,), "gamma")
     if slopes is not None:
         _need(slopes, torch.uint8, (bitnet_gated_slopes_bytes(M, N),), "slopes")
-    _same_device(y, x_q=x_q, s_x=s_x, w_packed=w_packed, gamma=gamma, slopes=slopes, workspace=workspace)
+    _same_device(y, x=x, x_q=x_q, s_x=s_x, w_packed=w_packed, gamma=gamma, slopes=slopes, workspace=workspace)
     ws, n = _ws_args(workspace, bitnet_gated_fwd_workspace_bytes(M, N, K), y, stream)
-    _run(lib().bitnet_gated_fwd, y, stream, int(act), _ptr(x_q), _ptr(s_x), _ptr(w_packed), _ptr(gamma), M, N, int(K),
-         _ptr(y), _ptr(slopes), ws, n)
+    _run(lib().bitnet_gated_fwd, y, stream, int(act), _ptr(x), _ptr(x_q), _ptr(s_x), _ptr(w_packed), _ptr(gamma), M, N,
+         int(K), _ptr(y), _ptr(slopes), ws, n)
 
 
 def bitnet_gated_bwd(dY, slopes, x_q, s_x, w_packed, gamma, K, dX=None, dW_gate=None, dW_up=None, workspace=None,
@@ -978,19 +987,22 @@ def bitnet_int8_bwd_workspace_bytes(M, N, K):
     return int(lib().bitnet_int8_bwd_workspace_bytes(int(M), int(N), int(K)))
 
 
-def bitnet_int8_fwd(x_q, s_x, w_q, s_w, K, y, bias=None, workspace=None, stream=None):
-    """y [M, N] bf16 of 8-bit rows x_q, s_x (tokens) and w_q, s_w (channels), with an
-    optional bf16 bias [N]."""
+def bitnet_int8_fwd(x_q, s_x, w_q, s_w, K, y, bias=None, workspace=None, stream=None, x=None):
+    """y [M, N] bf16 of 8-bit rows x_q, s_x (tokens; or of x bf16 [M, K], M <=
+    bitnet_rows_direct(K)) and w_q, s_w (channels), with an optional bf16 bias [N]."""
     M, N = y.shape
     _need(y, torch.bfloat16, (M, N), "y")
-    _need_rows8(x_q, s_x, M, K, "x")
+    if x is None:
+        _need_rows8(x_q, s_x, M, K, "x")
+    else:
+        _need(x, torch.bfloat16, (M, K), "x")
     _need_rows8(w_q, s_w, N, K, "w")
     if bias is not None:
         _need(bias, torch.bfloat16, (N,), "bias")
-    _same_device(y, x_q=x_q, s_x=s_x, w_q=w_q, s_w=s_w, bias=bias, workspace=workspace)
+    _same_device(y, x=x, x_q=x_q, s_x=s_x, w_q=w_q, s_w=s_w, bias=bias, workspace=workspace)
     ws, n = _ws_args(workspace, bitnet_int8_fwd_workspace_bytes(M, N, K), y, stream)
-    _run(lib().bitnet_int8_fwd, y, stream, _ptr(x_q), _ptr(s_x), _ptr(w_q), _ptr(s_w), _ptr(bias), M, N, int(K), _ptr(y),
-         ws, n)
+    _run(lib().bitnet_int8_fwd, y, stream, _ptr(x), _ptr(x_q), _ptr(s_x), _ptr(w_q), _ptr(s_w), _ptr(bias), M, N, int(K),
+         _ptr(y), ws, n)
 
 
 def bitnet_int8_bwd(dY, x_q, s_x, w_q, s_w, K, dX=None, dW=None, db=None, workspace=None, stream=None):

@@ -629,18 +629,21 @@ size_t bitnet_gated_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   return check_gated_sizes(M, N, K) != BITNET_OK ? 0 : bitnet::gated_bwd_workspace(M, N, K);
 }
 
-bitnet_status bitnet_gated_fwd(bitnet_act act, const int8_t* x_q, const float* s_x, const uint8_t* w_packed,
+int bitnet_rows_direct(int64_t K) { return bitnet::rows_direct(K); }
+
+bitnet_status bitnet_gated_fwd(bitnet_act act, const uint16_t* x, const int8_t* x_q, const float* s_x, const uint8_t* w_packed,
                                const float* gamma, int64_t M, int64_t N, int64_t K, uint16_t* y, void* slopes,
                                void* workspace, size_t workspace_bytes, void* stream) {
-  if (!x_q || !s_x || !w_packed || !gamma || !y) return BITNET_ERR_NULL;
+  if ((!x && (!x_q || !s_x)) || !w_packed || !gamma || !y) return BITNET_ERR_NULL;
   if (act != BITNET_ACT_SILU && act != BITNET_ACT_RELU2) return BITNET_ERR_DTYPE;
   if (bitnet_status st = check_gated_sizes(M, N, K)) return st;
+  if (x && M > bitnet::rows_direct(K)) return BITNET_ERR_SHAPE;
   const size_t need = bitnet_gated_fwd_workspace_bytes(M, N, K);
   if (workspace_bytes < need || (workspace_bytes > 0 && !workspace)) return BITNET_ERR_WORKSPACE;
   if (!aligned(workspace, 16) || !aligned(x_q, 16) || !aligned(s_x, 16) || !aligned(w_packed, 16) ||
-      !aligned(gamma, 4) || !aligned(y, 16) || !aligned(slopes, 16))
+      !aligned(gamma, 4) || !aligned(y, 16) || !aligned(slopes, 16) || !aligned(x, 2))
     return BITNET_ERR_ALIGN;
-  return from_hip(bitnet::launch_gated_fwd(act == BITNET_ACT_RELU2, x_q, s_x, w_packed, gamma, M, N, K, y,
+  return from_hip(bitnet::launch_gated_fwd(act == BITNET_ACT_RELU2, x, x_q, s_x, w_packed, gamma, M, N, K, y,
                                            static_cast<uint16_t*>(slopes), workspace, workspace_bytes, static_cast<hipStream_t>(stream)));
 }
 
@@ -673,17 +676,18 @@ size_t bitnet_int8_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   return check_int8_sizes(M, N, K, true) != BITNET_OK ? 0 : bitnet::int8_bwd_workspace(M, N, K);
 }
 
-bitnet_status bitnet_int8_fwd(const int8_t* x_q, const float* s_x, const int8_t* w_q, const float* s_w,
+bitnet_status bitnet_int8_fwd(const uint16_t* x, const int8_t* x_q, const float* s_x, const int8_t* w_q, const float* s_w,
                               const uint16_t* bias, int64_t M, int64_t N, int64_t K, uint16_t* y, void* workspace,
                               size_t workspace_bytes, void* stream) {
-  if (!x_q || !s_x || !w_q || !s_w || !y) return BITNET_ERR_NULL;
+  if ((!x && (!x_q || !s_x)) || !w_q || !s_w || !y) return BITNET_ERR_NULL;
   if (bitnet_status st = check_int8_sizes(M, N, K, false)) return st;
+  if (x && M > bitnet::rows_direct(K)) return BITNET_ERR_SHAPE;
   const size_t need = bitnet_int8_fwd_workspace_bytes(M, N, K);
   if (workspace_bytes < need || (workspace_bytes > 0 && !workspace)) return BITNET_ERR_WORKSPACE;
   if (!aligned(workspace, 16) || !aligned(x_q, 16) || !aligned(s_x, 16) || !aligned(w_q, 16) || !aligned(s_w, 16) ||
-      !aligned(bias, 16) || !aligned(y, 16))
+      !aligned(bias, 16) || !aligned(y, 16) || !aligned(x, 2))
     return BITNET_ERR_ALIGN;
-  return from_hip(bitnet::launch_int8_fwd(x_q, s_x, w_q, s_w, bias, M, N, K, y, workspace, workspace_bytes,
+  return from_hip(bitnet::launch_int8_fwd(x, x_q, s_x, w_q, s_w, bias, M, N, K, y, workspace, workspace_bytes,
                                           static_cast<hipStream_t>(stream)));
 }
 

@@ -27,6 +27,7 @@
 
 #include "device_common.h"
 #include "gemm_core.h"
+#include "rows_quant.h"
 
 namespace bitnet {
 
@@ -38,6 +39,8 @@ struct FewArgs {
   const int8_t* xq;  // [M][Kp]
   int64_t Kp;
   int M;
+  const uint16_t* x;  // [M][K] (FewRows)
+  int K;
 };
 
 template <bool CODES>
@@ -64,14 +67,90 @@ constexpr int few_lds() {
   return x > red ? x : red;
 }
 
+// The codes of up to NX tokens of at most kMaxK values, which every workgroup makes
+// of the bf16 rows for itself while its first weights are on the way: no launch before
+// this one, and no codes in memory. Measured, us, against the rows' launch and the
+// product: codes, 2560 -> 2 x 6912 1 token 6.3 (2.8 + 5.9), 4 tokens 8.5 (2.8 + 6.1);
+// int8, 2560 -> 32000 1 token 14.7 (2.9 + 15.6), 4 tokens 19.6 (3.9 + 15.8). The work is a
+// row's reduction and codes for each token in every workgroup, so more tokens lose.
+template <int NX, int W>
+struct FewRows {
+  static constexpr int kThreads = kWave * W, kChunks = 2, kMaxK = 8 * kChunks * kThreads;
+  __attribute__((aligned(16))) int8_t codes[NX][kMaxK];
+  float s[NX], slot[NX][W];
+};
+template <int W>
+struct FewRows<0, W> {};
+
+template <int NX, int W>
+struct FewChunks {
+  ChunkBf16 c[NX][FewRows<NX, W>::kChunks];
+};
+template <int W>
+struct FewChunks<0, W> {};
+
+// 8 <= K <= kMaxK
+template <int NX, int W>
+__device__ __forceinline__ void few_rows_load(const FewArgs& a, FewChunks<NX, W>& v) {
+  typedef FewRows<NX, W> R;
+#pragma unroll
+  for (int m = 0; m < NX; ++m)
+#pragma unroll
+    for (int i = 0; i < R::kChunks; ++i)
+      v.c[m][i] = load8<false>(a.x + (int64_t)(m < a.M ? m : 0) * a.K, 8 * ((int)threadIdx.x + i * R::kThreads), a.K);
+}
+
+// Ends with a barrier.
+template <int NX, int W>
+__device__ __forceinline__ void few_rows_quantize(const FewArgs& a, FewChunks<NX, W>& v, FewRows<NX, W>& r) {
+  typedef FewRows<NX, W> R;
+  const int t = threadIdx.x, lane = t % kWave, wave = t / kWave, nq = (int)(a.Kp / 8);
+#pragma unroll
+  for (int m = 0; m < NX; ++m) {
+    uint32_t mx = 0;
+#pragma unroll
+    for (int i = 0; i < R::kChunks; ++i) {
+      settle8<false>(v.c[m][i], 8 * (t + i * R::kThreads), a.K);
+      const uint32_t o = magnitude8(v.c[m][i]);
+      mx = o > mx ? o : mx;
+    }
+    mx = row_max_bits<kWave>(mx, nullptr);
+    if (lane == 0) r.slot[m][wave] = __uint_as_float(mx);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int m = 0; m < NX; ++m) {
+    if (m >= a.M) break;
+    uint32_t mx = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const uint32_t o = __float_as_uint(r.slot[m][w]);
+      mx = o > mx ? o : mx;
+    }
+    const float s = row_scale(mx);
+    if (t == 0) r.s[m] = s;
+#pragma unroll
+    for (int i = 0; i < R::kChunks; ++i) {
+      const int ch = t + i * R::kThreads;
+      if (ch >= nq) continue;
+      float f[8];
+      v.c[m][i].get(f);
+      *reinterpret_cast<uint2*>(&r.codes[m][8 * ch]) = codes8(f, s);
+    }
+  }
+  __syncthreads();
+}
+
 // The waves' partial tiles in smem (few_lds bytes), after a barrier. row[t]: this
 // lane's weight row of tile t (of lane % 16), negative for none; TW: row[0] the first of
-// 16 RT consecutive rows.
-template <bool CODES, int RT, int MT, int W, int P, bool TX, bool TW>
-__device__ __forceinline__ void few_tokens_product(const FewArgs& a, const int64_t (&row)[RT], char* smem) {
+// 16 RT consecutive rows. NX (MT 1, not TX): the tokens are a.x's, not a.xq's.
+template <bool CODES, int RT, int MT, int W, int P, bool TX, bool TW, int NX>
+__device__ __forceinline__ void few_tokens_product(const FewArgs& a, const int64_t (&row)[RT], char* smem,
+                                                   FewRows<NX, W>& rows) {
+  static_assert(NX == 0 || (MT == 1 && !TX), "codes made here are read where they lie");
   typedef FewStep<CODES> S;
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, q = lane >> 4, r16 = lane & 15;
-  const rsrc_t rw = make_rsrc(a.w, (uint32_t)(a.rows * a.pitch)), rx = make_rsrc(a.xq, (uint32_t)(a.M * a.Kp));
+  const rsrc_t rw = make_rsrc(a.w, (uint32_t)(a.rows * a.pitch)), rx = make_rsrc(a.xq, NX > 0 ? 0u : (uint32_t)(a.M * a.Kp));
   constexpr int kLanes = S::kK / 16, kRows = kWave / kLanes;  // of a row, of a load (kTurn)
   constexpr int kPitch = S::kK + 16;
   char* xl = smem + wave * (16 * ((TX ? MT : 0) + (TW ? RT : 0)) * kPitch);
@@ -100,7 +179,8 @@ __device__ __forceinline__ void few_tokens_product(const FewArgs& a, const int64
         const int64_t k = k0 + 64 * (CODES ? q : j);
         b.w[t][j] = buf_load16(rw, k < a.Kp ? woff[t] + (uint32_t)(CODES ? k / 4 : k + 16 * q) : kOob);
       }
-    if constexpr (TX) {
+    if constexpr (NX > 0) {
+    } else if constexpr (TX) {
 #pragma unroll
       for (int i = 0; i < MT * S::kJ; ++i) {
         const int r = i * kRows + xr;
@@ -120,7 +200,15 @@ __device__ __forceinline__ void few_tokens_product(const FewArgs& a, const int64
   for (int t = 0; t < RT; ++t)
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) acc[t][mt] = i32x4acc_t{0, 0, 0, 0};
-  const auto compute = [&](Step& b) {
+  const auto compute = [&](Step& b, int64_t s) {
+    if constexpr (NX > 0) {
+#pragma unroll
+      for (int j = 0; j < S::kJ; ++j) {
+        const int64_t k = s * S::kK + 64 * j;
+        b.x[0][j] = make_uint4(0u, 0u, 0u, 0u);
+        if (r16 < a.M && k < a.Kp) b.x[0][j] = *reinterpret_cast<const uint4*>(&rows.codes[r16][k + 16 * q]);
+      }
+    }
     if constexpr (CODES) {
 #pragma unroll
       for (int t = 0; t < RT; ++t) transpose4(b.w[t][0]);
@@ -167,12 +255,15 @@ __device__ __forceinline__ void few_tokens_product(const FewArgs& a, const int64
 
   const int64_t steps = (a.Kp + S::kK - 1) / S::kK;
   Step buf[P];
+  FewChunks<NX, W> chunks;
+  if constexpr (NX > 0) few_rows_load<NX, W>(a, chunks);
 #pragma unroll
   for (int d = 0; d < P; ++d) load(buf[d], wave + d * W);
+  if constexpr (NX > 0) few_rows_quantize<NX, W>(a, chunks, rows);
   for (int64_t s = wave; s < steps; s += P * W) {
 #pragma unroll
     for (int d = 0; d < P; ++d) {
-      compute(buf[d]);  // past the last step: zeros
+      compute(buf[d], s + d * W);  // past the last step: zeros
       load(buf[d], s + (P + d) * W);
     }
   }

@@ -224,11 +224,12 @@ struct GatedEpilogue {
 // ---------------------------------------------------------------------------
 
 // RP: pairs of tiles.
-template <class ACT, int RP, int MT, int W, int P, bool TX>
+template <class ACT, int RP, int MT, int W, int P, bool TX, int NX>
 __global__ __launch_bounds__(kWave * W) void gated_few_kernel(FewArgs a, const float* __restrict__ s,
                                                               const float* __restrict__ gamma, int64_t N, int64_t Nd,
                                                               uint16_t* __restrict__ y, uint16_t* __restrict__ slopes) {
   __shared__ __attribute__((aligned(16))) char smem[few_lds<true, 2 * RP, MT, W, TX, false>()];
+  __shared__ FewRows<NX, W> rows;
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int64_t n0 = (int64_t)blockIdx.x * (16 * RP);
   int64_t row[2 * RP];
@@ -238,7 +239,7 @@ __global__ __launch_bounds__(kWave * W) void gated_few_kernel(FewArgs a, const f
     row[2 * p] = n < N ? n : -1;
     row[2 * p + 1] = n < N ? N + n : -1;
   }
-  few_tokens_product<true, 2 * RP, MT, W, P, TX, false>(a, row, smem);
+  few_tokens_product<true, 2 * RP, MT, W, P, TX, false>(a, row, smem, rows);
   for (int i = wave; i < RP * MT; i += W) {
     const int p = i % RP, mt = i / RP;
     const int64_t m = 16 * mt + (lane & 15);
@@ -246,7 +247,10 @@ __global__ __launch_bounds__(kWave * W) void gated_few_kernel(FewArgs a, const f
     int vg[4], vu[4];
     few_tokens_sum<2 * RP, MT, W>(smem, 2 * p, mt, vg);
     few_tokens_sum<2 * RP, MT, W>(smem, 2 * p + 1, mt, vu);
-    const float cg = s[m] * gamma[0] / 127.0f, cu = s[m] * gamma[1] / 127.0f;  // the large-M epilogue's expressions
+    float sm;
+    if constexpr (NX > 0) sm = rows.s[m];
+    else sm = s[m];
+    const float cg = sm * gamma[0] / 127.0f, cu = sm * gamma[1] / 127.0f;  // the large-M epilogue's expressions
     const int64_t nb = n0 + 16 * p + 4 * (lane >> 4);
     float dg[4], du[4], o[4];
 #pragma unroll
@@ -419,25 +423,34 @@ size_t gated_fwd_workspace(int64_t M, int64_t N, int64_t K) {
   return split_workspace(g, split_grid(g, device_cus()));
 }
 
-template <class ACT, int RP, int MT, int W, int P, bool TX>
+template <class ACT, int RP, int MT, int W, int P, bool TX, int NX = 0>
 static void gated_few(const FewArgs& a, const float* s, const float* gamma, int64_t N, int64_t Nd, uint16_t* y,
                       uint16_t* slopes, hipStream_t st) {
-  gated_few_kernel<ACT, RP, MT, W, P, TX>
+  gated_few_kernel<ACT, RP, MT, W, P, TX, NX>
       <<<(unsigned)((N + 16 * RP - 1) / (16 * RP)), kWave * W, 0, st>>>(a, s, gamma, N, Nd, y, slopes);
 }
 
 template <class ACT>
-static hipError_t gated_fwd(const int8_t* x_q, const float* s_x, const uint8_t* w_packed, const float* gamma, int64_t M,
-                            int64_t N, int64_t K, uint16_t* y, uint16_t* slopes, void* ws, size_t ws_bytes,
-                            hipStream_t stream) {
+static hipError_t gated_fwd(const uint16_t* x, const int8_t* x_q, const float* s_x, const uint8_t* w_packed,
+                            const float* gamma, int64_t M, int64_t N, int64_t K, uint16_t* y, uint16_t* slopes, void* ws,
+                            size_t ws_bytes, hipStream_t stream) {
   const int64_t Kp = k_pad(K), Nd = n_half(N);
   if (few(M)) {
-    const FewArgs a{w_packed, 2 * N, Kp / 4, x_q, Kp, (int)M};
+    const FewArgs a{w_packed, 2 * N, Kp / 4, x_q, Kp, (int)M, x, (int)K};
     // Up to 32 tokens 16 outputs a workgroup of 4 waves, or 8 where each would have more
     // than 3 steps (1 token, 6912 -> 2 x 2560: 6.0 us with 8, 7.1 with 4; 2560 -> 2 x 6912
     // 8.1 and 5.7). Above, x_q's traffic counts: 32 outputs share it (64 tokens, 2560 -> 2 x
     // 6912: 8.7 us against 15.3 with 16, 6912 -> 2 x 2560 12.4 against 13.5).
     const bool deep = Kp > 12 * FewStep<true>::kK;
+    if (x != nullptr) {  // M <= rows_direct(K)
+      if (M > 2 && deep) gated_few<ACT, 1, 1, 8, 3, false, 4>(a, s_x, gamma, N, Nd, y, slopes, stream);
+      else if (M > 2) gated_few<ACT, 1, 1, 4, 3, false, 4>(a, s_x, gamma, N, Nd, y, slopes, stream);
+      else if (M > 1 && deep) gated_few<ACT, 1, 1, 8, 3, false, 2>(a, s_x, gamma, N, Nd, y, slopes, stream);
+      else if (M > 1) gated_few<ACT, 1, 1, 4, 3, false, 2>(a, s_x, gamma, N, Nd, y, slopes, stream);
+      else if (deep) gated_few<ACT, 1, 1, 8, 3, false, 1>(a, s_x, gamma, N, Nd, y, slopes, stream);
+      else gated_few<ACT, 1, 1, 4, 3, false, 1>(a, s_x, gamma, N, Nd, y, slopes, stream);
+      return hipGetLastError();
+    }
     if (M > 32) gated_few<ACT, 2, 4, 8, 1, true>(a, s_x, gamma, N, Nd, y, slopes, stream);
     else if (M > 16 && deep) gated_few<ACT, 1, 2, 8, 2, true>(a, s_x, gamma, N, Nd, y, slopes, stream);
     else if (M > 16) gated_few<ACT, 1, 2, 4, 2, true>(a, s_x, gamma, N, Nd, y, slopes, stream);
@@ -459,11 +472,11 @@ static hipError_t gated_fwd(const int8_t* x_q, const float* s_x, const uint8_t* 
   return run_gemm<MfmaI8, 1>(pl, ql, GatedEpilogue<ACT, false>{y, nullptr, s_x, gamma, N, Nd, M}, g, ws, ws_bytes, stream);
 }
 
-hipError_t launch_gated_fwd(bool relu2, const int8_t* x_q, const float* s_x, const uint8_t* w_packed, const float* gamma,
-                            int64_t M, int64_t N, int64_t K, uint16_t* y, uint16_t* slopes, void* ws, size_t ws_bytes,
-                            hipStream_t stream) {
-  return relu2 ? gated_fwd<ActRelu2>(x_q, s_x, w_packed, gamma, M, N, K, y, slopes, ws, ws_bytes, stream)
-               : gated_fwd<ActSilu>(x_q, s_x, w_packed, gamma, M, N, K, y, slopes, ws, ws_bytes, stream);
+hipError_t launch_gated_fwd(bool relu2, const uint16_t* x, const int8_t* x_q, const float* s_x, const uint8_t* w_packed,
+                            const float* gamma, int64_t M, int64_t N, int64_t K, uint16_t* y, uint16_t* slopes, void* ws,
+                            size_t ws_bytes, hipStream_t stream) {
+  return relu2 ? gated_fwd<ActRelu2>(x, x_q, s_x, w_packed, gamma, M, N, K, y, slopes, ws, ws_bytes, stream)
+               : gated_fwd<ActSilu>(x, x_q, s_x, w_packed, gamma, M, N, K, y, slopes, ws, ws_bytes, stream);
 }
 
 // The backward's workspace: D, the transposed codes, x_hat, then the products'

@@ -569,19 +569,23 @@ Tensor rows_values(const Tensor& carrier, const Tensor& codes, const Tensor& sca
 struct Rows {
   Tensor q, s, x2;  // x2: activations that are still to be quantized into q and s
   int64_t M, K;
-  Rows(const Tensor& x, const Tensor& codes, const Tensor& scales) : K(x.size(-1)) {
+  bool direct = false;  // x2 goes to the kernel as it is; there are no q and s
+  // may_direct: where the product takes so few rows itself.
+  Rows(const Tensor& x, const Tensor& codes, const Tensor& scales, bool may_direct = false) : K(x.size(-1)) {
     M = x.numel() / K;
     if (codes.defined()) {
       q = aligned(codes);
       s = aligned(scales);
       return;
     }
-    x2 = aligned(rows(x));
+    direct = may_direct && M <= bitnet_rows_direct(K);
+    x2 = direct ? rows(x) : aligned(rows(x));
+    if (direct) return;
     q = at::empty({M, bitnet_k_pad(K)}, x.options().dtype(at::kChar));
     s = at::empty({M}, x.options().dtype(at::kFloat));
   }
   void quantize(void* stream) const {
-    if (x2.defined()) check(bitnet_rows_quant(bf16(x2), BITNET_BF16, M, K, i8(q), f32(s), stream));
+    if (x2.defined() && !direct) check(bitnet_rows_quant(bf16(x2), BITNET_BF16, M, K, i8(q), f32(s), stream));
   }
 };
 
@@ -763,8 +767,8 @@ Tensor gated_forward(const Rows& x, at::IntArrayRef shape, const Tensor& packed,
   const size_t bytes = bitnet_gated_fwd_workspace_bytes(x.M, N, x.K);
   const Tensor ws = scratch(bytes, packed);
   On on(packed);
-  check(bitnet_gated_fwd(static_cast<bitnet_act>(act), i8(x.q), f32(x.s), static_cast<uint8_t*>(ptr(packed)), f32(gamma),
-                         x.M, N, x.K, bf16(y), ptr(slopes), bytes ? ptr(ws) : nullptr, bytes, on.stream));
+  check(bitnet_gated_fwd(static_cast<bitnet_act>(act), x.direct ? bf16(x.x2) : nullptr, i8(x.q), f32(x.s),
+                         static_cast<uint8_t*>(ptr(packed)), f32(gamma), x.M, N, x.K, bf16(y), ptr(slopes), bytes ? ptr(ws) : nullptr, bytes, on.stream));
   return y;
 }
 
@@ -846,10 +850,10 @@ Tensor gated_bitlinear(const Tensor& x, const optional<Tensor>& codes, const opt
 struct GatedFrozenFn : torch::autograd::Function<GatedFrozenFn> {
   static Tensor forward(AutogradContext* ctx, const Tensor& x, const optional<Tensor>& codes,
                         const optional<Tensor>& scales, const Tensor& packed, const Tensor& gamma, int64_t act) {
-    const Rows r(x, codes.value_or(Tensor()), scales.value_or(Tensor()));
-    const Tensor slopes = empty_slopes(r.M, packed.size(0) / 2, r.q);
+    const Rows r(x, codes.value_or(Tensor()), scales.value_or(Tensor()), true);
+    const Tensor slopes = empty_slopes(r.M, packed.size(0) / 2, packed);
     if (r.M > 0) {
-      On on(r.q);
+      On on(packed);
       r.quantize(on.stream);
     }
     Tensor y = gated_forward(r, x.sizes(), packed, gamma, act, slopes);
@@ -895,9 +899,9 @@ Tensor gated_bitlinear_inference(const Tensor& x, const optional<Tensor>& codes,
                     "x, w_packed and gamma: must be GPU tensors of one device");
   const Tensor packed = aligned(w_packed), gamma = gamma_.contiguous();
   if (wants_grad({&x})) return GatedFrozenFn::apply(x, codes, scales, packed, gamma, act);
-  const Rows r(x, q, s);
+  const Rows r(x, q, s, true);
   if (r.M > 0) {
-    On on(r.q);
+    On on(packed);
     r.quantize(on.stream);
   }
   return gated_forward(r, x.sizes(), packed, gamma, act, Tensor());
@@ -925,7 +929,7 @@ Tensor int8_forward(const Rows& x, at::IntArrayRef shape, const Tensor& wq, cons
   const size_t bytes = bitnet_int8_fwd_workspace_bytes(x.M, N, x.K);
   const Tensor ws = scratch(bytes, wq);
   On on(wq);
-  check(bitnet_int8_fwd(i8(x.q), f32(x.s), i8(wq), f32(sw), bf16(b), x.M, N, x.K, bf16(y), bytes ? ptr(ws) : nullptr,
+  check(bitnet_int8_fwd(x.direct ? bf16(x.x2) : nullptr, i8(x.q), f32(x.s), i8(wq), f32(sw), bf16(b), x.M, N, x.K, bf16(y), bytes ? ptr(ws) : nullptr,
                         bytes, on.stream));
   return y;
 }
@@ -986,9 +990,9 @@ struct Int8Fn : torch::autograd::Function<Int8Fn> {
 struct Int8FrozenFn : torch::autograd::Function<Int8FrozenFn> {
   static Tensor forward(AutogradContext* ctx, const Tensor& x, const optional<Tensor>& codes,
                         const optional<Tensor>& scales, const Tensor& wq, const Tensor& sw, const optional<Tensor>& bias) {
-    const Rows r(x, codes.value_or(Tensor()), scales.value_or(Tensor()));
+    const Rows r(x, codes.value_or(Tensor()), scales.value_or(Tensor()), true);
     if (r.M > 0) {
-      On on(r.q);
+      On on(wq);
       r.quantize(on.stream);
     }
     Tensor y = int8_forward(r, x.sizes(), wq, sw, bias.value_or(Tensor()));
@@ -1051,9 +1055,9 @@ Tensor int8_linear_inference(const Tensor& x, const optional<Tensor>& codes, con
   check_bias(b, w_q.size(0), x);
   const Tensor wq = aligned(w_q), sw = aligned(s_w);
   if (wants_grad({&x, &b})) return Int8FrozenFn::apply(x, codes, scales, wq, sw, bias);
-  const Rows r(x, q, s);
+  const Rows r(x, q, s, true);
   if (r.M > 0) {
-    On on(r.q);
+    On on(wq);
     r.quantize(on.stream);
   }
   return int8_forward(r, x.sizes(), wq, sw, b);

@@ -76,25 +76,29 @@ struct Int8Epilogue {
 };
 
 // Few tokens (few8.h).
-template <int RT, int MT, int W, int P, bool TX>
+template <int RT, int MT, int W, int P, bool TX, int NX>
 __global__ __launch_bounds__(kWave * W) void int8_few_kernel(FewArgs a, const float* __restrict__ s,
                                                              const float* __restrict__ sw,
                                                              const uint16_t* __restrict__ bias,
                                                              uint16_t* __restrict__ y) {
   __shared__ __attribute__((aligned(16))) char smem[few_lds<false, RT, MT, W, TX, true>()];
+  __shared__ FewRows<NX, W> rows;
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int64_t n0 = (int64_t)blockIdx.x * (16 * RT), N = a.rows;
   int64_t row[RT];
 #pragma unroll
   for (int t = 0; t < RT; ++t) row[t] = n0;
-  few_tokens_product<false, RT, MT, W, P, TX, true>(a, row, smem);
+  few_tokens_product<false, RT, MT, W, P, TX, true>(a, row, smem, rows);
   for (int i = wave; i < RT * MT; i += W) {
     const int t = i % RT, mt = i / RT;
     const int64_t m = 16 * mt + (lane & 15);
     if (m >= a.M) continue;
     int v[4];
     few_tokens_sum<RT, MT, W>(smem, t, mt, v);
-    const float c = s[m] / 127.0f;  // the large-M epilogue's expressions
+    float sm;
+    if constexpr (NX > 0) sm = rows.s[m];
+    else sm = s[m];
+    const float c = sm / 127.0f;  // the large-M epilogue's expressions
     const int64_t nb = n0 + 16 * t + 4 * (lane >> 4);
     float f[4];
 #pragma unroll
@@ -105,10 +109,10 @@ __global__ __launch_bounds__(kWave * W) void int8_few_kernel(FewArgs a, const fl
   }
 }
 
-template <int RT, int MT, int W, int P, bool TX>
+template <int RT, int MT, int W, int P, bool TX, int NX = 0>
 static void int8_few_at(const FewArgs& a, const float* s, const float* sw, const uint16_t* bias, uint16_t* y,
                         hipStream_t st) {
-  int8_few_kernel<RT, MT, W, P, TX><<<(unsigned)((a.rows + 16 * RT - 1) / (16 * RT)), kWave * W, 0, st>>>(a, s, sw, bias, y);
+  int8_few_kernel<RT, MT, W, P, TX, NX><<<(unsigned)((a.rows + 16 * RT - 1) / (16 * RT)), kWave * W, 0, st>>>(a, s, sw, bias, y);
 }
 
 // Up to 16 tokens 16 rows a workgroup of 4 waves, at every N (16 tokens 2560 -> 32000: 15.5
@@ -119,7 +123,15 @@ static void int8_few_at(const FewArgs& a, const float* s, const float* sw, const
 static void int8_few(const FewArgs& a, const float* s, const float* sw, const uint16_t* bias, uint16_t* y,
                      hipStream_t st) {
   const int64_t tiles = (a.rows + 15) / 16;
-  if (a.M <= 2) int8_few_at<1, 1, 4, 5, false>(a, s, sw, bias, y, st);
+  if (a.x != nullptr) {  // M <= rows_direct(K)
+    const bool deep = a.Kp > FewRows<1, 4>::kMaxK;
+    if (a.M > 2 && deep) int8_few_at<1, 1, 8, 5, false, 4>(a, s, sw, bias, y, st);
+    else if (a.M > 2) int8_few_at<1, 1, 4, 5, false, 4>(a, s, sw, bias, y, st);
+    else if (a.M > 1 && deep) int8_few_at<1, 1, 8, 5, false, 2>(a, s, sw, bias, y, st);
+    else if (a.M > 1) int8_few_at<1, 1, 4, 5, false, 2>(a, s, sw, bias, y, st);
+    else if (deep) int8_few_at<1, 1, 8, 5, false, 1>(a, s, sw, bias, y, st);
+    else int8_few_at<1, 1, 4, 5, false, 1>(a, s, sw, bias, y, st);
+  } else if (a.M <= 2) int8_few_at<1, 1, 4, 5, false>(a, s, sw, bias, y, st);
   else if (a.M <= 16) int8_few_at<1, 1, 4, 5, true>(a, s, sw, bias, y, st);
   else if (a.M <= 32 && tiles <= 256) int8_few_at<1, 2, 4, 5, true>(a, s, sw, bias, y, st);
   else if (a.M <= 32 && tiles <= 512) int8_few_at<2, 2, 4, 4, true>(a, s, sw, bias, y, st);
@@ -139,12 +151,14 @@ size_t int8_fwd_workspace(int64_t M, int64_t N, int64_t K) {
   return split_workspace(g, split_grid(g, device_cus()));
 }
 
-hipError_t launch_int8_fwd(const int8_t* x_q, const float* s_x, const int8_t* w_q, const float* s_w,
+int rows_direct(int64_t K) { return few(1) && K >= 8 && K <= FewRows<1, 8>::kMaxK ? 4 : 0; }
+
+hipError_t launch_int8_fwd(const uint16_t* x, const int8_t* x_q, const float* s_x, const int8_t* w_q, const float* s_w,
                            const uint16_t* bias, int64_t M, int64_t N, int64_t K, uint16_t* y, void* ws,
                            size_t ws_bytes, hipStream_t stream) {
   const int64_t Kp = k_pad(K);
   if (few(M)) {
-    const FewArgs a{reinterpret_cast<const uint8_t*>(w_q), N, Kp, x_q, Kp, (int)M};
+    const FewArgs a{reinterpret_cast<const uint8_t*>(w_q), N, Kp, x_q, Kp, (int)M, x, (int)K};
     int8_few(a, s_x, s_w, bias, y, stream);
     return hipGetLastError();
   }

@@ -246,14 +246,18 @@ hipError_t launch_rows_quant(const uint16_t* x, int64_t M, int8_t* x_q, float* s
 hipError_t launch_rows_unpack(const int8_t* x_q, const float* s_x, int64_t M, int64_t K, uint16_t* x,
                               hipStream_t stream);
 
+// The most tokens whose bf16 rows of K values the two forwards below take as x (not
+// NULL: x_q and s_x are not read).
+int rows_direct(int64_t K);
+
 // The gated pair of ternary projections: codes [2N][Kp/4] and scales gamma [2],
 // gate first. slopes: dy/dg and dy/du in 24 bits (NULL: not kept). dWg and dWu
 // both or neither; s_x NULL only without them.
 size_t gated_slopes_bytes(int64_t M, int64_t N);
 size_t gated_fwd_workspace(int64_t M, int64_t N, int64_t K);
-hipError_t launch_gated_fwd(bool relu2, const int8_t* x_q, const float* s_x, const uint8_t* w_packed, const float* gamma,
-                            int64_t M, int64_t N, int64_t K, uint16_t* y, uint16_t* slopes, void* ws, size_t ws_bytes,
-                            hipStream_t stream);
+hipError_t launch_gated_fwd(bool relu2, const uint16_t* x, const int8_t* x_q, const float* s_x, const uint8_t* w_packed,
+                            const float* gamma, int64_t M, int64_t N, int64_t K, uint16_t* y, uint16_t* slopes, void* ws,
+                            size_t ws_bytes, hipStream_t stream);
 size_t gated_bwd_workspace(int64_t M, int64_t N, int64_t K);
 hipError_t launch_gated_bwd(const uint16_t* dY, const uint16_t* slopes, const int8_t* x_q, const float* s_x,
                             const uint8_t* w_packed, const float* gamma, int64_t M, int64_t N, int64_t K, uint16_t* dX,
@@ -261,9 +265,9 @@ hipError_t launch_gated_bwd(const uint16_t* dY, const uint16_t* slopes, const in
 
 // Linear layer in 8-bit integers: x_q [M][Kp], w_q [N][Kp], a scale a row each.
 size_t int8_fwd_workspace(int64_t M, int64_t N, int64_t K);
-hipError_t launch_int8_fwd(const int8_t* x_q, const float* s_x, const int8_t* w_q, const float* s_w,
-                           const uint16_t* bias, int64_t M, int64_t N, int64_t K, uint16_t* y, void* ws,
-                           size_t ws_bytes, hipStream_t stream);
+hipError_t launch_int8_fwd(const uint16_t* x, const int8_t* x_q, const float* s_x, const int8_t* w_q, const float* s_w,
+                           const uint16_t* bias, int64_t M, int64_t N, int64_t K, uint16_t* y, void* ws, size_t ws_bytes,
+                           hipStream_t stream);
 size_t int8_bwd_workspace(int64_t M, int64_t N, int64_t K);
 hipError_t launch_int8_bwd(const uint16_t* dY, const int8_t* x_q, const float* s_x, const int8_t* w_q,
                            const float* s_w, int64_t M, int64_t N, int64_t K, uint16_t* dX, void* dW, bool dw_f32,

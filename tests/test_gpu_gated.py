@@ -289,6 +289,36 @@ def test_both_weights_and_the_rows_together(dtype, K):
                 assert (q == 7).all() and not s.any()
 
 
+@pytest.mark.parametrize("K", [8, 64, 100, 2048, 2555, 2560, 4096, 4100, 6912, 8192])
+@pytest.mark.parametrize("N", [1, 16, 75])
+def test_rows_taken_as_they_are(K, N):
+    """Few tokens of bf16 rows have the bits of their 8-bit rows, from any element
+    on, a NaN kept to its row."""
+    from ternary_weight_quantization_amd import binding as B
+    from ternary_weight_quantization_amd.layer import ternarize
+
+    note(f"gated rows as they are K={K} N={N}")
+    (pg, gg), (pu, gu) = (ternarize(w) for w in weights(N, K, K))
+    packed, gamma = torch.cat([pg, pu]), torch.cat([gg, gu])
+    Kp = packed.shape[1] * 4
+    for M in range(1, B.bitnet_rows_direct(K) + 1):
+        for off in (0, 1):
+            x = randn(M * K + 1, seed=M)[off:off + M * K].view(M, K)
+            x[M - 1, K // 3] = 0 if off else 77.0
+            x[0] *= 0.0 if M > 2 else 1.0
+            if M == 2:
+                x[1, K - 1] = float("nan")
+            q, s = torch.empty(M, Kp, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+            B.bitnet_rows_quant(x, q, s)
+            for act in (B.BITNET_ACT_SILU, B.BITNET_ACT_RELU2):
+                y, y2 = torch.empty(M, N, dtype=BF, device="cuda"), torch.zeros(M, N, dtype=BF, device="cuda")
+                sl, sl2 = (torch.zeros(B.bitnet_gated_slopes_bytes(M, N), dtype=torch.uint8, device="cuda") for _ in range(2))
+                B.bitnet_gated_fwd(act, q, s, packed, gamma, K, y, sl)
+                B.bitnet_gated_fwd(act, None, None, packed, gamma, K, y2, sl2, x=x)
+                assert torch.equal(y.view(torch.int16), y2.view(torch.int16)) and torch.equal(sl, sl2)
+                assert y2[1].isnan().all() if M == 2 else y2.isfinite().all()
+
+
 def test_shapes_and_empty_batches():
     from ternary_weight_quantization_amd.ffn import QATGatedBitLinear, gated_bitlinear
 

@@ -180,6 +180,35 @@ def test_weight_and_activations_quantized_together(dtype, K):
         assert torch.equal(q1, q) and torch.equal(s1, s)
 
 
+@pytest.mark.parametrize("K", [8, 64, 100, 2048, 2555, 2560, 4096, 4100, 6912, 8192])
+@pytest.mark.parametrize("N", [1, 16, 75])
+def test_rows_taken_as_they_are(K, N):
+    """Few tokens of bf16 rows have the bits of their 8-bit rows, from any element on, a
+    NaN kept to its row."""
+    from ternary_weight_quantization_amd import binding as B
+
+    note(f"int8 rows as they are K={K} N={N}")
+    Kp = -(-K // 64) * 64
+    new = lambda n: (torch.empty(n, Kp, dtype=torch.int8, device="cuda"), torch.empty(n, device="cuda"))  # noqa: E731
+    wq, sw = new(N)
+    B.bitnet_rows_quant(randn(N, K, seed=K), wq, sw)
+    b = randn(N, seed=K + 1)
+    for M in range(1, B.bitnet_rows_direct(K) + 1):
+        for off in (0, 1):
+            x = randn(M * K + 1, seed=M)[off:off + M * K].view(M, K)
+            x[M - 1, K // 3] = 0 if off else 77.0
+            x[0] *= 0.0 if M > 2 else 1.0
+            if M == 2:
+                x[1, K - 1] = float("nan")
+            q, s = new(M)
+            B.bitnet_rows_quant(x, q, s)
+            y, y2 = torch.empty(M, N, dtype=BF, device="cuda"), torch.zeros(M, N, dtype=BF, device="cuda")
+            B.bitnet_int8_fwd(q, s, wq, sw, K, y, bias=b)
+            B.bitnet_int8_fwd(None, None, wq, sw, K, y2, bias=b, x=x)
+            assert torch.equal(y.view(torch.int16), y2.view(torch.int16))
+            assert y2[1].isnan().all() if M == 2 else y2.isfinite().all()
+
+
 def test_gradients_one_at_a_time():
     from ternary_weight_quantization_amd.int8_layer import int8_linear
 

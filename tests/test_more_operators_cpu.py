@@ -92,8 +92,8 @@ def test_gated_refusals(L):
         assert f(0, N, K) == 0 and f(M, 0, K) == 0 and f(M, N, 0) == 0 and f(1 << 20, 1 << 12, K) == 0
         assert f(M, 1 << 30, K) == 0 and f(1 << 31, N, K) == 0
 
-    def fwd(act=0, q=P, s=P, w=P, g=P, M=M, N=N, K=K, y=P, sl=P, ws=P, n=nf):
-        return L.bitnet_gated_fwd(act, q, s, w, g, M, N, K, y, sl, ws, n, None)
+    def fwd(act=0, q=P, s=P, w=P, g=P, M=M, N=N, K=K, y=P, sl=P, ws=P, n=nf, x=None):
+        return L.bitnet_gated_fwd(act, x, q, s, w, g, M, N, K, y, sl, ws, n, None)
 
     assert fwd(q=None) == ENULL and fwd(s=None) == ENULL and fwd(w=None) == ENULL and fwd(g=None) == ENULL
     assert fwd(y=None) == ENULL and fwd(act=2) == EDTYPE and fwd(M=0) == ESHAPE and fwd(M=1 << 20, N=1 << 12) == ESHAPE
@@ -101,6 +101,11 @@ def test_gated_refusals(L):
     if nf:
         assert fwd(ws=None) == EWS and fwd(n=nf - 1) == EWS
     assert fwd(ws=None, n=nf + 1) == EWS
+    most = L.bitnet_rows_direct(K)
+    assert most >= 1 and L.bitnet_rows_direct(7) == 0 and L.bitnet_rows_direct(1 << 20) == 0
+    few = dict(q=None, s=None, n=0)
+    assert fwd(x=P, M=most + 1, **few) == ESHAPE and fwd(x=P, M=1, K=1 << 15, **few) == ESHAPE
+    assert fwd(x=P + 1, M=1, **few) == EALIGN and fwd(x=P, M=1, y=P + 2, **few) == EALIGN and fwd(x=P, M=0, **few) == ESHAPE
 
     def bwd(dY=P, sl=P, q=P, s=P, w=P, g=P, M=M, N=N, K=K, dX=P, a=P, b=P, d=BF, ws=P, n=nb):
         return L.bitnet_gated_bwd(dY, sl, q, s, w, g, M, N, K, dX, a, b, d, ws, n, None)
@@ -134,13 +139,16 @@ def test_int8_refusals(L):
     for f in (L.bitnet_int8_fwd_workspace_bytes, L.bitnet_int8_bwd_workspace_bytes):
         assert f(0, N, K) == 0 and f(M, 0, K) == 0 and f(M, N, 0) == 0 and f(M, N, 131073) == 0 and f(1 << 24, N, K) == 0
 
-    def fwd(q=P, s=P, w=P, sw=P, b=P, M=M, N=N, K=K, y=P, ws=P, n=nf):
-        return L.bitnet_int8_fwd(q, s, w, sw, b, M, N, K, y, ws, n, None)
+    def fwd(q=P, s=P, w=P, sw=P, b=P, M=M, N=N, K=K, y=P, ws=P, n=nf, x=None):
+        return L.bitnet_int8_fwd(x, q, s, w, sw, b, M, N, K, y, ws, n, None)
 
     assert fwd(q=None) == ENULL and fwd(s=None) == ENULL and fwd(w=None) == ENULL and fwd(sw=None) == ENULL
     assert fwd(y=None) == ENULL and fwd(K=131073) == ESHAPE and fwd(M=0) == ESHAPE and fwd(N=(1 << 24) + 1) == ESHAPE
     assert fwd(q=P + 8) == EALIGN and fwd(sw=P + 4) == EALIGN and fwd(b=P + 2) == EALIGN and fwd(y=P + 2) == EALIGN
     assert fwd(ws=None, n=nf + 1) == EWS
+    most = L.bitnet_rows_direct(K)
+    assert fwd(x=P, M=most + 1, q=None, s=None) == ESHAPE and fwd(x=P + 1, M=most, q=None, s=None) == EALIGN
+    assert fwd(x=P, M=0, q=None, s=None) == ESHAPE and fwd(x=P, M=1, w=None) == ENULL
 
     def bwd(dY=P, q=P, s=P, w=P, sw=P, M=M, N=N, K=K, dX=P, dW=P, d=BF, db=P, bd=BF, ws=P, n=nb):
         return L.bitnet_int8_bwd(dY, q, s, w, sw, M, N, K, dX, dW, d, db, bd, ws, n, None)
