@@ -26,6 +26,7 @@
 #pragma once
 
 #include "device_common.h"
+#include "bwd_prep.h"
 #include "gemm_core.h"
 #include "rows_quant.h"
 
@@ -42,6 +43,19 @@ struct FewArgs {
   const uint16_t* x;  // [M][K] (FewRows)
   int K;
 };
+
+// More than kFewM tokens are groups of kFewM. A workgroup's tile of weight rows and
+// first token; a becomes the group's. The groups of a tile are neighbours on one XCD, so
+// that the weights come to it once.
+constexpr int kFewM = 64;
+__device__ __forceinline__ void few_place(FewArgs& a, int& tile, int& m0) {
+  const int groups = (a.M + kFewM - 1) / kFewM;
+  const int v = groups > 1 ? xcd_major(blockIdx.x, gridDim.x) : (int)blockIdx.x;
+  tile = v / groups;
+  m0 = v % groups * kFewM;
+  a.xq += (int64_t)m0 * a.Kp;
+  a.M = a.M - m0 < kFewM ? a.M - m0 : kFewM;
+}
 
 template <bool CODES>
 struct FewStep {

@@ -32,6 +32,7 @@
 #include "bwd_prep.h"
 #include "few8.h"
 #include "gemm_split.h"
+#include "mid.h"
 #include "row_io.h"
 
 namespace bitnet {
@@ -56,55 +57,7 @@ struct GatedCodesLoader : RowCodesLoader<CodesI8Frags> {
   }
 };
 
-// LDS staging of 32 output rows x 64 columns of bf16 (EpStage's scheme): a lane
-// puts 4 values of row l % 32 at column 32fi + 8g + 4(l / 32), and every wave
-// store is 8 rows of 128 bytes.
-struct HalfStage {
-  static constexpr int kPitch = 128 + 16;
-  static constexpr int kBytes = 32 * kPitch;
-  static __device__ __forceinline__ void put(char* w, int lane, int fi, int g, uint2 v) {
-    *reinterpret_cast<uint2*>(w + (lane & 31) * kPitch + 8 * (lane >> 5) + (32 * fi + 8 * g) * 2) = v;
-  }
-  // Rows j0 .. j0 + 31 (those below J), columns i0 .. i0 + 63 (those below I) of
-  // out [J][ld]. i0, j0 are uniform in the wave; 32 * ld * 2 < 2^31.
-  static __device__ __forceinline__ void drain(const char* w, uint16_t* out, int64_t ld, int64_t I, int64_t J, int i0,
-                                               int j0, int lane) {
-    i0 = __builtin_amdgcn_readfirstlane(i0);
-    j0 = __builtin_amdgcn_readfirstlane(j0);
-    int c = lane & 7, rl = lane >> 3;
-    asm volatile("" : "+v"(c), "+v"(rl));  // as EpStage::drain
-    const char* src = w + rl * kPitch + 16 * c;
-    uint4 v[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const uint4*>(src + 8 * k * kPitch);
-    const int rows_in = J - j0 < 32 ? (int)(J - j0) : 32;
-    if (((ld | I) & 7) == 0) {
-      const uint32_t row_b = (uint32_t)ld * 2;
-      const rsrc_t rs = make_rsrc(out + (int64_t)j0 * ld + i0, 32u * row_b);
-      const uint32_t lane_off = i0 + 8 * c < I ? rl * row_b + 16 * c : kOob;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        buf_store16_stream(rs, rl < rows_in - 8 * k ? lane_off : kOob, (uint32_t)(8 * k) * row_b, v[k]);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (8 * k + rl >= rows_in) continue;
-        uint16_t* row = out + (int64_t)(j0 + 8 * k + rl) * ld + i0 + 8 * c;
-        const int64_t n = I - (i0 + 8 * c);  // values of this chunk inside the row
-        if (n >= 8) {
-          memcpy(row, &v[k], 16);
-        } else {
-          const uint32_t wv[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (e < n) row[e] = (uint16_t)(wv[e >> 1] >> (16 * (e & 1)));
-        }
-      }
-    }
-  }
-};
-
-// The same for the slopes' low bytes: 32 rows x 64 bytes, a lane's 4 values one
+// HalfStage for the slopes' low bytes: 32 rows x 64 bytes, a lane's 4 values one
 // dword, every wave store 16 rows of 64 bytes (ld, I multiples of 64).
 struct ByteStage {
   static constexpr int kPitch = 64 + 16;
@@ -231,7 +184,10 @@ __global__ __launch_bounds__(kWave * W) void gated_few_kernel(FewArgs a, const f
   __shared__ __attribute__((aligned(16))) char smem[few_lds<true, 2 * RP, MT, W, TX, false>()];
   __shared__ FewRows<NX, W> rows;
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  const int64_t n0 = (int64_t)blockIdx.x * (16 * RP);
+  const int64_t M = a.M;
+  int tile, m0;
+  few_place(a, tile, m0);
+  const int64_t n0 = (int64_t)tile * (16 * RP);
   int64_t row[2 * RP];
 #pragma unroll
   for (int p = 0; p < RP; ++p) {
@@ -242,8 +198,8 @@ __global__ __launch_bounds__(kWave * W) void gated_few_kernel(FewArgs a, const f
   few_tokens_product<true, 2 * RP, MT, W, P, TX, false>(a, row, smem, rows);
   for (int i = wave; i < RP * MT; i += W) {
     const int p = i % RP, mt = i / RP;
-    const int64_t m = 16 * mt + (lane & 15);
-    if (m >= a.M) continue;
+    const int64_t ml = 16 * mt + (lane & 15), m = m0 + ml;
+    if (ml >= a.M) continue;
     int vg[4], vu[4];
     few_tokens_sum<2 * RP, MT, W>(smem, 2 * p, mt, vg);
     few_tokens_sum<2 * RP, MT, W>(smem, 2 * p + 1, mt, vu);
@@ -258,11 +214,72 @@ __global__ __launch_bounds__(kWave * W) void gated_few_kernel(FewArgs a, const f
     store4(y + m * N, nb, N, o);
     if (slopes != nullptr && nb < Nd) {  // the padding's columns past the last workgroup's stay unwritten and are not read
       uint16_t* r = slopes + m * 2 * Nd + nb;
-      uint8_t* lo = reinterpret_cast<uint8_t*>(slopes + a.M * 2 * Nd) + m * 2 * Nd + nb;
+      uint8_t* lo = reinterpret_cast<uint8_t*>(slopes + M * 2 * Nd) + m * 2 * Nd + nb;
       *reinterpret_cast<uint2*>(r) = slopes_hi(dg);
       *reinterpret_cast<uint2*>(r + Nd) = slopes_hi(du);
       *reinterpret_cast<uint32_t*>(lo) = slopes_lo(dg);
       *reinterpret_cast<uint32_t*>(lo + Nd) = slopes_lo(du);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Middling M (mid.h): the 64 rows of a wave are 32 of the gate and the same 32 of the up
+// projection.
+// ---------------------------------------------------------------------------
+
+struct GatedRow {
+  int n0;
+  int64_t N;
+  __device__ __forceinline__ int64_t operator()(int r) const {
+    const int64_t n = n0 + 32 * (r >> 6) + (r & 31);
+    return n < N ? ((r & 32) ? N + n : n) : -1;
+  }
+};
+
+template <class ACT, int FJ, int P>
+__global__ __launch_bounds__(256) void gated_mid_kernel(const uint8_t* __restrict__ packed, const int8_t* __restrict__ xq,
+                                                        const float* __restrict__ s, const float* __restrict__ gamma,
+                                                        int64_t M, int64_t N, int64_t Nd, int64_t Kp, int tiles_j,
+                                                        uint16_t* __restrict__ y, uint16_t* __restrict__ slopes) {
+  typedef MidShape<2, FJ, 2, 2> S;
+  __shared__ __attribute__((aligned(16))) char lds[S::kLds];
+  const int v = xcd_major(blockIdx.x, gridDim.x), lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int n0 = v / tiles_j * (S::kI / 2), j0 = v % tiles_j * S::kJ;
+  const int nw = n0 + 32 * (wave % 2), jw = j0 + 32 * FJ * (wave / 2);
+  float sj[FJ];
+#pragma unroll
+  for (int fj = 0; fj < FJ; ++fj) {
+    const int64_t m = jw + 32 * fj + (lane & 31);
+    sj[fj] = m < M ? s[m] : 0.0f;
+  }
+  const float gg = gamma[0], gu = gamma[1];
+  const MidCodes<GatedRow> lp{packed, 2 * N, Kp / 4, {n0, N}};
+  const MidRows<TileRow> lq{xq, M, Kp, {j0, M}};
+  MfmaI8::Acc acc[2][FJ] = {};
+  mid_tile<MfmaI8, 2, FJ, 2, 2, P>(lp, lq, (int)((Kp + kStageBytes - 1) / kStageBytes), lds, acc);
+  const bool save = slopes != nullptr;
+#pragma unroll
+  for (int fj = 0; fj < FJ; ++fj) {
+    const int64_t m = jw + 32 * fj + (lane & 31);
+    if (m >= M) continue;
+    const float cg = sj[fj] * gg / 127.0f, cu = sj[fj] * gu / 127.0f;  // the large tiles' expressions
+#pragma unroll
+    for (int gi = 0; gi < 4; ++gi) {
+      const int64_t n = nw + 8 * gi + 4 * (lane >> 5);
+      float dg[4], du[4], o[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        gated_value<ACT, true>((float)acc[0][fj][4 * gi + e] * cg, (float)acc[1][fj][4 * gi + e] * cu, o[e], dg[e], du[e]);
+      store4(y + m * N, n, N, o);
+      if (save && n < Nd) {
+        uint16_t* r = slopes + m * 2 * Nd + n;
+        uint8_t* lo = reinterpret_cast<uint8_t*>(slopes + M * 2 * Nd) + m * 2 * Nd + n;
+        *reinterpret_cast<uint2*>(r) = slopes_hi(dg);
+        *reinterpret_cast<uint2*>(r + Nd) = slopes_hi(du);
+        *reinterpret_cast<uint32_t*>(lo) = slopes_lo(dg);
+        *reinterpret_cast<uint32_t*>(lo + Nd) = slopes_lo(du);
+      }
     }
   }
 }
@@ -417,8 +434,19 @@ static GemmShape fwd_shape(int64_t M, int64_t N, int64_t K) {
   return {(N + 127) / 128, (M + kBJ - 1) / kBJ, (k_pad(K) + kStageBytes - 1) / kStageBytes, kFwdPieceCost};
 }
 
+// The forward's kernel: kFew up to 64 tokens, and up to 256 while the workgroups of 32
+// outputs and 64 tokens fit the device at once (2560 -> 2 x 1728, 256 tokens: 9.4 us, 13.2
+// with mid.h's tiles; 2560 -> 2 x 6912, 128: 16.6 and 14.3).
+enum GatedForm { kFew, kMid1, kMid2, kTiles };
+static GatedForm gated_form(int64_t M, int64_t N) {
+  const int64_t groups = (M + kFewM - 1) / kFewM;
+  if (few(M) || (few(1) && M <= 4 * kFewM && (N + 31) / 32 * groups <= device_cus())) return kFew;
+  const int fj = mid_blocks(M, (N + 63) / 64);
+  return fj == 1 ? kMid1 : fj == 2 ? kMid2 : kTiles;
+}
+
 size_t gated_fwd_workspace(int64_t M, int64_t N, int64_t K) {
-  if (few(M)) return 0;
+  if (gated_form(M, N) != kTiles) return 0;
   const GemmShape g = fwd_shape(M, N, K);
   return split_workspace(g, split_grid(g, device_cus()));
 }
@@ -427,7 +455,17 @@ template <class ACT, int RP, int MT, int W, int P, bool TX, int NX = 0>
 static void gated_few(const FewArgs& a, const float* s, const float* gamma, int64_t N, int64_t Nd, uint16_t* y,
                       uint16_t* slopes, hipStream_t st) {
   gated_few_kernel<ACT, RP, MT, W, P, TX, NX>
-      <<<(unsigned)((N + 16 * RP - 1) / (16 * RP)), kWave * W, 0, st>>>(a, s, gamma, N, Nd, y, slopes);
+      <<<(unsigned)((N + 16 * RP - 1) / (16 * RP) * ((a.M + kFewM - 1) / kFewM)), kWave * W, 0, st>>>(a, s, gamma, N, Nd, y,
+                                                                                                   slopes);
+}
+
+template <class ACT, int FJ, int P>
+static hipError_t gated_mid(const uint8_t* w_packed, const int8_t* x_q, const float* s_x, const float* gamma, int64_t M,
+                            int64_t N, int64_t Kp, uint16_t* y, uint16_t* slopes, hipStream_t st) {
+  const int64_t tj = (M + 64 * FJ - 1) / (64 * FJ), ti = (N + 63) / 64;
+  gated_mid_kernel<ACT, FJ, P><<<(unsigned)(ti * tj), 256, 0, st>>>(w_packed, x_q, s_x, gamma, M, N, n_half(N), Kp,
+                                                                     (int)tj, y, slopes);
+  return hipGetLastError();
 }
 
 template <class ACT>
@@ -435,7 +473,8 @@ static hipError_t gated_fwd(const uint16_t* x, const int8_t* x_q, const float* s
                             const float* gamma, int64_t M, int64_t N, int64_t K, uint16_t* y, uint16_t* slopes, void* ws,
                             size_t ws_bytes, hipStream_t stream) {
   const int64_t Kp = k_pad(K), Nd = n_half(N);
-  if (few(M)) {
+  const GatedForm form = gated_form(M, N);
+  if (form == kFew) {
     const FewArgs a{w_packed, 2 * N, Kp / 4, x_q, Kp, (int)M, x, (int)K};
     // Up to 32 tokens 16 outputs a workgroup of 4 waves, or 8 where each would have more
     // than 3 steps (1 token, 6912 -> 2 x 2560: 6.0 us with 8, 7.1 with 4; 2560 -> 2 x 6912
@@ -460,6 +499,8 @@ static hipError_t gated_fwd(const uint16_t* x, const int8_t* x_q, const float* s
     else gated_few<ACT, 1, 1, 4, 3, false>(a, s_x, gamma, N, Nd, y, slopes, stream);
     return hipGetLastError();
   }
+  if (form == kMid1) return gated_mid<ACT, 1, 4>(w_packed, x_q, s_x, gamma, M, N, Kp, y, slopes, stream);
+  if (form == kMid2) return gated_mid<ACT, 2, 2>(w_packed, x_q, s_x, gamma, M, N, Kp, y, slopes, stream);
   GatedCodesLoader pl;
   pl.packed = w_packed;
   pl.pitch = Kp / 4;

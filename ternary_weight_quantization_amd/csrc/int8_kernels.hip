@@ -14,6 +14,7 @@
 #include "bwd_prep.h"
 #include "few8.h"
 #include "gemm_split.h"
+#include "mid.h"
 #include "row_io.h"
 
 namespace bitnet {
@@ -84,15 +85,17 @@ __global__ __launch_bounds__(kWave * W) void int8_few_kernel(FewArgs a, const fl
   __shared__ __attribute__((aligned(16))) char smem[few_lds<false, RT, MT, W, TX, true>()];
   __shared__ FewRows<NX, W> rows;
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  const int64_t n0 = (int64_t)blockIdx.x * (16 * RT), N = a.rows;
+  int tile, m0;
+  few_place(a, tile, m0);
+  const int64_t n0 = (int64_t)tile * (16 * RT), N = a.rows;
   int64_t row[RT];
 #pragma unroll
   for (int t = 0; t < RT; ++t) row[t] = n0;
   few_tokens_product<false, RT, MT, W, P, TX, true>(a, row, smem, rows);
   for (int i = wave; i < RT * MT; i += W) {
     const int t = i % RT, mt = i / RT;
-    const int64_t m = 16 * mt + (lane & 15);
-    if (m >= a.M) continue;
+    const int64_t ml = 16 * mt + (lane & 15), m = m0 + ml;
+    if (ml >= a.M) continue;
     int v[4];
     few_tokens_sum<RT, MT, W>(smem, t, mt, v);
     float sm;
@@ -112,17 +115,79 @@ __global__ __launch_bounds__(kWave * W) void int8_few_kernel(FewArgs a, const fl
 template <int RT, int MT, int W, int P, bool TX, int NX = 0>
 static void int8_few_at(const FewArgs& a, const float* s, const float* sw, const uint16_t* bias, uint16_t* y,
                         hipStream_t st) {
-  int8_few_kernel<RT, MT, W, P, TX, NX><<<(unsigned)((a.rows + 16 * RT - 1) / (16 * RT)), kWave * W, 0, st>>>(a, s, sw, bias, y);
+  const int64_t grid = (a.rows + 16 * RT - 1) / (16 * RT) * ((a.M + kFewM - 1) / kFewM);
+  int8_few_kernel<RT, MT, W, P, TX, NX><<<(unsigned)grid, kWave * W, 0, st>>>(a, s, sw, bias, y);
 }
 
-// Up to 16 tokens 16 rows a workgroup of 4 waves, at every N (16 tokens 2560 -> 32000: 15.5
-// us, with 32 rows 16.5). Above, x_q's traffic counts and more rows share it as long as
-// the workgroups fill the CUs: 32 tokens 2560 -> 32000 18.7 us with 64 rows, 24.6 with 16;
-// 6912 -> 2560 8.7 with 16, 11.0 with 32; 64 tokens 2560 -> 6912 8.9 with 32 rows and 8
-// waves, 10.4 with 16, 9.7 with 64.
+// Middling M (mid.h).
+template <int FJ, int P>
+__global__ __launch_bounds__(256) void int8_mid_kernel(const int8_t* __restrict__ wq, const int8_t* __restrict__ xq,
+                                                       const float* __restrict__ s, const float* __restrict__ sw,
+                                                       const uint16_t* __restrict__ bias, int64_t M, int64_t N,
+                                                       int64_t Kp, int tiles_j, uint16_t* __restrict__ y) {
+  typedef MidShape<2, FJ, 2, 2> S;
+  __shared__ __attribute__((aligned(16))) char lds[S::kLds];
+  const int v = xcd_major(blockIdx.x, gridDim.x), lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int i0 = v / tiles_j * S::kI, j0 = v % tiles_j * S::kJ;
+  if (threadIdx.x < S::kI) {
+    const int64_t n = i0 + threadIdx.x;
+    s_tile_sw[threadIdx.x] = n < N ? sw[n] / 127.0f : 0.0f;
+    s_tile_b[threadIdx.x] = bias != nullptr && n < N ? bf16_to_f32(bias[n]) : 0.0f;
+  }
+  const int jw = j0 + 32 * FJ * (wave / 2), iw = 64 * (wave % 2);
+  float sj[FJ];
+#pragma unroll
+  for (int fj = 0; fj < FJ; ++fj) {
+    const int64_t m = jw + 32 * fj + (lane & 31);
+    sj[fj] = m < M ? s[m] : 0.0f;
+  }
+  const MidRows<TileRow> lp{wq, N, Kp, {i0, N}}, lq{xq, M, Kp, {j0, M}};
+  MfmaI8::Acc acc[2][FJ] = {};
+  mid_tile<MfmaI8, 2, FJ, 2, 2, P>(lp, lq, (int)((Kp + kStageBytes - 1) / kStageBytes), lds, acc);
+  char* wlds = lds + wave * HalfStage::kBytes;
+#pragma unroll
+  for (int fj = 0; fj < FJ; ++fj) {
+    const float c = sj[fj] / 127.0f;  // the large tiles' expressions
+#pragma unroll
+    for (int fi = 0; fi < 2; ++fi)
+#pragma unroll
+      for (int gi = 0; gi < 4; ++gi) {
+        const int at = iw + 32 * fi + 8 * gi + 4 * (lane >> 5);
+        const float4 w = *reinterpret_cast<const float4*>(s_tile_sw + at);
+        const float4 b = *reinterpret_cast<const float4*>(s_tile_b + at);
+        const float v0 = fmaf((float)acc[fi][fj][4 * gi] * c, w.x, b.x);
+        const float v1 = fmaf((float)acc[fi][fj][4 * gi + 1] * c, w.y, b.y);
+        const float v2 = fmaf((float)acc[fi][fj][4 * gi + 2] * c, w.z, b.z);
+        const float v3 = fmaf((float)acc[fi][fj][4 * gi + 3] * c, w.w, b.w);
+        HalfStage::put(wlds, lane, fi, gi, make_uint2(pack_bf16x2(v0, v1), pack_bf16x2(v2, v3)));
+      }
+    HalfStage::drain(wlds, y, N, N, M, i0 + iw, jw + 32 * fj, lane);
+  }
+}
+
+static bool few(int64_t M) {
+  return M <= kSkinnyMaxM && test_knobs().no_skinny.load(std::memory_order_relaxed) == 0;
+}
+
+// Tiles of 16 rows a workgroup of the few-token kernel takes, 0: the kernel is not used.
+// Up to 16 tokens one at every N (16 tokens 2560 -> 32000: 15.5 us, with two 16.5). Above,
+// x_q's traffic counts and more rows share it as long as the workgroups fill the CUs: 32
+// tokens 2560 -> 32000 18.7 us with 64 rows, 24.6 with 16; 6912 -> 2560 8.7 with 16, 11.0
+// with 32; 64 tokens 2560 -> 6912 8.9 with 32, 10.4 with 16, 9.7 with 64. Up to 256 tokens in
+// groups of 64 while the workgroups fit the device at once (6912 -> 2560, 256 tokens: 17.9 us
+// with 64 rows, 25.5 with mid.h's tiles; 2560 -> 6912, 192: 18.2 and 12.6).
+static int few_tiles(int64_t M, int64_t N) {
+  if (!few(1) || M > 4 * kFewM) return 0;
+  if (M <= 16) return 1;
+  const int64_t groups = (M + kFewM - 1) / kFewM;
+  for (int rt = 1; rt <= 4; rt *= 2)
+    if ((N + 16 * rt - 1) / (16 * rt) * groups <= device_cus()) return rt;
+  return groups > 1 ? 0 : 4;
+}
+
 static void int8_few(const FewArgs& a, const float* s, const float* sw, const uint16_t* bias, uint16_t* y,
                      hipStream_t st) {
-  const int64_t tiles = (a.rows + 15) / 16;
+  const int rt = few_tiles(a.M, a.rows);
   if (a.x != nullptr) {  // M <= rows_direct(K)
     const bool deep = a.Kp > FewRows<1, 4>::kMaxK;
     if (a.M > 2 && deep) int8_few_at<1, 1, 8, 5, false, 4>(a, s, sw, bias, y, st);
@@ -133,20 +198,24 @@ static void int8_few(const FewArgs& a, const float* s, const float* sw, const ui
     else int8_few_at<1, 1, 4, 5, false, 1>(a, s, sw, bias, y, st);
   } else if (a.M <= 2) int8_few_at<1, 1, 4, 5, false>(a, s, sw, bias, y, st);
   else if (a.M <= 16) int8_few_at<1, 1, 4, 5, true>(a, s, sw, bias, y, st);
-  else if (a.M <= 32 && tiles <= 256) int8_few_at<1, 2, 4, 5, true>(a, s, sw, bias, y, st);
-  else if (a.M <= 32 && tiles <= 512) int8_few_at<2, 2, 4, 4, true>(a, s, sw, bias, y, st);
+  else if (a.M <= 32 && rt == 1) int8_few_at<1, 2, 4, 5, true>(a, s, sw, bias, y, st);
+  else if (a.M <= 32 && rt == 2) int8_few_at<2, 2, 4, 4, true>(a, s, sw, bias, y, st);
   else if (a.M <= 32) int8_few_at<4, 2, 4, 2, true>(a, s, sw, bias, y, st);
-  else if (tiles <= 256) int8_few_at<1, 4, 8, 3, true>(a, s, sw, bias, y, st);
-  else if (tiles <= 512) int8_few_at<2, 4, 8, 2, true>(a, s, sw, bias, y, st);
+  else if (rt == 1) int8_few_at<1, 4, 8, 3, true>(a, s, sw, bias, y, st);
+  else if (rt == 2) int8_few_at<2, 4, 8, 2, true>(a, s, sw, bias, y, st);
   else int8_few_at<4, 4, 8, 1, true>(a, s, sw, bias, y, st);
 }
 
-static bool few(int64_t M) {
-  return M <= kSkinnyMaxM && test_knobs().no_skinny.load(std::memory_order_relaxed) == 0;
+template <int FJ, int P>
+static hipError_t int8_mid(const int8_t* w_q, const int8_t* x_q, const float* s_x, const float* s_w,
+                           const uint16_t* bias, int64_t M, int64_t N, int64_t Kp, uint16_t* y, hipStream_t st) {
+  const int64_t tj = (M + 64 * FJ - 1) / (64 * FJ), ti = (N + 127) / 128;
+  int8_mid_kernel<FJ, P><<<(unsigned)(ti * tj), 256, 0, st>>>(w_q, x_q, s_x, s_w, bias, M, N, Kp, (int)tj, y);
+  return hipGetLastError();
 }
 
 size_t int8_fwd_workspace(int64_t M, int64_t N, int64_t K) {
-  if (few(M)) return 0;
+  if (few_tiles(M, N) || mid_blocks(M, (N + 127) / 128)) return 0;
   const GemmShape g = shape_of(GemmKind::kFwd, M, N, K);
   return split_workspace(g, split_grid(g, device_cus()));
 }
@@ -157,11 +226,14 @@ hipError_t launch_int8_fwd(const uint16_t* x, const int8_t* x_q, const float* s_
                            const uint16_t* bias, int64_t M, int64_t N, int64_t K, uint16_t* y, void* ws,
                            size_t ws_bytes, hipStream_t stream) {
   const int64_t Kp = k_pad(K);
-  if (few(M)) {
+  if (few_tiles(M, N)) {
     const FewArgs a{reinterpret_cast<const uint8_t*>(w_q), N, Kp, x_q, Kp, (int)M, x, (int)K};
     int8_few(a, s_x, s_w, bias, y, stream);
     return hipGetLastError();
   }
+  const int fj = mid_blocks(M, (N + 127) / 128);
+  if (fj == 1) return int8_mid<1, 4>(w_q, x_q, s_x, s_w, bias, M, N, Kp, y, stream);
+  if (fj == 2) return int8_mid<2, 2>(w_q, x_q, s_x, s_w, bias, M, N, Kp, y, stream);
   const CopyLoader<1, true, 1> pl{reinterpret_cast<const char*>(w_q), Kp, N, Kp};
   const CopyLoader<1, true, 5> ql{reinterpret_cast<const char*>(x_q), Kp, M, Kp};
   return run_gemm<MfmaI8, 1>(pl, ql, Int8Epilogue{y, s_x, s_w, bias, N, M}, shape_of(GemmKind::kFwd, M, N, K), ws,

@@ -147,14 +147,31 @@ def test_several_tiles():
     check(530, 333, 715, seed=11)
 
 
-@pytest.mark.parametrize("M,K,N", [(3, 130, 70), (40, 300, 129), (64, 64, 33)])
+@pytest.mark.parametrize("M,K,N", [(70, 130, 75), (300, 192, 140), (530, 333, 715)])
+def test_the_large_tiles(M, K, N):
+    """Sizes that take smaller tiles, on those of long batches."""
+    with knobs(no_skinny=1):
+        check(M, K, N, seed=M)
+
+
+@pytest.mark.parametrize("M,K,N", [(3, 130, 70), (40, 300, 129), (64, 64, 33), (65, 300, 129), (130, 2555, 77),
+                                   (256, 64, 33), (257, 130, 70), (333, 1000, 1001), (129, 700, 9000), (400, 320, 6000),
+                                   (1000, 65, 2050)])
 def test_few_tokens_have_the_bits_of_the_tiles(M, K, N):
     from ternary_weight_quantization_amd.ffn import gated_bitlinear
 
     x, (wg, wu) = randn(M, K, seed=1), weights(N, K, 2)
     few = gated_bitlinear(x, wg, wu)
+    a = x.clone().requires_grad_(True)
+    saved = gated_bitlinear(a, wg, wu)
+    dx, = torch.autograd.grad(saved, a, torch.ones_like(saved))
+    assert torch.equal(saved, few)
     with knobs(no_skinny=1):
         assert torch.equal(gated_bitlinear(x, wg, wu), few)
+        y = gated_bitlinear(a, wg, wu)
+    if M > 64:  # dX from the slopes that either kernel saved
+        dx2, = torch.autograd.grad(y, a, torch.ones_like(y))
+        assert torch.equal(dx, dx2)
 
 
 def test_split_tiles_have_the_bits_of_whole_ones():
