@@ -243,7 +243,9 @@ __global__ __launch_bounds__(256) void gated_mid_kernel(const uint8_t* __restric
                                                         int64_t M, int64_t N, int64_t Nd, int64_t Kp, int tiles_j,
                                                         uint16_t* __restrict__ y, uint16_t* __restrict__ slopes) {
   typedef MidShape<2, FJ, 2, 2> S;
-  __shared__ __attribute__((aligned(16))) char lds[S::kLds];
+  typedef MidCodes<GatedRow> LP;
+  typedef MidRows<TileRow> LQ;
+  __shared__ __attribute__((aligned(16))) char lds[S::template kLds<LP, LQ>];
   const int v = xcd_major(blockIdx.x, gridDim.x), lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int n0 = v / tiles_j * (S::kI / 2), j0 = v % tiles_j * S::kJ;
   const int nw = n0 + 32 * (wave % 2), jw = j0 + 32 * FJ * (wave / 2);
@@ -254,8 +256,8 @@ __global__ __launch_bounds__(256) void gated_mid_kernel(const uint8_t* __restric
     sj[fj] = m < M ? s[m] : 0.0f;
   }
   const float gg = gamma[0], gu = gamma[1];
-  const MidCodes<GatedRow> lp{packed, 2 * N, Kp / 4, {n0, N}};
-  const MidRows<TileRow> lq{xq, M, Kp, {j0, M}};
+  const LP lp{{}, packed, 2 * N, Kp / 4, {n0, N}};
+  const LQ lq{{}, xq, M, Kp, {j0, M}};
   MfmaI8::Acc acc[2][FJ] = {};
   mid_tile<MfmaI8, 2, FJ, 2, 2, P>(lp, lq, (int)((Kp + kStageBytes - 1) / kStageBytes), lds, acc);
   const bool save = slopes != nullptr;
@@ -422,6 +424,22 @@ struct HalvesEpilogue {
   }
 };
 
+// The same for mid.h's tiles.
+template <int EB>
+struct MidHalves {
+  static constexpr int kEB = EB;
+  void* out[2];
+  const float* gamma;
+  int64_t I, N, Nd;
+  __device__ __forceinline__ float scale(int64_t j) const { return 1.0f / gamma[j >= Nd ? 1 : 0]; }
+  __device__ __forceinline__ void* part(int& j, int64_t& rows) const {
+    const bool up = j >= Nd;  // of all 32 rows: Nd is a multiple of 64
+    if (up) j -= (int)Nd;
+    rows = N;
+    return up ? out[1] : out[0];
+  }
+};
+
 // ---------------------------------------------------------------------------
 // Launches
 // ---------------------------------------------------------------------------
@@ -540,13 +558,6 @@ size_t gated_bwd_workspace(int64_t M, int64_t N, int64_t K) {
   return w.d + w.wt + w.xhat + w.split;
 }
 
-// As gemm_kernels.hip's rule for its own pair: both products split on the whole
-// device under a 3-stage piece cost.
-static bool pair_pays(GemmShape dx, GemmShape dw) {
-  dx.overhead = dw.overhead = 3;
-  return split_pays(dx, device_cus()) > 0 && split_pays(dw, device_cus()) > 0;
-}
-
 template <bool OUT_F32>
 static hipError_t gated_products(const uint16_t* D, const uint8_t* wt, const uint16_t* xhat, const float* gamma,
                                  const float* s_x, int64_t M, int64_t N, int64_t K, uint16_t* dX, void* dWg, void* dWu, char* ws,
@@ -559,16 +570,26 @@ static hipError_t gated_products(const uint16_t* D, const uint8_t* wt, const uin
   const RowCopyBf16Loader<1> p2{xhat, Kp, M, Kp};
   const RowCopyBf16Loader<5> q2{D, J, M, J};
   const HalvesEpilogue<OUT_F32> e2{{dWg, dWu}, gamma, K, N, Nd};
-  if (dX != nullptr && dWg != nullptr && !few(M) && pair_pays(g1, g2)) {
+  const bool dx = dX != nullptr && !few(M), dw = dWg != nullptr;  // few tokens' dX has a kernel of its own
+  if (dX != nullptr && !dx)
+    if (hipError_t e = launch_dx_skinny(wt, D, nullptr, s_x, M, J, K, dX, stream)) return e;
+  if (!dx && !dw) return hipSuccess;
+  if (const int fj = mid_bwd_blocks(g1, g2, dx, dw, pair_pays(g1, g2), M, K, J)) {
+    const MidFp4<TileRow> lp1{{}, wt, Kp, J / 2, {0, Kp}};
+    const MidRows<TileRow> lq1{{}, D, M, 2 * J, {0, M}};
+    const MidOut<2> m1{dX, K, M, s_x};
+    const MidCols lp2{xhat, M, Kp, Kp, 0}, lq2{D, M, J, J, 0};
+    const MidHalves<OUT_F32 ? 4 : 2> m2{{dWg, dWu}, gamma, K, N, Nd};
+    return fj == 1 ? mid_products_at<1, 4>(lp1, lq1, m1, lp2, lq2, m2, dx, dw, M, K, J, J, stream)
+                   : mid_products_at<2, 2>(lp1, lq1, m1, lp2, lq2, m2, dx, dw, M, K, J, J, stream);
+  }
+  if (dx && dw && pair_pays(g1, g2)) {
     const hipError_t e = run_pair<1, 0>(p1, q1, e1, g1, kDxCosts, p2, q2, e2, g2, kDwCosts, ws, ws_bytes, stream);
     if (e != hipErrorNotSupported) return e;
   }
-  if (dX != nullptr) {
-    const hipError_t e = few(M) ? launch_dx_skinny(wt, D, nullptr, s_x, M, J, K, dX, stream)
-                                : run_gemm<MfmaBf16, 1>(p1, q1, e1, g1, ws, ws_bytes, stream);
-    if (e != hipSuccess) return e;
-  }
-  return dWg != nullptr ? run_gemm<MfmaBf16, 0>(p2, q2, e2, g2, ws, ws_bytes, stream) : hipSuccess;
+  if (dx)
+    if (hipError_t e = run_gemm<MfmaBf16, 1>(p1, q1, e1, g1, ws, ws_bytes, stream)) return e;
+  return dw ? run_gemm<MfmaBf16, 0>(p2, q2, e2, g2, ws, ws_bytes, stream) : hipSuccess;
 }
 
 hipError_t launch_gated_bwd(const uint16_t* dY, const uint16_t* slopes, const int8_t* x_q, const float* s_x,

@@ -126,7 +126,8 @@ __global__ __launch_bounds__(256) void int8_mid_kernel(const int8_t* __restrict_
                                                        const uint16_t* __restrict__ bias, int64_t M, int64_t N,
                                                        int64_t Kp, int tiles_j, uint16_t* __restrict__ y) {
   typedef MidShape<2, FJ, 2, 2> S;
-  __shared__ __attribute__((aligned(16))) char lds[S::kLds];
+  typedef MidRows<TileRow> LP, LQ;
+  __shared__ __attribute__((aligned(16))) char lds[S::template kLds<LP, LQ>];
   const int v = xcd_major(blockIdx.x, gridDim.x), lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int i0 = v / tiles_j * S::kI, j0 = v % tiles_j * S::kJ;
   if (threadIdx.x < S::kI) {
@@ -141,7 +142,7 @@ __global__ __launch_bounds__(256) void int8_mid_kernel(const int8_t* __restrict_
     const int64_t m = jw + 32 * fj + (lane & 31);
     sj[fj] = m < M ? s[m] : 0.0f;
   }
-  const MidRows<TileRow> lp{wq, N, Kp, {i0, N}}, lq{xq, M, Kp, {j0, M}};
+  const LP lp{{}, wq, N, Kp, {i0, N}}, lq{{}, xq, M, Kp, {j0, M}};
   MfmaI8::Acc acc[2][FJ] = {};
   mid_tile<MfmaI8, 2, FJ, 2, 2, P>(lp, lq, (int)((Kp + kStageBytes - 1) / kStageBytes), lds, acc);
   char* wlds = lds + wave * HalfStage::kBytes;
@@ -327,7 +328,19 @@ hipError_t launch_int8_bwd(const uint16_t* dY, const int8_t* x_q, const float* s
   if (db != nullptr)
     if (hipError_t e = launch_norm_cols(dy.sums, dy.groups, 1, N, db, nullptr, db_f32, stream)) return e;
   if (!products) return hipSuccess;
-  return launch_ttq_bwd(pad ? dy.padded : dY, ldy, xhat, Kp, what, nullptr, M, N, K, dX, dW, dw_f32, nullptr,
+  const uint16_t* y = pad ? dy.padded : dY;
+  const GemmShape g1 = shape_of(GemmKind::kBwdDx, M, N, K), g2 = shape_of(GemmKind::kBwdDw, M, N, K);
+  if (const int fj = mid_bwd_blocks(g1, g2, dX != nullptr, dW != nullptr, pair_pays(g1, g2), M, K, N)) {
+    const MidCols lp1{what, N, Kp, Kp, 0}, lp2{xhat, M, Kp, Kp, 0}, lq2{y, M, ldy, ldy, 0};
+    const MidRows<TileRow> lq1{{}, y, M, 2 * ldy, {0, M}};
+    const MidOut<2> e1{dX, K, M, nullptr};
+    const auto run = [&](auto e2) {
+      return fj == 1 ? mid_products_at<1, 4>(lp1, lq1, e1, lp2, lq2, e2, dX != nullptr, dW != nullptr, M, K, N, N, stream)
+                     : mid_products_at<2, 2>(lp1, lq1, e1, lp2, lq2, e2, dX != nullptr, dW != nullptr, M, K, N, N, stream);
+    };
+    return dw_f32 ? run(MidOut<4>{dW, K, N, nullptr}) : run(MidOut<2>{dW, K, N, nullptr});
+  }
+  return launch_ttq_bwd(y, ldy, xhat, Kp, what, nullptr, M, N, K, dX, dW, dw_f32, nullptr,
                         base + w.before(), ws_bytes - w.before(), stream);
 }
 
