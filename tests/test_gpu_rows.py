@@ -111,7 +111,7 @@ def test_several_layers_share_rows():
     assert torch.equal(both, want)
 
 
-@pytest.mark.parametrize("M", [5, 200])
+@pytest.mark.parametrize("M", [5, 200, 300])
 def test_a_block_in_a_graph(M):
     """A training step captured and replayed on other inputs has the bits of the
     eager step."""
@@ -229,6 +229,33 @@ def test_two_threads_at_once():
     assert not errors, errors
     for i in range(2):
         assert all(torch.equal(a, b) for a, b in zip(got[i], want[i]))
+
+
+@pytest.mark.parametrize("M", [3, 100])
+def test_one_tensor_in_two_places(M):
+    """The input as its own residual, one weight as gate and up, a matrix as input and
+    weight: the result of two equal tensors, the gradients their sum."""
+    from ternary_weight_quantization_amd import gated_bitlinear, int8_linear, rms_norm
+
+    note(f"one tensor in two places M={M}")
+    K = 72
+
+    def grads(f, shared, n, seed):
+        t = [randn(*shared, seed=seed).requires_grad_(True) for _ in range(n)]
+        y = f(*t)
+        y = y if isinstance(y, tuple) else (y,)
+        d = [randn(*v.shape, seed=seed + 1 + i).to(v.dtype) for i, v in enumerate(y)]
+        return list(y), torch.autograd.grad(y, t, d)
+
+    x = randn(M, K, seed=50)
+    cases = [(lambda a: rms_norm(a, None, a), lambda a, b: rms_norm(a, None, b), (M, K)),
+             (lambda a: gated_bitlinear(x, a, a), lambda a, b: gated_bitlinear(x, a, b), (40, K)),
+             (lambda a: int8_linear(a, a), lambda a, b: int8_linear(a, b), (M, K))]
+    for i, (one, two, shape) in enumerate(cases):
+        y1, (g,) = grads(one, shape, 1, 10 * i)
+        y2, (ga, gb) = grads(two, shape, 2, 10 * i)
+        assert all(torch.equal(a, b) for a, b in zip(y1, y2))
+        assert torch.equal(g, ga + gb)
 
 
 def test_offsets_past_2_to_the_31():
