@@ -25,6 +25,12 @@
 // 0.0037, and 0.0044 for relu2). Rows of D, of the slopes and of the transposed
 // codes are padded to Nd = N rounded up to 64 in each half, so that every width
 // runs the aligned loaders and no 32 rows of dW belong to both halves.
+//
+// Measured, 4096 x 2560 -> 2 x 6912: forward 195 us (290 G operations; the 227 MB of y and
+// slopes in its epilogue are 44 of it at a copy's rate), D and the operands 65 (400 MB, 6.1
+// TB/s, half of it left in the last-level cache), both products 445 (580 GFLOP, 1.30
+// PFLOP/s, what the largest library product reaches). Up to 256 tokens few8.h's kernels
+// and up to about 1000 mid.h's tiles run instead.
 
 #include <algorithm>
 
@@ -288,7 +294,8 @@ __global__ __launch_bounds__(256) void gated_mid_kernel(const uint8_t* __restric
 
 // ---------------------------------------------------------------------------
 // Backward, what the products read, in one launch: D, the codes of both weights
-// transposed to fp4 [Kp][2 Nd / 2] and the int8 rows as bf16 [M][Kp].
+// transposed to fp4 [Kp][2 Nd / 2] and the int8 rows as bf16 [M][Kp]. (D in a launch of
+// its own: 51.5 + 15.6 us for 64.8 at 4096 x 2560 -> 2 x 6912.)
 // ---------------------------------------------------------------------------
 
 // D [M][2 Nd] from dY [M][N] and the slopes, times the half's gamma and (sx not

@@ -4,10 +4,15 @@
 //   dX = dY w_hat,  dW = dY^T x_hat                  (straight through both quantizations)
 //
 // with x_hat = bf16(x_q sx/127), w_hat = bf16(w_q sw/127). The forward is the
-// scheme of gemm_kernels.hip with both operands int8 copied as stored; the
-// backward rebuilds both bf16 operands in one launch, which also takes dY's column
-// sums for the bias, and runs the bf16 products of the TTQ layer on them
-// (launch_ttq_bwd), which take any widths once dY's rows are a multiple of 8.
+// scheme of gemm_kernels.hip with both operands int8 copied as stored, or few8.h's or
+// mid.h's for fewer tokens; the backward rebuilds both bf16 operands in one launch,
+// which also takes dY's column sums for the bias, and runs on them the bf16 products of
+// the TTQ layer (launch_ttq_bwd), which take any widths once dY's rows are a multiple
+// of 8, or mid.h's.
+//
+// Measured, 4096 x 2560 -> 6912: forward 84 us (145 G operations, 1.73 P/s; a library
+// product of these sizes 83.9), operands 18, products 255 (290 GFLOP, 1.14 PFLOP/s).
+// 1000 x 2555 -> 2561: 19, 13 and 54.
 
 #include <algorithm>
 

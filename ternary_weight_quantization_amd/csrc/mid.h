@@ -1,8 +1,11 @@
 // Products for a middling number of tokens, out[j][i] = sum_k p[i][k] q[j][k]: too many
 // for the few-token kernels, too few for the 256 x 256 tiles of gemm_core.h to fill the
-// CUs. There a workgroup has a CU for itself and a tile's time is its chain of stages,
-// 1.3 us each; here tiles are 128 x 64 or 128 x 128, two workgroups share a CU, and the
-// loads of P stages are in flight from the first cycle on.
+// CUs. There a tile's time is its chain of stages, 1.2 to 1.6 us each whatever the other
+// CUs do; here tiles are 128 x 64 or 128 x 128 and take 0.4 to 0.8 us a stage, two
+// workgroups share a CU, and the loads of P stages are in flight from the first cycle on.
+// What bounds a stage is its LDS traffic (24 to 32 KB stored and 48 to 64 KB read for 8 or 16
+// instructions a wave) and the barrier: twice the stages in flight, or reading each step's
+// fragments while the one before is multiplied, changed nothing.
 //
 // A stage is 128 bytes of every row (128 int8 or 64 bf16). Loaded into registers P stages
 // ahead, it is stored to one of two LDS buffers, expanded there if it is codes, while the

@@ -10,7 +10,9 @@
 // largest |h w| is taken along with the sum of squares, before r is known: then
 // s = r max |h w|, q = round(h w (127 r / s)), one reduction and one pass over the
 // row's registers. Statistics are fp32, and no rounding to bf16 comes between h
-// and q.
+// and q. Bound by HBM once there are rows enough: 16384 x 6912 bf16 to 8-bit rows 67.6
+// us (340 MB, 5.0 TB/s), 4096 x 2560 with a residual 15.0 (73 MB, 4.9 TB/s), 1537 x 6905
+// bf16 onto an f32 stream 24.5 (127 MB, 5.2 TB/s); one row of 2560 is a launch's 4.5.
 
 #include <algorithm>
 

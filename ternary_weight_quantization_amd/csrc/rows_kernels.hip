@@ -82,7 +82,8 @@ hipError_t launch_rows_quant(const uint16_t* x, int64_t M, int8_t* x_q, float* s
 
 // ---------------------------------------------------------------------------
 // What 8-bit rows stand for: x[m,k] = fp32(q * fp32(s / 127)), rounded to bf16.
-// A thread takes 8 codes.
+// A thread takes 8 codes (16384 x 6912: 59 us, 340 MB at 5.8 TB/s, the codes partly from
+// the last-level cache).
 // ---------------------------------------------------------------------------
 
 __global__ __launch_bounds__(256) void rows_unpack_kernel(const int8_t* __restrict__ xq, const float* __restrict__ s,
