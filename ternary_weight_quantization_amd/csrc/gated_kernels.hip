@@ -459,19 +459,24 @@ static GemmShape fwd_shape(int64_t M, int64_t N, int64_t K) {
   return {(N + 127) / 128, (M + kBJ - 1) / kBJ, (k_pad(K) + kStageBytes - 1) / kStageBytes, kFwdPieceCost};
 }
 
-// The forward's kernel: kFew up to 64 tokens, and up to 256 while the workgroups of 32
+// The forward's kernel: kFew up to 32 tokens, and up to 256 while the workgroups of 32
 // outputs and 64 tokens fit the device at once (2560 -> 2 x 1728, 256 tokens: 9.4 us, 13.2
-// with mid.h's tiles; 2560 -> 2 x 6912, 128: 16.6 and 14.3).
+// with mid.h's tiles; 2560 -> 2 x 6912, 128: 16.6 and 14.3; 2560 -> 2 x 13824, 64: 16.8 and
+// 14.2). Up to 64 tokens a long reduction is better off in it too, whose waves share it
+// (6912 -> 2 x 9000, 64 tokens: 23.7 and 29.0).
 enum GatedForm { kFew, kMid1, kMid2, kTiles };
-static GatedForm gated_form(int64_t M, int64_t N) {
+static bool deep(int64_t K) { return k_pad(K) > 12 * FewStep<true>::kK; }
+static GatedForm gated_form(int64_t M, int64_t N, int64_t K) {
   const int64_t groups = (M + kFewM - 1) / kFewM;
-  if (few(M) || (few(1) && M <= 4 * kFewM && (N + 31) / 32 * groups <= device_cus())) return kFew;
+  if (few(1) && (M <= 32 || (M <= kFewM && deep(K)) ||
+                 (M <= 4 * kFewM && (N + 31) / 32 * groups <= device_cus())))
+    return kFew;
   const int fj = mid_blocks(M, (N + 63) / 64);
-  return fj == 1 ? kMid1 : fj == 2 ? kMid2 : kTiles;
+  return fj == 1 || (fj == 0 && few(M)) ? kMid1 : fj == 2 ? kMid2 : kTiles;
 }
 
 size_t gated_fwd_workspace(int64_t M, int64_t N, int64_t K) {
-  if (gated_form(M, N) != kTiles) return 0;
+  if (gated_form(M, N, K) != kTiles) return 0;
   const GemmShape g = fwd_shape(M, N, K);
   return split_workspace(g, split_grid(g, device_cus()));
 }
@@ -498,14 +503,14 @@ static hipError_t gated_fwd(const uint16_t* x, const int8_t* x_q, const float* s
                             const float* gamma, int64_t M, int64_t N, int64_t K, uint16_t* y, uint16_t* slopes, void* ws,
                             size_t ws_bytes, hipStream_t stream) {
   const int64_t Kp = k_pad(K), Nd = n_half(N);
-  const GatedForm form = gated_form(M, N);
+  const GatedForm form = gated_form(M, N, K);
   if (form == kFew) {
     const FewArgs a{w_packed, 2 * N, Kp / 4, x_q, Kp, (int)M, x, (int)K};
     // Up to 32 tokens 16 outputs a workgroup of 4 waves, or 8 where each would have more
     // than 3 steps (1 token, 6912 -> 2 x 2560: 6.0 us with 8, 7.1 with 4; 2560 -> 2 x 6912
     // 8.1 and 5.7). Above, x_q's traffic counts: 32 outputs share it (64 tokens, 2560 -> 2 x
     // 6912: 8.7 us against 15.3 with 16, 6912 -> 2 x 2560 12.4 against 13.5).
-    const bool deep = Kp > 12 * FewStep<true>::kK;
+    const bool deep = bitnet::deep(K);
     if (x != nullptr) {  // M <= rows_direct(K)
       if (M > 2 && deep) gated_few<ACT, 1, 1, 8, 3, false, 4>(a, s_x, gamma, N, Nd, y, slopes, stream);
       else if (M > 2) gated_few<ACT, 1, 1, 4, 3, false, 4>(a, s_x, gamma, N, Nd, y, slopes, stream);

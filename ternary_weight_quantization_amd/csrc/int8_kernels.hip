@@ -177,18 +177,27 @@ static bool few(int64_t M) {
 
 // Tiles of 16 rows a workgroup of the few-token kernel takes, 0: the kernel is not used.
 // Up to 16 tokens one at every N (16 tokens 2560 -> 32000: 15.5 us, with two 16.5). Above,
-// x_q's traffic counts and more rows share it as long as the workgroups fill the CUs: 32
-// tokens 2560 -> 32000 18.7 us with 64 rows, 24.6 with 16; 6912 -> 2560 8.7 with 16, 11.0
-// with 32; 64 tokens 2560 -> 6912 8.9 with 32, 10.4 with 16, 9.7 with 64. Up to 256 tokens in
-// groups of 64 while the workgroups fit the device at once (6912 -> 2560, 256 tokens: 17.9 us
-// with 64 rows, 25.5 with mid.h's tiles; 2560 -> 6912, 192: 18.2 and 12.6).
+// x_q's traffic counts and more rows share it as long as the workgroups fill the CUs (32
+// tokens 6912 -> 2560 8.7 us with 16, 11.0 with 32; 64 tokens 2560 -> 6912 8.9 with 32, 10.4
+// with 16, 9.7 with 64) and fit the device at once, up to 256 tokens in groups of 64;
+// mid.h's tiles take over there (6912 -> 2560, 256 tokens: 17.9 us here with 64 rows, 25.5
+// there; 2560 -> 6912, 192: 18.2 and 12.6; 2560 -> 32000, 64: 24.1 and 17.2, 32: 19.3 and
+// 17.3).
 static int few_tiles(int64_t M, int64_t N) {
   if (!few(1) || M > 4 * kFewM) return 0;
   if (M <= 16) return 1;
   const int64_t groups = (M + kFewM - 1) / kFewM;
   for (int rt = 1; rt <= 4; rt *= 2)
     if ((N + 16 * rt - 1) / (16 * rt) * groups <= device_cus()) return rt;
-  return groups > 1 ? 0 : 4;
+  return 0;
+}
+
+// The token blocks of mid.h's tiles where the few-token kernel is not used, 0: 256 x 256
+// tiles. Up to 64 tokens any number of 128 x 64 tiles, in rounds (64 tokens 2560 -> 128256:
+// 66 us for 63 of bytes, 106 in the few-token kernel).
+static int mid_form(int64_t M, int64_t N) {
+  const int fj = mid_blocks(M, (N + 127) / 128);
+  return fj == 0 && few(M) ? 1 : fj;
 }
 
 static void int8_few(const FewArgs& a, const float* s, const float* sw, const uint16_t* bias, uint16_t* y,
@@ -221,7 +230,7 @@ static hipError_t int8_mid(const int8_t* w_q, const int8_t* x_q, const float* s_
 }
 
 size_t int8_fwd_workspace(int64_t M, int64_t N, int64_t K) {
-  if (few_tiles(M, N) || mid_blocks(M, (N + 127) / 128)) return 0;
+  if (few_tiles(M, N) || mid_form(M, N)) return 0;
   const GemmShape g = shape_of(GemmKind::kFwd, M, N, K);
   return split_workspace(g, split_grid(g, device_cus()));
 }
@@ -237,7 +246,7 @@ hipError_t launch_int8_fwd(const uint16_t* x, const int8_t* x_q, const float* s_
     int8_few(a, s_x, s_w, bias, y, stream);
     return hipGetLastError();
   }
-  const int fj = mid_blocks(M, (N + 127) / 128);
+  const int fj = mid_form(M, N);
   if (fj == 1) return int8_mid<1, 4>(w_q, x_q, s_x, s_w, bias, M, N, Kp, y, stream);
   if (fj == 2) return int8_mid<2, 2>(w_q, x_q, s_x, s_w, bias, M, N, Kp, y, stream);
   const CopyLoader<1, true, 1> pl{reinterpret_cast<const char*>(w_q), Kp, N, Kp};

@@ -156,7 +156,7 @@ def test_the_large_tiles(M, K, N):
 
 @pytest.mark.parametrize("M,K,N", [(3, 130, 70), (40, 300, 129), (64, 64, 33), (65, 300, 129), (130, 2555, 77),
                                    (256, 64, 33), (257, 130, 70), (333, 1000, 1001), (129, 700, 9000), (400, 320, 6000),
-                                   (1000, 65, 2050)])
+                                   (1000, 65, 2050), (40, 130, 9001), (64, 64, 33000)])
 def test_few_tokens_have_the_bits_of_the_tiles(M, K, N):
     from ternary_weight_quantization_amd.ffn import gated_bitlinear
 

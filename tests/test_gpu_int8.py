@@ -118,7 +118,8 @@ def test_the_large_tiles(M, K, N):
 
 @pytest.mark.parametrize("M,K,N", [(3, 130, 70), (40, 300, 129), (64, 64, 33), (65, 300, 129), (130, 2555, 77),
                                    (192, 130, 4000), (256, 64, 10000), (256, 1000, 13), (257, 130, 70), (333, 1000, 1001),
-                                   (129, 700, 18000), (400, 320, 13000), (1000, 65, 4100)])
+                                   (129, 700, 18000), (400, 320, 13000), (1000, 65, 4100), (20, 64, 33000),
+                                   (40, 130, 17001), (64, 64, 70000)])
 def test_few_tokens_have_the_bits_of_the_tiles(M, K, N):
     from ternary_weight_quantization_amd.int8_layer import int8_linear
 
