@@ -9,7 +9,7 @@
 // over the rows of a block, LDS over its row groups, one partial row a block,
 // added in block order by a second launch (launch_norm_cols). No atomics: the
 // same inputs give the same bits. Measured with the second launch: 16384 x 6912 bf16
-// 152 us (680 MB, 4.5 TB/s), 1537 x 6905 f32 with dH 39 (149 MB, 3.8), 4096 x 2560 bf16
+// 152 us (680 MB, 4.5 TB/s), 1537 x 6905 f32 with dH 39 (170 MB, 4.3), 4096 x 2560 bf16
 // with dH 22.8 (84 MB, 3.7): the smaller ones end with the blocks' partial rows and the
 // second launch, 4 to 5 us of it.
 
