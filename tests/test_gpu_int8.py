@@ -109,6 +109,11 @@ def test_several_tiles():
     check(530, 333, 715, seed=11)
 
 
+@pytest.mark.parametrize("M,K,N", [(66, 131, 75), (300, 333, 141), (1100, 70, 65)])
+def test_float_masters_of_odd_widths(M, K, N):
+    check(M, K, N, dtype=F32, seed=M)
+
+
 @pytest.mark.parametrize("M,K,N", [(70, 130, 75), (300, 192, 140), (530, 333, 715)])
 def test_the_large_tiles(M, K, N):
     """Sizes that take smaller tiles, on those of long batches."""
