@@ -211,12 +211,12 @@ struct MidCols {
   }
 };
 
-// LDS staging of 32 output rows x 64 columns of EB bytes each (EpStage's scheme): a lane
+// LDS staging of 32 output rows x COLS columns of EB bytes each (EpStage's scheme): a lane
 // puts 4 values of row l % 32 at column 32fi + 8g + 4(l / 32), and every wave store is
-// whole rows of 64 values.
-template <int EB>
-struct Stage64 {
-  static constexpr int kRow = 64 * EB, kPitch = kRow + 16;
+// whole rows of COLS values.
+template <int EB, int COLS = 64>
+struct RowStage {
+  static constexpr int kRow = COLS * EB, kPitch = kRow + 16;
   static constexpr int kBytes = 32 * kPitch;
   static constexpr int kLanes = kRow / 16, kRows = kWave / kLanes, kPer = 16 / EB;  // of a row, of a store, values a lane
   template <class V>
@@ -224,8 +224,9 @@ struct Stage64 {
     static_assert(sizeof(V) == 4 * EB, "");
     *reinterpret_cast<V*>(w + (lane & 31) * kPitch + 4 * EB * (lane >> 5) + (32 * fi + 8 * g) * EB) = v;
   }
-  // Rows j0 .. j0 + 31 (those below J), columns i0 .. i0 + 63 (those below I) of
-  // out [J][ld]. i0, j0 are uniform in the wave; 32 * ld * EB < 2^31.
+  // Rows j0 .. j0 + 31 (those below J), columns i0 .. i0 + COLS - 1 (those below I) of
+  // out [J][ld]. i0, j0 are uniform in the wave; 32 * ld * EB < 2^31. EB 1: ld and I
+  // multiples of 16.
   static __device__ __forceinline__ void drain(const char* w, void* out, int64_t ld, int64_t I, int64_t J, int i0,
                                                int j0, int lane) {
     i0 = __builtin_amdgcn_readfirstlane(i0);
@@ -239,14 +240,14 @@ struct Stage64 {
     for (int k = 0; k < kStores; ++k) v[k] = *reinterpret_cast<const uint4*>(src + kRows * k * kPitch);
     const int rows_in = J - j0 < 32 ? (int)(J - j0) : 32;
     char* base = static_cast<char*>(out) + ((int64_t)j0 * ld + i0) * EB;
-    if (((ld | I) % kPer) == 0) {
+    if (EB == 1 || ((ld | I) % kPer) == 0) {
       const uint32_t row_b = (uint32_t)ld * EB;
       const rsrc_t rs = make_rsrc(base, 32u * row_b);
       const uint32_t lane_off = i0 + kPer * c < I ? rl * row_b + 16 * c : kOob;
 #pragma unroll
       for (int k = 0; k < kStores; ++k)
         buf_store16_stream(rs, rl < rows_in - kRows * k ? lane_off : kOob, (uint32_t)(kRows * k) * row_b, v[k]);
-    } else {
+    } else if constexpr (EB > 1) {
 #pragma unroll
       for (int k = 0; k < kStores; ++k) {
         if (kRows * k + rl >= rows_in) continue;
@@ -267,7 +268,7 @@ struct Stage64 {
     }
   }
 };
-using HalfStage = Stage64<2>;
+using HalfStage = RowStage<2>;
 
 template <int FI, int FJ, int WI, int WJ>
 struct MidShape {
@@ -339,7 +340,7 @@ struct MidProduct {
   typedef LQ_ LQ;
   typedef EP_ EP;
   typedef MidShape<2, FJ, 2, 2> S;
-  typedef Stage64<EP::kEB> Out;
+  typedef RowStage<EP::kEB> Out;
   static constexpr int kLds = S::template kLds<LP, LQ>;
   static_assert(4 * Out::kBytes <= kLds, "the epilogue's staging");
   LP lp;
