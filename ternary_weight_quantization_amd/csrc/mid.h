@@ -463,7 +463,7 @@ static int mid_bwd_blocks(const GemmShape& g1, const GemmShape& g2, bool dx, boo
     return base + 1.45 * (double)(g.tiles() * g.nstages) / device_cus();
   };
   const auto one_us = [&](const GemmShape& g) {
-    const double whole = (double)((g.tiles() + device_cus() - 1) / device_cus()) * (1.65 * g.nstages + 6);
+    const double whole = (double)((g.tiles() + device_cus() - 1) / device_cus()) * (1.65 * g.nstages + 8);
     return split_pays(g, device_cus()) ? std::min(whole, split_us(g, 95)) : whole;
   };
   const double there = dx && dw && both ? split_us(g1, 45) + split_us(g2, 0)
