@@ -598,8 +598,10 @@ bitnet_status bitnet_xent_bwd(const uint16_t* h, const uint16_t* w, const int64_
  *   r[m]   = (sum_k h[m,k]^2 / K + eps)^(-1/2),  v[m,k] = h[m,k] * r[m] * w[k]
  *   y[m,k] = round(v[m,k]),  or
  *   s[m]   = max(max_k |v[m,k]|, 1e-8f),
- *   x_q[m,k] = round_half_even(127 * v[m,k] / s[m]), the quotient in fp32 (off by a
- *              few 2^-24 of its value)
+ *   x_q[m,k] = round_half_even(127 * v[m,k] / s[m]), the quotient taken in fp32 as
+ *              h w (127 / max|h w|), the factor rounded up: off by less than 2^-22 of
+ *              its value, and right at the exact ties of values of up to 8 bits (half
+ *              of the row's largest; half integers where that is 127 * 2^j)
  *
  *   g[m,k]  = dY[m,k] * w[k],  hn[m,k] = h[m,k] * r[m]
  *   dh[m,k] = r[m] * (g[m,k] - hn[m,k] * sum_j g[m,j] hn[m,j] / K) + dH[m,k]

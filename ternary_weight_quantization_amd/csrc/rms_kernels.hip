@@ -8,7 +8,7 @@
 // in chunks of 8 values, as in the layer norm (norm_kernels.hip): every input
 // is read once, the stream and the rows are written once. For 8-bit rows the
 // largest |h w| is taken along with the sum of squares, before r is known: then
-// s = r max |h w|, q = round(h w (127 r / s)), one reduction and one pass over the
+// s = r max |h w|, q = round(h w (127 / max |h w|)), one reduction and one pass over the
 // row's registers. Statistics are fp32, and no rounding to bf16 comes between h
 // and q. Bound by HBM once there are rows enough: 16384 x 6912 bf16 to 8-bit rows 67.6
 // us (340 MB, 5.0 TB/s), 4096 x 2560 with a residual 15.0 (73 MB, 4.9 TB/s), 1537 x 6905
@@ -66,6 +66,12 @@ __device__ __forceinline__ uint2 codes8_scaled(const float (&f)[8], float k) {
     return perm(perm(d, c, 0x0C0C0400u), perm(b, a, 0x0C0C0400u), 0x05040100u);
   };
   return make_uint2(pack(t[0], t[1], t[2], t[3]), pack(t[4], t[5], t[6], t[7]));
+}
+
+// a / b in fp32, rounded up (a, b > 0).
+__device__ __forceinline__ float div_up(float a, float b) {
+  const float k = a / b;
+  return fmaf(k, b, -a) < 0.0f ? __uint_as_float(__float_as_uint(k) + 1u) : k;
 }
 
 // Sum of v and maximum of m over the TPR threads of a row, in every one of them.
@@ -189,8 +195,13 @@ __global__ __launch_bounds__(BLOCK, (rms_fwd_waves<rms_fwd_bytes<T, X, ADD>(), C
     if constexpr (QUANT) {
       // a row that holds an infinity or a NaN stands for NaN throughout
       const bool fine = sq < __uint_as_float(0x7F800000u) && mx < __uint_as_float(0x7F800000u) && !w_bad;
-      const float s = fine ? fmaxf(r * mx, 1e-8f) : __uint_as_float(0x7FC00000u);
-      const float k = 127.0f * r / s;
+      const float top = r * mx;
+      const float s = fine ? fmaxf(top, 1e-8f) : __uint_as_float(0x7FC00000u);
+      // 127 r / s without r where it cancels, rounded up: half of the largest |h w| then
+      // gives 63.5 or more, to 64 as half-even wants it, and where the largest is 127 2^j
+      // the factor and every tie are exact. (Each quotient decided exactly, as codes8
+      // does: 16384 x 6912 81 us, 64.6 so.)
+      const float k = top > 1e-8f ? div_up(127.0f, mx) : 127.0f * r / 1e-8f;
       if (ok) {
         if (t == 0) a.sx[row] = s;
 #pragma unroll
