@@ -611,7 +611,8 @@ bitnet_status bitnet_xent_bwd(const uint16_t* h, const uint16_t* w, const int64_
  * quantization). Statistics and sums are fp32, in a fixed order; squares are
  * summed in fp32, so magnitudes have to stay below about 1e19 / sqrt(K). Each
  * output is rounded once. NaN and infinities propagate within their row (and
- * into dw): a row of 8-bit codes that holds one has s = NaN. K <= 16384.
+ * into dw), and so does a root of no positive number (eps 0 over a row of zeros, eps
+ * below 0): a row of 8-bit codes that holds one has s = NaN. K <= 16384.
  *
  * x       [M][K] in x_dtype: with res BITNET_BF16 or the stream's type, without
  *         res the stream's type h_dtype.

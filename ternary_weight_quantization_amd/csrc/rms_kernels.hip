@@ -193,8 +193,10 @@ __global__ __launch_bounds__(BLOCK, (rms_fwd_waves<rms_fwd_bytes<T, X, ADD>(), C
     const float r = 1.0f / sqrtf(sq * inv_k + a.eps);
     if (ok && t == 0 && a.rstd) a.rstd[row] = r;
     if constexpr (QUANT) {
-      // a row that holds an infinity or a NaN stands for NaN throughout
-      const bool fine = sq < __uint_as_float(0x7F800000u) && mx < __uint_as_float(0x7F800000u) && !w_bad;
+      // a row that holds an infinity or a NaN, or whose r is one (no positive sum under
+      // the root), stands for NaN throughout
+      const float inf = __uint_as_float(0x7F800000u);
+      const bool fine = sq < inf && r < inf && mx < inf && !w_bad;
       const float top = r * mx;
       const float s = fine ? fmaxf(top, 1e-8f) : __uint_as_float(0x7FC00000u);
       // 127 r / s without r where it cancels, rounded up: half of the largest |h w| then

@@ -55,3 +55,22 @@ def test_codes_of_the_norm_at_ties(K, ht):
         assert torch.equal(rows.codes[:, :K].double(), want)
         both, s = rms_norm(torch.zeros_like(h), w, h.to(ht), quantize=True)
         assert torch.equal(both.codes, rows.codes) and torch.equal(both.scales, rows.scales) and torch.equal(s, h.to(ht))
+
+
+@pytest.mark.parametrize("w", [None, BF])
+@pytest.mark.parametrize("K", [3, 300, 5000])
+def test_rows_of_the_norm_with_no_root(K, w):
+    """eps below 0 or of 0 where the mean square and it have no positive sum: r is NaN
+    or infinite, the row NaN as it is in bf16, and the others stay."""
+    from ternary_weight_quantization_amd import rms_norm
+
+    note(f"rms without a root K={K}")
+    x = randn(9, K, seed=K)
+    w = None if w is None else randn(K, seed=1)
+    x[2], x[7] = 0, x[7] * 2.0 ** -12
+    for eps, bad in ((0.0, [2]), (-1e-4, [2, 7])):
+        rows, y = rms_norm(x, w, eps=eps, quantize=True), rms_norm(x, w, eps=eps)
+        keep = [i for i in range(9) if i not in bad]
+        assert y[bad].isnan().all() and rows.scales[bad].isnan().all() and rows.dequantize()[bad].isnan().all()
+        assert y[keep].isfinite().all() and rows.scales[keep].isfinite().all() and not rows.codes[:, K:].any()
+        assert torch.equal(rows.scales[keep], rms_norm(x[keep], w, eps=eps, quantize=True).scales)
