@@ -690,7 +690,7 @@ bitnet_status bitnet_rows_unpack(const int8_t* x_q, const float* s_x, int64_t M,
  * y, dY      [M][N] bf16 bits.
  * slopes     bitnet_gated_slopes_bytes(M, N) bytes: y's derivatives p = u act'(g) and
  *            a = act(g), written by the forward (NULL: not written) and read by the
- *            backward, the upper 24 bits of their fp32 values.
+ *            backward, their fp32 values rounded to 24 bits.
  * dX         [M][K] bf16 bits, or NULL.
  * dW_gate, dW_up [N][K] in dW_dtype (BITNET_BF16 or BITNET_F32), both or neither.
  * The backward without dW takes x_q NULL, and s_x NULL too (c is then 1); without dX

@@ -12,8 +12,8 @@
 // projection, so that a lane holds g and u of the same outputs in its
 // accumulators and the epilogue applies the activation there: neither
 // projection is written and read again. For the backward it stores y's slopes
-// dy/dg = u act'(g) and dy/du = act(g) next to y, as the upper 24 bits of their
-// fp32 values (cut off: at most 2^-16 of the value).
+// dy/dg = u act'(g) and dy/du = act(g) next to y, their fp32 values rounded to 24 bits
+// (half a step: 2^-16 of the value; cut off they would be twice as far, and all short).
 //
 // Backward: one pass makes D = [gamma_g dg | gamma_u du] s/127 in bf16, then the
 // two products of gemm_kernels.hip on D, the codes of both weights below each
@@ -63,15 +63,21 @@ struct GatedCodesLoader : RowCodesLoader<CodesI8Frags> {
   }
 };
 
-// A slope is kept as the upper 16 bits of its fp32 value and the 8 bits below
-// them, in two planes: [M][2 Nd] of 16 bits, then [M][2 Nd] bytes.
+// A slope, rounded to the nearest multiple of 2^8 in its bits, is kept as the upper 16
+// and the 8 below them, in two planes: [M][2 Nd] of 16 bits, then [M][2 Nd] bytes. The
+// carry takes no NaN away: all that reach here stem from g's and u's factors
+// (quiet_nan) or from the operations, whose own has no low bits.
+__device__ __forceinline__ uint32_t slope24(float v) { return __float_as_uint(v) + 0x80u; }
 __device__ __forceinline__ uint2 slopes_hi(const float (&v)[4]) {
-  return make_uint2(perm(__float_as_uint(v[1]), __float_as_uint(v[0]), 0x07060302u),
-                    perm(__float_as_uint(v[3]), __float_as_uint(v[2]), 0x07060302u));
+  return make_uint2(perm(slope24(v[1]), slope24(v[0]), 0x07060302u), perm(slope24(v[3]), slope24(v[2]), 0x07060302u));
 }
 __device__ __forceinline__ uint32_t slopes_lo(const float (&v)[4]) {
-  return perm(perm(__float_as_uint(v[3]), __float_as_uint(v[2]), 0x0C0C0501u),
-              perm(__float_as_uint(v[1]), __float_as_uint(v[0]), 0x0C0C0501u), 0x05040100u);
+  return perm(perm(slope24(v[3]), slope24(v[2]), 0x0C0C0501u), perm(slope24(v[1]), slope24(v[0]), 0x0C0C0501u),
+              0x05040100u);
+}
+__device__ __forceinline__ float quiet_nan(float c) {
+  const uint32_t b = __float_as_uint(c);
+  return __uint_as_float((b & 0x7FFFFFFFu) > 0x7F800000u ? 0x7FC00000u : b);
 }
 __device__ __forceinline__ void slopes8(uint4 hi, uint2 lo, float (&f)[8]) {
   const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[2] = {lo.x, lo.y};
@@ -123,7 +129,7 @@ struct GatedEpilogue {
     const int n0 = i0 / 2;
 #pragma unroll
     for (int fj = 0; fj < kFJ; ++fj) {
-      const float cg = pre.sj[fj] * pre.gg / 127.0f, cu = pre.sj[fj] * pre.gu / 127.0f;
+      const float cg = quiet_nan(pre.sj[fj] * pre.gg / 127.0f), cu = quiet_nan(pre.sj[fj] * pre.gu / 127.0f);
 #pragma unroll
       for (int fi = 0; fi < 2; ++fi)
 #pragma unroll
@@ -188,7 +194,8 @@ __global__ __launch_bounds__(kWave * W) void gated_few_kernel(FewArgs a, const f
     float sm;
     if constexpr (NX > 0) sm = rows.s[m];
     else sm = s[m];
-    const float cg = sm * gamma[0] / 127.0f, cu = sm * gamma[1] / 127.0f;  // the large-M epilogue's expressions
+    // the large-M epilogue's expressions
+    const float cg = quiet_nan(sm * gamma[0] / 127.0f), cu = quiet_nan(sm * gamma[1] / 127.0f);
     const int64_t nb = n0 + 16 * p + 4 * (lane >> 4);
     float dg[4], du[4], o[4];
 #pragma unroll
@@ -254,7 +261,8 @@ __global__ __launch_bounds__(256) void gated_mid_kernel(const uint8_t* __restric
   uint8_t* lo = save ? reinterpret_cast<uint8_t*>(slopes + M * 2 * Nd) : nullptr;
 #pragma unroll
   for (int fj = 0; fj < FJ; ++fj) {
-    const float cg = sj[fj] * gg / 127.0f, cu = sj[fj] * gu / 127.0f;  // the large tiles' expressions
+    // the large tiles' expressions
+    const float cg = quiet_nan(sj[fj] * gg / 127.0f), cu = quiet_nan(sj[fj] * gu / 127.0f);
 #pragma unroll
     for (int gi = 0; gi < 4; ++gi) {
       float dg[4], du[4], o[4];

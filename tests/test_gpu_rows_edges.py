@@ -4,7 +4,7 @@ sizes end."""
 import pytest
 import torch
 
-from tests.gpu_util import note
+from tests.gpu_util import knobs, note
 
 pytestmark = pytest.mark.gpu
 
@@ -74,3 +74,82 @@ def test_rows_of_the_norm_with_no_root(K, w):
         assert y[bad].isnan().all() and rows.scales[bad].isnan().all() and rows.dequantize()[bad].isnan().all()
         assert y[keep].isfinite().all() and rows.scales[keep].isfinite().all() and not rows.codes[:, K:].any()
         assert torch.equal(rows.scales[keep], rms_norm(x[keep], w, eps=eps, quantize=True).scales)
+
+
+# --- the pair's slopes -------------------------------------------------------
+
+# Tokens and launch knobs of each form of the forward: few tokens, a middling number on
+# the smaller and the larger of its tiles, the tiles of long batches, whole and split.
+FORMS = [(1, {}), (5, {}), (40, {}), (90, {}), (700, {}), (90, dict(no_skinny=1)),
+         (300, dict(no_skinny=1, split_ctas=3)), (300, dict(no_skinny=1, split_ctas=-1))]
+
+
+def slopes_of(buf, M, N):
+    """p and a [M, N] float32 of the bytes that the forward stores."""
+    Nd = -(-N // 64) * 64
+    n = 2 * M * 2 * Nd
+    hi = buf[:n].view(torch.int16).view(M, 2, Nd)[:, :, :N].int() & 0xFFFF
+    lo = buf[n:].view(M, 2, Nd)[:, :, :N].int()
+    v = ((hi << 16) | (lo << 8)).view(torch.float32)
+    return v[:, 0], v[:, 1]
+
+
+def pair(M, K, N, seed):
+    """8-bit rows and codes as the C entry points take them."""
+    from ternary_weight_quantization_amd.layer import act_quant, ternarize
+
+    x, packed = randn(M, K, seed=seed), []
+    for i in (1, 2):
+        packed.append(ternarize(randn(N, K, seed=seed + i) / K ** 0.5))
+    q, s = act_quant(x)
+    return x, q, s, torch.cat([p for p, _ in packed]), torch.cat([g for _, g in packed])
+
+
+@pytest.mark.parametrize("M,kw", FORMS)
+def test_slopes_are_rounded_to_24_bits(M, kw):
+    """a = g^2 and p = 2 g u have the same fp32 operations here, on the CPU: what is kept
+    of them is off by at most half a step of 16 bits, 2^-16 of the value, and not to one
+    side. NaN with any payload stays NaN, infinity itself."""
+    from ternary_weight_quantization_amd import binding as B
+
+    K, N = 200, 75
+    note(f"slopes M={M} {kw}")
+    x, q, s, packed, gamma = pair(M, K, N, M)
+
+    def forward(s, gamma):
+        y = torch.empty(M, N, dtype=BF, device="cuda")
+        sl = torch.zeros(B.bitnet_gated_slopes_bytes(M, N), dtype=torch.uint8, device="cuda")
+        B.bitnet_gated_fwd(B.BITNET_ACT_RELU2, q, s, packed, gamma, K, y, sl)
+        return y, slopes_of(sl, M, N)
+
+    with knobs(**kw):
+        y, (p, a) = forward(s, gamma)
+        t = packed.view(2 * N, -1, 1, 4).int() >> (2 * torch.arange(4, device="cuda"))[:, None]  # [word][j // 4][j % 4]
+        t = (t & 3).reshape(2 * N, -1)
+        acc = (q.double() @ torch.where(t == 3, -1, t).double().t()).float().cpu()
+        c = [(s.cpu() * v / torch.full((M,), 127.0))[:, None] for v in gamma.cpu()]
+        g, u = (acc[:, :N] * c[0]).clamp(min=0), acc[:, N:] * c[1]
+        off = []
+        for got, want in ((a, g * g), (p, 2 * g * u)):
+            got, want = got.cpu().double(), want.double()
+            assert ((got - want).abs() <= 2.0 ** -16 * want.abs()).all()
+            off.append(((got - want) / want)[want != 0])
+        off = torch.cat(off)
+        # the mean of n errors of at most h = 2^-16, evenly spread: h / sqrt(3 n)
+        assert off.mean().abs().item() <= 6 * 2.0 ** -16 / (3 * off.numel()) ** 0.5
+        bits = torch.tensor([0x7FFFFFFF, 0x7FFFFF80, 0x7F800001, -1, -128, 0x7FC00000], dtype=torch.int32, device="cuda")
+        for b in bits:
+            nan = s.clone().view(torch.int32)
+            nan[M // 2] = b
+            y, (p, a) = forward(nan.view(torch.float32), gamma)
+            assert y[M // 2].isnan().all() and p[M // 2].isnan().all() and a[M // 2].isnan().all()
+            assert y.isnan().sum() == N and a.isnan().sum() == N
+            gn = gamma.clone().view(torch.int32)
+            gn[1] = b
+            y, (p, a) = forward(s, gn.view(torch.float32))
+            assert y.isnan().all() and p.isnan().all() and not a.isnan().any()
+        big = s.clone()
+        big[M // 2] = 3e38
+        y, (p, a) = forward(big, gamma)
+        pos = g[M // 2] > 0
+        assert (a[M // 2][pos] == float("inf")).all() and (a[M // 2][~pos] == 0).all()
