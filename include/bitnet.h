@@ -761,8 +761,9 @@ bitnet_status bitnet_int8_bwd(const uint16_t* dY, const int8_t* x_q, const float
  *   spin_limit  polls (each a short sleep) before a workgroup waiting for
  *               another's partial tile gives up; the default,
  *               bitnet_default_spin_limit(), is about a second. A wait
- *               that gives up writes its output tile as NaN (int32
- *               accumulators: INT32_MIN) and is counted.
+ *               that gives up writes its output tile as NaN (outputs of
+ *               int32 accumulators, but the gated pair's: as of INT32_MIN)
+ *               and is counted.
  *               The one-pass weight quantization waits at most the same
  *               number of polls, and at most 200 us, for the other
  *               workgroups' partial sums; when it gives up, a workgroup

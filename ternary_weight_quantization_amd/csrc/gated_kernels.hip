@@ -127,9 +127,13 @@ struct GatedEpilogue {
   __device__ __forceinline__ void store(MfmaI8::Acc (&acc)[kFI][kFJ], const Pre& pre, int i0, int j0, int lane,
                                         char* wlds) const {
     const int n0 = i0 / 2;
+    // The tile of a wait that gave up, whose accumulators are INT32_MIN throughout (no sum
+    // of codes is): y would be 0 there, act's value far below 0, so the factors are NaN.
+    const bool lost = (uint32_t)acc[0][0][0] == MfmaI8::kPoisonBits;
 #pragma unroll
     for (int fj = 0; fj < kFJ; ++fj) {
-      const float cg = quiet_nan(pre.sj[fj] * pre.gg / 127.0f), cu = quiet_nan(pre.sj[fj] * pre.gu / 127.0f);
+      const float sj = lost ? __uint_as_float(0x7FC00000u) : pre.sj[fj];
+      const float cg = quiet_nan(sj * pre.gg / 127.0f), cu = quiet_nan(sj * pre.gu / 127.0f);
 #pragma unroll
       for (int fi = 0; fi < 2; ++fi)
 #pragma unroll

@@ -153,3 +153,45 @@ def test_slopes_are_rounded_to_24_bits(M, kw):
         y, (p, a) = forward(big, gamma)
         pos = g[M // 2] > 0
         assert (a[M // 2][pos] == float("inf")).all() and (a[M // 2][~pos] == 0).all()
+
+
+# --- waits that give up ------------------------------------------------------
+
+@pytest.mark.parametrize("act", ["silu", "relu2"])
+def test_a_split_gated_forward_that_gives_up_is_visible(act):
+    """A wait for another workgroup's partial tile that gives up (forced with a zero
+    spin limit: every kernel ends) leaves its tile of y and of the slopes NaN as a
+    whole and is counted; the other tiles are exact."""
+    from ternary_weight_quantization_amd import binding as B
+    from ternary_weight_quantization_amd.checkpoint import ACTIVATIONS
+
+    M, K, N = 768, 2560, 384
+    note(f"gated split gives up {act}")
+    x, q, s, packed, gamma = pair(M, K, N, 5)
+
+    def forward():
+        y = torch.empty(M, N, dtype=BF, device="cuda")
+        sl = torch.zeros(B.bitnet_gated_slopes_bytes(M, N), dtype=torch.uint8, device="cuda")
+        B.bitnet_gated_fwd(ACTIVATIONS[act], q, s, packed, gamma, K, y, sl)
+        return (y, *slopes_of(sl, M, N))
+
+    B.bitnet_split_timeouts()
+    with knobs(split_ctas=64):
+        ref = forward()
+    assert B.bitnet_split_timeouts() == 0
+    with knobs(split_ctas=64, spin_limit=0):
+        got = forward()
+    count, bad = B.bitnet_split_timeouts(), 0
+    for m in range(0, M, 256):
+        for n in range(0, N, 128):  # 256 rows of codes are 128 of the gate and 128 of the up projection
+            tile = [t[m:m + 256, n:n + 128] for t in got]
+            want = [t[m:m + 256, n:n + 128] for t in ref]
+            if all(torch.equal(a, b) for a, b in zip(tile, want)):
+                continue
+            bad += 1
+            assert all(a.isnan().all() for a in tile), (m, n)
+    note(f"  counted {count}, {bad} tiles")
+    assert count == bad
+    assert B.bitnet_split_timeouts() == 0
+    with knobs(split_ctas=64):
+        assert all(torch.equal(a, b) for a, b in zip(forward(), ref))
