@@ -179,8 +179,8 @@ bitnet_status bitnet_quantize_static(const void* W, bitnet_dtype w_dtype, int64_
  * and below them those of W1, gamma[0] and gamma[1], each bit for bit what
  * that call alone gives. x may be NULL (M, x_q and s_x are not used then);
  * otherwise its M rows become x_q and s_x as bitnet_rows_quant makes them, in
- * the weights' launch. Errors as those calls'; workspace as
- * bitnet_ternarize_pack's.
+ * the weights' launch. Errors and limits as those calls' (with x M <= 2^23 and
+ * K <= 2^24); workspace as bitnet_ternarize_pack's.
  */
 bitnet_status bitnet_quantize2(const void* W0, const void* W1, bitnet_dtype w_dtype, int64_t N, int64_t K,
                                const uint16_t* x, int64_t M, uint8_t* w_packed, float* gamma,

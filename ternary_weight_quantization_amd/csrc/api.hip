@@ -90,6 +90,11 @@ bitnet_status check_rms_sizes(int64_t M, int64_t K) {
   return K > bitnet::kRmsMaxK ? BITNET_ERR_SHAPE : BITNET_OK;
 }
 
+// Rows to be quantized: up to a workgroup of 256 threads each, fewer than 2^32 in all.
+bitnet_status check_rows_sizes(int64_t M, int64_t K) {
+  return M < 1 || M > (int64_t(1) << 23) || K < 1 || K > (int64_t(1) << 24) ? BITNET_ERR_SHAPE : BITNET_OK;
+}
+
 // The products over a weight of 2 Nd rows, in both directions.
 bitnet_status check_gated_sizes(int64_t M, int64_t N, int64_t K) {
   if (M < 1 || N < 1 || K < 1 || N > kMaxDim / 4) return BITNET_ERR_SHAPE;
@@ -199,7 +204,7 @@ bitnet_status bitnet_quantize2(const void* W0, const void* W1, bitnet_dtype w_dt
   if (w_dtype != BITNET_BF16 && w_dtype != BITNET_F32) return BITNET_ERR_DTYPE;
   if (bitnet_status st = check_sizes(N, K)) return st;
   if (x)
-    if (bitnet_status st = check_sizes(M, K)) return st;
+    if (bitnet_status st = check_rows_sizes(M, K)) return st;
   if (N * K > (int64_t(1) << 53)) return BITNET_ERR_SHAPE;
   if (!aligned(W0, 16) || !aligned(W1, 16) || !aligned(w_packed, 16) || !aligned(gamma, 4)) return BITNET_ERR_ALIGN;
   if (x && (!aligned(x, 16) || !aligned(x_q, 16) || !aligned(s_x, 16))) return BITNET_ERR_ALIGN;

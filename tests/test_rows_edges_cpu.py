@@ -1,0 +1,30 @@
+"""Refusals around 8-bit rows without a GPU, each before the device is touched."""
+
+import os
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+LIB = os.path.join(ROOT, "ternary_weight_quantization_amd", "libbitnet.so")
+OK, ENULL, ESHAPE, EDTYPE, EALIGN, EWS, EHIP = range(7)
+P = 1 << 20  # a stand-in device address, aligned; never dereferenced
+BF, F32 = 0, 1
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(LIB):
+        pytest.fail("libbitnet.so is not built (run `python -m ternary_weight_quantization_amd.build`)")
+    from ternary_weight_quantization_amd import binding
+    return binding.lib()
+
+
+def test_rows_that_two_weights_share_have_the_limits_of_rows(L):
+    def f(x=P, N=200, M=4, K=130, ws=P):
+        return L.bitnet_quantize2(P, P, BF, N, K, x, M, P, P, P, P, ws, 1 << 40, None)
+
+    assert f(M=(1 << 23) + 1) == ESHAPE and f(M=1 << 27) == ESHAPE and f(M=1 << 30) == ESHAPE
+    assert f(K=(1 << 24) + 1) == ESHAPE
+    # at the limits the call goes on to its other checks, and without rows it has none of theirs
+    assert f(M=1 << 23, ws=None) == EWS and f(K=1 << 24, ws=None) == EWS
+    assert f(x=None, M=1 << 27, ws=None) == EWS and f(x=None, K=(1 << 24) + 1, ws=None) == EWS
