@@ -652,7 +652,7 @@ bitnet_status bitnet_rmsnorm_bwd(const void* dY, bitnet_dtype y_dtype, const voi
  *             s_x [M], both 16-byte aligned. A row that holds an infinity or a NaN has
  *             s_x = NaN.
  * rows_quant2: the rows of bf16 x [M][K] and of w [N][K] in w_dtype (a layer's activations
- *             and channels) in one launch; M or N may be 0.
+ *             and channels) in one launch; M or N may be 0, M + N < 2^24.
  * rows_unpack: x [M][K] bf16 bits, 2-byte aligned. M * Kp <= 2^34.
  * rows_direct: how many tokens of K values the forwards of the layers below take as
  *             they are, each workgroup making the codes for itself (0: none).

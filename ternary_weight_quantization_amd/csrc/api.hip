@@ -2,6 +2,8 @@
 // validation, then the launches on the caller's stream. Nothing here
 // allocates device memory or synchronizes the host.
 
+#include <algorithm>
+
 #include <hip/hip_runtime.h>
 
 #include "../../include/bitnet.h"
@@ -603,8 +605,8 @@ bitnet_status bitnet_rows_quant(const void* x, bitnet_dtype x_dtype, int64_t M, 
 
 bitnet_status bitnet_rows_quant2(const uint16_t* x, int64_t M, int8_t* x_q, float* s_x, const void* w,
                                  bitnet_dtype w_dtype, int64_t N, int8_t* w_q, float* s_w, int64_t K, void* stream) {
-  if (M < 0 || N < 0 || M + N < 1 || M > (int64_t(1) << 23) || N > (int64_t(1) << 23) || K < 1 || K > (int64_t(1) << 24))
-    return BITNET_ERR_SHAPE;
+  if (M < 0 || N < 0 || M + N < 1 || M + N >= (int64_t(1) << 24)) return BITNET_ERR_SHAPE;
+  if (bitnet_status st = check_rows_sizes(std::max(M, N), K)) return st;
   if ((M > 0 && (!x || !x_q || !s_x)) || (N > 0 && (!w || !w_q || !s_w))) return BITNET_ERR_NULL;
   if (N > 0 && !is_value(w_dtype)) return BITNET_ERR_DTYPE;
   if (M > 0 && (!aligned(x, 2) || !aligned(x_q, 16) || !aligned(s_x, 16))) return BITNET_ERR_ALIGN;

@@ -28,3 +28,13 @@ def test_rows_that_two_weights_share_have_the_limits_of_rows(L):
     # at the limits the call goes on to its other checks, and without rows it has none of theirs
     assert f(M=1 << 23, ws=None) == EWS and f(K=1 << 24, ws=None) == EWS
     assert f(x=None, M=1 << 27, ws=None) == EWS and f(x=None, K=(1 << 24) + 1, ws=None) == EWS
+
+
+def test_both_sides_of_one_launch_have_a_limit_together(L):
+    def f(M, N, K=2048, x=P):
+        return L.bitnet_rows_quant2(x, M, P, P, P, F32, N, P, P, K, None)
+
+    most = 1 << 23
+    assert f(most, most) == ESHAPE and f(most + 1, 1) == ESHAPE and f(0, most + 1) == ESHAPE and f(0, 0) == ESHAPE
+    assert f(-1, 4) == ESHAPE and f(4, -1) == ESHAPE and f(4, 4, K=0) == ESHAPE and f(4, 4, K=(1 << 24) + 1) == ESHAPE
+    assert f(most, most - 1, x=P + 1) == EALIGN and f(1, most, x=P + 1) == EALIGN  # on to its other checks
