@@ -1022,6 +1022,16 @@ void check_bias(const Tensor& b, int64_t N, const Tensor& x) {
   TORCH_CHECK_VALUE(b.device() == x.device(), "bias: on ", b.device(), ", expected ", x.device());
 }
 
+// A backward pass has narrower limits than the forward: a call whose gradients are wanted
+// is refused before its forward runs.
+void check_int8_bwd(const Tensor& x, int64_t N) {
+  const int64_t K = x.size(-1), M = x.numel() / K;
+  TORCH_CHECK_VALUE(M == 0 || bitnet_int8_bwd_workspace_bytes(M, N, K) > 0, "int8_linear: ", M, " x ", K, " -> ", N,
+                    " is too large for its backward pass, (rows + 256) * 2 * width <= 2^31 for each of its operands [",
+                    M, ", ", K, "], [", N, ", ", K, "] and [", M, ", ", N,
+                    "] with widths rounded up to 64: take fewer tokens at once, or torch.no_grad() for the forward alone");
+}
+
 Tensor int8_linear(const Tensor& x, const optional<Tensor>& codes, const optional<Tensor>& scales, const Tensor& weight,
                    const optional<Tensor>& bias) {
   const Tensor q = codes.value_or(Tensor()), s = scales.value_or(Tensor()), b = bias.value_or(Tensor());
@@ -1032,7 +1042,10 @@ Tensor int8_linear(const Tensor& x, const optional<Tensor>& codes, const optiona
                     "weight: expected [out_features, ", x.size(-1), "], got ", weight.sizes());
   TORCH_CHECK_VALUE(weight.device() == x.device(), "x and weight: must be GPU tensors of one device");
   check_bias(b, weight.size(0), x);
-  if (wants_grad({&x, &weight, &b})) return Int8Fn::apply(x, codes, scales, weight, bias);
+  if (wants_grad({&x, &weight, &b})) {
+    check_int8_bwd(x, weight.size(0));
+    return Int8Fn::apply(x, codes, scales, weight, bias);
+  }
   const Rows r(x, q, s);
   const auto w = int8_weight(weight, &r);
   return int8_forward(r, x.sizes(), w.first, w.second, b);
@@ -1054,6 +1067,8 @@ Tensor int8_linear_inference(const Tensor& x, const optional<Tensor>& codes, con
                     "x, w_q and s_w: must be GPU tensors of one device");
   check_bias(b, w_q.size(0), x);
   const Tensor wq = aligned(w_q), sw = aligned(s_w);
+  // a frozen module's bias wants a gradient in evaluation too: only that of x is looked at here
+  if (wants_grad({&x})) check_int8_bwd(x, wq.size(0));
   if (wants_grad({&x, &b})) return Int8FrozenFn::apply(x, codes, scales, wq, sw, bias);
   const Rows r(x, q, s, true);
   if (r.M > 0) {

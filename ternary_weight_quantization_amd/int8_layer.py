@@ -22,7 +22,10 @@ def int8_linear(x, weight, bias=None):
     largest magnitude over 127; bias [N] bf16 or float32 (rounded to bf16), added
     before the output's rounding. K <= 131072. Gradients, straight through both
     quantizations: of x in bf16, of weight and bias in their dtypes
-    (differentiable once, in reverse mode)."""
+    (differentiable once, in reverse mode). With widths rounded up to 64, the forward
+    takes (rows + 256) * K <= 2^31 for the rows of x and of weight; where gradients
+    are wanted (rows + 256) * 2 * width <= 2^31 has to hold for x, weight and
+    the output, and a call past that raises before it computes."""
     return B.ops().int8_linear(*layer_input(x), weight, bias)
 
 
@@ -30,7 +33,7 @@ def int8_linear_inference(x, w_q, s_w, in_features, bias=None):
     """The same from stored 8-bit weights, e.g. what
     ``QATInt8Linear.export_inference`` returns: w_q int8 [N, Kp] (Kp = in_features
     rounded up to 64, zeros past in_features), s_w float32 [N], a channel's largest
-    magnitude. Differentiable in x and bias."""
+    magnitude. Differentiable in x and bias, within int8_linear's sizes."""
     return B.ops().int8_linear_inference(*layer_input(x), w_q, s_w, int(in_features), bias)
 
 

@@ -195,3 +195,28 @@ def test_a_split_gated_forward_that_gives_up_is_visible(act):
     assert B.bitnet_split_timeouts() == 0
     with knobs(split_ctas=64):
         assert all(torch.equal(a, b) for a, b in zip(forward(), ref))
+
+
+# --- refusals ----------------------------------------------------------------
+
+def test_a_layer_too_large_for_its_backward_is_refused_in_the_forward():
+    """(M + 256) 2 Nd past 2^31: the forward alone runs, one whose gradients are wanted
+    raises at once."""
+    from ternary_weight_quantization_amd import binding as B
+    from ternary_weight_quantization_amd import int8_linear, int8_linear_inference
+
+    M, K, N = 33000, 64, 32768
+    note("int8 too large for its backward")
+    x, w = randn(M, K, seed=1), randn(N, K, seed=2)
+    with torch.no_grad():
+        y = int8_linear(x, w)
+    assert torch.equal(y[-1], int8_linear(x[-1], w))
+    with pytest.raises(ValueError, match="backward"):
+        int8_linear(x, w.requires_grad_(True))
+    assert torch.equal(int8_linear(x[:32000], w).detach(), y[:32000])
+    wq, sw = B.ops().int8_quantize_weight(w.detach())
+    bias = torch.zeros(N, dtype=BF, device="cuda", requires_grad=True)
+    assert torch.equal(int8_linear_inference(x, wq, sw, K), y)
+    assert torch.equal(int8_linear_inference(x, wq, sw, K, bias).detach(), y)
+    with pytest.raises(ValueError, match="backward"):
+        int8_linear_inference(x.requires_grad_(True), wq, sw, K)
