@@ -17,7 +17,7 @@ import math
 import torch
 
 from . import binding as B
-from .rows import QuantizedRows, layer_input
+from .rows import QuantizedRows, layer_input, need_activations
 
 
 def ternarize(weight):
@@ -69,6 +69,7 @@ class BitLinearFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, weight, bias=None):
+        need_activations("BitLinearFunction", x)
         if x.dtype != torch.bfloat16:
             raise TypeError("BitLinear expects bf16 activations")
         N, K = weight.shape
@@ -123,6 +124,7 @@ class FrozenBitLinearFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, w_packed, gamma, in_features, bias=None):
+        need_activations("FrozenBitLinearFunction", x)
         if x.dtype != torch.bfloat16:
             raise TypeError("BitLinear expects bf16 activations")
         K, N = int(in_features), w_packed.shape[0]

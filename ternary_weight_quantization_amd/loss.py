@@ -10,6 +10,7 @@ import math
 import torch
 
 from . import binding as B
+from .rows import need_activations
 
 REDUCTIONS = {"none": B.BITNET_REDUCE_NONE, "sum": B.BITNET_REDUCE_SUM, "mean": B.BITNET_REDUCE_MEAN}
 
@@ -25,6 +26,7 @@ def linear_cross_entropy(hidden, weight, targets, ignore_index=-100, reduction="
     hidden in bf16, of weight in its dtype (differentiable once, in reverse
     mode). Of a float32 weight each call makes a bf16 copy, which is kept until
     the backward."""
+    need_activations("linear_cross_entropy", hidden)
     code = REDUCTIONS.get(reduction)
     if code is None:
         raise ValueError(f"reduction: expected one of {sorted(REDUCTIONS)}, got {reduction!r}")

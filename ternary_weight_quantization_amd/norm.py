@@ -13,7 +13,7 @@ activations or the 8-bit rows (``rows``) that the layers multiply. torch provide
 import torch
 
 from . import binding as B
-from .rows import QuantizedRows
+from .rows import QuantizedRows, need_activations
 
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5, out_dtype=torch.bfloat16, checkpoint=False):
@@ -23,6 +23,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, out_dtype=torch.bfloat16, ch
     float32). ``checkpoint=True`` keeps x in 8 bits for the backward. Gradients:
     dX in x's dtype, those of weight and bias in theirs (differentiable once,
     in reverse mode)."""
+    need_activations("layer_norm", x)
     return B.ops().layer_norm(x, weight, bias, eps, out_dtype, checkpoint)
 
 
@@ -56,6 +57,7 @@ def rms_norm(x, weight=None, residual=None, eps=1e-6, out_dtype=torch.bfloat16, 
     ``QuantizedRows`` that the layers take, made from the norm's float32 values.
     Gradients, straight through the quantization: of x, residual and weight in
     their dtypes (differentiable once, in reverse mode)."""
+    need_activations("rms_norm", x)
     y, codes, scales, h = B.ops().rms_norm(x, weight, residual, eps, bool(quantize), out_dtype)
     if quantize:
         y = QuantizedRows(codes, scales, y)

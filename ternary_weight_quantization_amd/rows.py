@@ -5,7 +5,8 @@ float32 scale a row, the form in which the ternary layers multiply them anyway.
 ``rms_norm(..., quantize=True)`` makes them; ``QATBitLinear``,
 ``gated_bitlinear`` and ``int8_linear`` (with their modules) take them in place
 of activations and skip their own quantization, so one set of rows serves
-several layers.
+several layers. What else takes activations (``TTQLinear``, ``LinearCrossEntropy``,
+the norms) refuses them; ``dequantize`` gives it theirs.
 """
 
 from . import binding as B
@@ -44,6 +45,12 @@ class QuantizedRows:
 
     def __repr__(self):
         return f"QuantizedRows(shape={tuple(self.shape)}, requires_grad={self.requires_grad})"
+
+
+def need_activations(what, x):
+    """Refuses 8-bit rows where only activations are taken."""
+    if isinstance(x, QuantizedRows):
+        raise TypeError(f"{what} takes activations, not QuantizedRows (their dequantize() gives them)")
 
 
 def layer_input(x):

@@ -19,6 +19,7 @@ import math
 import torch
 
 from . import binding as B
+from .rows import need_activations
 
 
 def _inverse_softplus(v):
@@ -51,6 +52,7 @@ def ttq_forward_codes(x, w_packed, params):
     """Inference forward from the exported state (``TTQLinear.export_inference``):
     x [..., K] bf16, codes [N, Kp/4], params (delta, Wp, Wn) -> y [..., N]
     bf16. Few tokens read only the 2-bit codes."""
+    need_activations("TTQ", x)
     K = x.shape[-1]
     lead = x.shape[:-1]
     x2 = x.reshape(-1, K).contiguous()
@@ -71,6 +73,7 @@ class TTQFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, weight, params):
+        need_activations("TTQ", x)
         if x.dtype != torch.bfloat16:
             raise TypeError("TTQ expects bf16 activations")
         N, K = weight.shape
@@ -117,6 +120,7 @@ def ttq_linear(x, weight, params, checkpoint=False):
     bf16 for the product (whose relative error grows from 0.0017 to 0.0023
     against fp32 values)."""
     if checkpoint:
+        need_activations("TTQ", x)
         return B.ops().ttq_linear_checkpoint(x, weight, params)
     return TTQFunction.apply(x, weight, params)
 

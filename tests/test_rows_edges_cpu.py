@@ -38,3 +38,24 @@ def test_both_sides_of_one_launch_have_a_limit_together(L):
     assert f(most, most) == ESHAPE and f(most + 1, 1) == ESHAPE and f(0, most + 1) == ESHAPE and f(0, 0) == ESHAPE
     assert f(-1, 4) == ESHAPE and f(4, -1) == ESHAPE and f(4, 4, K=0) == ESHAPE and f(4, 4, K=(1 << 24) + 1) == ESHAPE
     assert f(most, most - 1, x=P + 1) == EALIGN and f(1, most, x=P + 1) == EALIGN  # on to its other checks
+
+
+def test_what_does_not_take_rows_says_so():
+    import torch
+
+    from tests.test_more_operators_cpu import rows_of
+    from ternary_weight_quantization_amd import LinearCrossEntropy, TTQLinear, layer_norm, linear_cross_entropy, rms_norm
+    from ternary_weight_quantization_amd.layer import BitLinearFunction, FrozenBitLinearFunction
+    from ternary_weight_quantization_amd.ttq_layer import ttq_forward_codes, ttq_linear
+
+    r, w, p = rows_of(4, 64), torch.zeros(9, 64, dtype=torch.bfloat16), torch.ones(3)
+    t = torch.zeros(4, dtype=torch.int64)
+    ttq = TTQLinear.__new__(TTQLinear)  # its scales are made on the GPU
+    torch.nn.Module.__init__(ttq)
+    ttq.weight, ttq.raw = torch.nn.Parameter(w), torch.nn.Parameter(p)
+    for call in (lambda: ttq(r), lambda: ttq_linear(r, w, p), lambda: ttq_linear(r, w, p, checkpoint=True),
+                 lambda: ttq_forward_codes(r, w, p), lambda: linear_cross_entropy(r, w, t),
+                 lambda: LinearCrossEntropy(64, 9, device="cpu")(r, t), lambda: BitLinearFunction.apply(r, w, None),
+                 lambda: FrozenBitLinearFunction.apply(r, w.byte(), p[:1], 64), lambda: layer_norm(r), lambda: rms_norm(r)):
+        with pytest.raises(TypeError, match="not QuantizedRows"):
+            call()
