@@ -28,7 +28,10 @@ def ternarize(weight):
     w_packed = torch.empty((N, Kp // 4), dtype=torch.uint8, device=weight.device)
     gamma = torch.empty((1,), dtype=torch.float32, device=weight.device)
     ws = torch.empty((B.bitnet_ternarize_workspace_bytes(N, K),), dtype=torch.uint8, device=weight.device)
-    B.bitnet_ternarize_pack(weight.contiguous(), w_packed, gamma, ws)
+    w = weight.contiguous()
+    if w.data_ptr() % 16:  # a view into a larger buffer
+        w = w.clone()
+    B.bitnet_ternarize_pack(w, w_packed, gamma, ws)
     return w_packed, gamma
 
 

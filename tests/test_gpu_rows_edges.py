@@ -220,3 +220,25 @@ def test_a_layer_too_large_for_its_backward_is_refused_in_the_forward():
     assert torch.equal(int8_linear_inference(x, wq, sw, K, bias).detach(), y)
     with pytest.raises(ValueError, match="backward"):
         int8_linear_inference(x.requires_grad_(True), wq, sw, K)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_master_weights_off_alignment_freeze(dtype):
+    """Masters that are views of a larger buffer, from any element on, train and freeze."""
+    from ternary_weight_quantization_amd import QATGatedBitLinear
+    from ternary_weight_quantization_amd.layer import ternarize
+
+    note(f"masters off alignment {dtype}")
+    N, K = 21, 67
+    m = QATGatedBitLinear(K, N, dtype=dtype)
+    flat = torch.empty(2 * N * K + 1, dtype=dtype, device="cuda")
+    for i, p in enumerate((m.gate_weight, m.up_weight)):
+        view = flat[1 + i * N * K:1 + (i + 1) * N * K].view(N, K)
+        view.copy_(p.data)
+        p.data = view
+    x = randn(5, K, seed=1)
+    y = m(x)
+    m.freeze()
+    assert torch.equal(m(x), y)
+    packed, gamma = ternarize(m.up_weight.detach().clone())
+    assert torch.equal(m.export_inference()[0][N:], packed) and torch.equal(m.export_inference()[1][1:], gamma)
