@@ -363,9 +363,11 @@ def bitnet_quantize2(W0, W1, x, w_packed, gamma, x_q, s_x, workspace, stream=Non
         _need(x, torch.bfloat16, (M, K), "x")
         _need(x_q, torch.int8, (M, Kp), "x_q")
         _need(s_x, torch.float32, (M,), "s_x")
+    _same_device(W0, W1=W1, x=x, w_packed=w_packed, gamma=gamma, x_q=None if x is None else x_q,
+                 s_x=None if x is None else s_x, workspace=workspace)
     ws_bytes = workspace.numel() * workspace.element_size()
-    _check(lib().bitnet_quantize2(_ptr(W0), _ptr(W1), wd, N, K, _ptr(x), M, _ptr(w_packed), _ptr(gamma), _ptr(x_q),
-                                  _ptr(s_x), _ptr(workspace), ws_bytes, _stream(stream)))
+    _run(lib().bitnet_quantize2, W0, stream, _ptr(W0), _ptr(W1), wd, N, K, _ptr(x), M, _ptr(w_packed), _ptr(gamma),
+         _ptr(x_q), _ptr(s_x), _ptr(workspace), ws_bytes)
 
 
 def bitnet_quantize_static(W, x, w_packed, gamma, x_q, s_x, stream=None):

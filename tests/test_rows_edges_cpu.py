@@ -59,3 +59,28 @@ def test_what_does_not_take_rows_says_so():
                  lambda: FrozenBitLinearFunction.apply(r, w.byte(), p[:1], 64), lambda: layer_norm(r), lambda: rms_norm(r)):
         with pytest.raises(TypeError, match="not QuantizedRows"):
             call()
+
+
+def test_two_weights_on_their_own_device(L, monkeypatch):
+    """The call runs on the weights' device and its current stream, and every tensor has
+    to be there (the CPU and "meta" stand for two GPUs)."""
+    import torch
+
+    from ternary_weight_quantization_amd import binding as B
+
+    ran = []
+    monkeypatch.setattr(B, "_need", lambda *a: None)
+    monkeypatch.setattr(B, "_run", lambda fn, like, stream, *args: ran.append((like, stream, len(args))))
+    monkeypatch.setattr(B, "_stream", lambda stream: None)
+    f32, kinds = torch.float32, [((9, 64), torch.float32)] * 2  # W0, W1, x, codes, gamma, x_q, s_x, workspace
+    kinds += [((4, 64), torch.bfloat16), ((18, 16), torch.uint8), ((2,), f32), ((4, 64), torch.int8), ((4,), f32),
+              ((64,), torch.uint8)]
+    make = lambda i, device: torch.empty(kinds[i][0], dtype=kinds[i][1], device=device)  # noqa: E731
+    here = [make(i, "cpu") for i in range(8)]
+    B.bitnet_quantize2(*here)
+    assert ran[0][0] is here[0] and ran[0][1] is None
+    for i in range(1, 8):
+        with pytest.raises(ValueError, match="on meta, expected cpu"):
+            B.bitnet_quantize2(*[make(j, "meta" if j == i else "cpu") for j in range(8)])
+    B.bitnet_quantize2(here[0], here[1], None, here[3], here[4], None, None, here[7])
+    assert len(ran) == 2
