@@ -1,5 +1,7 @@
 """8-bit rows, the gated pair and the 8-bit layer where their arithmetic and their
-sizes end."""
+sizes end: codes at exact ties, the slopes' rounding, roots of no positive number,
+waits that give up, memory full of garbage in every form of the kernels, sizes that
+only the forward takes, masters off alignment."""
 
 import pytest
 import torch
@@ -195,6 +197,133 @@ def test_a_split_gated_forward_that_gives_up_is_visible(act):
     assert B.bitnet_split_timeouts() == 0
     with knobs(split_ctas=64):
         assert all(torch.equal(a, b) for a, b in zip(forward(), ref))
+
+
+def test_a_split_gated_backward_that_gives_up_is_visible():
+    from ternary_weight_quantization_amd import binding as B
+
+    M, K, N = 768, 768, 384  # D has 2 x 384 columns, dW 2 x 384 rows: 3 x 3 tiles each
+    note("gated backward gives up")
+    x, q, s, packed, gamma = pair(M, K, N, 6)
+    dY = randn(M, N, seed=7)
+    y = torch.empty(M, N, dtype=BF, device="cuda")
+    sl = torch.zeros(B.bitnet_gated_slopes_bytes(M, N), dtype=torch.uint8, device="cuda")
+    B.bitnet_gated_fwd(B.BITNET_ACT_SILU, q, s, packed, gamma, K, y, sl)
+
+    def backward():
+        dX, dg, du = (torch.empty(n, K, dtype=BF, device="cuda") for n in (M, N, N))
+        B.bitnet_gated_bwd(dY, sl, q, s, packed, gamma, K, dX=dX, dW_gate=dg, dW_up=du)
+        return dX, torch.cat([dg, du])
+
+    B.bitnet_split_timeouts()
+    with knobs(split_ctas=36):
+        ref = backward()
+    assert B.bitnet_split_timeouts() == 0
+    with knobs(split_ctas=36, spin_limit=0):
+        got = backward()
+    count, bad = B.bitnet_split_timeouts(), 0
+    for a, b in zip(got, ref):
+        for j in range(0, M, 256):
+            for k in range(0, K, 256):
+                t = a[j:j + 256, k:k + 256]
+                if t.isnan().any():
+                    bad += 1
+                    assert t.isnan().all()
+                else:
+                    assert torch.equal(t, b[j:j + 256, k:k + 256])
+    note(f"  counted {count}, {bad} tiles")
+    assert count == bad and B.bitnet_split_timeouts() == 0
+
+
+def test_a_split_8_bit_forward_that_gives_up_is_visible():
+    """Its accumulators are INT32_MIN there, which no sum of products is."""
+    from ternary_weight_quantization_amd import binding as B
+
+    M, K, N = 768, 2560, 768
+    note("int8 split gives up")
+    new = lambda n: (torch.empty(n, K, dtype=torch.int8, device="cuda"), torch.empty(n, device="cuda"))  # noqa: E731
+    (q, s), (wq, sw) = new(M), new(N)
+    B.bitnet_rows_quant2(randn(M, K, seed=1), q, s, randn(N, K, seed=2), wq, sw)
+
+    def forward():
+        y = torch.empty(M, N, dtype=BF, device="cuda")
+        B.bitnet_int8_fwd(q, s, wq, sw, K, y)
+        return y
+
+    B.bitnet_split_timeouts()
+    with knobs(split_ctas=64):
+        ref = forward()
+    assert B.bitnet_split_timeouts() == 0
+    with knobs(split_ctas=64, spin_limit=0):
+        got = forward()
+    count, bad = B.bitnet_split_timeouts(), 0
+    c, cw = s / torch.full_like(s, 127.0), sw / torch.full_like(sw, 127.0)
+    lost = (-2.0 ** 31 * c[:, None] * cw).to(BF)
+    for m in range(0, M, 256):
+        for n in range(0, N, 256):
+            at = (slice(m, m + 256), slice(n, n + 256))
+            if not torch.equal(got[at], ref[at]):
+                bad += 1
+                assert torch.equal(got[at], lost[at])
+    note(f"  counted {count}, {bad} tiles")
+    assert count == bad and B.bitnet_split_timeouts() == 0
+
+
+# --- memory full of garbage --------------------------------------------------
+
+@pytest.mark.parametrize("N", [75, 129])
+@pytest.mark.parametrize("M,kw", FORMS)
+def test_gated_pair_in_garbage(M, kw, N):
+    """Slopes, workspaces and outputs full of NaN or zeros before the calls, every form
+    of the forward: the same bits, trained and for dX alone without the rows."""
+    from ternary_weight_quantization_amd import binding as B
+
+    K = 130
+    note(f"gated in garbage M={M} N={N} {kw}")
+    x, q, s, packed, gamma = pair(M, K, N, 1)
+    dY = randn(M, N, seed=3)
+    outs = []
+    with knobs(**kw):
+        for fill in (0xFF, 0x00):
+            new = lambda n: torch.full((max(n, 16),), fill, dtype=torch.uint8, device="cuda")  # noqa: E731
+            out = lambda *n: new(2 * n[0] * n[1]).view(BF)[:n[0] * n[1]].view(n)  # noqa: E731
+            y, slopes = out(M, N), new(B.bitnet_gated_slopes_bytes(M, N))
+            B.bitnet_gated_fwd(B.BITNET_ACT_SILU, q, s, packed, gamma, K, y, slopes,
+                               workspace=new(B.bitnet_gated_fwd_workspace_bytes(M, N, K)))
+            need = B.bitnet_gated_bwd_workspace_bytes(M, N, K)
+            dX, dg, du, only, w0, w1 = out(M, K), out(N, K), out(N, K), out(M, K), out(N, K), out(N, K)
+            B.bitnet_gated_bwd(dY, slopes, q, s, packed, gamma, K, dX=dX, dW_gate=dg, dW_up=du, workspace=new(need))
+            B.bitnet_gated_bwd(dY, slopes, None, None, packed, gamma, K, dX=only, workspace=new(need))
+            B.bitnet_gated_bwd(dY, slopes, q, s, None, gamma, K, dW_gate=w0, dW_up=w1, workspace=new(need))
+            outs.append((y, dX, dg, du, only, w0, w1))
+    for a, b in zip(*outs):
+        assert a.isfinite().all() and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("N", [75, 129])
+@pytest.mark.parametrize("M,kw", FORMS)
+def test_8_bit_layer_in_garbage(M, kw, N):
+    from ternary_weight_quantization_amd import binding as B
+
+    K, Kp = 130, 192
+    note(f"int8 in garbage M={M} N={N} {kw}")
+    dY, outs = randn(M, N, seed=3), []
+    with knobs(**kw):
+        for fill in (0xFF, 0x00):
+            new = lambda n: torch.full((max(n, 16),), fill, dtype=torch.uint8, device="cuda")  # noqa: E731
+            out = lambda *n: new(2 * n[0] * n[1]).view(BF)[:n[0] * n[1]].view(n)  # noqa: E731
+            rows = lambda n: (new(n * Kp).view(torch.int8).view(n, Kp), new(4 * n).view(F32)[:n])  # noqa: E731
+            (q, s), (wq, sw) = rows(M), rows(N)
+            B.bitnet_rows_quant(randn(M, K, seed=1), q, s)
+            B.bitnet_rows_quant(randn(N, K, seed=2, dtype=F32), wq, sw)
+            y, dX, dW, db, only = out(M, N), out(M, K), out(N, K), out(1, N)[0], out(M, K)
+            B.bitnet_int8_fwd(q, s, wq, sw, K, y, workspace=new(B.bitnet_int8_fwd_workspace_bytes(M, N, K)))
+            need = B.bitnet_int8_bwd_workspace_bytes(M, N, K)
+            B.bitnet_int8_bwd(dY, q, s, wq, sw, K, dX=dX, dW=dW, db=db, workspace=new(need))
+            B.bitnet_int8_bwd(dY, None, None, wq, sw, K, dX=only, workspace=new(need))
+            outs.append((y, dX, dW, db, only))
+    for a, b in zip(*outs):
+        assert a.isfinite().all() and torch.equal(a, b)
 
 
 # --- refusals ----------------------------------------------------------------
