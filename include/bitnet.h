@@ -675,7 +675,7 @@ bitnet_status bitnet_rows_unpack(const int8_t* x_q, const float* s_x, int64_t M,
  * after them; and its straight-through backward (gamma treated as constants)
  *
  *   Dg = bf16(dY p gamma[0] c),  Du = bf16(dY a gamma[1] c),  c[m] = s_x[m]/127
- *   dX[m,k] = sum_n (Dg[m,n] q_g[n,k] + Du[m,n] q_u[n,k]) / c[m]
+ *   dX[m,k] = sum_n (Dg[m,n] q_g[n,k] + Du[m,n] q_u[n,k]) / c[m], 0 where |s_x[m]| < 2^-100
  *   dW_gate[n,k] = sum_m Dg[m,n] x_q[m,k] / gamma[0],  dW_up likewise with Du, gamma[1]
  *
  * (dg = dY u act'(g) and du = dY act(g) with the scales of what they are multiplied

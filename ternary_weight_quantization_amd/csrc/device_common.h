@@ -44,6 +44,10 @@ __device__ __forceinline__ uint16_t f32_to_bf16_bits(float v) {
   return __builtin_bit_cast(uint16_t, a);
 }
 
+// The factor of a token's row of dX whose operand holds s/127. A row of scale 0 (a token
+// masked out), or of one so small that its quotient overflows, has an operand of zeros.
+__device__ __forceinline__ float per_scale(float s) { return fabsf(s) < 0x1p-100f ? 0.0f : 127.0f / s; }
+
 // Byte permute: selector bytes 0..3 pick bytes of `lo`, 4..7 bytes of `hi`.
 __device__ __forceinline__ uint32_t perm(uint32_t hi, uint32_t lo, uint32_t sel) {
   return __builtin_amdgcn_perm(hi, lo, sel);

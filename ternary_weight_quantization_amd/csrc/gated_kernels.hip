@@ -372,7 +372,7 @@ struct TokenEpilogue {
 #pragma unroll
     for (int fj = 0; fj < kFJ; ++fj) {
       const int64_t j = j0 + 32 * fj + (lane & 31);
-      pre.c[fj] = s != nullptr && j < J ? 127.0f / s[j] : 1.0f;
+      pre.c[fj] = s != nullptr && j < J ? per_scale(s[j]) : 1.0f;
     }
     return pre;
   }

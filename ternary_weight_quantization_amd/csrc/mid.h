@@ -405,7 +405,7 @@ struct MidOut {
   void* out;
   int64_t I, J;
   const float* s;
-  __device__ __forceinline__ float scale(int64_t j) const { return s != nullptr && j < J ? 127.0f / s[j] : 1.0f; }
+  __device__ __forceinline__ float scale(int64_t j) const { return s != nullptr && j < J ? per_scale(s[j]) : 1.0f; }
   __device__ __forceinline__ void* part(int&, int64_t& rows) const {
     rows = J;
     return out;

@@ -275,7 +275,7 @@ __global__ __launch_bounds__(kWave * W) void dx_skinny_kernel(SkArgs a, const fl
   const int64_t m = 32 * mt + (lane & 31);
   if (mt >= MT || m >= a.M) return;
   // bf16(gamma) is exact in fp32
-  const float sc = gamma ? bf16_to_f32(f32_to_bf16_bits(*gamma)) : s ? 127.0f / s[m] : 1.0f;
+  const float sc = gamma ? bf16_to_f32(f32_to_bf16_bits(*gamma)) : s ? per_scale(s[m]) : 1.0f;
   const int64_t kb = (int64_t)blockIdx.x * 32 + 8 * g + 4 * h;
   uint16_t* dr = dX + m * K;
   if (K % 4 == 0 && kb + 4 <= K) {

@@ -157,6 +157,30 @@ def test_slopes_are_rounded_to_24_bits(M, kw):
         assert (a[M // 2][pos] == float("inf")).all() and (a[M // 2][~pos] == 0).all()
 
 
+@pytest.mark.parametrize("M,kw", FORMS)
+def test_rows_of_scale_zero(M, kw):
+    """A token masked out by a scale of 0, or one of the least scales, stands for zeros:
+    no gradient, and none of its own in the weights'."""
+    from ternary_weight_quantization_amd import QATGatedBitLinear, rms_norm
+
+    note(f"rows of scale 0 M={M} {kw}")
+    m = QATGatedBitLinear(130, 75)
+    x, dy = randn(M, 130, seed=M).requires_grad_(True), randn(M, 75, seed=1)
+    off = torch.arange(0, M, 3, device="cuda")
+    with knobs(**kw):
+        for low in (0.0, 1e-40, 2.0 ** -126):
+            rows = rms_norm(x, quantize=True)
+            rows.scales[off] = low
+            y = m(rows)
+            assert not y[off].any()
+            dx, dg, du = torch.autograd.grad(y, [rows._carrier, m.gate_weight, m.up_weight], dy)
+            assert not dx[off].any() and dx.isfinite().all()
+            d0 = dy.clone()
+            d0[off] = 0
+            wx, wg, wu = torch.autograd.grad(m(rows), [rows._carrier, m.gate_weight, m.up_weight], d0)
+            assert torch.equal(dx, wx) and torch.equal(dg, wg) and torch.equal(du, wu)
+
+
 # --- waits that give up ------------------------------------------------------
 
 @pytest.mark.parametrize("act", ["silu", "relu2"])
