@@ -1,9 +1,9 @@
-// Products of 8-bit rows for few tokens (M <= 64): acc[m][n] = sum_k x_q[m][k] *
-// w[n][k] in int32 for weights in 8 bits or as 2-bit codes. At these sizes the
-// cost is reading the weights once, so that as many bytes as possible have to be
+// Products of 8-bit rows for few tokens, groups of up to kFewM: acc[m][n] = sum_k
+// x_q[m][k] * w[n][k] in int32 for weights in 8 bits or as 2-bit codes. At these sizes
+// the cost is reading the weights once, so that as many bytes as possible have to be
 // in flight from the first cycle on.
 //
-// A workgroup of W waves takes RT tiles of 16 weight rows and every token. The
+// A workgroup of W waves takes RT tiles of 16 weight rows and the tokens of a group. The
 // waves share the reduction: wave w takes steps w, w + W, ... of 256 (codes) or 128
 // (int8) k, so that a step is 64 or 128 consecutive bytes of each row, and requests P
 // steps ahead. v_mfma_i32_16x16x64_i8 takes 16 bytes of weight row l % 16 and of
@@ -83,10 +83,12 @@ constexpr int few_lds() {
 
 // The codes of up to NX tokens of at most kMaxK values, which every workgroup makes
 // of the bf16 rows for itself while its first weights are on the way: no launch before
-// this one, and no codes in memory. Measured, us, against the rows' launch and the
-// product: codes, 2560 -> 2 x 6912 1 token 6.3 (2.8 + 5.9), 4 tokens 8.5 (2.8 + 6.1);
-// int8, 2560 -> 32000 1 token 14.7 (2.9 + 15.6), 4 tokens 19.6 (3.9 + 15.8). The work is a
-// row's reduction and codes for each token in every workgroup, so more tokens lose.
+// this one, and no codes in memory. The work is a row's reduction and codes for each
+// token in every workgroup, so it pays at 1 and 2 tokens and less with each more.
+// Measured, us a call among others, 1 / 2 / 3 / 4 tokens, and 5 with the rows' launch and
+// the product: codes, 2560 -> 2 x 6912 6.0 / 7.0 / 8.1 / 8.4, 9.0; 6912 -> 2 x 2560 7.0 / 7.9 /
+// 9.8 / 10.1, 9.9; int8, 6912 -> 2560 6.7 / 7.8 / 9.1 / 10.3, 9.9; 2560 -> 32000 (2000
+// workgroups) 15.0 / 17.0 / 20.6 / 22.0, 18.5: there 3 and 4 tokens lose.
 template <int NX, int W>
 struct FewRows {
   static constexpr int kThreads = kWave * W, kChunks = 2, kMaxK = 8 * kChunks * kThreads;

@@ -26,11 +26,11 @@
 // codes are padded to Nd = N rounded up to 64 in each half, so that every width
 // runs the aligned loaders and no 32 rows of dW belong to both halves.
 //
-// Measured, 4096 x 2560 -> 2 x 6912: forward 195 us (290 G operations; the 227 MB of y and
-// slopes in its epilogue are 44 of it at a copy's rate), D and the operands 65 (400 MB, 6.1
-// TB/s, half of it left in the last-level cache), both products 445 (580 GFLOP, 1.30
-// PFLOP/s, what the largest library product reaches). Up to 256 tokens few8.h's kernels
-// and up to about 1000 mid.h's tiles run instead.
+// Measured, 4096 x 2560 -> 2 x 6912: forward 195 to 208 us (290 G operations; the 227 MB
+// of y and slopes in its epilogue are 44 of it at a copy's rate), D and the operands 65
+// (400 MB, 6.1 TB/s, half of it left in the last-level cache), both products 445 to 489 (580 GFLOP, 1.19
+// to 1.30 PFLOP/s by the card's clock; the largest library product reaches 1.32). Up to
+// 256 tokens few8.h's kernels and up to about 1000 mid.h's tiles run instead.
 
 #include <algorithm>
 
@@ -164,8 +164,8 @@ struct GatedEpilogue {
 };
 
 // ---------------------------------------------------------------------------
-// Few tokens (M <= kSkinnyMaxM, few8.h): a workgroup's two tiles are 16 rows of the
-// gate and the same 16 of the up projection.
+// Few tokens (few8.h; up to 4 groups of kFewM, gated_form): a workgroup's pairs of tiles
+// are 16 rows of the gate and the same 16 of the up projection.
 // ---------------------------------------------------------------------------
 
 // RP: pairs of tiles.

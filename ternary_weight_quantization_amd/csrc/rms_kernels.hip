@@ -10,9 +10,12 @@
 // largest |h w| is taken along with the sum of squares, before r is known: then
 // s = r max |h w|, q = round(h w (127 / max |h w|)), one reduction and one pass over the
 // row's registers. Statistics are fp32, and no rounding to bf16 comes between h
-// and q. Bound by HBM once there are rows enough: 16384 x 6912 bf16 to 8-bit rows 67.6
-// us (340 MB, 5.0 TB/s), 4096 x 2560 with a residual 15.0 (73 MB, 4.9 TB/s), 1537 x 6905
-// bf16 onto an f32 stream 24.5 (127 MB, 5.2 TB/s); one row of 2560 is a launch's 4.5.
+// and q. Bound by HBM once there are rows enough: 16384 x 6912 bf16 to 8-bit rows 69
+// us (340 MB, 4.9 TB/s), 4096 x 2560 with a residual 15.0 (73 MB, 4.9 TB/s), 1537 x 6905
+// bf16 onto an f32 stream 24 (127 MB, 5.3 TB/s). One row of 2560 takes 4.6, where a launch
+// of little work is 1.9 and a row's 8-bit codes alone are 2.9: its threads are chosen for
+// many rows, one wave that loads five chunks of three operands, after a vote of the
+// block on the weight.
 
 #include <algorithm>
 

@@ -22,7 +22,9 @@ def int8_linear(x, weight, bias=None):
     largest magnitude over 127; bias [N] bf16 or float32 (rounded to bf16), added
     before the output's rounding. K <= 131072. Gradients, straight through both
     quantizations: of x in bf16, of weight and bias in their dtypes
-    (differentiable once, in reverse mode). With widths rounded up to 64, the forward
+    (differentiable once, in reverse mode). Their products take both quantized
+    operands rounded to bf16, those of float32 masters too: gradients are about
+    0.0025 of their norm off exact ones, where fp32 products would be 0.0017. With widths rounded up to 64, the forward
     takes (rows + 256) * K <= 2^31 for the rows of x and of weight; where gradients
     are wanted (rows + 256) * 2 * width <= 2^31 has to hold for x, weight and
     the output, and a call past that raises before it computes."""
